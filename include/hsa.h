@@ -131,7 +131,9 @@ enum hsa_op {
   HSA_OP_ATTEND = 2,
   HSA_OP_DENSE = 3,
   HSA_OP_STEP = 4,
-  HSA_OP_CACHED = 5
+  HSA_OP_CACHED = 5,
+  HSA_OP_KV8_DECODE = 6,  /* hsa_kv8_decode and hsa_kv8_attend */
+  HSA_OP_KV8_PREFILL = 7
 };
 
 /* Workspace bytes `op` needs for descriptor `d` (0 if `d` is invalid). */
@@ -375,6 +377,91 @@ int32_t hsa_select_noalloc(const hsa_dims* d, const void* q, const int8_t* kq,
  * kernel, attention). Host I/O adds a staging kernel. -1 for an invalid d.
  */
 int32_t hsa_decode_step_kernels(const hsa_dims* d);
+
+/*
+ * ---- 8-bit K/V cache ("KV Cache 与长上下文推理", section "KV Cache 量化") ----
+ *
+ * K and V themselves in 8 bits (the int8 key codes above are a scoring copy of K beside the
+ * bf16 cache): codes [num_pages][hkv][16][128] for K and for V, pages and page table as in the
+ * bf16 cache, and one f32 scale for each (page, kv head), K and V apart:
+ *     value = code * scale.
+ * Format 0: int8 codes in [-127, 127], L = 127. Format 1: FP8 E4M3 codes, L = 448.
+ *
+ * Conventions of the hsa_kv8 calls:
+ *  - d: batch, hq, hkv (any hq / hkv from 1 to 8), head_dim, page_size, max_pages_per_seq and
+ *    num_pages as above; kv_on_host must be 0 (the cache is device memory), else UNSUPPORTED;
+ *    sink, window, k2 and per_head are used by hsa_kv8_attend alone.
+ *  - New tokens: seq_lens already count them. cu_tokens (int32 [batch + 1], ascending from 0 to
+ *    total_tokens, device memory): sequence b's new tokens are rows [cu_tokens[b],
+ *    cu_tokens[b + 1]) of the row arrays and positions [N_b - n_b, N_b), n_b their number (0
+ *    allowed). cu_tokens NULL: one new token a sequence, row b of sequence b (total_tokens must
+ *    equal batch). A sequence whose rows or length do not fit (n_b > N_b, N_b longer than its
+ *    page-table row, rows outside the arrays), or a bad page-table entry, is left out and
+ *    reported as HSA_ERR_DEVICE_CHECK through the error word.
+ *  - Row strides are in elements, at least the row's own length, and a multiple of 8.
+ *  - Pointers are 16-byte aligned (code arrays 128-byte); the page table and lengths 4-byte.
+ */
+typedef struct hsa_kv8 {
+  void* k;        /* K codes [num_pages][hkv][16][128] */
+  void* v;        /* V codes */
+  float* k_scale; /* f32 [num_pages][hkv] */
+  float* v_scale; /* f32 [num_pages][hkv] */
+  int32_t format; /* 0: int8, 1: FP8 E4M3 */
+} hsa_kv8;
+
+/*
+ * Quantises new tokens into the cache as they arrive: k_new and v_new are bf16 rows
+ * [total_tokens][hkv][128] with row strides k_stride and v_stride (slices of a fused
+ * projection's output need no copy). For each block (page, kv head) that receives tokens:
+ *     amax = the largest finite |x| among its new tokens, s_t = f32(amax / L), taken as 0
+ *            when below 2^-126;
+ *     s    = s_t when no older token of the sequence is in the block, else max(s_old, s_t);
+ *     inv  = f32(1 / s), 0 when s = 0;
+ *     older tokens' codes, when s > s_old: round(f32(code * f32(s_old * inv)));
+ *     new codes: round(f32(x * inv)) to the format, halves to even, at most L in magnitude;
+ *     a NaN becomes 0 and an infinity +-L.
+ * Whole blocks written at once are therefore within half a code step of bf16, and a block that
+ * grows token by token is within half a step more for each time its scale grew. Slots behind
+ * the last token keep their codes. Rewriting positions (after a rejected draft) keeps the
+ * block's scale unless it has no older token. Two sequences must not write the same page.
+ * workspace (nullable) supplies the error word only: at least 256 bytes.
+ */
+int32_t hsa_kv8_write(const hsa_dims* d, const hsa_kv8* cache, const void* k_new,
+                      int64_t k_stride, const void* v_new, int64_t v_stride,
+                      const int32_t* cu_tokens, int32_t total_tokens, const int32_t* page_table,
+                      const int32_t* seq_lens, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/*
+ * Reads the last n_b tokens of each sequence back: k_out and v_out are bf16 rows
+ * [total_tokens][hkv][128] with row strides k_stride and v_stride, each value
+ * bf16(f32(code * scale)). Pages may be shared between sequences. workspace as hsa_kv8_write.
+ */
+int32_t hsa_kv8_read(const hsa_dims* d, const hsa_kv8* cache, void* k_out, int64_t k_stride,
+                     void* v_out, int64_t v_stride, const int32_t* cu_tokens,
+                     int32_t total_tokens, const int32_t* page_table, const int32_t* seq_lens,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dense_decode over the 8-bit cache: one query token a sequence, q bf16 [batch][hq][128],
+ * attends every token [0, N_b). out f32 [batch][hq][128], lse f32 [batch][hq] (nullable). A
+ * sequence of no tokens gives 0 and lse -inf. Needs the HSA_OP_KV8_DECODE workspace.
+ */
+int32_t hsa_kv8_decode(const hsa_dims* d, const hsa_kv8* cache, const void* q,
+                       const int32_t* page_table, const int32_t* seq_lens, float* out,
+                       float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * hsa_attend over the 8-bit cache: the attended set T_b of the sink, the window and the kept
+ * blocks block_idx [batch][rows][k2] / n_blocks [batch][rows] as hsa_select writes them (rows =
+ * hkv, or hq with per_head = 1; ids distinct in a row, ids outside the candidate region add
+ * nothing). A row that attends nothing gives 0 and lse -inf. Outputs and workspace as
+ * hsa_kv8_decode.
+ */
+int32_t hsa_kv8_attend(const hsa_dims* d, const hsa_kv8* cache, const void* q,
+                       const int32_t* page_table, const int32_t* seq_lens,
+                       const int32_t* block_idx, const int32_t* n_blocks, float* out, float* lse,
+                       void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Reads and clears the device error word of `workspace` after synchronising `stream`:

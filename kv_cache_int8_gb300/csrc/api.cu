@@ -31,15 +31,16 @@ inline bool aligned(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
 
-// Structural checks of the descriptor; fills `s`. `need_prune` adds the module fields.
-int32_t check_dims(const hsa_dims* d, Shape& s, bool need_prune) {
+// Structural checks of the descriptor; fills `s`. `need_prune` adds the module fields;
+// `any_group` allows every group of 1 to 8 query heads a kv head (the 8-bit cache's calls).
+int32_t check_dims(const hsa_dims* d, Shape& s, bool need_prune, bool any_group = false) {
   if (d == nullptr) return HSA_ERR_INVALID_ARG;
   if (d->batch < 1 || d->hq < 1 || d->hkv < 1 || d->max_pages_per_seq < 1 || d->num_pages < 1)
     return HSA_ERR_INVALID_ARG;
   if (d->hq % d->hkv != 0) return HSA_ERR_INVALID_ARG;
   if (d->head_dim != hsa::kHeadDim || d->page_size != hsa::kPage) return HSA_ERR_UNSUPPORTED;
   const int g = d->hq / d->hkv;
-  if (g != 1 && g != 2 && g != 4 && g != 8) return HSA_ERR_UNSUPPORTED;
+  if (g != 1 && g != 2 && g != 4 && g != 8 && !(any_group && g < 8)) return HSA_ERR_UNSUPPORTED;
   if (d->batch > kMaxBatch || d->hkv > kMaxHkv) return HSA_ERR_UNSUPPORTED;
   if ((long long)d->num_pages * d->hkv * hsa::kPage > INT32_MAX ||
       (long long)d->max_pages_per_seq * hsa::kPage > INT32_MAX / 2)
@@ -178,6 +179,19 @@ hsa::BlockCache block_cache_at(const Shape& s, void* buf, int capacity) {
   c.data = p + l.data;
   c.capacity = capacity;
   return c;
+}
+
+// The 8-bit cache's decode attention: counters a selection row, then two parts a CTA.
+struct Kv8Layout {
+  size_t counters, part_ml, part_o, end;
+};
+Kv8Layout kv8_layout(const Shape& s) {
+  Kv8Layout l;
+  l.counters = kErrBytes;
+  l.part_ml = l.counters + up((size_t)s.batch * s.hq * 4);
+  l.part_o = l.part_ml + (size_t)2 * hsa::kKv8MaxCtas * 8 * 2 * 4;
+  l.end = l.part_o + (size_t)2 * hsa::kKv8MaxCtas * 8 * hsa::kHeadDim * 4;
+  return l;
 }
 
 struct StepLayout {
@@ -466,6 +480,84 @@ int32_t copy_outputs_back(const Shape& s, const hsa_step_io* io, const float* ou
   return e == cudaSuccess ? HSA_OK : HSA_ERR_CUDA;
 }
 
+// ---- the 8-bit K/V cache
+int32_t check_kv8(const hsa_dims* d, const hsa_kv8* c, Shape& s, hsa::Kv8* out) {
+  const int32_t rc = check_dims(d, s, false, true);
+  if (rc != HSA_OK) return rc;
+  if (d->kv_on_host) return HSA_ERR_UNSUPPORTED;
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return HSA_ERR_INVALID_ARG;
+  if (!aligned(c->k, 128) || !aligned(c->v, 128) || !aligned(c->k_scale, 16) ||
+      !aligned(c->v_scale, 16))
+    return HSA_ERR_INVALID_ARG;
+  if (c->format != 0 && c->format != 1) return HSA_ERR_INVALID_ARG;
+  *out = hsa::Kv8{c->k, c->v, c->k_scale, c->v_scale, c->format};
+  return HSA_OK;
+}
+
+// Rows of new tokens: their number, strides (elements) of rows of `heads` heads, the lists.
+int32_t check_rows(const Shape& s, const int32_t* cu, int32_t total, const int32_t* page_table,
+                   const int32_t* seq_lens) {
+  if (!page_table || !seq_lens || total < 0) return HSA_ERR_INVALID_ARG;
+  if (!aligned(cu, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4))
+    return HSA_ERR_INVALID_ARG;
+  if (cu == nullptr && total != s.batch) return HSA_ERR_INVALID_ARG;
+  // work items (blocks x heads x K and V) are counted in 32 bits
+  if (((long long)total / hsa::kPage + 2 * s.batch) * s.hkv * 2 > INT32_MAX / 2)
+    return HSA_ERR_UNSUPPORTED;
+  return HSA_OK;
+}
+int32_t check_row_array(const void* p, int64_t stride, int heads) {
+  if (!p || !aligned(p, 16)) return HSA_ERR_INVALID_ARG;
+  if (stride < (int64_t)heads * hsa::kHeadDim || stride % 8 != 0 || stride > INT32_MAX)
+    return HSA_ERR_INVALID_ARG;
+  return HSA_OK;
+}
+// The error word of calls whose workspace is only that.
+int32_t error_word(void* workspace, size_t bytes, int** err) {
+  *err = nullptr;
+  if (workspace == nullptr) return HSA_OK;
+  if (!aligned(workspace, kAlign)) return HSA_ERR_INVALID_ARG;
+  if (bytes < kErrBytes) return HSA_ERR_WORKSPACE_TOO_SMALL;
+  *err = static_cast<int*>(workspace);
+  return HSA_OK;
+}
+
+int32_t do_kv8_attend(const hsa_dims* d, const hsa_kv8* cache, bool kept, const void* q,
+                      const int32_t* page_table, const int32_t* seq_lens,
+                      const int32_t* block_idx, const int32_t* n_blocks, float* out, float* lse,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  Shape s;
+  hsa::Kv8 c;
+  int32_t rc = check_kv8(d, cache, s, &c);
+  if (rc != HSA_OK) return rc;
+  if (!q || !page_table || !seq_lens || !out ||
+      (kept && (!n_blocks || (!block_idx && s.k2 > 0))))
+    return HSA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(page_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(block_idx, 4) || !aligned(n_blocks, 4))
+    return HSA_ERR_INVALID_ARG;
+  const Kv8Layout l = kv8_layout(s);
+  rc = check_ws(s, workspace, workspace_bytes, l.end);
+  if (rc != HSA_OK) return rc;
+  // the visits of a sequence's rows are counted in 32 bits
+  if (kept && (s.k2 + std::min<long long>(s.sink / hsa::kPage + 1, s.max_pages) +
+               std::min<long long>(s.window / hsa::kPage + 2, s.max_pages)) *
+                      (s.per_head ? s.hq : s.hkv) >
+                  UINT32_MAX)
+    return HSA_ERR_UNSUPPORTED;
+  s.key_bits = 8;  // the codes' tensor maps: 16 rows of 128 bytes a block
+  CUtensorMap km, vm, four;
+  rc = encode_kq_map(s, static_cast<const int8_t*>(c.k), &km, &four);
+  if (rc == HSA_OK) rc = encode_kq_map(s, static_cast<const int8_t*>(c.v), &vm, &four);
+  if (rc != HSA_OK) return rc;
+  char* ws = static_cast<char*>(workspace);
+  return cuda_status(hsa::launch_kv8_attend(
+      s, kept, c, km, vm, q, page_table, seq_lens, block_idx, n_blocks, out, lse,
+      reinterpret_cast<int*>(ws + l.counters), reinterpret_cast<float*>(ws + l.part_ml),
+      reinterpret_cast<float*>(ws + l.part_o), reinterpret_cast<int*>(ws), num_sms(),
+      as_stream(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -473,7 +565,8 @@ extern "C" {
 size_t hsa_workspace_bytes(const hsa_dims* d, int32_t op) {
   Shape s;
   const bool prune = op == HSA_OP_SELECT || op == HSA_OP_STEP;
-  if (check_dims(d, s, prune) != HSA_OK) return 0;
+  const bool kv8 = op == HSA_OP_KV8_DECODE;
+  if (check_dims(d, s, prune, kv8) != HSA_OK || (kv8 && d->kv_on_host)) return 0;
   switch (op) {
     case HSA_OP_QUANTIZE: return quantize_ws(s);
     case HSA_OP_SELECT: return select_ws(s);
@@ -481,6 +574,7 @@ size_t hsa_workspace_bytes(const hsa_dims* d, int32_t op) {
     case HSA_OP_DENSE: return attend_ws(s);
     case HSA_OP_STEP: return step_layout(s).end;
     case HSA_OP_CACHED: return cached_ws(s);
+    case HSA_OP_KV8_DECODE: return kv8_layout(s).end;
     default: return 0;
   }
 }
@@ -978,6 +1072,58 @@ int32_t hsa_decode_step_reuse(const hsa_dims* d, const hsa_step_io* io, void* k_
   return decode_step_impl(d, io, k_cache, v_cache, kq, k_scale, page_table, seq_lens,
                           const_cast<int32_t*>(block_idx), const_cast<int32_t*>(n_blocks),
                           workspace, workspace_bytes, stream, true);
+}
+
+int32_t hsa_kv8_write(const hsa_dims* d, const hsa_kv8* cache, const void* k_new,
+                      int64_t k_stride, const void* v_new, int64_t v_stride,
+                      const int32_t* cu_tokens, int32_t total_tokens, const int32_t* page_table,
+                      const int32_t* seq_lens, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  Shape s;
+  hsa::Kv8 c;
+  int* err = nullptr;
+  int32_t rc = check_kv8(d, cache, s, &c);
+  if (rc == HSA_OK) rc = check_rows(s, cu_tokens, total_tokens, page_table, seq_lens);
+  if (rc == HSA_OK) rc = check_row_array(k_new, k_stride, s.hkv);
+  if (rc == HSA_OK) rc = check_row_array(v_new, v_stride, s.hkv);
+  if (rc == HSA_OK) rc = error_word(workspace, workspace_bytes, &err);
+  if (rc != HSA_OK || total_tokens == 0) return rc;
+  return cuda_status(hsa::launch_kv8_write(s, c, k_new, k_stride, v_new, v_stride, cu_tokens,
+                                           total_tokens, page_table, seq_lens, err,
+                                           as_stream(stream)));
+}
+
+int32_t hsa_kv8_read(const hsa_dims* d, const hsa_kv8* cache, void* k_out, int64_t k_stride,
+                     void* v_out, int64_t v_stride, const int32_t* cu_tokens,
+                     int32_t total_tokens, const int32_t* page_table, const int32_t* seq_lens,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  Shape s;
+  hsa::Kv8 c;
+  int* err = nullptr;
+  int32_t rc = check_kv8(d, cache, s, &c);
+  if (rc == HSA_OK) rc = check_rows(s, cu_tokens, total_tokens, page_table, seq_lens);
+  if (rc == HSA_OK) rc = check_row_array(k_out, k_stride, s.hkv);
+  if (rc == HSA_OK) rc = check_row_array(v_out, v_stride, s.hkv);
+  if (rc == HSA_OK) rc = error_word(workspace, workspace_bytes, &err);
+  if (rc != HSA_OK || total_tokens == 0) return rc;
+  return cuda_status(hsa::launch_kv8_read(s, c, k_out, k_stride, v_out, v_stride, cu_tokens,
+                                          total_tokens, page_table, seq_lens, err,
+                                          as_stream(stream)));
+}
+
+int32_t hsa_kv8_decode(const hsa_dims* d, const hsa_kv8* cache, const void* q,
+                       const int32_t* page_table, const int32_t* seq_lens, float* out,
+                       float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return do_kv8_attend(d, cache, false, q, page_table, seq_lens, nullptr, nullptr, out, lse,
+                       workspace, workspace_bytes, stream);
+}
+
+int32_t hsa_kv8_attend(const hsa_dims* d, const hsa_kv8* cache, const void* q,
+                       const int32_t* page_table, const int32_t* seq_lens,
+                       const int32_t* block_idx, const int32_t* n_blocks, float* out, float* lse,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  return do_kv8_attend(d, cache, true, q, page_table, seq_lens, block_idx, n_blocks, out, lse,
+                       workspace, workspace_bytes, stream);
 }
 
 int32_t hsa_read_device_error(void* workspace, void* stream, int32_t* code) {

@@ -164,4 +164,30 @@ cudaError_t launch_attend_select(const Shape& s, const void* q, const void* k_ca
                                  int32_t* block_idx, int32_t* n_blocks, float* out, float* lse,
                                  const AttendBuffers& buf, int* err, cudaStream_t st);
 
+// ---- kv8_cache.cu, kv8_attend.cu: the 8-bit K/V cache
+struct Kv8 {
+  void* k;  // codes [num_pages][hkv][16][128]
+  void* v;
+  float* k_scale;  // [num_pages][hkv]
+  float* v_scale;
+  int format;  // 0: int8, 1: E4M3
+};
+// cu nullable: one new token a sequence
+cudaError_t launch_kv8_write(const Shape& s, const Kv8& c, const void* k_new, long long k_stride,
+                             const void* v_new, long long v_stride, const int32_t* cu, int total,
+                             const int32_t* page_table, const int32_t* seq_lens, int* err,
+                             cudaStream_t st);
+cudaError_t launch_kv8_read(const Shape& s, const Kv8& c, void* k_out, long long k_stride,
+                            void* v_out, long long v_stride, const int32_t* cu, int total,
+                            const int32_t* page_table, const int32_t* seq_lens, int* err,
+                            cudaStream_t st);
+// part_ml [2 kKv8MaxCtas][8][2], part_o [2 kKv8MaxCtas][8 * 128], counters [batch][rows] (zero)
+constexpr int kKv8MaxCtas = 512;
+cudaError_t launch_kv8_attend(const Shape& s, bool kept, const Kv8& c, const CUtensorMap& k_map,
+                              const CUtensorMap& v_map, const void* q, const int32_t* page_table,
+                              const int32_t* seq_lens, const int32_t* block_idx,
+                              const int32_t* n_blocks, float* out, float* lse, int* counters,
+                              float* part_ml, float* part_o, int* err, int num_sms,
+                              cudaStream_t st);
+
 }  // namespace hsa

@@ -31,6 +31,8 @@ HSA_OP_ATTEND = 2
 HSA_OP_DENSE = 3
 HSA_OP_STEP = 4
 HSA_OP_CACHED = 5
+HSA_OP_KV8_DECODE = 6
+HSA_OP_KV8_PREFILL = 7
 
 # Every entry point declared in include/hsa.h.
 EXPORTS = (
@@ -40,6 +42,7 @@ EXPORTS = (
     "hsa_decode_step_kernels",
     "hsa_block_cache_bytes", "hsa_block_cache_mass", "hsa_attend_cached",
     "hsa_decode_step_cached",
+    "hsa_kv8_write", "hsa_kv8_read", "hsa_kv8_decode", "hsa_kv8_attend",
 )
 
 
@@ -63,6 +66,11 @@ class hsa_step_io(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p),
                 ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
                 ("io_on_host", ctypes.c_int32)]
+
+
+class hsa_kv8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int32)]
 
 
 _DIMS_CACHE: dict = {}  # field values -> their C struct (read-only to the library)
@@ -119,7 +127,8 @@ def load(path: Optional[str] = None):
     if not os.path.exists(path):
         raise RuntimeError(f"libhsa.so is not built ({path}); run __graft_entry__.build()")
     lib = ctypes.CDLL(path)
-    P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    C = ctypes.POINTER(hsa_kv8)
     D = ctypes.POINTER(hsa_dims)
     sig = {
         "hsa_workspace_bytes": (SZ, [D, I32]),
@@ -143,6 +152,10 @@ def load(path: Optional[str] = None):
         "hsa_read_device_error": (I32, [P, P, ctypes.POINTER(I32)]),
         "hsa_select_noalloc": (I32, [D, P, P, P, P, P, P, P, P, P, P]),
         "hsa_decode_step_kernels": (I32, [D]),
+        "hsa_kv8_write": (I32, [D, C, P, I64, P, I64, P, I32, P, P, P, SZ, P]),
+        "hsa_kv8_read": (I32, [D, C, P, I64, P, I64, P, I32, P, P, P, SZ, P]),
+        "hsa_kv8_decode": (I32, [D, C, P, P, P, P, P, P, SZ, P]),
+        "hsa_kv8_attend": (I32, [D, C, P, P, P, P, P, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -371,6 +384,80 @@ def hsa_decode_step_cached(d: Dims, q, k_new, v_new, out, lse, k_cache, v_cache,
 def hsa_decode_step_kernels(d: Dims) -> int:
     """Kernels that hsa_decode_step launches for d (device I/O)."""
     return int(load().hsa_decode_step_kernels(ctypes.byref(d.c())))
+
+
+class KV8:
+    """The 8-bit K/V cache of include/hsa.h: code tensors k and v [num_pages][hkv][16][128],
+    both torch.int8 or both torch.float8_e4m3fn (the format follows), and float32 scales
+    [num_pages][hkv]. Keeps the tensors; the C struct is built once."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        formats = {torch.int8: 0, torch.float8_e4m3fn: 1}
+        for codes, scale in ((k, k_scale), (v, v_scale)):
+            if (codes.dtype not in formats or codes.dtype != k.dtype or codes.dim() != 4 or
+                    codes.shape != k.shape or scale.shape != k.shape[:2] or
+                    scale.dtype != torch.float32 or not codes.is_contiguous() or
+                    not scale.is_contiguous()):
+                raise HsaError("KV8", HSA_ERR_INVALID_ARG, "shapes, types or layout rejected")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._c = hsa_kv8(_p(k), _p(v), _p(k_scale), _p(v_scale), formats[k.dtype])
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def zeros(cls, d: Dims, fp8: bool = False, device="cuda"):
+        """An empty cache for d's pages: int8 codes, or FP8 E4M3 ones."""
+        codes = [torch.zeros((d.num_pages, d.hkv, 16, 128), dtype=torch.int8, device=device)
+                 for _ in range(2)]
+        if fp8:
+            codes = [c.view(torch.float8_e4m3fn) for c in codes]
+        return cls(*codes, *(torch.zeros((d.num_pages, d.hkv), dtype=torch.float32, device=device)
+                             for _ in range(2)))
+
+
+def _row_stride(name: str, t, heads: int) -> int:
+    """The row stride of a bf16 tensor [tokens][heads][128] whose rows are contiguous."""
+    if (t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or
+            t.stride(1) != t.shape[2] or t.stride(2) != 1):
+        raise HsaError(name, HSA_ERR_INVALID_ARG, "rows must be bf16 [tokens][heads][128]")
+    return t.stride(0)
+
+
+def hsa_kv8_write(d: Dims, cache: KV8, k_new, v_new, cu_tokens, page_table, seq_lens, ws=None,
+                  stream=None) -> None:
+    """k_new / v_new: bf16 [total_tokens][hkv][128], rows contiguous (any row stride)."""
+    if v_new.shape[0] != k_new.shape[0]:
+        raise HsaError("hsa_kv8_write", HSA_ERR_INVALID_ARG, "k_new and v_new differ in rows")
+    _check("hsa_kv8_write", load().hsa_kv8_write(
+        ctypes.byref(d.c()), cache._ref, k_new.data_ptr(),
+        _row_stride("hsa_kv8_write", k_new, d.hkv), v_new.data_ptr(),
+        _row_stride("hsa_kv8_write", v_new, d.hkv), _p(cu_tokens), k_new.shape[0], _p(page_table),
+        _p(seq_lens), _p(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+
+
+def hsa_kv8_read(d: Dims, cache: KV8, k_out, v_out, cu_tokens, page_table, seq_lens, ws=None,
+                 stream=None) -> None:
+    """k_out / v_out: bf16 [total_tokens][hkv][128], rows contiguous (any row stride)."""
+    if v_out.shape[0] != k_out.shape[0]:
+        raise HsaError("hsa_kv8_read", HSA_ERR_INVALID_ARG, "k_out and v_out differ in rows")
+    _check("hsa_kv8_read", load().hsa_kv8_read(
+        ctypes.byref(d.c()), cache._ref, k_out.data_ptr(),
+        _row_stride("hsa_kv8_read", k_out, d.hkv), v_out.data_ptr(),
+        _row_stride("hsa_kv8_read", v_out, d.hkv), _p(cu_tokens), k_out.shape[0], _p(page_table),
+        _p(seq_lens), _p(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+
+
+def hsa_kv8_decode(d: Dims, cache: KV8, q, page_table, seq_lens, out, lse, ws,
+                   stream=None) -> None:
+    _check("hsa_kv8_decode", load().hsa_kv8_decode(
+        ctypes.byref(d.c()), cache._ref, _p(q), _p(page_table), _p(seq_lens), _p(out), _p(lse),
+        _p(ws), ws.numel(), _stream(stream)))
+
+
+def hsa_kv8_attend(d: Dims, cache: KV8, q, page_table, seq_lens, block_idx, n_blocks, out, lse,
+                   ws, stream=None) -> None:
+    _check("hsa_kv8_attend", load().hsa_kv8_attend(
+        ctypes.byref(d.c()), cache._ref, _p(q), _p(page_table), _p(seq_lens), _p(block_idx),
+        _p(n_blocks), _p(out), _p(lse), _p(ws), ws.numel(), _stream(stream)))
 
 
 def hsa_read_device_error(ws, stream=None) -> int:

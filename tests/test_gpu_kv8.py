@@ -1,0 +1,305 @@
+"""The 8-bit K/V cache on the GPU against its numpy oracle: writes bit for bit, values read
+back bit for bit, decode attention (dense and over kept blocks) within derived fp32 bounds."""
+import numpy as np
+import pytest
+import torch
+
+from kv8_harness import (D, PAGE, Batch, assert_rows, assert_same_cache, bf16, codes_of, to_bf16)
+from kv_cache_int8_gb300 import hsa
+from oracle import kv8 as O
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = ["int8", "e4m3"]
+
+
+def error_word():
+    return torch.zeros(256, dtype=torch.uint8, device="cuda")
+
+
+def cu_of(new):
+    return torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+
+
+# ---------------------------------------------------------------------------------- write
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("hkv,before,new", [
+    (1, [0], [1]), (1, [0], [16]), (2, [0], [17]), (1, [5], [3]), (8, [15, 16, 17], [1, 1, 1]),
+    (2, [0, 0, 100, 31, 7], [40, 0, 33, 1, 9]), (3, [1, 250], [300, 5]), (4, [12] * 9, [4] * 9),
+])
+def test_write_matches_the_definition(fmt, hkv, before, new):
+    lens = [a + n for a, n in zip(before, new)]
+    s = Batch(lens, hkv, hkv, fmt, seed=hkv, fill=False)
+    for b, a in enumerate(before):  # older tokens, of half the size: most scales will grow
+        if a:
+            O.write(s.cache, bf16(0.5 * s.rows(a)), bf16(0.5 * s.rows(a)), s.table[b], 0)
+    cache = s.gpu_cache()
+    k, v = s.rows(sum(new), True), s.rows(sum(new))
+    at = 0
+    for b, n in enumerate(new):
+        O.write(s.cache, k[at:at + n], v[at:at + n], s.table[b], before[b])
+        at += n
+    err = error_word()
+    hsa.hsa_kv8_write(s.dims(), cache, to_bf16(k), to_bf16(v), cu_of(new), s.gpu_table(),
+                      s.gpu_lens(), err)
+    assert hsa.hsa_read_device_error(err) == 0
+    assert_same_cache(cache, s.cache)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_token_by_token_writes(fmt):
+    """A decode loop's appends without offsets; rows are slices of one fused projection."""
+    hkv, steps = 2, 37
+    s = Batch([steps, steps + 11, steps + 16], 4, hkv, fmt, seed=5, fill=False)
+    for b, a in ((1, 11), (2, 16)):
+        O.write(s.cache, s.rows(a), s.rows(a), s.table[b], 0)
+    cache, table = s.gpu_cache(), s.gpu_table()
+    for i in range(steps):
+        qkv = bf16(s.rng.standard_normal((3, 4 + 2 * hkv, D)) * (1 + i % 5))
+        dev = to_bf16(qkv)
+        hsa.hsa_kv8_write(s.dims(), cache, dev[:, 4:4 + hkv], dev[:, 4 + hkv:], None, table,
+                          s.gpu_lens([i + 1, i + 12, i + 17]))
+        for b, a in enumerate((0, 11, 16)):
+            O.write(s.cache, qkv[b:b + 1, 4:4 + hkv], qkv[b:b + 1, 4 + hkv:], s.table[b], a + i)
+    assert_same_cache(cache, s.cache)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_write_of_awkward_values(fmt):
+    """Zero blocks, the smallest and largest numbers, infinities and NaN, ties between codes."""
+    s = Batch([16 * 7], 1, 1, fmt, fill=False)
+    x = np.zeros((16 * 7, 1, D), np.float32)
+    x[16:32] = bf16(s.rng.standard_normal((16, 1, D)) * 2.0 ** -130)
+    x[32:48] = bf16(s.rng.standard_normal((16, 1, D)) * 2.0 ** 120)
+    x[48:64] = s.rows(16)
+    x[50, 0, 3], x[51, 0, 4], x[52, 0, 5] = np.inf, -np.inf, np.nan
+    x[64:80] = np.nan
+    x[70, 0, 0] = np.inf
+    x[80:96] = bf16(np.arange(16 * D).reshape(16, 1, D) % 255 - 127) / 2  # halves of codes
+    x[80, 0, 0] = 127
+    x[96:112] = bf16(np.arange(16 * D).reshape(16, 1, D) % 448)
+    x[96, 0, 0] = 448
+    cache = s.gpu_cache()
+    O.write(s.cache, x, -x, s.table[0], 0)
+    hsa.hsa_kv8_write(s.dims(), cache, to_bf16(x), to_bf16(-x), cu_of([len(x)]), s.gpu_table(),
+                      s.gpu_lens())
+    assert_same_cache(cache, s.cache)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_rewriting_a_rejected_draft(fmt):
+    """Positions written twice: the block keeps its scale, the older tokens their codes."""
+    s = Batch([30], 1, 1, fmt, seed=9, fill=False)
+    O.write(s.cache, s.rows(20), s.rows(20), s.table[0], 0)
+    cache = s.gpu_cache()
+    for scale in (3.0, 0.25):
+        k, v = bf16(scale * s.rows(10)), bf16(scale * s.rows(10))
+        O.write(s.cache, k, v, s.table[0], 20)
+        hsa.hsa_kv8_write(s.dims(), cache, to_bf16(k), to_bf16(v), cu_of([10]), s.gpu_table(),
+                          s.gpu_lens())
+        assert_same_cache(cache, s.cache)
+
+
+def test_quantisation_error_of_whole_blocks():
+    """Half a step: int8 amax / 254, E4M3 2^-4 of the value (2^-10 of the scale when small)."""
+    for fmt in FORMATS:
+        s = Batch([640], 1, 1, fmt, seed=3, fill=False)
+        k, v = s.rows(640, True), s.rows(640)
+        cache = s.gpu_cache()
+        hsa.hsa_kv8_write(s.dims(), cache, to_bf16(k), to_bf16(v), cu_of([640]), s.gpu_table(),
+                          s.gpu_lens())
+        got = {**codes_of(cache), "fmt": fmt}
+        for name, x in (("k", k), ("v", v)):
+            y = O.values(got, name, s.table[0], 640, 0).reshape(40, 16, D)
+            x = x[:, 0].reshape(40, 16, D).astype(np.float64)
+            scale = np.abs(x).max((1, 2), keepdims=True) / float(O.LEVELS[fmt])
+            half = scale / 2 if fmt == "int8" else np.maximum(np.abs(x) * 2.0 ** -4,
+                                                              scale * 2.0 ** -10)
+            # s, 1 / s and x * inv are each rounded once: x * inv is off by up to 3 * 2^-24 of
+            # itself, at most 127 * 3 * 2^-24 = 2.3e-5 steps of an int8 code (4.6e-5 of half a
+            # step) and less of an E4M3 one
+            assert (np.abs(y - x) <= half * (1 + 5e-5)).all()
+
+
+# ----------------------------------------------------------------------------------- read
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("hkv,lens,new", [
+    (1, [1], [1]), (2, [100, 16, 7, 333], [100, 16, 7, 333]), (8, [50, 200], [3, 65]),
+    (4, [33, 20, 64], [0, 20, 1]),
+])
+def test_read_returns_the_values(fmt, hkv, lens, new):
+    s = Batch(lens, hkv, hkv, fmt, seed=2)
+    T = sum(new)
+    big = torch.full((T, 3 * hkv, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    hsa.hsa_kv8_read(s.dims(), s.gpu_cache(), big[:, hkv:2 * hkv], big[:, 2 * hkv:], cu_of(new),
+                     s.gpu_table(), s.gpu_lens())
+    at = 0
+    for b, (n, m) in enumerate(zip(lens, new)):
+        for h in range(hkv):
+            for name, off in (("k", hkv), ("v", 2 * hkv)):
+                want = O.values(s.cache, name, s.table[b], n, h)[n - m:]
+                got = big[at:at + m, off + h].float().cpu().numpy()
+                np.testing.assert_array_equal(got, bf16(want.astype(np.float32)))
+        at += m
+    assert (big[:, :hkv] == 7.0).all()  # between the rows: as it was
+
+
+# ------------------------------------------------------------------------- decode attention
+
+def run_decode(s, q, kept=None, **kw):
+    d = s.dims(**kw)
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_DECODE)
+    out = torch.full((len(s.lens), s.hq, D), float("nan"), device="cuda")
+    lse = torch.full((len(s.lens), s.hq), float("nan"), device="cuda")
+    args = (d, s.gpu_cache(), to_bf16(q), s.gpu_table(), s.gpu_lens())
+    if kept is None:
+        hsa.hsa_kv8_decode(*args, out, lse, ws)
+    else:
+        hsa.hsa_kv8_attend(*args, *kept, out, lse, ws)
+    assert hsa.hsa_read_device_error(ws) == 0
+    assert int(ws[256:256 + 4 * len(s.lens) * s.hq].sum()) == 0  # counters left at zero
+    return out.cpu().numpy(), lse.cpu().numpy()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("hq,hkv,lens", [
+    (1, 1, [1]), (4, 1, [16]), (8, 1, [17, 1000]), (3, 3, [15, 130, 2]), (10, 2, [257]),
+    (14, 2, [600, 0, 31]), (32, 8, [4096]), (24, 4, [0, 0]), (64, 8, [129, 2000, 1, 777]),
+    (8, 8, [300] * 40),
+])
+def test_dense_decode(fmt, hq, hkv, lens):
+    s = Batch(lens, hq, hkv, fmt, seed=hq, extra_pages=2)
+    q = bf16(s.rng.standard_normal((len(lens), hq, D)))
+    out, lse = run_decode(s, q)
+    g = hq // hkv
+    for b, n in enumerate(lens):
+        for h in range(hkv):
+            rows = slice(h * g, (h + 1) * g)
+            k, v = (O.values(s.cache, w, s.table[b], n, h) for w in "kv")
+            want, wl, tol = O.attend(q[b, rows], k, v, np.ones((g, n), bool), D ** -0.5)
+            assert_rows(out[b, rows], lse[b, rows], want, wl, tol)
+
+
+def test_dense_decode_of_extreme_queries_and_scale():
+    """Queries from 2^-40 to 2^30 in one group (the fp16 operands carry a power of two a head),
+    zero queries, a given softmax scale, logits far apart."""
+    s = Batch([500, 37], 8, 1, "int8", seed=4)
+    q = bf16(s.rng.standard_normal((2, 8, D)))
+    q *= (2.0 ** np.array([-40, -20, -3, 0, 2, 4, -100, 0], np.float32))[:, None]
+    q[:, 7] = 0
+    q[1, 4] *= np.float32(2.0 ** 26)  # one token takes everything
+    out, lse = run_decode(s, q, sm_scale=0.25)
+    for b, n in enumerate(s.lens):
+        k, v = (O.values(s.cache, w, s.table[b], n, 0) for w in "kv")
+        want, wl, tol = O.attend(q[b], k, v, np.ones((8, n), bool), 0.25)
+        assert_rows(out[b], lse[b], want, wl, tol)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("per_head", [0, 1])
+@pytest.mark.parametrize("sink,window,k2,lens", [
+    (0, 0, 4, [200, 64]), (4, 1, 8, [1000, 3, 5]), (20, 40, 0, [50, 61, 300]),
+    (64, 256, 16, [2048, 319, 0, 321]), (16, 37, 200, [5000]), (0, 0, 0, [90]),
+])
+def test_attend_over_kept_blocks(fmt, per_head, sink, window, k2, lens):
+    hq, hkv = 8, 2
+    g, rows = hq // hkv, hq if per_head else hkv
+    s = Batch(lens, hq, hkv, fmt, seed=k2 + 1)
+    q = bf16(s.rng.standard_normal((len(lens), hq, D)))
+    idx = np.full((len(lens), rows, max(k2, 1)), -1, np.int32)
+    cnt = np.zeros((len(lens), rows), np.int32)
+    for b, n in enumerate(lens):
+        for r in range(rows):
+            m = min(k2, s.rng.integers(0, k2 + 1), -(-n // PAGE))
+            # any blocks, those of the sink and the window too: they are clipped
+            idx[b, r, :m] = np.sort(s.rng.permutation(-(-n // PAGE))[:m])
+            cnt[b, r] = m
+    out, lse = run_decode(s, q, (torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda()),
+                          sink=sink, window=window, k2=k2, per_head=per_head)
+    for b, n in enumerate(lens):
+        t = np.arange(n)
+        for j in range(hq):
+            h, r = j // g, j if per_head else j // g
+            near = (t < sink) | (t >= n - window)
+            far = np.isin(t // PAGE, idx[b, r, :cnt[b, r]]) & (t >= sink) & (t < n - window)
+            k, v = (O.values(s.cache, w, s.table[b], n, h) for w in "kv")
+            want, wl, tol = O.attend(q[b, j:j + 1], k, v, (near | far)[None], D ** -0.5)
+            assert_rows(out[b, j:j + 1], lse[b, j:j + 1], want, wl, tol)
+
+
+def test_selection_ids_outside_the_context_add_nothing():
+    s = Batch([100], 2, 1, "int8", seed=6)
+    q = bf16(s.rng.standard_normal((1, 2, D)))
+    idx = torch.tensor([[[-5, 2, 6, 1 << 27, 40]]], dtype=torch.int32, device="cuda")
+    cnt = torch.tensor([[9]], dtype=torch.int32, device="cuda")  # more than k2
+    out, lse = run_decode(s, q, (idx, cnt), sink=8, window=4, k2=5)
+    t = np.arange(100)
+    seen = (t < 8) | (t >= 96) | (t // PAGE == 2) | ((t // PAGE == 6) & (t < 96))
+    k, v = (O.values(s.cache, w, s.table[0], 100, 0) for w in "kv")
+    want, wl, tol = O.attend(q[0], k, v, np.tile(seen, (2, 1)), D ** -0.5)
+    assert_rows(out[0], lse[0], want, wl, tol)
+
+
+def test_decode_is_the_same_every_time_and_from_a_graph():
+    """Bit-equal results call after call, on another stream, and replayed with new lengths."""
+    s = Batch([3000, 17, 900], 16, 4, "e4m3", seed=8)
+    q = to_bf16(s.rng.standard_normal((3, 16, D)))
+    d, cache, table, lens = s.dims(), s.gpu_cache(), s.gpu_table(), s.gpu_lens()
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_DECODE)
+    outs = [torch.empty(3, 16, D, device="cuda") for _ in range(4)]
+    for o in outs[:2]:
+        hsa.hsa_kv8_decode(d, cache, q, table, lens, o, None, ws)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        hsa.hsa_kv8_decode(d, cache, q, table, lens, outs[2], None, ws)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hsa.hsa_kv8_decode(d, cache, q, table, lens, outs[3], None, ws)
+    lens.copy_(torch.tensor([5, 1, 2], device="cuda"))
+    graph.replay()
+    torch.cuda.synchronize()
+    short = outs[3].clone()
+    lens.copy_(s.gpu_lens())
+    graph.replay()
+    torch.cuda.synchronize()
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+    assert not torch.equal(short, outs[0])
+
+
+# -------------------------------------------------------------------------- bad page tables
+
+def test_bad_pages_and_lengths_are_reported_not_followed():
+    s = Batch([40, 64, 50], 2, 1, "int8", seed=1)
+    table = s.gpu_table()
+    table[0, 1] = s.num_pages          # one past the pool
+    lens = s.gpu_lens([40, 64, 16 * s.max_pages + 1])  # longer than its page-table row
+    d, cache = s.dims(), s.gpu_cache()
+    before = codes_of(cache)
+    k = to_bf16(s.rows(40 + 64 + 4))
+    cu = cu_of([40, 64, 4])
+    err = error_word()
+    hsa.hsa_kv8_write(d, cache, k, k, cu, table, lens, err)
+    assert hsa.hsa_read_device_error(err) == hsa.HSA_ERR_DEVICE_CHECK
+    after = codes_of(cache)
+    untouched = np.setdiff1d(np.arange(s.num_pages), np.r_[s.table[0, [0, 2]], s.table[1]])
+    np.testing.assert_array_equal(after["k"][untouched], before["k"][untouched])
+    outs = torch.full((108, 1, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    hsa.hsa_kv8_read(d, cache, outs, outs.clone(), cu, table, lens, err)
+    assert hsa.hsa_read_device_error(err) == hsa.HSA_ERR_DEVICE_CHECK
+    assert (outs[16:32] == 3.0).all() and (outs[104:] == 3.0).all()
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_DECODE)
+    out, lse = torch.empty(3, 2, D, device="cuda"), torch.empty(3, 2, device="cuda")
+    q = to_bf16(s.rng.standard_normal((3, 2, D)))
+    hsa.hsa_kv8_decode(d, cache, q, table, lens, out, lse, ws)
+    assert hsa.hsa_read_device_error(ws) == hsa.HSA_ERR_DEVICE_CHECK
+    assert torch.isfinite(out).all() and (out[2] == 0).all() and torch.isneginf(lse[2]).all()
+    # rows that do not fit the arrays
+    for bad in ([0, 40, 104, 200], [0, -3, 104, 108], [0, 40, 30, 108]):
+        hsa.hsa_kv8_write(d, cache, k, k, torch.tensor(bad, dtype=torch.int32, device="cuda"),
+                          s.gpu_table(), s.gpu_lens(), err)
+        assert hsa.hsa_read_device_error(err) == hsa.HSA_ERR_DEVICE_CHECK
