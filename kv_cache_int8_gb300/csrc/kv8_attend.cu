@@ -9,24 +9,31 @@
 // Both products run on the matrix pipe with fp16 operands and fp32 sums, and nothing is rounded
 // that matters: the codes are exact in fp16; a head's query is multiplied by the power of two
 // that puts its largest value in [2^13, 2^14), which makes every bf16 value down to 2^-27 of
-// that one exact in fp16; a probability p is split into fp16 hi + lo, 22 bits together (p is
-// carried 2^6 larger than 2^(x - m), and m may lag the maximum by up to 2^8, so p stays below
-// 2^14). The scales multiply the fp32 results, a block at a time.
+// that one exact in fp16; a probability is carried as 2^(x - m + 10), where m may lag the
+// maximum by up to 4, times its block's s_v in units of a power of two that follows the largest
+// s_v so far (below 2^15), and is split into fp16 hi + lo, 22 bits together. The relative error
+// against 64 bits is 3 to 5e-7 (2-norm).
 //
 // Layout. K's block is the left operand [16 tokens][128 channels], the group's heads (up to 8)
 // the 8 columns of m16n8k16; V's block enters transposed, 8 tiles of 16 channels. So a group of
 // 8 heads wastes no product, and scores, probabilities and outputs keep one layout: a lane has
 // heads 2t, 2t + 1. Which channel a product's k index stands for is free as long as both sides
 // agree: a lane takes whole 16-byte chunks, and the 128-byte swizzle of the tensor copies makes
-// all its reads free of bank conflicts.
+// all its reads free of bank conflicts. (tcgen05 would want 128 rows of queries; there are 8.)
 //
-// Work. Memory bound: a block's 4 KiB cost an SM about 175 cycles at the HBM rate, the products
-// a third of that. Every warp streams its own blocks through its own ring of tensor copies
-// (kStages blocks of K and V), no barriers between warps. All blocks of all rows (sequence, kv
-// head) form one line that is cut into equal slices, one a CTA, so ragged batches balance
-// without the host knowing any length; where a slice ends inside a row, the row's parts meet in
-// the workspace and the last CTA to arrive joins them in slice order (the result does not
-// depend on which one that is).
+// Work. Memory bound: a block's 4 KiB cost an SM about 175 cycles at the HBM rate, its
+// instructions about 100 of each scheduler's issue slots. Every warp streams its own blocks
+// through its own ring of tensor copies, no barriers between warps, two blocks at a time (two
+// independent chains of products). One CTA of 16 warps an SM: two of 8 had the same loop but
+// twice the parts to join (128K tokens 59 us). All blocks of all rows (sequence, kv head) form
+// one line that is cut into equal slices, one a CTA, so ragged batches balance without the host
+// knowing any length; where a slice ends inside a row, the row's parts meet in the workspace
+// and the last CTA to arrive joins them in slice order (the result does not depend on which one
+// that is).
+//
+// Measured (GB300, copy 6.8 TB/s; 32 query heads over 8): 8 x 32-128K tokens, groups of 8,
+// int8: 222 us, 6.35 TB/s; one sequence of 128K tokens: 53 us, 5.05 TB/s, of which about 7 us
+// pass before the first blocks are there everywhere and 5 us in joining; 8K tokens: 12 us.
 #include "kv8.cuh"
 
 #include <cmath>
@@ -36,14 +43,16 @@ namespace {
 
 using namespace kv8_detail;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;  // one CTA an SM
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 2;
+constexpr int kStages = 3;                     // a warp's ring: blocks in flight or in use
+constexpr int kMeta = 32, kBatch = 16;         // a warp's visits known ahead, fetched 16 at once
 constexpr int kUnitBytes = 2 * kBlockBytesI8;  // K block, then V block
 constexpr int kMinUnits = kWarps;              // smallest slice: one block a warp
 constexpr int kTile = 8 * kHeadDim;            // output values of a row (8 heads)
-constexpr float kHeadroom = 6.0f;              // p is 2^(x - m + kHeadroom)
-constexpr float kLag = 8.0f;                   // m follows a maximum that is this much larger
+constexpr int kAhead = 24;                     // parts of a row joined at a time
+constexpr float kHeadroom = 10.0f;             // p is 2^(x - m + kHeadroom)
+constexpr float kLag = 4.0f;                   // m follows a maximum that is this much larger
 
 struct Params {
   const __nv_bfloat16* q;
@@ -69,6 +78,18 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// d = a b
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1,
+                                              uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+      " {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// c += a b
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -84,10 +105,25 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
+__device__ __forceinline__ uint32_t word(const uint4& u, int w) {
+  return w == 0 ? u.x : w == 1 ? u.y : w == 2 ? u.z : u.w;
+}
+
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
+}
+
+__device__ __forceinline__ float max32(float x) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+  return x;
+}
+__device__ __forceinline__ float sum32(float x) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
 }
 
 // Units (blocks to visit) of a row of a sequence of n tokens. Kept form: the sink's blocks, the
@@ -102,15 +138,20 @@ __device__ __forceinline__ int row_units(const Params& p, int n) {
 }
 
 // One visit: the block's first row in the code arrays, its slots [lo, hi), its scales.
-struct Unit {
+struct alignas(16) Unit {
   int y;
   int span;  // lo | hi << 8; 0: nothing to do
   float sk, sv;
 };
 
+// Places of a row on the line: with per > 0 a whole number of slices of `per`.
+__device__ __forceinline__ unsigned row_places(unsigned units, unsigned per) {
+  return per > 0 ? (units + per - 1) / per * per : units;
+}
+
 template <bool kKept>
 __device__ __forceinline__ Unit locate(const Params& p, const long long* pre, const int* lens,
-                                       long long x) {
+                                       unsigned per, long long x) {
   int lo_b = 0, hi_b = p.batch;  // the sequence with pre[b] <= x < pre[b + 1]
   while (hi_b - lo_b > 1) {
     const int mid = (lo_b + hi_b) >> 1;
@@ -118,9 +159,12 @@ __device__ __forceinline__ Unit locate(const Params& p, const long long* pre, co
     else hi_b = mid;
   }
   const int b = lo_b, n = lens[b];
-  const unsigned u = row_units<kKept>(p, n);
+  const int units = row_units<kKept>(p, n);
+  const unsigned u = row_places(units, per);
   const unsigned at = (unsigned)(x - pre[b]);
   const int row = at / u, i = at % u;
+  Unit t = {0, 0, 0.0f, 0.0f};
+  if (i >= units) return t;
   int pg = i, lo = 0, hi = n;  // token range
   if (kKept) {
     const int head = min(p.sink, n), tail = max(n - p.window, head);
@@ -139,7 +183,6 @@ __device__ __forceinline__ Unit locate(const Params& p, const long long* pre, co
       hi = n - p.window;
     }
   }
-  Unit t = {0, 0, 0.0f, 0.0f};
   if (pg < 0 || pg >= p.max_pages) return t;
   lo = max(lo - pg * kPage, 0);
   hi = min(hi - pg * kPage, kPage);
@@ -158,18 +201,23 @@ __device__ __forceinline__ Unit locate(const Params& p, const long long* pre, co
 }
 
 struct Smem {
+  // a warp's blocks; where the warps' parts of a row meet, the slot it has just read holds its
+  // outputs (float4 [channel tile][lane], 4 KiB as well)
   alignas(1024) unsigned char ring[kWarps][kStages][kUnitBytes];
-  float4 o[kWarps][8][32];  // the warps' outputs: [channel tile][lane]
-  float ml[kWarps][8][2];
-  float total[8][2];  // a joined row's (m, l)
+  Unit meta[kWarps][kMeta];
+  float2 ml[8][kWarps];      // a head's (m, l) of each warp
+  float weight[kAhead][8];   // of the warps, then of the parts: 2^(m - the largest m)
+  float2 total[8];           // a row's (m, l)
+  int slot[kWarps];   // the ring slot of each warp's outputs
   alignas(8) uint64_t full[kWarps][kStages];
-  long long warp_sum[kWarps];
   int last;
+  long long per;
+  unsigned align;
 };
 // behind it: pre (long long [batch + 1]), lens (int [batch])
 
 template <int F, bool kKept>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     kv8_attend_kernel(const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map, const Params p) {
   extern __shared__ unsigned char smem_raw[];
@@ -179,48 +227,70 @@ __global__ void __launch_bounds__(kThreads, 2)
   int* lens = reinterpret_cast<int*>(pre + p.batch + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
 
-  // ---- the line of all units and this CTA's slice of it
-  const int per_thread = (p.batch + kThreads - 1) / kThreads;
-  long long sum = 0;
-  for (int k = 0; k < per_thread; k++) {
-    const int b = tid * per_thread + k;
-    if (b >= p.batch) break;
-    int n = p.seq_lens[b];
-    if (n < 0 || n > p.max_pages * kPage) {
-      set_error(p.err, kDevErrCheck);
-      n = 0;
-    }
-    lens[b] = n;
-    sum += (long long)row_units<kKept>(p, n) * p.rows;
-  }
-  long long incl = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += v;
-  }
-  if (lane == 31) sm.warp_sum[warp] = incl;
-  if (lane < kStages) mbar_init(&sm.full[warp][lane], 1);
   if (tid == 0) {
     tma_prefetch_descriptor(&k_map);
     tma_prefetch_descriptor(&v_map);
   }
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // ---- the line of all units and this CTA's slice of it
+  if (lane < kStages) mbar_init(&sm.full[warp][lane], 1);
   fence_barrier_init();
-  __syncthreads();
-  {
-    long long before = incl - sum;
-    for (int w = 0; w < warp; w++) before += sm.warp_sum[w];
-    for (int k = 0; k < per_thread; k++) {
-      const int b = tid * per_thread + k;
-      if (b >= p.batch) break;
-      pre[b] = before;
-      before += (long long)row_units<kKept>(p, lens[b]) * p.rows;
-      if (b == p.batch - 1) pre[p.batch] = before;
+  if (warp == 0) {
+    auto lay = [&](unsigned per) {  // pre from lens; the line's length
+      long long sum = 0;
+      for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        const unsigned units = b < p.batch ? row_units<kKept>(p, lens[b]) : 0;
+        long long incl = (long long)row_places(units, per) * p.rows;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += v;
+        }
+        if (b < p.batch) pre[b + 1] = sum + incl;
+        sum += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      return sum;
+    };
+    for (int b = lane; b < p.batch; b += 32) {
+      int n = p.seq_lens[b];
+      if (n < 0 || n > p.max_pages * kPage) {
+        set_error(p.err, kDevErrCheck);
+        n = 0;
+      }
+      lens[b] = n;
+    }
+    __syncwarp();
+    const long long sum = lay(0);
+    // Slices of `per` units. With at least two CTAs a row, the smallest of 32 sizes from the
+    // even cut on under which rows can begin with a slice of their own is taken: a CTA that
+    // ends one row and begins the next joins parts twice, 5 us at 128K tokens, the time of 54
+    // units.
+    long long per = max((sum + gridDim.x - 1) / gridDim.x, (long long)kMinUnits);
+    unsigned align = 0;
+    if (2LL * p.batch * p.rows <= gridDim.x) {
+      const unsigned mine = (unsigned)per + lane;
+      long long slices = 0;
+      for (int b = 0; b < p.batch; b++)
+        slices += (long long)((row_units<kKept>(p, lens[b]) + mine - 1) / mine) * p.rows;
+      const unsigned fits = __ballot_sync(0xffffffffu, slices <= gridDim.x);
+      if (fits != 0) {
+        per = align = (unsigned)per + __ffs(fits) - 1;
+        lay(align);
+      }
+    }
+    if (lane == 0) {
+      pre[0] = 0;
+      sm.per = per;
+      sm.align = align;
     }
   }
   __syncthreads();
+  const long long per = sm.per;
+  const unsigned align = sm.align;
   const long long all = pre[p.batch];
-  const long long per = max((all + gridDim.x - 1) / gridDim.x, (long long)kMinUnits);
   const long long begin = min(blockIdx.x * per, all), end = min(begin + per, all);
 
   // rows of no units at all
@@ -233,36 +303,46 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   if (begin >= end) return;
 
-  // ---- this warp's units: begin + warp + kWarps i; lane l holds those of i = 32 k + l
+  // ---- this warp's visits: places begin + warp + kWarps i, located kBatch at a time
   const long long x0 = begin + warp;
   const int mine = x0 < end ? (int)((end - x0 + kWarps - 1) / kWarps) : 0;
   auto fetch = [&](int i0) {
     const long long x = x0 + (long long)kWarps * (i0 + lane);
     Unit u = {0, 0, 0.0f, 0.0f};
-    if (x < end) u = locate<kKept>(p, pre, lens, x);
+    if (lane < kBatch && x < end) u = locate<kKept>(p, pre, lens, align, x);
     return u;
   };
-  Unit cur = fetch(0), next = mine > 32 ? fetch(32) : Unit{0, 0, 0.0f, 0.0f};
+  Unit* meta = sm.meta[warp];
+  auto store = [&](int i0, const Unit& u) {
+    __syncwarp();
+    if (lane < kBatch) meta[(i0 + lane) % kMeta] = u;
+    __syncwarp();
+  };
+  store(0, fetch(0));
+  int filled = kBatch;
+  bool pending = false;
+  Unit ahead = {0, 0, 0.0f, 0.0f};
   const uint64_t policy = l2_evict_first_policy();
+  int asked = 0;              // visits whose copies were begun (those that have any)
   int issued = 0, taken = 0;  // copies begun and waited for
   bool dead = false;
-  auto issue = [&](int i, int batch0) {
-    if (i >= mine) return;
-    const bool ahead = (i >> 5) != batch0;
-    const int span = __shfl_sync(0xffffffffu, ahead ? next.span : cur.span, i & 31);
-    const int y = __shfl_sync(0xffffffffu, ahead ? next.y : cur.y, i & 31);
-    if (span == 0 || dead) return;
-    if (lane == 0) {
-      const int st = issued % kStages;
-      unsigned char* dst = sm.ring[warp][st];
-      mbar_arrive_expect_tx(&sm.full[warp][st], kUnitBytes);
-      tma_load_2d_hint(dst, &k_map, 0, y, &sm.full[warp][st], policy);
-      tma_load_2d_hint(dst + kBlockBytesI8, &v_map, 0, y, &sm.full[warp][st], policy);
+  // Begins the copies of the visits before `upto`. Those of later rows (from place `stop` on)
+  // leave one slot of the ring free: the row's outputs will lie there.
+  auto issue_to = [&](int upto, long long stop) {
+    for (upto = min(upto, mine); asked < upto; asked++) {
+      const Unit& u = meta[asked % kMeta];
+      if (u.span == 0 || dead) continue;
+      if (issued - taken >= kStages - (x0 + (long long)kWarps * asked < stop ? 0 : 1)) break;
+      if (lane == 0) {
+        const int st = issued % kStages;
+        unsigned char* dst = sm.ring[warp][st];
+        mbar_arrive_expect_tx(&sm.full[warp][st], kUnitBytes);
+        tma_load_2d_hint(dst, &k_map, 0, u.y, &sm.full[warp][st], policy);
+        tma_load_2d_hint(dst + kBlockBytesI8, &v_map, 0, u.y, &sm.full[warp][st], policy);
+      }
+      issued++;
     }
-    issued++;
   };
-#pragma unroll
-  for (int i = 0; i < kStages; i++) issue(i, 0);
 
   int i = 0;
   for (long long x = begin; x < end;) {
@@ -274,10 +354,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       else hi_b = mid;
     }
     const int b = lo_b;
-    const unsigned units = row_units<kKept>(p, lens[b]);
+    const unsigned units = row_places(row_units<kKept>(p, lens[b]), align);
     const int row = (int)((unsigned)(x - pre[b]) / units);
     const long long row_begin = pre[b] + (long long)row * units, row_end = row_begin + units;
     const long long stop = min(row_end, end);
+    issue_to(i + kStages, stop);
 
     // ---- the query as right operands: head g, channels of chunk 2t + c, word w
     uint32_t qf[16];
@@ -312,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int k = 0; k < 4; k++)
           qf[c * 4 + k] = half_pair(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
       }
-      const float f = p.scale_log2 * Codes<F>::kUnit * down;
+      const float f = p.scale_log2 * down;
       f0 = __shfl_sync(0xffffffffu, f, (2 * t) * 4);
       f1 = __shfl_sync(0xffffffffu, f, (2 * t + 1) * 4);
     }
@@ -324,47 +405,77 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int c = 0; c < 4; c++) o[k][c] = 0.0f;
 
-    for (; i < mine && x0 + (long long)kWarps * i < stop; i++) {
-      if (i > 0 && (i & 31) == 0) {
-        cur = next;
-        next = fetch(i + 32);
+    // o carries the values in units of 2^e0, e0 the largest exponent of a block's scale so far
+    float inv_unit = __uint_as_float(253u << 23);  // 2^-e0
+
+    // two visits at a time: two independent chains of products, one reduction of the maximum
+    while (i < mine && x0 + (long long)kWarps * i < stop) {
+      const int two = i + 1 < mine && x0 + (long long)kWarps * (i + 1) < stop;
+      if (!pending && filled < mine && filled - i <= kBatch) {
+        ahead = fetch(filled);
+        pending = true;
+      } else if (pending && filled - i <= kBatch / 2) {
+        store(filled, ahead);
+        filled += kBatch;
+        pending = false;
       }
-      const int src = i & 31;
-      const int span = __shfl_sync(0xffffffffu, cur.span, src);
-      if (span != 0 && !dead) {
-        const float sk = __shfl_sync(0xffffffffu, cur.sk, src);
-        const float sv = __shfl_sync(0xffffffffu, cur.sv, src) * Codes<F>::kUnit;
-        const int st = taken % kStages;
-        if (!mbar_wait(&sm.full[warp][st], (taken / kStages) & 1)) {
-          set_error(p.err, kDevErrTimeout);
-          dead = true;
+      const Unit ua = meta[i % kMeta];
+      Unit ub = meta[(i + 1) % kMeta];
+      if (!two) ub.span = 0;
+      if ((ua.span | ub.span) != 0 && !dead) {
+        uint32_t kb[2], slot[2];
+        const int span[2] = {ua.span, ub.span};
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          slot[h] = (taken % kStages);
+          kb[h] = smem_addr(sm.ring[warp][slot[h]]);
+          if (span[h] == 0) continue;
+          if (!mbar_wait(&sm.full[warp][slot[h]], (taken / kStages) & 1)) {
+            set_error(p.err, kDevErrTimeout);
+            dead = true;
+          }
+          taken++;
         }
-        taken++;
-        const uint32_t kb = smem_addr(sm.ring[warp][st]), vb = kb + kBlockBytesI8;
-        // scores of tokens g and g + 8
-        float sa[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        // scores of tokens g (x[h][0], x[h][1]) and g + 8 (x[h][2], x[h][3])
+        float x[2][4];
 #pragma unroll
         for (int c = 0; c < 2; c++) {
-          const uint32_t at = kb + g * kHeadDim + (((2 * t + c) ^ g) << 4);
-          const uint4 ka = lds128(at), kc = lds128(at + 8 * kHeadDim);
-          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wc[4] = {kc.x, kc.y, kc.z, kc.w};
+          uint4 ka[2], kc[2];
 #pragma unroll
-          for (int w = 0; w < 4; w++) {
-            const uint32_t a = Codes<F>::prepare(wa[w]), d = Codes<F>::prepare(wc[w]);
-            mma16816(w & 1 ? sb : sa, Codes<F>::template pair<0>(a),
-                     Codes<F>::template pair<0>(d), Codes<F>::template pair<1>(a),
-                     Codes<F>::template pair<1>(d), qf[c * 8 + w * 2], qf[c * 8 + w * 2 + 1]);
+          for (int h = 0; h < 2; h++) {
+            const uint32_t at = kb[h] + g * kHeadDim + (((2 * t + c) ^ g) << 4);
+            ka[h] = lds128(at);
+            kc[h] = lds128(at + 8 * kHeadDim);
+          }
+#pragma unroll
+          for (int w = 0; w < 4; w++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              const uint32_t a = Codes<F>::prepare(word(ka[h], w));
+              const uint32_t d = Codes<F>::prepare(word(kc[h], w));
+              const uint32_t a0 = Codes<F>::template pair<0>(a), a1 = Codes<F>::template pair<0>(d);
+              const uint32_t a2 = Codes<F>::template pair<1>(a), a3 = Codes<F>::template pair<1>(d);
+              if (c == 0 && w == 0)
+                mma16816_zero(x[h], a0, a1, a2, a3, qf[0], qf[1]);
+              else
+                mma16816(x[h], a0, a1, a2, a3, qf[c * 8 + w * 2], qf[c * 8 + w * 2 + 1]);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const float sk = h ? ub.sk : ua.sk;
+          x[h][0] *= f0 * sk;
+          x[h][1] *= f1 * sk;
+          x[h][2] *= f0 * sk;
+          x[h][3] *= f1 * sk;
+          if (span[h] != (kPage << 8)) {
+            const int lo = span[h] & 255, hi = span[h] >> 8;
+            if (g < lo || g >= hi) x[h][0] = x[h][1] = -INFINITY;
+            if (g + 8 < lo || g + 8 >= hi) x[h][2] = x[h][3] = -INFINITY;
           }
         }
-        const float g0 = f0 * sk, g1 = f1 * sk;
-        float x00 = (sa[0] + sb[0]) * g0, x01 = (sa[1] + sb[1]) * g1;  // token g
-        float x10 = (sa[2] + sb[2]) * g0, x11 = (sa[3] + sb[3]) * g1;  // token g + 8
-        if (span != (kPage << 8)) {
-          const int lo = span & 255, hi = span >> 8;
-          if (g < lo || g >= hi) x00 = x01 = -INFINITY;
-          if (g + 8 < lo || g + 8 >= hi) x10 = x11 = -INFINITY;
-        }
-        float n0 = fmaxf(x00, x10), n1 = fmaxf(x01, x11);
+        float n0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+        float n1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
           n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, d));
@@ -386,49 +497,70 @@ __global__ void __launch_bounds__(kThreads, 2)
             o[k][3] *= a1;
           }
         }
-        const float p00 = ex2(x00 - m0 + kHeadroom), p01 = ex2(x01 - m1 + kHeadroom);
-        const float p10 = ex2(x10 - m0 + kHeadroom), p11 = ex2(x11 - m1 + kHeadroom);
-        l0 += p00 + p10;
-        l1 += p01 + p11;
-        const uint32_t ha = half_pair(p00, p01), hb = half_pair(p10, p11);
-        const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
-        const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hb));
-        const uint32_t b0 = transpose8x8(ha), b1 = transpose8x8(hb);
-        const uint32_t r0 = transpose8x8(half_pair(p00 - fa.x, p01 - fa.y));
-        const uint32_t r1 = transpose8x8(half_pair(p10 - fb.x, p11 - fb.y));
-        // values: tokens 2t, 2t + 1, 2t + 8, 2t + 9 of channels [16 g, 16 g + 16)
-        uint4 v[4];
+        const float sv = fmaxf(ua.span ? ua.sv : 0.0f, ub.span ? ub.sv : 0.0f);
+        if (sv * inv_unit >= 2.0f) {
+          const float to = __uint_as_float((254u << 23) - (__float_as_uint(sv) & 0x7F800000u));
+          const float by = to / inv_unit;
+          inv_unit = to;
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-          const int tok = 2 * t + (k & 1) + 8 * (k >> 1);
-          v[k] = lds128(vb + tok * kHeadDim + ((g ^ (tok & 7)) << 4));
+          for (int k = 0; k < 8; k++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) o[k][c] *= by;
         }
-        auto word = [](const uint4& u, int w) {
-          return w == 0 ? u.x : w == 1 ? u.y : w == 2 ? u.z : u.w;
-        };
 #pragma unroll
-        for (int w = 0; w < 4; w++) {
-          const uint32_t ta = word(v[0], w), tb = word(v[1], w);
-          const uint32_t tc = word(v[2], w), td = word(v[3], w);
+        for (int h = 0; h < 2; h++) {
+          if (span[h] == 0) continue;
+          float p00 = ex2(x[h][0] - m0 + kHeadroom), p01 = ex2(x[h][1] - m1 + kHeadroom);
+          float p10 = ex2(x[h][2] - m0 + kHeadroom), p11 = ex2(x[h][3] - m1 + kHeadroom);
+          l0 += p00 + p10;
+          l1 += p01 + p11;
+          const float scale = (h ? ub.sv : ua.sv) * inv_unit;
+          p00 *= scale;
+          p01 *= scale;
+          p10 *= scale;
+          p11 *= scale;
+          const uint32_t ha = half_pair(p00, p01), hb = half_pair(p10, p11);
+          const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
+          const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hb));
+          const uint32_t b0 = transpose8x8(ha), b1 = transpose8x8(hb);
+          const uint32_t r0 = transpose8x8(half_pair(p00 - fa.x, p01 - fa.y));
+          const uint32_t r1 = transpose8x8(half_pair(p10 - fb.x, p11 - fb.y));
+          // values: tokens 2t, 2t + 1, 2t + 8, 2t + 9 of channels [16 g, 16 g + 16)
+          const uint32_t vb = kb[h] + kBlockBytesI8;
+          uint4 v[4];
 #pragma unroll
-          for (int half = 0; half < 2; half++) {  // channels 4 w + 2 half + {0, 1}
-            const uint32_t sel = half ? 0x7362u : 0x5140u;
-            const uint32_t ab = Codes<F>::prepare(prmt(ta, tb, sel));
-            const uint32_t cd = Codes<F>::prepare(prmt(tc, td, sel));
-            const uint32_t a0 = Codes<F>::template pair<0>(ab);
-            const uint32_t a1 = Codes<F>::template pair<1>(ab);
-            const uint32_t a2 = Codes<F>::template pair<0>(cd);
-            const uint32_t a3 = Codes<F>::template pair<1>(cd);
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma16816(acc, a0, a1, a2, a3, b0, b1);
-            mma16816(acc, a0, a1, a2, a3, r0, r1);
+          for (int k = 0; k < 4; k++) {
+            const int tok = 2 * t + (k & 1) + 8 * (k >> 1);
+            v[k] = lds128(vb + tok * kHeadDim + ((g ^ (tok & 7)) << 4));
+          }
+          if (F == kE4m3 && span[h] != (kPage << 8)) {  // bytes no token wrote may be NaN
+            const int lo = span[h] & 255, hi = span[h] >> 8;
 #pragma unroll
-            for (int c = 0; c < 4; c++) o[2 * w + half][c] += sv * acc[c];
+            for (int k = 0; k < 4; k++) {
+              const int tok = 2 * t + (k & 1) + 8 * (k >> 1);
+              if (tok < lo || tok >= hi) v[k] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < 4; w++) {
+#pragma unroll
+            for (int c = 0; c < 2; c++) {  // channels 4 w + 2 c + {0, 1}
+              const uint32_t sel = c ? 0x7362u : 0x5140u;
+              const uint32_t ab = Codes<F>::prepare(prmt(word(v[0], w), word(v[1], w), sel));
+              const uint32_t cd = Codes<F>::prepare(prmt(word(v[2], w), word(v[3], w), sel));
+              const uint32_t a0 = Codes<F>::template pair<0>(ab);
+              const uint32_t a1 = Codes<F>::template pair<1>(ab);
+              const uint32_t a2 = Codes<F>::template pair<0>(cd);
+              const uint32_t a3 = Codes<F>::template pair<1>(cd);
+              mma16816(o[2 * w + c], a0, a1, a2, a3, b0, b1);
+              mma16816(o[2 * w + c], a0, a1, a2, a3, r0, r1);
+            }
           }
         }
-        __syncwarp();  // the slot is read before it is filled again
       }
-      issue(i + kStages, i >> 5);
+      i += 1 + two;
+      __syncwarp();  // the slots are read before they are filled again
+      issue_to(i + kStages, stop);
     }
 
     // ---- the warps' parts of the row meet
@@ -438,45 +570,53 @@ __global__ void __launch_bounds__(kThreads, 2)
       l1 += __shfl_xor_sync(0xffffffffu, l1, d);
     }
     if (g == 0) {
-      sm.ml[warp][2 * t][0] = m0;
-      sm.ml[warp][2 * t][1] = l0;
-      sm.ml[warp][2 * t + 1][0] = m1;
-      sm.ml[warp][2 * t + 1][1] = l1;
+      sm.ml[2 * t][warp] = make_float2(m0, l0);
+      sm.ml[2 * t + 1][warp] = make_float2(m1, l1);
     }
+    {
+      const float unit = 1.0f / inv_unit;
+      const int slot = (taken + kStages - 1) % kStages;  // free: see issue_to
+      float4* dst = reinterpret_cast<float4*>(sm.ring[warp][slot]);
 #pragma unroll
-    for (int k = 0; k < 8; k++) sm.o[warp][k][lane] = make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
+      for (int k = 0; k < 8; k++)
+        dst[k * 32 + lane] =
+            make_float4(o[k][0] * unit, o[k][1] * unit, o[k][2] * unit, o[k][3] * unit);
+      if (lane == 0) sm.slot[warp] = slot;
+    }
     __syncthreads();
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; w++) {
-      ma = fmaxf(ma, sm.ml[w][2 * t][0]);
-      mb = fmaxf(mb, sm.ml[w][2 * t + 1][0]);
+    // joins (m, l) pairs of head `warp`, one a lane, into `sum`, and leaves their weights
+    auto weigh = [&](float2 v, float2 sum) {
+      const float top = fmaxf(max32(v.x), sum.x);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      const float f = ex2(v.x - ref);  // 0 from -inf
+      if (lane < kAhead) sm.weight[lane][warp] = f;
+      return make_float2(top, sum32(f * v.y) + ex2(sum.x - ref) * sum.y);
+    };
+    const float2 nothing = make_float2(-INFINITY, 0.0f);
+    if (warp < 8) {
+      const float2 v = weigh(lane < kWarps ? sm.ml[warp][lane] : nothing, nothing);
+      if (lane == 0) sm.total[warp] = v;
     }
-#pragma unroll
+    __syncthreads();
+    // values 2 tid, 2 tid + 1 of the tile: channel 16 g' + tid / 64 * 2 + (tid & 1) of heads
+    // 2t', 2t' + 1, where lane 4 g' + t' = (tid / 2) % 32 held them
+    const int hl = (tid >> 1) & 31, ht = hl & 3;
+    float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll 4
     for (int w = 0; w < kWarps; w++) {
-      const float wa = sm.ml[w][2 * t][0], wb = sm.ml[w][2 * t + 1][0];
-      const float fa = wa == -INFINITY ? 0.0f : ex2(wa - ma);
-      const float fb = wb == -INFINITY ? 0.0f : ex2(wb - mb);
-      la += fa * sm.ml[w][2 * t][1];
-      lb += fb * sm.ml[w][2 * t + 1][1];
-      const float4 v = sm.o[w][warp][lane];
-      acc.x += fa * v.x;
-      acc.y += fb * v.y;
-      acc.z += fa * v.z;
-      acc.w += fb * v.w;
+      const float2 f = *reinterpret_cast<const float2*>(&sm.weight[w][2 * ht]);
+      const float2 v = reinterpret_cast<const float2*>(sm.ring[w][sm.slot[w]])[tid];
+      acc.x += f.x * v.x;
+      acc.y += f.y * v.y;
     }
     bool write = true;
     if (row_begin < begin || row_end > end) {  // a part of the row: to the workspace
-      const long long c0 = row_begin / per, c1 = (row_end - 1) / per;
+      const int c0 = (int)(row_begin / per), parts = (int)((row_end - 1) / per) - c0 + 1;
       const size_t slot = 2 * (size_t)blockIdx.x + (begin < row_begin ? 1 : 0);
-      reinterpret_cast<float4*>(p.part_o + slot * kTile)[warp * 32 + lane] = acc;
-      if (warp == 0 && g == 0)
-        reinterpret_cast<float4*>(p.part_ml + slot * 16)[t] = make_float4(ma, la, mb, lb);
-      __threadfence();
+      reinterpret_cast<float2*>(p.part_o + slot * kTile)[tid] = acc;
+      if (tid < 8) reinterpret_cast<float2*>(p.part_ml + slot * 16)[tid] = sm.total[tid];
       __syncthreads();
-      const int parts = (int)(c1 - c0) + 1;
-      if (tid == 0) {
+      if (tid == 0) {  // releases what the barrier has ordered before it
         int* counter = p.counters + (size_t)b * p.rows + row;
         const int last = atomic_add_acq_rel_gpu(counter, 1) == parts - 1;
         if (last) *counter = 0;
@@ -485,68 +625,63 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncthreads();
       write = sm.last != 0;
       if (write) {
-        // head `warp` of every part: its weight against the joint maximum
-        float* weight = reinterpret_cast<float*>(sm.o);  // [parts][8]
-        auto slot_of = [&](int c) {
-          return 2 * (size_t)(c0 + c) + ((c0 + c) * per < row_begin ? 1 : 0);
-        };
-        float top = -INFINITY;
-        for (int c = lane; c < parts; c += 32)
-          top = fmaxf(top, __ldcg(p.part_ml + slot_of(c) * 16 + warp * 2));
+        // What is left of the call's time is the latency of these loads: kAhead parts' values
+        // and their (m, l) are under way at once. Part c is the first one of CTA c0 + c, but
+        // for c = 0 where that CTA has an earlier row.
+        const size_t first = 2 * (size_t)c0 + (c0 * per < row_begin ? 1 : 0);
+        const float2* values = reinterpret_cast<const float2*>(p.part_o) + tid;
+        auto slot_of = [&](int c) { return c == 0 ? first : 2 * (size_t)(c0 + c); };
+        acc = make_float2(0.0f, 0.0f);
+        float2 sum = nothing;  // head `warp`
+        float2 was = make_float2(-INFINITY, -INFINITY);  // the maxima under which acc is kept
+        for (int c = 0; c < parts; c += kAhead) {
+          float2 ml = nothing, v[kAhead];
+          if (warp < 8 && lane < kAhead && c + lane < parts)
+            ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot_of(c + lane) * 16) +
+                        warp);
+          v[0] = __ldcg(values + slot_of(c) * (kTile / 2));
+          const float2* more = values + (size_t)(c0 + c) * kTile;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        float l = 0.0f;
-        for (int c = lane; c < parts; c += 32) {
-          const float2 v =
-              __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot_of(c) * 16 + warp * 2));
-          const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - top);
-          weight[c * 8 + warp] = f;
-          l += f * v.y;
-        }
+          for (int k = 1; k < kAhead; k++) {
+            v[k] = make_float2(0.0f, 0.0f);
+            if (c + k < parts) v[k] = __ldcg(more + k * kTile);
+          }
+          if (warp < 8) {
+            sum = weigh(ml, sum);
+            if (lane == 0) sm.total[warp] = sum;
+          }
+          __syncthreads();
+          const float2 now = make_float2(fmaxf(sm.total[2 * ht].x, -1e30f),
+                                         fmaxf(sm.total[2 * ht + 1].x, -1e30f));
+          acc.x *= ex2(was.x - now.x);  // by 0 the first time
+          acc.y *= ex2(was.y - now.y);
+          was = now;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        if (lane == 0) {
-          sm.total[warp][0] = top;
-          sm.total[warp][1] = l;
-        }
-        __syncthreads();
-        ma = sm.total[2 * t][0];
-        la = sm.total[2 * t][1];
-        mb = sm.total[2 * t + 1][0];
-        lb = sm.total[2 * t + 1][1];
-        acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int c = 0; c < parts; c++) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot_of(c) * kTile) +
-                                  warp * 32 + lane);
-          const float fa = weight[c * 8 + 2 * t], fb = weight[c * 8 + 2 * t + 1];
-          acc.x += fa * v.x;
-          acc.y += fb * v.y;
-          acc.z += fa * v.z;
-          acc.w += fb * v.w;
+          for (int k = 0; k < kAhead; k++) {
+            const float2 f = *reinterpret_cast<const float2*>(&sm.weight[k][2 * ht]);
+            acc.x += f.x * v[k].x;
+            acc.y += f.y * v[k].y;
+          }
+          if (c + kAhead < parts) __syncthreads();  // the weights are read
         }
       }
     }
     if (write) {
-      // tile `warp`: channels 16 g + 2 warp + {0, 1} of heads 2t (x, z) and 2t + 1 (y, w)
-      const size_t head = (size_t)b * p.hq + (size_t)row * p.group + 2 * t;
-      const int ch = 16 * g + 2 * warp;
-      if (2 * t < p.group) {
-        const float r = la > 0.0f ? 1.0f / la : 0.0f;
-        *reinterpret_cast<float2*>(p.out + head * kHeadDim + ch) =
-            make_float2(acc.x * r, acc.z * r);
-        if (p.lse != nullptr && warp == 0 && g == 0)
-          p.lse[head] = (ma - kHeadroom + log2f(la)) * 0.693147180559945309f;
+      const float2 ta = sm.total[2 * ht], tb = sm.total[2 * ht + 1];
+      const size_t head = (size_t)b * p.hq + (size_t)row * p.group + 2 * ht;
+      const int ch = 16 * (hl >> 2) + 2 * (tid >> 6) + (tid & 1);
+      const bool sums = p.lse != nullptr && tid < 8 && (tid & 1) == 0;
+      if (2 * ht < p.group) {
+        p.out[head * kHeadDim + ch] = ta.y > 0.0f ? acc.x / ta.y : 0.0f;
+        if (sums) p.lse[head] = (ta.x - kHeadroom + log2f(ta.y)) * 0.693147180559945309f;
       }
-      if (2 * t + 1 < p.group) {
-        const float r = lb > 0.0f ? 1.0f / lb : 0.0f;
-        *reinterpret_cast<float2*>(p.out + (head + 1) * kHeadDim + ch) =
-            make_float2(acc.y * r, acc.w * r);
-        if (p.lse != nullptr && warp == 0 && g == 0)
-          p.lse[head + 1] = (mb - kHeadroom + log2f(lb)) * 0.693147180559945309f;
+      if (2 * ht + 1 < p.group) {
+        p.out[(head + 1) * kHeadDim + ch] = tb.y > 0.0f ? acc.y / tb.y : 0.0f;
+        if (sums) p.lse[head + 1] = (tb.x - kHeadroom + log2f(tb.y)) * 0.693147180559945309f;
       }
     }
-    __syncthreads();  // the meeting place is free for the next row
+    fence_proxy_async();  // the slots were written here and are free for copies again
+    __syncthreads();
     x = stop;
   }
 }
@@ -555,7 +690,7 @@ size_t smem_bytes(int batch) { return 1024 + sizeof(Smem) + 8 * (size_t)(batch +
 
 }  // namespace
 
-int kv8_attend_ctas(int num_sms) { return std::min(2 * num_sms, kKv8MaxCtas); }
+int kv8_attend_ctas(int num_sms) { return std::min(num_sms, kKv8MaxCtas); }
 
 cudaError_t launch_kv8_attend(const Shape& s, bool kept, const Kv8& c, const CUtensorMap& k_map,
                               const CUtensorMap& v_map, const void* q, const int32_t* page_table,
@@ -603,7 +738,7 @@ cudaError_t launch_kv8_attend(const Shape& s, bool kept, const Kv8& c, const CUt
   const size_t smem = smem_bytes(s.batch);
   const cudaError_t e = set_kernel_smem(kernel, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kernel, dim3(grid), dim3(kThreads), smem, st, false, k_map, v_map, p);
+  return launch_kernel(kernel, dim3(grid), dim3(kThreads), smem, st, true, k_map, v_map, p);
 }
 
 }  // namespace hsa

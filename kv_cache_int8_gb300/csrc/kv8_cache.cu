@@ -76,10 +76,10 @@ __device__ __forceinline__ void values4(uint32_t w, float* f) {
     const uint32_t lo = Codes<kE4m3>::pair<0>(w), hi = Codes<kE4m3>::pair<1>(w);
     const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
     const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    f[0] = a.x * 256.0f;
-    f[1] = a.y * 256.0f;
-    f[2] = b.x * 256.0f;
-    f[3] = b.y * 256.0f;
+    f[0] = a.x;
+    f[1] = a.y;
+    f[2] = b.x;
+    f[3] = b.y;
   }
 }
 
@@ -89,6 +89,8 @@ template <int F>
 __global__ void __launch_bounds__(kWarps * 32) kv8_write_kernel(
     NewRows rows, WriteSide ks, WriteSide vs, const int32_t* __restrict__ page_table, int hkv,
     int num_pages, int units, int* err) {
+  grid_dep_wait();
+  grid_dep_launch();
   const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (unit >= units) return;
   const int lane = threadIdx.x & 31;
@@ -210,6 +212,8 @@ template <int F>
 __global__ void __launch_bounds__(kWarps * 32) kv8_read_kernel(
     NewRows rows, ReadSide ks, ReadSide vs, const int32_t* __restrict__ page_table, int hkv,
     int num_pages, int units, int* err) {
+  grid_dep_wait();
+  grid_dep_launch();
   const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (unit >= units) return;
   const int lane = threadIdx.x & 31;
@@ -268,7 +272,7 @@ cudaError_t launch_kv8_write(const Shape& s, const Kv8& c, const void* k_new, lo
   const int units = new_block_items(s.batch, total, cu != nullptr) * s.hkv * 2;
   auto kernel = c.format == kE4m3 ? kv8_write_kernel<kE4m3> : kv8_write_kernel<kInt8>;
   return launch_kernel(kernel, dim3((units + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, st,
-                       false, rows, ks, vs, page_table, s.hkv, s.num_pages, units, err);
+                       true, rows, ks, vs, page_table, s.hkv, s.num_pages, units, err);
 }
 
 cudaError_t launch_kv8_read(const Shape& s, const Kv8& c, void* k_out, long long k_stride,
@@ -283,7 +287,7 @@ cudaError_t launch_kv8_read(const Shape& s, const Kv8& c, void* k_out, long long
   const int units = new_block_items(s.batch, total, cu != nullptr) * s.hkv * 2;
   auto kernel = c.format == kE4m3 ? kv8_read_kernel<kE4m3> : kv8_read_kernel<kInt8>;
   return launch_kernel(kernel, dim3((units + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, st,
-                       false, rows, ks, vs, page_table, s.hkv, s.num_pages, units, err);
+                       true, rows, ks, vs, page_table, s.hkv, s.num_pages, units, err);
 }
 
 }  // namespace hsa
