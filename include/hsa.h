@@ -464,6 +464,18 @@ int32_t hsa_kv8_attend(const hsa_dims* d, const hsa_kv8* cache, const void* q,
                        void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Causal attention of the last n_b tokens of each sequence over the 8-bit cache (their own K
+ * and V written before): query row r of sequence b, at position p, attends tokens [0, p]. q:
+ * bf16 rows [total_tokens][hq][128] with row stride q_stride; out: bf16 rows, contiguous; lse:
+ * f32 [total_tokens][hq] (nullable). Rows of a sequence that is left out (see above) get 0 and
+ * lse -inf. Needs the HSA_OP_KV8_PREFILL workspace.
+ */
+int32_t hsa_kv8_prefill(const hsa_dims* d, const hsa_kv8* cache, const void* q, int64_t q_stride,
+                        const int32_t* cu_tokens, int32_t total_tokens,
+                        const int32_t* page_table, const int32_t* seq_lens, void* out, float* lse,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Reads and clears the device error word of `workspace` after synchronising `stream`:
  * *code receives HSA_OK, HSA_ERR_TIMEOUT or HSA_ERR_DEVICE_CHECK. workspace NULL: the error
  * word of hsa_select_noalloc's fixed scratch array on the current device. This is the one

@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libhsa.so")
 SOURCES = ["api.cu", "quantize.cu", "score.cu", "prune.cu", "attend.cu",
-           "kv8_cache.cu", "kv8_attend.cu"]
+           "kv8_cache.cu", "kv8_attend.cu", "kv8_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", os.path.join(ROOT, "include")]

@@ -194,6 +194,15 @@ Kv8Layout kv8_layout(const Shape& s) {
   return l;
 }
 
+Kv8Layout kv8_prefill_layout() {
+  Kv8Layout l;
+  l.counters = kErrBytes;
+  l.part_ml = l.counters + up((size_t)2 * hsa::kKv8MaxCtas * 4);
+  l.part_o = l.part_ml + up(hsa::kv8_prefill_ml_floats() * 4);
+  l.end = l.part_o + up(hsa::kv8_prefill_part_floats() * 4);
+  return l;
+}
+
 struct StepLayout {
   size_t block_max, tile_max, row_range, block_idx, n_blocks, sel_pages, q, k_new, v_new, out,
       lse;
@@ -565,7 +574,7 @@ extern "C" {
 size_t hsa_workspace_bytes(const hsa_dims* d, int32_t op) {
   Shape s;
   const bool prune = op == HSA_OP_SELECT || op == HSA_OP_STEP;
-  const bool kv8 = op == HSA_OP_KV8_DECODE;
+  const bool kv8 = op == HSA_OP_KV8_DECODE || op == HSA_OP_KV8_PREFILL;
   if (check_dims(d, s, prune, kv8) != HSA_OK || (kv8 && d->kv_on_host)) return 0;
   switch (op) {
     case HSA_OP_QUANTIZE: return quantize_ws(s);
@@ -575,6 +584,7 @@ size_t hsa_workspace_bytes(const hsa_dims* d, int32_t op) {
     case HSA_OP_STEP: return step_layout(s).end;
     case HSA_OP_CACHED: return cached_ws(s);
     case HSA_OP_KV8_DECODE: return kv8_layout(s).end;
+    case HSA_OP_KV8_PREFILL: return kv8_prefill_layout().end;
     default: return 0;
   }
 }
@@ -1124,6 +1134,28 @@ int32_t hsa_kv8_attend(const hsa_dims* d, const hsa_kv8* cache, const void* q,
                        void* workspace, size_t workspace_bytes, void* stream) {
   return do_kv8_attend(d, cache, true, q, page_table, seq_lens, block_idx, n_blocks, out, lse,
                        workspace, workspace_bytes, stream);
+}
+
+int32_t hsa_kv8_prefill(const hsa_dims* d, const hsa_kv8* cache, const void* q, int64_t q_stride,
+                        const int32_t* cu_tokens, int32_t total_tokens,
+                        const int32_t* page_table, const int32_t* seq_lens, void* out, float* lse,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  Shape s;
+  hsa::Kv8 c;
+  int32_t rc = check_kv8(d, cache, s, &c);
+  if (rc == HSA_OK) rc = check_rows(s, cu_tokens, total_tokens, page_table, seq_lens);
+  if (rc == HSA_OK) rc = check_row_array(q, q_stride, s.hq);
+  if (rc != HSA_OK) return rc;
+  if (!out || !aligned(out, 16) || !aligned(lse, 4)) return HSA_ERR_INVALID_ARG;
+  const Kv8Layout l = kv8_prefill_layout();
+  rc = check_ws(s, workspace, workspace_bytes, l.end);
+  if (rc != HSA_OK || total_tokens == 0) return rc;
+  char* ws = static_cast<char*>(workspace);
+  return cuda_status(hsa::launch_kv8_prefill(
+      s, c, q, q_stride, cu_tokens, total_tokens, page_table, seq_lens, out, lse,
+      reinterpret_cast<int*>(ws + l.counters), reinterpret_cast<float*>(ws + l.part_ml),
+      reinterpret_cast<float*>(ws + l.part_o), reinterpret_cast<int*>(ws), num_sms(),
+      as_stream(stream)));
 }
 
 int32_t hsa_read_device_error(void* workspace, void* stream, int32_t* code) {

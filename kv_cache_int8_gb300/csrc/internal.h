@@ -164,7 +164,7 @@ cudaError_t launch_attend_select(const Shape& s, const void* q, const void* k_ca
                                  int32_t* block_idx, int32_t* n_blocks, float* out, float* lse,
                                  const AttendBuffers& buf, int* err, cudaStream_t st);
 
-// ---- kv8_cache.cu, kv8_attend.cu: the 8-bit K/V cache
+// ---- kv8_cache.cu, kv8_attend.cu, kv8_prefill.cu: the 8-bit K/V cache
 struct Kv8 {
   void* k;  // codes [num_pages][hkv][16][128]
   void* v;
@@ -189,5 +189,13 @@ cudaError_t launch_kv8_attend(const Shape& s, bool kept, const Kv8& c, const CUt
                               const int32_t* n_blocks, float* out, float* lse, int* counters,
                               float* part_ml, float* part_o, int* err, int num_sms,
                               cudaStream_t st);
+// counters [2 kKv8MaxCtas] (zero), part_ml and part_o of the sizes given
+size_t kv8_prefill_part_floats();
+size_t kv8_prefill_ml_floats();
+cudaError_t launch_kv8_prefill(const Shape& s, const Kv8& c, const void* q, long long q_stride,
+                               const int32_t* cu, int total, const int32_t* page_table,
+                               const int32_t* seq_lens, void* out, float* lse, int* counters,
+                               float* part_ml, float* part_o, int* err, int num_sms,
+                               cudaStream_t st);
 
 }  // namespace hsa

@@ -1,0 +1,787 @@
+// kv8_prefill.cu -- causal attention of many new tokens over the 8-bit K/V cache, on the
+// 5th-generation tensor cores.
+//
+// Source: "KV Cache 与长上下文推理", sections "KV Cache 回顾" (the prompt's attention fills and
+// reads the cache) and "KV Cache 量化".
+//
+// Mathematics. As in the decode attention, the codes enter the products exactly (fp16) and the
+// blocks' scales (16 tokens) are applied in fp32: with row factor f = sm_scale log2 e 2^-shift,
+//   y_t = f s_k S_t + log2 s_v,   out = sum_t 2^(y_t - M) c_t / sum_t 2^(y_t - M) / s_v
+// so V's scale costs nothing but the offset of an exponent that is computed anyway, and the sum
+// takes one multiplication a block. P = 2^(y - M + 10) is rounded to fp16 (11 bits, against 8
+// of the bf16 result); M lags the running maximum by at most 4, so the output accumulator is
+// rarely rescaled.
+//
+// Layout. 256 rows (a kv head's group of query heads x 256 / group tokens) as two tiles of 128
+// against tiles of 128 tokens. Warps 0-3 and 4-7: one row a thread, softmax of tile 0 and 1;
+// warps 8-11 turn the codes into swizzled fp16 tiles (two buffers of K and of V); warp 12 issues
+// the products. While one tile's scores are in the softmax, the tensor cores work on the other
+// tile. TMEM: S0 S1 O0 O1, 128 columns each; P overwrites its S (a product that reads P is
+// issued before the product that overwrites it, and they run in order).
+//
+// Work. All steps (row block, token tile) of all sequences and heads form one line, cut into
+// equal slices, one CTA each, as in the decode attention; parts of a row block meet in the
+// workspace.
+#include "kv8.cuh"
+#include "tcgen05.cuh"
+
+#include <cmath>
+
+namespace hsa {
+namespace {
+
+using namespace kv8_detail;
+
+constexpr int kRows = 256;         // rows of a block: two tiles
+constexpr int kTokens = 128;       // tokens of a step
+constexpr int kTilePages = kTokens / kPage;
+constexpr int kTileBytes = 128 * kHeadDim * 2;
+constexpr int kHalfBytes = kTileBytes / 2;  // 64 channels of 128 rows
+constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
+constexpr int kMmaWarp = kSoftmaxWarps + kConvertWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kPageRing = 4;
+constexpr float kHeadroom = 10.0f;
+constexpr float kLag = 4.0f;
+constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns; tile i at + 128 i
+
+struct Params {
+  NewRows rows;
+  const __nv_bfloat16* q;
+  long long q_stride;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* page_table;
+  __nv_bfloat16* out;
+  float* lse;
+  float* part_ml;  // [2 CTAs][kRows] (M, l)
+  float* part_o;   // [2 CTAs][32][kRows] float4
+  int* counters;   // [CTAs][2 tiles]
+  int* err;
+  int hq, hkv, group, num_pages, block_tokens;  // block_tokens = kRows / group
+  float scale_log2;
+};
+
+struct Smem {
+  alignas(1024) unsigned char q[2][kTileBytes];
+  unsigned char k[2][kTileBytes];
+  unsigned char v[2][kTileBytes];
+  float4 page[kPageRing][kTilePages];  // s_k, log2 s_v, 1 / s_v
+  alignas(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2],
+      p_full[2], o_full[2];
+  long long per;
+  int start_b, start_h, start_q, start_tile;
+  uint32_t tmem;
+  int last[2];
+  int dead;
+};
+// behind it: pre (long long [batch + 1]), then len, n, row0 (int [batch] each)
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Waits with a limit, a whole warp alike; once a wait has run out every wait of the CTA gives up.
+__device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity, int* err) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const long long t0 = clock64();
+    while (!(ok = mbar_try_wait(bar, parity))) {
+      if (*reinterpret_cast<volatile int*>(&sm.dead)) break;
+      if (clock64() - t0 > kWaitLimitCycles) {
+        *reinterpret_cast<volatile int*>(&sm.dead) = 1;
+        set_error(err, kDevErrTimeout);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+struct Seqs {
+  const long long* pre;
+  const int* len;
+  const int* n;
+  const int* row0;
+};
+
+// Token tiles that row block q of a sequence visits.
+__device__ __forceinline__ int block_tiles(int len, int n, int block_tokens, int q) {
+  return (len - n + min((q + 1) * block_tokens, n) - 1) / kTokens + 1;
+}
+
+// A stretch of one row block's tiles: what a CTA does at a time.
+struct Piece {
+  int b, h, q;      // sequence, kv head, row block
+  int tile, tiles;  // first tile, number of tiles
+  int all_tiles;    // of the whole row block
+  int rows;         // rows of the block that exist
+};
+
+// The pieces of the slice [x, end), in order.
+struct Walk {
+  const Seqs s;
+  int batch, hkv, group, block_tokens;
+  long long x, end;
+  int b, h, q, tile;
+
+  __device__ __forceinline__ bool next(Piece& p) {
+    if (x >= end) return false;
+    p.b = b;
+    p.h = h;
+    p.q = q;
+    p.tile = tile;
+    p.all_tiles = block_tiles(s.len[b], s.n[b], block_tokens, q);
+    p.tiles = (int)min((long long)(p.all_tiles - tile), end - x);
+    p.rows = min(block_tokens, s.n[b] - q * block_tokens) * group;
+    x += p.tiles;
+    tile = 0;
+    if ((q + 1) * block_tokens < s.n[b]) {
+      q++;
+    } else {
+      q = 0;
+      if (++h == hkv) {
+        h = 0;
+        do b++;
+        while (b < batch && s.n[b] == 0);
+      }
+    }
+    return true;
+  }
+};
+
+template <int F>
+__global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p) {
+  extern __shared__ unsigned char smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(
+      smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+  const int batch = p.rows.batch;
+  long long* pre = reinterpret_cast<long long*>(&sm + 1);
+  int* len = reinterpret_cast<int*>(pre + batch + 1);
+  int* num = len + batch;
+  int* row0 = num + batch;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&sm.q_full[i], 128);
+      mbar_init(&sm.k_full[i], 32 * kConvertWarps);
+      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.v_full[i], 32 * kConvertWarps);
+      mbar_init(&sm.v_empty[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 128);
+      mbar_init(&sm.o_full[i], 1);
+    }
+    sm.dead = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) tc::alloc(&sm.tmem, 512);
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // ---- the line of all steps; warp 0 finds where this CTA's slice begins
+  if (warp == 0) {
+    long long sum = 0;
+    for (int b0 = 0; b0 < batch; b0 += 32) {
+      const int b = b0 + lane;
+      NewSpan sp = {0, 0, 0, false};
+      int blocks = 0, tiles = 0;
+      if (b < batch) {
+        sp = new_span(p.rows, b);
+        if (sp.bad) set_error(p.err, kDevErrCheck);
+        len[b] = sp.start + sp.n;
+        num[b] = sp.n;
+        row0[b] = sp.row0;
+        blocks = (sp.n + p.block_tokens - 1) / p.block_tokens;
+        if (blocks <= 8)
+          for (int q = 0; q < blocks; q++)
+            tiles += block_tiles(sp.start + sp.n, sp.n, p.block_tokens, q);
+      }
+      // sequences of many row blocks: the warp together
+      for (unsigned many = __ballot_sync(0xffffffffu, blocks > 8); many != 0; many &= many - 1) {
+        const int from = __ffs(many) - 1;
+        const int n = __shfl_sync(0xffffffffu, sp.n, from);
+        const int l = __shfl_sync(0xffffffffu, sp.start, from) + n;
+        const int bl = __shfl_sync(0xffffffffu, blocks, from);
+        int t = 0;
+        for (int q = lane; q < bl; q += 32) t += block_tiles(l, n, p.block_tokens, q);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+        if (lane == from) tiles = t;
+      }
+      long long incl = (long long)tiles * p.hkv;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      if (b < batch) pre[b + 1] = sum + incl;
+      sum += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) pre[0] = 0;
+    __syncwarp();
+    const long long per = max((sum + gridDim.x - 1) / gridDim.x, 2LL);
+    const long long begin = min(blockIdx.x * per, sum);
+    if (lane == 0) sm.per = per;
+    if (begin < sum) {
+      int lo = 0, hi = batch;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= begin) lo = mid;
+        else hi = mid;
+      }
+      const int b = lo;
+      const unsigned tiles = (unsigned)((pre[b + 1] - pre[b]) / p.hkv);
+      const long long at = begin - pre[b];
+      const int h = (int)(at / tiles);
+      unsigned rem = (unsigned)(at - (long long)h * tiles);
+      const int blocks = (num[b] + p.block_tokens - 1) / p.block_tokens;
+      int q0 = 0;
+      for (;; q0 += 32) {  // the block whose tiles hold place `rem`
+        const int q = q0 + lane;
+        const unsigned t = q < blocks ? block_tiles(len[b], num[b], p.block_tokens, q) : 0;
+        unsigned incl = t;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const unsigned v = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, rem < incl);
+        if (hit != 0) {
+          if (lane == __ffs(hit) - 1) {
+            sm.start_b = b;
+            sm.start_h = h;
+            sm.start_q = q;
+            sm.start_tile = (int)(rem - (incl - t));
+          }
+          break;
+        }
+        rem -= __shfl_sync(0xffffffffu, incl, 31);
+        if (q0 + 32 >= blocks) break;
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = sm.tmem;
+  const long long per = sm.per, all = pre[batch];
+  const long long begin = min(blockIdx.x * per, all), end = min(begin + per, all);
+  Walk walk = {{pre, len, num, row0}, batch, p.hkv, p.group, p.block_tokens, begin, end,
+               sm.start_b, sm.start_h, sm.start_q, sm.start_tile};
+  Piece pc;
+
+  if (warp < kSoftmaxWarps) {
+    // ================================================= softmax: one row a thread
+    const int tile = warp >> 2, r = tid & 127, row = tile * 128 + r;
+    const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+    const uint32_t s_col = at + kColS + 128 * tile, o_col = at + kColO + 128 * tile;
+    uint32_t s_phase = 0, o_phase = 0;
+    int step = 0;  // steps of all pieces so far (the page table ring)
+    // rows of sequences that do not fit: 0 and -inf
+    for (int b = blockIdx.x; b < batch; b += gridDim.x) {
+      if (p.rows.cu == nullptr ? num[b] != 0 : p.rows.cu[b + 1] - p.rows.cu[b] == num[b]) continue;
+      const int first = max(row0[b], 0);
+      const int count = min(p.rows.cu ? p.rows.cu[b + 1] : b + 1, p.rows.total) - first;
+      for (long long i = tid; i < (long long)count * p.hq * (kHeadDim / 8); i += 256)
+        reinterpret_cast<uint4*>(p.out + (size_t)first * p.hq * kHeadDim)[i] =
+            make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse != nullptr)
+        for (long long i = tid; i < (long long)count * p.hq; i += 256)
+          p.lse[(size_t)first * p.hq + i] = -INFINITY;
+    }
+    while (walk.next(pc)) {
+      if (tile * 128 >= pc.rows) {
+        step += pc.tiles;
+        continue;
+      }
+      // ---- the query row in fp16, its largest value in [2^13, 2^14)
+      const bool real = row < pc.rows;
+      const int token = pc.q * p.block_tokens + row / p.group;  // among the new tokens
+      const int head = pc.h * p.group + row % p.group;
+      const int pos = real ? len[pc.b] - num[pc.b] + token : -1;
+      const size_t out_row = (size_t)(row0[pc.b] + token) * p.hq + head;
+      float f;
+      {
+        const uint4* q = reinterpret_cast<const uint4*>(
+            p.q + (long long)(row0[pc.b] + token) * p.q_stride + head * kHeadDim);
+        uint4 raw[16];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int c = 0; c < 16; c++) {
+          raw[c] = real ? q[c] : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int c = 0; c < 16; c++) {
+          mx = __vmaxu2(mx, __vmaxu2(raw[c].x & 0x7FFF7FFFu, raw[c].y & 0x7FFF7FFFu));
+          mx = __vmaxu2(mx, __vmaxu2(raw[c].z & 0x7FFF7FFFu, raw[c].w & 0x7FFF7FFFu));
+        }
+        const uint32_t m16 = max(mx & 0xFFFFu, mx >> 16);
+        const int e = m16 >> 7;
+        const int shift = (m16 == 0 || e == 255) ? 0 : min(13 + 127 - e, 126);
+        const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+        f = p.scale_log2 * __uint_as_float((uint32_t)(127 - shift) << 23);
+        unsigned char* dst = sm.q[tile] + (r >> 3) * 1024 + (r & 7) * 128;
+#pragma unroll
+        for (int c = 0; c < 16; c++) {
+          const uint4 w = make_uint4(half_pair(bf16_lo(raw[c].x) * up, bf16_hi(raw[c].x) * up),
+                                     half_pair(bf16_lo(raw[c].y) * up, bf16_hi(raw[c].y) * up),
+                                     half_pair(bf16_lo(raw[c].z) * up, bf16_hi(raw[c].z) * up),
+                                     half_pair(bf16_lo(raw[c].w) * up, bf16_hi(raw[c].w) * up));
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalfBytes + (((c & 7) ^ (r & 7)) << 4)) = w;
+        }
+        fence_proxy_async();
+        mbar_arrive(&sm.q_full[tile]);
+      }
+      // the first position of this tile's rows: tiles of tokens up to it need no mask
+      const int first_pos = len[pc.b] - num[pc.b] + pc.q * p.block_tokens +
+                            tile * 128 / p.group;
+      const bool full_rows = pc.rows >= (tile + 1) * 128;
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < pc.tiles; j++, step++) {
+        const int base = (pc.tile + j) * kTokens;
+        if (!wait(sm, &sm.s_full[tile], s_phase, p.err)) break;
+        s_phase ^= 1;
+        tc::fence_after();
+        const float4* page = sm.page[step % kPageRing];
+        const bool masked = !full_rows || base + kTokens - 1 > first_pos;
+        const int limit = pos - base;  // columns up to it are seen
+        // ---- the row's maximum
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          uint32_t s[32];
+          tc::load32(s_col + c * 32, s);
+          tc::wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 32; k++)
+              if (c * 32 + k > limit) s[k] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int g = 0; g < 2; g++) {
+            const float4 pg = page[2 * c + g];
+            float a = __uint_as_float(s[16 * g]), b = __uint_as_float(s[16 * g + 1]);
+#pragma unroll
+            for (int k = 2; k < 16; k += 2) {
+              a = fmaxf(a, __uint_as_float(s[16 * g + k]));
+              b = fmaxf(b, __uint_as_float(s[16 * g + k + 1]));
+            }
+            a = fmaxf(a, b);
+            if (a != -INFINITY) top = fmaxf(top, a * (f * pg.x) + pg.y);
+          }
+        }
+        // ---- the accumulator follows a maximum that has grown by more than kLag
+        if (__any_sync(0xffffffffu, top > m + kLag)) {
+          top = fmaxf(top, m);
+          const float by = m == -INFINITY ? 0.0f : ex2(m - top);
+          m = top;
+          l *= by;
+          if (j > 0) {
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+              uint32_t o[32];
+              tc::load32(o_col + c * 32, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
+              tc::store32(o_col + c * 32, o);
+            }
+          }
+        }
+        const float ref = (m == -INFINITY ? 0.0f : m) - kHeadroom;
+        // ---- P, over S
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          uint32_t s[32], w[16];
+          tc::load32(s_col + c * 32, s);
+          tc::wait_ld();
+#pragma unroll
+          for (int g = 0; g < 2; g++) {
+            const float4 pg = page[2 * c + g];
+            const float mul = f * pg.x, add = pg.y - ref;
+            float sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              float a = fmaf(__uint_as_float(s[16 * g + k]), mul, add);
+              float b = fmaf(__uint_as_float(s[16 * g + k + 1]), mul, add);
+              if (masked) {
+                if (c * 32 + 16 * g + k > limit) a = -INFINITY;
+                if (c * 32 + 16 * g + k + 1 > limit) b = -INFINITY;
+              }
+              a = ex2(a);
+              b = ex2(b);
+              sum += a + b;
+              w[8 * g + k / 2] = half_pair(a, b);
+            }
+            l = fmaf(sum, pg.z, l);
+          }
+          tc::store16(s_col + c * 16, w);
+        }
+        tc::wait_st();
+        tc::fence_before();
+        mbar_arrive(&sm.p_full[tile]);
+      }
+      // ---- the result
+      if (!wait(sm, &sm.o_full[tile], o_phase, p.err)) break;
+      o_phase ^= 1;
+      tc::fence_after();
+      const bool whole = pc.tiles == pc.all_tiles;
+      if (whole) {
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          uint32_t o[32];
+          tc::load32(o_col + c * 32, o);
+          tc::wait_ld();
+          if (real) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * kHeadDim + c * 32);
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; i++)
+                w[i] = bf16_pair(__uint_as_float(o[8 * k + 2 * i]) * inv,
+                                 __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
+              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (real && p.lse != nullptr)
+          p.lse[out_row] = (m - kHeadroom + log2f(l)) * 0.693147180559945309f;
+      } else {
+        // a part: to the workspace; the last of the block's CTAs to arrive joins them
+        const long long piece_end = walk.x, block_begin = piece_end - pc.tiles - pc.tile;
+        const int c0 = (int)(block_begin / per);
+        const int parts = (int)((block_begin + pc.all_tiles - 1) / per) - c0 + 1;
+        const size_t slot = 2 * (size_t)blockIdx.x + (begin < block_begin ? 1 : 0);
+        float4* po = reinterpret_cast<float4*>(p.part_o) + slot * 32 * kRows + row;
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          uint32_t o[32];
+          tc::load32(o_col + c * 32, o);
+          tc::wait_ld();
+          if (real) {
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+              po[(c * 8 + k) * kRows] =
+                  make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                              __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+          }
+        }
+        float2* pml = reinterpret_cast<float2*>(p.part_ml);
+        if (real) pml[slot * kRows + row] = make_float2(m, l);
+        named_sync(1 + tile, 128);
+        if (r == 0) {
+          int* counter = p.counters + 2 * c0 + tile;
+          const int last = atomic_add_acq_rel_gpu(counter, 1) == parts - 1;
+          if (last) *counter = 0;
+          sm.last[tile] = last;
+        }
+        named_sync(1 + tile, 128);
+        if (sm.last[tile] && real) {
+          const size_t first = 2 * (size_t)c0 + (c0 * per < block_begin ? 1 : 0);
+          auto slot_of = [&](int c) { return c == 0 ? first : 2 * (size_t)(c0 + c); };
+          float top = -INFINITY, sum = 0.0f;
+          for (int c = 0; c < parts; c++)
+            top = fmaxf(top, __ldcg(pml + slot_of(c) * kRows + row).x);
+          const float ref = top == -INFINITY ? 0.0f : top;
+          for (int c = 0; c < parts; c++) {
+            const float2 v = __ldcg(pml + slot_of(c) * kRows + row);
+            sum += ex2(v.x - ref) * v.y;
+          }
+          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+          for (int c4 = 0; c4 < 4; c4++) {  // 32 channels at a time
+            float4 acc[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int c = 0; c < parts; c++) {
+              const size_t sl = slot_of(c);
+              const float w = ex2(__ldcg(pml + sl * kRows + row).x - ref) * inv;
+              const float4* src = reinterpret_cast<const float4*>(p.part_o) +
+                                  (sl * 32 + c4 * 8) * kRows + row;
+              float4 v[8];
+#pragma unroll
+              for (int k = 0; k < 8; k++) v[k] = __ldcg(src + k * kRows);
+#pragma unroll
+              for (int k = 0; k < 8; k++) {
+                acc[k].x += w * v[k].x;
+                acc[k].y += w * v[k].y;
+                acc[k].z += w * v[k].z;
+                acc[k].w += w * v[k].w;
+              }
+            }
+            uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * kHeadDim + c4 * 32);
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+              dst[k] = make_uint4(bf16_pair(acc[2 * k].x, acc[2 * k].y),
+                                  bf16_pair(acc[2 * k].z, acc[2 * k].w),
+                                  bf16_pair(acc[2 * k + 1].x, acc[2 * k + 1].y),
+                                  bf16_pair(acc[2 * k + 1].z, acc[2 * k + 1].w));
+          }
+          if (p.lse != nullptr)
+            p.lse[out_row] = (top - kHeadroom + log2f(sum)) * 0.693147180559945309f;
+        }
+      }
+      tc::fence_before();
+    }
+  } else if (warp < kMmaWarp) {
+    // ================================================= codes to fp16 tiles
+    const int w = warp - kSoftmaxWarps;  // tokens [32 w, 32 w + 32) of a tile
+    const int sub = lane >> 3, ch = lane & 7;  // token 4 i + sub, channels [16 ch, 16 ch + 16)
+    int step = 0;
+    // the pages of this warp's tokens, and whether they hold any
+    auto pages_of = [&](const Piece& pc, int tile, int (&pg)[2]) {
+#pragma unroll
+      for (int k = 0; k < 2; k++) {
+        const int i = tile * kTilePages + 2 * w + k;
+        pg[k] = -1;
+        if (i * kPage < len[pc.b]) {
+          const int page = p.page_table[(size_t)pc.b * p.rows.max_pages + i];
+          if (page >= 0 && page < p.num_pages) pg[k] = page * p.hkv + pc.h;
+          else set_error(p.err, kDevErrCheck);
+        }
+      }
+    };
+    auto load = [&](const uint8_t* codes, const int (&pg)[2], int base, int n, uint4 (&raw)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const int t = 4 * i + sub;  // token of the warp's 32
+        raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (pg[i >> 2] >= 0 && base + 32 * w + t < n)
+          raw[i] = ldg128_nc(codes + (size_t)pg[i >> 2] * kBlockBytesI8 + (t & 15) * kHeadDim +
+                             ch * 16);
+      }
+    };
+    // 16 codes are two 16-byte chunks; lanes of the upper channels store theirs in the other
+    // order, so that the 8 lanes of a row meet no bank twice
+    auto put = [&](unsigned char* tile, const uint4 (&raw)[8]) {
+      const int swap = ch >> 2;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const int t = 32 * w + 4 * i + sub;
+        unsigned char* row = tile + (ch >> 2) * kHalfBytes + (t >> 3) * 1024 + (t & 7) * 128;
+        uint32_t h[8];
+        const uint32_t c[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const uint32_t u = Codes<F>::prepare(c[k]);
+          h[2 * k] = Codes<F>::template pair<0>(u);
+          h[2 * k + 1] = Codes<F>::template pair<1>(u);
+        }
+        const int c0 = 2 * (ch & 3);
+        const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]);
+        const uint4 hi = make_uint4(h[4], h[5], h[6], h[7]);
+        *reinterpret_cast<uint4*>(row + (((c0 + swap) ^ (t & 7)) << 4)) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(row + (((c0 + 1 - swap) ^ (t & 7)) << 4)) = swap ? lo : hi;
+      }
+    };
+    // scales (s_k, s_v) of the tile's 8 pages: lanes 0-7 of the first warp
+    auto scales_of = [&](const Piece& pc, int tile) {
+      const int i = tile * kTilePages + (lane & 7);
+      float2 s = make_float2(0.0f, -1.0f);  // no tokens: p = 0
+      if (w == 0 && i * kPage < len[pc.b]) {
+        const int page = p.page_table[(size_t)pc.b * p.rows.max_pages + i];
+        if (page >= 0 && page < p.num_pages)
+          s = make_float2(p.k_scale[(size_t)page * p.hkv + pc.h],
+                          p.v_scale[(size_t)page * p.hkv + pc.h]);
+      }
+      return s;
+    };
+    auto publish = [&](const float2& s, int at) {
+      float big = s.y;
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+      // a block of zeros counts with the tile's largest scale (its codes are 0)
+      const float sv = s.y > 0.0f ? s.y : big > 0.0f ? big : 1.0f;
+      if (lane < 8)
+        sm.page[at % kPageRing][lane] = s.y < 0.0f
+                                            ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
+                                            : make_float4(s.x, lg2(sv), 1.0f / sv, 0.0f);
+    };
+    bool more = walk.next(pc);
+    int j = 0;
+    int pg[2];
+    uint4 rk[8], rv[8];
+    float2 scale = make_float2(0.0f, -1.0f);
+    if (more) {
+      scale = scales_of(pc, pc.tile);
+      pages_of(pc, pc.tile, pg);
+      load(p.k, pg, pc.tile * kTokens, len[pc.b], rk);
+      load(p.v, pg, pc.tile * kTokens, len[pc.b], rv);
+    }
+    while (more) {
+      const int st = step & 1, parity = ((step >> 1) & 1) ^ 1;
+      // the step after this one
+      Piece np = pc;
+      int nj = j + 1;
+      bool next = true;
+      if (nj == pc.tiles) {
+        nj = 0;
+        next = walk.next(np);
+      }
+      int npg[2] = {-1, -1};
+      const int base = next ? (np.tile + nj) * kTokens : 0, n = next ? len[np.b] : 0;
+      if (next) pages_of(np, np.tile + nj, npg);
+      if (!wait(sm, &sm.k_empty[st], parity, p.err)) break;
+      if (w == 0) publish(scale, step);
+      if (next) scale = scales_of(np, np.tile + nj);
+      put(sm.k[st], rk);
+      fence_proxy_async();
+      mbar_arrive(&sm.k_full[st]);
+      load(p.k, npg, base, n, rk);
+      if (!wait(sm, &sm.v_empty[st], parity, p.err)) break;
+      put(sm.v[st], rv);
+      fence_proxy_async();
+      mbar_arrive(&sm.v_full[st]);
+      load(p.v, npg, base, n, rv);
+      pc = np;
+      j = nj;
+      more = next;
+      step++;
+    }
+  } else {
+    // ================================================= the products
+    const uint32_t qk = tc::instr_f16(128, kTokens, false);
+    const uint32_t pv = tc::instr_f16(128, kHeadDim, true);
+    const uint32_t q_at[2] = {smem_addr(sm.q[0]), smem_addr(sm.q[1])};
+    int step = 0;
+    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+    bool ok = true;
+    // S of tile i against the K tile of step `at`
+    auto scores = [&](int i, int at) {
+      if (lane == 0) {
+        const uint32_t kb = smem_addr(sm.k[at & 1]);
+#pragma unroll
+        for (int c = 0; c < 8; c++) {
+          const uint32_t off = (c >> 2) * kHalfBytes + (c & 3) * 32;
+          tc::mma_ss(tmem + kColS + 128 * i, tc::smem_desc(q_at[i] + off, 16),
+                     tc::smem_desc(kb + off, 16), qk, c > 0);
+        }
+        tc::commit(&sm.s_full[i]);
+      }
+    };
+    while (ok && walk.next(pc)) {
+      const int tiles = pc.rows > 128 ? 2 : 1;
+      ok = wait(sm, &sm.k_full[step & 1], (step >> 1) & 1, p.err);
+      for (int i = 0; ok && i < tiles; i++) {
+        ok = wait(sm, &sm.q_full[i], q_phase[i], p.err);
+        if (!ok) break;
+        q_phase[i] ^= 1;
+        tc::fence_after();
+        scores(i, step);
+      }
+      if (!ok) break;
+      if (lane == 0) tc::commit(&sm.k_empty[step & 1]);
+      for (int j = 0; j < pc.tiles; j++, step++) {
+        const uint32_t vb = smem_addr(sm.v[step & 1]);
+        const bool more = j + 1 < pc.tiles;
+        for (int i = 0; i < tiles; i++) {
+          ok = wait(sm, &sm.p_full[i], p_phase[i], p.err);
+          if (ok && i == 0) {
+            ok = wait(sm, &sm.v_full[step & 1], (step >> 1) & 1, p.err);
+            if (ok && more) ok = wait(sm, &sm.k_full[(step + 1) & 1], ((step + 1) >> 1) & 1, p.err);
+          }
+          if (!ok) break;
+          p_phase[i] ^= 1;
+          tc::fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int c = 0; c < 8; c++)
+              tc::mma_ts(tmem + kColO + 128 * i, tmem + kColS + 128 * i + c * 8,
+                         tc::smem_desc(vb + c * 2048, kHalfBytes), pv, j > 0 || c > 0);
+            if (!more) tc::commit(&sm.o_full[i]);
+          }
+          __syncwarp();
+          if (more) scores(i, step + 1);
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          tc::commit(&sm.v_empty[step & 1]);
+          if (more) tc::commit(&sm.k_empty[(step + 1) & 1]);
+        }
+        __syncwarp();
+      }
+    }
+    // the last arrivals on the barriers come before the CTA ends
+    if (ok && step > 0) {
+      wait(sm, &sm.k_empty[(step - 1) & 1], ((step - 1) >> 1) & 1, p.err);
+      wait(sm, &sm.v_empty[(step - 1) & 1], ((step - 1) >> 1) & 1, p.err);
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after();
+    tc::dealloc(tmem, 512);
+  }
+}
+
+size_t smem_bytes(int batch) {
+  return 1024 + sizeof(Smem) + 8 * (size_t)(batch + 1) + 12 * (size_t)batch;
+}
+
+}  // namespace
+
+size_t kv8_prefill_part_floats() { return (size_t)2 * kKv8MaxCtas * kRows * kHeadDim; }
+size_t kv8_prefill_ml_floats() { return (size_t)2 * kKv8MaxCtas * kRows * 2; }
+
+cudaError_t launch_kv8_prefill(const Shape& s, const Kv8& c, const void* q, long long q_stride,
+                               const int32_t* cu, int total, const int32_t* page_table,
+                               const int32_t* seq_lens, void* out, float* lse, int* counters,
+                               float* part_ml, float* part_o, int* err, int num_sms,
+                               cudaStream_t st) {
+  Params p;
+  p.rows = NewRows{cu, seq_lens, s.batch, total, s.max_pages};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.k = static_cast<const uint8_t*>(c.k);
+  p.v = static_cast<const uint8_t*>(c.v);
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.page_table = page_table;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.part_ml = part_ml;
+  p.part_o = part_o;
+  p.counters = counters;
+  p.err = err;
+  p.hq = s.hq;
+  p.hkv = s.hkv;
+  p.group = s.group;
+  p.num_pages = s.num_pages;
+  p.block_tokens = kRows / s.group;
+  p.scale_log2 = s.sm_scale * 1.44269504088896341f;
+  auto kernel = c.format == kE4m3 ? kv8_prefill_kernel<kE4m3> : kv8_prefill_kernel<kInt8>;
+  const size_t smem = smem_bytes(s.batch);
+  const cudaError_t e = set_kernel_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kernel, dim3(std::min(num_sms, kKv8MaxCtas)), dim3(kThreads), smem, st,
+                       true, p);
+}
+
+}  // namespace hsa

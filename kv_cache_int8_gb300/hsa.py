@@ -43,6 +43,7 @@ EXPORTS = (
     "hsa_block_cache_bytes", "hsa_block_cache_mass", "hsa_attend_cached",
     "hsa_decode_step_cached",
     "hsa_kv8_write", "hsa_kv8_read", "hsa_kv8_decode", "hsa_kv8_attend",
+    "hsa_kv8_prefill",
 )
 
 
@@ -156,6 +157,7 @@ def load(path: Optional[str] = None):
         "hsa_kv8_read": (I32, [D, C, P, I64, P, I64, P, I32, P, P, P, SZ, P]),
         "hsa_kv8_decode": (I32, [D, C, P, P, P, P, P, P, SZ, P]),
         "hsa_kv8_attend": (I32, [D, C, P, P, P, P, P, P, P, P, SZ, P]),
+        "hsa_kv8_prefill": (I32, [D, C, P, I64, P, I32, P, P, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -458,6 +460,17 @@ def hsa_kv8_attend(d: Dims, cache: KV8, q, page_table, seq_lens, block_idx, n_bl
     _check("hsa_kv8_attend", load().hsa_kv8_attend(
         ctypes.byref(d.c()), cache._ref, _p(q), _p(page_table), _p(seq_lens), _p(block_idx),
         _p(n_blocks), _p(out), _p(lse), _p(ws), ws.numel(), _stream(stream)))
+
+
+def hsa_kv8_prefill(d: Dims, cache: KV8, q, cu_tokens, page_table, seq_lens, out, lse, ws,
+                    stream=None) -> None:
+    """q: bf16 [total_tokens][hq][128], rows contiguous (any row stride); out: bf16, contiguous."""
+    if not out.is_contiguous() or out.shape != q.shape or out.dtype != torch.bfloat16:
+        raise HsaError("hsa_kv8_prefill", HSA_ERR_INVALID_ARG, "out must be contiguous, as q")
+    _check("hsa_kv8_prefill", load().hsa_kv8_prefill(
+        ctypes.byref(d.c()), cache._ref, q.data_ptr(), _row_stride("hsa_kv8_prefill", q, d.hq),
+        _p(cu_tokens), q.shape[0], _p(page_table), _p(seq_lens), out.data_ptr(), _p(lse), _p(ws),
+        ws.numel(), _stream(stream)))
 
 
 def hsa_read_device_error(ws, stream=None) -> int:

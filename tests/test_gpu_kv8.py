@@ -303,3 +303,49 @@ def test_bad_pages_and_lengths_are_reported_not_followed():
         hsa.hsa_kv8_write(d, cache, k, k, torch.tensor(bad, dtype=torch.int32, device="cuda"),
                           s.gpu_table(), s.gpu_lens(), err)
         assert hsa.hsa_read_device_error(err) == hsa.HSA_ERR_DEVICE_CHECK
+
+
+# ------------------------------------------------------------------------ prompt attention
+
+def run_prefill(s, q, new, **kw):
+    d = s.dims(**kw)
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_PREFILL)
+    T = sum(new)
+    rows = to_bf16(q)
+    out = torch.full((T, s.hq, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, s.hq), float("nan"), device="cuda")
+    hsa.hsa_kv8_prefill(d, s.gpu_cache(), rows, cu_of(new), s.gpu_table(), s.gpu_lens(), out, lse,
+                        ws)
+    assert hsa.hsa_read_device_error(ws) == 0
+    assert int(ws[256:256 + 4 * 512].sum()) == 0  # counters left at zero
+    return out.float().cpu().numpy(), lse.cpu().numpy()
+
+
+def check_prefill(s, q, new, out, lse, sm_scale=D ** -0.5):
+    g = s.hq // s.hkv
+    at = 0
+    for b, (n, m) in enumerate(zip(s.lens, new)):
+        for h in range(s.hkv):
+            k, v = (O.values(s.cache, w, s.table[b], n, h) for w in "kv")
+            seen = np.arange(n)[None] <= (n - m + np.arange(m))[:, None]
+            for j in range(h * g, (h + 1) * g):
+                want, wl, tol = O.attend(q[at:at + m, j], k, v, seen, sm_scale)
+                # probabilities are rounded to fp16 before the product with V (half a step
+                # 2^-11 of each, so that much of the largest value), the result to bf16
+                tol["out"] = tol["out"] + 2.0 ** -11 * np.abs(v).max()
+                assert_rows(out[at:at + m, j], lse[at:at + m, j], want, wl, tol, 2.0 ** -8)
+        at += m
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("hq,hkv,lens,new", [
+    (1, 1, [1], [1]), (4, 1, [64], [64]), (8, 1, [128, 129], [128, 1]), (8, 8, [200], [200]),
+    (4, 1, [300], [300]), (3, 1, [500, 90], [170, 90]), (14, 2, [400], [77]),
+    (16, 2, [1, 17, 260, 1000], [1, 16, 0, 130]), (32, 8, [1500], [40]),
+    (64, 8, [333, 700], [1, 65]), (5, 1, [2048], [700]), (8, 2, [40] * 33, [3] * 33),
+])
+def test_prefill(fmt, hq, hkv, lens, new):
+    s = Batch(lens, hq, hkv, fmt, seed=len(lens) + hq, extra_pages=1)
+    q = bf16(s.rng.standard_normal((sum(new), hq, D)))
+    out, lse = run_prefill(s, q, new)
+    check_prefill(s, q, new, out, lse)
