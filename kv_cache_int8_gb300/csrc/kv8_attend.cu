@@ -99,6 +99,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// o += d. The products' own accumulation rounds towards zero: over the thousands of blocks that
+// a warp adds up, that alone put results 3e-6 off.
+__device__ __forceinline__ void add4(float (&o)[4], const float (&d)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2)
+    asm("{.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;}"
+        : "+f"(o[i]), "+f"(o[i + 1])
+        : "f"(d[i]), "f"(d[i + 1]));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -113,6 +124,12 @@ __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ float max32(float x) {
@@ -140,8 +157,8 @@ __device__ __forceinline__ int row_units(const Params& p, int n) {
 // One visit: the block's first row in the code arrays, its slots [lo, hi), its scales.
 struct alignas(16) Unit {
   int y;
-  int span;  // lo | hi << 8; 0: nothing to do
-  float sk, sv;
+  int span;       // lo | hi << 8; 0: nothing to do
+  float sk, sv;  // the scales; sv as it is used: log2 s_v (0 for a block of zeros)
 };
 
 // Places of a row on the line: with per > 0 a whole number of slices of `per`.
@@ -196,7 +213,8 @@ __device__ __forceinline__ Unit locate(const Params& p, const long long* pre, co
   t.y = block * kPage;
   t.span = lo | (hi << 8);
   t.sk = p.k_scale[block];
-  t.sv = p.v_scale[block];
+  const float sv = p.v_scale[block];
+  t.sv = sv > 0.0f ? lg2(sv) : 0.0f;
   return t;
 }
 
@@ -323,24 +341,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool pending = false;
   Unit ahead = {0, 0, 0.0f, 0.0f};
   const uint64_t policy = l2_evict_first_policy();
-  int asked = 0;              // visits whose copies were begun (those that have any)
-  int issued = 0, taken = 0;  // copies begun and waited for
+  int asked = 0;             // visits whose copies were begun (those that have any)
+  int flying = 0;            // copies begun and not yet waited for
+  int in = 0, out = 0;       // ring slots of the next copy to begin and to wait for
+  uint32_t phase = 0;        // of the barriers that `out` comes to
+  unsigned char* const ring = sm.ring[warp][0];
+  uint64_t* const full = sm.full[warp];
   bool dead = false;
-  // Begins the copies of the visits before `upto`. Those of later rows (from place `stop` on)
+  // Begins the copies of the visits before `upto`. Those of later rows (from visit `stop` on)
   // leave one slot of the ring free: the row's outputs will lie there.
-  auto issue_to = [&](int upto, long long stop) {
+  auto issue_to = [&](int upto, int stop) {
     for (upto = min(upto, mine); asked < upto; asked++) {
       const Unit& u = meta[asked % kMeta];
       if (u.span == 0 || dead) continue;
-      if (issued - taken >= kStages - (x0 + (long long)kWarps * asked < stop ? 0 : 1)) break;
+      if (flying >= kStages - (asked < stop ? 0 : 1)) break;
       if (lane == 0) {
-        const int st = issued % kStages;
-        unsigned char* dst = sm.ring[warp][st];
-        mbar_arrive_expect_tx(&sm.full[warp][st], kUnitBytes);
-        tma_load_2d_hint(dst, &k_map, 0, u.y, &sm.full[warp][st], policy);
-        tma_load_2d_hint(dst + kBlockBytesI8, &v_map, 0, u.y, &sm.full[warp][st], policy);
+        unsigned char* dst = ring + in * kUnitBytes;
+        mbar_arrive_expect_tx(full + in, kUnitBytes);
+        tma_load_2d_hint(dst, &k_map, 0, u.y, full + in, policy);
+        tma_load_2d_hint(dst + kBlockBytesI8, &v_map, 0, u.y, full + in, policy);
       }
-      issued++;
+      in = in == kStages - 1 ? 0 : in + 1;
+      flying++;
     }
   };
 
@@ -358,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (int)((unsigned)(x - pre[b]) / units);
     const long long row_begin = pre[b] + (long long)row * units, row_end = row_begin + units;
     const long long stop = min(row_end, end);
-    issue_to(i + kStages, stop);
+    const int i_stop = (int)((stop - x0 + kWarps - 1) / kWarps);  // this warp's visits before it
+    issue_to(i + kStages, i_stop);
 
     // ---- the query as right operands: head g, channels of chunk 2t + c, word w
     uint32_t qf[16];
@@ -405,12 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 4; c++) o[k][c] = 0.0f;
 
-    // o carries the values in units of 2^e0, e0 the largest exponent of a block's scale so far
-    float inv_unit = __uint_as_float(253u << 23);  // 2^-e0
-
     // two visits at a time: two independent chains of products, one reduction of the maximum
-    while (i < mine && x0 + (long long)kWarps * i < stop) {
-      const int two = i + 1 < mine && x0 + (long long)kWarps * (i + 1) < stop;
+    while (i < i_stop) {
+      const int two = i + 1 < i_stop;
       if (!pending && filled < mine && filled - i <= kBatch) {
         ahead = fetch(filled);
         pending = true;
@@ -423,18 +443,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       Unit ub = meta[(i + 1) % kMeta];
       if (!two) ub.span = 0;
       if ((ua.span | ub.span) != 0 && !dead) {
-        uint32_t kb[2], slot[2];
+        uint32_t kb[2];
         const int span[2] = {ua.span, ub.span};
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-          slot[h] = (taken % kStages);
-          kb[h] = smem_addr(sm.ring[warp][slot[h]]);
+          kb[h] = smem_addr(ring) + out * kUnitBytes;
           if (span[h] == 0) continue;
-          if (!mbar_wait(&sm.full[warp][slot[h]], (taken / kStages) & 1)) {
+          if (!mbar_wait(full + out, phase)) {
             set_error(p.err, kDevErrTimeout);
             dead = true;
           }
-          taken++;
+          flying--;
+          out++;
+          if (out == kStages) {
+            out = 0;
+            phase ^= 1;
+          }
         }
         // scores of tokens g (x[h][0], x[h][1]) and g + 8 (x[h][2], x[h][3])
         float x[2][4];
@@ -461,21 +485,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma16816(x[h], a0, a1, a2, a3, qf[c * 8 + w * 2], qf[c * 8 + w * 2 + 1]);
             }
         }
+        const float cv[2] = {ua.sv, ub.sv};
+        float n0 = -INFINITY, n1 = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
+        for (int h = 0; h < 2; h++) {  // y = x + log2 s_v
           const float sk = h ? ub.sk : ua.sk;
-          x[h][0] *= f0 * sk;
-          x[h][1] *= f1 * sk;
-          x[h][2] *= f0 * sk;
-          x[h][3] *= f1 * sk;
+          x[h][0] = fmaf(x[h][0], f0 * sk, cv[h]);
+          x[h][1] = fmaf(x[h][1], f1 * sk, cv[h]);
+          x[h][2] = fmaf(x[h][2], f0 * sk, cv[h]);
+          x[h][3] = fmaf(x[h][3], f1 * sk, cv[h]);
           if (span[h] != (kPage << 8)) {
             const int lo = span[h] & 255, hi = span[h] >> 8;
             if (g < lo || g >= hi) x[h][0] = x[h][1] = -INFINITY;
             if (g + 8 < lo || g + 8 >= hi) x[h][2] = x[h][3] = -INFINITY;
           }
+          n0 = fmaxf(n0, fmaxf(x[h][0], x[h][2]));
+          n1 = fmaxf(n1, fmaxf(x[h][1], x[h][3]));
         }
-        float n0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-        float n1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
           n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, d));
@@ -497,28 +523,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[k][3] *= a1;
           }
         }
-        const float sv = fmaxf(ua.span ? ua.sv : 0.0f, ub.span ? ub.sv : 0.0f);
-        if (sv * inv_unit >= 2.0f) {
-          const float to = __uint_as_float((254u << 23) - (__float_as_uint(sv) & 0x7F800000u));
-          const float by = to / inv_unit;
-          inv_unit = to;
-#pragma unroll
-          for (int k = 0; k < 8; k++)
-#pragma unroll
-            for (int c = 0; c < 4; c++) o[k][c] *= by;
-        }
+        const float ref0 = m0 - kHeadroom, ref1 = m1 - kHeadroom;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
           if (span[h] == 0) continue;
-          float p00 = ex2(x[h][0] - m0 + kHeadroom), p01 = ex2(x[h][1] - m1 + kHeadroom);
-          float p10 = ex2(x[h][2] - m0 + kHeadroom), p11 = ex2(x[h][3] - m1 + kHeadroom);
-          l0 += p00 + p10;
-          l1 += p01 + p11;
-          const float scale = (h ? ub.sv : ua.sv) * inv_unit;
-          p00 *= scale;
-          p01 *= scale;
-          p10 *= scale;
-          p11 *= scale;
+          const float p00 = ex2(x[h][0] - ref0), p01 = ex2(x[h][1] - ref1);
+          const float p10 = ex2(x[h][2] - ref0), p11 = ex2(x[h][3] - ref1);
+          const float per_s = ex2(-cv[h]);  // 1 / s_v
+          l0 = fmaf(p00 + p10, per_s, l0);
+          l1 = fmaf(p01 + p11, per_s, l1);
           const uint32_t ha = half_pair(p00, p01), hb = half_pair(p10, p11);
           const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
           const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hb));
@@ -552,15 +565,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t a1 = Codes<F>::template pair<1>(ab);
               const uint32_t a2 = Codes<F>::template pair<0>(cd);
               const uint32_t a3 = Codes<F>::template pair<1>(cd);
-              mma16816(o[2 * w + c], a0, a1, a2, a3, b0, b1);
-              mma16816(o[2 * w + c], a0, a1, a2, a3, r0, r1);
+              float d[4];
+              mma16816_zero(d, a0, a1, a2, a3, b0, b1);
+              mma16816(d, a0, a1, a2, a3, r0, r1);
+              add4(o[2 * w + c], d);
             }
           }
         }
       }
       i += 1 + two;
       __syncwarp();  // the slots are read before they are filled again
-      issue_to(i + kStages, stop);
+      issue_to(i + kStages, i_stop);
     }
 
     // ---- the warps' parts of the row meet
@@ -574,13 +589,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm.ml[2 * t + 1][warp] = make_float2(m1, l1);
     }
     {
-      const float unit = 1.0f / inv_unit;
-      const int slot = (taken + kStages - 1) % kStages;  // free: see issue_to
+      const int slot = out == 0 ? kStages - 1 : out - 1;  // free: see issue_to
       float4* dst = reinterpret_cast<float4*>(sm.ring[warp][slot]);
 #pragma unroll
       for (int k = 0; k < 8; k++)
-        dst[k * 32 + lane] =
-            make_float4(o[k][0] * unit, o[k][1] * unit, o[k][2] * unit, o[k][3] * unit);
+        dst[k * 32 + lane] = make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
       if (lane == 0) sm.slot[warp] = slot;
     }
     __syncthreads();

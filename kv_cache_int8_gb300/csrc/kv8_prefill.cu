@@ -39,10 +39,14 @@ constexpr int kTileBytes = 128 * kHeadDim * 2;
 constexpr int kHalfBytes = kTileBytes / 2;  // 64 channels of 128 rows
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kConvertWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kThreads = 512;  // four warpgroups, the last of which is warp 12 and three idle ones
+// registers a thread of the softmax, conversion and product warpgroups: 128 on average
+constexpr int kSoftmaxRegs = 176, kConvertRegs = 104, kMmaRegs = 56;
+static_assert(2 * kSoftmaxRegs + kConvertRegs + kMmaRegs == 4 * 128, "the launch's registers");
 constexpr int kPageRing = 4;
 constexpr float kHeadroom = 10.0f;
 constexpr float kLag = 4.0f;
+constexpr float kTiny = 1e-37f;  // scales of scores stay positive: a masked -inf stays one
 constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns; tile i at + 128 i
 
 struct Params {
@@ -82,6 +86,28 @@ struct Smem {
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// a * m + c and a + b on two values at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 m, float2 c) {
+  float2 y;
+  asm("{.reg .b64 a, m, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 m, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 a, a, m, c;\n\tmov.b64 {%0, %1}, a;}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(m.x), "f"(m.y), "f"(c.x), "f"(c.y));
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return y;
 }
 __device__ __forceinline__ float lg2(float x) {
@@ -295,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
   Piece pc;
 
   if (warp < kSoftmaxWarps) {
+    tc::more_registers<kSoftmaxRegs>();
     // ================================================= softmax: one row a thread
     const int tile = warp >> 2, r = tid & 127, row = tile * 128 + r;
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
@@ -369,30 +396,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         const float4* page = sm.page[step % kPageRing];
         const bool masked = !full_rows || base + kTokens - 1 > first_pos;
         const int limit = pos - base;  // columns up to it are seen
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; c++) tc::load32(s_col + c * 32, s[c]);
+        tc::wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 4; c++)
+#pragma unroll
+            for (int k = 0; k < 32; k++)
+              if (c * 32 + k > limit) s[c][k] = 0xFF800000u;
+        }
         // ---- the row's maximum
         float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
-          uint32_t s[32];
-          tc::load32(s_col + c * 32, s);
-          tc::wait_ld();
-          if (masked) {
+        for (int g = 0; g < kTilePages; g++) {
+          const uint32_t* v = &s[g >> 1][16 * (g & 1)];
+          float a = __uint_as_float(v[0]);
 #pragma unroll
-            for (int k = 0; k < 32; k++)
-              if (c * 32 + k > limit) s[k] = 0xFF800000u;
-          }
-#pragma unroll
-          for (int g = 0; g < 2; g++) {
-            const float4 pg = page[2 * c + g];
-            float a = __uint_as_float(s[16 * g]), b = __uint_as_float(s[16 * g + 1]);
-#pragma unroll
-            for (int k = 2; k < 16; k += 2) {
-              a = fmaxf(a, __uint_as_float(s[16 * g + k]));
-              b = fmaxf(b, __uint_as_float(s[16 * g + k + 1]));
-            }
-            a = fmaxf(a, b);
-            if (a != -INFINITY) top = fmaxf(top, a * (f * pg.x) + pg.y);
-          }
+          for (int k = 1; k < 15; k += 2) a = max3(a, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+          a = fmaxf(a, __uint_as_float(v[15]));
+          const float4 pg = page[g];
+          top = fmaxf(top, fmaf(a, fmaxf(f * pg.x, kTiny), pg.y));
         }
         // ---- the accumulator follows a maximum that has grown by more than kLag
         if (__any_sync(0xffffffffu, top > m + kLag)) {
@@ -401,14 +426,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           m = top;
           l *= by;
           if (j > 0) {
-#pragma unroll
-            for (int c = 0; c < 4; c++) {
-              uint32_t o[32];
-              tc::load32(o_col + c * 32, o);
+#pragma unroll 1
+            for (int c = 0; c < 8; c++) {
+              uint32_t o[16];
+              tc::load16(o_col + c * 16, o);
               tc::wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
-              tc::store32(o_col + c * 32, o);
+              for (int k = 0; k < 16; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
+              tc::store16(o_col + c * 16, o);
             }
           }
         }
@@ -416,28 +441,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         // ---- P, over S
 #pragma unroll
         for (int c = 0; c < 4; c++) {
-          uint32_t s[32], w[16];
-          tc::load32(s_col + c * 32, s);
-          tc::wait_ld();
+          uint32_t w[16];
 #pragma unroll
           for (int g = 0; g < 2; g++) {
             const float4 pg = page[2 * c + g];
-            const float mul = f * pg.x, add = pg.y - ref;
-            float sum = 0.0f;
+            const float mul = fmaxf(f * pg.x, kTiny), add = pg.y - ref;
+            float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
-              float a = fmaf(__uint_as_float(s[16 * g + k]), mul, add);
-              float b = fmaf(__uint_as_float(s[16 * g + k + 1]), mul, add);
-              if (masked) {
-                if (c * 32 + 16 * g + k > limit) a = -INFINITY;
-                if (c * 32 + 16 * g + k + 1 > limit) b = -INFINITY;
-              }
-              a = ex2(a);
-              b = ex2(b);
-              sum += a + b;
-              w[8 * g + k / 2] = half_pair(a, b);
+              float2 y = fma2(make_float2(__uint_as_float(s[c][16 * g + k]),
+                                          __uint_as_float(s[c][16 * g + k + 1])),
+                              make_float2(mul, mul), make_float2(add, add));
+              y.x = ex2(y.x);
+              y.y = ex2(y.y);
+              sum = k == 0 ? y : add2(sum, y);
+              w[8 * g + k / 2] = half_pair(y.x, y.y);
             }
-            l = fmaf(sum, pg.z, l);
+            l = fmaf(sum.x + sum.y, pg.z, l);
           }
           tc::store16(s_col + c * 16, w);
         }
@@ -452,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       const bool whole = pc.tiles == pc.all_tiles;
       if (whole) {
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; c++) {
           uint32_t o[32];
           tc::load32(o_col + c * 32, o);
@@ -479,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         const int parts = (int)((block_begin + pc.all_tiles - 1) / per) - c0 + 1;
         const size_t slot = 2 * (size_t)blockIdx.x + (begin < block_begin ? 1 : 0);
         float4* po = reinterpret_cast<float4*>(p.part_o) + slot * 32 * kRows + row;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; c++) {
           uint32_t o[32];
           tc::load32(o_col + c * 32, o);
@@ -514,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
             sum += ex2(v.x - ref) * v.y;
           }
           const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
+#pragma unroll 1
           for (int c4 = 0; c4 < 4; c4++) {  // 32 channels at a time
             float4 acc[8];
 #pragma unroll
@@ -550,6 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       tc::fence_before();
     }
   } else if (warp < kMmaWarp) {
+    tc::fewer_registers<kConvertRegs>();
     // ================================================= codes to fp16 tiles
     const int w = warp - kSoftmaxWarps;  // tokens [32 w, 32 w + 32) of a tile
     const int sub = lane >> 3, ch = lane & 7;  // token 4 i + sub, channels [16 ch, 16 ch + 16)
@@ -665,6 +686,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       step++;
     }
   } else {
+    tc::fewer_registers<kMmaRegs>();
+  }
+  if (warp == kMmaWarp) {
     // ================================================= the products
     const uint32_t qk = tc::instr_f16(128, kTokens, false);
     const uint32_t pv = tc::instr_f16(128, kHeadDim, true);
