@@ -63,6 +63,14 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return d;
 }
 
+__device__ __forceinline__ uint2 ldg64_nc(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "l"(p));
+  return v;
+}
+
 // Code bytes to fp16 pairs, exactly.
 //  int8: the byte with its sign bit flipped, u = code + 128, under the byte 0x64 is the fp16
 //    number 1024 + u; less 1152 that is the code (a permute and an add a pair).

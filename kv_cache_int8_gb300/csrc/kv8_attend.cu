@@ -158,7 +158,8 @@ __device__ __forceinline__ int row_units(const Params& p, int n) {
 struct alignas(16) Unit {
   int y;
   int span;       // lo | hi << 8; 0: nothing to do
-  float sk, sv;  // the scales; sv as it is used: log2 s_v (0 for a block of zeros)
+  float sk, sv;  // the scales; sv as it is used: log2 s_v (-100 for a block of zeros:
+                 // below any other, it then takes no part in the choice of m)
 };
 
 // Places of a row on the line: with per > 0 a whole number of slices of `per`.
@@ -214,7 +215,7 @@ __device__ __forceinline__ Unit locate(const Params& p, const long long* pre, co
   t.span = lo | (hi << 8);
   t.sk = p.k_scale[block];
   const float sv = p.v_scale[block];
-  t.sv = sv > 0.0f ? lg2(sv) : 0.0f;
+  t.sv = sv > 0.0f ? lg2(sv) : -100.0f;
   return t;
 }
 

@@ -199,14 +199,6 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return d;
 }
 
-__device__ __forceinline__ uint2 ldg64_nc(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
-               : "l"(p));
-  return v;
-}
-
 // Lanes as in the write: 8 bytes of codes in, 16 bytes of bf16 out.
 template <int F>
 __global__ void __launch_bounds__(kWarps * 32) kv8_read_kernel(

@@ -37,12 +37,12 @@ constexpr int kTokens = 128;       // tokens of a step
 constexpr int kTilePages = kTokens / kPage;
 constexpr int kTileBytes = 128 * kHeadDim * 2;
 constexpr int kHalfBytes = kTileBytes / 2;  // 64 channels of 128 rows
-constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
-constexpr int kMmaWarp = kSoftmaxWarps + kConvertWarps;
-constexpr int kThreads = 512;  // four warpgroups, the last of which is warp 12 and three idle ones
-// registers a thread of the softmax, conversion and product warpgroups: 128 on average
-constexpr int kSoftmaxRegs = 176, kConvertRegs = 104, kMmaRegs = 56;
-static_assert(2 * kSoftmaxRegs + kConvertRegs + kMmaRegs == 4 * 128, "the launch's registers");
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 12;  // warps 0-7; 12; the other 7 convert
+constexpr int kConvertWarps = 7;
+constexpr int kThreads = 512;
+// registers a thread of the softmax warpgroups and of the other two: 128 on average
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
+static_assert(2 * (kSoftmaxRegs + kOtherRegs) == 4 * 128, "the launch's registers");
 constexpr int kPageRing = 4;
 constexpr float kHeadroom = 10.0f;
 constexpr float kLag = 4.0f;
@@ -213,9 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
   if (tid == 0) {
     for (int i = 0; i < 2; i++) {
       mbar_init(&sm.q_full[i], 128);
-      mbar_init(&sm.k_full[i], 32 * kConvertWarps);
+      mbar_init(&sm.k_full[i], kTilePages);
       mbar_init(&sm.k_empty[i], 1);
-      mbar_init(&sm.v_full[i], 32 * kConvertWarps);
+      mbar_init(&sm.v_full[i], kTilePages);
       mbar_init(&sm.v_empty[i], 1);
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], 128);
@@ -569,182 +569,180 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       }
       tc::fence_before();
     }
-  } else if (warp < kMmaWarp) {
-    tc::fewer_registers<kConvertRegs>();
-    // ================================================= codes to fp16 tiles
-    const int w = warp - kSoftmaxWarps;  // tokens [32 w, 32 w + 32) of a tile
-    const int sub = lane >> 3, ch = lane & 7;  // token 4 i + sub, channels [16 ch, 16 ch + 16)
-    int step = 0;
-    // the pages of this warp's tokens, and whether they hold any
-    auto pages_of = [&](const Piece& pc, int tile, int (&pg)[2]) {
-#pragma unroll
-      for (int k = 0; k < 2; k++) {
-        const int i = tile * kTilePages + 2 * w + k;
-        pg[k] = -1;
-        if (i * kPage < len[pc.b]) {
-          const int page = p.page_table[(size_t)pc.b * p.rows.max_pages + i];
-          if (page >= 0 && page < p.num_pages) pg[k] = page * p.hkv + pc.h;
-          else set_error(p.err, kDevErrCheck);
-        }
-      }
-    };
-    auto load = [&](const uint8_t* codes, const int (&pg)[2], int base, int n, uint4 (&raw)[8]) {
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        const int t = 4 * i + sub;  // token of the warp's 32
-        raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (pg[i >> 2] >= 0 && base + 32 * w + t < n)
-          raw[i] = ldg128_nc(codes + (size_t)pg[i >> 2] * kBlockBytesI8 + (t & 15) * kHeadDim +
-                             ch * 16);
-      }
-    };
-    // 16 codes are two 16-byte chunks; lanes of the upper channels store theirs in the other
-    // order, so that the 8 lanes of a row meet no bank twice
-    auto put = [&](unsigned char* tile, const uint4 (&raw)[8]) {
-      const int swap = ch >> 2;
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        const int t = 32 * w + 4 * i + sub;
-        unsigned char* row = tile + (ch >> 2) * kHalfBytes + (t >> 3) * 1024 + (t & 7) * 128;
-        uint32_t h[8];
-        const uint32_t c[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-          const uint32_t u = Codes<F>::prepare(c[k]);
-          h[2 * k] = Codes<F>::template pair<0>(u);
-          h[2 * k + 1] = Codes<F>::template pair<1>(u);
-        }
-        const int c0 = 2 * (ch & 3);
-        const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]);
-        const uint4 hi = make_uint4(h[4], h[5], h[6], h[7]);
-        *reinterpret_cast<uint4*>(row + (((c0 + swap) ^ (t & 7)) << 4)) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(row + (((c0 + 1 - swap) ^ (t & 7)) << 4)) = swap ? lo : hi;
-      }
-    };
-    // scales (s_k, s_v) of the tile's 8 pages: lanes 0-7 of the first warp
-    auto scales_of = [&](const Piece& pc, int tile) {
-      const int i = tile * kTilePages + (lane & 7);
-      float2 s = make_float2(0.0f, -1.0f);  // no tokens: p = 0
-      if (w == 0 && i * kPage < len[pc.b]) {
-        const int page = p.page_table[(size_t)pc.b * p.rows.max_pages + i];
-        if (page >= 0 && page < p.num_pages)
-          s = make_float2(p.k_scale[(size_t)page * p.hkv + pc.h],
-                          p.v_scale[(size_t)page * p.hkv + pc.h]);
-      }
-      return s;
-    };
-    auto publish = [&](const float2& s, int at) {
-      float big = s.y;
-#pragma unroll
-      for (int d = 1; d < 8; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-      // a block of zeros counts with the tile's largest scale (its codes are 0)
-      const float sv = s.y > 0.0f ? s.y : big > 0.0f ? big : 1.0f;
-      if (lane < 8)
-        sm.page[at % kPageRing][lane] = s.y < 0.0f
-                                            ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
-                                            : make_float4(s.x, lg2(sv), 1.0f / sv, 0.0f);
-    };
-    bool more = walk.next(pc);
-    int j = 0;
-    int pg[2];
-    uint4 rk[8], rv[8];
-    float2 scale = make_float2(0.0f, -1.0f);
-    if (more) {
-      scale = scales_of(pc, pc.tile);
-      pages_of(pc, pc.tile, pg);
-      load(p.k, pg, pc.tile * kTokens, len[pc.b], rk);
-      load(p.v, pg, pc.tile * kTokens, len[pc.b], rv);
-    }
-    while (more) {
-      const int st = step & 1, parity = ((step >> 1) & 1) ^ 1;
-      // the step after this one
-      Piece np = pc;
-      int nj = j + 1;
-      bool next = true;
-      if (nj == pc.tiles) {
-        nj = 0;
-        next = walk.next(np);
-      }
-      int npg[2] = {-1, -1};
-      const int base = next ? (np.tile + nj) * kTokens : 0, n = next ? len[np.b] : 0;
-      if (next) pages_of(np, np.tile + nj, npg);
-      if (!wait(sm, &sm.k_empty[st], parity, p.err)) break;
-      if (w == 0) publish(scale, step);
-      if (next) scale = scales_of(np, np.tile + nj);
-      put(sm.k[st], rk);
-      fence_proxy_async();
-      mbar_arrive(&sm.k_full[st]);
-      load(p.k, npg, base, n, rk);
-      if (!wait(sm, &sm.v_empty[st], parity, p.err)) break;
-      put(sm.v[st], rv);
-      fence_proxy_async();
-      mbar_arrive(&sm.v_full[st]);
-      load(p.v, npg, base, n, rv);
-      pc = np;
-      j = nj;
-      more = next;
-      step++;
-    }
   } else {
-    tc::fewer_registers<kMmaRegs>();
+    tc::fewer_registers<kOtherRegs>();
+  }
+  if (warp > kSoftmaxWarps - 1 && warp != kMmaWarp) {
+    // ================================================= codes to fp16 tiles
+    // A step's 16 items, the 8 blocks of K and then of V, go to the warps in turn, across steps:
+    // warp c has items c, c + 7, c + 14, ... of all. Lane: 8 channels of tokens 2 i + lane / 16.
+    const int sub = lane >> 4, ch = lane & 15;
+    uint32_t off[4];  // of token 2 i + sub, i < 4, in the block's part of the tile
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int t = 2 * i + sub;
+      off[i] = (ch >> 3) * kHalfBytes + t * 128 + (((ch & 7) ^ t) << 4);
+    }
+    struct Item {
+      int block;  // in the code arrays, or -1
+      int valid;  // its first tokens that exist
+    };
+    // the locating side runs ahead of the converting side
+    bool more = walk.next(pc);
+    int tile = 0, at_k = warp < kMmaWarp ? warp - kSoftmaxWarps : warp - kSoftmaxWarps - 1;
+    auto locate = [&]() {
+      Item it = {-1, 0};
+      if (more) {
+        const int i = (pc.tile + tile) * kTilePages + (at_k & 7);
+        it.valid = min(max(len[pc.b] - i * kPage, 0), kPage);
+        if (it.valid > 0) {
+          const int page = p.page_table[(size_t)pc.b * p.rows.max_pages + i];
+          if (page >= 0 && page < p.num_pages) {
+            it.block = page * p.hkv + pc.h;
+          } else {
+            set_error(p.err, kDevErrCheck);
+            it.valid = 0;
+          }
+        }
+        at_k += kConvertWarps;
+        if (at_k >= 2 * kTilePages) {
+          at_k -= 2 * kTilePages;
+          if (++tile == pc.tiles) {
+            tile = 0;
+            more = walk.next(pc);
+          }
+        }
+      } else {
+        it.valid = -1;  // there is none
+      }
+      return it;
+    };
+    auto load = [&](const Item& it, int k, uint2 (&raw)[8], float2& scale) {
+      const uint8_t* src = (k < kTilePages ? p.k : p.v) + (size_t)max(it.block, 0) * kBlockBytesI8 +
+                           sub * kHeadDim + ch * 8;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        raw[i] = make_uint2(0u, 0u);
+        if (2 * i + sub < it.valid) raw[i] = ldg64_nc(src + 2 * i * kHeadDim);
+      }
+      scale = make_float2(0.0f, -1.0f);
+      if (k < kTilePages && it.valid > 0)
+        scale = make_float2(p.k_scale[it.block], p.v_scale[it.block]);
+    };
+    int step = 0, k = at_k;  // the converting side
+    auto convert = [&](const uint2 (&raw)[8], const float2& scale) {
+      const int st = step & 1, parity = ((step >> 1) & 1) ^ 1;
+      const bool is_k = k < kTilePages;
+      if (!wait(sm, is_k ? &sm.k_empty[st] : &sm.v_empty[st], parity, p.err)) return false;
+      unsigned char* dst = (is_k ? sm.k[st] : sm.v[st]) + (k & 7) * (kPage * 128);
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const uint32_t x = Codes<F>::prepare(raw[i].x), y = Codes<F>::prepare(raw[i].y);
+        *reinterpret_cast<uint4*>(dst + off[i & 3] + (i >> 2) * 1024) =
+            make_uint4(Codes<F>::template pair<0>(x), Codes<F>::template pair<1>(x),
+                       Codes<F>::template pair<0>(y), Codes<F>::template pair<1>(y));
+      }
+      // s_k, log2 s_v, 1 / s_v. No tokens: p = 0. A block of zeros in V counts as 2^-100, below
+      // any other, so that it takes no part in the choice of M.
+      if (is_k && lane == 0)
+        sm.page[step % kPageRing][k] =
+            scale.y < 0.0f    ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
+            : scale.y == 0.0f ? make_float4(scale.x, -100.0f, 0x1p100f, 0.0f)
+                              : make_float4(scale.x, lg2(scale.y), 1.0f / scale.y, 0.0f);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(is_k ? &sm.k_full[st] : &sm.v_full[st]);
+      k += kConvertWarps;
+      if (k >= 2 * kTilePages) {
+        k -= 2 * kTilePages;
+        step++;
+      }
+      return true;
+    };
+    // two items of codes under way, the place of a third known
+    auto after = [](int k) {  // the item kConvertWarps on
+      return k + kConvertWarps >= 2 * kTilePages ? k + kConvertWarps - 2 * kTilePages
+                                                 : k + kConvertWarps;
+    };
+    uint2 ra[8], rb[8];
+    float2 sa, sb;
+    Item ia = locate(), ib = locate(), ic = locate();
+    load(ia, k, ra, sa);
+    load(ib, after(k), rb, sb);
+    while (ia.valid >= 0) {
+      if (!convert(ra, sa)) break;
+      ia = ic;
+      load(ia, after(k), ra, sa);
+      ic = locate();
+      if (ib.valid < 0 || !convert(rb, sb)) break;
+      ib = ic;
+      load(ib, after(k), rb, sb);
+      ic = locate();
+    }
   }
   if (warp == kMmaWarp) {
     // ================================================= the products
-    const uint32_t qk = tc::instr_f16(128, kTokens, false);
-    const uint32_t pv = tc::instr_f16(128, kHeadDim, true);
-    const uint32_t q_at[2] = {smem_addr(sm.q[0]), smem_addr(sm.q[1])};
+    constexpr uint32_t kQk = tc::instr_f16(128, kTokens, false);
+    constexpr uint32_t kPv = tc::instr_f16(128, kHeadDim, true);
+    const uint32_t q_low = tc::desc_low(smem_addr(sm.q[0]), 16);
+    const uint32_t k_low = tc::desc_low(smem_addr(sm.k[0]), 16);
+    const uint32_t v_low = tc::desc_low(smem_addr(sm.v[0]), kHalfBytes);
+    const bool lead = tc::elect();
     int step = 0;
     uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
     bool ok = true;
     // S of tile i against the K tile of step `at`
     auto scores = [&](int i, int at) {
-      if (lane == 0) {
-        const uint32_t kb = smem_addr(sm.k[at & 1]);
+      if (lead) {
+        const uint32_t q = q_low + i * (kTileBytes >> 4), k = k_low + (at & 1) * (kTileBytes >> 4);
 #pragma unroll
         for (int c = 0; c < 8; c++) {
-          const uint32_t off = (c >> 2) * kHalfBytes + (c & 3) * 32;
-          tc::mma_ss(tmem + kColS + 128 * i, tc::smem_desc(q_at[i] + off, 16),
-                     tc::smem_desc(kb + off, 16), qk, c > 0);
+          const uint32_t off = ((c >> 2) * kHalfBytes + (c & 3) * 32) >> 4;
+          tc::mma_ss<kQk>(tmem + kColS + 128 * i, q + off, k + off, c > 0);
         }
         tc::commit(&sm.s_full[i]);
       }
     };
+    // O of tile i += P V of step `at`
+    auto values = [&](int i, int at, bool add, bool last) {
+      if (lead) {
+        const uint32_t v = v_low + (at & 1) * (kTileBytes >> 4);
+#pragma unroll
+        for (int c = 0; c < 8; c++)
+          tc::mma_ts<kPv>(tmem + kColO + 128 * i, tmem + kColS + 128 * i + c * 8,
+                          v + c * (2048 >> 4), add || c > 0);
+        if (last) tc::commit(&sm.o_full[i]);
+      }
+    };
     while (ok && walk.next(pc)) {
-      const int tiles = pc.rows > 128 ? 2 : 1;
+      const bool two = pc.rows > 128;
       ok = wait(sm, &sm.k_full[step & 1], (step >> 1) & 1, p.err);
-      for (int i = 0; ok && i < tiles; i++) {
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        if (!ok || (i == 1 && !two)) continue;
         ok = wait(sm, &sm.q_full[i], q_phase[i], p.err);
-        if (!ok) break;
+        if (!ok) continue;
         q_phase[i] ^= 1;
         tc::fence_after();
         scores(i, step);
       }
       if (!ok) break;
-      if (lane == 0) tc::commit(&sm.k_empty[step & 1]);
-      for (int j = 0; j < pc.tiles; j++, step++) {
-        const uint32_t vb = smem_addr(sm.v[step & 1]);
+      if (lead) tc::commit(&sm.k_empty[step & 1]);
+      for (int j = 0; ok && j < pc.tiles; j++, step++) {
         const bool more = j + 1 < pc.tiles;
-        for (int i = 0; i < tiles; i++) {
+        ok = wait(sm, &sm.v_full[step & 1], (step >> 1) & 1, p.err);
+        if (ok && more) ok = wait(sm, &sm.k_full[(step + 1) & 1], ((step + 1) >> 1) & 1, p.err);
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          if (!ok || (i == 1 && !two)) continue;
           ok = wait(sm, &sm.p_full[i], p_phase[i], p.err);
-          if (ok && i == 0) {
-            ok = wait(sm, &sm.v_full[step & 1], (step >> 1) & 1, p.err);
-            if (ok && more) ok = wait(sm, &sm.k_full[(step + 1) & 1], ((step + 1) >> 1) & 1, p.err);
-          }
-          if (!ok) break;
+          if (!ok) continue;
           p_phase[i] ^= 1;
           tc::fence_after();
-          if (lane == 0) {
-#pragma unroll
-            for (int c = 0; c < 8; c++)
-              tc::mma_ts(tmem + kColO + 128 * i, tmem + kColS + 128 * i + c * 8,
-                         tc::smem_desc(vb + c * 2048, kHalfBytes), pv, j > 0 || c > 0);
-            if (!more) tc::commit(&sm.o_full[i]);
-          }
-          __syncwarp();
+          values(i, step, j > 0, !more);
           if (more) scores(i, step + 1);
         }
-        if (!ok) break;
-        if (lane == 0) {
+        if (ok && lead) {
           tc::commit(&sm.v_empty[step & 1]);
           if (more) tc::commit(&sm.k_empty[(step + 1) & 1]);
         }

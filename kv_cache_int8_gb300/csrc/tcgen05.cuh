@@ -40,12 +40,21 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
       : "memory");
 }
 
-// Shared-memory operand of 16-bit values under the 128-byte swizzle, in rows of 128 bytes and
-// groups of 8 rows (1024 bytes). lbo: bytes between 64-value parts of the N extent (operands
-// whose N runs along the rows); the groups of 8 rows are 1024 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | (1ULL << 46) | (2ULL << 61);
+// One lane of the warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
+// Shared-memory operands are described by 64 bits, of which the upper half is the same for all
+// here: 16-bit values under the 128-byte swizzle in rows of 128 bytes, groups of 8 rows 1024
+// bytes apart. The lower half holds the address / 16 (add distances / 16 to it) and `lbo`: the
+// bytes between 64-value parts of the N extent, for operands whose N runs along the rows.
+constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) {
+  return (addr >> 4) | ((lbo >> 4) << 16);
 }
 
 // fp16 operands, fp32 result, M x N; b_along_n: B's rows run along N (each row one k).
@@ -54,22 +63,26 @@ __host__ __device__ constexpr uint32_t instr_f16(int m, int n, bool b_along_n) {
          ((uint32_t)(m >> 4) << 24);
 }
 
-// d (TMEM) = a b (+ d): a and b in shared memory, 16 values of k.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t instr,
-                                       bool add) {
+// d (TMEM) = a b (+ d): a and b in shared memory, 16 values of k. One lane issues them; what it
+// passes is the same in the whole warp and the instruction word a constant, or the registers'
+// way to the tensor core costs more than the product (64 cycles at 128 x 128).
+template <uint32_t kInstr>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(instr), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+      "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"((uint32_t)add), "r"(kDescHigh), "r"(kInstr)
       : "memory");
 }
 // The same with a in TMEM.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t instr,
-                                       bool add) {
+template <uint32_t kInstr>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(instr), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+      "mov.b64 b, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"((uint32_t)add), "r"(kDescHigh), "r"(kInstr)
       : "memory");
 }
 
