@@ -584,26 +584,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       off[i] = (ch >> 3) * kHalfBytes + t * 128 + (((ch & 7) ^ t) << 4);
     }
     struct Item {
-      int block;  // in the code arrays, or -1
-      int valid;  // its first tokens that exist
+      int page, h;  // the page (looked at only when the codes are loaded: its own load takes
+                    // hundreds of cycles) and the kv head
+      int valid;    // its first tokens that exist; -1: there is no such item
     };
     // the locating side runs ahead of the converting side
     bool more = walk.next(pc);
     int tile = 0, at_k = warp < kMmaWarp ? warp - kSoftmaxWarps : warp - kSoftmaxWarps - 1;
     auto locate = [&]() {
-      Item it = {-1, 0};
+      Item it = {-1, 0, 0};
       if (more) {
         const int i = (pc.tile + tile) * kTilePages + (at_k & 7);
+        it.h = pc.h;
         it.valid = min(max(len[pc.b] - i * kPage, 0), kPage);
-        if (it.valid > 0) {
-          const int page = p.page_table[(size_t)pc.b * p.rows.max_pages + i];
-          if (page >= 0 && page < p.num_pages) {
-            it.block = page * p.hkv + pc.h;
-          } else {
-            set_error(p.err, kDevErrCheck);
-            it.valid = 0;
-          }
-        }
+        if (it.valid > 0) it.page = p.page_table[(size_t)pc.b * p.rows.max_pages + i];
         at_k += kConvertWarps;
         if (at_k >= 2 * kTilePages) {
           at_k -= 2 * kTilePages;
@@ -613,21 +607,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           }
         }
       } else {
-        it.valid = -1;  // there is none
+        it.valid = -1;
       }
       return it;
     };
     auto load = [&](const Item& it, int k, uint2 (&raw)[8], float2& scale) {
-      const uint8_t* src = (k < kTilePages ? p.k : p.v) + (size_t)max(it.block, 0) * kBlockBytesI8 +
-                           sub * kHeadDim + ch * 8;
+      int valid = it.valid;
+      if (valid > 0 && (it.page < 0 || it.page >= p.num_pages)) {
+        set_error(p.err, kDevErrCheck);
+        valid = 0;
+      }
+      const int block = valid > 0 ? it.page * p.hkv + it.h : 0;
+      const uint8_t* src =
+          (k < kTilePages ? p.k : p.v) + (size_t)block * kBlockBytesI8 + sub * kHeadDim + ch * 8;
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         raw[i] = make_uint2(0u, 0u);
-        if (2 * i + sub < it.valid) raw[i] = ldg64_nc(src + 2 * i * kHeadDim);
+        if (2 * i + sub < valid) raw[i] = ldg64_nc(src + 2 * i * kHeadDim);
       }
       scale = make_float2(0.0f, -1.0f);
-      if (k < kTilePages && it.valid > 0)
-        scale = make_float2(p.k_scale[it.block], p.v_scale[it.block]);
+      if (k < kTilePages && valid > 0) scale = make_float2(p.k_scale[block], p.v_scale[block]);
     };
     int step = 0, k = at_k;  // the converting side
     auto convert = [&](const uint2 (&raw)[8], const float2& scale) {
