@@ -37,12 +37,13 @@ constexpr int kTokens = 128;       // tokens of a step
 constexpr int kTilePages = kTokens / kPage;
 constexpr int kTileBytes = 128 * kHeadDim * 2;
 constexpr int kHalfBytes = kTileBytes / 2;  // 64 channels of 128 rows
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 12;  // warps 0-7; 12; the other 7 convert
-constexpr int kConvertWarps = 7;
-constexpr int kThreads = 512;
-// registers a thread of the softmax warpgroups and of the other two: 128 on average
-constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
-static_assert(2 * (kSoftmaxRegs + kOtherRegs) == 4 * 128, "the launch's registers");
+constexpr int kSoftmaxWarps = 8, kConvertWarps = 8;  // 0-7, 8-15
+constexpr int kMmaWarp = 16;
+constexpr int kThreads = 640;  // five warpgroups; the last is warp 16 and three idle ones
+// registers a thread of the softmax, conversion and product warpgroups: 96 on average
+constexpr int kSoftmaxRegs = 136, kConvertRegs = 80, kMmaRegs = 48;
+static_assert(2 * kSoftmaxRegs + 2 * kConvertRegs + kMmaRegs == 5 * 96, "the launch's registers");
+static_assert(kConvertWarps == kTilePages, "a warp converts one block of K and of V a step");
 constexpr int kPageRing = 4;
 constexpr float kHeadroom = 10.0f;
 constexpr float kLag = 4.0f;
@@ -72,7 +73,7 @@ struct Smem {
   alignas(1024) unsigned char q[2][kTileBytes];
   unsigned char k[2][kTileBytes];
   unsigned char v[2][kTileBytes];
-  float4 page[kPageRing][kTilePages];  // s_k, log2 s_v, 1 / s_v
+  float4 page[kPageRing][kTilePages];  // s_k, log2 s_v, 1 / s_v of a step's blocks
   alignas(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2],
       p_full[2], o_full[2];
   long long per;
@@ -396,28 +397,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         const float4* page = sm.page[step % kPageRing];
         const bool masked = !full_rows || base + kTokens - 1 > first_pos;
         const int limit = pos - base;  // columns up to it are seen
-        uint32_t s[4][32];
+        // ---- the row's maximum, 64 columns at a time
+        auto scores = [&](int c, uint32_t (&s)[2][32]) {
+          tc::load32(s_col + c * 64, s[0]);
+          tc::load32(s_col + c * 64 + 32, s[1]);
+          tc::wait_ld();
+          if (masked) {
 #pragma unroll
-        for (int c = 0; c < 4; c++) tc::load32(s_col + c * 32, s[c]);
-        tc::wait_ld();
-        if (masked) {
-#pragma unroll
-          for (int c = 0; c < 4; c++)
-#pragma unroll
-            for (int k = 0; k < 32; k++)
-              if (c * 32 + k > limit) s[c][k] = 0xFF800000u;
-        }
-        // ---- the row's maximum
+            for (int k = 0; k < 64; k++)
+              if (c * 64 + k > limit) s[k >> 5][k & 31] = 0xFF800000u;
+          }
+        };
         float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 2; c++) {
+          uint32_t s[2][32];
+          scores(c, s);
 #pragma unroll
-        for (int g = 0; g < kTilePages; g++) {
-          const uint32_t* v = &s[g >> 1][16 * (g & 1)];
-          float a = __uint_as_float(v[0]);
+          for (int g = 0; g < 4; g++) {
+            const uint32_t* v = &s[g >> 1][16 * (g & 1)];
+            float a = __uint_as_float(v[0]);
 #pragma unroll
-          for (int k = 1; k < 15; k += 2) a = max3(a, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-          a = fmaxf(a, __uint_as_float(v[15]));
-          const float4 pg = page[g];
-          top = fmaxf(top, fmaf(a, fmaxf(f * pg.x, kTiny), pg.y));
+            for (int k = 1; k < 15; k += 2)
+              a = max3(a, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+            a = fmaxf(a, __uint_as_float(v[15]));
+            const float4 pg = page[4 * c + g];
+            top = fmaxf(top, fmaf(a, fmaxf(f * pg.x, kTiny), pg.y));
+          }
         }
         // ---- the accumulator follows a maximum that has grown by more than kLag
         if (__any_sync(0xffffffffu, top > m + kLag)) {
@@ -439,18 +445,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         }
         const float ref = (m == -INFINITY ? 0.0f : m) - kHeadroom;
         // ---- P, over S
+#pragma unroll 1
+        for (int c = 0; c < 2; c++) {
+          uint32_t s[2][32], w[32];
+          scores(c, s);
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
-          uint32_t w[16];
-#pragma unroll
-          for (int g = 0; g < 2; g++) {
-            const float4 pg = page[2 * c + g];
+          for (int g = 0; g < 4; g++) {
+            const float4 pg = page[4 * c + g];
             const float mul = fmaxf(f * pg.x, kTiny), add = pg.y - ref;
             float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
-              float2 y = fma2(make_float2(__uint_as_float(s[c][16 * g + k]),
-                                          __uint_as_float(s[c][16 * g + k + 1])),
+              const uint32_t* v = &s[g >> 1][16 * (g & 1) + k];
+              float2 y = fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])),
                               make_float2(mul, mul), make_float2(add, add));
               y.x = ex2(y.x);
               y.y = ex2(y.y);
@@ -459,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
             }
             l = fmaf(sum.x + sum.y, pg.z, l);
           }
-          tc::store16(s_col + c * 16, w);
+          tc::store32(s_col + c * 32, w);
         }
         tc::wait_st();
         tc::fence_before();
@@ -569,115 +576,118 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       }
       tc::fence_before();
     }
-  } else {
-    tc::fewer_registers<kOtherRegs>();
-  }
-  if (warp > kSoftmaxWarps - 1 && warp != kMmaWarp) {
+  } else if (warp < kMmaWarp) {
+    tc::fewer_registers<kConvertRegs>();
     // ================================================= codes to fp16 tiles
-    // A step's 16 items, the 8 blocks of K and then of V, go to the warps in turn, across steps:
-    // warp c has items c, c + 7, c + 14, ... of all. Lane: 8 channels of tokens 2 i + lane / 16.
-    const int sub = lane >> 4, ch = lane & 15;
+    // Warp w turns block w of each tile, of K and of V. Lane: 8 channels of tokens 2 i +
+    // lane / 16. Pages and scales of 32 tiles ahead are fetched at once, one tile a lane, and
+    // the codes of the next step are under way while this one's are converted.
+    const int w = warp - kSoftmaxWarps, sub = lane >> 4, ch = lane & 15;
     uint32_t off[4];  // of token 2 i + sub, i < 4, in the block's part of the tile
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       const int t = 2 * i + sub;
-      off[i] = (ch >> 3) * kHalfBytes + t * 128 + (((ch & 7) ^ t) << 4);
+      off[i] = w * (kPage * 128) + (ch >> 3) * kHalfBytes + t * 128 + (((ch & 7) ^ t) << 4);
     }
-    struct Item {
-      int page, h;  // the page (looked at only when the codes are loaded: its own load takes
-                    // hundreds of cycles) and the kv head
-      int valid;    // its first tokens that exist; -1: there is no such item
+    struct Ahead {      // 32 tiles of a piece
+      int count;        // of them, in the piece (0: the end)
+      int block;        // this lane's tile: the block in the code arrays
+      int valid;        // its first tokens that exist
+      float sk, sv;
     };
-    // the locating side runs ahead of the converting side
     bool more = walk.next(pc);
-    int tile = 0, at_k = warp < kMmaWarp ? warp - kSoftmaxWarps : warp - kSoftmaxWarps - 1;
-    auto locate = [&]() {
-      Item it = {-1, 0, 0};
-      if (more) {
-        const int i = (pc.tile + tile) * kTilePages + (at_k & 7);
-        it.h = pc.h;
-        it.valid = min(max(len[pc.b] - i * kPage, 0), kPage);
-        if (it.valid > 0) it.page = p.page_table[(size_t)pc.b * p.rows.max_pages + i];
-        at_k += kConvertWarps;
-        if (at_k >= 2 * kTilePages) {
-          at_k -= 2 * kTilePages;
-          if (++tile == pc.tiles) {
-            tile = 0;
-            more = walk.next(pc);
+    int done = 0;  // tiles of the piece that were fetched
+    auto fetch = [&]() {
+      Ahead a = {0, 0, 0, 0.0f, -1.0f};
+      if (!more) return a;
+      a.count = min(pc.tiles - done, 32);
+      const int i = (pc.tile + done + lane) * kTilePages + w;
+      if (lane < a.count) {
+        a.valid = min(max(len[pc.b] - i * kPage, 0), kPage);
+        if (a.valid > 0) {
+          const int page = p.page_table[(size_t)pc.b * p.rows.max_pages + i];
+          if (page >= 0 && page < p.num_pages) {
+            a.block = page * p.hkv + pc.h;
+            a.sk = p.k_scale[a.block];
+            a.sv = p.v_scale[a.block];
+          } else {
+            set_error(p.err, kDevErrCheck);
+            a.valid = 0;
           }
         }
-      } else {
-        it.valid = -1;
       }
-      return it;
+      done += a.count;
+      if (done == pc.tiles) {
+        done = 0;
+        more = walk.next(pc);
+      }
+      return a;
     };
-    auto load = [&](const Item& it, int k, uint2 (&raw)[8], float2& scale) {
-      int valid = it.valid;
-      if (valid > 0 && (it.page < 0 || it.page >= p.num_pages)) {
-        set_error(p.err, kDevErrCheck);
-        valid = 0;
-      }
-      const int block = valid > 0 ? it.page * p.hkv + it.h : 0;
-      const uint8_t* src =
-          (k < kTilePages ? p.k : p.v) + (size_t)block * kBlockBytesI8 + sub * kHeadDim + ch * 8;
+    auto load = [&](const uint8_t* codes, const Ahead& a, int j, uint2 (&raw)[8]) {
+      const int valid = __shfl_sync(0xffffffffu, a.valid, j);
+      const uint8_t* src = codes +
+                           (size_t)__shfl_sync(0xffffffffu, a.block, j) * kBlockBytesI8 +
+                           sub * kHeadDim + ch * 8;
+      if (valid == kPage) {
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        raw[i] = make_uint2(0u, 0u);
-        if (2 * i + sub < valid) raw[i] = ldg64_nc(src + 2 * i * kHeadDim);
+        for (int i = 0; i < 8; i++) raw[i] = ldg64_nc(src + 2 * i * kHeadDim);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          raw[i] = make_uint2(0u, 0u);
+          if (2 * i + sub < valid) raw[i] = ldg64_nc(src + 2 * i * kHeadDim);
+        }
       }
-      scale = make_float2(0.0f, -1.0f);
-      if (k < kTilePages && valid > 0) scale = make_float2(p.k_scale[block], p.v_scale[block]);
     };
-    int step = 0, k = at_k;  // the converting side
-    auto convert = [&](const uint2 (&raw)[8], const float2& scale) {
-      const int st = step & 1, parity = ((step >> 1) & 1) ^ 1;
-      const bool is_k = k < kTilePages;
-      if (!wait(sm, is_k ? &sm.k_empty[st] : &sm.v_empty[st], parity, p.err)) return false;
-      unsigned char* dst = (is_k ? sm.k[st] : sm.v[st]) + (k & 7) * (kPage * 128);
+    auto put = [&](unsigned char* tile, const uint2 (&raw)[8]) {
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         const uint32_t x = Codes<F>::prepare(raw[i].x), y = Codes<F>::prepare(raw[i].y);
-        *reinterpret_cast<uint4*>(dst + off[i & 3] + (i >> 2) * 1024) =
+        *reinterpret_cast<uint4*>(tile + off[i & 3] + (i >> 2) * 1024) =
             make_uint4(Codes<F>::template pair<0>(x), Codes<F>::template pair<1>(x),
                        Codes<F>::template pair<0>(y), Codes<F>::template pair<1>(y));
       }
-      // s_k, log2 s_v, 1 / s_v. No tokens: p = 0. A block of zeros in V counts as 2^-100, below
-      // any other, so that it takes no part in the choice of M.
-      if (is_k && lane == 0)
-        sm.page[step % kPageRing][k] =
-            scale.y < 0.0f    ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
-            : scale.y == 0.0f ? make_float4(scale.x, -100.0f, 0x1p100f, 0.0f)
-                              : make_float4(scale.x, lg2(scale.y), 1.0f / scale.y, 0.0f);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(is_k ? &sm.k_full[st] : &sm.v_full[st]);
-      k += kConvertWarps;
-      if (k >= 2 * kTilePages) {
-        k -= 2 * kTilePages;
-        step++;
-      }
-      return true;
     };
-    // two items of codes under way, the place of a third known
-    auto after = [](int k) {  // the item kConvertWarps on
-      return k + kConvertWarps >= 2 * kTilePages ? k + kConvertWarps - 2 * kTilePages
-                                                 : k + kConvertWarps;
-    };
-    uint2 ra[8], rb[8];
-    float2 sa, sb;
-    Item ia = locate(), ib = locate(), ic = locate();
-    load(ia, k, ra, sa);
-    load(ib, after(k), rb, sb);
-    while (ia.valid >= 0) {
-      if (!convert(ra, sa)) break;
-      ia = ic;
-      load(ia, after(k), ra, sa);
-      ic = locate();
-      if (ib.valid < 0 || !convert(rb, sb)) break;
-      ib = ic;
-      load(ib, after(k), rb, sb);
-      ic = locate();
+    Ahead cur = fetch(), next = fetch();
+    uint2 rk[8], rv[8];
+    if (cur.count > 0) {
+      load(p.k, cur, 0, rk);
+      load(p.v, cur, 0, rv);
     }
+    int step = 0;
+    bool ok = true;
+    while (ok && cur.count > 0) {
+      for (int j = 0; j < cur.count; j++, step++) {
+        const int st = step & 1, parity = ((step >> 1) & 1) ^ 1;
+        const bool turn = j + 1 == cur.count;  // the next step is the next 32's first
+        const bool another = !turn || next.count > 0;
+        const int nj = turn ? 0 : j + 1;
+        ok = wait(sm, &sm.k_empty[st], parity, p.err);
+        if (!ok) break;
+        const float sk = __shfl_sync(0xffffffffu, cur.sk, j);
+        const float sv = __shfl_sync(0xffffffffu, cur.sv, j);
+        // s_k, log2 s_v, 1 / s_v. No tokens: p = 0. A block of zeros in V counts as 2^-100,
+        // below any other, so that it takes no part in the choice of M.
+        if (lane == 0)
+          sm.page[step % kPageRing][w] = sv < 0.0f    ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
+                                         : sv == 0.0f ? make_float4(sk, -100.0f, 0x1p100f, 0.0f)
+                                                      : make_float4(sk, lg2(sv), 1.0f / sv, 0.0f);
+        put(sm.k[st], rk);
+        if (lane == 0) mbar_arrive(&sm.k_full[st]);
+        if (another) load(p.k, turn ? next : cur, nj, rk);
+        ok = wait(sm, &sm.v_empty[st], parity, p.err);
+        if (!ok) break;
+        put(sm.v[st], rv);
+        if (lane == 0) mbar_arrive(&sm.v_full[st]);
+        if (another) load(p.v, turn ? next : cur, nj, rv);
+      }
+      cur = next;
+      next = fetch();
+    }
+  } else {
+    tc::fewer_registers<kMmaRegs>();
   }
   if (warp == kMmaWarp) {
     // ================================================= the products
