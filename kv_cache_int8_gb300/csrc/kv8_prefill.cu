@@ -47,7 +47,7 @@ static_assert(kConvertWarps == kTilePages, "a warp converts one block of K and o
 constexpr int kPageRing = 4;
 constexpr float kHeadroom = 10.0f;
 constexpr float kLag = 4.0f;
-constexpr float kTiny = 1e-37f;  // scales of scores stay positive: a masked -inf stays one
+constexpr float kTiny = 1e-37f;  // scales of scores are at least that: a masked -inf stays one
 constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns; tile i at + 128 i
 
 struct Params {
@@ -73,9 +73,10 @@ struct Smem {
   alignas(1024) unsigned char q[2][kTileBytes];
   unsigned char k[2][kTileBytes];
   unsigned char v[2][kTileBytes];
-  float4 page[kPageRing][kTilePages];  // s_k, log2 s_v, 1 / s_v of a step's blocks
+  // log2 s_v, 1 / s_v, s_k of a step's blocks (x and y are read alone, as an aligned pair)
+  float4 page[kPageRing][kTilePages];
   alignas(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2],
-      p_full[2], o_full[2];
+      p_full[2][2], o_full[2];  // p_full[tile][half of the step's tokens]
   long long per;
   int start_b, start_h, start_q, start_tile;
   uint32_t tmem;
@@ -219,7 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       mbar_init(&sm.v_full[i], kTilePages);
       mbar_init(&sm.v_empty[i], 1);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 128);
+      mbar_init(&sm.p_full[i][0], 128);
+      mbar_init(&sm.p_full[i][1], 128);
       mbar_init(&sm.o_full[i], 1);
     }
     sm.dead = 0;
@@ -416,13 +418,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
 #pragma unroll
           for (int g = 0; g < 4; g++) {
             const uint32_t* v = &s[g >> 1][16 * (g & 1)];
-            float a = __uint_as_float(v[0]);
+            float a = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+            float b = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
 #pragma unroll
-            for (int k = 1; k < 15; k += 2)
+            for (int k = 6; k < 14; k += 4) {
               a = max3(a, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-            a = fmaxf(a, __uint_as_float(v[15]));
+              b = max3(b, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+            }
+            a = max3(a, __uint_as_float(v[14]), __uint_as_float(v[15]));
             const float4 pg = page[4 * c + g];
-            top = fmaxf(top, fmaf(a, fmaxf(f * pg.x, kTiny), pg.y));
+            top = fmaxf(top, fmaf(fmaxf(a, b), fmaxf(f * pg.z, kTiny), pg.x));
           }
         }
         // ---- the accumulator follows a maximum that has grown by more than kLag
@@ -444,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           }
         }
         const float ref = (m == -INFINITY ? 0.0f : m) - kHeadroom;
-        // ---- P, over S
+        // ---- P, over S: the products with V begin after the first half
 #pragma unroll 1
         for (int c = 0; c < 2; c++) {
           uint32_t s[2][32], w[32];
@@ -452,25 +457,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
 #pragma unroll
           for (int g = 0; g < 4; g++) {
             const float4 pg = page[4 * c + g];
-            const float mul = fmaxf(f * pg.x, kTiny), add = pg.y - ref;
+            const float add = pg.x - ref, mul = fmaxf(f * pg.z, kTiny);
+            const float2 mul2 = make_float2(mul, mul);
             float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
               const uint32_t* v = &s[g >> 1][16 * (g & 1) + k];
-              float2 y = fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])),
-                              make_float2(mul, mul), make_float2(add, add));
+              float2 y = fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), mul2,
+                              make_float2(add, add));
               y.x = ex2(y.x);
               y.y = ex2(y.y);
               sum = k == 0 ? y : add2(sum, y);
               w[8 * g + k / 2] = half_pair(y.x, y.y);
             }
-            l = fmaf(sum.x + sum.y, pg.z, l);
+            l = fmaf(sum.x + sum.y, pg.y, l);
           }
           tc::store32(s_col + c * 32, w);
+          tc::wait_st();
+          tc::fence_before();
+          mbar_arrive(&sm.p_full[tile][c]);
         }
-        tc::wait_st();
-        tc::fence_before();
-        mbar_arrive(&sm.p_full[tile]);
       }
       // ---- the result
       if (!wait(sm, &sm.o_full[tile], o_phase, p.err)) break;
@@ -668,12 +674,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         if (!ok) break;
         const float sk = __shfl_sync(0xffffffffu, cur.sk, j);
         const float sv = __shfl_sync(0xffffffffu, cur.sv, j);
-        // s_k, log2 s_v, 1 / s_v. No tokens: p = 0. A block of zeros in V counts as 2^-100,
-        // below any other, so that it takes no part in the choice of M.
+        // No tokens: p = 0. A block of zeros in V counts as 2^-100, below any other, so that it
+        // takes no part in the choice of M.
         if (lane == 0)
-          sm.page[step % kPageRing][w] = sv < 0.0f    ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
-                                         : sv == 0.0f ? make_float4(sk, -100.0f, 0x1p100f, 0.0f)
-                                                      : make_float4(sk, lg2(sv), 1.0f / sv, 0.0f);
+          sm.page[step % kPageRing][w] = sv < 0.0f    ? make_float4(-INFINITY, 0.0f, sk, 0.0f)
+                                         : sv == 0.0f ? make_float4(-100.0f, 0x1p100f, sk, 0.0f)
+                                                      : make_float4(lg2(sv), 1.0f / sv, sk, 0.0f);
         put(sm.k[st], rk);
         if (lane == 0) mbar_arrive(&sm.k_full[st]);
         if (another) load(p.k, turn ? next : cur, nj, rk);
@@ -712,15 +718,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         tc::commit(&sm.s_full[i]);
       }
     };
-    // O of tile i += P V of step `at`
-    auto values = [&](int i, int at, bool add, bool last) {
+    // O of tile i += P V of half h of step `at`
+    auto values = [&](int i, int h, int at, bool add) {
       if (lead) {
         const uint32_t v = v_low + (at & 1) * (kTileBytes >> 4);
 #pragma unroll
-        for (int c = 0; c < 8; c++)
+        for (int c = 4 * h; c < 4 * h + 4; c++)
           tc::mma_ts<kPv>(tmem + kColO + 128 * i, tmem + kColS + 128 * i + c * 8,
                           v + c * (2048 >> 4), add || c > 0);
-        if (last) tc::commit(&sm.o_full[i]);
       }
     };
     while (ok && walk.next(pc)) {
@@ -744,12 +749,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
 #pragma unroll
         for (int i = 0; i < 2; i++) {
           if (!ok || (i == 1 && !two)) continue;
-          ok = wait(sm, &sm.p_full[i], p_phase[i], p.err);
+          ok = wait(sm, &sm.p_full[i][0], p_phase[i], p.err);
+          if (!ok) continue;
+          tc::fence_after();
+          values(i, 0, step, j > 0);
+          ok = wait(sm, &sm.p_full[i][1], p_phase[i], p.err);
           if (!ok) continue;
           p_phase[i] ^= 1;
           tc::fence_after();
-          values(i, step, j > 0, !more);
+          values(i, 1, step, true);
           if (more) scores(i, step + 1);
+          else if (lead) tc::commit(&sm.o_full[i]);
         }
         if (ok && lead) {
           tc::commit(&sm.v_empty[step & 1]);
