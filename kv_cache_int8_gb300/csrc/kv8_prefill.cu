@@ -25,6 +25,7 @@
 #include "kv8.cuh"
 #include "tcgen05.cuh"
 
+#include <climits>
 #include <cmath>
 
 namespace hsa {
@@ -122,10 +123,30 @@ __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+__device__ __forceinline__ uint32_t bf16_max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
+}
+// 64 bytes of an output row, one thread a row: stores of 32 bytes fill whole sectors.
+__device__ __forceinline__ void store_row_part(__nv_bfloat16* dst, const uint32_t (&w)[16]) {
+  if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+#pragma unroll
+    for (int k = 0; k < 16; k += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 2 * k),
+                   "r"(w[k]), "r"(w[k + 1]), "r"(w[k + 2]), "r"(w[k + 3]), "r"(w[k + 4]),
+                   "r"(w[k + 5]), "r"(w[k + 6]), "r"(w[k + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; k += 4)
+      *reinterpret_cast<uint4*>(dst + 2 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+  }
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -352,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       const bool real = row < pc.rows;
       const int token = pc.q * p.block_tokens + row / p.group;  // among the new tokens
       const int head = pc.h * p.group + row % p.group;
-      const int pos = real ? len[pc.b] - num[pc.b] + token : -1;
+      // its position; rows that do not exist (zeros) see everything and are not stored
+      const int pos = real ? len[pc.b] - num[pc.b] + token : INT_MAX;
       const size_t out_row = (size_t)(row0[pc.b] + token) * p.hq + head;
       float f;
       {
@@ -366,8 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         }
 #pragma unroll
         for (int c = 0; c < 16; c++) {
-          mx = __vmaxu2(mx, __vmaxu2(raw[c].x & 0x7FFF7FFFu, raw[c].y & 0x7FFF7FFFu));
-          mx = __vmaxu2(mx, __vmaxu2(raw[c].z & 0x7FFF7FFFu, raw[c].w & 0x7FFF7FFFu));
+          mx = bf16_max2(mx, bf16_max2(raw[c].x & 0x7FFF7FFFu, raw[c].y & 0x7FFF7FFFu));
+          mx = bf16_max2(mx, bf16_max2(raw[c].z & 0x7FFF7FFFu, raw[c].w & 0x7FFF7FFFu));
         }
         const uint32_t m16 = max(mx & 0xFFFFu, mx >> 16);
         const int e = m16 >> 7;
@@ -389,7 +411,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       // the first position of this tile's rows: tiles of tokens up to it need no mask
       const int first_pos = len[pc.b] - num[pc.b] + pc.q * p.block_tokens +
                             tile * 128 / p.group;
-      const bool full_rows = pc.rows >= (tile + 1) * 128;
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < pc.tiles; j++, step++) {
         const int base = (pc.tile + j) * kTokens;
@@ -397,14 +418,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         s_phase ^= 1;
         tc::fence_after();
         const float4* page = sm.page[step % kPageRing];
-        const bool masked = !full_rows || base + kTokens - 1 > first_pos;
         const int limit = pos - base;  // columns up to it are seen
         // ---- the row's maximum, 64 columns at a time
         auto scores = [&](int c, uint32_t (&s)[2][32]) {
           tc::load32(s_col + c * 64, s[0]);
           tc::load32(s_col + c * 64 + 32, s[1]);
           tc::wait_ld();
-          if (masked) {
+          if (base + c * 64 + 63 > first_pos) {
 #pragma unroll
             for (int k = 0; k < 64; k++)
               if (c * 64 + k > limit) s[k >> 5][k & 31] = 0xFF800000u;
@@ -491,16 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           tc::load32(o_col + c * 32, o);
           tc::wait_ld();
           if (real) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * kHeadDim + c * 32);
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; i++)
-                w[i] = bf16_pair(__uint_as_float(o[8 * k + 2 * i]) * inv,
-                                 __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
-              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int i = 0; i < 16; i++)
+              w[i] = bf16_pair(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+            store_row_part(p.out + out_row * kHeadDim + c * 32, w);
           }
         }
         if (real && p.lse != nullptr)
@@ -552,29 +567,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
             float4 acc[8];
 #pragma unroll
             for (int k = 0; k < 8; k++) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int c = 0; c < parts; c++) {
-              const size_t sl = slot_of(c);
-              const float w = ex2(__ldcg(pml + sl * kRows + row).x - ref) * inv;
-              const float4* src = reinterpret_cast<const float4*>(p.part_o) +
-                                  (sl * 32 + c4 * 8) * kRows + row;
-              float4 v[8];
-#pragma unroll
-              for (int k = 0; k < 8; k++) v[k] = __ldcg(src + k * kRows);
+            const float4* src =
+                reinterpret_cast<const float4*>(p.part_o) + c4 * 8 * kRows + row;
+            for (int c = 0; c < parts; c += 2) {  // two parts' loads under way at once
+              const bool two = c + 1 < parts;
+              const size_t s0 = slot_of(c), s1 = two ? slot_of(c + 1) : s0;
+              float4 v[2][8];
+              const float m0 = __ldcg(pml + s0 * kRows + row).x;
+              const float m1 = __ldcg(pml + s1 * kRows + row).x;
 #pragma unroll
               for (int k = 0; k < 8; k++) {
-                acc[k].x += w * v[k].x;
-                acc[k].y += w * v[k].y;
-                acc[k].z += w * v[k].z;
-                acc[k].w += w * v[k].w;
+                v[0][k] = __ldcg(src + (s0 * 32 + k) * kRows);
+                v[1][k] = __ldcg(src + (s1 * 32 + k) * kRows);
               }
-            }
-            uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * kHeadDim + c4 * 32);
+              const float w[2] = {ex2(m0 - ref) * inv, two ? ex2(m1 - ref) * inv : 0.0f};
 #pragma unroll
-            for (int k = 0; k < 4; k++)
-              dst[k] = make_uint4(bf16_pair(acc[2 * k].x, acc[2 * k].y),
-                                  bf16_pair(acc[2 * k].z, acc[2 * k].w),
-                                  bf16_pair(acc[2 * k + 1].x, acc[2 * k + 1].y),
-                                  bf16_pair(acc[2 * k + 1].z, acc[2 * k + 1].w));
+              for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                  acc[k].x += w[h] * v[h][k].x;
+                  acc[k].y += w[h] * v[h][k].y;
+                  acc[k].z += w[h] * v[h][k].z;
+                  acc[k].w += w[h] * v[h][k].w;
+                }
+            }
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+              w[2 * k] = bf16_pair(acc[k].x, acc[k].y);
+              w[2 * k + 1] = bf16_pair(acc[k].z, acc[k].w);
+            }
+            store_row_part(p.out + out_row * kHeadDim + c4 * 32, w);
           }
           if (p.lse != nullptr)
             p.lse[out_row] = (top - kHeadroom + log2f(sum)) * 0.693147180559945309f;
