@@ -46,6 +46,7 @@ constexpr int kSoftmaxRegs = 136, kConvertRegs = 80, kMmaRegs = 48;
 static_assert(2 * kSoftmaxRegs + 2 * kConvertRegs + kMmaRegs == 5 * 96, "the launch's registers");
 static_assert(kConvertWarps == kTilePages, "a warp converts one block of K and of V a step");
 constexpr int kPageRing = 4;
+constexpr int kBlockCost = 4;  // what a row block costs beside its tiles, in tiles (see Walk)
 constexpr float kHeadroom = 10.0f;
 constexpr float kLag = 4.0f;
 constexpr float kTiny = 1e-37f;  // scales of scores are at least that: a masked -inf stays one
@@ -79,7 +80,7 @@ struct Smem {
   alignas(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2],
       p_full[2][2], o_full[2];  // p_full[tile][half of the step's tokens]
   long long per;
-  int start_b, start_h, start_q, start_tile;
+  int start_b, start_h, start_q, start_off;
   uint32_t tmem;
   int last[2];
   int dead;
@@ -183,41 +184,49 @@ __device__ __forceinline__ int block_tiles(int len, int n, int block_tokens, int
 
 // A stretch of one row block's tiles: what a CTA does at a time.
 struct Piece {
-  int b, h, q;      // sequence, kv head, row block
-  int tile, tiles;  // first tile, number of tiles
-  int all_tiles;    // of the whole row block
-  int rows;         // rows of the block that exist
+  int b, h, q;       // sequence, kv head, row block
+  int tile, tiles;   // first tile, number of tiles
+  int all_tiles;     // of the whole row block
+  int rows;          // rows of the block that exist
+  long long begin;   // the row block's first place on the line
 };
 
-// The pieces of the slice [x, end), in order.
+// The pieces of the slice [x, end) of the line, in order. A row block's places are kBlockCost
+// for what it costs beside its tiles (queries in, results out), then
+// one a tile. Without the first, the CTAs with a head's first, short row blocks would take half
+// as long again as the others (8K prompt: 624 us without, 472 with 4, 479 with 6).
 struct Walk {
   const Seqs s;
   int batch, hkv, group, block_tokens;
   long long x, end;
-  int b, h, q, tile;
+  int b, h, q, off;  // off: place in the row block
 
   __device__ __forceinline__ bool next(Piece& p) {
-    if (x >= end) return false;
-    p.b = b;
-    p.h = h;
-    p.q = q;
-    p.tile = tile;
-    p.all_tiles = block_tiles(s.len[b], s.n[b], block_tokens, q);
-    p.tiles = (int)min((long long)(p.all_tiles - tile), end - x);
-    p.rows = min(block_tokens, s.n[b] - q * block_tokens) * group;
-    x += p.tiles;
-    tile = 0;
-    if ((q + 1) * block_tokens < s.n[b]) {
-      q++;
-    } else {
-      q = 0;
-      if (++h == hkv) {
-        h = 0;
-        do b++;
-        while (b < batch && s.n[b] == 0);
+    for (;;) {
+      if (x >= end) return false;
+      p.b = b;
+      p.h = h;
+      p.q = q;
+      p.begin = x - off;
+      p.all_tiles = block_tiles(s.len[b], s.n[b], block_tokens, q);
+      p.rows = min(block_tokens, s.n[b] - q * block_tokens) * group;
+      const int stop = (int)min((long long)(p.all_tiles + kBlockCost), off + (end - x));
+      p.tile = max(off - kBlockCost, 0);
+      p.tiles = max(stop - kBlockCost, 0) - p.tile;
+      x += stop - off;
+      off = 0;
+      if ((q + 1) * block_tokens < s.n[b]) {
+        q++;
+      } else {
+        q = 0;
+        if (++h == hkv) {
+          h = 0;
+          do b++;
+          while (b < batch && s.n[b] == 0);
+        }
       }
+      if (p.tiles > 0) return true;
     }
-    return true;
   }
 };
 
@@ -258,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     for (int b0 = 0; b0 < batch; b0 += 32) {
       const int b = b0 + lane;
       NewSpan sp = {0, 0, 0, false};
-      int blocks = 0, tiles = 0;
+      int blocks = 0, tiles = 0;  // tiles: places of the sequence's row blocks under one head
       if (b < batch) {
         sp = new_span(p.rows, b);
         if (sp.bad) set_error(p.err, kDevErrCheck);
@@ -268,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         blocks = (sp.n + p.block_tokens - 1) / p.block_tokens;
         if (blocks <= 8)
           for (int q = 0; q < blocks; q++)
-            tiles += block_tiles(sp.start + sp.n, sp.n, p.block_tokens, q);
+            tiles += block_tiles(sp.start + sp.n, sp.n, p.block_tokens, q) + kBlockCost;
       }
       // sequences of many row blocks: the warp together
       for (unsigned many = __ballot_sync(0xffffffffu, blocks > 8); many != 0; many &= many - 1) {
@@ -277,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         const int l = __shfl_sync(0xffffffffu, sp.start, from) + n;
         const int bl = __shfl_sync(0xffffffffu, blocks, from);
         int t = 0;
-        for (int q = lane; q < bl; q += 32) t += block_tiles(l, n, p.block_tokens, q);
+        for (int q = lane; q < bl; q += 32)
+          t += block_tiles(l, n, p.block_tokens, q) + kBlockCost;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
         if (lane == from) tiles = t;
@@ -310,9 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       unsigned rem = (unsigned)(at - (long long)h * tiles);
       const int blocks = (num[b] + p.block_tokens - 1) / p.block_tokens;
       int q0 = 0;
-      for (;; q0 += 32) {  // the block whose tiles hold place `rem`
+      for (;; q0 += 32) {  // the block that holds place `rem`
         const int q = q0 + lane;
-        const unsigned t = q < blocks ? block_tiles(len[b], num[b], p.block_tokens, q) : 0;
+        const unsigned t =
+            q < blocks ? block_tiles(len[b], num[b], p.block_tokens, q) + kBlockCost : 0;
         unsigned incl = t;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -325,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
             sm.start_b = b;
             sm.start_h = h;
             sm.start_q = q;
-            sm.start_tile = (int)(rem - (incl - t));
+            sm.start_off = (int)(rem - (incl - t));
           }
           break;
         }
@@ -341,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
   const long long per = sm.per, all = pre[batch];
   const long long begin = min(blockIdx.x * per, all), end = min(begin + per, all);
   Walk walk = {{pre, len, num, row0}, batch, p.hkv, p.group, p.block_tokens, begin, end,
-               sm.start_b, sm.start_h, sm.start_q, sm.start_tile};
+               sm.start_b, sm.start_h, sm.start_q, sm.start_off};
   Piece pc;
 
   if (warp < kSoftmaxWarps) {
@@ -522,10 +533,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           p.lse[out_row] = (m - kHeadroom + log2f(l)) * 0.693147180559945309f;
       } else {
         // a part: to the workspace; the last of the block's CTAs to arrive joins them
-        const long long piece_end = walk.x, block_begin = piece_end - pc.tiles - pc.tile;
-        const int c0 = (int)(block_begin / per);
-        const int parts = (int)((block_begin + pc.all_tiles - 1) / per) - c0 + 1;
-        const size_t slot = 2 * (size_t)blockIdx.x + (begin < block_begin ? 1 : 0);
+        const long long tiles_begin = pc.begin + kBlockCost;
+        const int c0 = (int)(tiles_begin / per);
+        const int parts = (int)((tiles_begin + pc.all_tiles - 1) / per) - c0 + 1;
+        const size_t slot = 2 * (size_t)blockIdx.x + (begin < pc.begin ? 1 : 0);
         float4* po = reinterpret_cast<float4*>(p.part_o) + slot * 32 * kRows + row;
 #pragma unroll 1
         for (int c = 0; c < 4; c++) {
@@ -551,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         }
         named_sync(1 + tile, 128);
         if (sm.last[tile] && real) {
-          const size_t first = 2 * (size_t)c0 + (c0 * per < block_begin ? 1 : 0);
+          const size_t first = 2 * (size_t)c0 + (c0 * per < pc.begin ? 1 : 0);
           auto slot_of = [&](int c) { return c == 0 ? first : 2 * (size_t)(c0 + c); };
           float top = -INFINITY, sum = 0.0f;
           for (int c = 0; c < parts; c++)
