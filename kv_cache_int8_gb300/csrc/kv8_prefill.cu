@@ -362,7 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
     const uint32_t s_col = at + kColS + 128 * tile, o_col = at + kColO + 128 * tile;
     uint32_t s_phase = 0, o_phase = 0;
-    int step = 0;  // steps of all pieces so far (the page table ring)
+    int step = 0;  // steps of all pieces so far (the ring of scales)
+    // After a wait that ran out a warp goes on through the pieces without work: the barriers of
+    // a tile's four warps must find all of them.
+    bool failed = false;
     // rows of sequences that do not fit: 0 and -inf
     for (int b = blockIdx.x; b < batch; b += gridDim.x) {
       if (p.rows.cu == nullptr ? num[b] != 0 : p.rows.cu[b + 1] - p.rows.cu[b] == num[b]) continue;
@@ -423,9 +426,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       const int first_pos = len[pc.b] - num[pc.b] + pc.q * p.block_tokens +
                             tile * 128 / p.group;
       float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < pc.tiles; j++, step++) {
+      for (int j = 0; !failed && j < pc.tiles; j++, step++) {
         const int base = (pc.tile + j) * kTokens;
-        if (!wait(sm, &sm.s_full[tile], s_phase, p.err)) break;
+        if (!wait(sm, &sm.s_full[tile], s_phase, p.err)) {
+          failed = true;
+          break;
+        }
         s_phase ^= 1;
         tc::fence_after();
         const float4* page = sm.page[step % kPageRing];
@@ -510,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         }
       }
       // ---- the result
-      if (!wait(sm, &sm.o_full[tile], o_phase, p.err)) break;
+      if (!wait(sm, &sm.o_full[tile], o_phase, p.err)) failed = true;
       o_phase ^= 1;
       tc::fence_after();
       const bool whole = pc.tiles == pc.all_tiles;
