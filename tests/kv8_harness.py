@@ -100,4 +100,4 @@ def assert_rows(got, lse, want, want_lse, tol, rounding=0.0):
         lse = np.asarray(lse, dtype=np.float64)
         none = np.isneginf(want_lse)
         assert (np.isneginf(lse) == none).all()
-        assert (np.abs(lse - want_lse)[~none] <= tol["lse"][~none]).all()
+        assert (np.abs(lse[~none] - want_lse[~none]) <= tol["lse"][~none]).all()

@@ -333,7 +333,8 @@ def check_prefill(s, q, new, out, lse, sm_scale=D ** -0.5):
                 # probabilities are rounded to fp16 before the product with V (half a step
                 # 2^-11 of each, so that much of the largest value), the result to bf16
                 tol["out"] = tol["out"] + 2.0 ** -11 * np.abs(v).max()
-                assert_rows(out[at:at + m, j], lse[at:at + m, j], want, wl, tol, 2.0 ** -8)
+                assert_rows(out[at:at + m, j], None if lse is None else lse[at:at + m, j], want, wl,
+                            tol, 2.0 ** -8)
         at += m
 
 
@@ -349,3 +350,265 @@ def test_prefill(fmt, hq, hkv, lens, new):
     q = bf16(s.rng.standard_normal((sum(new), hq, D)))
     out, lse = run_prefill(s, q, new)
     check_prefill(s, q, new, out, lse)
+
+
+def test_prefill_of_strided_queries_leaves_other_rows_alone():
+    """Queries as slices of a fused projection, rows behind the last sequence, no lse; the same
+    bits again on another stream and from a replayed graph."""
+    hq, hkv, new = 8, 2, [70, 0, 33]
+    s = Batch([600, 20, 33], hq, hkv, "int8", seed=11)
+    T = sum(new)
+    q = bf16(s.rng.standard_normal((T, hq, D)))
+    fused = torch.full((T + 9, hq + 2 * hkv, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    fused[:T, :hq] = to_bf16(q)
+    d, cache = s.dims(), s.gpu_cache()
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_PREFILL)
+    outs = [torch.full((T + 9, hq, D), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    args = (d, cache, fused[:, :hq], cu_of(new), s.gpu_table(), s.gpu_lens())
+    hsa.hsa_kv8_prefill(*args, outs[0], None, ws)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        hsa.hsa_kv8_prefill(*args, outs[1], None, ws)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hsa.hsa_kv8_prefill(*args, outs[2], None, ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert hsa.hsa_read_device_error(ws) == 0
+    for o in outs:
+        assert torch.equal(o, outs[0]) and (o[T:] == 5.0).all()
+    check_prefill(s, q, new, outs[0][:T].float().cpu().numpy(), None)
+
+
+def test_prefill_without_offsets_is_a_decode():
+    s = Batch([300, 17, 1], 4, 2, "e4m3", seed=12)
+    q = bf16(s.rng.standard_normal((3, 4, D)))
+    d = s.dims()
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_PREFILL)
+    out = torch.empty(3, 4, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(3, 4, device="cuda")
+    hsa.hsa_kv8_prefill(d, s.gpu_cache(), to_bf16(q), None, s.gpu_table(), s.gpu_lens(), out, lse,
+                        ws)
+    check_prefill(s, q, [1, 1, 1], out.float().cpu().numpy(), lse.cpu().numpy())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_over_blocks_of_zeros_and_of_unlike_scales(fmt):
+    """V blocks of zeros count in the sums, K blocks of zeros give equal logits; scales of V
+    that differ by 2^60 between blocks, queries by 2^60 between heads."""
+    s = Batch([16 * 40 + 5], 4, 1, fmt, seed=13, fill=False)
+    n = s.lens[0]
+    k, v = s.rows(n), s.rows(n)
+    block = np.arange(n) // PAGE
+    v[block % 3 == 0] = 0
+    v[block % 3 == 1] *= np.float32(2.0 ** -60)
+    k[block % 4 == 1] = 0
+    k[block == 40] = 0
+    O.write(s.cache, k, v, s.table[0], 0)
+    q = bf16(s.rng.standard_normal((8, 4, D)))
+    q[:, 1] *= np.float32(2.0 ** -40)
+    q[:, 2] *= np.float32(2.0 ** 20)  # one token takes all
+    q[:, 3] = 0
+    kk, vv = (O.values(s.cache, w, s.table[0], n, 0) for w in "kv")
+    out, lse = run_decode(s, q[:1])
+    want, wl, tol = O.attend(q[0], kk, vv, np.ones((4, n), bool), D ** -0.5)
+    ok = [0, 1, 3]  # at 2^20 the logits themselves are only known to a few units
+    assert_rows(out[0][ok], lse[0][ok], want[ok], wl[ok], {m: t[ok] for m, t in tol.items()})
+    assert np.isfinite(out).all()
+    out, lse = run_prefill(s, q, [8])
+    for j in ok:
+        seen = np.arange(n)[None] <= (n - 8 + np.arange(8))[:, None]
+        want, wl, tol = O.attend(q[:, j], kk, vv, seen, D ** -0.5)
+        tol["out"] = tol["out"] + 2.0 ** -11 * np.abs(vv).max()
+        assert_rows(out[:, j], lse[:, j], want, wl, tol, 2.0 ** -8)
+
+
+def test_long_decode_keeps_its_digits():
+    """2M tokens of one row: 54 blocks add up in each of 152 x 16 warps. 2-norm error against 64
+    bits below 1e-6: 54 + 16 + 152 roundings of at most 2^-24 of a running sum, as random ones
+    sqrt(222) * 2^-24 = 9e-7 where the running sum is already the result."""
+    n, hkv = 1 << 21, 1
+    d = hsa.Dims(batch=1, hq=4, hkv=hkv, max_pages_per_seq=n // 16, num_pages=n // 16, k2=0)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = [torch.randn(n, hkv, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    for fp8 in (False, True):
+        cache = hsa.KV8.zeros(d, fp8)
+        table = torch.randperm(n // 16, generator=g, device="cuda").to(torch.int32)[None]
+        lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+        cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        hsa.hsa_kv8_write(d, cache, x[0], x[1], cu, table, lens)
+        q = torch.randn(1, 4, D, generator=g, device="cuda").to(torch.bfloat16)
+        out, lse = torch.empty(1, 4, D, device="cuda"), torch.empty(1, 4, device="cuda")
+        hsa.hsa_kv8_decode(d, cache, q, table, lens, out, lse,
+                           hsa.workspace(d, hsa.HSA_OP_KV8_DECODE))
+        val = [(c.view(torch.int8)[table[0].long()].view(c.dtype).float().double() *
+                sc[table[0].long()].double()[..., None, None]).view(n, D)
+               for c, sc in ((cache.k, cache.k_scale), (cache.v, cache.v_scale))]
+        logit = q[0].double() @ val[0].T * D ** -0.5
+        want = torch.softmax(logit, -1) @ val[1]
+        assert float((out[0].double() - want).norm() / want.norm()) < 1e-6
+        assert float((lse[0].double() - torch.logsumexp(logit, -1)).abs().max()) < 2e-6
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_serving_loop(fmt):
+    """Prompts written and attended, then tokens appended one by one with dense and kept
+    attention, a drafted stretch verified and taken back: all four operators on one cache."""
+    hq, hkv = 8, 2
+    g = hq // hkv
+    prompt = [150, 33, 64]
+    s = Batch([n + 24 for n in prompt], hq, hkv, fmt, seed=21, fill=False)
+    d = s.dims(sink=16, window=20, k2=3)
+    cache, table = s.gpu_cache(), s.gpu_table()
+    wd = hsa.workspace(d, hsa.HSA_OP_KV8_DECODE)
+    wp = hsa.workspace(d, hsa.HSA_OP_KV8_PREFILL)
+
+    def values(b, n, h):
+        return [O.values(s.cache, w, s.table[b], n, h) for w in "kv"]
+
+    def extend(lens, new):  # writes and attends `new` tokens up to `lens`
+        T = sum(new)
+        qkv = bf16(s.rng.standard_normal((T, hq + 2 * hkv, D)))
+        dev = to_bf16(qkv)
+        k, v = dev[:, hq:hq + hkv], dev[:, hq + hkv:]
+        dl = s.gpu_lens(lens)
+        hsa.hsa_kv8_write(d, cache, k, v, cu_of(new), table, dl)
+        out = torch.empty(T, hq, D, dtype=torch.bfloat16, device="cuda")
+        hsa.hsa_kv8_prefill(d, cache, dev[:, :hq], cu_of(new), table, dl, out, None, wp)
+        at = 0
+        for b, (n, m) in enumerate(zip(lens, new)):
+            O.write(s.cache, qkv[at:at + m, hq:hq + hkv], qkv[at:at + m, hq + hkv:], s.table[b],
+                    n - m)
+            for h in range(hkv):
+                kk, vv = values(b, n, h)
+                seen = np.arange(n)[None] <= (n - m + np.arange(m))[:, None]
+                for j in range(h * g, h * g + g):
+                    want, _, tol = O.attend(qkv[at:at + m, j], kk, vv, seen, D ** -0.5)
+                    tol["out"] = tol["out"] + 2.0 ** -11 * np.abs(vv).max()
+                    assert_rows(out[at:at + m, j].float().cpu(), None, want, None, tol, 2.0 ** -8)
+            at += m
+
+    extend(prompt, prompt)
+    lens = list(prompt)
+    for step in range(5):
+        lens = [n + 1 for n in lens]
+        qkv = bf16(s.rng.standard_normal((3, hq + 2 * hkv, D)))
+        dev, dl = to_bf16(qkv), s.gpu_lens(lens)
+        hsa.hsa_kv8_write(d, cache, dev[:, hq:hq + hkv], dev[:, hq + hkv:], None, table, dl)
+        idx = np.tile(np.array([1, 2, 4], np.int32), (3, hkv, 1))
+        cnt = torch.full((3, hkv), 3, dtype=torch.int32, device="cuda")
+        q = dev[:, :hq].contiguous()
+        dense, kept = (torch.empty(3, hq, D, device="cuda") for _ in range(2))
+        hsa.hsa_kv8_decode(d, cache, q, table, dl, dense, None, wd)
+        hsa.hsa_kv8_attend(d, cache, q, table, dl, torch.from_numpy(idx).cuda(), cnt, kept, None, wd)
+        for b, n in enumerate(lens):
+            O.write(s.cache, qkv[b:b + 1, hq:hq + hkv], qkv[b:b + 1, hq + hkv:], s.table[b], n - 1)
+            t = np.arange(n)
+            seen = (t < 16) | (t >= n - 20) | np.isin(t // PAGE, [1, 2, 4])
+            for h in range(hkv):
+                kk, vv = values(b, n, h)
+                rows = slice(h * g, h * g + g)
+                for got, mask in ((dense, np.ones(n, bool)), (kept, seen)):
+                    want, _, tol = O.attend(qkv[b, rows], kk, vv, np.tile(mask, (g, 1)), D ** -0.5)
+                    assert_rows(got[b, rows].cpu(), None, want, None, tol)
+    extend([n + 7 for n in lens], [7, 7, 7])   # a draft ...
+    extend([n + 4 for n in lens], [3, 2, 4])   # ... of which a part is kept and written anew
+    assert_same_cache(cache, s.cache)
+    for ws in (wd, wp):
+        assert hsa.hsa_read_device_error(ws) == 0
+
+
+def test_codes_beyond_two_gigabytes():
+    """Pages whose bytes lie past 2^31 in each code array."""
+    hq, hkv, lens, new = 16, 8, [70, 33], [40, 5]
+    s = Batch(lens, hq, hkv, "int8", seed=14)
+    shift = 140000  # pages of 16 KiB
+    small, n = s.gpu_cache(), s.num_pages
+    codes = [torch.zeros(shift + n, hkv, 16, D, dtype=torch.int8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros(shift + n, hkv, device="cuda") for _ in range(2)]
+    for big, old in zip(codes + scales, (small.k, small.v, small.k_scale, small.v_scale)):
+        big[shift:] = old
+    cache = hsa.KV8(*codes, *scales)
+    table = s.gpu_table()
+    table += shift
+    d = s.dims()
+    d = hsa.Dims(**{**d.__dict__, "num_pages": shift + n})
+    k, v = s.rows(sum(new)), s.rows(sum(new))
+    at = 0
+    for b, m in enumerate(new):
+        O.write(s.cache, k[at:at + m], v[at:at + m], s.table[b], lens[b] - m)
+        at += m
+    hsa.hsa_kv8_write(d, cache, to_bf16(k), to_bf16(v), cu_of(new), table, s.gpu_lens())
+    assert_same_cache(hsa.KV8(codes[0][shift:], codes[1][shift:], scales[0][shift:].clone(),
+                              scales[1][shift:].clone()), s.cache)
+    assert not codes[0][:shift].any() and not scales[1][:shift].any()
+    back = torch.empty(2, sum(lens), hkv, D, dtype=torch.bfloat16, device="cuda")
+    hsa.hsa_kv8_read(d, cache, back[0], back[1], cu_of(lens), table, s.gpu_lens())
+    want = O.values(s.cache, "v", s.table[1], lens[1], 3)
+    np.testing.assert_array_equal(back[1, lens[0]:, 3].float().cpu().numpy(), bf16(want))
+    q = bf16(s.rng.standard_normal((sum(new), hq, D)))
+    out = torch.empty(sum(new), hq, D, dtype=torch.bfloat16, device="cuda")
+    hsa.hsa_kv8_prefill(d, cache, to_bf16(q), cu_of(new), table, s.gpu_lens(), out, None,
+                        hsa.workspace(d, hsa.HSA_OP_KV8_PREFILL))
+    check_prefill(s, q, new, out.float().cpu().numpy(), None)
+    rows = [new[0] - 1, sum(new) - 1]
+    o32, lse = torch.empty(2, hq, D, device="cuda"), torch.empty(2, hq, device="cuda")
+    hsa.hsa_kv8_decode(d, cache, to_bf16(q[rows]), table, s.gpu_lens(), o32, lse,
+                       hsa.workspace(d, hsa.HSA_OP_KV8_DECODE))
+    for b in range(2):
+        for h in range(hkv):
+            kk, vv = (O.values(s.cache, w, s.table[b], lens[b], h) for w in "kv")
+            r = slice(2 * h, 2 * h + 2)
+            want, wl, tol = O.attend(q[rows[b], r], kk, vv, np.ones((2, lens[b]), bool), D ** -0.5)
+            assert_rows(o32[b, r].cpu(), lse[b, r].cpu(), want, wl, tol)
+
+
+def test_a_large_batch():
+    """1024 sequences, most short, one long: every operator."""
+    lens = [1 + (i * 37) % 23 for i in range(1023)] + [700]
+    new = [min(n, 1 + i % 3) for i, n in enumerate(lens)]
+    s = Batch(lens, 4, 2, "e4m3", seed=15)
+    q = bf16(s.rng.standard_normal((len(lens), 4, D)))
+    out, lse = run_decode(s, q)
+    for b in (0, 1, 500, 1022, 1023):
+        for h in range(2):
+            kk, vv = (O.values(s.cache, w, s.table[b], lens[b], h) for w in "kv")
+            r = slice(2 * h, 2 * h + 2)
+            want, wl, tol = O.attend(q[b, r], kk, vv, np.ones((2, lens[b]), bool), D ** -0.5)
+            assert_rows(out[b, r], lse[b, r], want, wl, tol)
+    q = bf16(s.rng.standard_normal((sum(new), 4, D)))
+    out, lse = run_prefill(s, q, new)
+    at = np.concatenate([[0], np.cumsum(new)])
+    for b in (0, 2, 777, 1023):
+        n, m = lens[b], new[b]
+        for h in range(2):
+            kk, vv = (O.values(s.cache, w, s.table[b], n, h) for w in "kv")
+            seen = np.arange(n)[None] <= (n - m + np.arange(m))[:, None]
+            for j in (2 * h, 2 * h + 1):
+                want, wl, tol = O.attend(q[at[b]:at[b + 1], j], kk, vv, seen, D ** -0.5)
+                tol["out"] = tol["out"] + 2.0 ** -11 * np.abs(vv).max()
+                assert_rows(out[at[b]:at[b + 1], j], lse[at[b]:at[b + 1], j], want, wl, tol,
+                            2.0 ** -8)
+
+
+def test_prefill_reports_what_does_not_fit():
+    s = Batch([40, 64, 50], 2, 1, "int8", seed=1)
+    table = s.gpu_table()
+    table[0, 1] = -7
+    lens = s.gpu_lens([40, 64, 3])  # the third has fewer tokens than new ones
+    d = s.dims()
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_PREFILL)
+    q = to_bf16(s.rng.standard_normal((24, 2, D)))
+    out = torch.full((24, 2, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((24, 2), 9.0, device="cuda")
+    hsa.hsa_kv8_prefill(d, s.gpu_cache(), q, cu_of([10, 10, 4]), table, lens, out, lse, ws)
+    assert hsa.hsa_read_device_error(ws) == hsa.HSA_ERR_DEVICE_CHECK
+    assert torch.isfinite(out).all() and (out[20:] == 0).all() and torch.isneginf(lse[20:]).all()
+    check = Batch([40, 64, 50], 2, 1, "int8", seed=1)
+    kk, vv = (O.values(check.cache, w, check.table[1], 64, 0) for w in "kv")
+    seen = np.arange(64)[None] <= (54 + np.arange(10))[:, None]
+    want, wl, tol = O.attend(q[10:20, 0].float().cpu().numpy(), kk, vv, seen, D ** -0.5)
+    tol["out"] = tol["out"] + 2.0 ** -11 * np.abs(vv).max()
+    assert_rows(out[10:20, 0].float().cpu(), lse[10:20, 0].cpu(), want, wl, tol, 2.0 ** -8)

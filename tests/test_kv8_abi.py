@@ -1,0 +1,223 @@
+"""The 8-bit K/V cache without a GPU: its oracle pinned by hand-worked examples, the binding's
+struct against the header, workspace sizes, and the refusals that come before any CUDA call."""
+import ctypes
+import os
+import shutil
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv8 as O
+from test_abi import _header_struct_fields
+
+HAVE_NVCC = shutil.which("nvcc") is not None or os.path.exists("/usr/local/cuda/bin/nvcc")
+needs_lib = pytest.mark.skipif(not HAVE_NVCC, reason="nvcc is needed to build libhsa.so")
+
+
+# ------------------------------------------------------------------------------- the oracle
+
+def test_e4m3_codes_by_hand():
+    # 1 = 2^0 * 1.000 -> exponent field 7; 448 = 2^8 * 1.75; 2^-9 the smallest subnormal
+    assert list(O.e4m3_code([0.0, 1.0, -1.0, 448.0, 2.0 ** -9, 1e9])) == [0, 56, 184, 126, 1, 126]
+    assert np.array_equal(O.code_values("e4m3", np.array([56, 184, 126, 1], np.uint8)),
+                          [1.0, -1.0, 448.0, 2.0 ** -9])
+    # ties go to the even code: 17 between 16 and 18, 19 between 18 and 20
+    assert np.array_equal(O.code_values("e4m3", O.e4m3_code([17.0, 19.0])), [16.0, 20.0])
+
+
+def test_write_by_hand_grows_a_block():
+    c, s = np.zeros((16, 128), np.int8), np.float32(0)
+    row = np.zeros((1, 128), np.float32)
+    row[0, :3] = [127.0, -63.5, 2.0]
+    c, s = O.write_block("int8", c, s, row, 0)
+    assert s == 1.0 and list(c[0, :4]) == [127, -64, 2, 0]  # -63.5 to the even -64
+    row[0, :3] = [254.0, 1.0, -3.0]
+    c, s = O.write_block("int8", c, s, row, 1)
+    # the scale doubles: 127 / 2 = 63.5 -> 64 (even), -64 / 2 = -32, 2 / 2 = 1
+    assert s == 2.0 and list(c[0, :3]) == [64, -32, 1]
+    assert list(c[1, :3]) == [127, 0, -2]  # 0.5 -> 0, -1.5 -> -2
+    row[0, :3] = [1.0, 4.0, -5.0]
+    before = c.copy()
+    c, s = O.write_block("int8", c, s, row, 2)
+    assert s == 2.0 and np.array_equal(c[:2], before[:2]) and list(c[2, :3]) == [0, 2, -2]
+    c, s = O.write_block("int8", c, s, row, 0)  # from the first slot on: a scale of its own
+    assert s == np.float32(5.0) / np.float32(127.0) and c[0, 2] == -127
+
+
+def test_write_of_values_that_are_no_numbers():
+    row = np.array([[np.inf, -np.inf, np.nan, 10.0] + [0.0] * 124], np.float32)
+    c, s = O.write_block("int8", np.zeros((16, 128), np.int8), np.float32(0), row, 0)
+    assert s == np.float32(10) / np.float32(127) and list(c[0, :4]) == [127, -127, 0, 127]
+
+
+def test_attention_of_two_tokens_by_hand():
+    q = np.zeros((1, 128))
+    q[0, 0] = 1.0
+    k = np.zeros((2, 128))
+    k[1, 0] = np.log(3.0)
+    v = np.zeros((2, 128))
+    v[0, 5], v[1, 5] = 8.0, 4.0
+    out, lse, _ = O.attend(q, k, v, np.ones((1, 2), bool), 1.0)  # weights 1/4 and 3/4
+    assert out[0, 5] == pytest.approx(5.0) and lse[0] == pytest.approx(np.log(4.0))
+    out, lse, _ = O.attend(q, k, v, np.zeros((1, 2), bool), 1.0)
+    assert not out.any() and np.isneginf(lse[0])
+
+
+# ------------------------------------------------------------------------------ the library
+
+@pytest.fixture(scope="module")
+def lib():
+    from kv_cache_int8_gb300 import build, hsa
+    build.build()
+    return hsa
+
+
+def dims(lib, **kw):
+    return lib.Dims(**{**dict(batch=2, hq=32, hkv=8, max_pages_per_seq=64, num_pages=128, k2=4,
+                              sink=16, window=32), **kw})
+
+
+def test_binding_struct_matches_the_header():
+    from kv_cache_int8_gb300 import hsa
+    ctype = {"int32_t": ctypes.c_int32, "ptr": ctypes.c_void_p}
+    want = [("ptr", n) for n in ("k", "v", "k_scale", "v_scale")] + [("int32_t", "format")]
+    got = _header_struct_fields("hsa_kv8")
+    assert got == want
+    assert [(n, t) for n, t in hsa.hsa_kv8._fields_] == [(n, ctype[t]) for t, n in want]
+
+
+@needs_lib
+def test_workspace_sizes(lib):
+    for op in (lib.HSA_OP_KV8_DECODE, lib.HSA_OP_KV8_PREFILL):
+        assert lib.hsa_workspace_bytes(dims(lib), op) > 256
+        for hq in (8, 24, 40, 48, 56, 64):  # every group of 1 to 8
+            assert lib.hsa_workspace_bytes(dims(lib, hq=hq), op) > 256
+        for bad in (dict(hq=72), dict(hq=12), dict(head_dim=64), dict(page_size=32),
+                    dict(kv_on_host=True), dict(batch=0), dict(batch=2000)):
+            assert lib.hsa_workspace_bytes(dims(lib, **bad), op) == 0
+
+
+class Ws:
+    def __init__(self, ptr, n):
+        self.ptr, self.n = ptr, n
+
+    def data_ptr(self):
+        return self.ptr
+
+    def numel(self):
+        return self.n
+
+
+OK = 1 << 20  # an aligned address that validation never follows
+
+
+class Call:
+    """Raw C calls with fake addresses: every argument valid but those given."""
+
+    def __init__(self, lib, **kw):
+        self.lib = lib
+        self.a = dict(d=dims(lib), k=OK, v=OK, ks=OK, vs=OK, format=0, x=OK, y=OK, xs=8 * 128,
+                      ys=8 * 128, qs=32 * 128, cu=OK, total=100, table=OK, lens=OK, idx=OK,
+                      cnt=OK, out=OK, lse=OK, ws=OK, ws_bytes=1 << 40)
+        self.a.update(kw)
+
+    def __getattr__(self, name):
+        return self.a[name]
+
+    def run(self, fn):
+        c = self.lib.load()
+        d = ctypes.byref(self.d.c())
+        kv = ctypes.byref(self.lib.hsa_kv8(self.k, self.v, self.ks, self.vs, self.format))
+        if fn in ("write", "read"):
+            return getattr(c, "hsa_kv8_" + fn)(d, kv, self.x, self.xs, self.y, self.ys, self.cu,
+                                               self.total, self.table, self.lens, self.ws,
+                                               self.ws_bytes, None)
+        if fn == "decode":
+            return c.hsa_kv8_decode(d, kv, self.x, self.table, self.lens, self.out, self.lse,
+                                    self.ws, self.ws_bytes, None)
+        if fn == "attend":
+            return c.hsa_kv8_attend(d, kv, self.x, self.table, self.lens, self.idx, self.cnt,
+                                    self.out, self.lse, self.ws, self.ws_bytes, None)
+        return c.hsa_kv8_prefill(d, kv, self.x, self.qs, self.cu, self.total, self.table,
+                                 self.lens, self.out, self.lse, self.ws, self.ws_bytes, None)
+
+
+ALL = ("write", "read", "decode", "attend", "prefill")
+INVALID, UNSUPPORTED, SMALL = 1, 2, 5
+
+
+@needs_lib
+@pytest.mark.parametrize("fns,bad,code", [
+    (ALL, dict(k=None), INVALID), (ALL, dict(v=OK + 16), INVALID), (ALL, dict(ks=OK + 4), INVALID),
+    (ALL, dict(vs=None), INVALID), (ALL, dict(format=2), INVALID), (ALL, dict(x=None), INVALID),
+    (ALL, dict(x=OK + 8), INVALID), (ALL, dict(table=None), INVALID),
+    (ALL, dict(lens=None), INVALID), (ALL, dict(table=OK + 2), INVALID),
+    (("write", "read"), dict(y=None), INVALID), (("write", "read"), dict(xs=1020), INVALID),
+    (("write", "read"), dict(ys=1016), INVALID), (("prefill",), dict(qs=4092), INVALID),
+    (("prefill",), dict(qs=31 * 128), INVALID),
+    (("write", "read", "prefill"), dict(total=-1), INVALID),
+    (("write", "read", "prefill"), dict(cu=None), INVALID),  # no offsets: batch rows
+    (("write", "read", "prefill"), dict(cu=OK + 2), INVALID),
+    (("write", "read", "prefill"), dict(total=(1 << 31) - 1), UNSUPPORTED),
+    (("decode", "attend", "prefill"), dict(out=None), INVALID),
+    (("decode", "attend", "prefill"), dict(out=OK + 4), INVALID),
+    (("decode", "attend", "prefill"), dict(lse=OK + 2), INVALID),
+    (("decode", "attend", "prefill"), dict(ws=None), INVALID),
+    (("decode", "attend", "prefill"), dict(ws=OK + 128), INVALID),
+    (("decode", "attend", "prefill"), dict(ws_bytes=4096), SMALL),
+    (("write", "read"), dict(ws=OK + 128), INVALID),
+    (("write", "read"), dict(ws_bytes=128), SMALL),
+    (("attend",), dict(cnt=None), INVALID), (("attend",), dict(idx=None), INVALID),
+    (("attend",), dict(idx=OK + 2), INVALID),
+])
+def test_refusals_of_arguments(lib, fns, bad, code):
+    for fn in fns:
+        assert Call(lib, **bad).run(fn) == code, fn
+
+
+@needs_lib
+@pytest.mark.parametrize("kw,code", [
+    (dict(hq=72), UNSUPPORTED), (dict(hq=30), INVALID), (dict(head_dim=64), UNSUPPORTED),
+    (dict(page_size=8), UNSUPPORTED), (dict(batch=0), INVALID), (dict(batch=1025), UNSUPPORTED),
+    (dict(kv_on_host=True), UNSUPPORTED), (dict(num_pages=0), INVALID),
+    (dict(num_pages=1 << 30), UNSUPPORTED), (dict(sm_scale=float("nan")), INVALID),
+    (dict(window=-1), INVALID), (dict(per_head=2), INVALID),
+])
+def test_refusals_of_descriptors(lib, kw, code):
+    for fn in ALL:
+        assert Call(lib, d=dims(lib, **kw)).run(fn) == code, fn
+
+
+@needs_lib
+def test_too_many_visits_are_refused(lib):
+    # rows x (kept blocks + sink + window blocks) beyond 32 bits
+    d = dims(lib, hq=64, hkv=8, per_head=1, k2=1 << 27)
+    assert Call(lib, d=d).run("attend") == UNSUPPORTED
+    assert Call(lib, d=dims(lib, k2=0), idx=None, ws_bytes=64).run("attend") == SMALL
+
+
+@needs_lib
+def test_no_rows_are_no_call(lib):
+    for fn in ("write", "read", "prefill"):
+        assert Call(lib, total=0).run(fn) == 0
+
+
+def test_the_binding_refuses_other_tensors():
+    from kv_cache_int8_gb300 import hsa
+    k = torch.zeros(4, 2, 16, 128, dtype=torch.int8)
+    s = torch.zeros(4, 2)
+    hsa.KV8(k, k.clone(), s, s.clone())
+    for bad in ((k, k.view(torch.float8_e4m3fn), s, s), (k.float(), k.float(), s, s),
+                (k, k[:3], s, s), (k, k, s, s[:3]), (k, k, s, s.double()),
+                (k.transpose(0, 1), k.transpose(0, 1), s, s)):
+        with pytest.raises(hsa.HsaError):
+            hsa.KV8(*bad)
+    d = dims(hsa, hq=4, hkv=2)
+    cache = hsa.KV8(k, k.clone(), s, s.clone())
+    rows = torch.zeros(5, 2, 128, dtype=torch.bfloat16)
+    for x, y in ((rows.float(), rows), (rows[:, :1], rows), (rows, rows[:4]),
+                 (rows.transpose(0, 1).contiguous().transpose(0, 1), rows),
+                 (torch.zeros(5, 2, 256, dtype=torch.bfloat16)[..., ::2], rows)):
+        with pytest.raises(hsa.HsaError):
+            hsa.hsa_kv8_write(d, cache, x, y, None, None, None)
