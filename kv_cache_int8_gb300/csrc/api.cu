@@ -1094,10 +1094,11 @@ int32_t hsa_kv8_write(const hsa_dims* d, const hsa_kv8* cache, const void* k_new
   int* err = nullptr;
   int32_t rc = check_kv8(d, cache, s, &c);
   if (rc == HSA_OK) rc = check_rows(s, cu_tokens, total_tokens, page_table, seq_lens);
-  if (rc == HSA_OK) rc = check_row_array(k_new, k_stride, s.hkv);
+  if (rc != HSA_OK || total_tokens == 0) return rc;  // no rows, no arrays of them
+  rc = check_row_array(k_new, k_stride, s.hkv);
   if (rc == HSA_OK) rc = check_row_array(v_new, v_stride, s.hkv);
   if (rc == HSA_OK) rc = error_word(workspace, workspace_bytes, &err);
-  if (rc != HSA_OK || total_tokens == 0) return rc;
+  if (rc != HSA_OK) return rc;
   return cuda_status(hsa::launch_kv8_write(s, c, k_new, k_stride, v_new, v_stride, cu_tokens,
                                            total_tokens, page_table, seq_lens, err,
                                            as_stream(stream)));
@@ -1112,10 +1113,11 @@ int32_t hsa_kv8_read(const hsa_dims* d, const hsa_kv8* cache, void* k_out, int64
   int* err = nullptr;
   int32_t rc = check_kv8(d, cache, s, &c);
   if (rc == HSA_OK) rc = check_rows(s, cu_tokens, total_tokens, page_table, seq_lens);
-  if (rc == HSA_OK) rc = check_row_array(k_out, k_stride, s.hkv);
+  if (rc != HSA_OK || total_tokens == 0) return rc;  // no rows, no arrays of them
+  rc = check_row_array(k_out, k_stride, s.hkv);
   if (rc == HSA_OK) rc = check_row_array(v_out, v_stride, s.hkv);
   if (rc == HSA_OK) rc = error_word(workspace, workspace_bytes, &err);
-  if (rc != HSA_OK || total_tokens == 0) return rc;
+  if (rc != HSA_OK) return rc;
   return cuda_status(hsa::launch_kv8_read(s, c, k_out, k_stride, v_out, v_stride, cu_tokens,
                                           total_tokens, page_table, seq_lens, err,
                                           as_stream(stream)));
@@ -1144,12 +1146,13 @@ int32_t hsa_kv8_prefill(const hsa_dims* d, const hsa_kv8* cache, const void* q, 
   hsa::Kv8 c;
   int32_t rc = check_kv8(d, cache, s, &c);
   if (rc == HSA_OK) rc = check_rows(s, cu_tokens, total_tokens, page_table, seq_lens);
-  if (rc == HSA_OK) rc = check_row_array(q, q_stride, s.hq);
+  if (rc != HSA_OK || total_tokens == 0) return rc;  // no rows, no arrays of them
+  rc = check_row_array(q, q_stride, s.hq);
   if (rc != HSA_OK) return rc;
   if (!out || !aligned(out, 16) || !aligned(lse, 4)) return HSA_ERR_INVALID_ARG;
   const Kv8Layout l = kv8_prefill_layout();
   rc = check_ws(s, workspace, workspace_bytes, l.end);
-  if (rc != HSA_OK || total_tokens == 0) return rc;
+  if (rc != HSA_OK) return rc;
   char* ws = static_cast<char*>(workspace);
   return cuda_status(hsa::launch_kv8_prefill(
       s, c, q, q_stride, cu_tokens, total_tokens, page_table, seq_lens, out, lse,

@@ -103,16 +103,17 @@ class Dims:
 
     def c(self) -> hsa_dims:
         """The C struct, built once per set of field values (every call of a step passes it)."""
-        key = (self.batch, self.hq, self.hkv, self.head_dim, self.page_size,
-               self.max_pages_per_seq, self.num_pages, self.chunk, self.block, self.k1,
-               self.k2, self.sink, self.window, float(self.sm_scale),
-               1 if self.kv_on_host else 0, self.chunk0, self.k0, self.key_bits, self.per_head,
-               self.key_fp8, self.cache_policy)
+        key = tuple(self.__dict__.values())
         c = _DIMS_CACHE.get(key)
         if c is None:
             if len(_DIMS_CACHE) > 256:
                 _DIMS_CACHE.clear()
-            c = _DIMS_CACHE[key] = hsa_dims(*key)
+            c = _DIMS_CACHE[key] = hsa_dims(
+                self.batch, self.hq, self.hkv, self.head_dim, self.page_size,
+                self.max_pages_per_seq, self.num_pages, self.chunk, self.block, self.k1,
+                self.k2, self.sink, self.window, float(self.sm_scale),
+                1 if self.kv_on_host else 0, self.chunk0, self.k0, self.key_bits, self.per_head,
+                self.key_fp8, self.cache_policy)
         return c
 
 
@@ -416,36 +417,46 @@ class KV8:
                              for _ in range(2)))
 
 
-def _row_stride(name: str, t, heads: int) -> int:
-    """The row stride of a bf16 tensor [tokens][heads][128] whose rows are contiguous."""
-    if (t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or
-            t.stride(1) != t.shape[2] or t.stride(2) != 1):
+def _rows(name: str, t, heads: int):
+    """(rows, row stride) of a bf16 tensor [tokens][heads][128] whose rows are contiguous."""
+    shape, stride = t.shape, t.stride()
+    if (t.dtype is not torch.bfloat16 or len(stride) != 3 or shape[1] != heads or
+            shape[2] != 128 or stride[2] != 1 or (stride[1] != 128 and heads > 1)):
         raise HsaError(name, HSA_ERR_INVALID_ARG, "rows must be bf16 [tokens][heads][128]")
-    return t.stride(0)
+    return shape[0], stride[0]
+
+
+def _row_pair(name: str, k, v, heads: int):
+    """(rows, k's row stride, v's) of two such tensors of as many rows."""
+    rows, k_stride = _rows(name, k, heads)
+    v_rows, v_stride = _rows(name, v, heads)
+    if v_rows != rows:
+        raise HsaError(name, HSA_ERR_INVALID_ARG, "k and v differ in rows")
+    return rows, k_stride, v_stride
 
 
 def hsa_kv8_write(d: Dims, cache: KV8, k_new, v_new, cu_tokens, page_table, seq_lens, ws=None,
                   stream=None) -> None:
     """k_new / v_new: bf16 [total_tokens][hkv][128], rows contiguous (any row stride)."""
-    if v_new.shape[0] != k_new.shape[0]:
-        raise HsaError("hsa_kv8_write", HSA_ERR_INVALID_ARG, "k_new and v_new differ in rows")
-    _check("hsa_kv8_write", load().hsa_kv8_write(
-        ctypes.byref(d.c()), cache._ref, k_new.data_ptr(),
-        _row_stride("hsa_kv8_write", k_new, d.hkv), v_new.data_ptr(),
-        _row_stride("hsa_kv8_write", v_new, d.hkv), _p(cu_tokens), k_new.shape[0], _p(page_table),
-        _p(seq_lens), _p(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+    rows, k_stride, v_stride = _row_pair("hsa_kv8_write", k_new, v_new, d.hkv)
+    rc = load().hsa_kv8_write(
+        ctypes.byref(d.c()), cache._ref, k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
+        _p(cu_tokens), rows, _p(page_table), _p(seq_lens), _p(ws),
+        0 if ws is None else ws.numel(), _stream(stream))
+    if rc != HSA_OK:
+        _check("hsa_kv8_write", rc)
 
 
 def hsa_kv8_read(d: Dims, cache: KV8, k_out, v_out, cu_tokens, page_table, seq_lens, ws=None,
                  stream=None) -> None:
     """k_out / v_out: bf16 [total_tokens][hkv][128], rows contiguous (any row stride)."""
-    if v_out.shape[0] != k_out.shape[0]:
-        raise HsaError("hsa_kv8_read", HSA_ERR_INVALID_ARG, "k_out and v_out differ in rows")
-    _check("hsa_kv8_read", load().hsa_kv8_read(
-        ctypes.byref(d.c()), cache._ref, k_out.data_ptr(),
-        _row_stride("hsa_kv8_read", k_out, d.hkv), v_out.data_ptr(),
-        _row_stride("hsa_kv8_read", v_out, d.hkv), _p(cu_tokens), k_out.shape[0], _p(page_table),
-        _p(seq_lens), _p(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+    rows, k_stride, v_stride = _row_pair("hsa_kv8_read", k_out, v_out, d.hkv)
+    rc = load().hsa_kv8_read(
+        ctypes.byref(d.c()), cache._ref, k_out.data_ptr(), k_stride, v_out.data_ptr(), v_stride,
+        _p(cu_tokens), rows, _p(page_table), _p(seq_lens), _p(ws),
+        0 if ws is None else ws.numel(), _stream(stream))
+    if rc != HSA_OK:
+        _check("hsa_kv8_read", rc)
 
 
 def hsa_kv8_decode(d: Dims, cache: KV8, q, page_table, seq_lens, out, lse, ws,
@@ -465,12 +476,15 @@ def hsa_kv8_attend(d: Dims, cache: KV8, q, page_table, seq_lens, block_idx, n_bl
 def hsa_kv8_prefill(d: Dims, cache: KV8, q, cu_tokens, page_table, seq_lens, out, lse, ws,
                     stream=None) -> None:
     """q: bf16 [total_tokens][hq][128], rows contiguous (any row stride); out: bf16, contiguous."""
-    if not out.is_contiguous() or out.shape != q.shape or out.dtype != torch.bfloat16:
+    rows, q_stride = _rows("hsa_kv8_prefill", q, d.hq)
+    if not out.is_contiguous() or out.shape != q.shape or out.dtype is not torch.bfloat16:
         raise HsaError("hsa_kv8_prefill", HSA_ERR_INVALID_ARG, "out must be contiguous, as q")
-    _check("hsa_kv8_prefill", load().hsa_kv8_prefill(
-        ctypes.byref(d.c()), cache._ref, q.data_ptr(), _row_stride("hsa_kv8_prefill", q, d.hq),
-        _p(cu_tokens), q.shape[0], _p(page_table), _p(seq_lens), out.data_ptr(), _p(lse), _p(ws),
-        ws.numel(), _stream(stream)))
+    rc = load().hsa_kv8_prefill(
+        ctypes.byref(d.c()), cache._ref, q.data_ptr(), q_stride, _p(cu_tokens), rows,
+        _p(page_table), _p(seq_lens), out.data_ptr(), _p(lse), _p(ws), ws.numel(),
+        _stream(stream))
+    if rc != HSA_OK:
+        _check("hsa_kv8_prefill", rc)
 
 
 def hsa_read_device_error(ws, stream=None) -> int:

@@ -201,6 +201,7 @@ def test_too_many_visits_are_refused(lib):
 def test_no_rows_are_no_call(lib):
     for fn in ("write", "read", "prefill"):
         assert Call(lib, total=0).run(fn) == 0
+        assert Call(lib, total=0, x=None, y=None, out=None).run(fn) == 0
 
 
 def test_the_binding_refuses_other_tensors():
