@@ -20,6 +20,8 @@
  *      -- "KV Cache 与长上下文推理", sections "KV Cache 回顾" (decode attention
  *      equation) and "Token Eviction 与 Sparse Attention" (StreamingLLM sinks +
  *      sliding window).
+ * Beside the step, a K/V cache held in 8 bits with the calls that write, read and attend it
+ * (its own section below).
  *
  * Conventions shared by every call:
  *  - Every pointer is a DEVICE pointer unless a flag below says otherwise. The caller
