@@ -402,6 +402,8 @@ int32_t hsa_decode_step_kernels(const hsa_dims* d);
  *    reported as HSA_ERR_DEVICE_CHECK through the error word.
  *  - Row strides are in elements, at least the row's own length, and a multiple of 8.
  *  - Pointers are 16-byte aligned (code arrays 128-byte); the page table and lengths 4-byte.
+ *  - Workspaces do not depend on the descriptor: one of hsa_workspace_bytes(d,
+ *    HSA_OP_KV8_PREFILL) bytes serves both attentions and every descriptor, one call at a time.
  */
 typedef struct hsa_kv8 {
   void* k;        /* K codes [num_pages][hkv][16][128] */

@@ -181,23 +181,27 @@ hsa::BlockCache block_cache_at(const Shape& s, void* buf, int capacity) {
   return c;
 }
 
-// The 8-bit cache's decode attention: counters a selection row, then two parts a CTA.
+// The 8-bit cache's attentions: a counter for each CTA whose last row (row block and tile) goes
+// on in the next one, then the parts. The counters of the two operations lie side by side at
+// places that no descriptor moves, so one workspace may serve both and any descriptor it is
+// large enough for.
 struct Kv8Layout {
   size_t counters, part_ml, part_o, end;
 };
-Kv8Layout kv8_layout(const Shape& s) {
+constexpr size_t kKv8Parts = kErrBytes + (size_t)3 * hsa::kKv8MaxCtas * 4;
+static_assert(kKv8Parts % kAlign == 0, "parts are aligned");
+Kv8Layout kv8_decode_layout() {
   Kv8Layout l;
   l.counters = kErrBytes;
-  l.part_ml = l.counters + up((size_t)s.batch * s.hq * 4);
+  l.part_ml = kKv8Parts;
   l.part_o = l.part_ml + (size_t)2 * hsa::kKv8MaxCtas * 8 * 2 * 4;
   l.end = l.part_o + (size_t)2 * hsa::kKv8MaxCtas * 8 * hsa::kHeadDim * 4;
   return l;
 }
-
 Kv8Layout kv8_prefill_layout() {
   Kv8Layout l;
-  l.counters = kErrBytes;
-  l.part_ml = l.counters + up((size_t)2 * hsa::kKv8MaxCtas * 4);
+  l.counters = kErrBytes + (size_t)hsa::kKv8MaxCtas * 4;
+  l.part_ml = kKv8Parts;
   l.part_o = l.part_ml + up(hsa::kv8_prefill_ml_floats() * 4);
   l.end = l.part_o + up(hsa::kv8_prefill_part_floats() * 4);
   return l;
@@ -545,7 +549,7 @@ int32_t do_kv8_attend(const hsa_dims* d, const hsa_kv8* cache, bool kept, const 
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(page_table, 4) ||
       !aligned(seq_lens, 4) || !aligned(block_idx, 4) || !aligned(n_blocks, 4))
     return HSA_ERR_INVALID_ARG;
-  const Kv8Layout l = kv8_layout(s);
+  const Kv8Layout l = kv8_decode_layout();
   rc = check_ws(s, workspace, workspace_bytes, l.end);
   if (rc != HSA_OK) return rc;
   // the visits of a sequence's rows are counted in 32 bits
@@ -583,7 +587,7 @@ size_t hsa_workspace_bytes(const hsa_dims* d, int32_t op) {
     case HSA_OP_DENSE: return attend_ws(s);
     case HSA_OP_STEP: return step_layout(s).end;
     case HSA_OP_CACHED: return cached_ws(s);
-    case HSA_OP_KV8_DECODE: return kv8_layout(s).end;
+    case HSA_OP_KV8_DECODE: return kv8_decode_layout().end;
     case HSA_OP_KV8_PREFILL: return kv8_prefill_layout().end;
     default: return 0;
   }

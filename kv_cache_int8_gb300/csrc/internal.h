@@ -181,7 +181,7 @@ cudaError_t launch_kv8_read(const Shape& s, const Kv8& c, void* k_out, long long
                             void* v_out, long long v_stride, const int32_t* cu, int total,
                             const int32_t* page_table, const int32_t* seq_lens, int* err,
                             cudaStream_t st);
-// part_ml [2 kKv8MaxCtas][8][2], part_o [2 kKv8MaxCtas][8 * 128], counters [batch][rows] (zero)
+// part_ml [2 kKv8MaxCtas][8][2], part_o [2 kKv8MaxCtas][8 * 128], counters [kKv8MaxCtas] (zero)
 constexpr int kKv8MaxCtas = 256;
 cudaError_t launch_kv8_attend(const Shape& s, bool kept, const Kv8& c, const CUtensorMap& k_map,
                               const CUtensorMap& v_map, const void* q, const int32_t* page_table,

@@ -66,7 +66,7 @@ struct Params {
   float* lse;
   float* part_ml;  // [2 CTAs][8 heads] (m, l)
   float* part_o;   // [2 CTAs][kTile]
-  int* counters;   // [batch][rows]
+  int* counters;   // [CTAs]: of the row that begins in a CTA and goes on behind it
   int* err;
   int batch, hq, hkv, rows, group, kv_div, max_pages, num_pages, sink, window, k2;
   float scale_log2;  // sm_scale log2 e
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tid < 8) reinterpret_cast<float2*>(p.part_ml + slot * 16)[tid] = sm.total[tid];
       __syncthreads();
       if (tid == 0) {  // releases what the barrier has ordered before it
-        int* counter = p.counters + (size_t)b * p.rows + row;
+        int* counter = p.counters + c0;
         const int last = atomic_add_acq_rel_gpu(counter, 1) == parts - 1;
         if (last) *counter = 0;
         sm.last = last;
@@ -741,7 +741,7 @@ cudaError_t launch_kv8_attend(const Shape& s, bool kept, const Kv8& c, const CUt
   p.scale_log2 = s.sm_scale * 1.44269504088896341f;
   // no more CTAs than the longest possible line has smallest slices
   const long long most_row =
-      kept ? std::min<long long>((s.sink + kPage - 1) / kPage, s.max_pages) +
+      kept ? std::min<long long>(s.sink / kPage + 1, s.max_pages) +
                  std::min<long long>(s.window / kPage + 2, s.max_pages) + s.k2
            : s.max_pages;
   const long long most = (most_row * p.rows * s.batch + kMinUnits - 1) / kMinUnits;
