@@ -226,16 +226,19 @@ struct Smem {
   Unit meta[kWarps][kMeta];
   float2 ml[8][kWarps];      // a head's (m, l) of each warp
   float weight[kAhead][8];   // of the warps, then of the parts: 2^(m - the largest m)
-  float2 total[8];           // a row's (m, l)
+  float2 total[4][8];        // a row's (m, l), of each team
   int slot[kWarps];   // the ring slot of each warp's outputs
   alignas(8) uint64_t full[kWarps][kStages];
   int last;
   long long per;
   unsigned align;
+  int team;
 };
 // behind it: pre (long long [batch + 1]), lens (int [batch])
 
-template <int F, bool kKept>
+// kTeams: more rows than CTAs, which a team of 16, 4 or 1 warps may then take whole. (Without it
+// the code is a fifth shorter, which a call of a few rows feels: 12.6 against 13.7 us.)
+template <int F, bool kKept, bool kTeams>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_attend_kernel(const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map, const Params p) {
@@ -283,13 +286,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     const long long sum = lay(0);
-    // Slices of `per` units. With at least two CTAs a row, the smallest of 32 sizes from the
-    // even cut on under which rows can begin with a slice of their own is taken: a CTA that
-    // ends one row and begins the next joins parts twice, 5 us at 128K tokens, the time of 54
-    // units.
+    // How the line is cut, and how many warps share a row (rows: sequences x kv heads):
+    //  - up to a row a CTA: 16 warps, slices of the smallest of 32 sizes from the even cut on
+    //    under which every row begins with a slice of its own (a CTA that ends one row and
+    //    begins the next joins parts twice, 5 us at 128K tokens, the time of 54 units);
+    //  - else by what the three team sizes would take, in us, from fits to the cases below: the
+    //    stream's 0.09 a unit and SM, or the rows that a team takes one after the other, and a
+    //    last row that no other team helps with. Teams of 4 and of 1 take whole rows; teams of
+    //    16 (a CTA) even slices, whatever rows they cut. Measured, teams of 16 alone and this
+    //    rule: 8192 rows of 80 tokens 304 and 67 us, of 450 tokens 419 and 207; 2048 rows of 650
+    //    147 and 89; 512 rows of 650 51 and 37, of 2500 (where it takes 16) 88 and 94; 240 rows
+    //    of 28 33 and 9.3; 160 rows of 620 22.6 and 17.8.
+    const long long rows = (long long)p.batch * p.rows;
     long long per = max((sum + gridDim.x - 1) / gridDim.x, (long long)kMinUnits);
     unsigned align = 0;
-    if (2LL * p.batch * p.rows <= gridDim.x) {
+    int team = kWarps;
+    if (!kTeams && rows <= gridDim.x) {
       const unsigned mine = (unsigned)per + lane;
       long long slices = 0;
       for (int b = 0; b < p.batch; b++)
@@ -300,17 +312,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         lay(align);
       }
     }
+    if (kTeams) {
+      int longest = 0;
+      for (int b = lane; b < p.batch; b += 32) longest = max(longest, row_units<kKept>(p, lens[b]));
+      longest = (int)max32((float)longest);
+      const float stream = 0.09f * sum / gridDim.x, each = (float)rows / gridDim.x;
+      const float mean = (float)sum / rows;
+      const float t16 = stream + 5.0f * each + 15.0f;
+      const float t4 = fmaxf(stream, each / 4 * (5.0f + 0.42f * mean)) + 0.3f * longest;
+      const float t1 = fmaxf(stream, each / 16 * (8.0f + 1.45f * mean)) + 0.7f * longest;
+      team = t1 <= fminf(t4, t16) ? 1 : t4 <= t16 ? 4 : kWarps;
+      const long long teams = (long long)gridDim.x * (kWarps / team);
+      if (team < kWarps) per = max((sum + teams - 1) / teams, 1LL);
+    }
     if (lane == 0) {
       pre[0] = 0;
       sm.per = per;
       sm.align = align;
+      sm.team = team;
     }
   }
   __syncthreads();
   const long long per = sm.per;
   const unsigned align = sm.align;
+  const int team = kTeams ? sm.team : kWarps;  // warps that share a row: 16, 4 or 1
+  const int first_warp = warp & ~(team - 1);
   const long long all = pre[p.batch];
-  const long long begin = min(blockIdx.x * per, all), end = min(begin + per, all);
+  auto sequence_at = [&](long long x) {  // the b with pre[b] <= x < pre[b + 1]
+    int lo_b = 0, hi_b = p.batch;
+    while (hi_b - lo_b > 1) {
+      const int mid = (lo_b + hi_b) >> 1;
+      if (pre[mid] <= x) lo_b = mid;
+      else hi_b = mid;
+    }
+    return lo_b;
+  };
+  auto row_from = [&](long long x) {  // where the first row from place x on begins
+    if (x >= all) return all;
+    const int b = sequence_at(x);
+    const unsigned u = row_places(row_units<kKept>(p, lens[b]), align);
+    return pre[b] + (long long)((unsigned)(x - pre[b] + u - 1) / u) * u;
+  };
+  const int slice = (blockIdx.x * kWarps + first_warp) / team;
+  long long begin = min(slice * per, all), end = min(begin + per, all);
+  if (kTeams && team < kWarps) {  // whole rows
+    begin = row_from(begin);
+    end = row_from(end);
+  }
+  auto team_sync = [&]() {
+    asm volatile("bar.sync %0, %1;" ::"r"(team == kWarps ? 0 : 1 + first_warp / 4), "r"(team * 32)
+                 : "memory");
+  };
 
   // rows of no units at all
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
@@ -322,11 +374,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (begin >= end) return;
 
-  // ---- this warp's visits: places begin + warp + kWarps i, located kBatch at a time
-  const long long x0 = begin + warp;
-  const int mine = x0 < end ? (int)((end - x0 + kWarps - 1) / kWarps) : 0;
+  // ---- this warp's visits: places x0 + stride i, located kBatch at a time
+  const long long x0 = begin + (warp - first_warp);
+  const int stride = team;
+  const int mine = x0 < end ? (int)((end - x0 + stride - 1) / stride) : 0;
   auto fetch = [&](int i0) {
-    const long long x = x0 + (long long)kWarps * (i0 + lane);
+    const long long x = x0 + (long long)stride * (i0 + lane);
     Unit u = {0, 0, 0.0f, 0.0f};
     if (lane < kBatch && x < end) u = locate<kKept>(p, pre, lens, align, x);
     return u;
@@ -370,18 +423,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   int i = 0;
   for (long long x = begin; x < end;) {
     // ---- the row at x, and how far this slice goes in it
-    int lo_b = 0, hi_b = p.batch;
-    while (hi_b - lo_b > 1) {
-      const int mid = (lo_b + hi_b) >> 1;
-      if (pre[mid] <= x) lo_b = mid;
-      else hi_b = mid;
-    }
-    const int b = lo_b;
+    const int b = sequence_at(x);
     const unsigned units = row_places(row_units<kKept>(p, lens[b]), align);
     const int row = (int)((unsigned)(x - pre[b]) / units);
     const long long row_begin = pre[b] + (long long)row * units, row_end = row_begin + units;
     const long long stop = min(row_end, end);
-    const int i_stop = (int)((stop - x0 + kWarps - 1) / kWarps);  // this warp's visits before it
+    const int i_stop = (int)((stop - x0 + stride - 1) / stride);  // this warp's visits before it
     issue_to(i + kStages, i_stop);
 
     // ---- the query as right operands: head g, channels of chunk 2t + c, word w
@@ -585,6 +632,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       l0 += __shfl_xor_sync(0xffffffffu, l0, d);
       l1 += __shfl_xor_sync(0xffffffffu, l1, d);
     }
+    if (kTeams && team == 1) {  // the row is this warp's
+      const size_t head = (size_t)b * p.hq + (size_t)row * p.group + 2 * t;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        if (2 * t + h >= p.group) continue;
+        const float l = h ? l1 : l0;
+        const float r = l > 0.0f ? 1.0f / l : 0.0f;
+        float4* dst = reinterpret_cast<float4*>(p.out + (head + h) * kHeadDim + 16 * g);
+#pragma unroll
+        for (int k = 0; k < 8; k += 2)
+          dst[k / 2] = make_float4(o[k][h] * r, o[k][2 + h] * r, o[k + 1][h] * r, o[k + 1][2 + h] * r);
+        if (p.lse != nullptr && g == 0)
+          p.lse[head + h] = ((h ? m1 : m0) - kHeadroom + log2f(l)) * 0.693147180559945309f;
+      }
+      x = stop;
+      continue;
+    }
     if (g == 0) {
       sm.ml[2 * t][warp] = make_float2(m0, l0);
       sm.ml[2 * t + 1][warp] = make_float2(m1, l1);
@@ -597,21 +661,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         dst[k * 32 + lane] = make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
       if (lane == 0) sm.slot[warp] = slot;
     }
-    __syncthreads();
-    // joins (m, l) pairs of head `warp`, one a lane, into `sum`, and leaves their weights
-    auto weigh = [&](float2 v, float2 sum) {
+    team_sync();
+    // joins (m, l) pairs of a head, one a lane (n of them), into `sum`, and leaves their weights
+    // from place `at` on
+    auto weigh = [&](float2 v, float2 sum, int head, int at, int n) {
       const float top = fmaxf(max32(v.x), sum.x);
       const float ref = top == -INFINITY ? 0.0f : top;
       const float f = ex2(v.x - ref);  // 0 from -inf
-      if (lane < kAhead) sm.weight[lane][warp] = f;
+      if (lane < n) sm.weight[at + lane][head] = f;
       return make_float2(top, sum32(f * v.y) + ex2(sum.x - ref) * sum.y);
     };
     const float2 nothing = make_float2(-INFINITY, 0.0f);
-    if (warp < 8) {
-      const float2 v = weigh(lane < kWarps ? sm.ml[warp][lane] : nothing, nothing);
-      if (lane == 0) sm.total[warp] = v;
+    float2* const total = sm.total[first_warp / 4];
+    for (int h = warp - first_warp; h < 8; h += team) {
+      const float2 v =
+          weigh(lane < team ? sm.ml[h][first_warp + lane] : nothing, nothing, h, first_warp, team);
+      if (lane == 0) total[h] = v;
     }
-    __syncthreads();
+    team_sync();
+    if (kTeams && team < kWarps) {  // the row is complete: value pairs i of the tile (see below)
+      for (int i = tid - first_warp * 32; i < kTile / 2; i += team * 32) {
+        const int hl = (i >> 1) & 31, ht = hl & 3;
+        float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const int w = first_warp + k;
+          const float2 f = *reinterpret_cast<const float2*>(&sm.weight[w][2 * ht]);
+          const float2 v = reinterpret_cast<const float2*>(sm.ring[w][sm.slot[w]])[i];
+          acc.x += f.x * v.x;
+          acc.y += f.y * v.y;
+        }
+        const float2 ta = total[2 * ht], tb = total[2 * ht + 1];
+        const size_t head = (size_t)b * p.hq + (size_t)row * p.group + 2 * ht;
+        const int ch = 16 * (hl >> 2) + 2 * (i >> 6) + (i & 1);
+        const bool sums = p.lse != nullptr && i < 8 && (i & 1) == 0;
+        if (2 * ht < p.group) {
+          p.out[head * kHeadDim + ch] = ta.y > 0.0f ? acc.x / ta.y : 0.0f;
+          if (sums) p.lse[head] = (ta.x - kHeadroom + log2f(ta.y)) * 0.693147180559945309f;
+        }
+        if (2 * ht + 1 < p.group) {
+          p.out[(head + 1) * kHeadDim + ch] = tb.y > 0.0f ? acc.y / tb.y : 0.0f;
+          if (sums) p.lse[head + 1] = (tb.x - kHeadroom + log2f(tb.y)) * 0.693147180559945309f;
+        }
+      }
+      fence_proxy_async();
+      team_sync();  // the slots are free for the next row's blocks
+      x = stop;
+      continue;
+    }
     // values 2 tid, 2 tid + 1 of the tile: channel 16 g' + tid / 64 * 2 + (tid & 1) of heads
     // 2t', 2t' + 1, where lane 4 g' + t' = (tid / 2) % 32 held them
     const int hl = (tid >> 1) & 31, ht = hl & 3;
@@ -628,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int c0 = (int)(row_begin / per), parts = (int)((row_end - 1) / per) - c0 + 1;
       const size_t slot = 2 * (size_t)blockIdx.x + (begin < row_begin ? 1 : 0);
       reinterpret_cast<float2*>(p.part_o + slot * kTile)[tid] = acc;
-      if (tid < 8) reinterpret_cast<float2*>(p.part_ml + slot * 16)[tid] = sm.total[tid];
+      if (tid < 8) reinterpret_cast<float2*>(p.part_ml + slot * 16)[tid] = total[tid];
       __syncthreads();
       if (tid == 0) {  // releases what the barrier has ordered before it
         int* counter = p.counters + c0;
@@ -661,12 +758,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c + k < parts) v[k] = __ldcg(more + k * kTile);
           }
           if (warp < 8) {
-            sum = weigh(ml, sum);
-            if (lane == 0) sm.total[warp] = sum;
+            sum = weigh(ml, sum, warp, 0, kAhead);
+            if (lane == 0) total[warp] = sum;
           }
           __syncthreads();
-          const float2 now = make_float2(fmaxf(sm.total[2 * ht].x, -1e30f),
-                                         fmaxf(sm.total[2 * ht + 1].x, -1e30f));
+          const float2 now = make_float2(fmaxf(total[2 * ht].x, -1e30f),
+                                         fmaxf(total[2 * ht + 1].x, -1e30f));
           acc.x *= ex2(was.x - now.x);  // by 0 the first time
           acc.y *= ex2(was.y - now.y);
           was = now;
@@ -681,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (write) {
-      const float2 ta = sm.total[2 * ht], tb = sm.total[2 * ht + 1];
+      const float2 ta = total[2 * ht], tb = total[2 * ht + 1];
       const size_t head = (size_t)b * p.hq + (size_t)row * p.group + 2 * ht;
       const int ch = 16 * (hl >> 2) + 2 * (tid >> 6) + (tid & 1);
       const bool sums = p.lse != nullptr && tid < 8 && (tid & 1) == 0;
@@ -745,10 +842,18 @@ cudaError_t launch_kv8_attend(const Shape& s, bool kept, const Kv8& c, const CUt
                  std::min<long long>(s.window / kPage + 2, s.max_pages) + s.k2
            : s.max_pages;
   const long long most = (most_row * p.rows * s.batch + kMinUnits - 1) / kMinUnits;
-  const int grid = (int)std::max(1LL, std::min<long long>(kv8_attend_ctas(num_sms), most));
-  auto kernel = c.format == kE4m3
-                    ? (kept ? kv8_attend_kernel<kE4m3, true> : kv8_attend_kernel<kE4m3, false>)
-                    : (kept ? kv8_attend_kernel<kInt8, true> : kv8_attend_kernel<kInt8, false>);
+  const int grid = (int)std::max(
+      1LL, std::min<long long>(kv8_attend_ctas(num_sms),
+                               std::max(most, (long long)s.batch * p.rows)));
+  const bool teams = (long long)s.batch * p.rows > grid;
+  auto kernel = kv8_attend_kernel<kInt8, false, false>;
+  if (c.format == kE4m3) {
+    if (kept) kernel = teams ? kv8_attend_kernel<kE4m3, true, true> : kv8_attend_kernel<kE4m3, true, false>;
+    else kernel = teams ? kv8_attend_kernel<kE4m3, false, true> : kv8_attend_kernel<kE4m3, false, false>;
+  } else {
+    if (kept) kernel = teams ? kv8_attend_kernel<kInt8, true, true> : kv8_attend_kernel<kInt8, true, false>;
+    else kernel = teams ? kv8_attend_kernel<kInt8, false, true> : kv8_attend_kernel<kInt8, false, false>;
+  }
   const size_t smem = smem_bytes(s.batch);
   const cudaError_t e = set_kernel_smem(kernel, smem);
   if (e != cudaSuccess) return e;

@@ -182,6 +182,36 @@ def test_dense_decode(fmt, hq, hkv, lens):
             assert_rows(out[b, rows], lse[b, rows], want, wl, tol)
 
 
+@pytest.mark.parametrize("hq,hkv,lens", [
+    (4, 1, [1 + i % 20 for i in range(300)]),            # a warp a row
+    (6, 2, [10 + (i * 13) % 330 for i in range(170)]),   # four warps a row
+    (2, 1, [17] * 160 + [6000, 0, 3]),                   # a CTA for them all, the long row cut
+])
+@pytest.mark.parametrize("kept", [False, True])
+def test_decode_of_more_rows_than_ctas(hq, hkv, lens, kept):
+    s = Batch(lens, hq, hkv, "e4m3", seed=hq)
+    q = bf16(s.rng.standard_normal((len(lens), hq, D)))
+    args, kw = None, {}
+    if kept:
+        idx = np.tile(np.array([0, 1, 5], np.int32), (len(lens), hkv, 1))
+        cnt = np.full((len(lens), hkv), 3, np.int32)
+        args, kw = (torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda()), dict(
+            sink=3, window=9, k2=3)
+    out, lse = run_decode(s, q, args, **kw)
+    g = hq // hkv
+    for b in list(range(0, len(lens), 17)) + [len(lens) - 3, len(lens) - 2, len(lens) - 1]:
+        n = lens[b]
+        t = np.arange(n)
+        seen = np.ones(n, bool)
+        if kept:
+            seen = (t < 3) | (t >= n - 9) | np.isin(t // PAGE, [0, 1, 5])
+        for h in range(hkv):
+            rows = slice(h * g, (h + 1) * g)
+            k, v = (O.values(s.cache, w, s.table[b], n, h) for w in "kv")
+            want, wl, tol = O.attend(q[b, rows], k, v, np.tile(seen, (g, 1)), D ** -0.5)
+            assert_rows(out[b, rows], lse[b, rows], want, wl, tol)
+
+
 def test_dense_decode_of_extreme_queries_and_scale():
     """Queries from 2^-40 to 2^30 in one group (the fp16 operands carry a power of two a head),
     zero queries, a given softmax scale, logits far apart."""
