@@ -45,6 +45,7 @@ constexpr int kThreads = 640;  // five warpgroups; the last is warp 16 and three
 constexpr int kSoftmaxRegs = 136, kConvertRegs = 80, kMmaRegs = 48;
 static_assert(2 * kSoftmaxRegs + 2 * kConvertRegs + kMmaRegs == 5 * 96, "the launch's registers");
 static_assert(kConvertWarps == kTilePages, "a warp converts one block of K and of V a step");
+constexpr float kPartCost = 1.3f;  // us
 constexpr int kPageRing = 4;
 constexpr int kBlockCost = 4;  // what a row block costs beside its tiles, in tiles (see Walk)
 constexpr float kHeadroom = 10.0f;
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
 
   // ---- the line of all steps; warp 0 finds where this CTA's slice begins
   if (warp == 0) {
-    long long sum = 0;
+    long long sum = 0, all_blocks = 0;
     for (int b0 = 0; b0 < batch; b0 += 32) {
       const int b = b0 + lane;
       NewSpan sp = {0, 0, 0, false};
@@ -300,10 +301,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       }
       if (b < batch) pre[b + 1] = sum + incl;
       sum += __shfl_sync(0xffffffffu, incl, 31);
+      all_blocks += (long long)__reduce_add_sync(0xffffffffu, blocks) * p.hkv;
     }
     if (lane == 0) pre[0] = 0;
     __syncwarp();
-    const long long per = max((sum + gridDim.x - 1) / gridDim.x, 2LL);
+    // Equal slices, but none so short that joining costs more than it saves: a step is 1.9 us, a
+    // further part of a row block kPartCost in the joining CTA, so with t tiles a block slices of
+    // t' have the least of 1.9 t' + kPartCost t / t'.
+    const float mean = all_blocks > 0 ? (float)sum / all_blocks : 0.0f;
+    const long long per = max((sum + gridDim.x - 1) / gridDim.x,
+                              max((long long)(sqrtf(kPartCost / 1.9f * mean) + 0.5f), 2LL));
     const long long begin = min(blockIdx.x * per, sum);
     if (lane == 0) sm.per = per;
     if (begin < sum) {
