@@ -31,9 +31,10 @@
 // and the last CTA to arrive joins them in slice order (the result does not depend on which one
 // that is).
 //
-// Measured (GB300, copy 6.8 TB/s; 32 query heads over 8): 8 x 32-128K tokens, groups of 8,
-// int8: 222 us, 6.35 TB/s; one sequence of 128K tokens: 53 us, 5.05 TB/s, of which about 7 us
-// pass before the first blocks are there everywhere and 5 us in joining; 8K tokens: 12 us.
+// Measured (GB300, copy 6.8 TB/s; 8 kv heads): 8 x 32-128K tokens, groups of 8, int8: 224 us,
+// 6.3 TB/s; one sequence of 128K tokens, groups of 4: 51-53 us, 5.1 TB/s (a further byte costs
+// 1 / 7.0 TB/s; about 7 us pass before the first blocks are there everywhere and 5 us in
+// joining); 8K tokens: 12 us; 128 kept blocks, sink and window of 128K: 11.8 us.
 #include "kv8.cuh"
 
 #include <cmath>

@@ -9,6 +9,10 @@
 // values a lane, which stay in registers between the maximum and the codes, so the input is
 // read once and no shared memory or second launch is needed. Sequences share nothing, so any
 // block of any sequence is one work item (new_block_items) and ragged batches balance.
+//
+// Measured (GB300, copy 6.8 TB/s, 8 kv heads): 108K new tokens of 8 prompts written in 108 us
+// (664 MB, 6.1 TB/s), 117K tokens read back in 109 us (720 MB, 6.6 TB/s); one token of one
+// sequence written in 2.3 us, of 256 sequences in 3.7, 1024 tokens read in 2.9.
 #include "append.cuh"
 #include "kv8.cuh"
 

@@ -22,6 +22,13 @@
 // Work. All steps (row block, token tile) of all sequences and heads form one line, cut into
 // equal slices, one CTA each, as in the decode attention; parts of a row block meet in the
 // workspace.
+//
+// Measured (GB300, 1884 TFLOP/s bf16 burst, 1693 sustained; 32 query heads over 8): 2048 tokens
+// behind 30K 785 us, 1360 TFLOP/s; an 8K prompt 470 us, 1170 TFLOP/s of what its rows see (a
+// diagonal tile is computed whole); 4 x 7-24 tokens behind 6-12K 44 us. A step's products take
+// 2048 cycles, a step 3750: each tile's way from S over the softmax (2300) and P V to its next S
+// is one chain, and two tiles overlap it only in part. Instructions: 1990 a step and scheduler,
+// half its slots (softmax 1300, conversion 580).
 #include "kv8.cuh"
 #include "tcgen05.cuh"
 
