@@ -428,11 +428,13 @@ def _rows(name: str, t, heads: int):
 
 def _row_pair(name: str, k, v, heads: int):
     """(rows, k's row stride, v's) of two such tensors of as many rows."""
-    rows, k_stride = _rows(name, k, heads)
-    v_rows, v_stride = _rows(name, v, heads)
-    if v_rows != rows:
-        raise HsaError(name, HSA_ERR_INVALID_ARG, "k and v differ in rows")
-    return rows, k_stride, v_stride
+    shape, ks, vs = k.shape, k.stride(), v.stride()
+    if (k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or shape != v.shape or
+            len(ks) != 3 or shape[1] != heads or shape[2] != 128 or ks[2] != 1 or vs[2] != 1 or
+            (heads > 1 and (ks[1] != 128 or vs[1] != 128))):
+        raise HsaError(name, HSA_ERR_INVALID_ARG,
+                       "k and v must be bf16 [tokens][heads][128], of as many rows")
+    return shape[0], ks[0], vs[0]
 
 
 def hsa_kv8_write(d: Dims, cache: KV8, k_new, v_new, cu_tokens, page_table, seq_lens, ws=None,
