@@ -103,17 +103,16 @@ class Dims:
 
     def c(self) -> hsa_dims:
         """The C struct, built once per set of field values (every call of a step passes it)."""
-        key = tuple(self.__dict__.values())
+        key = (self.batch, self.hq, self.hkv, self.head_dim, self.page_size,
+               self.max_pages_per_seq, self.num_pages, self.chunk, self.block, self.k1,
+               self.k2, self.sink, self.window, float(self.sm_scale),
+               1 if self.kv_on_host else 0, self.chunk0, self.k0, self.key_bits, self.per_head,
+               self.key_fp8, self.cache_policy)
         c = _DIMS_CACHE.get(key)
         if c is None:
             if len(_DIMS_CACHE) > 256:
                 _DIMS_CACHE.clear()
-            c = _DIMS_CACHE[key] = hsa_dims(
-                self.batch, self.hq, self.hkv, self.head_dim, self.page_size,
-                self.max_pages_per_seq, self.num_pages, self.chunk, self.block, self.k1,
-                self.k2, self.sink, self.window, float(self.sm_scale),
-                1 if self.kv_on_host else 0, self.chunk0, self.k0, self.key_bits, self.per_head,
-                self.key_fp8, self.cache_policy)
+            c = _DIMS_CACHE[key] = hsa_dims(*key)
         return c
 
 
