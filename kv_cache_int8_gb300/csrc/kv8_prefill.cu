@@ -14,7 +14,7 @@
 //
 // Layout. 256 rows (a kv head's group of query heads x 256 / group tokens) as two tiles of 128
 // against tiles of 128 tokens. Warps 0-3 and 4-7: one row a thread, softmax of tile 0 and 1;
-// warps 8-11 turn the codes into swizzled fp16 tiles (two buffers of K and of V); warp 12 issues
+// warps 8-15 turn the codes into swizzled fp16 tiles (two buffers of K and of V); warp 16 issues
 // the products. While one tile's scores are in the softmax, the tensor cores work on the other
 // tile. TMEM: S0 S1 O0 O1, 128 columns each; P overwrites its S (a product that reads P is
 // issued before the product that overwrites it, and they run in order).
@@ -265,9 +265,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     sm.dead = 0;
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) tc::alloc(&sm.tmem, 512);
+  // TMEM is taken once the kernels in front are done and before the next one may start: whichever
+  // of two kernels holds it on an SM never waits for the other.
   grid_dep_wait();
-  grid_dep_launch();
+  if (warp == kMmaWarp) tc::alloc(&sm.tmem, 512);
 
   // ---- the line of all steps; warp 0 finds where this CTA's slice begins
   if (warp == 0) {
@@ -275,7 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     for (int b0 = 0; b0 < batch; b0 += 32) {
       const int b = b0 + lane;
       NewSpan sp = {0, 0, 0, false};
-      int blocks = 0, tiles = 0;  // tiles: places of the sequence's row blocks under one head
+      int blocks = 0;
+      long long tiles = 0;  // places of the sequence's row blocks under one head
       if (b < batch) {
         sp = new_span(p.rows, b);
         if (sp.bad) set_error(p.err, kDevErrCheck);
@@ -293,14 +295,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         const int n = __shfl_sync(0xffffffffu, sp.n, from);
         const int l = __shfl_sync(0xffffffffu, sp.start, from) + n;
         const int bl = __shfl_sync(0xffffffffu, blocks, from);
-        int t = 0;
+        long long t = 0;
         for (int q = lane; q < bl; q += 32)
           t += block_tiles(l, n, p.block_tokens, q) + kBlockCost;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
         if (lane == from) tiles = t;
       }
-      long long incl = (long long)tiles * p.hkv;
+      long long incl = tiles * p.hkv;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const long long v = __shfl_up_sync(0xffffffffu, incl, d);
@@ -328,15 +330,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         else hi = mid;
       }
       const int b = lo;
-      const unsigned tiles = (unsigned)((pre[b + 1] - pre[b]) / p.hkv);
+      const long long tiles = (pre[b + 1] - pre[b]) / p.hkv;
       const long long at = begin - pre[b];
       const int h = (int)(at / tiles);
-      unsigned rem = (unsigned)(at - (long long)h * tiles);
+      long long rem = at - h * tiles;
       const int blocks = (num[b] + p.block_tokens - 1) / p.block_tokens;
       int q0 = 0;
       for (;; q0 += 32) {  // the block that holds place `rem`
         const int q = q0 + lane;
-        const unsigned t =
+        const unsigned t =  // 32 blocks' places: at most 2^28
             q < blocks ? block_tiles(len[b], num[b], p.block_tokens, q) + kBlockCost : 0;
         unsigned incl = t;
 #pragma unroll
@@ -362,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
+  grid_dep_launch();
   const uint32_t tmem = sm.tmem;
   const long long per = sm.per, all = pre[batch];
   const long long begin = min(blockIdx.x * per, all), end = min(begin + per, all);
