@@ -449,7 +449,8 @@ int32_t hsa_kv8_read(const hsa_dims* d, const hsa_kv8* cache, void* k_out, int64
 /*
  * dense_decode over the 8-bit cache: one query token a sequence, q bf16 [batch][hq][128],
  * attends every token [0, N_b). out f32 [batch][hq][128], lse f32 [batch][hq] (nullable). A
- * sequence of no tokens gives 0 and lse -inf. Needs the HSA_OP_KV8_DECODE workspace.
+ * sequence of no tokens gives 0 and lse -inf; a head whose query is not finite gives NaN (so do
+ * the other attentions). Needs the HSA_OP_KV8_DECODE workspace.
  */
 int32_t hsa_kv8_decode(const hsa_dims* d, const hsa_kv8* cache, const void* q,
                        const int32_t* page_table, const int32_t* seq_lens, float* out,

@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int h = 0; h < 2; h++) {
         if (2 * t + h >= p.group) continue;
         const float l = h ? l1 : l0;
-        const float r = l > 0.0f ? 1.0f / l : 0.0f;
+        const float r = l != 0.0f ? 1.0f / l : 0.0f;
         float4* dst = reinterpret_cast<float4*>(p.out + (head + h) * kHeadDim + 16 * g);
 #pragma unroll
         for (int k = 0; k < 8; k += 2)
@@ -697,11 +697,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ch = 16 * (hl >> 2) + 2 * (i >> 6) + (i & 1);
         const bool sums = p.lse != nullptr && i < 8 && (i & 1) == 0;
         if (2 * ht < p.group) {
-          p.out[head * kHeadDim + ch] = ta.y > 0.0f ? acc.x / ta.y : 0.0f;
+          p.out[head * kHeadDim + ch] = ta.y != 0.0f ? acc.x / ta.y : 0.0f;
           if (sums) p.lse[head] = (ta.x - kHeadroom + log2f(ta.y)) * 0.693147180559945309f;
         }
         if (2 * ht + 1 < p.group) {
-          p.out[(head + 1) * kHeadDim + ch] = tb.y > 0.0f ? acc.y / tb.y : 0.0f;
+          p.out[(head + 1) * kHeadDim + ch] = tb.y != 0.0f ? acc.y / tb.y : 0.0f;
           if (sums) p.lse[head + 1] = (tb.x - kHeadroom + log2f(tb.y)) * 0.693147180559945309f;
         }
       }
@@ -784,11 +784,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ch = 16 * (hl >> 2) + 2 * (tid >> 6) + (tid & 1);
       const bool sums = p.lse != nullptr && tid < 8 && (tid & 1) == 0;
       if (2 * ht < p.group) {
-        p.out[head * kHeadDim + ch] = ta.y > 0.0f ? acc.x / ta.y : 0.0f;
+        p.out[head * kHeadDim + ch] = ta.y != 0.0f ? acc.x / ta.y : 0.0f;
         if (sums) p.lse[head] = (ta.x - kHeadroom + log2f(ta.y)) * 0.693147180559945309f;
       }
       if (2 * ht + 1 < p.group) {
-        p.out[(head + 1) * kHeadDim + ch] = tb.y > 0.0f ? acc.y / tb.y : 0.0f;
+        p.out[(head + 1) * kHeadDim + ch] = tb.y != 0.0f ? acc.y / tb.y : 0.0f;
         if (sums) p.lse[head + 1] = (tb.x - kHeadroom + log2f(tb.y)) * 0.693147180559945309f;
       }
     }

@@ -655,3 +655,30 @@ def test_unlimited_sink_and_window_see_everything():
         # the same products, at most 40 sums in another order: 40 * 2^-24 * max |v| (4.5)
         np.testing.assert_allclose(out, dense, rtol=0, atol=1.1e-5)
         np.testing.assert_allclose(lse, dense_lse, rtol=0, atol=1.1e-5)
+
+
+@pytest.mark.parametrize("hq,hkv,lens", [
+    (4, 2, [1, 20, 5000]),                               # CTAs share rows
+    (4, 1, [1 + i % 20 for i in range(300)]),            # a warp a row
+    (4, 2, [10 + (i * 13) % 330 for i in range(170)]),   # four warps a row
+])
+def test_queries_that_are_not_finite_stay_in_their_rows(hq, hkv, lens):
+    """A NaN or an infinity in a query head makes that head's results NaN, however the rows are
+    shared out, and no other's."""
+    s = Batch(lens, hq, hkv, "int8", seed=17)
+    q = bf16(s.rng.standard_normal((len(lens), hq, D)))
+    q[0, 1, 7], q[2, 3, 100], q[-1, 0, 0] = np.nan, np.inf, -np.inf
+    bad = ~np.isfinite(q).all(-1)
+    out, lse = run_decode(s, q)
+    rows, row_lse = run_prefill(s, q, [1] * len(lens))
+    for o, l in ((out, lse), (rows, row_lse)):
+        np.testing.assert_array_equal(np.isnan(o).any(-1), bad)
+        np.testing.assert_array_equal(np.isnan(l), bad)
+    g = hq // hkv
+    for b in (0, 2, len(lens) - 1):
+        for j in range(hq):
+            if not bad[b, j]:
+                k, v = (O.values(s.cache, w, s.table[b], lens[b], j // g) for w in "kv")
+                want, wl, tol = O.attend(q[b, j:j + 1], k, v, np.ones((1, lens[b]), bool),
+                                         D ** -0.5)
+                assert_rows(out[b, j:j + 1], lse[b, j:j + 1], want, wl, tol)
