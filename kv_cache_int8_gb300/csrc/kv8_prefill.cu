@@ -58,6 +58,8 @@ constexpr int kBlockCost = 4;  // what a row block costs beside its tiles, in ti
 constexpr float kHeadroom = 10.0f;
 constexpr float kLag = 4.0f;
 constexpr float kTiny = 1e-37f;  // scales of scores are at least that: a masked -inf stays one
+// s_full and p_full of the tiles and, where a row block has one tile, of its odd steps
+constexpr int kOdd = 2;
 constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns; tile i at + 128 i
 
 struct Params {
@@ -85,8 +87,8 @@ struct Smem {
   unsigned char v[2][kTileBytes];
   // log2 s_v, 1 / s_v, s_k of a step's blocks (x and y are read alone, as an aligned pair)
   float4 page[kPageRing][kTilePages];
-  alignas(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2],
-      p_full[2][2], o_full[2];  // p_full[tile][half of the step's tokens]
+  alignas(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[3],
+      p_full[3][2], o_full[2], pv_done;  // s_full, p_full: kOdd; p_full[..][half of the tokens]
   long long per;
   int start_b, start_h, start_q, start_off;
   uint32_t tmem;
@@ -262,6 +264,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       mbar_init(&sm.p_full[i][1], 128);
       mbar_init(&sm.o_full[i], 1);
     }
+    mbar_init(&sm.s_full[kOdd], 1);
+    mbar_init(&sm.p_full[kOdd][0], 128);
+    mbar_init(&sm.p_full[kOdd][1], 128);
+    mbar_init(&sm.pv_done, 1);
     sm.dead = 0;
     fence_barrier_init();
   }
@@ -377,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     // ================================================= softmax: one row a thread
     const int tile = warp >> 2, r = tid & 127, row = tile * 128 + r;
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
-    const uint32_t s_col = at + kColS + 128 * tile, o_col = at + kColO + 128 * tile;
-    uint32_t s_phase = 0, o_phase = 0;
+    const uint32_t o_col = at + kColO + 128 * tile;
+    uint32_t s_phase = 0, odd_phase = 0, o_phase = 0, pv_phase = 0;
     int step = 0;  // steps of all pieces so far (the ring of scales)
     // After a wait that ran out a warp goes on through the pieces without work: the barriers of
     // a tile's four warps must find all of them.
@@ -396,7 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           p.lse[(size_t)first * p.hq + i] = -INFINITY;
     }
     while (walk.next(pc)) {
-      if (tile * 128 >= pc.rows) {
+      const bool two = pc.rows > 128;
+      if (tile == 1 && !two) {
         step += pc.tiles;
         continue;
       }
@@ -445,11 +452,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; !failed && j < pc.tiles; j++, step++) {
         const int base = (pc.tile + j) * kTokens;
-        if (!wait(sm, &sm.s_full[tile], s_phase, p.err)) {
+        const bool odd = !two && (j & 1);  // one tile: its S and P alternate between the buffers
+        const uint32_t s_col = at + kColS + 128 * (odd ? 1 : tile);
+        if (!wait(sm, &sm.s_full[odd ? kOdd : tile], odd ? odd_phase : s_phase, p.err)) {
           failed = true;
           break;
         }
-        s_phase ^= 1;
+        if (odd) odd_phase ^= 1;
+        else s_phase ^= 1;
         tc::fence_after();
         const float4* page = sm.page[step % kPageRing];
         const int limit = pos - base;  // columns up to it are seen
@@ -491,6 +501,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           m = top;
           l *= by;
           if (j > 0) {
+            if (!two) {  // its S came before the step in front had been added up
+              if (!wait(sm, &sm.pv_done, pv_phase ^ ((j - 1) & 1), p.err)) {
+                failed = true;
+                break;
+              }
+              tc::fence_after();
+            }
 #pragma unroll 1
             for (int c = 0; c < 8; c++) {
               uint32_t o[16];
@@ -529,9 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           tc::store32(s_col + c * 32, w);
           tc::wait_st();
           tc::fence_before();
-          mbar_arrive(&sm.p_full[tile][c]);
+          mbar_arrive(&sm.p_full[odd ? kOdd : tile][c]);
         }
       }
+      if (!two) pv_phase ^= (pc.tiles - 1) & 1;
       // ---- the result
       if (!wait(sm, &sm.o_full[tile], o_phase, p.err)) failed = true;
       o_phase ^= 1;
@@ -761,27 +779,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     const uint32_t v_low = tc::desc_low(smem_addr(sm.v[0]), kHalfBytes);
     const bool lead = tc::elect();
     int step = 0;
-    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, odd_phase = 0;
     bool ok = true;
-    // S of tile i against the K tile of step `at`
-    auto scores = [&](int i, int at) {
+    // S of tile i against the K tile of step `at`, into buffer `buf`
+    auto scores = [&](int i, int buf, int at, uint64_t* full) {
       if (lead) {
         const uint32_t q = q_low + i * (kTileBytes >> 4), k = k_low + (at & 1) * (kTileBytes >> 4);
 #pragma unroll
         for (int c = 0; c < 8; c++) {
           const uint32_t off = ((c >> 2) * kHalfBytes + (c & 3) * 32) >> 4;
-          tc::mma_ss<kQk>(tmem + kColS + 128 * i, q + off, k + off, c > 0);
+          tc::mma_ss<kQk>(tmem + kColS + 128 * buf, q + off, k + off, c > 0);
         }
-        tc::commit(&sm.s_full[i]);
+        tc::commit(full);
       }
     };
-    // O of tile i += P V of half h of step `at`
-    auto values = [&](int i, int h, int at, bool add) {
+    // O of tile i += P V of half h of step `at`, P in buffer `buf`
+    auto values = [&](int i, int buf, int h, int at, bool add) {
       if (lead) {
         const uint32_t v = v_low + (at & 1) * (kTileBytes >> 4);
 #pragma unroll
         for (int c = 4 * h; c < 4 * h + 4; c++)
-          tc::mma_ts<kPv>(tmem + kColO + 128 * i, tmem + kColS + 128 * i + c * 8,
+          tc::mma_ts<kPv>(tmem + kColO + 128 * i, tmem + kColS + 128 * buf + c * 8,
                           v + c * (2048 >> 4), add || c > 0);
       }
     };
@@ -795,11 +813,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         if (!ok) continue;
         q_phase[i] ^= 1;
         tc::fence_after();
-        scores(i, step);
+        scores(i, i, step, &sm.s_full[i]);
       }
       if (!ok) break;
       if (lead) tc::commit(&sm.k_empty[step & 1]);
-      for (int j = 0; ok && j < pc.tiles; j++, step++) {
+      // One tile: the next step's scores go into the other tile's buffer of S while this step's
+      // are in the softmax, which then never waits for them (pv_done: see there).
+      for (int j = 0; ok && !two && j < pc.tiles; j++, step++) {
+        const bool more = j + 1 < pc.tiles;
+        const int buf = j & 1;
+        if (more) {
+          ok = wait(sm, &sm.k_full[(step + 1) & 1], ((step + 1) >> 1) & 1, p.err);
+          if (!ok) break;
+          tc::fence_after();
+          scores(0, buf ^ 1, step + 1, &sm.s_full[buf ? 0 : kOdd]);
+          if (lead) tc::commit(&sm.k_empty[(step + 1) & 1]);
+        }
+        ok = wait(sm, &sm.v_full[step & 1], (step >> 1) & 1, p.err);
+        uint64_t* const full = sm.p_full[buf ? kOdd : 0];
+        const uint32_t phase = buf ? odd_phase : p_phase[0];
+        if (ok) ok = wait(sm, full, phase, p.err);
+        if (!ok) break;
+        tc::fence_after();
+        values(0, buf, 0, step, j > 0);
+        ok = wait(sm, full + 1, phase, p.err);
+        if (!ok) break;
+        if (buf) odd_phase ^= 1;
+        else p_phase[0] ^= 1;
+        tc::fence_after();
+        values(0, buf, 1, step, true);
+        if (lead) {
+          tc::commit(more ? &sm.pv_done : &sm.o_full[0]);
+          tc::commit(&sm.v_empty[step & 1]);
+        }
+        __syncwarp();
+      }
+      for (int j = 0; ok && two && j < pc.tiles; j++, step++) {
         const bool more = j + 1 < pc.tiles;
         ok = wait(sm, &sm.v_full[step & 1], (step >> 1) & 1, p.err);
         if (ok && more) ok = wait(sm, &sm.k_full[(step + 1) & 1], ((step + 1) >> 1) & 1, p.err);
@@ -809,13 +858,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           ok = wait(sm, &sm.p_full[i][0], p_phase[i], p.err);
           if (!ok) continue;
           tc::fence_after();
-          values(i, 0, step, j > 0);
+          values(i, i, 0, step, j > 0);
           ok = wait(sm, &sm.p_full[i][1], p_phase[i], p.err);
           if (!ok) continue;
           p_phase[i] ^= 1;
           tc::fence_after();
-          values(i, 1, step, true);
-          if (more) scores(i, step + 1);
+          values(i, i, 1, step, true);
+          if (more) scores(i, i, step + 1, &sm.s_full[i]);
           else if (lead) tc::commit(&sm.o_full[i]);
         }
         if (ok && lead) {
