@@ -23,12 +23,18 @@
 // equal slices, one CTA each, as in the decode attention; parts of a row block meet in the
 // workspace.
 //
+// A row block of one tile (up to 128 rows) takes the buffers of S in turn, so its softmax finds
+// the next step's scores ready: a step 1.55 us instead of 1.9 (16 tokens over 128K, 8 heads over
+// one: 89 -> 76 us).
+//
 // Measured (GB300, 1884 TFLOP/s bf16 burst, 1693 sustained; 32 query heads over 8): 2048 tokens
-// behind 30K 785 us, 1360 TFLOP/s; an 8K prompt 470 us, 1170 TFLOP/s of what its rows see (a
-// diagonal tile is computed whole); 4 x 7-24 tokens behind 6-12K 44 us. A step's products take
-// 2048 cycles, a step 3750: each tile's way from S over the softmax (2300) and P V to its next S
-// is one chain, and two tiles overlap it only in part. Instructions: 1990 a step and scheduler,
-// half its slots (softmax 1300, conversion 580).
+// behind 30K 766 us, 1390 TFLOP/s; an 8K prompt 465 us, 1185 TFLOP/s of what its rows see (a
+// diagonal tile is computed whole); 4 x 7-24 tokens behind 6-12K 40 us. A step's products take
+// 2048 cycles, a step 3650: each tile's way from S over the softmax and P V to its next S is one
+// chain, and two tiles overlap it only in part. Instructions: 1940 a step and scheduler, half its
+// slots (1/3 of them the conversion). With registers to spare nothing changes (144 / 80 / 32 and
+// 136 / 88 / 32 instead of 136 / 80 / 48: 765-775, 466-471, 40 us); queries loaded two rows an
+// instruction instead of a row a thread: 767, 468, 40.
 #include "kv8.cuh"
 #include "tcgen05.cuh"
 
@@ -464,34 +470,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         const float4* page = sm.page[step % kPageRing];
         const int limit = pos - base;  // columns up to it are seen
         // ---- the row's maximum, 64 columns at a time
+        const bool masked = base + kTokens - 1 > first_pos;
         auto scores = [&](int c, uint32_t (&s)[2][32]) {
           tc::load32(s_col + c * 64, s[0]);
           tc::load32(s_col + c * 64 + 32, s[1]);
           tc::wait_ld();
-          if (base + c * 64 + 63 > first_pos) {
+          if (masked) {
 #pragma unroll
             for (int k = 0; k < 64; k++)
               if (c * 64 + k > limit) s[k >> 5][k & 31] = 0xFF800000u;
           }
         };
         float top = -INFINITY;
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < 2; c++) {
           uint32_t s[2][32];
-          scores(c, s);
+          float of[4];  // the blocks' largest scores
+          if (!masked) {  // the load's own maxima (in 64 instructions here: chunk 792 us, not
+                          // 765; 8K prompt 480, not 465)
+#pragma unroll
+            for (int g = 0; g < 4; g++)
+              tc::load16_max(s_col + c * 64 + g * 16, &s[g >> 1][16 * (g & 1)], of[g]);
+            tc::wait_ld();
+          } else {
+            scores(c, s);
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+              const uint32_t* v = &s[g >> 1][16 * (g & 1)];
+              float a = __uint_as_float(v[0]);
+#pragma unroll
+              for (int k = 1; k < 15; k += 2)
+                a = max3(a, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+              of[g] = fmaxf(a, __uint_as_float(v[15]));
+            }
+          }
 #pragma unroll
           for (int g = 0; g < 4; g++) {
-            const uint32_t* v = &s[g >> 1][16 * (g & 1)];
-            float a = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
-            float b = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
-#pragma unroll
-            for (int k = 6; k < 14; k += 4) {
-              a = max3(a, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-              b = max3(b, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
-            }
-            a = max3(a, __uint_as_float(v[14]), __uint_as_float(v[15]));
             const float4 pg = page[4 * c + g];
-            top = fmaxf(top, fmaf(fmaxf(a, b), fmaxf(f * pg.z, kTiny), pg.x));
+            top = fmaxf(top, fmaf(of[g], fmaxf(f * pg.z, kTiny), pg.x));
           }
         }
         // ---- the accumulator follows a maximum that has grown by more than kLag

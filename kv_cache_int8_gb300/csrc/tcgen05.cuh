@@ -106,6 +106,16 @@ __device__ __forceinline__ void load16(uint32_t addr, uint32_t (&r)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
 }
+// The same 16 columns with each lane's largest of them (as floats; NaN does not count).
+__device__ __forceinline__ void load16_max(uint32_t addr, uint32_t* r, float& top) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9,"
+      " %10, %11, %12, %13, %14, %15}, %16, [%17];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=f"(top)
+      : "r"(addr));
+}
 __device__ __forceinline__ void load32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11,"

@@ -682,3 +682,19 @@ def test_queries_that_are_not_finite_stay_in_their_rows(hq, hkv, lens):
                 want, wl, tol = O.attend(q[b, j:j + 1], k, v, np.ones((1, lens[b]), bool),
                                          D ** -0.5)
                 assert_rows(out[b, j:j + 1], lse[b, j:j + 1], want, wl, tol)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_prefill_where_one_token_takes_everything(fmt):
+    """Each query's weight lies on one token, at any place of a tile: a maximum that misses it
+    would push its probability out of fp16."""
+    n, m = 700, 260
+    s = Batch([n], 4, 1, fmt, seed=18)
+    k = O.values(s.cache, "k", s.table[0], n, 0)
+    q = np.empty((m, 4, D), np.float32)
+    for i in range(m):
+        for j in range(4):
+            q[i, j] = 40.0 * k[(37 * i + 131 * j) % (n - m + i + 1)]
+    q = bf16(q)
+    out, lse = run_prefill(s, q, [m])
+    check_prefill(s, q, [m], out, lse)
