@@ -8,9 +8,10 @@
 // blocks' scales (16 tokens) are applied in fp32: with row factor f = sm_scale log2 e 2^-shift,
 //   y_t = f s_k S_t + log2 s_v,   out = sum_t 2^(y_t - M) c_t / sum_t 2^(y_t - M) / s_v
 // so V's scale costs nothing but the offset of an exponent that is computed anyway, and the sum
-// takes one multiplication a block. P = 2^(y - M + 10) is rounded to fp16 (11 bits, against 8
-// of the bf16 result); M lags the running maximum by at most 4, so the output accumulator is
-// rarely rescaled.
+// takes one multiplication a block. P = 2^(y - M + 7) is rounded to fp16 (11 bits, against 8
+// of the bf16 result); M lags the running maximum by at most 8, so the output accumulator is
+// rarely rescaled (with 10 and 4: 2048 tokens behind 30K 767 us, not 756; 8K prompt 465, not
+// 443).
 //
 // Layout. 256 rows (a kv head's group of query heads x 256 / group tokens) as two tiles of 128
 // against tiles of 128 tokens. Warps 0-3 and 4-7: one row a thread, softmax of tile 0 and 1;
@@ -28,7 +29,7 @@
 // one: 89 -> 76 us).
 //
 // Measured (GB300, 1884 TFLOP/s bf16 burst, 1693 sustained; 32 query heads over 8): 2048 tokens
-// behind 30K 766 us, 1390 TFLOP/s; an 8K prompt 465 us, 1185 TFLOP/s of what its rows see (a
+// behind 30K 756 us, 1410 TFLOP/s; an 8K prompt 443-450 us, 1240 TFLOP/s of what its rows see (a
 // diagonal tile is computed whole); 4 x 7-24 tokens behind 6-12K 40 us. A step's products take
 // 2048 cycles, a step 3650: each tile's way from S over the softmax and P V to its next S is one
 // chain, and two tiles overlap it only in part. Instructions: 1940 a step and scheduler, half its
@@ -61,8 +62,11 @@ static_assert(kConvertWarps == kTilePages, "a warp converts one block of K and o
 constexpr float kPartCost = 1.3f;  // us
 constexpr int kPageRing = 4;
 constexpr int kBlockCost = 4;  // what a row block costs beside its tiles, in tiles (see Walk)
-constexpr float kHeadroom = 10.0f;
-constexpr float kLag = 4.0f;
+// P = 2^(y - M + kHeadroom), y - M up to kLag: at most 2^15. A smaller headroom leaves small
+// probabilities in fp16's subnormals, 2^-25 off each: 2^20 tokens off the same way and together
+// as heavy as the largest make 2^-5 of 2^7, 2^-12 of the result (bf16 rounds it to 2^-9).
+constexpr float kHeadroom = 7.0f;
+constexpr float kLag = 8.0f;
 constexpr float kTiny = 1e-37f;  // scales of scores are at least that: a masked -inf stays one
 // s_full and p_full of the tiles and, where a row block has one tile, of its odd steps
 constexpr int kOdd = 2;
