@@ -29,9 +29,9 @@
 // one: 89 -> 76 us).
 //
 // Measured (GB300, 1884 TFLOP/s bf16 burst, 1693 sustained; 32 query heads over 8): 2048 tokens
-// behind 30K 756 us, 1410 TFLOP/s; an 8K prompt 443-450 us, 1240 TFLOP/s of what its rows see (a
-// diagonal tile is computed whole); 4 x 7-24 tokens behind 6-12K 40 us. A step's products take
-// 2048 cycles, a step 3650: each tile's way from S over the softmax and P V to its next S is one
+// behind 30K 745-758 us, 1410 TFLOP/s; an 8K prompt 430-444 us, 1240 TFLOP/s of what its rows see
+// (a diagonal tile is computed whole); 4 x 7-24 tokens behind 6-12K 39 us. A step's products take
+// 2048 cycles, a step 3600: each tile's way from S over the softmax and P V to its next S is one
 // chain, and two tiles overlap it only in part. Instructions: 1940 a step and scheduler, half its
 // slots (1/3 of them the conversion). With registers to spare nothing changes (144 / 80 / 32 and
 // 136 / 88 / 32 instead of 136 / 80 / 48: 765-775, 466-471, 40 us); queries loaded two rows an
@@ -98,7 +98,8 @@ struct Smem {
   // log2 s_v, 1 / s_v, s_k of a step's blocks (x and y are read alone, as an aligned pair)
   float4 page[kPageRing][kTilePages];
   alignas(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[3],
-      p_full[3][2], o_full[2], pv_done;  // s_full, p_full: kOdd; p_full[..][half of the tokens]
+      p_full[3][2], o_full[2];  // s_full, p_full: kOdd; p_full[..][half of the tokens]
+  uint64_t pv_done, h_done[2];  // products with V complete: one tile's step, a first half
   long long per;
   int start_b, start_h, start_q, start_off;
   uint32_t tmem;
@@ -273,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       mbar_init(&sm.p_full[i][0], 128);
       mbar_init(&sm.p_full[i][1], 128);
       mbar_init(&sm.o_full[i], 1);
+      mbar_init(&sm.h_done[i], 1);
     }
     mbar_init(&sm.s_full[kOdd], 1);
     mbar_init(&sm.p_full[kOdd][0], 128);
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     const int tile = warp >> 2, r = tid & 127, row = tile * 128 + r;
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
     const uint32_t o_col = at + kColO + 128 * tile;
-    uint32_t s_phase = 0, odd_phase = 0, o_phase = 0, pv_phase = 0;
+    uint32_t s_phase = 0, odd_phase = 0, o_phase = 0, pv_phase = 0, h_phase = 0;
     int step = 0;  // steps of all pieces so far (the ring of scales)
     // After a wait that ran out a warp goes on through the pieces without work: the barriers of
     // a tile's four warps must find all of them.
@@ -473,7 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         tc::fence_after();
         const float4* page = sm.page[step % kPageRing];
         const int limit = pos - base;  // columns up to it are seen
-        // ---- the row's maximum, 64 columns at a time
+        // ---- S to P, 64 columns at a time (the products with V begin after the first half): a
+        // half's maximum comes with its load (in 64 instructions instead, and in a pass of its
+        // own over both halves: chunk 792 us, not 756; 8K prompt 480, not 440)
         const bool masked = base + kTokens - 1 > first_pos;
         auto scores = [&](int c, uint32_t (&s)[2][32]) {
           tc::load32(s_col + c * 64, s[0]);
@@ -485,13 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
               if (c * 64 + k > limit) s[k >> 5][k & 31] = 0xFF800000u;
           }
         };
-        float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 2; c++) {
-          uint32_t s[2][32];
+          uint32_t s[2][32], w[32];
           float of[4];  // the blocks' largest scores
-          if (!masked) {  // the load's own maxima (in 64 instructions here: chunk 792 us, not
-                          // 765; 8K prompt 480, not 465)
+          if (!masked) {
 #pragma unroll
             for (int g = 0; g < 4; g++)
               tc::load16_max(s_col + c * 64 + g * 16, &s[g >> 1][16 * (g & 1)], of[g]);
@@ -508,43 +510,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
               of[g] = fmaxf(a, __uint_as_float(v[15]));
             }
           }
+          float top = -INFINITY;
 #pragma unroll
           for (int g = 0; g < 4; g++) {
             const float4 pg = page[4 * c + g];
             top = fmaxf(top, fmaf(of[g], fmaxf(f * pg.z, kTiny), pg.x));
           }
-        }
-        // ---- the accumulator follows a maximum that has grown by more than kLag
-        if (__any_sync(0xffffffffu, top > m + kLag)) {
-          top = fmaxf(top, m);
-          const float by = m == -INFINITY ? 0.0f : ex2(m - top);
-          m = top;
-          l *= by;
-          if (j > 0) {
-            if (!two) {  // its S came before the step in front had been added up
-              if (!wait(sm, &sm.pv_done, pv_phase ^ ((j - 1) & 1), p.err)) {
+          // the accumulator follows a maximum that has grown by more than kLag
+          if (__any_sync(0xffffffffu, top > m + kLag)) {
+            top = fmaxf(top, m);
+            const float by = m == -INFINITY ? 0.0f : ex2(m - top);
+            m = top;
+            l *= by;
+            if (j > 0 || c > 0) {
+              // the products with V in front are complete: one tile's S may come before the last
+              // step's, a second half before the first half's
+              if (!two && j > 0 && !wait(sm, &sm.pv_done, pv_phase ^ ((j - 1) & 1), p.err))
                 failed = true;
-                break;
-              }
+              if (c > 0 && !wait(sm, &sm.h_done[tile], h_phase, p.err)) failed = true;
+              if (failed) break;
               tc::fence_after();
-            }
 #pragma unroll 1
-            for (int c = 0; c < 8; c++) {
-              uint32_t o[16];
-              tc::load16(o_col + c * 16, o);
-              tc::wait_ld();
+              for (int k0 = 0; k0 < 8; k0++) {
+                uint32_t o[16];
+                tc::load16(o_col + k0 * 16, o);
+                tc::wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
-              tc::store16(o_col + c * 16, o);
+                for (int k = 0; k < 16; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
+                tc::store16(o_col + k0 * 16, o);
+              }
             }
           }
-        }
-        const float ref = (m == -INFINITY ? 0.0f : m) - kHeadroom;
-        // ---- P, over S: the products with V begin after the first half
-#pragma unroll 1
-        for (int c = 0; c < 2; c++) {
-          uint32_t s[2][32], w[32];
-          scores(c, s);
+          const float ref = (m == -INFINITY ? 0.0f : m) - kHeadroom;
 #pragma unroll
           for (int g = 0; g < 4; g++) {
             const float4 pg = page[4 * c + g];
@@ -568,6 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           tc::fence_before();
           mbar_arrive(&sm.p_full[odd ? kOdd : tile][c]);
         }
+        if (failed) break;
+        h_phase ^= 1;
       }
       if (!two) pv_phase ^= (pc.tiles - 1) & 1;
       // ---- the result
@@ -856,6 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         if (!ok) break;
         tc::fence_after();
         values(0, buf, 0, step, j > 0);
+        if (lead) tc::commit(&sm.h_done[0]);
         ok = wait(sm, full + 1, phase, p.err);
         if (!ok) break;
         if (buf) odd_phase ^= 1;
@@ -879,6 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           if (!ok) continue;
           tc::fence_after();
           values(i, i, 0, step, j > 0);
+          if (lead) tc::commit(&sm.h_done[i]);
           ok = wait(sm, &sm.p_full[i][1], p_phase[i], p.err);
           if (!ok) continue;
           p_phase[i] ^= 1;

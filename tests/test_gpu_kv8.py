@@ -698,3 +698,18 @@ def test_prefill_where_one_token_takes_everything(fmt):
     q = bf16(q)
     out, lse = run_prefill(s, q, [m])
     check_prefill(s, q, [m], out, lse)
+
+
+@pytest.mark.parametrize("rise", [0.02, 0.3, 3.0])
+@pytest.mark.parametrize("m", [9, 20, 150])
+def test_prefill_whose_scores_grow_along_the_context(m, rise):
+    """Each half of a tile raises the maximum, by up to 64 tokens x `rise` x 100 x 0.01 x 128 /
+    sqrt(128): the accumulator follows it before and between the products with V."""
+    n = 900
+    s = Batch([n], 4, 1, "int8", seed=19, fill=False)
+    u = np.sign(s.rng.standard_normal(D)).astype(np.float32)
+    k = bf16(np.arange(n, dtype=np.float32)[:, None, None] * 0.01 * u)
+    O.write(s.cache, k, s.rows(n), s.table[0], 0)
+    q = bf16(100.0 * rise * u * s.rng.uniform(0.5, 1.0, (m, 4, 1)))
+    out, lse = run_prefill(s, q, [m])
+    check_prefill(s, q, [m], out, lse)
