@@ -29,10 +29,10 @@
 // one: 89 -> 76 us).
 //
 // Measured (GB300, 1884 TFLOP/s bf16 burst, 1693 sustained; 32 query heads over 8): 2048 tokens
-// behind 30K 745-758 us, 1410 TFLOP/s; an 8K prompt 430-444 us, 1240 TFLOP/s of what its rows see
+// behind 30K 749-758 us, 1415 TFLOP/s; an 8K prompt 440-444 us, 1240 TFLOP/s of what its rows see
 // (a diagonal tile is computed whole); 4 x 7-24 tokens behind 6-12K 39 us. A step's products take
 // 2048 cycles, a step 3600: each tile's way from S over the softmax and P V to its next S is one
-// chain, and two tiles overlap it only in part. Instructions: 1940 a step and scheduler, half its
+// chain, and two tiles overlap it only in part. Instructions: 1880 a step and scheduler, half its
 // slots (1/3 of them the conversion). With registers to spare nothing changes (144 / 80 / 32 and
 // 136 / 88 / 32 instead of 136 / 80 / 48: 765-775, 466-471, 40 us); queries loaded two rows an
 // instruction instead of a row a thread: 767, 468, 40.
@@ -59,7 +59,7 @@ constexpr int kThreads = 640;  // five warpgroups; the last is warp 16 and three
 constexpr int kSoftmaxRegs = 136, kConvertRegs = 80, kMmaRegs = 48;
 static_assert(2 * kSoftmaxRegs + 2 * kConvertRegs + kMmaRegs == 5 * 96, "the launch's registers");
 static_assert(kConvertWarps == kTilePages, "a warp converts one block of K and of V a step");
-constexpr float kPartCost = 1.3f;  // us
+constexpr float kPartCost = 1.3f, kStepCost = 1.55f;  // us
 constexpr int kPageRing = 4;
 constexpr int kBlockCost = 4;  // what a row block costs beside its tiles, in tiles (see Walk)
 // P = 2^(y - M + kHeadroom), y - M up to kLag: at most 2^15. A smaller headroom leaves small
@@ -215,7 +215,8 @@ struct Piece {
 // The pieces of the slice [x, end) of the line, in order. A row block's places are kBlockCost
 // for what it costs beside its tiles (queries in, results out), then
 // one a tile. Without the first, the CTAs with a head's first, short row blocks would take half
-// as long again as the others (8K prompt: 624 us without, 472 with 4, 479 with 6).
+// as long again as the others (8K prompt: 624 us without, 472 with 4 when that was found; now 454
+// with 3, 442 with 4, 444 with 5).
 struct Walk {
   const Seqs s;
   int batch, hkv, group, block_tokens;
@@ -332,12 +333,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     }
     if (lane == 0) pre[0] = 0;
     __syncwarp();
-    // Equal slices, but none so short that joining costs more than it saves: a step is 1.9 us, a
-    // further part of a row block kPartCost in the joining CTA, so with t tiles a block slices of
-    // t' have the least of 1.9 t' + kPartCost t / t'.
+    // Equal slices, but none so short that joining costs more than it saves: a step of a row block
+    // of one tile (few rows; else every slice is longer) is kStepCost, a further part of a row
+    // block kPartCost in the joining CTA, so with t tiles a block slices of t' have the least of
+    // kStepCost t' + kPartCost t / t'.
     const float mean = all_blocks > 0 ? (float)sum / all_blocks : 0.0f;
     const long long per = max((sum + gridDim.x - 1) / gridDim.x,
-                              max((long long)(sqrtf(kPartCost / 1.9f * mean) + 0.5f), 2LL));
+                              max((long long)(sqrtf(kPartCost / kStepCost * mean) + 0.5f), 2LL));
     const long long begin = min(blockIdx.x * per, sum);
     if (lane == 0) sm.per = per;
     if (begin < sum) {
