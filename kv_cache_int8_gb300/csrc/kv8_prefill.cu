@@ -429,6 +429,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       const int pos = real ? len[pc.b] - num[pc.b] + token : INT_MAX;
       const size_t out_row = (size_t)(row0[pc.b] + token) * p.hq + head;
       float f;
+      // the row's sum starts as NaN where the query has an infinity: its scores may all be -inf,
+      // which would look like a row that sees nothing (a NaN makes every score NaN by itself)
+      float l;
       {
         const uint4* q = reinterpret_cast<const uint4*>(
             p.q + (long long)(row0[pc.b] + token) * p.q_stride + head * kHeadDim);
@@ -445,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         }
         const uint32_t m16 = max(mx & 0xFFFFu, mx >> 16);
         const int e = m16 >> 7;
+        l = e == 255 ? NAN : 0.0f;
         const int shift = (m16 == 0 || e == 255) ? 0 : min(13 + 127 - e, 126);
         const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
         f = p.scale_log2 * __uint_as_float((uint32_t)(127 - shift) << 23);
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       // the first position of this tile's rows: tiles of tokens up to it need no mask
       const int first_pos = len[pc.b] - num[pc.b] + pc.q * p.block_tokens +
                             tile * 128 / p.group;
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY;
       for (int j = 0; !failed && j < pc.tiles; j++, step++) {
         const int base = (pc.tile + j) * kTokens;
         const bool odd = !two && (j & 1);  // one tile: its S and P alternate between the buffers
@@ -577,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       tc::fence_after();
       const bool whole = pc.tiles == pc.all_tiles;
       if (whole) {
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
         for (int c = 0; c < 4; c++) {
           uint32_t o[32];
@@ -634,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
             const float2 v = __ldcg(pml + slot_of(c) * kRows + row);
             sum += ex2(v.x - ref) * v.y;
           }
-          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+          const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll 1
           for (int c4 = 0; c4 < 4; c4++) {  // 32 channels at a time
             float4 acc[8];

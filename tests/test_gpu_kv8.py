@@ -713,3 +713,28 @@ def test_prefill_whose_scores_grow_along_the_context(m, rise):
     q = bf16(100.0 * rise * u * s.rng.uniform(0.5, 1.0, (m, 4, 1)))
     out, lse = run_prefill(s, q, [m])
     check_prefill(s, q, [m], out, lse)
+
+
+@pytest.mark.parametrize("n,m", [(1, 1), (40, 3), (700, 260), (9000, 5)])
+def test_prefill_of_infinities_against_codes_of_one_sign(n, m):
+    """An infinity times key codes of the other sign makes every score of a row -inf, whether the
+    row sees one token or many, in a whole row block or in parts of one (9000 tokens)."""
+    s = Batch([n], 4, 2, "int8", seed=23, fill=False)
+    k = s.rows(n)
+    k[:, :, 7] = -np.abs(k[:, :, 7]) - 1.0  # a code below zero in every token
+    O.write(s.cache, k, s.rows(n), s.table[0], 0)
+    q = bf16(s.rng.standard_normal((m, 4, D)))
+    q[0, 0, 7], q[-1, 1, 7], q[m // 2, 3, 7] = np.inf, np.inf, np.inf
+    bad = ~np.isfinite(q).all(-1)
+    out, lse = run_prefill(s, q, [m])
+    np.testing.assert_array_equal(np.isnan(out).all(-1), bad)
+    np.testing.assert_array_equal(np.isnan(out).any(-1), bad)
+    np.testing.assert_array_equal(np.isnan(lse), bad)
+    for h in range(2):
+        kk, vv = (O.values(s.cache, w, s.table[0], n, h) for w in "kv")
+        seen = np.arange(n)[None] <= (n - m + np.arange(m))[:, None]
+        for j in (2 * h, 2 * h + 1):
+            ok = ~bad[:, j]
+            want, wl, tol = O.attend(q[ok, j], kk, vv, seen[ok], D ** -0.5)
+            tol["out"] = tol["out"] + 2.0 ** -11 * np.abs(vv).max()
+            assert_rows(out[ok, j], lse[ok, j], want, wl, tol, 2.0 ** -8)
