@@ -5,14 +5,19 @@
 // "KV Cache 量化"; the attended set is hsa_attend's.
 //
 // Mathematics. A block of 16 tokens has codes a_t, c_t (K, V) and scales s_k, s_v:
-//   x_tj = (sm_scale log2 e s_k) q_j . a_t     out_j = sum_t 2^(x_tj - m) s_v c_t / sum_t 2^(..)
+//   x_tj = (sm_scale log2 e s_k) q_j . a_t     y_tj = x_tj + log2 s_v
+//   out_j = sum_t 2^(y_tj - m) c_t / sum_t 2^(x_tj - m)
 // Both products run on the matrix pipe with fp16 operands and fp32 sums, and nothing is rounded
 // that matters: the codes are exact in fp16; a head's query is multiplied by the power of two
 // that puts its largest value in [2^13, 2^14), which makes every bf16 value down to 2^-27 of
-// that one exact in fp16; a probability is carried as 2^(x - m + 10), where m may lag the
-// maximum by up to 4, times its block's s_v in units of a power of two that follows the largest
-// s_v so far (below 2^15), and is split into fp16 hi + lo, 22 bits together. The relative error
-// against 64 bits is 3 to 5e-7 (2-norm).
+// that one exact in fp16; a probability is carried with V's scale as 2^(y - m + 10), where m
+// follows the maximum of y and may lag it by up to 4, so at most 2^14, and is split into fp16
+// hi + lo, 22 bits together. The sum of the weights takes them times 1 / s_v, a factor a block,
+// as long as every s_v is within 2^-40 .. 2^40: below 2^54 a token then, and a token that matters
+// is no smaller than 2^-70. From a row's first block on whose s_v is not (a block of zeros has
+// none), a second form of the loop sums 2^x under a maximum of its own: right for any mixture of
+// scales, at the price of more exponentials. The relative error against 64 bits is 3 to 5e-7
+// (2-norm).
 //
 // Layout. K's block is the left operand [16 tokens][128 channels], the group's heads (up to 8)
 // the 8 columns of m16n8k16; V's block enters transposed, 8 tiles of 16 channels. So a group of
@@ -38,6 +43,7 @@
 #include "kv8.cuh"
 
 #include <cmath>
+#include <type_traits>
 
 namespace hsa {
 namespace {
@@ -54,6 +60,8 @@ constexpr int kTile = 8 * kHeadDim;            // output values of a row (8 head
 constexpr int kAhead = 24;                     // parts of a row joined at a time
 constexpr float kHeadroom = 10.0f;             // p is 2^(x - m + kHeadroom)
 constexpr float kLag = 4.0f;                   // m follows a maximum that is this much larger
+constexpr float kPlainScale = 40.0f;           // largest |log2 s_v| of the loop's plain form
+constexpr float kLow = -1e30f;                 // below any m
 
 struct Params {
   const __nv_bfloat16* q;
@@ -138,6 +146,12 @@ __device__ __forceinline__ float max32(float x) {
   for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
   return x;
 }
+// over the lanes of one pair of heads
+__device__ __forceinline__ float max_tokens(float x) {
+#pragma unroll
+  for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+  return x;
+}
 __device__ __forceinline__ float sum32(float x) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
@@ -159,8 +173,7 @@ __device__ __forceinline__ int row_units(const Params& p, int n) {
 struct alignas(16) Unit {
   int y;
   int span;       // lo | hi << 8; 0: nothing to do
-  float sk, sv;  // the scales; sv as it is used: log2 s_v (-100 for a block of zeros:
-                 // below any other, it then takes no part in the choice of m)
+  float sk, sv;  // the scales; sv as it is used: log2 s_v (-inf for a block of zeros)
 };
 
 // Places of a row on the line: with per > 0 a whole number of slices of `per`.
@@ -216,7 +229,7 @@ __device__ __forceinline__ Unit locate(const Params& p, const long long* pre, co
   t.span = lo | (hi << 8);
   t.sk = p.k_scale[block];
   const float sv = p.v_scale[block];
-  t.sv = sv > 0.0f ? lg2(sv) : -100.0f;
+  t.sv = lg2(sv);
   return t;
 }
 
@@ -477,8 +490,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 4; c++) o[k][c] = 0.0f;
 
-    // two visits at a time: two independent chains of products, one reduction of the maximum
-    while (i < i_stop) {
+    // Two visits at a time: two independent chains of products, one reduction of the maximum.
+    // kApart: l0 and l1 are the lanes' sums of 2^(x - top), not of 2^(y - m + kHeadroom) / s_v.
+    bool apart = false;
+    float top0, top1;
+    auto visit = [&](auto form) {
+      constexpr bool kApart = decltype(form)::value;
       const int two = i + 1 < i_stop;
       if (!pending && filled < mine && filled - i <= kBatch) {
         ahead = fetch(filled);
@@ -490,7 +507,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const Unit ua = meta[i % kMeta];
       Unit ub = meta[(i + 1) % kMeta];
-      if (!two) ub.span = 0;
+      if (!two) ub.span = 0, ub.sv = 0.0f;
+      if (!kApart && !(fmaxf(fabsf(ua.sv), fabsf(ub.sv)) <= kPlainScale)) {
+        apart = true;
+        return;
+      }
       if ((ua.span | ub.span) != 0 && !dead) {
         uint32_t kb[2];
         const int span[2] = {ua.span, ub.span};
@@ -535,6 +556,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         const float cv[2] = {ua.sv, ub.sv};
+        if (kApart) {
+          float z[2][4], z0 = top0, z1 = top1;
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            const float sk = h ? ub.sk : ua.sk;
+            const int lo = span[h] & 255, hi = span[h] >> 8;
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+              const int tok = g + 4 * (c & 2);
+              z[h][c] = tok >= lo && tok < hi ? x[h][c] * ((c & 1 ? f1 : f0) * sk) : -INFINITY;
+            }
+            z0 = fmaxf(z0, fmaxf(z[h][0], z[h][2]));
+            z1 = fmaxf(z1, fmaxf(z[h][1], z[h][3]));
+          }
+          z0 = max_tokens(z0);  // finite, as one token at least is seen
+          z1 = max_tokens(z1);
+          l0 = l0 * ex2(top0 - z0) + (ex2(z[0][0] - z0) + ex2(z[0][2] - z0)) +
+               (ex2(z[1][0] - z0) + ex2(z[1][2] - z0));
+          l1 = l1 * ex2(top1 - z1) + (ex2(z[0][1] - z1) + ex2(z[0][3] - z1)) +
+               (ex2(z[1][1] - z1) + ex2(z[1][3] - z1));
+          top0 = z0;
+          top1 = z1;
+        }
         float n0 = -INFINITY, n1 = -INFINITY;
 #pragma unroll
         for (int h = 0; h < 2; h++) {  // y = x + log2 s_v
@@ -562,8 +606,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float a0 = ex2(m0 - n0), a1 = ex2(m1 - n1);  // 0 from -inf: n is finite
           m0 = n0;
           m1 = n1;
-          l0 *= a0;
-          l1 *= a1;
+          if (!kApart) {
+            l0 *= a0;
+            l1 *= a1;
+          }
 #pragma unroll
           for (int k = 0; k < 8; k++) {
             o[k][0] *= a0;
@@ -578,9 +624,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (span[h] == 0) continue;
           const float p00 = ex2(x[h][0] - ref0), p01 = ex2(x[h][1] - ref1);
           const float p10 = ex2(x[h][2] - ref0), p11 = ex2(x[h][3] - ref1);
-          const float per_s = ex2(-cv[h]);  // 1 / s_v
-          l0 = fmaf(p00 + p10, per_s, l0);
-          l1 = fmaf(p01 + p11, per_s, l1);
+          if (!kApart) {
+            const float per_s = ex2(-cv[h]);  // 1 / s_v
+            l0 = fmaf(p00 + p10, per_s, l0);
+            l1 = fmaf(p01 + p11, per_s, l1);
+          }
           const uint32_t ha = half_pair(p00, p01), hb = half_pair(p10, p11);
           const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
           const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hb));
@@ -625,6 +673,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       i += 1 + two;
       __syncwarp();  // the slots are read before they are filled again
       issue_to(i + kStages, i_stop);
+    };
+    while (i < i_stop && !apart) visit(std::false_type{});
+    if (apart) {
+      top0 = m0 - kHeadroom;
+      top1 = m1 - kHeadroom;
+      m0 = fmaxf(m0, kLow);  // before any block but those of zeros: y is -inf, m must not be
+      m1 = fmaxf(m1, kLow);
+      while (i < i_stop) visit(std::true_type{});
+      // Back into one frame, within 2^50 of the sums' own: o (the result times the sum, in that
+      // frame) and l stay in fp32's range, and of two parts that are joined the frames differ by
+      // 2^100 at most beside their sums: a factor that fp32 flushes to 0, below 2^-126, belongs
+      // to a part that counts for less than 2^-26.
+      const float to0 = fminf(fmaxf(m0 - kHeadroom, top0 - 50.0f), top0 + 50.0f);
+      const float to1 = fminf(fmaxf(m1 - kHeadroom, top1 - 50.0f), top1 + 50.0f);
+      // in two factors, as one alone may leave the range
+      const float a0 = ex2(0.5f * (m0 - kHeadroom - to0)), a1 = ex2(0.5f * (m1 - kHeadroom - to1));
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        o[k][0] = o[k][0] * a0 * a0;
+        o[k][1] = o[k][1] * a1 * a1;
+        o[k][2] = o[k][2] * a0 * a0;
+        o[k][3] = o[k][3] * a1 * a1;
+      }
+      l0 *= ex2(top0 - to0);
+      l1 *= ex2(top1 - to1);
+      m0 = to0 + kHeadroom;
+      m1 = to1 + kHeadroom;
     }
 
     // ---- the warps' parts of the row meet

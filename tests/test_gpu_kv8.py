@@ -738,3 +738,81 @@ def test_prefill_of_infinities_against_codes_of_one_sign(n, m):
             want, wl, tol = O.attend(q[ok, j], kk, vv, seen[ok], D ** -0.5)
             tol["out"] = tol["out"] + 2.0 ** -11 * np.abs(vv).max()
             assert_rows(out[ok, j], lse[ok, j], want, wl, tol, 2.0 ** -8)
+
+
+# Magnitudes of V's blocks (powers of two, None: zeros), repeated along the sequence.
+V_MAGNITUDES = {"tiny": [-115], "zero": [None], "zero, then large": [None] * 30 + [60],
+                "large, then tiny": [100] * 20 + [-110], "tiny, then large": [-110] * 20 + [100],
+                "all kinds": [None, -100, 0, 50, 120], "zero within": [0, 0, None]}
+
+
+def unlike_batch(lens, hq, hkv, fmt, magnitudes):
+    s = Batch(lens, hq, hkv, fmt, seed=len(lens), fill=False)
+    for b, n in enumerate(lens):
+        v = s.rows(n)
+        for i in range(0, n, PAGE):
+            e = magnitudes[i // PAGE % len(magnitudes)]
+            v[i:i + PAGE] *= np.float32(0.0 if e is None else 2.0 ** e)
+        O.write(s.cache, s.rows(n), v, s.table[b], 0)
+    return s
+
+
+def unlike_bounds(q, k, v, seen, tol, levels, probability, floor):
+    """Bounds of an output row by what its own tokens weigh, not by the largest value: every
+    weight is off by twice the oracle's relative bound and by the rounding of its fp16 form,
+    `probability` of itself, and never by less than `floor` of the heaviest token's (the fp16
+    form's smallest step against the least that the heaviest one is carried as)."""
+    x = np.where(seen, q @ k.T * D ** -0.5, -np.inf)
+    p = np.exp(x - x.max(-1, keepdims=True))
+    p /= p.sum(-1, keepdims=True)
+    top = np.abs(v).max() if v.any() else 1.0
+    rel = tol["out"] / top  # 2 (eps + sums)
+    heaviest = (p * np.abs(v).max(-1)).max(-1)  # a value is at most `levels` scales
+    return ((rel + probability)[:, None] * (p @ np.abs(v)) +
+            (len(k) * floor * levels * heaviest)[:, None])
+
+
+@pytest.mark.parametrize("kind", list(V_MAGNITUDES))
+@pytest.mark.parametrize("fmt,hq,hkv,lens", [
+    ("int8", 4, 1, [1, 645, 0, 5000]),                           # CTAs share rows
+    ("e4m3", 7, 1, [16, 700]), ("int8", 8, 1, [3000]),
+    ("e4m3", 4, 1, [1 + i % 60 for i in range(300)]),            # a warp a row
+    ("int8", 6, 2, [10 + (i * 13) % 330 for i in range(170)]),   # four warps a row
+])
+def test_decode_sums_where_v_is_zero_tiny_or_large(kind, fmt, hq, hkv, lens):
+    """The sum of the weights has nothing to do with V: no scale of V, nor any mixture of them,
+    may push it out of fp32 or lose a part of it."""
+    s = unlike_batch(lens, hq, hkv, fmt, V_MAGNITUDES[kind])
+    q = bf16(s.rng.standard_normal((len(lens), hq, D)))
+    out, lse = run_decode(s, q)
+    g = hq // hkv
+    for b in list(range(0, len(lens), 23)) + [len(lens) - 1]:
+        n = lens[b]
+        if n == 0:
+            continue
+        for h in range(hkv):
+            rows = slice(h * g, (h + 1) * g)
+            k, v = (O.values(s.cache, w, s.table[b], n, h) for w in "kv")
+            seen = np.ones((g, n), bool)
+            want, wl, tol = O.attend(q[b, rows], k, v, seen, D ** -0.5)
+            # fp16 in two halves: nothing but its floor, 2^-25 against at least 2^10
+            bound = unlike_bounds(q[b, rows].astype(np.float64), k, v, seen, tol,
+                                  float(O.LEVELS[fmt]), 0.0, 2.0 ** -35)
+            assert (np.abs(lse[b, rows] - wl) <= tol["lse"]).all(), (b, h)
+            assert (np.abs(out[b, rows] - want) <= bound).all(), (b, h)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_over_a_million_tokens_of_zeros(fp8):
+    """An empty V (a fresh cache's): 2^20 equal weights, whose sums are whole numbers; the
+    logarithm and its two scalings are off by 2^-22 of ln 2^20 at most."""
+    n = 1 << 20
+    d = hsa.Dims(batch=1, hq=4, hkv=1, max_pages_per_seq=n // 16, num_pages=n // 16, k2=0)
+    table = torch.arange(n // 16, device="cuda", dtype=torch.int32)[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out, lse = torch.ones(1, 4, D, device="cuda"), torch.empty(1, 4, device="cuda")
+    q = torch.ones(1, 4, D, device="cuda", dtype=torch.bfloat16)
+    hsa.hsa_kv8_decode(d, hsa.KV8.zeros(d, fp8), q, table, lens, out, lse,
+                       hsa.workspace(d, hsa.HSA_OP_KV8_DECODE))
+    assert not out.any()
+    assert float((lse.double() - np.log(n)).abs().max()) <= np.log(n) * 2.0 ** -22
