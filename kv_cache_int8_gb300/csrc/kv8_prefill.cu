@@ -8,7 +8,10 @@
 // blocks' scales (16 tokens) are applied in fp32: with row factor f = sm_scale log2 e 2^-shift,
 //   y_t = f s_k S_t + log2 s_v,   out = sum_t 2^(y_t - M) c_t / sum_t 2^(y_t - M) / s_v
 // so V's scale costs nothing but the offset of an exponent that is computed anyway, and the sum
-// takes one multiplication a block. P = 2^(y - M + 7) is rounded to fp16 (11 bits, against 8
+// takes one multiplication a block, as long as every s_v is within 2^-40 .. 2^40 (P / s_v then
+// stays below 2^55, and above 2^-73 where it matters). From the first tile on that has another
+// s_v (or a block of zeros, that has none), the rest of a stretch of tiles sums 2^(x - its own
+// maximum) beside P, in a second form of the step: right for any mixture of scales. P = 2^(y - M + 7) is rounded to fp16 (11 bits, against 8
 // of the bf16 result); M lags the running maximum by at most 8, so the output accumulator is
 // rarely rescaled (with 10 and 4: 2048 tokens behind 30K 767 us, not 756; 8K prompt 465, not
 // 443).
@@ -41,6 +44,7 @@
 
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 namespace hsa {
 namespace {
@@ -67,6 +71,7 @@ constexpr int kBlockCost = 4;  // what a row block costs beside its tiles, in ti
 // as heavy as the largest make 2^-5 of 2^7, 2^-12 of the result (bf16 rounds it to 2^-9).
 constexpr float kHeadroom = 7.0f;
 constexpr float kLag = 8.0f;
+constexpr float kPlainScale = 40.0f;  // largest |log2 s_v| under which the sum is made of P / s_v
 constexpr float kTiny = 1e-37f;  // scales of scores are at least that: a masked -inf stays one
 // s_full and p_full of the tiles and, where a row block has one tile, of its odd steps
 constexpr int kOdd = 2;
@@ -95,7 +100,9 @@ struct Smem {
   alignas(1024) unsigned char q[2][kTileBytes];
   unsigned char k[2][kTileBytes];
   unsigned char v[2][kTileBytes];
-  // log2 s_v, 1 / s_v, s_k of a step's blocks (x and y are read alone, as an aligned pair)
+  // Of a step's blocks: x = w, but +inf where |w| is above kPlainScale; y = 1 / s_v (any number
+  // above 0 for zeros, 0 where there are no tokens); z = s_k; w = log2 s_v (-inf for both). x and
+  // y are read alone, as an aligned pair.
   float4 page[kPageRing][kTilePages];
   alignas(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[3],
       p_full[3][2], o_full[2];  // s_full, p_full: kOdd; p_full[..][half of the tokens]
@@ -468,17 +475,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       const int first_pos = len[pc.b] - num[pc.b] + pc.q * p.block_tokens +
                             tile * 128 / p.group;
       float m = -INFINITY;
-      for (int j = 0; !failed && j < pc.tiles; j++, step++) {
-        const int base = (pc.tile + j) * kTokens;
-        const bool odd = !two && (j & 1);  // one tile: its S and P alternate between the buffers
-        const uint32_t s_col = at + kColS + 128 * (odd ? 1 : tile);
+      int j = 0;
+      auto scores_ready = [&]() {
+        const bool odd = !two && (j & 1);
         if (!wait(sm, &sm.s_full[odd ? kOdd : tile], odd ? odd_phase : s_phase, p.err)) {
           failed = true;
-          break;
+          return false;
         }
         if (odd) odd_phase ^= 1;
         else s_phase ^= 1;
         tc::fence_after();
+        return true;
+      };
+      // One step from half c0 on; returns the half that it stopped before. The plain form stops
+      // before a block whose s_v is zero or far from 1: from there on in the piece kApart, in
+      // which l is the sum of 2^(x - top_x), not of P / s_v.
+      float top_x;
+      auto one_step = [&](auto form, int c0) {
+        constexpr bool kApart = decltype(form)::value;
+        const int base = (pc.tile + j) * kTokens;
+        const bool odd = !two && (j & 1);  // one tile: its S and P alternate between the buffers
+        const uint32_t s_col = at + kColS + 128 * (odd ? 1 : tile);
         const float4* page = sm.page[step % kPageRing];
         const int limit = pos - base;  // columns up to it are seen
         // ---- S to P, 64 columns at a time (the products with V begin after the first half): a
@@ -496,9 +513,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           }
         };
 #pragma unroll 1
-        for (int c = 0; c < 2; c++) {
+        for (int c = c0; c < 2; c++) {
           uint32_t s[2][32], w[32];
           float of[4];  // the blocks' largest scores
+          float top = -INFINITY;
           if (!masked) {
 #pragma unroll
             for (int g = 0; g < 4; g++)
@@ -514,27 +532,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
               for (int k = 1; k < 15; k += 2)
                 a = max3(a, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
               of[g] = fmaxf(a, __uint_as_float(v[15]));
+              // a block that the warp's rows may not see: -inf from it would turn into NaN
+              if (!kApart && page[4 * c + g].x == INFINITY) top = INFINITY;
             }
           }
-          float top = -INFINITY;
+          if (kApart) {
+            float z = top_x;
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+              const float4 pg = page[4 * c + g];
+              if (pg.y > 0.0f) z = fmaxf(z, of[g] * fmaxf(f * pg.z, kTiny));
+            }
+            const float ref_x = z == -INFINITY ? 0.0f : z;  // nothing seen so far
+            l *= ex2(top_x - ref_x);
+            top_x = z;
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+              const float4 pg = page[4 * c + g];
+              const float mul = fmaxf(f * pg.z, kTiny);
+              float sum = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 16; k++)
+                sum += ex2(fmaf(__uint_as_float(s[g >> 1][16 * (g & 1) + k]), mul, -ref_x));
+              if (pg.y > 0.0f) l += sum;
+            }
+          }
 #pragma unroll
           for (int g = 0; g < 4; g++) {
             const float4 pg = page[4 * c + g];
-            top = fmaxf(top, fmaf(of[g], fmaxf(f * pg.z, kTiny), pg.x));
+            top = fmaxf(top, fmaf(of[g], fmaxf(f * pg.z, kTiny), kApart ? pg.w : pg.x));
           }
           // the accumulator follows a maximum that has grown by more than kLag
           if (__any_sync(0xffffffffu, top > m + kLag)) {
+            if (!kApart && __any_sync(0xffffffffu, top == INFINITY)) return c;
             top = fmaxf(top, m);
             const float by = m == -INFINITY ? 0.0f : ex2(m - top);
             m = top;
-            l *= by;
+            if (!kApart) l *= by;
             if (j > 0 || c > 0) {
               // the products with V in front are complete: one tile's S may come before the last
               // step's, a second half before the first half's
               if (!two && j > 0 && !wait(sm, &sm.pv_done, pv_phase ^ ((j - 1) & 1), p.err))
                 failed = true;
               if (c > 0 && !wait(sm, &sm.h_done[tile], h_phase, p.err)) failed = true;
-              if (failed) break;
+              if (failed) return c;
               tc::fence_after();
 #pragma unroll 1
               for (int k0 = 0; k0 < 8; k0++) {
@@ -551,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
 #pragma unroll
           for (int g = 0; g < 4; g++) {
             const float4 pg = page[4 * c + g];
-            const float add = pg.x - ref, mul = fmaxf(f * pg.z, kTiny);
+            const float add = (kApart ? pg.w : pg.x) - ref, mul = fmaxf(f * pg.z, kTiny);
             const float2 mul2 = make_float2(mul, mul);
             float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -564,14 +605,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
               sum = k == 0 ? y : add2(sum, y);
               w[8 * g + k / 2] = half_pair(y.x, y.y);
             }
-            l = fmaf(sum.x + sum.y, pg.y, l);
+            if (!kApart) l = fmaf(sum.x + sum.y, pg.y, l);
           }
           tc::store32(s_col + c * 32, w);
           tc::wait_st();
           tc::fence_before();
           mbar_arrive(&sm.p_full[odd ? kOdd : tile][c]);
         }
-        if (failed) break;
+        return 2;
+      };
+      bool apart = false;
+      for (; !failed && j < pc.tiles && scores_ready(); j++, step++) {
+        int c = 0;
+        if (!apart) {
+          c = one_step(std::false_type{}, 0);
+          if (c < 2 && !failed) {
+            apart = true;
+            top_x = m - kHeadroom;
+          }
+        }
+        if (apart) one_step(std::true_type{}, c);
         h_phase ^= 1;
       }
       if (!two) pv_phase ^= (pc.tiles - 1) & 1;
@@ -579,6 +632,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       if (!wait(sm, &sm.o_full[tile], o_phase, p.err)) failed = true;
       o_phase ^= 1;
       tc::fence_after();
+      if (apart) {
+        // Back into one frame, within 2^50 of the sum's own: O (the result times the sum, in that
+        // frame) and l stay in fp32's range, and of two parts that are joined the frames differ
+        // by 2^100 at most beside their sums: a factor that fp32 flushes to 0, below 2^-126,
+        // belongs to a part that counts for less than 2^-26.
+        const float ref = m - kHeadroom;
+        const float to = fminf(fmaxf(ref, top_x - 50.0f), top_x + 50.0f);
+        const bool none = top_x == -INFINITY;
+        // in two factors, as one alone may leave the range
+        const float by = none ? 1.0f : ex2(0.5f * (ref - to));
+        if (!none) l *= ex2(top_x - to);
+        m = to + kHeadroom;
+#pragma unroll 1
+        for (int k0 = 0; k0 < 8; k0++) {
+          uint32_t o[16];
+          tc::load16(o_col + k0 * 16, o);
+          tc::wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * by * by);
+          tc::store16(o_col + k0 * 16, o);
+        }
+        tc::wait_st();
+      }
       const bool whole = pc.tiles == pc.all_tiles;
       if (whole) {
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
@@ -774,12 +850,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         if (!ok) break;
         const float sk = __shfl_sync(0xffffffffu, cur.sk, j);
         const float sv = __shfl_sync(0xffffffffu, cur.sv, j);
-        // No tokens: p = 0. A block of zeros in V counts as 2^-100, below any other, so that it
-        // takes no part in the choice of M.
-        if (lane == 0)
-          sm.page[step % kPageRing][w] = sv < 0.0f    ? make_float4(-INFINITY, 0.0f, sk, 0.0f)
-                                         : sv == 0.0f ? make_float4(-100.0f, 0x1p100f, sk, 0.0f)
-                                                      : make_float4(lg2(sv), 1.0f / sv, sk, 0.0f);
+        if (lane == 0) {
+          const float log = lg2(sv);
+          sm.page[step % kPageRing][w] =
+              sv < 0.0f ? make_float4(-INFINITY, 0.0f, sk, -INFINITY)
+                        : make_float4(fabsf(log) <= kPlainScale ? log : INFINITY,
+                                      sv == 0.0f ? 1.0f : 1.0f / sv, sk, log);
+        }
         put(sm.k[st], rk);
         if (lane == 0) mbar_arrive(&sm.k_full[st]);
         if (another) load(p.k, turn ? next : cur, nj, rk);

@@ -816,3 +816,52 @@ def test_decode_over_a_million_tokens_of_zeros(fp8):
                        hsa.workspace(d, hsa.HSA_OP_KV8_DECODE))
     assert not out.any()
     assert float((lse.double() - np.log(n)).abs().max()) <= np.log(n) * 2.0 ** -22
+
+
+@pytest.mark.parametrize("kind", list(V_MAGNITUDES))
+@pytest.mark.parametrize("fmt,hq,hkv,lens,new", [
+    ("int8", 4, 1, [1, 645, 5000], [1, 30, 9]),   # row blocks in parts
+    ("e4m3", 4, 2, [700], [400]), ("int8", 7, 1, [900, 40], [200, 40]),
+])
+def test_prefill_sums_where_v_is_zero_tiny_or_large(kind, fmt, hq, hkv, lens, new):
+    s = unlike_batch(lens, hq, hkv, fmt, V_MAGNITUDES[kind])
+    q = bf16(s.rng.standard_normal((sum(new), hq, D)))
+    out, lse = run_prefill(s, q, new)
+    g, at = hq // hkv, 0
+    for b, (n, m) in enumerate(zip(lens, new)):
+        seen = np.arange(n)[None] <= (n - m + np.arange(m))[:, None]
+        for j in range(hq):
+            k, v = (O.values(s.cache, w, s.table[b], n, j // g) for w in "kv")
+            qj = q[at:at + m, j].astype(np.float64)
+            want, wl, tol = O.attend(qj, k, v, seen, D ** -0.5)
+            # fp16: half a step 2^-11, or its floor, 2^-25 against at least 2^7
+            bound = unlike_bounds(qj, k, v, seen, tol, float(O.LEVELS[fmt]), 2.0 ** -11,
+                                  2.0 ** -32)
+            bound += 2.0 ** -8 * (np.abs(want) + bound)  # the bf16 result
+            assert (np.abs(lse[at:at + m, j] - wl) <= tol["lse"]).all(), (b, j)
+            assert (np.abs(out[at:at + m, j] - want) <= bound).all(), (b, j)
+        at += m
+
+
+def test_prefill_over_zeros_whose_first_scores_are_lower():
+    """V all zero, one low score, then 16K equal ones: with a reference that stays behind, the
+    sum of 2^14 weights must not leave fp32. lse against 64 bits, the logits being exact: the
+    sums of equal weights are whole, the logarithm and its scalings off by 2^-22 of it."""
+    n, m = 1 << 14, 3
+    d = hsa.Dims(batch=1, hq=2, hkv=1, max_pages_per_seq=n // 16, num_pages=n // 16, k2=0)
+    cache = hsa.KV8.zeros(d)
+    cache.k_scale.fill_(1.0)
+    cache.k[:, :, :, 0] = 1
+    cache.k[0, :, :, 0] = 0
+    table = torch.arange(n // 16, device="cuda", dtype=torch.int32)[None]
+    q = torch.zeros(m, 2, D, device="cuda", dtype=torch.bfloat16)
+    q[:, 0, 0], q[:, 1, 0] = 56.0, 5.0  # times D^-1/2 log2 e: 7.1, just below the lag, and 0.64
+    out = torch.ones(m, 2, D, device="cuda", dtype=torch.bfloat16)
+    lse = torch.empty(m, 2, device="cuda")
+    hsa.hsa_kv8_prefill(d, cache, q, cu_of([m]), table, torch.tensor([n], dtype=torch.int32,
+                        device="cuda"), out, lse, hsa.workspace(d, hsa.HSA_OP_KV8_PREFILL))
+    assert not out.any()
+    x = q[:, :, 0].double().cpu().numpy() * D ** -0.5
+    ones = (n - m + np.arange(m) + 1 - 16)[:, None]
+    want = np.log(16.0 + ones * np.exp(x))
+    assert (np.abs(lse.cpu().numpy() - want) <= 2.0 ** -20 * want).all()
