@@ -70,6 +70,11 @@ constexpr int kBlockCost = 4;  // what a row block costs beside its tiles, in ti
 // probabilities in fp16's subnormals, 2^-25 off each: 2^20 tokens off the same way and together
 // as heavy as the largest make 2^-5 of 2^7, 2^-12 of the result (bf16 rounds it to 2^-9).
 constexpr float kHeadroom = 7.0f;
+// The products' own accumulation rounds towards zero: 1M tokens added up in O (65536 products)
+// gave results 2.6e-3 (equal scores) to 5e-3 (normal ones) too small, more than bf16's own
+// rounding. So O takes at most that many tiles' products, below 2048 x 2^-23 = 2.4e-4, and a
+// longer stretch is added up in fp32 outside. (Ending a stretch costs about four steps.)
+constexpr int kMaxTiles = 256;
 constexpr float kLag = 8.0f;
 constexpr float kPlainScale = 40.0f;  // largest |log2 s_v| under which the sum is made of P / s_v
 constexpr float kTiny = 1e-37f;  // scales of scores are at least that: a masked -inf stays one
@@ -217,6 +222,7 @@ struct Piece {
   int all_tiles;     // of the whole row block
   int rows;          // rows of the block that exist
   long long begin;   // the row block's first place on the line
+  bool after, before;  // the CTA's piece before / behind this one is of the same row block
 };
 
 // The pieces of the slice [x, end) of the line, in order. A row block's places are kBlockCost
@@ -229,6 +235,7 @@ struct Walk {
   int batch, hkv, group, block_tokens;
   long long x, end;
   int b, h, q, off;  // off: place in the row block
+  bool inside;       // of a stretch of more than kMaxTiles
 
   __device__ __forceinline__ bool next(Piece& p) {
     for (;;) {
@@ -239,10 +246,20 @@ struct Walk {
       p.begin = x - off;
       p.all_tiles = block_tiles(s.len[b], s.n[b], block_tokens, q);
       p.rows = min(block_tokens, s.n[b] - q * block_tokens) * group;
-      const int stop = (int)min((long long)(p.all_tiles + kBlockCost), off + (end - x));
+      int stop = (int)min((long long)(p.all_tiles + kBlockCost), off + (end - x));
       p.tile = max(off - kBlockCost, 0);
       p.tiles = max(stop - kBlockCost, 0) - p.tile;
+      p.after = inside;
+      p.before = inside = p.tiles > kMaxTiles;
+      if (inside) {
+        p.tiles = kMaxTiles;
+        stop = p.tile + kMaxTiles + kBlockCost;
+      }
       x += stop - off;
+      if (inside) {
+        off = stop;
+        return true;
+      }
       off = 0;
       if ((q + 1) * block_tokens < s.n[b]) {
         q++;
@@ -396,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
   const long long per = sm.per, all = pre[batch];
   const long long begin = min(blockIdx.x * per, all), end = min(begin + per, all);
   Walk walk = {{pre, len, num, row0}, batch, p.hkv, p.group, p.block_tokens, begin, end,
-               sm.start_b, sm.start_h, sm.start_q, sm.start_off};
+               sm.start_b, sm.start_h, sm.start_q, sm.start_off, false};
   Piece pc;
 
   if (warp < kSoftmaxWarps) {
@@ -655,14 +672,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         }
         tc::wait_st();
       }
-      const bool whole = pc.tiles == pc.all_tiles;
-      if (whole) {
+      const long long tiles_begin = pc.begin + kBlockCost, tiles_end = tiles_begin + pc.all_tiles;
+      const size_t slot = 2 * (size_t)blockIdx.x + (begin < pc.begin ? 1 : 0);
+      float4* const po = reinterpret_cast<float4*>(p.part_o) + slot * 32 * kRows + row;
+      float2* const pml = reinterpret_cast<float2*>(p.part_ml);
+      // The piece before of the same stretch is in the CTA's part, which only this thread reads
+      // and writes until the stretch ends: added to this one.
+      float keep = 1.0f, add = 0.0f;
+      if (pc.after && real) {
+        const float2 was = __ldcg(pml + slot * kRows + row);
+        const float top = fmaxf(m, was.x), ref = top == -INFINITY ? 0.0f : top;
+        keep = ex2(m - ref);
+        add = ex2(was.x - ref);
+        l = l * keep + was.y * add;
+        m = top;
+      }
+      auto add_up = [&](int c, uint32_t (&o)[32]) {  // 32 channels
+        if (!pc.after || !real) return;
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          const float4 v = __ldcg(po + (c * 8 + k) * kRows);
+          o[4 * k] = __float_as_uint(__uint_as_float(o[4 * k]) * keep + v.x * add);
+          o[4 * k + 1] = __float_as_uint(__uint_as_float(o[4 * k + 1]) * keep + v.y * add);
+          o[4 * k + 2] = __float_as_uint(__uint_as_float(o[4 * k + 2]) * keep + v.z * add);
+          o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * keep + v.w * add);
+        }
+      };
+      if (!pc.before && begin <= tiles_begin && tiles_end <= end) {  // the whole row block
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
         for (int c = 0; c < 4; c++) {
           uint32_t o[32];
           tc::load32(o_col + c * 32, o);
           tc::wait_ld();
+          add_up(c, o);
           if (real) {
             uint32_t w[16];
 #pragma unroll
@@ -675,16 +718,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           p.lse[out_row] = (m - kHeadroom + log2f(l)) * 0.693147180559945309f;
       } else {
         // a part: to the workspace; the last of the block's CTAs to arrive joins them
-        const long long tiles_begin = pc.begin + kBlockCost;
         const int c0 = (int)(tiles_begin / per);
-        const int parts = (int)((tiles_begin + pc.all_tiles - 1) / per) - c0 + 1;
-        const size_t slot = 2 * (size_t)blockIdx.x + (begin < pc.begin ? 1 : 0);
-        float4* po = reinterpret_cast<float4*>(p.part_o) + slot * 32 * kRows + row;
+        const int parts = (int)((tiles_end - 1) / per) - c0 + 1;
 #pragma unroll 1
         for (int c = 0; c < 4; c++) {
           uint32_t o[32];
           tc::load32(o_col + c * 32, o);
           tc::wait_ld();
+          add_up(c, o);
           if (real) {
 #pragma unroll
             for (int k = 0; k < 8; k++)
@@ -693,8 +734,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
                               __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
           }
         }
-        float2* pml = reinterpret_cast<float2*>(p.part_ml);
         if (real) pml[slot * kRows + row] = make_float2(m, l);
+        if (pc.before) {
+          tc::fence_before();
+          continue;
+        }
         named_sync(1 + tile, 128);
         if (r == 0) {
           int* counter = p.counters + 2 * c0 + tile;

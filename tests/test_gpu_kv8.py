@@ -865,3 +865,63 @@ def test_prefill_over_zeros_whose_first_scores_are_lower():
     ones = (n - m + np.arange(m) + 1 - 16)[:, None]
     want = np.log(16.0 + ones * np.exp(x))
     assert (np.abs(lse.cpu().numpy() - want) <= 2.0 ** -20 * want).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_long_prompts_lose_nothing_to_their_own_sums(fp8):
+    """Equal scores over half a million tokens, V with a mean in each channel: 4096 token tiles
+    add up in a row. A stretch of 256 (2048 products) may lose 2^-23 of the sum each, 2^-12 of
+    the result (its values are of one sign; the weights, all of a scale that is a power of two,
+    are not rounded); 2^-16 for the rest of the sums in fp32 and the division, and half a step of
+    bf16."""
+    n, m = 1 << 19, 8192
+    d = hsa.Dims(batch=1, hq=8, hkv=1, max_pages_per_seq=n // 16, num_pages=n // 16, k2=0)
+    cache = hsa.KV8.zeros(d, fp8)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = 10 + 100 * torch.rand(D, generator=g, device="cuda") + 8 * torch.rand(
+        n // 16, 1, 16, D, generator=g, device="cuda")
+    cache.v.copy_(x.round().to(cache.v.dtype))
+    cache.v_scale.fill_(2.0 ** -7)
+    table = torch.randperm(n // 16, generator=g, device="cuda").to(torch.int32)[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    q = torch.zeros(m, 8, D, device="cuda", dtype=torch.bfloat16)
+    out = torch.empty(m, 8, D, device="cuda", dtype=torch.bfloat16)
+    lse = torch.empty(m, 8, device="cuda")
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_PREFILL)
+    hsa.hsa_kv8_prefill(d, cache, q, cu_of([m]), table, lens, out, lse, ws)
+    assert hsa.hsa_read_device_error(ws) == 0
+    page = table[0].long()
+    values = (cache.v.view(torch.int8)[page].view(cache.v.dtype).float().double() *
+              cache.v_scale[page].double()[..., None, None]).view(n, D)
+    seen = torch.arange(n - m + 1, n + 1, device="cuda", dtype=torch.float64)[:, None]
+    want = values.cumsum(0)[n - m:] / seen
+    step = torch.exp2(torch.floor(torch.log2(want)) - 7)  # of bf16
+    for j in (0, 7):
+        err = (out[:, j].double() - want).abs()
+        assert bool((err <= step / 2 + want * (2.0 ** -12 + 2.0 ** -16)).all())
+        assert float((lse[:, j].double() - seen[:, 0].log()).abs().max()) <= 14 * 2.0 ** -20
+
+
+@pytest.mark.parametrize("hq,n,m", [(4, 40000, 700), (8, 70000, 90), (1, 36000, 40)])
+def test_prompts_of_stretches_longer_than_the_products_add_up(hq, n, m):
+    """More than 256 token tiles a row block, whole row blocks and parts, one tile of rows and
+    two; normal scores, a few rows checked against 64 bits."""
+    s = Batch([n], hq, 1, "int8", seed=24, fill=False)
+    for name in ("k", "v"):
+        s.cache[name][...] = s.rng.integers(-127, 128, s.cache[name].shape)
+        s.cache[name + "s"][...] = s.rng.uniform(0.005, 0.02, s.cache[name + "s"].shape)
+    # many copies of the sequence, so that a CTA's slice holds more than a stretch
+    copies = 1 + 152 * 600 // (max(1, m * hq // 256) * (n // 128))
+    s.lens, s.table = [n] * copies, np.tile(s.table, (copies, 1))
+    q = bf16(s.rng.standard_normal((m * copies, hq, D)))
+    out, lse = run_prefill(s, q, [m] * copies)
+    k, v = (O.values(s.cache, w, s.table[0], n, 0) for w in "kv")
+    for b in sorted({0, copies // 2, copies - 1}):
+        for j in sorted({0, hq - 1}):
+            i = np.unique([0, 1, m // 3, m // 2, m - 1])
+            seen = np.arange(n)[None] <= (n - m + i)[:, None]
+            want, wl, tol = O.attend(q[b * m + i, j], k, v, seen, D ** -0.5)
+            # fp16 weights; 2048 products a stretch, 2^-23 of the running sum each, whose values
+            # are no larger than max |v|
+            tol["out"] = tol["out"] + (2.0 ** -11 + 2.0 ** -12) * np.abs(v).max()
+            assert_rows(out[b * m + i, j], lse[b * m + i, j], want, wl, tol, 2.0 ** -8)
