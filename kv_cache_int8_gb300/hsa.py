@@ -402,6 +402,7 @@ class KV8:
                     not scale.is_contiguous()):
                 raise HsaError("KV8", HSA_ERR_INVALID_ARG, "shapes, types or layout rejected")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.hkv = k.shape[:2]
         self._c = hsa_kv8(_p(k), _p(v), _p(k_scale), _p(v_scale), formats[k.dtype])
         self._ref = ctypes.byref(self._c)
 
@@ -414,6 +415,16 @@ class KV8:
             codes = [c.view(torch.float8_e4m3fn) for c in codes]
         return cls(*codes, *(torch.zeros((d.num_pages, d.hkv), dtype=torch.float32, device=device)
                              for _ in range(2)))
+
+
+def _cache(name: str, d: Dims, cache: KV8):
+    """The cache's C struct, for a descriptor of its heads and of no more pages than it has (the
+    library sees only addresses: it would follow page numbers past the arrays)."""
+    if cache.num_pages < d.num_pages or cache.hkv != d.hkv:
+        raise HsaError(name, HSA_ERR_INVALID_ARG,
+                       f"a cache of {cache.num_pages} pages x {cache.hkv} kv heads, a descriptor "
+                       f"of {d.num_pages} x {d.hkv}")
+    return cache._ref
 
 
 def _rows(name: str, t, heads: int):
@@ -441,8 +452,8 @@ def hsa_kv8_write(d: Dims, cache: KV8, k_new, v_new, cu_tokens, page_table, seq_
     """k_new / v_new: bf16 [total_tokens][hkv][128], rows contiguous (any row stride)."""
     rows, k_stride, v_stride = _row_pair("hsa_kv8_write", k_new, v_new, d.hkv)
     rc = load().hsa_kv8_write(
-        ctypes.byref(d.c()), cache._ref, k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
-        _p(cu_tokens), rows, _p(page_table), _p(seq_lens), _p(ws),
+        ctypes.byref(d.c()), _cache("hsa_kv8_write", d, cache), k_new.data_ptr(), k_stride,
+        v_new.data_ptr(), v_stride, _p(cu_tokens), rows, _p(page_table), _p(seq_lens), _p(ws),
         0 if ws is None else ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check("hsa_kv8_write", rc)
@@ -453,8 +464,8 @@ def hsa_kv8_read(d: Dims, cache: KV8, k_out, v_out, cu_tokens, page_table, seq_l
     """k_out / v_out: bf16 [total_tokens][hkv][128], rows contiguous (any row stride)."""
     rows, k_stride, v_stride = _row_pair("hsa_kv8_read", k_out, v_out, d.hkv)
     rc = load().hsa_kv8_read(
-        ctypes.byref(d.c()), cache._ref, k_out.data_ptr(), k_stride, v_out.data_ptr(), v_stride,
-        _p(cu_tokens), rows, _p(page_table), _p(seq_lens), _p(ws),
+        ctypes.byref(d.c()), _cache("hsa_kv8_read", d, cache), k_out.data_ptr(), k_stride,
+        v_out.data_ptr(), v_stride, _p(cu_tokens), rows, _p(page_table), _p(seq_lens), _p(ws),
         0 if ws is None else ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check("hsa_kv8_read", rc)
@@ -463,15 +474,15 @@ def hsa_kv8_read(d: Dims, cache: KV8, k_out, v_out, cu_tokens, page_table, seq_l
 def hsa_kv8_decode(d: Dims, cache: KV8, q, page_table, seq_lens, out, lse, ws,
                    stream=None) -> None:
     _check("hsa_kv8_decode", load().hsa_kv8_decode(
-        ctypes.byref(d.c()), cache._ref, _p(q), _p(page_table), _p(seq_lens), _p(out), _p(lse),
-        _p(ws), ws.numel(), _stream(stream)))
+        ctypes.byref(d.c()), _cache("hsa_kv8_decode", d, cache), _p(q), _p(page_table),
+        _p(seq_lens), _p(out), _p(lse), _p(ws), ws.numel(), _stream(stream)))
 
 
 def hsa_kv8_attend(d: Dims, cache: KV8, q, page_table, seq_lens, block_idx, n_blocks, out, lse,
                    ws, stream=None) -> None:
     _check("hsa_kv8_attend", load().hsa_kv8_attend(
-        ctypes.byref(d.c()), cache._ref, _p(q), _p(page_table), _p(seq_lens), _p(block_idx),
-        _p(n_blocks), _p(out), _p(lse), _p(ws), ws.numel(), _stream(stream)))
+        ctypes.byref(d.c()), _cache("hsa_kv8_attend", d, cache), _p(q), _p(page_table),
+        _p(seq_lens), _p(block_idx), _p(n_blocks), _p(out), _p(lse), _p(ws), ws.numel(), _stream(stream)))
 
 
 def hsa_kv8_prefill(d: Dims, cache: KV8, q, cu_tokens, page_table, seq_lens, out, lse, ws,
@@ -481,9 +492,9 @@ def hsa_kv8_prefill(d: Dims, cache: KV8, q, cu_tokens, page_table, seq_lens, out
     if not out.is_contiguous() or out.shape != q.shape or out.dtype is not torch.bfloat16:
         raise HsaError("hsa_kv8_prefill", HSA_ERR_INVALID_ARG, "out must be contiguous, as q")
     rc = load().hsa_kv8_prefill(
-        ctypes.byref(d.c()), cache._ref, q.data_ptr(), q_stride, _p(cu_tokens), rows,
-        _p(page_table), _p(seq_lens), out.data_ptr(), _p(lse), _p(ws), ws.numel(),
-        _stream(stream))
+        ctypes.byref(d.c()), _cache("hsa_kv8_prefill", d, cache), q.data_ptr(), q_stride,
+        _p(cu_tokens), rows, _p(page_table), _p(seq_lens), out.data_ptr(), _p(lse), _p(ws),
+        ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check("hsa_kv8_prefill", rc)
 

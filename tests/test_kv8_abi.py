@@ -222,3 +222,77 @@ def test_the_binding_refuses_other_tensors():
                  (torch.zeros(5, 2, 256, dtype=torch.bfloat16)[..., ::2], rows)):
         with pytest.raises(hsa.HsaError):
             hsa.hsa_kv8_write(d, cache, x, y, None, None, None)
+
+
+def _aligned(shape, dtype):
+    """A zero CPU tensor on a 256-byte boundary (what the library's checks ask of device memory)."""
+    n = torch.Size(shape).numel() * torch.empty(0, dtype=dtype).element_size()
+    raw = torch.zeros(n + 256, dtype=torch.uint8)
+    off = -raw.data_ptr() % 256
+    return raw[off:off + n].view(dtype).view(shape)
+
+
+class NoLibrary:
+    """In the library's place: counts the calls that the binding lets through, runs none."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return 0
+        return call
+
+
+@pytest.fixture
+def binding(monkeypatch):
+    from kv_cache_int8_gb300 import hsa
+    lib = NoLibrary()
+    monkeypatch.setattr(hsa, "_LIB", lib)
+    monkeypatch.setattr(hsa, "_stream", lambda stream=None: 0)
+    return hsa, lib
+
+
+def binding_calls(hsa, d, cache, **kw):
+    """The five calls of the binding with valid tensors of d's sizes, but those given."""
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    B, T = d.batch, 5
+    a = dict(k=torch.zeros(T, d.hkv, 128, dtype=bf), v=torch.zeros(T, d.hkv, 128, dtype=bf),
+             rows=torch.zeros(T, d.hq, 128, dtype=bf), rows_out=torch.zeros(T, d.hq, 128, dtype=bf),
+             cu=torch.zeros(B + 1, dtype=i32), table=torch.zeros(B, d.max_pages_per_seq, dtype=i32),
+             lens=torch.zeros(B, dtype=i32), q=torch.zeros(B, d.hq, 128, dtype=bf),
+             idx=torch.zeros(B, d.hkv, d.k2, dtype=i32), cnt=torch.zeros(B, d.hkv, dtype=i32),
+             out=torch.zeros(B, d.hq, 128, dtype=f32), lse=torch.zeros(B, d.hq, dtype=f32),
+             ws=torch.zeros(64, dtype=torch.uint8))
+    a.update(kw)
+    lists = (a["cu"], a["table"], a["lens"])
+    return {
+        "write": lambda: hsa.hsa_kv8_write(d, cache, a["k"], a["v"], *lists),
+        "read": lambda: hsa.hsa_kv8_read(d, cache, a["k"], a["v"], *lists),
+        "decode": lambda: hsa.hsa_kv8_decode(d, cache, a["q"], a["table"], a["lens"], a["out"],
+                                             a["lse"], a["ws"]),
+        "attend": lambda: hsa.hsa_kv8_attend(d, cache, a["q"], a["table"], a["lens"], a["idx"],
+                                             a["cnt"], a["out"], a["lse"], a["ws"]),
+        "prefill": lambda: hsa.hsa_kv8_prefill(d, cache, a["rows"], *lists, a["rows_out"], None,
+                                               a["ws"]),
+    }
+
+
+def cpu_cache(hsa, pages, hkv):
+    return hsa.KV8(*(_aligned((pages, hkv, 16, 128), torch.int8) for _ in range(2)),
+                   *(_aligned((pages, hkv), torch.float32) for _ in range(2)))
+
+
+def test_the_binding_refuses_a_cache_of_other_sizes(binding):
+    hsa, lib = binding
+    d = dims(hsa, hq=4, hkv=2, num_pages=8, max_pages_per_seq=4)
+    for pages, hkv in ((8, 2), (9, 2)):  # the descriptor may leave pages out
+        for name, call in binding_calls(hsa, d, cpu_cache(hsa, pages, hkv)).items():
+            call()
+            assert lib.calls.pop() == "hsa_kv8_" + name
+    for pages, hkv in ((7, 2), (8, 1), (8, 4), (1, 2)):
+        for name, call in binding_calls(hsa, d, cpu_cache(hsa, pages, hkv)).items():
+            with pytest.raises(hsa.HsaError):
+                call()
+            assert not lib.calls, name
