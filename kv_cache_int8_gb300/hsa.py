@@ -427,6 +427,23 @@ def _cache(name: str, d: Dims, cache: KV8):
     return cache._ref
 
 
+def _dense(name: str, what: str, t, dtype, n: int) -> Optional[int]:
+    """The address of a contiguous tensor of n values (None stays None, an address itself)."""
+    if t is None or type(t) is int:
+        return t
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise HsaError(name, HSA_ERR_INVALID_ARG, f"{what} must be contiguous {dtype}, {n} values")
+    return t.data_ptr()
+
+
+def _heads(name: str, d: Dims, q, out, lse):
+    """The addresses of a decode attention's q, out and lse."""
+    n = d.batch * d.hq
+    return (_dense(name, "q", q, torch.bfloat16, n * 128),
+            _dense(name, "out", out, torch.float32, n * 128),
+            _dense(name, "lse", lse, torch.float32, n))
+
+
 def _rows(name: str, t, heads: int):
     """(rows, row stride) of a bf16 tensor [tokens][heads][128] whose rows are contiguous."""
     shape, stride = t.shape, t.stride()
@@ -473,16 +490,21 @@ def hsa_kv8_read(d: Dims, cache: KV8, k_out, v_out, cu_tokens, page_table, seq_l
 
 def hsa_kv8_decode(d: Dims, cache: KV8, q, page_table, seq_lens, out, lse, ws,
                    stream=None) -> None:
+    """q: bf16 [batch][hq][128]; out: float32, as q; lse: float32 [batch][hq] or None; all
+    contiguous."""
+    q, out, lse = _heads("hsa_kv8_decode", d, q, out, lse)
     _check("hsa_kv8_decode", load().hsa_kv8_decode(
-        ctypes.byref(d.c()), _cache("hsa_kv8_decode", d, cache), _p(q), _p(page_table),
-        _p(seq_lens), _p(out), _p(lse), _p(ws), ws.numel(), _stream(stream)))
+        ctypes.byref(d.c()), _cache("hsa_kv8_decode", d, cache), q, _p(page_table), _p(seq_lens),
+        out, lse, _p(ws), ws.numel(), _stream(stream)))
 
 
 def hsa_kv8_attend(d: Dims, cache: KV8, q, page_table, seq_lens, block_idx, n_blocks, out, lse,
                    ws, stream=None) -> None:
+    """q, out, lse: as hsa_kv8_decode."""
+    q, out, lse = _heads("hsa_kv8_attend", d, q, out, lse)
     _check("hsa_kv8_attend", load().hsa_kv8_attend(
-        ctypes.byref(d.c()), _cache("hsa_kv8_attend", d, cache), _p(q), _p(page_table),
-        _p(seq_lens), _p(block_idx), _p(n_blocks), _p(out), _p(lse), _p(ws), ws.numel(), _stream(stream)))
+        ctypes.byref(d.c()), _cache("hsa_kv8_attend", d, cache), q, _p(page_table), _p(seq_lens),
+        _p(block_idx), _p(n_blocks), out, lse, _p(ws), ws.numel(), _stream(stream)))
 
 
 def hsa_kv8_prefill(d: Dims, cache: KV8, q, cu_tokens, page_table, seq_lens, out, lse, ws,
@@ -491,9 +513,10 @@ def hsa_kv8_prefill(d: Dims, cache: KV8, q, cu_tokens, page_table, seq_lens, out
     rows, q_stride = _rows("hsa_kv8_prefill", q, d.hq)
     if not out.is_contiguous() or out.shape != q.shape or out.dtype is not torch.bfloat16:
         raise HsaError("hsa_kv8_prefill", HSA_ERR_INVALID_ARG, "out must be contiguous, as q")
+    lse = _dense("hsa_kv8_prefill", "lse", lse, torch.float32, rows * d.hq)
     rc = load().hsa_kv8_prefill(
         ctypes.byref(d.c()), _cache("hsa_kv8_prefill", d, cache), q.data_ptr(), q_stride,
-        _p(cu_tokens), rows, _p(page_table), _p(seq_lens), out.data_ptr(), _p(lse), _p(ws),
+        _p(cu_tokens), rows, _p(page_table), _p(seq_lens), out.data_ptr(), lse, _p(ws),
         ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check("hsa_kv8_prefill", rc)

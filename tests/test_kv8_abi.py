@@ -260,6 +260,7 @@ def binding_calls(hsa, d, cache, **kw):
     B, T = d.batch, 5
     a = dict(k=torch.zeros(T, d.hkv, 128, dtype=bf), v=torch.zeros(T, d.hkv, 128, dtype=bf),
              rows=torch.zeros(T, d.hq, 128, dtype=bf), rows_out=torch.zeros(T, d.hq, 128, dtype=bf),
+             rows_lse=torch.zeros(T, d.hq, dtype=f32),
              cu=torch.zeros(B + 1, dtype=i32), table=torch.zeros(B, d.max_pages_per_seq, dtype=i32),
              lens=torch.zeros(B, dtype=i32), q=torch.zeros(B, d.hq, 128, dtype=bf),
              idx=torch.zeros(B, d.hkv, d.k2, dtype=i32), cnt=torch.zeros(B, d.hkv, dtype=i32),
@@ -274,8 +275,8 @@ def binding_calls(hsa, d, cache, **kw):
                                              a["lse"], a["ws"]),
         "attend": lambda: hsa.hsa_kv8_attend(d, cache, a["q"], a["table"], a["lens"], a["idx"],
                                              a["cnt"], a["out"], a["lse"], a["ws"]),
-        "prefill": lambda: hsa.hsa_kv8_prefill(d, cache, a["rows"], *lists, a["rows_out"], None,
-                                               a["ws"]),
+        "prefill": lambda: hsa.hsa_kv8_prefill(d, cache, a["rows"], *lists, a["rows_out"],
+                                               a["rows_lse"], a["ws"]),
     }
 
 
@@ -296,3 +297,32 @@ def test_the_binding_refuses_a_cache_of_other_sizes(binding):
             with pytest.raises(hsa.HsaError):
                 call()
             assert not lib.calls, name
+
+
+def test_the_binding_refuses_arrays_that_it_would_misread(binding):
+    """The attentions read and write their arrays densely: a slice of a fused projection, another
+    type or another size would be misread or written past."""
+    hsa, lib = binding
+    d = dims(hsa, batch=3, hq=4, hkv=2, num_pages=8, max_pages_per_seq=4)
+    cache = cpu_cache(hsa, 8, 2)
+    bf, f32 = torch.bfloat16, torch.float32
+    fused = torch.zeros(3, 8, 128, dtype=bf)
+    for good in (dict(), dict(q=fused[:, :4].contiguous()), dict(out=torch.zeros(3, 512)),
+                 dict(q=torch.zeros(3, 1, 4, 128, dtype=bf)), dict(lse=None, rows_lse=None)):
+        for name, call in binding_calls(hsa, d, cache, **good).items():
+            call()
+            assert lib.calls.pop() == "hsa_kv8_" + name
+    for bad in (dict(q=fused[:, :4]), dict(q=torch.zeros(3, 4, 128)),
+                dict(q=fused[:2, :4].contiguous()), dict(out=torch.zeros(3, 4, 128, dtype=bf)),
+                dict(q=torch.zeros(3, 4, 256, dtype=bf)[..., ::2]),
+                dict(out=torch.zeros(3, 8, 128)[:, :4]), dict(out=torch.zeros(3, 4, 64)),
+                dict(out=torch.zeros(3, 4, 128, dtype=torch.float64)), dict(lse=torch.zeros(3)),
+                dict(lse=torch.zeros(3, 4, dtype=bf)), dict(lse=torch.zeros(3, 8)[:, ::2])):
+        calls = binding_calls(hsa, d, cache, **bad)
+        for name in ("decode", "attend"):
+            with pytest.raises(hsa.HsaError):
+                calls[name]()
+    for bad in (torch.zeros(5, 3), torch.zeros(5, 4, dtype=bf), torch.zeros(5, 8)[:, :4]):
+        with pytest.raises(hsa.HsaError):
+            binding_calls(hsa, d, cache, rows_lse=bad)["prefill"]()
+    assert not lib.calls
