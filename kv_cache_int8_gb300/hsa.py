@@ -427,6 +427,25 @@ def _cache(name: str, d: Dims, cache: KV8):
     return cache._ref
 
 
+def _list(name: str, t) -> Optional[int]:
+    """The address of a page table, of lengths, blocks or their numbers."""
+    if t is None or type(t) is int:
+        return t
+    if t.dtype is not torch.int32:
+        raise HsaError(name, HSA_ERR_INVALID_ARG, "page tables, lengths and blocks are torch.int32")
+    return t.data_ptr()
+
+
+def _offsets(name: str, d: Dims, cu) -> Optional[int]:
+    """The address of the new tokens' offsets: contiguous int32, batch + 1 of them at least."""
+    if cu is None or type(cu) is int:
+        return cu
+    if cu.dtype is not torch.int32 or cu.numel() <= d.batch or not cu.is_contiguous():
+        raise HsaError(name, HSA_ERR_INVALID_ARG,
+                       "cu_tokens must be contiguous torch.int32, batch + 1 offsets")
+    return cu.data_ptr()
+
+
 def _dense(name: str, what: str, t, dtype, n: int) -> Optional[int]:
     """The address of a contiguous tensor of n values (None stays None, an address itself)."""
     if t is None or type(t) is int:
@@ -467,59 +486,66 @@ def _row_pair(name: str, k, v, heads: int):
 def hsa_kv8_write(d: Dims, cache: KV8, k_new, v_new, cu_tokens, page_table, seq_lens, ws=None,
                   stream=None) -> None:
     """k_new / v_new: bf16 [total_tokens][hkv][128], rows contiguous (any row stride)."""
-    rows, k_stride, v_stride = _row_pair("hsa_kv8_write", k_new, v_new, d.hkv)
+    name = "hsa_kv8_write"
+    rows, k_stride, v_stride = _row_pair(name, k_new, v_new, d.hkv)
     rc = load().hsa_kv8_write(
-        ctypes.byref(d.c()), _cache("hsa_kv8_write", d, cache), k_new.data_ptr(), k_stride,
-        v_new.data_ptr(), v_stride, _p(cu_tokens), rows, _p(page_table), _p(seq_lens), _p(ws),
-        0 if ws is None else ws.numel(), _stream(stream))
+        ctypes.byref(d.c()), _cache(name, d, cache), k_new.data_ptr(), k_stride, v_new.data_ptr(),
+        v_stride, _offsets(name, d, cu_tokens), rows, _list(name, page_table),
+        _list(name, seq_lens), _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
     if rc != HSA_OK:
-        _check("hsa_kv8_write", rc)
+        _check(name, rc)
 
 
 def hsa_kv8_read(d: Dims, cache: KV8, k_out, v_out, cu_tokens, page_table, seq_lens, ws=None,
                  stream=None) -> None:
     """k_out / v_out: bf16 [total_tokens][hkv][128], rows contiguous (any row stride)."""
-    rows, k_stride, v_stride = _row_pair("hsa_kv8_read", k_out, v_out, d.hkv)
+    name = "hsa_kv8_read"
+    rows, k_stride, v_stride = _row_pair(name, k_out, v_out, d.hkv)
     rc = load().hsa_kv8_read(
-        ctypes.byref(d.c()), _cache("hsa_kv8_read", d, cache), k_out.data_ptr(), k_stride,
-        v_out.data_ptr(), v_stride, _p(cu_tokens), rows, _p(page_table), _p(seq_lens), _p(ws),
-        0 if ws is None else ws.numel(), _stream(stream))
+        ctypes.byref(d.c()), _cache(name, d, cache), k_out.data_ptr(), k_stride, v_out.data_ptr(),
+        v_stride, _offsets(name, d, cu_tokens), rows, _list(name, page_table),
+        _list(name, seq_lens), _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
     if rc != HSA_OK:
-        _check("hsa_kv8_read", rc)
+        _check(name, rc)
 
 
 def hsa_kv8_decode(d: Dims, cache: KV8, q, page_table, seq_lens, out, lse, ws,
                    stream=None) -> None:
     """q: bf16 [batch][hq][128]; out: float32, as q; lse: float32 [batch][hq] or None; all
     contiguous."""
-    q, out, lse = _heads("hsa_kv8_decode", d, q, out, lse)
-    _check("hsa_kv8_decode", load().hsa_kv8_decode(
-        ctypes.byref(d.c()), _cache("hsa_kv8_decode", d, cache), q, _p(page_table), _p(seq_lens),
-        out, lse, _p(ws), ws.numel(), _stream(stream)))
+    name = "hsa_kv8_decode"
+    q, out, lse = _heads(name, d, q, out, lse)
+    _check(name, load().hsa_kv8_decode(
+        ctypes.byref(d.c()), _cache(name, d, cache), q, _list(name, page_table),
+        _list(name, seq_lens), out, lse, _p(ws), ws.numel(), _stream(stream)))
 
 
 def hsa_kv8_attend(d: Dims, cache: KV8, q, page_table, seq_lens, block_idx, n_blocks, out, lse,
                    ws, stream=None) -> None:
     """q, out, lse: as hsa_kv8_decode."""
-    q, out, lse = _heads("hsa_kv8_attend", d, q, out, lse)
-    _check("hsa_kv8_attend", load().hsa_kv8_attend(
-        ctypes.byref(d.c()), _cache("hsa_kv8_attend", d, cache), q, _p(page_table), _p(seq_lens),
-        _p(block_idx), _p(n_blocks), out, lse, _p(ws), ws.numel(), _stream(stream)))
+    name = "hsa_kv8_attend"
+    q, out, lse = _heads(name, d, q, out, lse)
+    _check(name, load().hsa_kv8_attend(
+        ctypes.byref(d.c()), _cache(name, d, cache), q, _list(name, page_table),
+        _list(name, seq_lens), _list(name, block_idx), _list(name, n_blocks), out, lse, _p(ws),
+        ws.numel(), _stream(stream)))
 
 
 def hsa_kv8_prefill(d: Dims, cache: KV8, q, cu_tokens, page_table, seq_lens, out, lse, ws,
                     stream=None) -> None:
-    """q: bf16 [total_tokens][hq][128], rows contiguous (any row stride); out: bf16, contiguous."""
-    rows, q_stride = _rows("hsa_kv8_prefill", q, d.hq)
+    """q: bf16 [total_tokens][hq][128], rows contiguous (any row stride); out: bf16, contiguous;
+    lse: float32 [total_tokens][hq], contiguous, or None."""
+    name = "hsa_kv8_prefill"
+    rows, q_stride = _rows(name, q, d.hq)
     if not out.is_contiguous() or out.shape != q.shape or out.dtype is not torch.bfloat16:
-        raise HsaError("hsa_kv8_prefill", HSA_ERR_INVALID_ARG, "out must be contiguous, as q")
-    lse = _dense("hsa_kv8_prefill", "lse", lse, torch.float32, rows * d.hq)
+        raise HsaError(name, HSA_ERR_INVALID_ARG, "out must be contiguous, as q")
+    lse = _dense(name, "lse", lse, torch.float32, rows * d.hq)
     rc = load().hsa_kv8_prefill(
-        ctypes.byref(d.c()), _cache("hsa_kv8_prefill", d, cache), q.data_ptr(), q_stride,
-        _p(cu_tokens), rows, _p(page_table), _p(seq_lens), out.data_ptr(), lse, _p(ws),
-        ws.numel(), _stream(stream))
+        ctypes.byref(d.c()), _cache(name, d, cache), q.data_ptr(), q_stride,
+        _offsets(name, d, cu_tokens), rows, _list(name, page_table), _list(name, seq_lens),
+        out.data_ptr(), lse, _p(ws), ws.numel(), _stream(stream))
     if rc != HSA_OK:
-        _check("hsa_kv8_prefill", rc)
+        _check(name, rc)
 
 
 def hsa_read_device_error(ws, stream=None) -> int:

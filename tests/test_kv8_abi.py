@@ -326,3 +326,29 @@ def test_the_binding_refuses_arrays_that_it_would_misread(binding):
         with pytest.raises(hsa.HsaError):
             binding_calls(hsa, d, cache, rows_lse=bad)["prefill"]()
     assert not lib.calls
+
+
+def test_the_binding_refuses_lists_of_another_type(binding):
+    """int64 lists (torch.cumsum's, for one, of int32 lengths) would be read as twice as many
+    int32, every other one 0."""
+    hsa, lib = binding
+    d = dims(hsa, batch=3, hq=4, hkv=2, num_pages=8, max_pages_per_seq=4)
+    cache = cpu_cache(hsa, 8, 2)
+    lens = torch.tensor([2, 3, 4], dtype=torch.int32)
+    i32 = torch.int32
+    for good in (dict(cu=torch.zeros(9, dtype=i32)), dict(cu=None)):
+        for name in ("write", "read", "prefill"):
+            binding_calls(hsa, d, cache, **good)[name]()
+            assert lib.calls.pop() == "hsa_kv8_" + name
+    for bad in (torch.cumsum(lens, 0), torch.zeros(4), torch.zeros(3, dtype=i32),
+                torch.zeros(8, dtype=i32)[::2]):
+        for name in ("write", "read", "prefill"):
+            with pytest.raises(hsa.HsaError):
+                binding_calls(hsa, d, cache, cu=bad)[name]()
+    for bad, names in ((dict(lens=lens.long()), ALL), (dict(table=torch.zeros(3, 4).long()), ALL),
+                       (dict(idx=torch.zeros(3, 2, 4).long()), ("attend",)),
+                       (dict(cnt=torch.zeros(3, 2)), ("attend",))):
+        for name in names:
+            with pytest.raises(hsa.HsaError):
+                binding_calls(hsa, d, cache, **bad)[name]()
+    assert not lib.calls
