@@ -464,12 +464,13 @@ def _heads(name: str, d: Dims, q, out, lse):
 
 
 def _rows(name: str, t, heads: int):
-    """(rows, row stride) of a bf16 tensor [tokens][heads][128] whose rows are contiguous."""
+    """(rows, row stride) of a bf16 tensor [tokens][heads][128] whose rows are contiguous. A
+    single row's stride means nothing and may be any: it is given the row's length."""
     shape, stride = t.shape, t.stride()
     if (t.dtype is not torch.bfloat16 or len(stride) != 3 or shape[1] != heads or
             shape[2] != 128 or stride[2] != 1 or (stride[1] != 128 and heads > 1)):
         raise HsaError(name, HSA_ERR_INVALID_ARG, "rows must be bf16 [tokens][heads][128]")
-    return shape[0], stride[0]
+    return shape[0], stride[0] if shape[0] > 1 else heads * 128
 
 
 def _row_pair(name: str, k, v, heads: int):
@@ -480,6 +481,8 @@ def _row_pair(name: str, k, v, heads: int):
             (heads > 1 and (ks[1] != 128 or vs[1] != 128))):
         raise HsaError(name, HSA_ERR_INVALID_ARG,
                        "k and v must be bf16 [tokens][heads][128], of as many rows")
+    if shape[0] < 2:
+        return shape[0], heads * 128, heads * 128
     return shape[0], ks[0], vs[0]
 
 

@@ -352,3 +352,26 @@ def test_the_binding_refuses_lists_of_another_type(binding):
             with pytest.raises(hsa.HsaError):
                 binding_calls(hsa, d, cache, **bad)[name]()
     assert not lib.calls
+
+
+def test_a_single_row_may_have_any_stride(binding, monkeypatch):
+    """One token taken out of a [heads][tokens][128] tensor: its rows are contiguous, the stride
+    between them is the heads'."""
+    hsa, lib = binding
+    d = dims(hsa, batch=1, hq=4, hkv=2, num_pages=8, max_pages_per_seq=4)
+    cache = cpu_cache(hsa, 8, 2)
+    got = []
+    lib.hsa_kv8_write = lambda *a: got.append((a[7], a[3], a[5])) or 0
+    lib.hsa_kv8_prefill = lambda *a: got.append((a[5], a[3])) or 0
+    one = torch.zeros(2, 1, 128, dtype=torch.bfloat16).transpose(0, 1)
+    many = torch.zeros(7, 8, 128, dtype=torch.bfloat16)
+    assert one.stride() == (128, 128, 1)
+    for k in (one, many[:1, 2:4], many[3:4, :2], one.expand(1, 2, 128)):
+        binding_calls(hsa, d, cache, k=k, v=one, cu=None)["write"]()
+        assert got.pop() == (1, 256, 256)
+    q = torch.zeros(4, 1, 128, dtype=torch.bfloat16).transpose(0, 1)
+    binding_calls(hsa, d, cache, rows=q, rows_out=torch.zeros(1, 4, 128, dtype=torch.bfloat16),
+                  rows_lse=None, cu=None)["prefill"]()
+    assert got.pop() == (1, 512)
+    binding_calls(hsa, d, cache, k=many[:5, 2:4], v=many[:5, 4:6])["write"]()
+    assert got.pop() == (5, 1024, 1024)
