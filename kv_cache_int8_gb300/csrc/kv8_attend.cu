@@ -42,6 +42,7 @@
 // joining); 8K tokens: 12 us; 128 kept blocks, sink and window of 128K: 11.8 us.
 #include "kv8.cuh"
 
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
@@ -158,6 +159,24 @@ __device__ __forceinline__ float sum32(float x) {
   return x;
 }
 
+// Waits with a limit, the warp's lanes alike: a wait that runs out does so for all of them, as
+// what follows (shuffles, products) takes them all.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+    if (__any_sync(0xffffffffu, clock64() - t0 > kWaitLimitCycles)) return false;
+  return true;
+}
+
+__device__ __noinline__ void wait_for_all(uint64_t* full, int slot, uint32_t ph, int n) {
+  for (; n > 0; n--) {
+    warp_wait(full + slot, ph);
+    ph ^= slot == kStages - 1;
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+  }
+}
+
 // Units (blocks to visit) of a row of a sequence of n tokens. Kept form: the sink's blocks, the
 // window's, then k2 places for kept blocks.
 template <bool kKept>
@@ -170,9 +189,10 @@ __device__ __forceinline__ int row_units(const Params& p, int n) {
 }
 
 // One visit: the block's first row in the code arrays, its slots [lo, hi), its scales.
+constexpr int kFar = INT_MIN;  // of a span: the loop's plain form does not take s_v
 struct alignas(16) Unit {
   int y;
-  int span;       // lo | hi << 8; 0: nothing to do
+  int span;       // lo | hi << 8, negative with kFar; 0: nothing to do
   float sk, sv;  // the scales; sv as it is used: log2 s_v (-inf for a block of zeros)
 };
 
@@ -230,6 +250,7 @@ __device__ __forceinline__ Unit locate(const Params& p, const long long* pre, co
   t.sk = p.k_scale[block];
   const float sv = p.v_scale[block];
   t.sv = lg2(sv);
+  if (!(fabsf(t.sv) <= kPlainScale)) t.span |= kFar;
   return t;
 }
 
@@ -415,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t phase = 0;        // of the barriers that `out` comes to
   unsigned char* const ring = sm.ring[warp][0];
   uint64_t* const full = sm.full[warp];
-  bool dead = false;
+  bool dead = false;  // a copy did not come: no further ones, no further work
   // Begins the copies of the visits before `upto`. Those of later rows (from visit `stop` on)
   // leave one slot of the ring free: the row's outputs will lie there.
   auto issue_to = [&](int upto, int stop) {
@@ -491,12 +512,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; c++) o[k][c] = 0.0f;
 
     // Two visits at a time: two independent chains of products, one reduction of the maximum.
-    // kApart: l0 and l1 are the lanes' sums of 2^(x - top), not of 2^(y - m + kHeadroom) / s_v.
+    // kApart: one, and l0 and l1 are the lanes' sums of 2^(x - top), not of 2^(y - m + kHeadroom)
+    // / s_v.
     bool apart = false;
     float top0, top1;
     auto visit = [&](auto form) {
       constexpr bool kApart = decltype(form)::value;
-      const int two = i + 1 < i_stop;
+      constexpr int kPair = kApart ? 1 : 2;  // visits
+      const int two = !kApart && i + 1 < i_stop;
       if (!pending && filled < mine && filled - i <= kBatch) {
         ahead = fetch(filled);
         pending = true;
@@ -507,21 +530,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const Unit ua = meta[i % kMeta];
       Unit ub = meta[(i + 1) % kMeta];
-      if (!two) ub.span = 0, ub.sv = 0.0f;
-      if (!kApart && !(fmaxf(fabsf(ua.sv), fabsf(ub.sv)) <= kPlainScale)) {
-        apart = true;
-        return;
-      }
-      if ((ua.span | ub.span) != 0 && !dead) {
+      if (!two) ub.span = 0;
+      const int spans = ua.span | ub.span;
+      if (kApart ? spans != 0 && !dead : spans > 0 && !dead) {
         uint32_t kb[2];
-        const int span[2] = {ua.span, ub.span};
+        const int mask = kApart ? ~kFar : -1;
+        const int span[2] = {ua.span & mask, ub.span & mask};
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
+        for (int h = 0; h < kPair; h++) {
           kb[h] = smem_addr(ring) + out * kUnitBytes;
           if (span[h] == 0) continue;
-          if (!mbar_wait(full + out, phase)) {
+          if (!warp_wait(full + out, phase)) {
             set_error(p.err, kDevErrTimeout);
             dead = true;
+            // copies under way write this CTA's shared memory: one more wait for each
+            wait_for_all(full, out, phase, flying);
           }
           flying--;
           out++;
@@ -536,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 2; c++) {
           uint4 ka[2], kc[2];
 #pragma unroll
-          for (int h = 0; h < 2; h++) {
+          for (int h = 0; h < kPair; h++) {
             const uint32_t at = kb[h] + g * kHeadDim + (((2 * t + c) ^ g) << 4);
             ka[h] = lds128(at);
             kc[h] = lds128(at + 8 * kHeadDim);
@@ -544,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int w = 0; w < 4; w++)
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
+            for (int h = 0; h < kPair; h++) {
               const uint32_t a = Codes<F>::prepare(word(ka[h], w));
               const uint32_t d = Codes<F>::prepare(word(kc[h], w));
               const uint32_t a0 = Codes<F>::template pair<0>(a), a1 = Codes<F>::template pair<0>(d);
@@ -557,31 +580,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float cv[2] = {ua.sv, ub.sv};
         if (kApart) {
-          float z[2][4], z0 = top0, z1 = top1;
+          float z[4];
+          const int lo = span[0] & 255, hi = span[0] >> 8;
 #pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const float sk = h ? ub.sk : ua.sk;
-            const int lo = span[h] & 255, hi = span[h] >> 8;
-#pragma unroll
-            for (int c = 0; c < 4; c++) {
-              const int tok = g + 4 * (c & 2);
-              z[h][c] = tok >= lo && tok < hi ? x[h][c] * ((c & 1 ? f1 : f0) * sk) : -INFINITY;
-            }
-            z0 = fmaxf(z0, fmaxf(z[h][0], z[h][2]));
-            z1 = fmaxf(z1, fmaxf(z[h][1], z[h][3]));
+          for (int c = 0; c < 4; c++) {
+            const int tok = g + 4 * (c & 2);
+            z[c] = tok >= lo && tok < hi ? x[0][c] * ((c & 1 ? f1 : f0) * ua.sk) : -INFINITY;
           }
+          float z0 = fmaxf(top0, fmaxf(z[0], z[2])), z1 = fmaxf(top1, fmaxf(z[1], z[3]));
           z0 = max_tokens(z0);  // finite, as one token at least is seen
           z1 = max_tokens(z1);
-          l0 = l0 * ex2(top0 - z0) + (ex2(z[0][0] - z0) + ex2(z[0][2] - z0)) +
-               (ex2(z[1][0] - z0) + ex2(z[1][2] - z0));
-          l1 = l1 * ex2(top1 - z1) + (ex2(z[0][1] - z1) + ex2(z[0][3] - z1)) +
-               (ex2(z[1][1] - z1) + ex2(z[1][3] - z1));
+          l0 = l0 * ex2(top0 - z0) + (ex2(z[0] - z0) + ex2(z[2] - z0));
+          l1 = l1 * ex2(top1 - z1) + (ex2(z[1] - z1) + ex2(z[3] - z1));
           top0 = z0;
           top1 = z1;
         }
         float n0 = -INFINITY, n1 = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {  // y = x + log2 s_v
+        for (int h = 0; h < kPair; h++) {  // y = x + log2 s_v
           const float sk = h ? ub.sk : ua.sk;
           x[h][0] = fmaf(x[h][0], f0 * sk, cv[h]);
           x[h][1] = fmaf(x[h][1], f1 * sk, cv[h]);
@@ -620,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float ref0 = m0 - kHeadroom, ref1 = m1 - kHeadroom;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
+        for (int h = 0; h < kPair; h++) {
           if (span[h] == 0) continue;
           const float p00 = ex2(x[h][0] - ref0), p01 = ex2(x[h][1] - ref1);
           const float p10 = ex2(x[h][2] - ref0), p11 = ex2(x[h][3] - ref1);
@@ -669,13 +685,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+      } else if (!kApart && __builtin_expect(spans < 0, 0)) {
+        apart = true;
+        return;
       }
       i += 1 + two;
       __syncwarp();  // the slots are read before they are filled again
       issue_to(i + kStages, i_stop);
     };
     while (i < i_stop && !apart) visit(std::false_type{});
-    if (apart) {
+    if (__builtin_expect(apart, 0)) {
       top0 = m0 - kHeadroom;
       top1 = m1 - kHeadroom;
       m0 = fmaxf(m0, kLow);  // before any block but those of zeros: y is -inf, m must not be
