@@ -112,6 +112,7 @@ struct Smem {
   alignas(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[3],
       p_full[3][2], o_full[2];  // s_full, p_full: kOdd; p_full[..][half of the tokens]
   uint64_t pv_done, h_done[2];  // products with V complete: one tile's step, a first half
+  uint64_t all_done;            // all products, after a wait that ran out
   long long per;
   int start_b, start_h, start_q, start_off;
   uint32_t tmem;
@@ -305,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     mbar_init(&sm.p_full[kOdd][0], 128);
     mbar_init(&sm.p_full[kOdd][1], 128);
     mbar_init(&sm.pv_done, 1);
+    mbar_init(&sm.all_done, 1);
     sm.dead = 0;
     fence_barrier_init();
   }
@@ -1026,6 +1028,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     if (ok && step > 0) {
       wait(sm, &sm.k_empty[(step - 1) & 1], ((step - 1) >> 1) & 1, p.err);
       wait(sm, &sm.v_empty[(step - 1) & 1], ((step - 1) >> 1) & 1, p.err);
+    }
+    // nor may products go on in shared and tensor memory that are given up
+    if (!ok) {
+      if (lead) tc::commit(&sm.all_done);
+      mbar_wait(&sm.all_done, 0);
     }
   }
   tc::fence_before();
