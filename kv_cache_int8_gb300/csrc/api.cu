@@ -268,8 +268,23 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Two views of the key-code cache, both stored with the 128-byte swizzle. map: 2-D, rows of
-// 128 bytes (one token of 8-bit codes, two of 4-bit codes), a box is one (page, head) block.
+// 2-D, rows of 128 bytes (one token of 8-bit codes, two of 4-bit codes), stored with the 128-byte
+// swizzle; a box is one (page, head) block of `block_rows` rows.
+int32_t encode_block_map(const void* codes, long long blocks, int block_rows, CUtensorMap* map) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return HSA_ERR_CUDA;
+  cuuint64_t dims[2] = {(cuuint64_t)hsa::kHeadDim, (cuuint64_t)(blocks * block_rows)};
+  cuuint64_t strides[1] = {(cuuint64_t)hsa::kHeadDim};
+  cuuint32_t box[2] = {(cuuint32_t)hsa::kHeadDim, (cuuint32_t)block_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? HSA_OK : HSA_ERR_CUDA;
+}
+
+// Two views of the key-code cache, both stored with the 128-byte swizzle. map: as above.
 // map4: 4-D [page][head][row][128 B], a box is the blocks of one head in 4 consecutive pages
 // (one copy instead of four where the page table is contiguous).
 int32_t encode_kq_map(const Shape& s, const int8_t* kq, CUtensorMap* map, CUtensorMap* map4) {
@@ -286,7 +301,6 @@ int32_t encode_kq_map(const Shape& s, const int8_t* kq, CUtensorMap* map, CUtens
   thread_local int next = 0;
   // 8-bit codes: one 128-byte row per token, 16 rows a block; 4-bit: two tokens a row
   const int rows_per_block = s.key_bits == 4 ? hsa::kPage / 2 : hsa::kPage;
-  const long long rows = (long long)s.num_pages * s.hkv * rows_per_block;
   for (int i = 0; i < kKeep; i++) {
     const Entry& e = kept[i];
     if (e.kq == kq && e.pages == s.num_pages && e.hkv == s.hkv &&
@@ -296,22 +310,17 @@ int32_t encode_kq_map(const Shape& s, const int8_t* kq, CUtensorMap* map, CUtens
       return HSA_OK;
     }
   }
+  const int32_t rc = encode_block_map(kq, (long long)s.num_pages * s.hkv, rows_per_block, map);
+  if (rc != HSA_OK) return rc;
   auto fn = encode_fn();
-  if (fn == nullptr) return HSA_ERR_CUDA;
-  cuuint64_t dims[2] = {(cuuint64_t)hsa::kHeadDim, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)hsa::kHeadDim};
-  cuuint32_t box[2] = {(cuuint32_t)hsa::kHeadDim, (cuuint32_t)rows_per_block};
   cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(kq), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return HSA_ERR_CUDA;
   const cuuint64_t blk = (cuuint64_t)rows_per_block * hsa::kHeadDim;  // bytes per block
   cuuint64_t dims4[4] = {(cuuint64_t)hsa::kHeadDim, (cuuint64_t)rows_per_block,
                          (cuuint64_t)s.hkv, (cuuint64_t)s.num_pages};
   cuuint64_t strides4[3] = {(cuuint64_t)hsa::kHeadDim, blk, blk * s.hkv};
   cuuint32_t box4[4] = {(cuuint32_t)hsa::kHeadDim, (cuuint32_t)rows_per_block, 1, 4};
-  r = fn(map4, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<int8_t*>(kq), dims4, strides4, box4,
+  const CUresult r =
+      fn(map4, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<int8_t*>(kq), dims4, strides4, box4,
          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return HSA_ERR_CUDA;
@@ -558,10 +567,12 @@ int32_t do_kv8_attend(const hsa_dims* d, const hsa_kv8* cache, bool kept, const 
                       (s.per_head ? s.hq : s.hkv) >
                   UINT32_MAX)
     return HSA_ERR_UNSUPPORTED;
-  s.key_bits = 8;  // the codes' tensor maps: 16 rows of 128 bytes a block
-  CUtensorMap km, vm, four;
-  rc = encode_kq_map(s, static_cast<const int8_t*>(c.k), &km, &four);
-  if (rc == HSA_OK) rc = encode_kq_map(s, static_cast<const int8_t*>(c.v), &vm, &four);
+  // Encoded anew in every call: two maps of the kind needed cost less than looking them up in the
+  // scorer's table, whose entries (one a layer) two more a layer would push out.
+  CUtensorMap km, vm;
+  const long long blocks = (long long)s.num_pages * s.hkv;
+  rc = encode_block_map(c.k, blocks, hsa::kPage, &km);
+  if (rc == HSA_OK) rc = encode_block_map(c.v, blocks, hsa::kPage, &vm);
   if (rc != HSA_OK) return rc;
   char* ws = static_cast<char*>(workspace);
   return cuda_status(hsa::launch_kv8_attend(

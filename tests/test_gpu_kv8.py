@@ -926,3 +926,32 @@ def test_prompts_of_stretches_longer_than_the_products_add_up(hq, n, m):
             # are no larger than max |v|
             tol["out"] = tol["out"] + (2.0 ** -11 + 2.0 ** -12) * np.abs(v).max()
             assert_rows(out[b * m + i, j], lse[b * m + i, j], want, wl, tol, 2.0 ** -8)
+
+
+def test_many_layers_in_turn():
+    """70 caches of one shape in turn, beside as many key-code caches of the scorer's: each call
+    reads its own."""
+    d = hsa.Dims(batch=1, hq=4, hkv=1, max_pages_per_seq=1, num_pages=1, k2=1, sink=0, window=1)
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([9], dtype=torch.int32, device="cuda")
+    q = torch.ones(1, 4, D, device="cuda", dtype=torch.bfloat16)
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_DECODE)
+    layers = []
+    for i in range(70):
+        cache = hsa.KV8.zeros(d)
+        cache.v.fill_(i)
+        cache.v_scale.fill_(1.0)
+        kq = torch.full((1, 1, 16, D), i, dtype=torch.int8, device="cuda")
+        layers.append((cache, kq, torch.zeros(1, 4, D, device="cuda"),
+                       torch.zeros(1, 1, 1, dtype=torch.int32, device="cuda")))
+    k_scale = torch.ones(1, 1, D, device="cuda")
+    for _ in range(2):
+        for cache, kq, out, block_max in layers:
+            hsa.hsa_score_blocks(d, q, kq, k_scale, table, lens, block_max)
+            hsa.hsa_kv8_decode(d, cache, q, table, lens, out, None, ws)
+    first = int(layers[1][3][0, 0, 0])
+    assert first > 0
+    for i, (_, _, out, block_max) in enumerate(layers):
+        # 9 equal weights of one value: sums of whole numbers, one division
+        np.testing.assert_allclose(out.cpu().numpy(), i, rtol=2.0 ** -21)
+        assert abs(int(block_max[0, 0, 0]) - i * first) <= i  # scores grow with the codes
