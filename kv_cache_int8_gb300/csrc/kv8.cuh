@@ -32,8 +32,8 @@ __device__ __forceinline__ NewSpan new_span(const NewRows& r, int b) {
   s.row0 = r.cu ? r.cu[b] : b;
   s.n = r.cu ? r.cu[b + 1] - s.row0 : 1;
   s.start = len - s.n;
-  s.bad = s.n < 0 || s.row0 < 0 || (long long)s.row0 + s.n > r.total || s.start < 0 ||
-          len > r.max_pages * kPage;
+  s.bad = s.n < 0 || s.row0 < 0 || (long long)s.row0 + s.n > r.total || len < s.n ||
+          len > r.max_pages * kPage;  // (start itself may have wrapped around)
   if (s.bad) s.n = 0;
   return s;
 }

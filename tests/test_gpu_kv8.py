@@ -955,3 +955,33 @@ def test_many_layers_in_turn():
         # 9 equal weights of one value: sums of whole numbers, one division
         np.testing.assert_allclose(out.cpu().numpy(), i, rtol=2.0 ** -21)
         assert abs(int(block_max[0, 0, 0]) - i * first) <= i  # scores grow with the codes
+
+
+def test_lengths_far_below_zero_are_reported():
+    """-2^31 less one new token is a large position in 32 bits: the sequence is left out all the
+    same, and the others are not."""
+    s = Batch([40, 40], 2, 1, "int8", seed=1)
+    d, cache, table, err = s.dims(), s.gpu_cache(), s.gpu_table(), error_word()
+    before = codes_of(cache)
+    q = to_bf16(s.rng.standard_normal((6, 2, D)))
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_PREFILL)
+    for n in (-2 ** 31, -2 ** 31 + 2, -1):
+        lens = torch.tensor([n, 40], dtype=torch.int32, device="cuda")
+        for cu in (cu_of([3, 3]), None):
+            m = 3 if cu is not None else 1
+            k = torch.full((2 * m, 1, D), 2.0, dtype=torch.bfloat16, device="cuda")
+            hsa.hsa_kv8_read(d, cache, k, k.clone(), cu, table, lens, err)
+            assert hsa.hsa_read_device_error(err) == hsa.HSA_ERR_DEVICE_CHECK
+            assert (k[:m] == 2.0).all() and not (k[m:] == 2.0).all()
+            hsa.hsa_kv8_write(d, cache, k, k, cu, table, lens, err)
+            assert hsa.hsa_read_device_error(err) == hsa.HSA_ERR_DEVICE_CHECK
+            out = torch.full((2 * m, 2, D), 9.0, dtype=torch.bfloat16, device="cuda")
+            lse = torch.full((2 * m, 2), 9.0, device="cuda")
+            hsa.hsa_kv8_prefill(d, cache, q[:2 * m], cu, table, lens, out, lse, ws)
+            assert hsa.hsa_read_device_error(ws) == hsa.HSA_ERR_DEVICE_CHECK
+            assert not out[:m].any() and torch.isneginf(lse[:m]).all()
+            assert torch.isfinite(lse[m:]).all() and out[m:].any(-1).all()
+    after = codes_of(cache)
+    other = np.setdiff1d(np.arange(s.num_pages), s.table[1])
+    for name in before:
+        np.testing.assert_array_equal(after[name][other], before[name][other])
