@@ -24,6 +24,13 @@ using append_detail::unpack8;
 
 constexpr int kWarps = 8;  // work items a CTA
 
+// One warp behind the units: sequences that do not fit (offsets that lead outside the arrays may
+// have no unit at all).
+__device__ __forceinline__ void report_bad(const NewRows& rows, int lane, int* err) {
+  for (int b = lane; b < rows.batch; b += 32)
+    if (new_span(rows, b).bad) set_error(err, kDevErrCheck);
+}
+
 struct WriteSide {
   const __nv_bfloat16* x;  // rows
   long long stride;        // elements
@@ -96,15 +103,15 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_write_kernel(
   grid_dep_wait();
   grid_dep_launch();
   const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (unit >= units) return;
   const int lane = threadIdx.x & 31;
+  if (unit == units) report_bad(rows, lane, err);
+  if (unit >= units) return;
   const bool is_v = unit & 1;
   const int h = (unit >> 1) % hkv, item = (unit >> 1) / hkv;
   const WriteSide& w = is_v ? vs : ks;
   const int b = rows.cu ? item_sequence(rows, item) : item;
   const NewSpan sp = new_span(rows, b);
   const int j = rows.cu ? item - item_base(rows, b) : 0;
-  if (sp.bad && j == 0 && lane == 0) set_error(err, kDevErrCheck);
   const int end = sp.start + sp.n;  // N_b
   const long long p = (long long)sp.start / kPage + j;
   if (sp.n == 0 || j < 0 || p * kPage >= end) return;
@@ -211,15 +218,15 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_read_kernel(
   grid_dep_wait();
   grid_dep_launch();
   const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (unit >= units) return;
   const int lane = threadIdx.x & 31;
+  if (unit == units) report_bad(rows, lane, err);
+  if (unit >= units) return;
   const bool is_v = unit & 1;
   const int h = (unit >> 1) % hkv, item = (unit >> 1) / hkv;
   const ReadSide& r = is_v ? vs : ks;
   const int b = rows.cu ? item_sequence(rows, item) : item;
   const NewSpan sp = new_span(rows, b);
   const int j = rows.cu ? item - item_base(rows, b) : 0;
-  if (sp.bad && j == 0 && lane == 0) set_error(err, kDevErrCheck);
   const int end = sp.start + sp.n;
   const long long p = (long long)sp.start / kPage + j;
   if (sp.n == 0 || j < 0 || p * kPage >= end) return;
@@ -267,7 +274,7 @@ cudaError_t launch_kv8_write(const Shape& s, const Kv8& c, const void* k_new, lo
                         static_cast<uint8_t*>(c.v), c.v_scale};
   const int units = new_block_items(s.batch, total, cu != nullptr) * s.hkv * 2;
   auto kernel = c.format == kE4m3 ? kv8_write_kernel<kE4m3> : kv8_write_kernel<kInt8>;
-  return launch_kernel(kernel, dim3((units + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, st,
+  return launch_kernel(kernel, dim3(units / kWarps + 1), dim3(kWarps * 32), 0, st,
                        true, rows, ks, vs, page_table, s.hkv, s.num_pages, units, err);
 }
 
@@ -282,7 +289,7 @@ cudaError_t launch_kv8_read(const Shape& s, const Kv8& c, void* k_out, long long
                        static_cast<const uint8_t*>(c.v), c.v_scale};
   const int units = new_block_items(s.batch, total, cu != nullptr) * s.hkv * 2;
   auto kernel = c.format == kE4m3 ? kv8_read_kernel<kE4m3> : kv8_read_kernel<kInt8>;
-  return launch_kernel(kernel, dim3((units + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, st,
+  return launch_kernel(kernel, dim3(units / kWarps + 1), dim3(kWarps * 32), 0, st,
                        true, rows, ks, vs, page_table, s.hkv, s.num_pages, units, err);
 }
 

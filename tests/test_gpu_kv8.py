@@ -985,3 +985,25 @@ def test_lengths_far_below_zero_are_reported():
     other = np.setdiff1d(np.arange(s.num_pages), s.table[1])
     for name in before:
         np.testing.assert_array_equal(after[name][other], before[name][other])
+
+
+@pytest.mark.parametrize("lens,cu", [
+    ([16], [5000, 5016]), ([16, 16], [900, 916, 932]), ([16, 4, 4], [0, 16, 16, 90000]),
+    ([4] * 300, [0] * 300 + [-4]),
+])
+def test_offsets_outside_the_arrays_are_reported(lens, cu):
+    """Wherever they lead: sequences behind every row, the only one, the last of many."""
+    s = Batch(lens, 2, 1, "int8", seed=1)
+    d, err = s.dims(), error_word()
+    cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    k = torch.full((20, 1, D), 2.0, dtype=torch.bfloat16, device="cuda")
+    cache = s.gpu_cache()
+    hsa.hsa_kv8_read(d, cache, k, k.clone(), cu, s.gpu_table(), s.gpu_lens(), err)
+    assert hsa.hsa_read_device_error(err) == hsa.HSA_ERR_DEVICE_CHECK
+    hsa.hsa_kv8_write(d, cache, k, k, cu, s.gpu_table(), s.gpu_lens(), err)
+    assert hsa.hsa_read_device_error(err) == hsa.HSA_ERR_DEVICE_CHECK
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_PREFILL)
+    q = to_bf16(s.rng.standard_normal((20, 2, D)))
+    out = torch.full((20, 2, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    hsa.hsa_kv8_prefill(d, cache, q, cu, s.gpu_table(), s.gpu_lens(), out, None, ws)
+    assert hsa.hsa_read_device_error(ws) == hsa.HSA_ERR_DEVICE_CHECK
