@@ -446,6 +446,19 @@ def _offsets(name: str, d: Dims, cu) -> Optional[int]:
     return cu.data_ptr()
 
 
+def _lists(name: str, d: Dims, cu, page_table, seq_lens):
+    """The addresses of new tokens' offsets, page table and lengths."""
+    try:  # the lists as they should be, without a call for each
+        if (page_table.dtype is torch.int32 and seq_lens.dtype is torch.int32 and
+                (cu is None or (cu.dtype is torch.int32 and cu.numel() > d.batch and
+                                cu.is_contiguous()))):
+            return (cu if cu is None else cu.data_ptr(), page_table.data_ptr(),
+                    seq_lens.data_ptr())
+    except AttributeError:  # addresses
+        pass
+    return _offsets(name, d, cu), _list(name, page_table), _list(name, seq_lens)
+
+
 def _dense(name: str, what: str, t, dtype, n: int) -> Optional[int]:
     """The address of a contiguous tensor of n values (None stays None, an address itself)."""
     if t is None or type(t) is int:
@@ -498,10 +511,10 @@ def hsa_kv8_write(d: Dims, cache: KV8, k_new, v_new, cu_tokens, page_table, seq_
     """k_new / v_new: bf16 [total_tokens][hkv][128], rows contiguous (any row stride)."""
     name = "hsa_kv8_write"
     rows, k_stride, v_stride = _row_pair(name, k_new, v_new, d.hkv)
+    cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
     rc = load().hsa_kv8_write(
         ctypes.byref(d.c()), _cache(name, d, cache), k_new.data_ptr(), k_stride, v_new.data_ptr(),
-        v_stride, _offsets(name, d, cu_tokens), rows, _list(name, page_table),
-        _list(name, seq_lens), _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
+        v_stride, cu, rows, table, lens, _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check(name, rc)
 
@@ -511,10 +524,10 @@ def hsa_kv8_read(d: Dims, cache: KV8, k_out, v_out, cu_tokens, page_table, seq_l
     """k_out / v_out: bf16 [total_tokens][hkv][128], rows contiguous (any row stride)."""
     name = "hsa_kv8_read"
     rows, k_stride, v_stride = _row_pair(name, k_out, v_out, d.hkv)
+    cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
     rc = load().hsa_kv8_read(
         ctypes.byref(d.c()), _cache(name, d, cache), k_out.data_ptr(), k_stride, v_out.data_ptr(),
-        v_stride, _offsets(name, d, cu_tokens), rows, _list(name, page_table),
-        _list(name, seq_lens), _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
+        v_stride, cu, rows, table, lens, _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check(name, rc)
 
@@ -550,9 +563,9 @@ def hsa_kv8_prefill(d: Dims, cache: KV8, q, cu_tokens, page_table, seq_lens, out
     if not out.is_contiguous() or out.shape != q.shape or out.dtype is not torch.bfloat16:
         raise HsaError(name, HSA_ERR_INVALID_ARG, "out must be contiguous, as q")
     lse = _dense(name, "lse", lse, torch.float32, rows * d.hq)
+    cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
     rc = load().hsa_kv8_prefill(
-        ctypes.byref(d.c()), _cache(name, d, cache), q.data_ptr(), q_stride,
-        _offsets(name, d, cu_tokens), rows, _list(name, page_table), _list(name, seq_lens),
+        ctypes.byref(d.c()), _cache(name, d, cache), q.data_ptr(), q_stride, cu, rows, table, lens,
         out.data_ptr(), lse, _p(ws), ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check(name, rc)
