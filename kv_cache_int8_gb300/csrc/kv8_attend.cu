@@ -16,7 +16,9 @@
 // as long as every s_v is within 2^-40 .. 2^40: below 2^54 a token then, and a token that matters
 // is no smaller than 2^-70. From a row's first block on whose s_v is not (a block of zeros has
 // none), a second form of the loop sums 2^x under a maximum of its own: right for any mixture of
-// scales, at the price of more exponentials. The relative error against 64 bits is 3 to 5e-7
+// scales, at the price of more exponentials. log2 s_v takes log2f, not the fast instruction, as its
+// error enters the result whole: one token under scales of 2^-10 to 2^-5 is 1.8e-7 off (7.7e-7),
+// of 2^-40 1.8e-7 (2.8e-6), for 0.05 us a call. The relative error against 64 bits is 3 to 5e-7
 // (2-norm).
 //
 // Layout. K's block is the left operand [16 tokens][128 channels], the group's heads (up to 8)
@@ -136,12 +138,6 @@ __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
   return d;
 }
 
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ float max32(float x) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
@@ -249,7 +245,7 @@ __device__ __forceinline__ Unit locate(const Params& p, const long long* pre, co
   t.span = lo | (hi << 8);
   t.sk = p.k_scale[block];
   const float sv = p.v_scale[block];
-  t.sv = lg2(sv);
+  t.sv = log2f(sv);
   if (!(fabsf(t.sv) <= kPlainScale)) t.span |= kFar;
   return t;
 }

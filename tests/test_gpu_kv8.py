@@ -1007,3 +1007,25 @@ def test_offsets_outside_the_arrays_are_reported(lens, cu):
     out = torch.full((20, 2, D), 9.0, dtype=torch.bfloat16, device="cuda")
     hsa.hsa_kv8_prefill(d, cache, q, cu, s.gpu_table(), s.gpu_lens(), out, None, ws)
     assert hsa.hsa_read_device_error(ws) == hsa.HSA_ERR_DEVICE_CHECK
+
+
+@pytest.mark.parametrize("lo,hi", [(-126, -100), (-40, -30), (-10, 2), (30, 40), (100, 119)])
+def test_decode_of_one_token_gives_its_value(lo, hi):
+    """Weight 1 on one value, under any scale. log2 of the scale is off by an ulp, 2^-23 of itself,
+    and enters as an exponent; two exponentials of 2^-22 and a few roundings of 2^-24."""
+    n = 500
+    d = hsa.Dims(batch=n, hq=3, hkv=1, max_pages_per_seq=1, num_pages=n, k2=0)
+    cache = hsa.KV8.zeros(d)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    cache.v.copy_(torch.randint(-127, 128, cache.v.shape, generator=g, device="cuda"))
+    scale = torch.exp2(lo + (hi - lo) * torch.rand(n, 1, generator=g, device="cuda")).clamp(min=2.0 ** -126)
+    cache.v_scale.copy_(scale)
+    q = torch.zeros(n, 3, D, device="cuda", dtype=torch.bfloat16)
+    out, lse = torch.empty(n, 3, D, device="cuda"), torch.empty(n, 3, device="cuda")
+    hsa.hsa_kv8_decode(d, cache, q, torch.arange(n, device="cuda", dtype=torch.int32)[:, None],
+                       torch.ones(n, device="cuda", dtype=torch.int32), out, lse,
+                       hsa.workspace(d, hsa.HSA_OP_KV8_DECODE))
+    want = (cache.v[:, 0, 0].double() * scale.double())[:, None]
+    rel = np.log(2) * 2.0 ** -23 * max(abs(lo), abs(hi)) + 2 * 2.0 ** -22 + 8 * 2.0 ** -24
+    assert bool(((out.double() - want).abs() <= rel * want.abs() + 2.0 ** -149).all())
+    assert float(lse.abs().max()) <= rel
