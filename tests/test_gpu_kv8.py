@@ -1029,3 +1029,105 @@ def test_decode_of_one_token_gives_its_value(lo, hi):
     rel = np.log(2) * 2.0 ** -23 * max(abs(lo), abs(hi)) + 2 * 2.0 ** -22 + 8 * 2.0 ** -24
     assert bool(((out.double() - want).abs() <= rel * want.abs() + 2.0 ** -149).all())
     assert float(lse.abs().max()) <= rel
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("hq,hkv,per_head", [(7, 1, 0), (8, 1, 0), (24, 3, 1)])
+@pytest.mark.parametrize("lens", [
+    [1 + i % 20 for i in range(300)],             # a warp a row
+    [10 + (i * 13) % 330 for i in range(170)],    # four warps a row
+    [17] * 160 + [6000, 0, 3],                    # a CTA for them all, the long row cut
+], ids=["warp", "four", "cta"])
+def test_more_rows_than_ctas_of_every_kind(fmt, hq, hkv, per_head, lens):
+    """Full and odd groups, a selection of its own for each query head, both formats, dense and
+    over kept blocks, for each way in which rows are shared out."""
+    s = Batch(lens, hq, hkv, fmt, seed=hq + len(lens))
+    q = bf16(s.rng.standard_normal((len(lens), hq, D)))
+    rows, g = hq if per_head else hkv, hq // hkv
+    idx = np.empty((len(lens), rows, 3), np.int32)
+    for r in range(rows):  # a row's own blocks
+        idx[:, r] = [r % 3, 3 + r % 2, 7 + r]
+    cnt = np.tile(np.arange(rows, dtype=np.int32) % 4, (len(lens), 1))
+    kept = (torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda())
+    results = [(run_decode(s, q), None),
+               (run_decode(s, q, kept, sink=3, window=9, k2=3, per_head=per_head), kept)]
+    for b in list(range(0, len(lens), 29)) + [len(lens) - 3, len(lens) - 2, len(lens) - 1]:
+        n = lens[b]
+        t = np.arange(n)
+        for j in range(hq):
+            k, v = (O.values(s.cache, w, s.table[b], n, j // g) for w in "kv")
+            r = j if per_head else j // g
+            near = (t < 3) | (t >= n - 9) | np.isin(t // PAGE, idx[b, r, :cnt[b, r]])
+            for (out, lse), form in results:
+                seen = np.ones(n, bool) if form is None else near
+                want, wl, tol = O.attend(q[b, j:j + 1], k, v, seen[None], D ** -0.5)
+                assert_rows(out[b, j:j + 1], lse[b, j:j + 1], want, wl, tol)
+
+
+@pytest.mark.parametrize("fmt,hq,n,m", [("int8", 8, 131072, 3), ("e4m3", 4, 100001, 70),
+                                        ("int8", 5, 60000, 128)])
+def test_prompt_rows_joined_of_many_parts(fmt, hq, n, m):
+    """Few new tokens over a long context: a row block in up to 152 parts, one tile or two."""
+    s = Batch([n], hq, 1, fmt, seed=25, fill=False)
+    for name in ("k", "v"):
+        c = s.cache[name]
+        c[...] = s.rng.integers(-100, 101, c.shape) if fmt == "int8" else O.e4m3_code(
+            s.rng.standard_normal(c.shape, dtype=np.float32) * 100.0)
+        s.cache[name + "s"][...] = s.rng.uniform(0.005, 0.02, s.cache[name + "s"].shape)
+    q = bf16(s.rng.standard_normal((m, hq, D)))
+    out, lse = run_prefill(s, q, [m])
+    i = np.unique([0, 1, m // 2, m - 1])
+    k, v = (O.values(s.cache, w, s.table[0], n, 0) for w in "kv")
+    seen = np.arange(n)[None] <= (n - m + i)[:, None]
+    for j in range(hq):
+        want, wl, tol = O.attend(q[i, j], k, v, seen, D ** -0.5)
+        tol["out"] = tol["out"] + 2.0 ** -11 * np.abs(v).max()
+        assert_rows(out[i, j], lse[i, j], want, wl, tol, 2.0 ** -8)
+
+
+def test_long_stretches_over_unlike_scales():
+    """The sums' own frame (V of zeros, tiny and large) across stretches of 256 tiles and parts."""
+    hq, n, m, copies = 4, 40000, 300, 60
+    s = Batch([n], hq, 1, "int8", seed=26, fill=False)
+    pages = s.cache["v"].shape[0]
+    for name in ("k", "v"):
+        s.cache[name][...] = s.rng.integers(-127, 128, s.cache[name].shape)
+        s.cache[name + "s"][...] = s.rng.uniform(0.005, 0.02, (pages, 1))
+    e = s.rng.choice([-110, -60, 0, 0, 0, 0, 50, 100], (pages, 1))
+    s.cache["vs"] *= (2.0 ** e).astype(np.float32)
+    zero = s.rng.random(pages) < 0.1
+    s.cache["v"][zero], s.cache["vs"][zero] = 0, 0
+    s.lens, s.table = [n] * copies, np.tile(s.table, (copies, 1))
+    q = bf16(s.rng.standard_normal((m * copies, hq, D)))
+    out, lse = run_prefill(s, q, [m] * copies)
+    k, v = (O.values(s.cache, w, s.table[0], n, 0) for w in "kv")
+    i = np.array([0, m // 2, m - 1])
+    seen = np.arange(n)[None] <= (n - m + i)[:, None]
+    for b in (0, 1, copies // 2, copies - 1):
+        for j in (0, hq - 1):
+            qj = q[b * m + i, j].astype(np.float64)
+            want, wl, tol = O.attend(qj, k, v, seen, D ** -0.5)
+            bound = unlike_bounds(qj, k, v, seen, tol, 127.0, 2.0 ** -11 + 2.0 ** -12, 2.0 ** -32)
+            bound += 2.0 ** -8 * (np.abs(want) + bound)
+            assert (np.abs(lse[b * m + i, j] - wl) <= tol["lse"]).all(), (b, j)
+            assert (np.abs(out[b * m + i, j] - want) <= bound).all(), (b, j)
+
+
+def test_prompt_rows_are_the_same_every_time():
+    """Parts meet in the order of their slices, whichever CTA joins them: the same bits, call
+    after call."""
+    s = Batch([6000, 9000, 12000, 7000], 8, 2, "int8", seed=27, fill=False)
+    for name in ("k", "v"):
+        s.cache[name][...] = s.rng.integers(-127, 128, s.cache[name].shape)
+    new = [7, 24, 11, 300]
+    d, cache, table, lens, cu = s.dims(), s.gpu_cache(), s.gpu_table(), s.gpu_lens(), cu_of(new)
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_PREFILL)
+    q = to_bf16(s.rng.standard_normal((sum(new), 8, D)) * 0.1)
+    first = None
+    for _ in range(20):
+        out = torch.empty(sum(new), 8, D, dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty(sum(new), 8, device="cuda")
+        hsa.hsa_kv8_prefill(d, cache, q, cu, table, lens, out, lse, ws)
+        first = first or (out, lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert torch.isfinite(first[0]).all() and torch.isfinite(first[1]).all()
