@@ -423,7 +423,7 @@ typedef struct hsa_kv8 {
  *     inv  = f32(1 / s), 0 when s = 0;
  *     older tokens' codes, when s > s_old: round(f32(code * f32(s_old * inv)));
  *     new codes: round(f32(x * inv)) to the format, halves to even, at most L in magnitude;
- *     a NaN becomes 0 and an infinity +-L.
+ *     a NaN becomes 0 and an infinity +-L (0 under s = 0, whose values are 0 anyway).
  * Whole blocks written at once are therefore within half a code step of bf16, and a block that
  * grows token by token is within half a step more for each time its scale grew. Slots behind
  * the last token keep their codes. Rewriting positions (after a rejected draft) keeps the
@@ -448,9 +448,10 @@ int32_t hsa_kv8_read(const hsa_dims* d, const hsa_kv8* cache, void* k_out, int64
 
 /*
  * dense_decode over the 8-bit cache: one query token a sequence, q bf16 [batch][hq][128],
- * attends every token [0, N_b). out f32 [batch][hq][128], lse f32 [batch][hq] (nullable). A
- * sequence of no tokens gives 0 and lse -inf; a head whose query is not finite gives NaN (so do
- * the other attentions). Needs the HSA_OP_KV8_DECODE workspace.
+ * attends every token [0, N_b). q and out are dense; out f32 [batch][hq][128], lse f32
+ * [batch][hq] (nullable). A sequence of no tokens gives 0 and lse -inf; a head whose query is not
+ * finite gives NaN (so do the other attentions). lse does not depend on V: blocks of zeros and
+ * scales of any size mix freely. Needs the HSA_OP_KV8_DECODE workspace.
  */
 int32_t hsa_kv8_decode(const hsa_dims* d, const hsa_kv8* cache, const void* q,
                        const int32_t* page_table, const int32_t* seq_lens, float* out,
@@ -460,8 +461,9 @@ int32_t hsa_kv8_decode(const hsa_dims* d, const hsa_kv8* cache, const void* q,
  * hsa_attend over the 8-bit cache: the attended set T_b of the sink, the window and the kept
  * blocks block_idx [batch][rows][k2] / n_blocks [batch][rows] as hsa_select writes them (rows =
  * hkv, or hq with per_head = 1; ids distinct in a row, ids outside the candidate region add
- * nothing). A row that attends nothing gives 0 and lse -inf. Outputs and workspace as
- * hsa_kv8_decode.
+ * nothing). hsa_select scores key codes made from a bf16 cache, for groups of 1, 2, 4 and 8 query
+ * heads; lists from elsewhere serve as well. A row that attends nothing gives 0 and lse -inf.
+ * Outputs and workspace as hsa_kv8_decode.
  */
 int32_t hsa_kv8_attend(const hsa_dims* d, const hsa_kv8* cache, const void* q,
                        const int32_t* page_table, const int32_t* seq_lens,
@@ -472,7 +474,8 @@ int32_t hsa_kv8_attend(const hsa_dims* d, const hsa_kv8* cache, const void* q,
  * Causal attention of the last n_b tokens of each sequence over the 8-bit cache (their own K
  * and V written before): query row r of sequence b, at position p, attends tokens [0, p]. q:
  * bf16 rows [total_tokens][hq][128] with row stride q_stride; out: bf16 rows, contiguous; lse:
- * f32 [total_tokens][hq] (nullable). Rows of a sequence that is left out (see above) get 0 and
+ * f32 [total_tokens][hq] (nullable). The weights enter the product with V as fp16 numbers, within
+ * 2^-11 of themselves. Rows of a sequence that is left out (see above) get 0 and
  * lse -inf. Needs the HSA_OP_KV8_PREFILL workspace.
  */
 int32_t hsa_kv8_prefill(const hsa_dims* d, const hsa_kv8* cache, const void* q, int64_t q_stride,

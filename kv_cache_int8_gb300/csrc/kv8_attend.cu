@@ -18,7 +18,7 @@
 // none), a second form of the loop sums 2^x under a maximum of its own: right for any mixture of
 // scales, at the price of more exponentials. log2 s_v takes log2f, not the fast instruction, as its
 // error enters the result whole: one token under scales of 2^-10 to 2^-5 is 1.8e-7 off (7.7e-7),
-// of 2^-40 1.8e-7 (2.8e-6), for 0.05 us a call. The relative error against 64 bits is 3 to 5e-7
+// of 2^-40 1.8e-7 (2.8e-6), for 0.05 us a call. The relative error against 64 bits is 3 to 7e-7
 // (2-norm).
 //
 // Layout. K's block is the left operand [16 tokens][128 channels], the group's heads (up to 8)
@@ -38,10 +38,10 @@
 // and the last CTA to arrive joins them in slice order (the result does not depend on which one
 // that is).
 //
-// Measured (GB300, copy 6.8 TB/s; 8 kv heads): 8 x 32-128K tokens, groups of 8, int8: 224 us,
-// 6.3 TB/s; one sequence of 128K tokens, groups of 4: 51-53 us, 5.1 TB/s (a further byte costs
+// Measured (GB300, copy 6.8 TB/s; 8 kv heads): 8 x 32-128K tokens, groups of 8, int8: 226 us,
+// 6.2 TB/s; one sequence of 128K tokens, groups of 4: 53.5 us, 5.0 TB/s (a further byte costs
 // 1 / 7.0 TB/s; about 7 us pass before the first blocks are there everywhere and 5 us in
-// joining); 8K tokens: 12 us; 128 kept blocks, sink and window of 128K: 11.8 us.
+// joining); 8K tokens of one kv head: 12.9 us; 128 kept blocks, sink and window of 128K: 12.2 us.
 #include "kv8.cuh"
 
 #include <climits>
