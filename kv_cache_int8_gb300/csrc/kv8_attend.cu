@@ -700,10 +700,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // frame) and l stay in fp32's range, and of two parts that are joined the frames differ by
       // 2^100 at most beside their sums: a factor that fp32 flushes to 0, below 2^-126, belongs
       // to a part that counts for less than 2^-26.
-      const float to0 = fminf(fmaxf(m0 - kHeadroom, top0 - 50.0f), top0 + 50.0f);
-      const float to1 = fminf(fmaxf(m1 - kHeadroom, top1 - 50.0f), top1 + 50.0f);
+      const float was0 = m0 - kHeadroom, was1 = m1 - kHeadroom;
+      m0 = fminf(fmaxf(was0, top0 - 50.0f), top0 + 50.0f) + kHeadroom;
+      m1 = fminf(fmaxf(was1, top1 - 50.0f), top1 + 50.0f) + kHeadroom;
+      const float to0 = m0 - kHeadroom, to1 = m1 - kHeadroom;  // as they are read again
       // in two factors, as one alone may leave the range
-      const float a0 = ex2(0.5f * (m0 - kHeadroom - to0)), a1 = ex2(0.5f * (m1 - kHeadroom - to1));
+      const float a0 = ex2(0.5f * (was0 - to0)), a1 = ex2(0.5f * (was1 - to1));
 #pragma unroll
       for (int k = 0; k < 8; k++) {
         o[k][0] = o[k][0] * a0 * a0;
@@ -713,8 +715,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       l0 *= ex2(top0 - to0);
       l1 *= ex2(top1 - to1);
-      m0 = to0 + kHeadroom;
-      m1 = to1 + kHeadroom;
     }
 
     // ---- the warps' parts of the row meet

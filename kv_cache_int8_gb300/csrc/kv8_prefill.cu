@@ -659,12 +659,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         // by 2^100 at most beside their sums: a factor that fp32 flushes to 0, below 2^-126,
         // belongs to a part that counts for less than 2^-26.
         const float ref = m - kHeadroom;
-        const float to = fminf(fmaxf(ref, top_x - 50.0f), top_x + 50.0f);
+        m = fminf(fmaxf(ref, top_x - 50.0f), top_x + 50.0f) + kHeadroom;
+        const float to = m - kHeadroom;  // as it is read again
         const bool none = top_x == -INFINITY;
         // in two factors, as one alone may leave the range
         const float by = none ? 1.0f : ex2(0.5f * (ref - to));
         if (!none) l *= ex2(top_x - to);
-        m = to + kHeadroom;
 #pragma unroll 1
         for (int k0 = 0; k0 < 8; k0++) {
           uint32_t o[16];
