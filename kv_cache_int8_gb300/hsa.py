@@ -471,16 +471,18 @@ def _dense(name: str, what: str, t, dtype, n: int) -> Optional[int]:
 def _heads(name: str, d: Dims, q, out, lse):
     """The addresses of a decode attention's q, out and lse."""
     n = d.batch * d.hq
+    f32 = torch.float32
     try:  # the arrays as they should be, without a call for each
-        if (q.dtype is torch.bfloat16 and out.dtype is torch.float32 and q.numel() == n * 128 and
-                out.numel() == n * 128 and q.is_contiguous() and out.is_contiguous()):
-            return (q.data_ptr(), out.data_ptr(), lse if lse is None else
-                    _dense(name, "lse", lse, torch.float32, n))
+        if (q.dtype is torch.bfloat16 and out.dtype is f32 and q.numel() == n * 128 == out.numel()
+                and q.is_contiguous() and out.is_contiguous()):
+            if lse is None:
+                return q.data_ptr(), out.data_ptr(), None
+            if lse.dtype is f32 and lse.numel() == n and lse.is_contiguous():
+                return q.data_ptr(), out.data_ptr(), lse.data_ptr()
     except AttributeError:  # addresses
         pass
     return (_dense(name, "q", q, torch.bfloat16, n * 128),
-            _dense(name, "out", out, torch.float32, n * 128),
-            _dense(name, "lse", lse, torch.float32, n))
+            _dense(name, "out", out, f32, n * 128), _dense(name, "lse", lse, f32, n))
 
 
 def _rows(name: str, t, heads: int):
@@ -538,9 +540,11 @@ def hsa_kv8_decode(d: Dims, cache: KV8, q, page_table, seq_lens, out, lse, ws,
     contiguous."""
     name = "hsa_kv8_decode"
     q, out, lse = _heads(name, d, q, out, lse)
-    _check(name, load().hsa_kv8_decode(
-        ctypes.byref(d.c()), _cache(name, d, cache), q, _list(name, page_table),
-        _list(name, seq_lens), out, lse, _p(ws), ws.numel(), _stream(stream)))
+    _, table, lens = _lists(name, d, None, page_table, seq_lens)
+    rc = load().hsa_kv8_decode(ctypes.byref(d.c()), _cache(name, d, cache), q, table, lens, out,
+                               lse, _p(ws), ws.numel(), _stream(stream))
+    if rc != HSA_OK:
+        _check(name, rc)
 
 
 def hsa_kv8_attend(d: Dims, cache: KV8, q, page_table, seq_lens, block_idx, n_blocks, out, lse,
@@ -548,10 +552,12 @@ def hsa_kv8_attend(d: Dims, cache: KV8, q, page_table, seq_lens, block_idx, n_bl
     """q, out, lse: as hsa_kv8_decode."""
     name = "hsa_kv8_attend"
     q, out, lse = _heads(name, d, q, out, lse)
-    _check(name, load().hsa_kv8_attend(
-        ctypes.byref(d.c()), _cache(name, d, cache), q, _list(name, page_table),
-        _list(name, seq_lens), _list(name, block_idx), _list(name, n_blocks), out, lse, _p(ws),
-        ws.numel(), _stream(stream)))
+    _, table, lens = _lists(name, d, None, page_table, seq_lens)
+    rc = load().hsa_kv8_attend(ctypes.byref(d.c()), _cache(name, d, cache), q, table, lens,
+                               _list(name, block_idx), _list(name, n_blocks), out, lse, _p(ws),
+                               ws.numel(), _stream(stream))
+    if rc != HSA_OK:
+        _check(name, rc)
 
 
 def hsa_kv8_prefill(d: Dims, cache: KV8, q, cu_tokens, page_table, seq_lens, out, lse, ws,
