@@ -9,12 +9,12 @@
 //   y_t = f s_k S_t + log2 s_v,   out = sum_t 2^(y_t - M) c_t / sum_t 2^(y_t - M) / s_v
 // so V's scale costs nothing but the offset of an exponent that is computed anyway, and the sum
 // takes one multiplication a block, as long as every s_v is within 2^-40 .. 2^40 (P / s_v then
-// stays below 2^55, and above 2^-73 where it matters). From the first tile on that has another
-// s_v (or a block of zeros, that has none), the rest of a stretch of tiles sums 2^(x - its own
-// maximum) beside P, in a second form of the step: right for any mixture of scales. P = 2^(y - M + 7) is rounded to fp16 (11 bits, against 8
-// of the bf16 result); M lags the running maximum by at most 8, so the output accumulator is
-// rarely rescaled (with 10 and 4: 2048 tokens behind 30K 767 us, not 756; 8K prompt 465, not
-// 443).
+// stays below 2^55, and above 2^-73 where it matters). From the first half tile on that has
+// another s_v (or a block of zeros, that has none), the rest of a stretch of tiles sums
+// 2^(x - its own maximum) beside P, in a second form of the step: right for any mixture of
+// scales. P = 2^(y - M + 7) is rounded to fp16 (11 bits, against 8 of the bf16 result); M lags the
+// running maximum by at most 8, so the output accumulator is rarely rescaled (with 10 and 4: 2048
+// tokens behind 30K 767 us, not 756; 8K prompt 465, not 443).
 //
 // Layout. 256 rows (a kv head's group of query heads x 256 / group tokens) as two tiles of 128
 // against tiles of 128 tokens. Warps 0-3 and 4-7: one row a thread, softmax of tile 0 and 1;
@@ -72,12 +72,12 @@ constexpr int kBlockCost = 4;  // what a row block costs beside its tiles, in ti
 // probabilities in fp16's subnormals, 2^-25 off each: 2^20 tokens off the same way and together
 // as heavy as the largest make 2^-5 of 2^7, 2^-12 of the result (bf16 rounds it to 2^-9).
 constexpr float kHeadroom = 7.0f;
+constexpr float kLag = 8.0f;
 // The products' own accumulation rounds towards zero: 1M tokens added up in O (65536 products)
 // gave results 2.6e-3 (equal scores) to 5e-3 (normal ones) too small, more than bf16's own
 // rounding. So O takes at most that many tiles' products, below 2048 x 2^-23 = 2.4e-4, and a
 // longer stretch is added up in fp32 outside. (Ending a stretch costs about four steps.)
 constexpr int kMaxTiles = 256;
-constexpr float kLag = 8.0f;
 constexpr float kPlainScale = 40.0f;  // largest |log2 s_v| under which the sum is made of P / s_v
 constexpr float kTiny = 1e-37f;  // scales of scores are at least that: a masked -inf stays one
 // s_full and p_full of the tiles and, where a row block has one tile, of its odd steps
