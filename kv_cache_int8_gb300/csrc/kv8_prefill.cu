@@ -225,7 +225,6 @@ struct Piece {
   int all_tiles;     // of the whole row block
   int rows;          // rows of the block that exist
   long long begin;   // the row block's first place on the line
-  bool after, before;  // the CTA's piece before / behind this one is of the same row block
 };
 
 // The pieces of the slice [x, end) of the line, in order. A row block's places are kBlockCost
@@ -238,7 +237,6 @@ struct Walk {
   int batch, hkv, group, block_tokens;
   long long x, end;
   int b, h, q, off;  // off: place in the row block
-  bool inside;       // of a stretch of more than kMaxTiles
 
   __device__ __forceinline__ bool next(Piece& p) {
     for (;;) {
@@ -252,17 +250,14 @@ struct Walk {
       int stop = (int)min((long long)(p.all_tiles + kBlockCost), off + (end - x));
       p.tile = max(off - kBlockCost, 0);
       p.tiles = max(stop - kBlockCost, 0) - p.tile;
-      p.after = inside;
-      p.before = inside = p.tiles > kMaxTiles;
-      if (inside) {
+      if (p.tiles > kMaxTiles) {  // the rest of the stretch is the next piece
         p.tiles = kMaxTiles;
         stop = p.tile + kMaxTiles + kBlockCost;
-      }
-      x += stop - off;
-      if (inside) {
+        x += stop - off;
         off = stop;
         return true;
       }
+      x += stop - off;
       off = 0;
       if ((q + 1) * block_tokens < s.n[b]) {
         q++;
@@ -417,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
   const long long per = sm.per, all = pre[batch];
   const long long begin = min(blockIdx.x * per, all), end = min(begin + per, all);
   Walk walk = {{pre, len, num, row0}, batch, p.hkv, p.group, p.block_tokens, begin, end,
-               sm.start_b, sm.start_h, sm.start_q, sm.start_off, false};
+               sm.start_b, sm.start_h, sm.start_q, sm.start_off};
   Piece pc;
 
   if (warp < kSoftmaxWarps) {
@@ -677,39 +672,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         tc::wait_st();
       }
       const long long tiles_begin = pc.begin + kBlockCost, tiles_end = tiles_begin + pc.all_tiles;
+      // of the same stretch: a piece in front of this one, a piece behind it
+      const bool after = pc.tile > 0 && tiles_begin + pc.tile > begin;
+      const bool before = tiles_begin + pc.tile + pc.tiles < min(tiles_end, end);
       const size_t slot = 2 * (size_t)blockIdx.x + (begin < pc.begin ? 1 : 0);
       float4* const po = reinterpret_cast<float4*>(p.part_o) + slot * 32 * kRows + row;
       float2* const pml = reinterpret_cast<float2*>(p.part_ml);
-      // The piece before of the same stretch is in the CTA's part, which only this thread reads
-      // and writes until the stretch ends: added to this one.
-      float keep = 1.0f, add = 0.0f;
-      if (pc.after && real) {
-        const float2 was = __ldcg(pml + slot * kRows + row);
+      if (after) {
+        // The piece in front is in the CTA's part, which only this thread reads and writes until
+        // the stretch ends: added to this one.
+        const float2 was = real ? __ldcg(pml + slot * kRows + row) : make_float2(-INFINITY, 0.0f);
         const float top = fmaxf(m, was.x), ref = top == -INFINITY ? 0.0f : top;
-        keep = ex2(m - ref);
-        add = ex2(was.x - ref);
+        const float keep = ex2(m - ref), add = ex2(was.x - ref);
         l = l * keep + was.y * add;
         m = top;
-      }
-      auto add_up = [&](int c, uint32_t (&o)[32]) {  // 32 channels
-        if (!pc.after || !real) return;
+#pragma unroll 1
+        for (int k0 = 0; k0 < 8; k0++) {
+          uint32_t o[16];
+          tc::load16(o_col + k0 * 16, o);
+          tc::wait_ld();
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-          const float4 v = __ldcg(po + (c * 8 + k) * kRows);
-          o[4 * k] = __float_as_uint(__uint_as_float(o[4 * k]) * keep + v.x * add);
-          o[4 * k + 1] = __float_as_uint(__uint_as_float(o[4 * k + 1]) * keep + v.y * add);
-          o[4 * k + 2] = __float_as_uint(__uint_as_float(o[4 * k + 2]) * keep + v.z * add);
-          o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * keep + v.w * add);
+          for (int k = 0; k < 4; k++) {
+            const float4 v =
+                real ? __ldcg(po + (k0 * 4 + k) * kRows) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            o[4 * k] = __float_as_uint(__uint_as_float(o[4 * k]) * keep + v.x * add);
+            o[4 * k + 1] = __float_as_uint(__uint_as_float(o[4 * k + 1]) * keep + v.y * add);
+            o[4 * k + 2] = __float_as_uint(__uint_as_float(o[4 * k + 2]) * keep + v.z * add);
+            o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * keep + v.w * add);
+          }
+          tc::store16(o_col + k0 * 16, o);
         }
-      };
-      if (!pc.before && begin <= tiles_begin && tiles_end <= end) {  // the whole row block
+        tc::wait_st();
+      }
+      if (!before && begin <= tiles_begin && tiles_end <= end) {  // the whole row block
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
         for (int c = 0; c < 4; c++) {
           uint32_t o[32];
           tc::load32(o_col + c * 32, o);
           tc::wait_ld();
-          add_up(c, o);
           if (real) {
             uint32_t w[16];
 #pragma unroll
@@ -729,7 +730,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           uint32_t o[32];
           tc::load32(o_col + c * 32, o);
           tc::wait_ld();
-          add_up(c, o);
           if (real) {
 #pragma unroll
             for (int k = 0; k < 8; k++)
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           }
         }
         if (real) pml[slot * kRows + row] = make_float2(m, l);
-        if (pc.before) {
+        if (before) {
           tc::fence_before();
           continue;
         }
