@@ -41,7 +41,7 @@
 // Measured (GB300, copy 6.8 TB/s; 8 kv heads): 8 x 32-128K tokens, groups of 8, int8: 226 us,
 // 6.2 TB/s; one sequence of 128K tokens, groups of 4: 53.5 us, 5.0 TB/s (a further byte costs
 // 1 / 7.0 TB/s; about 7 us pass before the first blocks are there everywhere and 5 us in
-// joining); 8K tokens of one kv head: 12.9 us; 128 kept blocks, sink and window of 128K: 12.2 us.
+// joining); 8K tokens of one kv head: 13 us; 128 kept blocks, sink and window of 128K: 12.2 us.
 #include "kv8.cuh"
 
 #include <climits>

@@ -32,9 +32,9 @@
 // one: 89 -> 76 us).
 //
 // Measured (GB300, 1884 TFLOP/s bf16 burst, 1693 sustained; 32 query heads over 8; figures beside
-// a choice below are of one box, which differ by 3 %): 2048 tokens behind 30K 778-786 us, 1370
-// TFLOP/s; an 8K prompt 455-460 us, 1200 TFLOP/s of what its rows see (a diagonal tile is computed
-// whole); 4 x 7-24 tokens behind 6-12K 39.5 us; 2048 behind 126K 3280 us (3210 with the products
+// a choice below are of one box, which differ by 3 %): 2048 tokens behind 30K 770-788 us, 1380
+// TFLOP/s; an 8K prompt 450-460 us, 1210 TFLOP/s of what its rows see (a diagonal tile is computed
+// whole); 4 x 7-24 tokens behind 6-12K 39.4 us; 2048 behind 126K 3245 us (3195 with the products
 // adding up over all 1024 tiles, see kMaxTiles). A step's products take
 // 2048 cycles, a step 3600: each tile's way from S over the softmax and P V to its next S is one
 // chain, and two tiles overlap it only in part. Instructions: 1880 a step and scheduler, half its
