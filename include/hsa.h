@@ -135,7 +135,8 @@ enum hsa_op {
   HSA_OP_STEP = 4,
   HSA_OP_CACHED = 5,
   HSA_OP_KV8_DECODE = 6,  /* hsa_kv8_decode and hsa_kv8_attend */
-  HSA_OP_KV8_PREFILL = 7
+  HSA_OP_KV8_PREFILL = 7,
+  HSA_OP_KV8_TREE = 8     /* hsa_kv8_tree; a workspace of HSA_OP_KV8_PREFILL serves it too */
 };
 
 /* Workspace bytes `op` needs for descriptor `d` (0 if `d` is invalid). */
@@ -403,7 +404,7 @@ int32_t hsa_decode_step_kernels(const hsa_dims* d);
  *  - Row strides are in elements, at least the row's own length, and a multiple of 8.
  *  - Pointers are 16-byte aligned (code arrays 128-byte); the page table and lengths 4-byte.
  *  - Workspaces do not depend on the descriptor: one of hsa_workspace_bytes(d,
- *    HSA_OP_KV8_PREFILL) bytes serves both attentions and every descriptor, one call at a time.
+ *    HSA_OP_KV8_PREFILL) bytes serves all attentions and every descriptor, one call at a time.
  */
 typedef struct hsa_kv8 {
   void* k;        /* K codes [num_pages][hkv][16][128] */
@@ -482,6 +483,118 @@ int32_t hsa_kv8_prefill(const hsa_dims* d, const hsa_kv8* cache, const void* q, 
                         const int32_t* cu_tokens, int32_t total_tokens,
                         const int32_t* page_table, const int32_t* seq_lens, void* out, float* lse,
                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---- Rotary positions and drafted tokens ----
+ *
+ * The pages' attentions take queries and keys that carry their positions, and a step's new tokens
+ * are a line. The calls below put the positions on (rotary embedding, Su et al. 2021), and verify
+ * drafted tokens on the 8-bit cache: a tree of them takes the places behind the context, in an
+ * order in which parents come first; hsa_kv8_write_rotated writes it with each node's depth as its
+ * position, hsa_kv8_tree attends it, and hsa_kv8_keep moves the accepted branch behind the context.
+ * cu_tokens, seq_lens, page tables, strides, alignment and the error word: as for the hsa_kv8 calls.
+ */
+
+/* How hsa_rotary_table's frequencies are made: f_i = base^(-2 i / dim), i < dim / 2, then with
+ * r_i = original f_i / (2 pi), the turns within the original context:
+ *   scaling 0: f_i;   1 (position interpolation, Chen et al. 2023): f_i / factor;
+ *   2 (by parts, Peng et al. 2023): f_i (w_i + (1 - w_i) / factor), w_i = (r_i - low) /
+ *     (high - low) clamped to [0, 1]. */
+typedef struct hsa_rotary_angles {
+  double base;       /* > 0 */
+  double factor;     /* scaling 1 and 2: > 0 */
+  double low;        /* scaling 2: low < high */
+  double high;
+  double original;   /* scaling 2: tokens of the original context, > 0 */
+  double magnitude;  /* factor of every cosine and sine (1: a plain rotation) */
+  int32_t scaling;
+} hsa_rotary_angles;
+
+/*
+ * Fills a rotary table: f32 [rows][dim], row p = magnitude cos(p f_i) for i < dim / 2, then
+ * magnitude sin(p f_i). Angles are computed in 64 bits (exact to about p 2^-53 radians). dim: a
+ * multiple of 8 from 8 to 128; rows >= 1; table 16-byte aligned. Made once, for every position that
+ * is to come.
+ */
+int32_t hsa_rotary_table(const hsa_rotary_angles* angles, float* table, int32_t rows, int32_t dim,
+                         void* stream);
+
+typedef struct hsa_rotary {
+  const float* table;  /* f32 [rows][dim], as hsa_rotary_table fills it (or of the caller's making) */
+  int32_t rows;        /* positions 0 .. rows - 1 */
+  int32_t dim;         /* the first dim channels of a head turn, the others stay: a multiple of 8
+                          from 8 to 128 */
+  int32_t neighbours;  /* pair i is channels 0: (i, i + dim / 2), 1: (2 i, 2 i + 1) */
+} hsa_rotary;
+
+/*
+ * Puts positions on rows of queries and keys: q and q_out bf16 [total_tokens][hq][128], k and k_out
+ * [total_tokens][hkv][128] (both nullable: queries alone), each with its row stride. With (a, b) a
+ * pair of channels and c, s its table values, every operation rounded to fp32 and the result to
+ * bf16:
+ *     y_a = x_a c - x_b s        y_b = x_b c + x_a s
+ * A row's position is positions[row] (int32 [total_tokens]), or with positions NULL its token's
+ * place in the sequence, N_b - n_b + i (seq_lens and cu_tokens as for the hsa_kv8 calls; both are
+ * unused and may be NULL when positions are given). A position outside the table is reported as
+ * HSA_ERR_DEVICE_CHECK through the error word and its row stays as it was, as do rows of no
+ * sequence. An output may be its input (same stride); otherwise they must not overlap. d: batch,
+ * hq and hkv are used (hq / hkv from 1 to 8). workspace (nullable) supplies the error word only.
+ */
+int32_t hsa_rotate(const hsa_dims* d, const hsa_rotary* rotary, const void* q, int64_t q_stride,
+                   void* q_out, int64_t q_out_stride, const void* k, int64_t k_stride, void* k_out,
+                   int64_t k_out_stride, const int32_t* positions, const int32_t* cu_tokens,
+                   int32_t total_tokens, const int32_t* seq_lens, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
+ * hsa_kv8_write with positions: the keys are turned as in hsa_rotate and quantised from fp32 (not
+ * rounded to bf16 in between), the values quantised as they are, and the queries of the same
+ * tokens, q (nullable, with q_out), turned into q_out. positions as for hsa_rotate: where a token
+ * lies in the cache and its position may differ (nodes of a drafted tree: context + depth). A
+ * position outside the table is reported; the token's block of the cache and its query row stay
+ * as they were. q_out may be q (same stride); k_new and v_new must not overlap it.
+ */
+int32_t hsa_kv8_write_rotated(const hsa_dims* d, const hsa_kv8* cache, const hsa_rotary* rotary,
+                              const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                              const void* k_new, int64_t k_stride, const void* v_new,
+                              int64_t v_stride, const int32_t* positions, const int32_t* cu_tokens,
+                              int32_t total_tokens, const int32_t* page_table,
+                              const int32_t* seq_lens, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * Attention of drafted tokens: the n_b last tokens of each sequence (their own K and V written
+ * before, at most 256 of them) are the nodes of a tree or of several; parents (int32
+ * [total_tokens], rows as q's) names each node's parent among its sequence's nodes, an earlier
+ * one, or -1 for a child of the context. Node i attends the context, tokens [0, N_b - n_b), its
+ * ancestors and itself. parents NULL: node i - 1 is node i's parent (a draft without branches:
+ * hsa_kv8_prefill's causal attention). q, out, lse and strides as hsa_kv8_prefill's; the weights
+ * enter the product with V as fp16 numbers, within 2^-11 of themselves. A parent that is no
+ * earlier node is reported as HSA_ERR_DEVICE_CHECK and counts as -1; rows of a sequence that is
+ * left out (also one of more than 256 nodes) get 0 and lse -inf; rows of no sequence stay as they
+ * were. Needs the HSA_OP_KV8_TREE workspace.
+ */
+int32_t hsa_kv8_tree(const hsa_dims* d, const hsa_kv8* cache, const void* q, int64_t q_stride,
+                     const int32_t* parents, const int32_t* cu_tokens, int32_t total_tokens,
+                     const int32_t* page_table, const int32_t* seq_lens, void* out, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Moves accepted tokens into place. Of sequence b's n_b last tokens (seq_lens counts them) the
+ * n_keep[b] with indices keep_idx[b * keep_stride + j], ascending in j, become the tokens behind
+ * the first N_b - n_b: their values f32(code * scale) are written to positions N_b - n_b + j by
+ * hsa_kv8_write's rules (a block's scale from the kept values, or with older tokens in it at least
+ * the old one), K and V of every kv head. Entries from n_keep[b] on are ignored. Tokens that are
+ * not kept are gone; slots behind the last kept one are as good as never written. new_lens
+ * (int32 [batch], nullable, not seq_lens itself) receives N_b - n_b + n_keep[b]. A sequence whose
+ * numbers, indices or pages do not fit is left as it was, its new length N_b, and reported as
+ * HSA_ERR_DEVICE_CHECK. Two sequences must not share a page that receives tokens. workspace
+ * (nullable) supplies the error word only.
+ */
+int32_t hsa_kv8_keep(const hsa_dims* d, const hsa_kv8* cache, const int32_t* keep_idx,
+                     int32_t keep_stride, const int32_t* n_keep, const int32_t* cu_tokens,
+                     const int32_t* page_table, const int32_t* seq_lens, int32_t* new_lens,
+                     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Reads and clears the device error word of `workspace` after synchronising `stream`:

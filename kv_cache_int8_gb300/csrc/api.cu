@@ -582,6 +582,15 @@ int32_t do_kv8_attend(const hsa_dims* d, const hsa_kv8* cache, bool kept, const 
       as_stream(stream)));
 }
 
+// ---- rotary positions, drafted tokens
+int32_t check_rotary(const hsa_rotary* r, hsa::RotaryTable* out) {
+  if (!r || !r->table || !aligned(r->table, 16) || r->rows < 1) return HSA_ERR_INVALID_ARG;
+  if (r->neighbours != 0 && r->neighbours != 1) return HSA_ERR_INVALID_ARG;
+  if (r->dim < 8 || r->dim > hsa::kHeadDim || r->dim % 8 != 0) return HSA_ERR_UNSUPPORTED;
+  *out = hsa::RotaryTable{r->table, r->rows, r->dim, r->neighbours};
+  return HSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -589,7 +598,7 @@ extern "C" {
 size_t hsa_workspace_bytes(const hsa_dims* d, int32_t op) {
   Shape s;
   const bool prune = op == HSA_OP_SELECT || op == HSA_OP_STEP;
-  const bool kv8 = op == HSA_OP_KV8_DECODE || op == HSA_OP_KV8_PREFILL;
+  const bool kv8 = op == HSA_OP_KV8_DECODE || op == HSA_OP_KV8_PREFILL || op == HSA_OP_KV8_TREE;
   if (check_dims(d, s, prune, kv8) != HSA_OK || (kv8 && d->kv_on_host)) return 0;
   switch (op) {
     case HSA_OP_QUANTIZE: return quantize_ws(s);
@@ -600,6 +609,7 @@ size_t hsa_workspace_bytes(const hsa_dims* d, int32_t op) {
     case HSA_OP_CACHED: return cached_ws(s);
     case HSA_OP_KV8_DECODE: return kv8_decode_layout().end;
     case HSA_OP_KV8_PREFILL: return kv8_prefill_layout().end;
+    case HSA_OP_KV8_TREE: return kv8_decode_layout().end;
     default: return 0;
   }
 }
@@ -1174,6 +1184,129 @@ int32_t hsa_kv8_prefill(const hsa_dims* d, const hsa_kv8* cache, const void* q, 
       reinterpret_cast<int*>(ws + l.counters), reinterpret_cast<float*>(ws + l.part_ml),
       reinterpret_cast<float*>(ws + l.part_o), reinterpret_cast<int*>(ws), num_sms(),
       as_stream(stream)));
+}
+
+int32_t hsa_rotary_table(const hsa_rotary_angles* a, float* table, int32_t rows, int32_t dim,
+                         void* stream) {
+  if (!a || !table || !aligned(table, 16) || rows < 1) return HSA_ERR_INVALID_ARG;
+  if (dim < 8 || dim > hsa::kHeadDim || dim % 8 != 0) return HSA_ERR_UNSUPPORTED;
+  if (!(a->base > 0.0) || !std::isfinite(a->base) || !std::isfinite(a->magnitude))
+    return HSA_ERR_INVALID_ARG;
+  if (a->scaling < 0 || a->scaling > 2) return HSA_ERR_INVALID_ARG;
+  if (a->scaling > 0 && (!(a->factor > 0.0) || !std::isfinite(a->factor)))
+    return HSA_ERR_INVALID_ARG;
+  if (a->scaling == 2 && (!(a->original > 0.0) || !std::isfinite(a->original) ||
+                          !std::isfinite(a->low) || !std::isfinite(a->high) || !(a->low < a->high)))
+    return HSA_ERR_INVALID_ARG;
+  return cuda_status(hsa::launch_rotary_table(
+      hsa::RotaryAngles{a->base, a->scaling, a->factor, a->low, a->high, a->original, a->magnitude},
+      table, rows, dim, as_stream(stream)));
+}
+
+int32_t hsa_rotate(const hsa_dims* d, const hsa_rotary* rotary, const void* q, int64_t q_stride,
+                   void* q_out, int64_t q_out_stride, const void* k, int64_t k_stride, void* k_out,
+                   int64_t k_out_stride, const int32_t* positions, const int32_t* cu_tokens,
+                   int32_t total_tokens, const int32_t* seq_lens, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  Shape s;
+  hsa::RotaryTable t;
+  int* err = nullptr;
+  int32_t rc = check_dims(d, s, false, true);
+  if (rc == HSA_OK) rc = check_rotary(rotary, &t);
+  if (rc != HSA_OK) return rc;
+  if (total_tokens < 0 || !aligned(positions, 4) || !aligned(cu_tokens, 4) || !aligned(seq_lens, 4))
+    return HSA_ERR_INVALID_ARG;
+  if (!positions && (!seq_lens || (!cu_tokens && total_tokens != s.batch)))
+    return HSA_ERR_INVALID_ARG;
+  if ((k == nullptr) != (k_out == nullptr)) return HSA_ERR_INVALID_ARG;
+  if (total_tokens == 0) return HSA_OK;  // no rows, no arrays of them
+  rc = check_row_array(q, q_stride, s.hq);
+  if (rc == HSA_OK) rc = check_row_array(q_out, q_out_stride, s.hq);
+  if (rc == HSA_OK && k) rc = check_row_array(k, k_stride, s.hkv);
+  if (rc == HSA_OK && k) rc = check_row_array(k_out, k_out_stride, s.hkv);
+  if (rc == HSA_OK) rc = error_word(workspace, workspace_bytes, &err);
+  if (rc != HSA_OK) return rc;
+  // an array turned in place keeps its stride
+  if ((q == q_out && q_stride != q_out_stride) || (k && k == k_out && k_stride != k_out_stride))
+    return HSA_ERR_INVALID_ARG;
+  // work items (a row and 16 heads) are counted in 32 bits
+  if ((long long)total_tokens * ((s.hq + 15) / 16 + (s.hkv + 15) / 16) > INT32_MAX / 2)
+    return HSA_ERR_UNSUPPORTED;
+  return cuda_status(hsa::launch_rotate(s, t, k != nullptr, q, q_stride, q_out, q_out_stride, k,
+                                        k_stride, k_out, k_out_stride, positions, cu_tokens,
+                                        total_tokens, seq_lens, err, as_stream(stream)));
+}
+
+int32_t hsa_kv8_write_rotated(const hsa_dims* d, const hsa_kv8* cache, const hsa_rotary* rotary,
+                              const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                              const void* k_new, int64_t k_stride, const void* v_new,
+                              int64_t v_stride, const int32_t* positions, const int32_t* cu_tokens,
+                              int32_t total_tokens, const int32_t* page_table,
+                              const int32_t* seq_lens, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  Shape s;
+  hsa::Kv8 c;
+  hsa::RotaryTable t;
+  int* err = nullptr;
+  int32_t rc = check_kv8(d, cache, s, &c);
+  if (rc == HSA_OK) rc = check_rotary(rotary, &t);
+  if (rc == HSA_OK) rc = check_rows(s, cu_tokens, total_tokens, page_table, seq_lens);
+  if (rc == HSA_OK && !aligned(positions, 4)) rc = HSA_ERR_INVALID_ARG;
+  if (rc == HSA_OK && (q == nullptr) != (q_out == nullptr)) rc = HSA_ERR_INVALID_ARG;
+  if (rc != HSA_OK || total_tokens == 0) return rc;  // no rows, no arrays of them
+  rc = check_row_array(k_new, k_stride, s.hkv);
+  if (rc == HSA_OK) rc = check_row_array(v_new, v_stride, s.hkv);
+  if (rc == HSA_OK && q) rc = check_row_array(q, q_stride, s.hq);
+  if (rc == HSA_OK && q) rc = check_row_array(q_out, q_out_stride, s.hq);
+  if (rc == HSA_OK && q && q == q_out && q_stride != q_out_stride) rc = HSA_ERR_INVALID_ARG;
+  if (rc == HSA_OK) rc = error_word(workspace, workspace_bytes, &err);
+  if (rc != HSA_OK) return rc;
+  // work items: check_rows counts the blocks'; a row and 16 query heads the others
+  if ((long long)total_tokens * ((s.hq + 15) / 16) > INT32_MAX / 4) return HSA_ERR_UNSUPPORTED;
+  return cuda_status(hsa::launch_kv8_write_rotated(
+      s, c, t, q, q_stride, q_out, q_out_stride, k_new, k_stride, v_new, v_stride, positions,
+      cu_tokens, total_tokens, page_table, seq_lens, err, as_stream(stream)));
+}
+
+int32_t hsa_kv8_tree(const hsa_dims* d, const hsa_kv8* cache, const void* q, int64_t q_stride,
+                     const int32_t* parents, const int32_t* cu_tokens, int32_t total_tokens,
+                     const int32_t* page_table, const int32_t* seq_lens, void* out, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  Shape s;
+  hsa::Kv8 c;
+  int32_t rc = check_kv8(d, cache, s, &c);
+  if (rc == HSA_OK) rc = check_rows(s, cu_tokens, total_tokens, page_table, seq_lens);
+  if (rc == HSA_OK && !aligned(parents, 4)) rc = HSA_ERR_INVALID_ARG;
+  if (rc != HSA_OK || total_tokens == 0) return rc;  // no rows, no arrays of them
+  rc = check_row_array(q, q_stride, s.hq);
+  if (rc != HSA_OK) return rc;
+  if (!out || !aligned(out, 16) || !aligned(lse, 4)) return HSA_ERR_INVALID_ARG;
+  rc = check_ws(s, workspace, workspace_bytes, kv8_decode_layout().end);
+  if (rc != HSA_OK) return rc;
+  return cuda_status(hsa::launch_kv8_tree(s, c, q, q_stride, parents, cu_tokens, total_tokens,
+                                          page_table, seq_lens, out, lse,
+                                          static_cast<int*>(workspace), as_stream(stream)));
+}
+
+int32_t hsa_kv8_keep(const hsa_dims* d, const hsa_kv8* cache, const int32_t* keep_idx,
+                     int32_t keep_stride, const int32_t* n_keep, const int32_t* cu_tokens,
+                     const int32_t* page_table, const int32_t* seq_lens, int32_t* new_lens,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  Shape s;
+  hsa::Kv8 c;
+  int* err = nullptr;
+  int32_t rc = check_kv8(d, cache, s, &c);
+  if (rc != HSA_OK) return rc;
+  if (!n_keep || !page_table || !seq_lens || keep_stride < 0 || (keep_stride > 0 && !keep_idx))
+    return HSA_ERR_INVALID_ARG;
+  if (!aligned(keep_idx, 4) || !aligned(n_keep, 4) || !aligned(cu_tokens, 4) ||
+      !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(new_lens, 4))
+    return HSA_ERR_INVALID_ARG;
+  if (new_lens == seq_lens) return HSA_ERR_INVALID_ARG;  // other warps still read the lengths
+  rc = error_word(workspace, workspace_bytes, &err);
+  if (rc != HSA_OK) return rc;
+  return cuda_status(hsa::launch_kv8_keep(s, c, keep_idx, keep_stride, n_keep, cu_tokens,
+                                          page_table, seq_lens, new_lens, err, as_stream(stream)));
 }
 
 int32_t hsa_read_device_error(void* workspace, void* stream, int32_t* code) {

@@ -198,4 +198,42 @@ cudaError_t launch_kv8_prefill(const Shape& s, const Kv8& c, const void* q, long
                                float* part_ml, float* part_o, int* err, int num_sms,
                                cudaStream_t st);
 
+// ---- rotary.cu, kv8_draft.cu, kv8_tree.cu: positions and drafted tokens
+struct RotaryTable {
+  const float* table;  // [rows][dim]: cos, then sin
+  int rows, dim;
+  int neighbours;
+};
+struct RotaryAngles {
+  double base;
+  int scaling;  // 0 none, 1 linear, 2 by parts
+  double factor, low, high, original, magnitude;
+};
+cudaError_t launch_rotary_table(const RotaryAngles& a, float* table, int rows, int dim,
+                                cudaStream_t st);
+// positions nullable (the tokens' places); cu nullable: one token a sequence
+cudaError_t launch_rotate(const Shape& s, const RotaryTable& t, bool with_k, const void* q,
+                          long long q_stride, void* q_out, long long q_out_stride, const void* k,
+                          long long k_stride, void* k_out, long long k_out_stride,
+                          const int32_t* positions, const int32_t* cu, int total,
+                          const int32_t* seq_lens, int* err, cudaStream_t st);
+// q nullable: no queries
+cudaError_t launch_kv8_write_rotated(const Shape& s, const Kv8& c, const RotaryTable& t,
+                                     const void* q, long long q_stride, void* q_out,
+                                     long long q_out_stride, const void* k_new, long long k_stride,
+                                     const void* v_new, long long v_stride,
+                                     const int32_t* positions, const int32_t* cu, int total,
+                                     const int32_t* page_table, const int32_t* seq_lens, int* err,
+                                     cudaStream_t st);
+// at most kKv8TreeNodes drafted tokens a sequence; parents nullable: a chain
+constexpr int kKv8TreeNodes = 256;
+cudaError_t launch_kv8_tree(const Shape& s, const Kv8& c, const void* q, long long q_stride,
+                            const int32_t* parents, const int32_t* cu, int total,
+                            const int32_t* page_table, const int32_t* seq_lens, void* out,
+                            float* lse, int* err, cudaStream_t st);
+cudaError_t launch_kv8_keep(const Shape& s, const Kv8& c, const int32_t* keep_idx, int keep_stride,
+                            const int32_t* n_keep, const int32_t* cu, const int32_t* page_table,
+                            const int32_t* seq_lens, int32_t* new_lens, int* err,
+                            cudaStream_t st);
+
 }  // namespace hsa

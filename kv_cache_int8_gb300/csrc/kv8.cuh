@@ -1,5 +1,5 @@
 // kv8.cuh -- what the kernels of the 8-bit K/V cache share: its layout, the rows of new tokens,
-// and the exact conversions of its codes to fp16.
+// the exact conversions of its codes to fp16 and fp32, and the codes of values.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -111,6 +111,69 @@ struct Codes<kE4m3> {
     return d;
   }
 };
+
+// One warp behind the units: sequences that do not fit (offsets that lead outside the arrays may
+// have no unit at all).
+__device__ __forceinline__ void report_bad(const NewRows& rows, int lane, int* err) {
+  for (int b = lane; b < rows.batch; b += 32)
+    if (new_span(rows, b).bad) set_error(err, kDevErrCheck);
+}
+
+template <int F>
+__device__ __forceinline__ constexpr float levels() {
+  return F == kE4m3 ? 448.0f : 127.0f;
+}
+
+// Codes of four values: f32(x * inv) rounded to the format, halves to even. int8: adding
+// 1.5 * 2^23 leaves the rounded integer in the low byte (|x * inv| <= 127 (1 + 2^-22)).
+template <int F>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
+  a = __fmul_rn(a, inv);
+  b = __fmul_rn(b, inv);
+  c = __fmul_rn(c, inv);
+  d = __fmul_rn(d, inv);
+  if constexpr (F == kInt8) {
+    const float magic = 12582912.0f;
+    const uint32_t ab = prmt(__float_as_uint(__fadd_rn(a, magic)),
+                             __float_as_uint(__fadd_rn(b, magic)), 0x0040u);
+    const uint32_t cd = prmt(__float_as_uint(__fadd_rn(c, magic)),
+                             __float_as_uint(__fadd_rn(d, magic)), 0x0040u);
+    return prmt(ab, cd, 0x5410u);
+  } else {
+    uint16_t ab, cd;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(ab) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(cd) : "f"(d), "f"(c));
+    return (uint32_t)ab | ((uint32_t)cd << 16);
+  }
+}
+
+// One value with NaN as 0 and infinities at the largest code.
+template <int F>
+__device__ __forceinline__ float tame(float x, float inv) {
+  if (x != x) return 0.0f;
+  const float y = __fmul_rn(x, inv);
+  if (y != y) return 0.0f;  // infinity under inv = 0
+  return fminf(fmaxf(y, -levels<F>()), levels<F>());
+}
+
+// Values of four codes (exact).
+template <int F>
+__device__ __forceinline__ void values4(uint32_t w, float* f) {
+  if constexpr (F == kInt8) {
+    w ^= 0x80808080u;  // code + 128 under 0x4B is the number 2^23 + 128 + code
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      f[i] = __fadd_rn(__uint_as_float(prmt(w, 0x4B000000u, 0x7440u + i)), -8388736.0f);
+  } else {
+    const uint32_t lo = Codes<kE4m3>::pair<0>(w), hi = Codes<kE4m3>::pair<1>(w);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    f[0] = a.x;
+    f[1] = a.y;
+    f[2] = b.x;
+    f[3] = b.y;
+  }
+}
 
 }  // namespace kv8_detail
 }  // namespace hsa

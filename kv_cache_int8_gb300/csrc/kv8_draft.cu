@@ -1,0 +1,359 @@
+// kv8_draft.cu -- drafted tokens and the 8-bit K/V cache: new tokens written with their rotary
+// positions on, and the accepted branch of a drafted tree moved into place.
+//
+// Source: "KV Cache 与长上下文推理", sections "KV Cache 回顾" (every step appends the new tokens' K
+// and V) and "KV Cache 量化"; formulas of the rotation: rotary.cuh. The pages have no drafted
+// tokens: a tree of them takes the places behind the context, and of an accepted branch only
+// the first child of every node already lies where it belongs.
+//
+// As in kv8_cache.cu one warp owns one block (page, kv head) of K or of V, 64 values a lane in
+// registers between the maximum and the codes, here in fp32: a rotated key is quantised as it is
+// computed, not rounded to bf16 in between (that would add 2^-9 of a value to half a code step,
+// 2^-8 of the block's largest). The queries of the same tokens turn in the same launch.
+#include "internal.h"
+#include "kv8.cuh"
+#include "rotary.cuh"
+
+namespace hsa {
+namespace {
+
+using namespace kv8_detail;
+using namespace rotary_detail;
+
+constexpr int kWarps = 8;
+
+// max |x| of three values, NaN if one is
+__device__ __forceinline__ float max_abs3(float m, float a, float b) {
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(m), "f"(a), "f"(b));
+  return y;
+}
+
+// The codes of one block from its new values: lane l has, of tokens 2 i + l / 16 (i = 0 .. 7),
+// channels a .. a + 3 (x[i][0..3]) and b .. b + 3; slots [first, last) are new, x is zero in the
+// others. `codes` points at the block. kRow: b = a + 4.
+template <int F, bool kRow>
+__device__ __forceinline__ void put_block(float (&x)[8][8], int first, int last, uint8_t* codes,
+                                          float* scale, int a, int b, int lane) {
+  const float s_old = *scale;
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) m = max_abs3(m, x[i][k], x[i][k + 1]);
+  // as bits, infinities and NaN above every number
+  uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7FFFFFFFu);
+  const bool odd_values = top >= 0x7F800000u;
+  if (odd_values) {  // the maximum of the finite ones
+    m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const float v = fabsf(x[i][k]);
+        if (v <= 3.402823466e38f) m = fmaxf(m, v);
+      }
+    top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+  }
+  float s = __fdiv_rn(__uint_as_float(top), levels<F>());
+  if (s < 1.17549435e-38f) s = 0.0f;
+  if (first > 0) s = fmaxf(s_old, s);
+  const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+  const int sub = lane >> 4;
+  uint8_t* const at_a = codes + sub * kHeadDim + a;
+  uint8_t* const at_b = codes + sub * kHeadDim + b;
+  auto store = [&](int i, uint32_t lo, uint32_t hi) {
+    if constexpr (kRow) {
+      *reinterpret_cast<uint2*>(at_a + 2 * i * kHeadDim) = make_uint2(lo, hi);
+    } else {
+      *reinterpret_cast<uint32_t*>(at_a + 2 * i * kHeadDim) = lo;
+      *reinterpret_cast<uint32_t*>(at_b + 2 * i * kHeadDim) = hi;
+    }
+  };
+  if (first > 0 && s > s_old) {  // the older tokens' codes under the larger scale
+    const float ratio = __fmul_rn(s_old, inv);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      if (2 * i + sub >= first) continue;
+      float f[8];
+      values4<F>(*reinterpret_cast<const uint32_t*>(at_a + 2 * i * kHeadDim), f);
+      values4<F>(*reinterpret_cast<const uint32_t*>(at_b + 2 * i * kHeadDim), f + 4);
+      store(i, codes4<F>(f[0], f[1], f[2], f[3], ratio), codes4<F>(f[4], f[5], f[6], f[7], ratio));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const int slot = 2 * i + sub;
+    if (slot < first || slot >= last) continue;
+    float by = inv;
+    if (odd_values) {
+#pragma unroll
+      for (int k = 0; k < 8; k++) x[i][k] = tame<F>(x[i][k], inv);
+      by = 1.0f;
+    }
+    store(i, codes4<F>(x[i][0], x[i][1], x[i][2], x[i][3], by),
+          codes4<F>(x[i][4], x[i][5], x[i][6], x[i][7], by));
+  }
+  if (lane == 0) *scale = s;
+}
+
+struct WriteSide {
+  const __nv_bfloat16* x;  // rows
+  long long stride;        // elements
+  uint8_t* codes;
+  float* scale;
+};
+
+// Units: blocks x heads x (K, V), then (row, 16 query heads); one warp behind them reports
+// sequences that do not fit.
+template <int F, bool kNeighbours>
+__global__ void __launch_bounds__(kWarps * 32, 2)
+    kv8_write_rotated_kernel(const NewRows rows, const Rotary rot, const WriteSide ks,
+                             const WriteSide vs, const RowSide qs,
+                             const int32_t* __restrict__ page_table, int hkv, int num_pages,
+                             int block_units, int units, int* err) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (unit == units) report_bad(rows, lane, err);
+  if (unit >= units) return;
+  if (unit >= block_units) {  // queries
+    const int per = row_units(qs.heads);
+    const int row = (unit - block_units) / per, part = (unit - block_units) % per;
+    const int b = rows.cu ? warp_search(rows.batch, row, lane, [&](int i) { return rows.cu[i]; })
+                          : row;
+    if (b < 0) return;
+    const NewSpan sp = new_span(rows, b);
+    if (row < sp.row0 || row - sp.row0 >= sp.n) return;
+    const int position = rot.positions ? rot.positions[row] : sp.start + (row - sp.row0);
+    if (position < 0 || position >= rot.rows) {
+      if (lane == 0) set_error(err, kDevErrCheck);
+      return;
+    }
+    turn_row<kNeighbours>(qs, rot, row, part * kRowHeads, position, lane);
+    return;
+  }
+  const bool is_v = unit & 1;
+  const int h = (unit >> 1) % hkv, item = (unit >> 1) / hkv;
+  const int b =
+      rows.cu ? warp_search(rows.batch, item, lane, [&](int i) { return item_base(rows, i); })
+              : item;
+  if (b < 0) return;
+  const NewSpan sp = new_span(rows, b);
+  const int j = rows.cu ? item - item_base(rows, b) : 0;
+  const int end = sp.start + sp.n;  // N_b
+  const long long p = (long long)sp.start / kPage + j;
+  if (sp.n == 0 || j < 0 || p * kPage >= end) return;
+  const int page = page_table[(size_t)b * rows.max_pages + p];
+  const int base = (int)p * kPage;
+  const int first = max(sp.start - base, 0), last = min(end - base, kPage);
+  const long long row = (long long)sp.row0 + base - sp.start;  // of slot 0
+  // lane l: position of slot l
+  int position = base + lane;
+  bool bad = page < 0 || page >= num_pages;
+  if (lane >= first && lane < last) {
+    if (rot.positions) position = rot.positions[row + lane];
+    bad = bad || position < 0 || position >= rot.rows;
+  }
+  if (__any_sync(0xffffffffu, bad)) {
+    if (lane == 0) set_error(err, kDevErrCheck);
+    return;
+  }
+  const size_t block = (size_t)page * hkv + h;
+  const int sub = lane >> 4, l16 = lane & 15;
+  float x[8][8];
+  if (is_v) {
+    const __nv_bfloat16* src = vs.x + (row + sub) * vs.stride + h * kHeadDim + 8 * l16;
+    uint4 raw[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const int slot = 2 * i + sub;
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (slot >= first && slot < last) raw[i] = ldg128_nc(src + 2 * i * vs.stride);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      unpack(make_uint2(raw[i].x, raw[i].y), make_uint2(raw[i].z, raw[i].w), x[i]);
+    put_block<F, true>(x, first, last, vs.codes + block * kBlockBytesI8, vs.scale + block,
+                       8 * l16, 8 * l16 + 4, lane);
+    return;
+  }
+  const Place pl = place<kNeighbours>(l16, rot.dim);
+  const __nv_bfloat16* src = ks.x + (row + sub) * ks.stride + h * kHeadDim;
+  uint2 u[8], v[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const int slot = 2 * i + sub;
+    u[i] = v[i] = make_uint2(0u, 0u);
+    if (slot >= first && slot < last) {
+      u[i] = load4(src + 2 * i * ks.stride + pl.a);
+      v[i] = load4(src + 2 * i * ks.stride + pl.b);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const int slot = 2 * i + sub;
+    const int at = __shfl_sync(0xffffffffu, position, slot);
+    unpack(u[i], v[i], x[i]);
+    if (pl.turns && slot >= first && slot < last) turn<kNeighbours>(x[i], angles(rot, at, l16));
+  }
+  put_block<F, kNeighbours>(x, first, last, ks.codes + block * kBlockBytesI8, ks.scale + block,
+                            pl.a, pl.b, lane);
+}
+
+// ------------------------------------------------------------- the accepted branch into place
+//
+// A warp has one (sequence, kv head) of K or of V and goes through the blocks that receive kept
+// tokens, first to last: node idx_j moves from place start + idx_j to start + j, never upwards,
+// so what a block receives lies in itself or behind it, where this warp has not written yet.
+// Latency counts (a branch is a few tokens): lengths, indices, pages and codes are four loads one
+// after the other.
+struct KeepArgs {
+  NewRows rows;
+  const int32_t* idx;  // [batch][stride]
+  const int32_t* count;
+  int stride;
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  int32_t* new_lens;
+  int hkv, num_pages;
+  int* err;
+};
+
+template <int F>
+__global__ void __launch_bounds__(kWarps * 32) kv8_keep_kernel(const KeepArgs p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (unit >= p.rows.batch * p.hkv * 2) return;
+  const int b = unit / (2 * p.hkv), h = unit / 2 % p.hkv, side = unit & 1;
+  const int m = p.count[b];
+  const int32_t* idx = p.idx + (size_t)b * p.stride;
+  // an index is asked for before it is known to count: the row has `stride` of them
+  int node = lane < p.stride ? idx[lane] : -1;
+  const NewSpan sp = new_span(p.rows, b);
+  const int32_t* table = p.page_table + (size_t)b * p.rows.max_pages;
+  auto page_ok = [&](int pos) {
+    const int page = table[pos / kPage];
+    return page >= 0 && page < p.num_pages;
+  };
+  bool bad = sp.bad || m < 0 || m > sp.n || m > p.stride;
+  if (!bad) {  // every index and page, before anything is written
+    for (int j0 = 0; j0 < m; j0 += 32) {
+      const int j = j0 + lane;
+      if (j < m) {
+        const int i = j0 == 0 ? node : idx[j];
+        const int before = j == 0 ? -1 : idx[j - 1];
+        bad = bad || i <= before || i >= sp.n;
+        if (!bad) bad = !page_ok(sp.start + i) || !page_ok(sp.start + j);
+      }
+    }
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  if (bad && lane == 0) set_error(p.err, kDevErrCheck);
+  if (p.new_lens != nullptr && h == 0 && side == 0 && lane == 0)
+    p.new_lens[b] = bad ? p.rows.seq_lens[b] : sp.start + m;
+  if (bad || m == 0) return;
+  uint8_t* const codes = side ? p.v : p.k;
+  float* const scale = side ? p.v_scale : p.k_scale;
+  const int sub = lane >> 4, l16 = lane & 15;
+  const int end = sp.start + m;
+  for (int base = sp.start / kPage * kPage; base < end; base += kPage) {
+    const int first = max(sp.start - base, 0), last = min(end - base, kPage);
+    // lane l: where slot l comes from, and its scale
+    long long from = 0;
+    float s = 0.0f;
+    if (lane >= first && lane < last) {
+      const int src = sp.start + idx[base + lane - sp.start];
+      const size_t block = (size_t)table[src / kPage] * p.hkv + h;
+      from = (long long)block * kBlockBytesI8 + src % kPage * kHeadDim;
+      s = __ldcg(scale + block);
+    }
+    const int to_page = table[base / kPage];
+    uint2 raw[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const int slot = 2 * i + sub;
+      const long long at = __shfl_sync(0xffffffffu, from, slot);
+      raw[i] = make_uint2(0u, 0u);
+      if (slot >= first && slot < last)
+        raw[i] = __ldcg(reinterpret_cast<const uint2*>(codes + at) + l16);
+    }
+    float x[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const int slot = 2 * i + sub;
+      const float by = __shfl_sync(0xffffffffu, s, slot);
+      values4<F>(raw[i].x, x[i]);
+      values4<F>(raw[i].y, x[i] + 4);
+#pragma unroll
+      for (int k = 0; k < 8; k++)
+        x[i][k] = slot >= first && slot < last ? __fmul_rn(x[i][k], by) : 0.0f;
+    }
+    // (the maximum over the lanes orders all their reads before the first write)
+    const size_t to = (size_t)to_page * p.hkv + h;
+    put_block<F, true>(x, first, last, codes + to * kBlockBytesI8, scale + to, 8 * l16,
+                       8 * l16 + 4, lane);
+    __syncwarp();
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_write_rotated(const Shape& s, const Kv8& c, const RotaryTable& t,
+                                     const void* q, long long q_stride, void* q_out,
+                                     long long q_out_stride, const void* k_new, long long k_stride,
+                                     const void* v_new, long long v_stride,
+                                     const int32_t* positions, const int32_t* cu, int total,
+                                     const int32_t* page_table, const int32_t* seq_lens, int* err,
+                                     cudaStream_t st) {
+  const NewRows rows = {cu, seq_lens, s.batch, total, s.max_pages};
+  const Rotary rot = {t.table, t.rows, t.dim, positions};
+  const WriteSide ks = {static_cast<const __nv_bfloat16*>(k_new), k_stride,
+                        static_cast<uint8_t*>(c.k), c.k_scale};
+  const WriteSide vs = {static_cast<const __nv_bfloat16*>(v_new), v_stride,
+                        static_cast<uint8_t*>(c.v), c.v_scale};
+  const RowSide qs = {static_cast<const __nv_bfloat16*>(q), q_stride,
+                      static_cast<__nv_bfloat16*>(q_out), q_out_stride, q ? s.hq : 0};
+  const int block_units = new_block_items(s.batch, total, cu != nullptr) * s.hkv * 2;
+  const int units = block_units + total * row_units(qs.heads);
+  auto kernel = kv8_write_rotated_kernel<kInt8, false>;
+  if (c.format == kE4m3)
+    kernel = t.neighbours ? kv8_write_rotated_kernel<kE4m3, true>
+                          : kv8_write_rotated_kernel<kE4m3, false>;
+  else if (t.neighbours)
+    kernel = kv8_write_rotated_kernel<kInt8, true>;
+  return launch_kernel(kernel, dim3(units / kWarps + 1), dim3(kWarps * 32), 0, st, true, rows, rot,
+                       ks, vs, qs, page_table, s.hkv, s.num_pages, block_units, units, err);
+}
+
+cudaError_t launch_kv8_keep(const Shape& s, const Kv8& c, const int32_t* keep_idx, int keep_stride,
+                            const int32_t* n_keep, const int32_t* cu, const int32_t* page_table,
+                            const int32_t* seq_lens, int32_t* new_lens, int* err,
+                            cudaStream_t st) {
+  KeepArgs p;
+  p.rows = NewRows{cu, seq_lens, s.batch, INT32_MAX, s.max_pages};
+  p.idx = keep_idx;
+  p.count = n_keep;
+  p.stride = keep_stride;
+  p.k = static_cast<uint8_t*>(c.k);
+  p.v = static_cast<uint8_t*>(c.v);
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.page_table = page_table;
+  p.new_lens = new_lens;
+  p.hkv = s.hkv;
+  p.num_pages = s.num_pages;
+  p.err = err;
+  const int units = s.batch * s.hkv * 2;
+  auto kernel = c.format == kE4m3 ? kv8_keep_kernel<kE4m3> : kv8_keep_kernel<kInt8>;
+  return launch_kernel(kernel, dim3((units + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, st, true,
+                       p);
+}
+
+}  // namespace hsa

@@ -33,6 +33,7 @@ HSA_OP_STEP = 4
 HSA_OP_CACHED = 5
 HSA_OP_KV8_DECODE = 6
 HSA_OP_KV8_PREFILL = 7
+HSA_OP_KV8_TREE = 8
 
 # Every entry point declared in include/hsa.h.
 EXPORTS = (
@@ -44,6 +45,7 @@ EXPORTS = (
     "hsa_decode_step_cached",
     "hsa_kv8_write", "hsa_kv8_read", "hsa_kv8_decode", "hsa_kv8_attend",
     "hsa_kv8_prefill",
+    "hsa_rotary_table", "hsa_rotate", "hsa_kv8_write_rotated", "hsa_kv8_tree", "hsa_kv8_keep",
 )
 
 
@@ -72,6 +74,16 @@ class hsa_step_io(ctypes.Structure):
 class hsa_kv8(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int32)]
+
+
+class hsa_rotary_angles(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("base", "factor", "low", "high", "original",
+                                               "magnitude")] + [("scaling", ctypes.c_int32)]
+
+
+class hsa_rotary(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p)] + [
+        (n, ctypes.c_int32) for n in ("rows", "dim", "neighbours")]
 
 
 _DIMS_CACHE: dict = {}  # field values -> their C struct (read-only to the library)
@@ -130,6 +142,7 @@ def load(path: Optional[str] = None):
     lib = ctypes.CDLL(path)
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     C = ctypes.POINTER(hsa_kv8)
+    R = ctypes.POINTER(hsa_rotary)
     D = ctypes.POINTER(hsa_dims)
     sig = {
         "hsa_workspace_bytes": (SZ, [D, I32]),
@@ -158,6 +171,12 @@ def load(path: Optional[str] = None):
         "hsa_kv8_decode": (I32, [D, C, P, P, P, P, P, P, SZ, P]),
         "hsa_kv8_attend": (I32, [D, C, P, P, P, P, P, P, P, P, SZ, P]),
         "hsa_kv8_prefill": (I32, [D, C, P, I64, P, I32, P, P, P, P, P, SZ, P]),
+        "hsa_rotary_table": (I32, [ctypes.POINTER(hsa_rotary_angles), P, I32, I32, P]),
+        "hsa_rotate": (I32, [D, R, P, I64, P, I64, P, I64, P, I64, P, P, I32, P, P, SZ, P]),
+        "hsa_kv8_write_rotated": (I32, [D, C, R, P, I64, P, I64, P, I64, P, I64, P, P, I32, P, P,
+                                        P, SZ, P]),
+        "hsa_kv8_tree": (I32, [D, C, P, I64, P, P, I32, P, P, P, P, P, SZ, P]),
+        "hsa_kv8_keep": (I32, [D, C, P, I32, P, P, P, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -573,6 +592,130 @@ def hsa_kv8_prefill(d: Dims, cache: KV8, q, cu_tokens, page_table, seq_lens, out
     rc = load().hsa_kv8_prefill(
         ctypes.byref(d.c()), _cache(name, d, cache), q.data_ptr(), q_stride, cu, rows, table, lens,
         out.data_ptr(), lse, _p(ws), ws.numel(), _stream(stream))
+    if rc != HSA_OK:
+        _check(name, rc)
+
+
+def hsa_rotary_table(rows: int, dim: int = 128, base: float = 10000.0, scaling: int = 0,
+                     factor: float = 1.0, low: float = 1.0, high: float = 4.0,
+                     original: float = 8192.0, magnitude: float = 1.0, device="cuda",
+                     stream=None) -> torch.Tensor:
+    """A rotary table for positions 0 .. rows - 1, float32 [rows][dim] (include/hsa.h: scaling 0
+    none, 1 linear, 2 by parts)."""
+    table = torch.empty((rows, dim), dtype=torch.float32, device=device)
+    a = hsa_rotary_angles(base, factor, low, high, original, magnitude, scaling)
+    _check("hsa_rotary_table", load().hsa_rotary_table(ctypes.byref(a), table.data_ptr(), rows, dim,
+                                                       _stream(stream)))
+    return table
+
+
+class Rotary:
+    """A rotary table, float32 [positions][dim] (cosines, then sines, of dim / 2 angles), and the
+    channels that make a pair: (i, i + dim / 2), or with `neighbours` (2 i, 2 i + 1). Keeps the
+    tensor; the C struct is built once."""
+
+    def __init__(self, table, neighbours: bool = False):
+        if table.dtype is not torch.float32 or table.dim() != 2 or not table.is_contiguous():
+            raise HsaError("Rotary", HSA_ERR_INVALID_ARG, "a table is contiguous float32 [rows][dim]")
+        self.table = table
+        self._c = hsa_rotary(_p(table), table.shape[0], table.shape[1], 1 if neighbours else 0)
+        self._ref = ctypes.byref(self._c)
+
+
+def _row_list(name: str, what: str, t, rows: int) -> Optional[int]:
+    """The address of one int32 a row (None stays None, an address itself)."""
+    if t is None or type(t) is int:
+        return t
+    if t.dtype is not torch.int32 or t.numel() < rows or not t.is_contiguous():
+        raise HsaError(name, HSA_ERR_INVALID_ARG, f"{what} must be contiguous torch.int32, one a row")
+    return t.data_ptr()
+
+
+def _same_rows(name: str, x, y, heads: int):
+    """(rows, row stride of x, of y) of an input and its output of as many rows."""
+    if x is None or y is None or x.shape != y.shape:
+        raise HsaError(name, HSA_ERR_INVALID_ARG, "an output has its input's shape")
+    rows, xs = _rows(name, x, heads)
+    return rows, xs, _rows(name, y, heads)[1]
+
+
+def hsa_rotate(d: Dims, rotary: Rotary, q, q_out, k, k_out, positions=None, cu_tokens=None,
+               seq_lens=None, ws=None, stream=None) -> None:
+    """q / q_out: bf16 [total_tokens][hq][128], k / k_out: [total_tokens][hkv][128] or both None;
+    rows contiguous (any row stride), an output may be its input. positions: int32 [total_tokens],
+    or None: the tokens' places by seq_lens and cu_tokens."""
+    name = "hsa_rotate"
+    rows, qs, qos = _same_rows(name, q, q_out, d.hq)
+    if (k is None) != (k_out is None):
+        raise HsaError(name, HSA_ERR_INVALID_ARG, "k and k_out go together")
+    ks = kos = 0
+    if k is not None:
+        n, ks, kos = _same_rows(name, k, k_out, d.hkv)
+        if n != rows:
+            raise HsaError(name, HSA_ERR_INVALID_ARG, "q and k must have as many rows")
+    rc = load().hsa_rotate(
+        ctypes.byref(d.c()), rotary._ref, q.data_ptr(), qs, q_out.data_ptr(), qos, _p(k), ks,
+        _p(k_out), kos, _row_list(name, "positions", positions, rows), _offsets(name, d, cu_tokens),
+        rows, _list(name, seq_lens), _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
+    if rc != HSA_OK:
+        _check(name, rc)
+
+
+def hsa_kv8_write_rotated(d: Dims, cache: KV8, rotary: Rotary, q, q_out, k_new, v_new, positions,
+                          cu_tokens, page_table, seq_lens, ws=None, stream=None) -> None:
+    """k_new / v_new: bf16 [total_tokens][hkv][128]; q / q_out: [total_tokens][hq][128] or both
+    None; rows contiguous (any row stride). positions: as hsa_rotate."""
+    name = "hsa_kv8_write_rotated"
+    rows, k_stride, v_stride = _row_pair(name, k_new, v_new, d.hkv)
+    if (q is None) != (q_out is None):
+        raise HsaError(name, HSA_ERR_INVALID_ARG, "q and q_out go together")
+    qs = qos = 0
+    if q is not None:
+        n, qs, qos = _same_rows(name, q, q_out, d.hq)
+        if n != rows:
+            raise HsaError(name, HSA_ERR_INVALID_ARG, "q and k must have as many rows")
+    cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
+    rc = load().hsa_kv8_write_rotated(
+        ctypes.byref(d.c()), _cache(name, d, cache), rotary._ref, _p(q), qs, _p(q_out), qos,
+        k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
+        _row_list(name, "positions", positions, rows), cu, rows, table, lens, _p(ws),
+        0 if ws is None else ws.numel(), _stream(stream))
+    if rc != HSA_OK:
+        _check(name, rc)
+
+
+def hsa_kv8_tree(d: Dims, cache: KV8, q, parents, cu_tokens, page_table, seq_lens, out, lse, ws,
+                 stream=None) -> None:
+    """q, out, lse: as hsa_kv8_prefill; parents: int32 [total_tokens] or None (no branches)."""
+    name = "hsa_kv8_tree"
+    rows, q_stride = _rows(name, q, d.hq)
+    if not out.is_contiguous() or out.shape != q.shape or out.dtype is not torch.bfloat16:
+        raise HsaError(name, HSA_ERR_INVALID_ARG, "out must be contiguous, as q")
+    lse = _dense(name, "lse", lse, torch.float32, rows * d.hq)
+    cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
+    rc = load().hsa_kv8_tree(
+        ctypes.byref(d.c()), _cache(name, d, cache), q.data_ptr(), q_stride,
+        _row_list(name, "parents", parents, rows), cu, rows, table, lens, out.data_ptr(), lse,
+        _p(ws), ws.numel(), _stream(stream))
+    if rc != HSA_OK:
+        _check(name, rc)
+
+
+def hsa_kv8_keep(d: Dims, cache: KV8, keep_idx, n_keep, cu_tokens, page_table, seq_lens,
+                 new_lens=None, ws=None, stream=None) -> None:
+    """keep_idx: int32 [batch][most kept], rows contiguous; n_keep and new_lens: int32 [batch],
+    new_lens another tensor than seq_lens, or None."""
+    name = "hsa_kv8_keep"
+    if (keep_idx.dtype is not torch.int32 or keep_idx.dim() != 2 or keep_idx.shape[0] != d.batch or
+            not keep_idx.is_contiguous()):
+        raise HsaError(name, HSA_ERR_INVALID_ARG,
+                       "keep_idx must be contiguous torch.int32 [batch][most kept]")
+    cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
+    rc = load().hsa_kv8_keep(
+        ctypes.byref(d.c()), _cache(name, d, cache), keep_idx.data_ptr(), keep_idx.shape[1],
+        _row_list(name, "n_keep", n_keep, d.batch), cu, table, lens,
+        _row_list(name, "new_lens", new_lens, d.batch), _p(ws), 0 if ws is None else ws.numel(),
+        _stream(stream))
     if rc != HSA_OK:
         _check(name, rc)
 
