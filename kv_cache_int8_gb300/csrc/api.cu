@@ -207,6 +207,19 @@ Kv8Layout kv8_prefill_layout() {
   return l;
 }
 
+// The tree attention: parts as the prompt attention's, no counters, a record for each CTA.
+struct TreeLayout {
+  size_t part_ml, part_o, records, end;
+};
+TreeLayout kv8_tree_layout() {
+  TreeLayout l;
+  l.part_ml = kKv8Parts;
+  l.part_o = l.part_ml + up(hsa::kv8_tree_ml_floats() * 4);
+  l.records = l.part_o + up(hsa::kv8_tree_part_floats() * 4);
+  l.end = l.records + up(hsa::kv8_tree_record_bytes());
+  return l;
+}
+
 struct StepLayout {
   size_t block_max, tile_max, row_range, block_idx, n_blocks, sel_pages, q, k_new, v_new, out,
       lse;
@@ -609,7 +622,7 @@ size_t hsa_workspace_bytes(const hsa_dims* d, int32_t op) {
     case HSA_OP_CACHED: return cached_ws(s);
     case HSA_OP_KV8_DECODE: return kv8_decode_layout().end;
     case HSA_OP_KV8_PREFILL: return kv8_prefill_layout().end;
-    case HSA_OP_KV8_TREE: return kv8_decode_layout().end;
+    case HSA_OP_KV8_TREE: return kv8_tree_layout().end;
     default: return 0;
   }
 }
@@ -1281,11 +1294,19 @@ int32_t hsa_kv8_tree(const hsa_dims* d, const hsa_kv8* cache, const void* q, int
   rc = check_row_array(q, q_stride, s.hq);
   if (rc != HSA_OK) return rc;
   if (!out || !aligned(out, 16) || !aligned(lse, 4)) return HSA_ERR_INVALID_ARG;
-  rc = check_ws(s, workspace, workspace_bytes, kv8_decode_layout().end);
+  const TreeLayout l = kv8_tree_layout();
+  rc = check_ws(s, workspace, workspace_bytes, l.end);
   if (rc != HSA_OK) return rc;
-  return cuda_status(hsa::launch_kv8_tree(s, c, q, q_stride, parents, cu_tokens, total_tokens,
-                                          page_table, seq_lens, out, lse,
-                                          static_cast<int*>(workspace), as_stream(stream)));
+  CUtensorMap km, vm;
+  const long long blocks = (long long)s.num_pages * s.hkv;
+  rc = encode_block_map(c.k, blocks, hsa::kPage, &km);
+  if (rc == HSA_OK) rc = encode_block_map(c.v, blocks, hsa::kPage, &vm);
+  if (rc != HSA_OK) return rc;
+  char* ws = static_cast<char*>(workspace);
+  return cuda_status(hsa::launch_kv8_tree(
+      s, c, km, vm, q, q_stride, parents, cu_tokens, total_tokens, page_table, seq_lens, out, lse,
+      reinterpret_cast<float*>(ws + l.part_ml), reinterpret_cast<float*>(ws + l.part_o),
+      ws + l.records, reinterpret_cast<int*>(ws), num_sms(), as_stream(stream)));
 }
 
 int32_t hsa_kv8_keep(const hsa_dims* d, const hsa_kv8* cache, const int32_t* keep_idx,

@@ -227,10 +227,16 @@ cudaError_t launch_kv8_write_rotated(const Shape& s, const Kv8& c, const RotaryT
                                      cudaStream_t st);
 // at most kKv8TreeNodes drafted tokens a sequence; parents nullable: a chain
 constexpr int kKv8TreeNodes = 256;
-cudaError_t launch_kv8_tree(const Shape& s, const Kv8& c, const void* q, long long q_stride,
+// part_ml, part_o and records of the sizes given
+size_t kv8_tree_part_floats();
+size_t kv8_tree_ml_floats();
+size_t kv8_tree_record_bytes();
+cudaError_t launch_kv8_tree(const Shape& s, const Kv8& c, const CUtensorMap& k_map,
+                            const CUtensorMap& v_map, const void* q, long long q_stride,
                             const int32_t* parents, const int32_t* cu, int total,
                             const int32_t* page_table, const int32_t* seq_lens, void* out,
-                            float* lse, int* err, cudaStream_t st);
+                            float* lse, float* part_ml, float* part_o, void* records, int* err,
+                            int num_sms, cudaStream_t st);
 cudaError_t launch_kv8_keep(const Shape& s, const Kv8& c, const int32_t* keep_idx, int keep_stride,
                             const int32_t* n_keep, const int32_t* cu, const int32_t* page_table,
                             const int32_t* seq_lens, int32_t* new_lens, int* err,

@@ -1,166 +1,1246 @@
 // kv8_tree.cu -- attention of drafted tokens over the 8-bit K/V cache: node i of a sequence's tree
 // sees the context in front of the tree, itself and its ancestors.
 //
-// Source: "KV Cache 与长上下文推理", section "KV Cache 回顾" (decode attention equation); the pages
-// have no drafted tokens.
+// Source: "KV Cache 与长上下文推理", section "KV Cache 回顾" (decode attention equation), section
+// "KV Cache 量化"; the pages have no drafted tokens.
 //
-// One warp has one (node, query head) and goes over all tokens, four channels a lane, with the
-// running maximum and sum of the softmax in fp32.
+// Mathematics. As in the prompt attention, the codes enter the products exactly (fp16) and the
+// blocks' scales (16 tokens) are applied in fp32: with row factor f = sm_scale log2 e 2^-shift,
+//   x_t = f s_k S_t    y_t = x_t + log2 s_v
+//   out = sum_t 2^(y_t - M) c_t / sum_t 2^(x_t - M)
+// The sum takes 2^(y - M) / s_v, one factor a token, as long as every s_v is within 2^-40 ..
+// 2^40; from the first step on that has another (or a block of zeros), a second form of the step
+// sums 2^x under a maximum of its own. P = 2^(y - M + 7) is rounded to fp16 (11 bits, against 8 of
+// the bf16 result); M lags the running maximum by at most 8.
+//
+// Layout. A tree is few rows against many tokens (a kv head's group of query heads x the nodes:
+// up to 128 rows here), so the products are turned round: the tokens are the 128 rows of the
+// tensor core's tile and the queries its columns,
+//   S^T [128 tokens][64 queries] = K Q^T        O^T [128 channels][64 queries] += V^T P^T
+// and everything but the turning of codes into fp16 costs what there are queries. A thread has one
+// token, so its scales are two numbers for a whole step; the rows' maxima are only looked at
+// (one vote of 128 threads a step), and found when a score passes the lag. K's codes go from
+// shared memory through registers into tensor memory (the left operand), V's into a swizzled fp16
+// tile in shared memory, read transposed.
+//   warps 0-3, 4-7: the softmax of two streams. More than 64 rows: each has its rows of every step;
+//     up to 64: both have all rows and take the steps in turn, with a maximum, a sum and an O of
+//     its own, joined where the rows end.
+//   warps 8-11 K's codes, 12-15 V's, warp 16 the products, 17 and 18 the copies (TMA, a block
+//     each) of K and V, several steps ahead.
+// Tensor memory: S 2 streams x 2 steps x 64 columns, O 2 x 64, K 2 steps x 64.
+//
+// Work. All steps (row block, token tile) of all sequences and heads form one line, cut into equal
+// slices, one CTA each; the parts of a row block that is cut go through the workspace to a second
+// kernel that joins them, a warp a row, so that joining takes all SMs and no CTA waits.
+#include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv8.cuh"
+#include "tcgen05.cuh"
 
 namespace hsa {
 namespace {
 
 using namespace kv8_detail;
 
-constexpr int kWarps = 8;
+constexpr int kRows = 128;        // rows of a block
+constexpr int kStreamRows = 64;   // of a stream: columns of its S and O
+constexpr int kTokens = 128;      // tokens of a step
+constexpr int kTilePages = kTokens / kPage;
+constexpr int kTileBytes = 128 * kHeadDim * 2;
+constexpr int kHalfBytes = kTileBytes / 2;            // 64 channels of 128 rows
+constexpr int kRawBytes = kTokens * kHeadDim;         // codes of a step, of K or V
+constexpr int kPBytes = kTokens * kStreamRows * 2;
+constexpr int kKStages = 3, kVStages = 2;             // steps of raw codes
+constexpr int kPageRing = 16;                         // steps whose scales are kept (see Smem)
 constexpr int kWords = kKv8TreeNodes / 32;
+constexpr int kSeqs = 256;                            // sequences of a launch
+constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 16, kKLoad = 17, kVLoad = 18;
+constexpr int kThreads = 640;
+// registers a thread: softmax warpgroups, converting ones, the last; 96 on average
+constexpr int kSoftmaxRegs = 144, kConvertRegs = 72, kOtherRegs = 48;
+static_assert(2 * kSoftmaxRegs + 2 * kConvertRegs + kOtherRegs == 5 * 96, "the launch's registers");
+constexpr float kHeadroom = 7.0f, kLag = 8.0f;  // P up to 2^15
+constexpr float kSumLag = 60.0f;     // of the second form's sum, in fp32
+constexpr float kPlainScale = 40.0f; // largest |log2 s_v| of the plain form
+constexpr float kTiny = 1e-37f;      // smallest factor of a score: a masked -inf stays one
+constexpr float kLow = -1e30f;       // a maximum before any score
+constexpr int kBlockCost = 4;        // what a row block costs beside its tiles, in tiles
+constexpr int kMinPlaces = 6;        // shortest slice
+// O takes the products of at most this many steps: their own sums round to zero, 2^-23 a product
+constexpr int kMaxSteps = 256;
+constexpr uint32_t kColS = 0, kColO = 256, kColK = 384;
+
+struct Record {  // a row block that begins in a CTA's slice and goes on behind it
+  int rows, parts;
+  int slot0, cta;  // the first part's slot; the CTA
+  int row0, head0; // q's row of its first node, its first query head
+  int pad[2];
+};
 
 struct Params {
   NewRows rows;
   const __nv_bfloat16* q;
   long long q_stride;
-  const uint8_t* k;
-  const uint8_t* v;
   const float* k_scale;
   const float* v_scale;
   const int32_t* parents;
   const int32_t* page_table;
   __nv_bfloat16* out;
   float* lse;
+  float* part_ml;  // [2 CTAs][kRows] (M, l)
+  float* part_o;   // [2 CTAs][kRows][kHeadDim]
+  Record* records; // [CTAs]
   int* err;
-  int hq, hkv, group, num_pages;
-  float scale;
+  int hq, hkv, group, num_pages, block_nodes;  // block_nodes: most nodes of a row block
+  float scale_log2;
 };
 
-__device__ __forceinline__ float sum32(float x) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-  return x;
+struct Smem {
+  alignas(1024) unsigned char q[kTileBytes];
+  unsigned char v[2][kTileBytes];
+  unsigned char p[2][kPBytes];  // of a stream; between row blocks its scratch
+  unsigned char k_raw[kKStages][kRawBytes];
+  unsigned char v_raw[kVStages][kRawBytes];
+  // Of a step's blocks: x = w, but +inf where |w| is above kPlainScale; y = 1 / s_v (any number
+  // above 0 for zeros, 0 where there are no tokens); z = s_k; w = log2 s_v (-inf for both). The
+  // copies of a step begin when the codes three steps back are converted, so when the scores
+  // five back are complete; their buffer was read by its stream's softmax two of its own steps
+  // before, at most nine back, and the other stream is at most one step behind.
+  float4 page[kPageRing][kTilePages];
+  uint32_t branch[kRows][kWords];  // of each row: its node and the node's ancestors
+  float c[2][kStreamRows];         // kHeadroom - m
+  float m[2][kStreamRows];         // the rows' maxima
+  float mx[2][kStreamRows];        // those under which the second form's sums are kept
+  float by[2][kStreamRows];
+  float f[kRows];                  // row factors (NaN where the query is not finite)
+  float red[2][4][kStreamRows];    // of a stream's warps: maxima, then sums
+  alignas(8) int v_valid[kVStages][kTilePages];
+  alignas(8) uint64_t q_full, k_raw_full[kKStages], k_raw_empty[kKStages], v_raw_full[kVStages],
+      v_raw_empty[kVStages], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2],
+      s_empty[2][2], p_full[2], pv_done[2], all_done;
+  long long per;
+  int start_b, start_h, start_q, start_off;
+  uint32_t tmem;
+  int shift_max[8], shift_min[8];
+  int dead;
+};
+// behind it: pre (long long [batch + 1]), then len, n, row0 (int [batch] each)
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+// a * m + c and a + b on two values at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 m, float2 c) {
+  float2 y;
+  asm("{.reg .b64 a, m, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 m, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 a, a, m, c;\n\tmov.b64 {%0, %1}, a;}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(m.x), "f"(m.y), "f"(c.x), "f"(c.y));
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// a barrier of the stream's 128 threads that tells whether any of them says so
+__device__ __forceinline__ bool any_of(int id, bool x) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.or.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(y)
+      : "r"(id), "r"((uint32_t)x)
+      : "memory");
+  return y != 0;
+}
+
+// Waits with a limit, a whole warp alike; once a wait has run out every wait of the CTA gives up.
+__device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity, int* err) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const long long t0 = clock64();
+    while (!(ok = mbar_try_wait(bar, parity))) {
+      if (*reinterpret_cast<volatile int*>(&sm.dead)) break;
+      if (clock64() - t0 > kWaitLimitCycles) {
+        *reinterpret_cast<volatile int*>(&sm.dead) = 1;
+        set_error(err, kDevErrTimeout);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Row blocks of a sequence of n nodes, as equal as they come, and the nodes of each.
+__device__ __forceinline__ int row_blocks(int n, int most) { return (n + most - 1) / most; }
+__device__ __forceinline__ int token_tiles(int len) { return (len + kTokens - 1) / kTokens; }
+
+// A stretch of one row block's tiles: what a CTA does at a time.
+struct Piece {
+  int b, h;          // sequence, kv head
+  int node, nodes;   // first node, number of nodes
+  int rows;          // nodes x group
+  int tile, tiles;   // first tile, number of tiles
+  int all_tiles;     // of the whole row block
+  long long begin;   // the row block's first place on the line
+};
+
+// The pieces of the slice [x, end) of the line, in order. A row block's places are kBlockCost for
+// what it costs beside its tiles, then one a tile.
+struct Walk {
+  const int* len;
+  const int* n;
+  int batch, hkv, group, block_nodes;
+  long long x, end;
+  int b, h, q, off;  // off: place in the row block
+
+  __device__ __forceinline__ bool next(Piece& p) {
+    for (;;) {
+      if (x >= end) return false;
+      const int blocks = row_blocks(n[b], block_nodes), most = (n[b] + blocks - 1) / blocks;
+      p.b = b;
+      p.h = h;
+      p.node = q * most;
+      p.nodes = min(most, n[b] - p.node);
+      p.rows = p.nodes * group;
+      p.begin = x - off;
+      p.all_tiles = token_tiles(len[b]);
+      int stop = (int)min((long long)(p.all_tiles + kBlockCost), off + (end - x));
+      p.tile = max(off - kBlockCost, 0);
+      p.tiles = max(stop - kBlockCost, 0) - p.tile;
+      const int limit = p.rows > kStreamRows ? kMaxSteps : 2 * kMaxSteps;
+      if (p.tiles > limit) {  // the rest of the stretch is the next piece
+        p.tiles = limit;
+        stop = p.tile + limit + kBlockCost;
+        x += stop - off;
+        off = stop;
+        return true;
+      }
+      x += stop - off;
+      off = 0;
+      // (equal blocks may be fewer than row_blocks says: the last ones would be empty)
+      if ((q + 1) * most < n[b]) {
+        q++;
+      } else {
+        q = 0;
+        if (++h == hkv) {
+          h = 0;
+          do b++;
+          while (b < batch && n[b] == 0);
+        }
+      }
+      if (p.tiles > 0) return true;
+    }
+  }
+};
+// row blocks that are not empty
+__device__ __forceinline__ int full_blocks(int n, int most_nodes) {
+  if (n == 0) return 0;
+  const int blocks = row_blocks(n, most_nodes), most = (n + blocks - 1) / blocks;
+  return (n + most - 1) / most;
 }
 
 template <int F>
-__global__ void __launch_bounds__(kWarps * 32) kv8_tree_kernel(const Params p) {
-  __shared__ uint32_t branch[kWarps][kWords];
+__global__ void __launch_bounds__(kThreads, 1)
+    kv8_tree_kernel(const __grid_constant__ CUtensorMap k_map,
+                    const __grid_constant__ CUtensorMap v_map, const Params p) {
+  extern __shared__ unsigned char smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(
+      smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+  const int batch = p.rows.batch;
+  long long* pre = reinterpret_cast<long long*>(&sm + 1);
+  int* len = reinterpret_cast<int*>(pre + batch + 1);
+  int* num = len + batch;
+  int* row0 = num + batch;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    tma_prefetch_descriptor(&k_map);
+    tma_prefetch_descriptor(&v_map);
+    mbar_init(&sm.q_full, 256);
+    for (int i = 0; i < kKStages; i++) {
+      mbar_init(&sm.k_raw_full[i], 1);
+      mbar_init(&sm.k_raw_empty[i], 4);
+    }
+    for (int i = 0; i < kVStages; i++) {
+      mbar_init(&sm.v_raw_full[i], 1);
+      mbar_init(&sm.v_raw_empty[i], 4);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&sm.k_full[i], 128);
+      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.v_full[i], 4);
+      mbar_init(&sm.v_empty[i], 1);
+      mbar_init(&sm.s_full[i][0], 1);
+      mbar_init(&sm.s_full[i][1], 1);
+      mbar_init(&sm.s_empty[i][0], 128);
+      mbar_init(&sm.s_empty[i][1], 128);
+      mbar_init(&sm.p_full[i], 128);
+      mbar_init(&sm.pv_done[i], 1);
+    }
+    mbar_init(&sm.all_done, 1);
+    sm.dead = 0;
+    fence_barrier_init();
+  }
+  // TMEM is taken once the kernels in front are done and before the next one may start: whichever
+  // of two kernels holds it on an SM never waits for the other.
+  grid_dep_wait();
+  if (warp == kMmaWarp) tc::alloc(&sm.tmem, 512);
+  if (tid == 0) p.records[blockIdx.x].rows = 0;
+
+  // ---- the line of all steps; warp 0 finds where this CTA's slice begins
+  if (warp == 0) {
+    long long sum = 0;
+    for (int b0 = 0; b0 < batch; b0 += 32) {
+      const int b = b0 + lane;
+      long long incl = 0;
+      if (b < batch) {
+        NewSpan sp = new_span(p.rows, b);
+        if (sp.n > kKv8TreeNodes) {
+          sp.bad = true;
+          sp.n = 0;
+        }
+        if (sp.bad) set_error(p.err, kDevErrCheck);
+        len[b] = sp.start + sp.n;
+        num[b] = sp.n;
+        row0[b] = sp.row0;
+        incl = (long long)full_blocks(sp.n, p.block_nodes) * p.hkv *
+               (token_tiles(len[b]) + kBlockCost);
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      if (b < batch) pre[b + 1] = sum + incl;
+      sum += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) pre[0] = 0;
+    __syncwarp();
+    const long long per = max((sum + gridDim.x - 1) / gridDim.x, (long long)kMinPlaces);
+    const long long begin = min(blockIdx.x * per, sum);
+    if (lane == 0) {
+      sm.per = per;
+      if (begin < sum) {
+        int lo = 0, hi = batch;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (pre[mid] <= begin) lo = mid;
+          else hi = mid;
+        }
+        const int one = token_tiles(len[lo]) + kBlockCost;  // places of a row block
+        const long long at = begin - pre[lo];
+        const int head = one * full_blocks(num[lo], p.block_nodes);
+        sm.start_b = lo;
+        sm.start_h = (int)(at / head);
+        const int rest = (int)(at % head);
+        sm.start_q = rest / one;
+        sm.start_off = rest % one;
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = sm.tmem;
+  const long long per = sm.per, all = pre[batch];
+  const long long begin = min(blockIdx.x * per, all), end = min(begin + per, all);
+  Walk walk = {len, num, batch, p.hkv, p.group, p.block_nodes, begin, end,
+               sm.start_b, sm.start_h, sm.start_q, sm.start_off};
+  Piece pc;
+
+  if (warp < kKWarp) {
+    tc::more_registers<kSoftmaxRegs>();
+    // ============================================ softmax: one token a thread, 64 rows
+    const int st = warp >> 2, t = tid & 127;
+    const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+    uint32_t used = 0;  // steps of this stream so far
+    int step0 = 0;      // steps of the pieces so far
+    // After a wait that ran out everything goes on, on whatever is there: the barriers must find
+    // all threads, every access stays in bounds, and no later wait takes time.
+    // rows of sequences that do not fit: 0 and -inf
+    for (int b = blockIdx.x; b < batch; b += gridDim.x) {
+      if (p.rows.cu == nullptr ? num[b] != 0 : p.rows.cu[b + 1] - p.rows.cu[b] == num[b]) continue;
+      const int first = max(row0[b], 0);
+      const int count = min(p.rows.cu ? p.rows.cu[b + 1] : b + 1, p.rows.total) - first;
+      for (long long i = tid; i < (long long)count * p.hq * (kHeadDim / 8); i += 256)
+        reinterpret_cast<uint4*>(p.out + (size_t)first * p.hq * kHeadDim)[i] =
+            make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse != nullptr)
+        for (long long i = tid; i < (long long)count * p.hq; i += 256)
+          p.lse[(size_t)first * p.hq + i] = -INFINITY;
+    }
+    while (walk.next(pc)) {
+      const bool two = pc.rows > kStreamRows;
+      const int base_row = two ? kStreamRows * st : 0;
+      const int rows = min(pc.rows - base_row, kStreamRows);  // of this stream
+      const int chunks = (rows + 15) / 16;
+      const int n_all = len[pc.b], start = n_all - num[pc.b];
+      const int q_row = row0[pc.b] + pc.node;
+      named_sync(1, 256);  // the row block before is read out of shared and tensor memory
+      // ---- the queries in fp16, four threads a row. All rows under one power of two that puts
+      // the largest value in [2^13, 2^14), as long as the smallest row's largest is within 2^-15
+      // of it (its values down to 2^-22 of their largest are then exact in fp16, and the rest is
+      // off by less than 2^-23 of it); else each under its own, and the second form of the step.
+      bool general = false;
+      float f = 0.0f;
+      {
+        const int part = tid & 3;
+        uint4 raw[2][4];
+        int e[2];
+        int e_max = 0, e_min = 255;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          const int r = (tid >> 2) + 64 * i;
+          const bool real = r < pc.rows;
+          const __nv_bfloat16* src = p.q + (long long)(q_row + r / p.group) * p.q_stride +
+                                     (pc.h * p.group + r % p.group) * kHeadDim + part * 32;
+          uint32_t mx = 0;
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            raw[i][k] = real ? *reinterpret_cast<const uint4*>(src + 8 * k)
+                             : make_uint4(0u, 0u, 0u, 0u);
+            mx = __vmaxu2(mx, __vmaxu2(raw[i][k].x & 0x7FFF7FFFu, raw[i][k].y & 0x7FFF7FFFu));
+            mx = __vmaxu2(mx, __vmaxu2(raw[i][k].z & 0x7FFF7FFFu, raw[i][k].w & 0x7FFF7FFFu));
+          }
+          uint32_t m16 = max(mx & 0xFFFFu, mx >> 16);
+          m16 = max(m16, __shfl_xor_sync(0xffffffffu, m16, 1));
+          m16 = max(m16, __shfl_xor_sync(0xffffffffu, m16, 2));
+          e[i] = m16 >> 7;
+          if (m16 != 0 && e[i] < 255) {
+            e_max = max(e_max, e[i]);
+            e_min = min(e_min, e[i]);
+          } else {
+            e[i] = m16 == 0 ? -1 : 255;
+          }
+        }
+        e_max = __reduce_max_sync(0xffffffffu, e_max);
+        e_min = __reduce_min_sync(0xffffffffu, e_min);
+        if (lane == 0) {
+          sm.shift_max[warp] = e_max;
+          sm.shift_min[warp] = e_min;
+        }
+        named_sync(1, 256);
+#pragma unroll
+        for (int w = 0; w < 8; w++) {
+          e_max = max(e_max, sm.shift_max[w]);
+          e_min = min(e_min, sm.shift_min[w]);
+        }
+        general = e_max - e_min > 15 && e_min < 255;
+        const int common = min(13 + 127 - e_max, 126);
+        f = p.scale_log2 * __uint_as_float((uint32_t)(127 - common) << 23);
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          const int r = (tid >> 2) + 64 * i;
+          if (i == 1 && !two) continue;
+          const int shift = !general || e[i] < 0 || e[i] == 255 ? common : min(13 + 127 - e[i], 126);
+          const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+          unsigned char* dst = sm.q + (part >> 1) * kHalfBytes + (r >> 3) * 1024 + (r & 7) * 128;
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            const uint4 v = raw[i][k];
+            const int chunk = (part & 1) * 4 + k;
+            *reinterpret_cast<uint4*>(dst + ((chunk ^ (r & 7)) << 4)) =
+                make_uint4(half_pair(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
+                           half_pair(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                           half_pair(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
+                           half_pair(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+          }
+          if (part == 0)
+            sm.f[r] = e[i] == 255
+                          ? NAN
+                          : p.scale_log2 * __uint_as_float((uint32_t)(127 - shift) << 23);
+        }
+        fence_proxy_async();
+        mbar_arrive(&sm.q_full);
+      }
+      // ---- which nodes a row sees
+      if (tid < pc.rows && (pc.tile + pc.tiles) * kTokens > start) {
+#pragma unroll
+        for (int k = 0; k < kWords; k++) sm.branch[tid][k] = 0;
+        const int32_t* parents = p.parents ? p.parents + row0[pc.b] : nullptr;
+        for (int i = pc.node + tid / p.group; i >= 0;) {
+          sm.branch[tid][i >> 5] |= 1u << (i & 31);
+          const int up = parents ? parents[i] : i - 1;
+          if (up < -1 || up >= i) {
+            set_error(p.err, kDevErrCheck);
+            break;
+          }
+          i = up;
+        }
+      }
+      if (t < kStreamRows) {
+        sm.m[st][t] = kLow;
+        sm.mx[st][t] = kLow;
+        sm.c[st][t] = kHeadroom - kLow;
+      }
+      named_sync(1, 256);
+
+      float l[kStreamRows];
+#pragma unroll
+      for (int k = 0; k < kStreamRows; k++) l[k] = 0.0f;
+      const int first = two ? 0 : st, stride = two ? 1 : 2;
+      const uint32_t o_col = at + kColO + kStreamRows * st;
+      for (int j = first; j < pc.tiles; j += stride, used++) {
+        wait(sm, &sm.s_full[st][used & 1], (used >> 1) & 1, p.err);
+        tc::fence_after();
+        const float4 pg = sm.page[(step0 + j) % kPageRing][t >> 4];
+        const uint32_t s_col = at + kColS + kStreamRows * (2 * st + (used & 1));
+        const int token = (pc.tile + j) * kTokens + t, node = token - start;
+        const bool seen = token < n_all && pg.y > 0.0f;
+        const bool masked = __any_sync(0xffffffffu, !seen || node >= 0);
+        const uint32_t* bits = &sm.branch[base_row][max(node, 0) >> 5 & (kWords - 1)];
+        // scores of rows [16 c, 16 c + 16)
+        auto scores = [&](int c, uint32_t (&s)[16]) {
+          tc::load16(s_col + c * 16, s);
+          tc::wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 16; k++) {
+              const bool on = seen && (node < 0 || (bits[(16 * c + k) * kWords] >> (node & 31) & 1));
+              if (!on) s[k] = 0xFF800000u;
+            }
+          }
+        };
+        const float g = fmaxf(f * pg.z, kTiny);
+        const float2 g2 = make_float2(g, g);
+        // ---- does any score pass the maxima by more than they may lag?
+        bool over = false;
+        if (!general) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            if (c >= chunks) continue;
+            uint32_t s[16];
+            scores(c, s);
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+              const float4 add = *reinterpret_cast<const float4*>(&sm.c[st][16 * c + k]);
+              const float2 a = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
+                                    g2, make_float2(add.x, add.y));
+              const float2 b = fma2(
+                  make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), g2,
+                  make_float2(add.z, add.w));
+              top = max3(top, a.x, a.y);
+              top = max3(top, b.x, b.y);
+            }
+          }
+          over = top + pg.w > kHeadroom + kLag || (seen && pg.x == INFINITY);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < chunks; c++) {
+            uint32_t s[16];
+            scores(c, s);
+#pragma unroll
+            for (int k = 0; k < 16; k++) {
+              const int r = 16 * c + k;
+              const float x = __uint_as_float(s[k]) * fmaxf(sm.f[base_row + r] * pg.z, kTiny);
+              over = over || x + (sm.c[st][r] + pg.w) > kHeadroom + kLag ||
+                     x - sm.mx[st][r] > kSumLag;
+            }
+          }
+        }
+        if (any_of(2 + st, over)) {
+          if (!general && any_of(2 + st, seen && pg.x == INFINITY)) {
+            general = true;
+            if (t < kStreamRows) sm.mx[st][t] = fmaxf(sm.m[st][t] - kHeadroom, kLow);
+          }
+          // ---- the rows' maxima, over the stream's tokens
+          const bool any_o = j > first;  // O holds something
+          if (any_o) {
+            wait(sm, &sm.pv_done[st], (used - 1) & 1, p.err);
+            tc::fence_after();
+          }
+#pragma unroll 1
+          for (int side = general ? 1 : 0; side >= 0; side--) {  // 1: of x, 0: of y
+#pragma unroll 1
+            for (int c = 0; c < chunks; c++) {
+              uint32_t s[16];
+              scores(c, s);
+              float mine = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 16; k++) {
+                const float by =
+                    general ? fmaxf(sm.f[base_row + 16 * c + k] * pg.z, kTiny) : g;
+                const float top =
+                    warp_max(fmaf(__uint_as_float(s[k]), by, side ? 0.0f : pg.w));
+                if (lane == k) mine = top;
+              }
+              if (lane < 16) sm.red[st][warp & 3][16 * c + lane] = mine;
+            }
+            named_sync(2 + st, 128);
+            if (t < 16 * chunks) {
+              float* const kept = side ? sm.mx[st] : sm.m[st];
+              const float was = kept[t];
+              const float now = fmaxf(max3(was, sm.red[st][0][t], sm.red[st][1][t]),
+                                      fmaxf(sm.red[st][2][t], sm.red[st][3][t]));
+              kept[t] = now;
+              sm.by[st][t] = ex2(was - now);
+              if (!side) sm.c[st][t] = kHeadroom - now;
+            }
+            named_sync(2 + st, 128);
+            if (side || !general) {  // the sums
+#pragma unroll
+              for (int k = 0; k < kStreamRows; k += 4) {
+                if (k >= 16 * chunks) continue;
+                const float4 by = *reinterpret_cast<const float4*>(&sm.by[st][k]);
+                l[k] *= by.x;
+                l[k + 1] *= by.y;
+                l[k + 2] *= by.z;
+                l[k + 3] *= by.w;
+              }
+            }
+            if (!side && any_o) {  // the results
+#pragma unroll 1
+              for (int c = 0; c < chunks; c++) {
+                uint32_t o[16];
+                tc::load16(o_col + c * 16, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; k++)
+                  o[k] = __float_as_uint(__uint_as_float(o[k]) * sm.by[st][16 * c + k]);
+                tc::store16(o_col + c * 16, o);
+              }
+              tc::wait_st();
+            }
+            if (side) named_sync(2 + st, 128);  // `by` is read
+          }
+        }
+        // ---- P: the products of the stream's step before have read theirs
+        if (used > 0) wait(sm, &sm.pv_done[st], (used - 1) & 1, p.err);
+        unsigned char* const row = sm.p[st] + t * 128;
+        if (!general) {
+          const float2 w2 = make_float2(pg.w, pg.w), inv2 = make_float2(pg.y, pg.y);
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            if (c >= chunks) continue;
+            uint32_t s[16], w[8];
+            scores(c, s);
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+              const float4 add = *reinterpret_cast<const float4*>(&sm.c[st][16 * c + k]);
+              float2 a = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), g2,
+                              add2(make_float2(add.x, add.y), w2));
+              float2 b = fma2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])),
+                              g2, add2(make_float2(add.z, add.w), w2));
+              a.x = ex2(a.x);
+              a.y = ex2(a.y);
+              b.x = ex2(b.x);
+              b.y = ex2(b.y);
+              float* const sum = l + 16 * c + k;
+              const float2 la = fma2(a, inv2, make_float2(sum[0], sum[1]));
+              const float2 lb = fma2(b, inv2, make_float2(sum[2], sum[3]));
+              sum[0] = la.x;
+              sum[1] = la.y;
+              sum[2] = lb.x;
+              sum[3] = lb.y;
+              w[k / 2] = half_pair(a.x, a.y);
+              w[k / 2 + 1] = half_pair(b.x, b.y);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+              *reinterpret_cast<uint4*>(row + (((2 * c + k) ^ (t & 7)) << 4)) =
+                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            if (c >= chunks) continue;
+            uint32_t s[16], w[8];
+            scores(c, s);
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              float y[2];
+#pragma unroll
+              for (int i = 0; i < 2; i++) {
+                const int r = 16 * c + k + i;
+                const float x = __uint_as_float(s[k + i]) * fmaxf(sm.f[base_row + r] * pg.z, kTiny);
+                y[i] = ex2(x + (sm.c[st][r] + pg.w));
+                l[16 * c + k + i] += ex2(x - sm.mx[st][r]);
+              }
+              w[k / 2] = half_pair(y[0], y[1]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+              *reinterpret_cast<uint4*>(row + (((2 * c + k) ^ (t & 7)) << 4)) =
+                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          }
+        }
+        tc::fence_before();
+        mbar_arrive(&sm.s_empty[st][used & 1]);
+        fence_proxy_async();
+        mbar_arrive(&sm.p_full[st]);
+      }
+      step0 += pc.tiles;
+      const bool any = pc.tiles > first;  // this stream had steps
+      if (any) wait(sm, &sm.pv_done[st], (used - 1) & 1, p.err);
+      tc::fence_after();
+
+      // ---- the sums over the stream's tokens: halves of the rows change lanes
+#pragma unroll
+      for (int d = 16, n = 32; d > 0; d >>= 1, n >>= 1) {
+        const bool upper = lane & d;
+#pragma unroll
+        for (int k = 0; k < n; k++) {
+          const float send = upper ? l[k] : l[k + n], stay = upper ? l[k + n] : l[k];
+          l[k] = stay + __shfl_xor_sync(0xffffffffu, send, d);
+        }
+      }
+      {  // this lane's two rows: bit 4 of the lane chose 32, bit 3 16, ..
+        const int r = ((lane & 16) << 1) | ((lane & 8) << 1) | ((lane & 4) << 1) |
+                      ((lane & 2) << 1) | ((lane & 1) << 1);
+        *reinterpret_cast<float2*>(&sm.red[st][warp & 3][r]) = make_float2(l[0], l[1]);
+      }
+      if (t < kStreamRows) {
+        // The second form's frames brought together, within 2^50 of the sum's own: O (the result
+        // times the sum, in that frame) and l stay in fp32's range, and of two parts that are
+        // joined the frames differ by 2^100 at most beside their sums: a factor that fp32 flushes
+        // to 0 belongs to a part that counts for less than 2^-26. by: of O, in two factors; mx: of
+        // l.
+        float by = 1.0f, of_l = 1.0f;
+        if (general) {
+          const float ref = sm.m[st][t] - kHeadroom, top = sm.mx[st][t];
+          const float to_m = fminf(fmaxf(ref, top - 50.0f), top + 50.0f) + kHeadroom;
+          const float to = to_m - kHeadroom;  // as it is read again
+          if (top > kLow) {
+            sm.m[st][t] = to_m;
+            by = ex2(0.5f * (ref - to));
+            of_l = ex2(top - to);
+          }
+        }
+        sm.by[st][t] = by;
+        sm.mx[st][t] = of_l;
+      }
+      tc::fence_before();
+      named_sync(1, 256);
+      tc::fence_after();
+
+      // ---- the rows' weights: thread t < 64 of each stream for the rows that it writes
+      struct Weights {  // O0 * a0 * b0 + O1 * a1 * b1 + part before * w, all times inv
+        float a0, b0, a1, b1, w, inv;
+        long long out;  // the output row
+      };
+      Weights* const weights = reinterpret_cast<Weights*>(sm.p[st]);
+      const long long tiles_begin = pc.begin + kBlockCost, tiles_end = tiles_begin + pc.all_tiles;
+      // of the same stretch: a piece in front of this one, a piece behind it
+      const bool after = pc.tile > 0 && tiles_begin + pc.tile > begin;
+      const bool before = tiles_begin + pc.tile + pc.tiles < min(tiles_end, end);
+      const bool whole = !before && begin <= tiles_begin && tiles_end <= end;
+      const size_t slot = 2 * (size_t)blockIdx.x + (begin < pc.begin ? 1 : 0);
+      float2* const pml = reinterpret_cast<float2*>(p.part_ml) + slot * kRows;
+      float* const po = p.part_o + slot * kRows * kHeadDim + t;
+      const bool both = !two && pc.tiles > 1;
+      float m = kLow, sum = 0.0f;
+      if (t < rows) {
+        const int s0 = two ? st : 0;
+        auto total = [&](int s) {
+          return ((sm.red[s][0][t] + sm.red[s][1][t]) + (sm.red[s][2][t] + sm.red[s][3][t])) *
+                 sm.mx[s][t];
+        };
+        m = sm.m[s0][t];
+        sum = total(s0);
+        Weights w = {sm.by[s0][t], sm.by[s0][t], 0.0f, 0.0f, 0.0f, 1.0f, 0};
+        if (both) {
+          const float m0 = m, m1 = sm.m[1][t];
+          m = fmaxf(m0, m1);
+          w.b0 *= ex2(m0 - m);
+          w.a1 = sm.by[1][t];
+          w.b1 = w.a1 * ex2(m1 - m);
+          sum = sum * ex2(m0 - m) + total(1) * ex2(m1 - m);
+        }
+        const int r = base_row + t;
+        if (sm.f[r] != sm.f[r]) sum = NAN;
+        if (after) {
+          const float2 was = __ldcg(pml + r);
+          const float top = fmaxf(m, was.x);
+          w.w = ex2(was.x - top);
+          const float keep = ex2(m - top);
+          w.b0 *= keep;
+          w.b1 *= keep;
+          sum = sum * keep + was.y * w.w;
+          m = top;
+        }
+        w.out = (long long)(q_row + r / p.group) * p.hq + pc.h * p.group + r % p.group;
+        if (whole) {
+          w.inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+          if (p.lse != nullptr && (two || st == 0))
+            p.lse[w.out] = (m - kHeadroom + log2f(sum)) * 0.693147180559945309f;
+        }
+        weights[t] = w;
+      }
+      if (after) named_sync(1, 256);  // both streams have read what is written now
+      if (!whole && t < rows && (two || st == 0)) pml[base_row + t] = make_float2(m, sum);
+      named_sync(2 + st, 128);
+      // ---- one channel a thread
+      const uint32_t o0 = at + kColO + (two ? kStreamRows * st : 0);
+#pragma unroll 1
+      for (int c = two ? 0 : st; c < chunks; c += two ? 1 : 2) {
+        uint32_t x[16], y[16];
+        tc::load16(o0 + c * 16, x);
+        if (both) tc::load16(at + kColO + kStreamRows + c * 16, y);
+        tc::wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; k++) {
+          const int r = 16 * c + k;
+          if (r >= rows) continue;
+          const Weights w = weights[r];
+          float v = __uint_as_float(x[k]) * w.a0 * w.b0;
+          if (both) v += __uint_as_float(y[k]) * w.a1 * w.b1;
+          if (after) v += __ldcg(po + (size_t)(base_row + r) * kHeadDim) * w.w;
+          if (whole) p.out[w.out * kHeadDim + t] = __float2bfloat16(v * w.inv);
+          else po[(size_t)(base_row + r) * kHeadDim] = v;
+        }
+      }
+      // the block's parts are joined by the kernel behind this one, from the CTA of the first
+      if (!whole && !before && tid == 0 && tiles_begin >= begin) {
+        const int c0 = (int)(tiles_begin / per);
+        Record rec;
+        rec.rows = pc.rows;
+        rec.parts = (int)((tiles_end - 1) / per) - c0 + 1;
+        rec.slot0 = (int)slot;
+        rec.cta = c0;
+        rec.row0 = q_row;
+        rec.head0 = pc.h * p.group;
+        rec.pad[0] = rec.pad[1] = 0;
+        p.records[blockIdx.x] = rec;
+      }
+      tc::fence_before();
+    }
+  } else if (warp < kVWarp) {
+    tc::fewer_registers<kConvertRegs>();
+    // ============================================ K's codes: one token a thread, into TMEM
+    const int t = tid & 127;
+    const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21) + kColK;
+    int step = 0, stage = 0;
+    uint32_t parity = 0;
+    bool ok = true;
+    while (ok && walk.next(pc)) {
+      for (int j = 0; ok && j < pc.tiles; j++, step++) {
+        ok = wait(sm, &sm.k_raw_full[stage], parity, p.err);
+        if (!ok) break;
+        const uint32_t raw = smem_addr(sm.k_raw[stage]) + t * 128;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            const uint4 v = lds128(raw + (((4 * h + c) ^ (t & 7)) << 4));
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+              const uint32_t x = Codes<F>::prepare(u[k]);
+              w[8 * c + 2 * k] = Codes<F>::template pair<0>(x);
+              w[8 * c + 2 * k + 1] = Codes<F>::template pair<1>(x);
+            }
+          }
+          if (h == 0) {
+            ok = wait(sm, &sm.k_empty[step & 1], ((step >> 1) & 1) ^ 1, p.err);
+            tc::fence_after();
+          }
+          tc::store32(at + kStreamRows * (step & 1) + 32 * h, w);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.k_raw_empty[stage]);
+        tc::wait_st();
+        tc::fence_before();
+        mbar_arrive(&sm.k_full[step & 1]);
+        stage = stage == kKStages - 1 ? 0 : stage + 1;
+        parity ^= stage == 0;
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    tc::fewer_registers<kConvertRegs>();
+    // ============================================ V's codes: into a swizzled tile
+    const int w0 = (warp - kVWarp) * 32, sub = lane >> 3, c = lane & 7;
+    int step = 0;
+    bool ok = true;
+    while (ok && walk.next(pc)) {
+      for (int j = 0; ok && j < pc.tiles; j++, step++) {
+        const int stage = step & 1, parity = (step >> 1) & 1;
+        ok = wait(sm, &sm.v_raw_full[stage], parity, p.err);
+        if (!ok) break;
+        const int2 valid = *reinterpret_cast<const int2*>(&sm.v_valid[stage][w0 / kPage]);
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          const int t = w0 + 4 * i + sub;
+          v[i] = lds128(smem_addr(sm.v_raw[stage]) + t * 128 + ((c ^ (t & 7)) << 4));
+          // bytes no token wrote may be NaN, and a weight of 0 does not hide one
+          if ((t & 15) >= (i < 4 ? valid.x : valid.y)) v[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.v_raw_empty[stage]);
+        ok = wait(sm, &sm.v_empty[stage], parity ^ 1, p.err);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          const int t = w0 + 4 * i + sub;
+          const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t w[8];
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            const uint32_t x = Codes<F>::prepare(u[k]);
+            w[2 * k] = Codes<F>::template pair<0>(x);
+            w[2 * k + 1] = Codes<F>::template pair<1>(x);
+          }
+          unsigned char* dst = sm.v[stage] + (c >> 2) * kHalfBytes + t * 128;
+          // the lanes of the other half of the channels store their second chunk first: the two
+          // halves' chunks then lie in different banks
+          const int swap = c >> 2;
+#pragma unroll
+          for (int k = 0; k < 2; k++) {
+            const int which = k ^ swap;
+            *reinterpret_cast<uint4*>(dst + ((((2 * c + which) & 7) ^ (t & 7)) << 4)) =
+                which ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.v_full[stage]);
+      }
+    }
+  } else {
+    tc::fewer_registers<kOtherRegs>();
+  }
+  if (warp == kMmaWarp) {
+    // ============================================ the products
+    constexpr uint32_t kQk = tc::instr_f16(128, kStreamRows, false);
+    constexpr uint32_t kPv = tc::instr_f16(128, kStreamRows, true, true);
+    const uint32_t q_low = tc::desc_low(smem_addr(sm.q), 16);
+    const uint32_t v_low = tc::desc_low(smem_addr(sm.v[0]), kHalfBytes);
+    const uint32_t p_low = tc::desc_low(smem_addr(sm.p[0]), 16);
+    const bool lead = tc::elect();
+    int step = 0;
+    uint32_t q_phase = 0, used[2] = {0, 0}, done[2] = {0, 0};
+    bool ok = true;
+    while (ok && walk.next(pc)) {
+      const bool two = pc.rows > kStreamRows;
+      // The products with V come one step (two streams on it) or two steps (in turn) behind the
+      // scores, so that a stream's next scores are there when its softmax is done.
+      const int behind = two ? 1 : 2;
+      ok = wait(sm, &sm.q_full, q_phase, p.err);
+      q_phase ^= 1;
+      for (int j = 0; ok && j < pc.tiles + behind; j++) {
+        if (j < pc.tiles) {
+          const int at = step + j;
+          ok = wait(sm, &sm.k_full[at & 1], (at >> 1) & 1, p.err);
+#pragma unroll
+          for (int i = 0; i < 2; i++) {
+            if (!ok || (!two && (j & 1) != i)) continue;
+            const int buf = used[i] & 1;
+            ok = wait(sm, &sm.s_empty[i][buf], ((used[i] >> 1) & 1) ^ 1, p.err);
+            if (!ok) continue;
+            tc::fence_after();
+            if (lead) {
+              const uint32_t q = q_low + (two ? i * (kStreamRows * 128 >> 4) : 0);
+#pragma unroll
+              for (int c = 0; c < 8; c++)
+                tc::mma_ts<kQk>(tmem + kColS + kStreamRows * (2 * i + buf),
+                                tmem + kColK + kStreamRows * (at & 1) + c * 8,
+                                q + (((c >> 2) * kHalfBytes + (c & 3) * 32) >> 4), c > 0);
+              tc::commit(&sm.s_full[i][buf]);
+            }
+            __syncwarp();
+            used[i]++;
+          }
+          if (ok && lead) tc::commit(&sm.k_empty[at & 1]);
+          __syncwarp();
+        }
+        const int jj = j - behind;
+        if (ok && jj >= 0) {
+          const int at = step + jj;
+          ok = wait(sm, &sm.v_full[at & 1], (at >> 1) & 1, p.err);
+#pragma unroll
+          for (int i = 0; i < 2; i++) {
+            if (!ok || (!two && (jj & 1) != i)) continue;
+            ok = wait(sm, &sm.p_full[i], done[i] & 1, p.err);
+            if (!ok) continue;
+            tc::fence_after();
+            if (lead) {
+              const uint32_t v = v_low + (at & 1) * (kTileBytes >> 4);
+              const uint32_t pp = p_low + i * (kPBytes >> 4);
+              const bool add = two ? jj > 0 : jj > 1;
+#pragma unroll
+              for (int c = 0; c < 8; c++)
+                tc::mma_ss<kPv>(tmem + kColO + kStreamRows * i, v + c * (2048 >> 4),
+                                pp + c * (2048 >> 4), add || c > 0);
+              tc::commit(&sm.pv_done[i]);
+            }
+            __syncwarp();
+            done[i]++;
+          }
+          if (ok && lead) tc::commit(&sm.v_empty[at & 1]);
+          __syncwarp();
+        }
+      }
+      step += pc.tiles;
+    }
+    // the last arrivals on the barriers come before the CTA ends
+    if (ok && step > 0) {
+      wait(sm, &sm.k_empty[(step - 1) & 1], ((step - 1) >> 1) & 1, p.err);
+      wait(sm, &sm.v_empty[(step - 1) & 1], ((step - 1) >> 1) & 1, p.err);
+    }
+    // nor may products go on in shared and tensor memory that are given up
+    if (!ok) {
+      if (lead) tc::commit(&sm.all_done);
+      mbar_wait(&sm.all_done, 0);
+    }
+  } else if (warp == kKLoad || warp == kVLoad) {
+    // ============================================ the copies: 4 tiles' blocks a batch, one a lane
+    const bool is_k = warp == kKLoad;
+    const int stages = is_k ? kKStages : kVStages;
+    uint64_t* const full = is_k ? sm.k_raw_full : sm.v_raw_full;
+    uint64_t* const empty = is_k ? sm.k_raw_empty : sm.v_raw_empty;
+    unsigned char* const raw = is_k ? sm.k_raw[0] : sm.v_raw[0];
+    const CUtensorMap* const map = is_k ? &k_map : &v_map;
+    const uint64_t policy = l2_evict_first_policy();
+    struct Ahead {
+      int count;      // tiles of the batch (0: the end)
+      int y;          // this lane's block: its first row in the code array
+      int valid;      // its tokens
+      bool again;     // other row blocks read it too
+      float sk, sv;
+    };
+    bool more = walk.next(pc);
+    int done = 0;  // tiles of the piece that were fetched
+    auto fetch = [&]() {
+      Ahead a = {0, 0, 0, false, 0.0f, -1.0f};
+      if (!more) return a;
+      a.count = min(pc.tiles - done, 4);
+      const int i = (pc.tile + done) * kTilePages + lane;
+      a.again = num[pc.b] > pc.nodes;
+      if (lane < a.count * kTilePages) {
+        a.valid = min(max(len[pc.b] - i * kPage, 0), kPage);
+        if (a.valid > 0) {
+          const int page = p.page_table[(size_t)pc.b * p.rows.max_pages + i];
+          if (page >= 0 && page < p.num_pages) {
+            const int block = page * p.hkv + pc.h;
+            a.y = block * kPage;
+            if (is_k) {
+              a.sk = p.k_scale[block];
+              a.sv = p.v_scale[block];
+            }
+          } else {
+            set_error(p.err, kDevErrCheck);
+            a.valid = 0;
+          }
+        }
+      }
+      done += a.count;
+      if (done == pc.tiles) {
+        done = 0;
+        more = walk.next(pc);
+      }
+      return a;
+    };
+    Ahead cur = fetch(), next = fetch();
+    int step = 0, stage = 0;
+    uint32_t parity = 0;  // of `full` in this round through the stages
+    bool ok = true;
+    while (ok && cur.count > 0) {
+      for (int j = 0; j < cur.count; j++, step++) {
+        ok = wait(sm, &empty[stage], parity ^ 1, p.err);
+        if (!ok) break;
+        const bool mine = lane >> 3 == j;
+        const int blocks = __popc(__ballot_sync(0xffffffffu, mine && cur.valid > 0));
+        if (mine) {
+          if (is_k) {
+            const float log = log2f(cur.sv);
+            sm.page[step % kPageRing][lane & 7] =
+                cur.valid == 0 ? make_float4(-INFINITY, 0.0f, 0.0f, -INFINITY)
+                               : make_float4(fabsf(log) <= kPlainScale ? log : INFINITY,
+                                             cur.sv == 0.0f ? 1.0f : 1.0f / cur.sv, cur.sk, log);
+          } else {
+            sm.v_valid[stage][lane & 7] = cur.valid;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&full[stage], blocks * kBlockBytesI8);
+        __syncwarp();
+        if (mine && cur.valid > 0) {
+          unsigned char* dst = raw + stage * kRawBytes + (lane & 7) * kBlockBytesI8;
+          if (cur.again) tma_load_2d(dst, map, 0, cur.y, &full[stage]);
+          else tma_load_2d_hint(dst, map, 0, cur.y, &full[stage], policy);
+        }
+        stage = stage == stages - 1 ? 0 : stage + 1;
+        parity ^= stage == 0;
+      }
+      cur = next;
+      next = fetch();
+    }
+    // copies under way write this CTA's shared memory: one more wait for each
+    if (!ok) {
+      for (int i = 0; i < min(step, stages); i++) {
+        stage = stage == 0 ? stages - 1 : stage - 1;
+        parity ^= stage == stages - 1;
+        mbar_wait(&full[stage], parity);
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  grid_dep_launch();
+  if (warp == kMmaWarp) {
+    tc::fence_after();
+    tc::dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------- row blocks that were cut, joined
+//
+// Grid: (CTAs of the attention, kRows / kJoinRows); a warp takes a row at a time, four channels a
+// lane. The weights of up to 256 parts come first, then their values, eight under way at once.
+constexpr int kJoinRows = 8, kJoinWarps = 4;
+
+struct JoinParams {
+  const float* part_ml;
+  const float* part_o;
+  const Record* records;
+  __nv_bfloat16* out;
+  float* lse;
+  int hq, group;
+};
+
+__global__ void __launch_bounds__(kJoinWarps * 32) kv8_tree_join_kernel(const JoinParams p) {
+  __shared__ float weight[kJoinWarps][kKv8MaxCtas];
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * kWarps + warp;
-  const int row = (int)(unit / p.hq), head = (int)(unit % p.hq);
-  if (unit == (long long)p.rows.total * p.hq) report_bad(p.rows, lane, p.err);
-  if (row >= p.rows.total) return;
-  int b = row;
-  if (p.rows.cu != nullptr) {
-    int lo = 0, hi = p.rows.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.rows.cu[mid] <= row) lo = mid;
-      else hi = mid;
-    }
-    b = lo;
-    if (row < p.rows.cu[b] || row >= p.rows.cu[b + 1]) return;  // of no sequence
-  }
-  const NewSpan sp = new_span(p.rows, b);
-  const size_t at = (size_t)row * p.hq + head;
-  // sums of up to 256 tokens (l1, o1), added up in (l, o): a million adds one after the other
-  // would be 5e-5 off
-  float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  float l1 = 0.0f, o1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  auto collect = [&]() {
-    l += l1;
-    l1 = 0.0f;
+  const Record rec = p.records[blockIdx.x];
+  for (int r = blockIdx.y * kJoinRows + warp; r < min(rec.rows, (int)(blockIdx.y + 1) * kJoinRows);
+       r += kJoinWarps) {
+    // part 0 in its own slot, part i in the first slot of the i-th CTA behind
+    auto slot_of = [&](int i) { return (size_t)(i == 0 ? rec.slot0 : 2 * (rec.cta + i)); };
+    float2 ml[kKv8MaxCtas / 32];
+    float top = kLow;
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-      o[k] += o1[k];
-      o1[k] = 0.0f;
+    for (int k = 0; k < kKv8MaxCtas / 32; k++) {
+      const int i = 32 * k + lane;
+      ml[k] = make_float2(kLow, 0.0f);
+      if (i < rec.parts)
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(i) * kRows + r);
+      top = fmaxf(top, ml[k].x);
     }
-  };
-  if (sp.n > kKv8TreeNodes && lane == 0) set_error(p.err, kDevErrCheck);
-  if (sp.n > 0 && sp.n <= kKv8TreeNodes) {
-    if (lane < kWords) branch[warp][lane] = 0;
+    top = warp_max(top);
+    float sum = 0.0f;
     __syncwarp();
-    if (lane == 0) {
-      for (int i = row - sp.row0; i >= 0;) {
-        branch[warp][i >> 5] |= 1u << (i & 31);
-        const int up = p.parents ? p.parents[sp.row0 + i] : i - 1;
-        if (up < -1 || up >= i) {
-          set_error(p.err, kDevErrCheck);
-          break;
-        }
-        i = up;
-      }
+#pragma unroll
+    for (int k = 0; k < kKv8MaxCtas / 32; k++) {
+      const float w = ex2(ml[k].x - top);
+      weight[warp][32 * k + lane] = w;
+      sum += w * ml[k].y;
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     __syncwarp();
-    const uint2 raw = *reinterpret_cast<const uint2*>(p.q + (long long)row * p.q_stride +
-                                                      head * kHeadDim + 4 * lane);
-    const float q[4] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y)};
-    const int len = sp.start + sp.n, h = head / p.group;
-    for (int t = 0; t < len; t++) {
-      const int i = t - sp.start;
-      if (i >= 0 && !(branch[warp][i >> 5] >> (i & 31) & 1)) continue;
-      const int page = p.page_table[(size_t)b * p.rows.max_pages + t / kPage];
-      if (page < 0 || page >= p.num_pages) {
-        if (lane == 0) set_error(p.err, kDevErrCheck);
-        continue;
-      }
-      const size_t block = (size_t)page * p.hkv + h;
-      const size_t off = block * kBlockBytesI8 + t % kPage * kHeadDim + 4 * lane;
-      float f[4];
-      values4<F>(*reinterpret_cast<const uint32_t*>(p.k + off), f);
-      float x = q[0] * f[0] + q[1] * f[1] + q[2] * f[2] + q[3] * f[3];
-      x = sum32(x) * p.k_scale[block] * p.scale;
-      const float top = fmaxf(m, x);
-      const float keep = m == -INFINITY ? 0.0f : expf(m - top), w = expf(x - top);
-      values4<F>(*reinterpret_cast<const uint32_t*>(p.v + off), f);
-      l *= keep;
-      l1 = l1 * keep + w;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) + r * (kHeadDim / 4) + lane;
+    for (int i0 = 0; i0 < rec.parts; i0 += 8) {
+      float4 v[8];
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
-        o[k] *= keep;
-        o1[k] = o1[k] * keep + w * f[k] * p.v_scale[block];
+      for (int k = 0; k < 8; k++) {
+        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i0 + k < rec.parts) v[k] = __ldcg(src + slot_of(i0 + k) * (kRows * kHeadDim / 4));
       }
-      m = top;
-      if (t % 256 == 255) collect();
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const float w = i0 + k < rec.parts ? weight[warp][i0 + k] : 0.0f;
+        acc.x += w * v[k].x;
+        acc.y += w * v[k].y;
+        acc.z += w * v[k].z;
+        acc.w += w * v[k].w;
+      }
     }
-    collect();
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+    const size_t out =
+        (size_t)(rec.row0 + r / p.group) * p.hq + rec.head0 + r % p.group;
+    __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+    __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    reinterpret_cast<uint2*>(p.out + out * kHeadDim)[lane] =
+        make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[out] = (top - kHeadroom + log2f(sum)) * 0.693147180559945309f;
   }
-  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-  for (int k = 0; k < 4; k++) p.out[at * kHeadDim + 4 * lane + k] = __float2bfloat16(o[k] * inv);
-  if (p.lse != nullptr && lane == 0) p.lse[at] = l != 0.0f ? m + logf(l) : -INFINITY;
 }
+
+size_t smem_bytes(int batch) {
+  return 1024 + sizeof(Smem) + 8 * (size_t)(batch + 1) + 12 * (size_t)batch;
+}
+static_assert(1024 + sizeof(Smem) + 8 * (kSeqs + 1) + 12 * kSeqs <= 227 * 1024, "shared memory");
 
 }  // namespace
 
-cudaError_t launch_kv8_tree(const Shape& s, const Kv8& c, const void* q, long long q_stride,
+size_t kv8_tree_part_floats() { return (size_t)2 * kKv8MaxCtas * kRows * kHeadDim; }
+size_t kv8_tree_ml_floats() { return (size_t)2 * kKv8MaxCtas * kRows * 2; }
+size_t kv8_tree_record_bytes() { return (size_t)kKv8MaxCtas * sizeof(Record); }
+
+cudaError_t launch_kv8_tree(const Shape& s, const Kv8& c, const CUtensorMap& k_map,
+                            const CUtensorMap& v_map, const void* q, long long q_stride,
                             const int32_t* parents, const int32_t* cu, int total,
                             const int32_t* page_table, const int32_t* seq_lens, void* out,
-                            float* lse, int* err, cudaStream_t st) {
-  Params p;
-  p.rows = NewRows{cu, seq_lens, s.batch, total, s.max_pages};
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.q_stride = q_stride;
-  p.k = static_cast<const uint8_t*>(c.k);
-  p.v = static_cast<const uint8_t*>(c.v);
-  p.k_scale = c.k_scale;
-  p.v_scale = c.v_scale;
-  p.parents = parents;
-  p.page_table = page_table;
-  p.out = static_cast<__nv_bfloat16*>(out);
-  p.lse = lse;
-  p.err = err;
-  p.hq = s.hq;
-  p.hkv = s.hkv;
-  p.group = s.group;
-  p.num_pages = s.num_pages;
-  p.scale = s.sm_scale;
-  const long long units = (long long)total * s.hq;
+                            float* lse, float* part_ml, float* part_o, void* records, int* err,
+                            int num_sms, cudaStream_t st) {
   auto kernel = c.format == kE4m3 ? kv8_tree_kernel<kE4m3> : kv8_tree_kernel<kInt8>;
-  return launch_kernel(kernel, dim3((unsigned)(units / kWarps + 1)), dim3(kWarps * 32), 0, st, true,
-                       p);
+  const size_t smem = smem_bytes(std::min(s.batch, kSeqs));
+  cudaError_t e = set_kernel_smem(kernel, smem);
+  const int grid = std::min(num_sms, kKv8MaxCtas);
+  for (int b0 = 0; e == cudaSuccess && b0 < s.batch; b0 += kSeqs) {
+    const int batch = std::min(s.batch - b0, kSeqs);
+    const int skip = cu ? 0 : b0;  // without offsets a sequence's row goes by its number
+    Params p;
+    p.rows = NewRows{cu ? cu + b0 : nullptr, seq_lens + b0, batch, total - skip, s.max_pages};
+    p.q = static_cast<const __nv_bfloat16*>(q) + skip * q_stride;
+    p.q_stride = q_stride;
+    p.k_scale = c.k_scale;
+    p.v_scale = c.v_scale;
+    p.parents = parents ? parents + skip : nullptr;
+    p.page_table = page_table + (size_t)b0 * s.max_pages;
+    p.out = static_cast<__nv_bfloat16*>(out) + (size_t)skip * s.hq * kHeadDim;
+    p.lse = lse ? lse + (size_t)skip * s.hq : nullptr;
+    p.part_ml = part_ml;
+    p.part_o = part_o;
+    p.records = static_cast<Record*>(records);
+    p.err = err;
+    p.hq = s.hq;
+    p.hkv = s.hkv;
+    p.group = s.group;
+    p.num_pages = s.num_pages;
+    p.block_nodes = kRows / s.group;
+    p.scale_log2 = s.sm_scale * 1.44269504088896341f;
+    e = launch_kernel(kernel, dim3(grid), dim3(kThreads), smem, st, true, k_map, v_map, p);
+    if (e != cudaSuccess) break;
+    const JoinParams jp = {part_ml, part_o, p.records, p.out, p.lse, s.hq, s.group};
+    e = launch_kernel(kv8_tree_join_kernel, dim3(grid, kRows / kJoinRows), dim3(kJoinWarps * 32), 0,
+                      st, true, jp);
+  }
+  return e;
 }
 
 }  // namespace hsa
