@@ -56,7 +56,7 @@ constexpr int kPBytes = kTokens * kStreamRows * 2;
 constexpr int kKStages = 3, kVStages = 2;             // steps of raw codes
 constexpr int kPageRing = 16;                         // steps whose scales are kept (see Smem)
 constexpr int kWords = kKv8TreeNodes / 32;
-constexpr int kSeqs = 256;                            // sequences of a launch
+constexpr int kSeqs = 192;                            // sequences of a launch
 constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 16, kKLoad = 17, kVLoad = 18;
 constexpr int kThreads = 640;
 // registers a thread: softmax warpgroups, converting ones, the last; 96 on average
@@ -71,6 +71,8 @@ constexpr int kBlockCost = 4;        // what a row block costs beside its tiles,
 constexpr int kMinPlaces = 6;        // shortest slice
 // O takes the products of at most this many steps: their own sums round to zero, 2^-23 a product
 constexpr int kMaxSteps = 256;
+// of a step: a block without tokens; an s_v that the plain form does not take
+constexpr int kHidden = 1, kFarScale = 2;
 constexpr uint32_t kColS = 0, kColO = 256, kColK = 384;
 
 struct Record {  // a row block that begins in a CTA's slice and goes on behind it
@@ -104,8 +106,8 @@ struct Smem {
   unsigned char p[2][kPBytes];  // of a stream; between row blocks its scratch
   unsigned char k_raw[kKStages][kRawBytes];
   unsigned char v_raw[kVStages][kRawBytes];
-  // Of a step's blocks: x = w, but +inf where |w| is above kPlainScale; y = 1 / s_v (any number
-  // above 0 for zeros, 0 where there are no tokens); z = s_k; w = log2 s_v (-inf for both). The
+  // Of a step's blocks: y = 1 / s_v (any number above 0 for zeros, 0 where there are no tokens);
+  // z = s_k; w = log2 s_v (-inf for both). The
   // copies of a step begin when the codes three steps back are converted, so when the scores
   // five back are complete; their buffer was read by its stream's softmax two of its own steps
   // before, at most nine back, and the other stream is at most one step behind.
@@ -117,6 +119,8 @@ struct Smem {
   float by[2][kStreamRows];
   float f[kRows];                  // row factors (NaN where the query is not finite)
   float red[2][4][kStreamRows];    // of a stream's warps: maxima, then sums
+  float extra[2][4][kStreamRows];  // sums of a warp's tokens, of the steps with hidden tokens
+  int flags[kPageRing];            // of a step: kHidden, kFarScale
   alignas(8) int v_valid[kVStages][kTilePages];
   alignas(8) uint64_t q_full, k_raw_full[kKStages], k_raw_empty[kKStages], v_raw_full[kVStages],
       v_raw_empty[kVStages], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2],
@@ -381,7 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ============================================ softmax: one token a thread, 64 rows
     const int st = warp >> 2, t = tid & 127;
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
-    uint32_t used = 0;  // steps of this stream so far
+    uint32_t used = 0;    // steps of this stream so far
+    uint32_t s_phase = 0; // bit i: of buffer i of its S
     int step0 = 0;      // steps of the pieces so far
     // After a wait that ran out everything goes on, on whatever is there: the barriers must find
     // all threads, every access stays in bounds, and no later wait takes time.
@@ -501,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.mx[st][t] = kLow;
         sm.c[st][t] = kHeadroom - kLow;
       }
+      for (int i = tid; i < 2 * 4 * kStreamRows; i += 256) (&sm.extra[0][0][0])[i] = 0.0f;
       named_sync(1, 256);
 
       float l[kStreamRows];
@@ -508,71 +514,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < kStreamRows; k++) l[k] = 0.0f;
       const int first = two ? 0 : st, stride = two ? 1 : 2;
       const uint32_t o_col = at + kColO + kStreamRows * st;
+      float* const extra = sm.extra[st][warp & 3];
+      // The maxima may be far off: before the first step, and behind a step that rows saw nothing of.
+      bool unknown = true;
       for (int j = first; j < pc.tiles; j += stride, used++) {
-        wait(sm, &sm.s_full[st][used & 1], (used >> 1) & 1, p.err);
+        const int buf = (two ? j : j >> 1) & 1;
+        wait(sm, &sm.s_full[st][buf], s_phase >> buf & 1, p.err);
+        s_phase ^= 1u << buf;
         tc::fence_after();
-        const float4 pg = sm.page[(step0 + j) % kPageRing][t >> 4];
-        const uint32_t s_col = at + kColS + kStreamRows * (2 * st + (used & 1));
+        const int ring = (step0 + j) % kPageRing;
+        const float4 pg = sm.page[ring][t >> 4];
+        const int flags = sm.flags[ring];
+        const uint32_t s_col = at + kColS + kStreamRows * st + 2 * kStreamRows * buf;
         const int token = (pc.tile + j) * kTokens + t, node = token - start;
         const bool seen = token < n_all && pg.y > 0.0f;
-        const bool masked = __any_sync(0xffffffffu, !seen || node >= 0);
-        const uint32_t* bits = &sm.branch[base_row][max(node, 0) >> 5 & (kWords - 1)];
+        // some of the tokens are hidden from some row
+        const bool masked = (flags & kHidden) != 0 || (pc.tile + j + 1) * kTokens > start;
         // scores of rows [16 c, 16 c + 16)
         auto scores = [&](int c, uint32_t (&s)[16]) {
           tc::load16(s_col + c * 16, s);
           tc::wait_ld();
           if (masked) {
+            const uint32_t* bits =
+                &sm.branch[base_row + 16 * c][max(node, 0) >> 5 & (kWords - 1)];
 #pragma unroll
             for (int k = 0; k < 16; k++) {
-              const bool on = seen && (node < 0 || (bits[(16 * c + k) * kWords] >> (node & 31) & 1));
+              const bool on = seen && (node < 0 || (bits[k * kWords] >> (node & 31) & 1));
               if (!on) s[k] = 0xFF800000u;
             }
           }
         };
-        const float g = fmaxf(f * pg.z, kTiny);
-        const float2 g2 = make_float2(g, g);
-        // ---- does any score pass the maxima by more than they may lag?
-        bool over = false;
-        if (!general) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; c++) {
-            if (c >= chunks) continue;
-            uint32_t s[16];
-            scores(c, s);
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              const float4 add = *reinterpret_cast<const float4*>(&sm.c[st][16 * c + k]);
-              const float2 a = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
-                                    g2, make_float2(add.x, add.y));
-              const float2 b = fma2(
-                  make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), g2,
-                  make_float2(add.z, add.w));
-              top = max3(top, a.x, a.y);
-              top = max3(top, b.x, b.y);
-            }
-          }
-          over = top + pg.w > kHeadroom + kLag || (seen && pg.x == INFINITY);
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < chunks; c++) {
-            uint32_t s[16];
-            scores(c, s);
-#pragma unroll
-            for (int k = 0; k < 16; k++) {
-              const int r = 16 * c + k;
-              const float x = __uint_as_float(s[k]) * fmaxf(sm.f[base_row + r] * pg.z, kTiny);
-              over = over || x + (sm.c[st][r] + pg.w) > kHeadroom + kLag ||
-                     x - sm.mx[st][r] > kSumLag;
-            }
-          }
-        }
-        if (any_of(2 + st, over)) {
-          if (!general && any_of(2 + st, seen && pg.x == INFINITY)) {
-            general = true;
-            if (t < kStreamRows) sm.mx[st][t] = fmaxf(sm.m[st][t] - kHeadroom, kLow);
-          }
-          // ---- the rows' maxima, over the stream's tokens
+        auto factor = [&](int r) { return fmaxf(sm.f[base_row + r] * pg.z, kTiny); };
+        // The rows' maxima up to this step, over the stream's tokens, and what is kept under them.
+        auto adjust = [&]() {
           const bool any_o = j > first;  // O holds something
           if (any_o) {
             wait(sm, &sm.pv_done[st], (used - 1) & 1, p.err);
@@ -587,10 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               float mine = 0.0f;
 #pragma unroll
               for (int k = 0; k < 16; k++) {
-                const float by =
-                    general ? fmaxf(sm.f[base_row + 16 * c + k] * pg.z, kTiny) : g;
-                const float top =
-                    warp_max(fmaf(__uint_as_float(s[k]), by, side ? 0.0f : pg.w));
+                const float top = warp_max(
+                    fmaf(__uint_as_float(s[k]), factor(16 * c + k), side ? 0.0f : pg.w));
                 if (lane == k) mine = top;
               }
               if (lane < 16) sm.red[st][warp & 3][16 * c + lane] = mine;
@@ -616,6 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l[k + 2] *= by.z;
                 l[k + 3] *= by.w;
               }
+              for (int r = lane; r < 16 * chunks; r += 32) extra[r] *= sm.by[st][r];
             }
             if (!side && any_o) {  // the results
 #pragma unroll 1
@@ -632,69 +605,130 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (side) named_sync(2 + st, 128);  // `by` is read
           }
-        }
-        // ---- P: the products of the stream's step before have read theirs
-        if (used > 0) wait(sm, &sm.pv_done[st], (used - 1) & 1, p.err);
+        };
         unsigned char* const row = sm.p[st] + t * 128;
-        if (!general) {
-          const float2 w2 = make_float2(pg.w, pg.w), inv2 = make_float2(pg.y, pg.y);
+        auto put = [&](int c, const uint32_t (&w)[8]) {
 #pragma unroll
-          for (int c = 0; c < 4; c++) {
-            if (c >= chunks) continue;
-            uint32_t s[16], w[8];
-            scores(c, s);
+          for (int k = 0; k < 2; k++)
+            *reinterpret_cast<uint4*>(row + (((2 * c + k) ^ (t & 7)) << 4)) =
+                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        };
+        if (!general && (flags & kFarScale)) {
+          general = true;
+          if (t < kStreamRows) sm.mx[st][t] = fmaxf(sm.m[st][t] - kHeadroom, kLow);
+          unknown = true;
+        }
+        if (!general && !masked) {
+          // ---- P and the sums in one pass, under the maxima as they are. Where that goes over the
+          // lag (rare), the pass is taken back, the sums by the same terms again (what is lost, 2^-24
+          // of those terms, is little beside the terms under the new maxima), and made anew.
+          if (unknown) adjust();
+          unknown = false;
+          if (used > 0) wait(sm, &sm.pv_done[st], (used - 1) & 1, p.err);
+          const float g = fmaxf(f * pg.z, kTiny);
+          const float2 g2 = make_float2(g, g), w2 = make_float2(pg.w, pg.w);
+          float sign = 1.0f;
+          for (;;) {
+            const float2 inv2 = make_float2(sign * pg.y, sign * pg.y);
+            float top = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              const float4 add = *reinterpret_cast<const float4*>(&sm.c[st][16 * c + k]);
-              float2 a = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), g2,
-                              add2(make_float2(add.x, add.y), w2));
-              float2 b = fma2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])),
-                              g2, add2(make_float2(add.z, add.w), w2));
-              a.x = ex2(a.x);
-              a.y = ex2(a.y);
-              b.x = ex2(b.x);
-              b.y = ex2(b.y);
-              float* const sum = l + 16 * c + k;
-              const float2 la = fma2(a, inv2, make_float2(sum[0], sum[1]));
-              const float2 lb = fma2(b, inv2, make_float2(sum[2], sum[3]));
-              sum[0] = la.x;
-              sum[1] = la.y;
-              sum[2] = lb.x;
-              sum[3] = lb.y;
-              w[k / 2] = half_pair(a.x, a.y);
-              w[k / 2 + 1] = half_pair(b.x, b.y);
+            for (int c = 0; c < 4; c++) {
+              if (c >= chunks) continue;
+              uint32_t s[16], w[8];
+              float y[16], of = -INFINITY;
+              tc::load16(s_col + c * 16, s);
+              tc::wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; k += 4) {
+                const float4 add = *reinterpret_cast<const float4*>(&sm.c[st][16 * c + k]);
+                const float2 a = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
+                                      g2, add2(make_float2(add.x, add.y), w2));
+                const float2 b =
+                    fma2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), g2,
+                         add2(make_float2(add.z, add.w), w2));
+                of = max3(of, a.x, a.y);
+                of = max3(of, b.x, b.y);
+                y[k] = ex2(a.x);
+                y[k + 1] = ex2(a.y);
+                y[k + 2] = ex2(b.x);
+                y[k + 3] = ex2(b.y);
+                w[k / 2] = half_pair(y[k], y[k + 1]);
+                w[k / 2 + 1] = half_pair(y[k + 2], y[k + 3]);
+              }
+              top = fmaxf(top, of);
+              if (of < 100.0f) {  // (the same both ways: an infinity could not be taken back)
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                  float* const sum = l + 16 * c + k;
+                  const float2 v =
+                      fma2(make_float2(y[k], y[k + 1]), inv2, make_float2(sum[0], sum[1]));
+                  sum[0] = v.x;
+                  sum[1] = v.y;
+                }
+              }
+              put(c, w);
             }
-#pragma unroll
-            for (int k = 0; k < 2; k++)
-              *reinterpret_cast<uint4*>(row + (((2 * c + k) ^ (t & 7)) << 4)) =
-                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            if (sign < 0.0f) {
+              adjust();
+              sign = 1.0f;
+            } else if (any_of(2 + st, top > kHeadroom + kLag)) {
+              sign = -1.0f;
+            } else {
+              break;
+            }
           }
         } else {
-#pragma unroll
-          for (int c = 0; c < 4; c++) {
-            if (c >= chunks) continue;
-            uint32_t s[16], w[8];
+          // ---- hidden tokens, or the second form: looked at first, 16 rows at a time, each under
+          // its own factor; a step's sums over a warp's tokens go to shared memory
+          bool over = unknown;
+#pragma unroll 1
+          for (int c = 0; c < chunks; c++) {
+            uint32_t s[16];
             scores(c, s);
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              float y[2];
+            for (int k = 0; k < 16; k++) {
+              const int r = 16 * c + k;
+              const float x = __uint_as_float(s[k]) * factor(r);
+              over = over || x + (sm.c[st][r] + pg.w) > kHeadroom + kLag ||
+                     (general && x - sm.mx[st][r] > kSumLag);
+            }
+          }
+          if (any_of(2 + st, over)) adjust();
+          unknown = true;  // (rows that saw nothing have no maximum yet)
+          if (used > 0) wait(sm, &sm.pv_done[st], (used - 1) & 1, p.err);
+#pragma unroll 1
+          for (int c = 0; c < chunks; c++) {
+            uint32_t s[16], w[8];
+            scores(c, s);
+            float z[16];
 #pragma unroll
-              for (int i = 0; i < 2; i++) {
-                const int r = 16 * c + k + i;
-                const float x = __uint_as_float(s[k + i]) * fmaxf(sm.f[base_row + r] * pg.z, kTiny);
-                y[i] = ex2(x + (sm.c[st][r] + pg.w));
-                l[16 * c + k + i] += ex2(x - sm.mx[st][r]);
-              }
-              w[k / 2] = half_pair(y[0], y[1]);
+            for (int k = 0; k < 16; k++) {
+              const int r = 16 * c + k;
+              const float x = __uint_as_float(s[k]) * factor(r);
+              const float y = ex2(x + (sm.c[st][r] + pg.w));
+              z[k] = general ? ex2(x - sm.mx[st][r]) : y * pg.y;
+              s[k] = __float_as_uint(y);
             }
 #pragma unroll
-            for (int k = 0; k < 2; k++)
-              *reinterpret_cast<uint4*>(row + (((2 * c + k) ^ (t & 7)) << 4)) =
-                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            for (int k = 0; k < 8; k++)
+              w[k] = half_pair(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
+            put(c, w);
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) {
+              const bool upper = lane & d;
+#pragma unroll
+              for (int k = 0; k < d; k++) {
+                const float send = upper ? z[k] : z[k + d], stay = upper ? z[k + d] : z[k];
+                z[k] = stay + __shfl_xor_sync(0xffffffffu, send, d);
+              }
+            }
+            z[0] += __shfl_xor_sync(0xffffffffu, z[0], 16);
+            if (lane < 16) extra[16 * c + lane] += z[0];
+            __syncwarp();
           }
         }
         tc::fence_before();
-        mbar_arrive(&sm.s_empty[st][used & 1]);
+        mbar_arrive(&sm.s_empty[st][buf]);
         fence_proxy_async();
         mbar_arrive(&sm.p_full[st]);
       }
@@ -716,7 +750,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       {  // this lane's two rows: bit 4 of the lane chose 32, bit 3 16, ..
         const int r = ((lane & 16) << 1) | ((lane & 8) << 1) | ((lane & 4) << 1) |
                       ((lane & 2) << 1) | ((lane & 1) << 1);
-        *reinterpret_cast<float2*>(&sm.red[st][warp & 3][r]) = make_float2(l[0], l[1]);
+        const float2 more = *reinterpret_cast<const float2*>(extra + r);
+        *reinterpret_cast<float2*>(&sm.red[st][warp & 3][r]) =
+            make_float2(l[0] + more.x, l[1] + more.y);
       }
       if (t < kStreamRows) {
         // The second form's frames brought together, within 2^50 of the sum's own: O (the result
@@ -931,72 +967,91 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == kMmaWarp) {
     // ============================================ the products
-    constexpr uint32_t kQk = tc::instr_f16(128, kStreamRows, false);
-    constexpr uint32_t kPv = tc::instr_f16(128, kStreamRows, true, true);
     const uint32_t q_low = tc::desc_low(smem_addr(sm.q), 16);
     const uint32_t v_low = tc::desc_low(smem_addr(sm.v[0]), kHalfBytes);
-    const uint32_t p_low = tc::desc_low(smem_addr(sm.p[0]), 16);
+    const uint32_t p_low = tc::desc_low(smem_addr(sm.p[0]), kPBytes);
     const bool lead = tc::elect();
     int step = 0;
-    uint32_t q_phase = 0, used[2] = {0, 0}, done[2] = {0, 0};
+    uint32_t q_phase = 0, done[2] = {0, 0};
+    uint32_t s_phase = 0xF;  // bit 2 i + b: of the next wait for buffer b of stream i's S
     bool ok = true;
     while (ok && walk.next(pc)) {
       const bool two = pc.rows > kStreamRows;
       // The products with V come one step (two streams on it) or two steps (in turn) behind the
-      // scores, so that a stream's next scores are there when its softmax is done.
+      // scores, so that a stream's next scores are there when its softmax is done. Two streams'
+      // products are one: 128 columns, K and V read once.
       const int behind = two ? 1 : 2;
       ok = wait(sm, &sm.q_full, q_phase, p.err);
       q_phase ^= 1;
+      // S of stream i (0: of both) in buffer `buf` from the K tile of step `at`
+      auto scores = [&](auto instr, uint32_t d, int at) {
+        const uint32_t a = tmem + kColK + kStreamRows * (at & 1);
+        if (lead) {
+#pragma unroll
+          for (int c = 0; c < 8; c++)
+            tc::mma_ts<decltype(instr)::value>(
+                d, a + c * 8, q_low + (((c >> 2) * kHalfBytes + (c & 3) * 32) >> 4), c > 0);
+        }
+      };
+      auto values = [&](auto instr, uint32_t d, uint32_t pp, int at, bool add) {
+        const uint32_t v = v_low + (at & 1) * (kTileBytes >> 4);
+        if (lead) {
+#pragma unroll
+          for (int c = 0; c < 8; c++)
+            tc::mma_ss<decltype(instr)::value>(d, v + c * (2048 >> 4), pp + c * (2048 >> 4),
+                                               add || c > 0);
+        }
+      };
       for (int j = 0; ok && j < pc.tiles + behind; j++) {
         if (j < pc.tiles) {
           const int at = step + j;
           ok = wait(sm, &sm.k_full[at & 1], (at >> 1) & 1, p.err);
+          const int buf = (two ? j : j >> 1) & 1;
 #pragma unroll
-          for (int i = 0; i < 2; i++) {
-            if (!ok || (!two && (j & 1) != i)) continue;
-            const int buf = used[i] & 1;
-            ok = wait(sm, &sm.s_empty[i][buf], ((used[i] >> 1) & 1) ^ 1, p.err);
-            if (!ok) continue;
-            tc::fence_after();
-            if (lead) {
-              const uint32_t q = q_low + (two ? i * (kStreamRows * 128 >> 4) : 0);
-#pragma unroll
-              for (int c = 0; c < 8; c++)
-                tc::mma_ts<kQk>(tmem + kColS + kStreamRows * (2 * i + buf),
-                                tmem + kColK + kStreamRows * (at & 1) + c * 8,
-                                q + (((c >> 2) * kHalfBytes + (c & 3) * 32) >> 4), c > 0);
-              tc::commit(&sm.s_full[i][buf]);
+          for (int i = 0; i < 2; i++)
+            if (ok && (two || (j & 1) == i)) {
+              ok = wait(sm, &sm.s_empty[i][buf], s_phase >> (2 * i + buf) & 1, p.err);
+              s_phase ^= 1u << (2 * i + buf);
             }
-            __syncwarp();
-            used[i]++;
-          }
-          if (ok && lead) tc::commit(&sm.k_empty[at & 1]);
+          if (!ok) break;
+          tc::fence_after();
+          const uint32_t d = tmem + kColS + 2 * kStreamRows * buf;
+          if (two)
+            scores(std::integral_constant<uint32_t, tc::instr_f16(128, 2 * kStreamRows, false)>{}, d,
+                   at);
+          else
+            scores(std::integral_constant<uint32_t, tc::instr_f16(128, kStreamRows, false)>{},
+                   d + kStreamRows * (j & 1), at);
+#pragma unroll
+          for (int i = 0; i < 2; i++)
+            if ((two || (j & 1) == i) && lead) tc::commit(&sm.s_full[i][buf]);
+          if (lead) tc::commit(&sm.k_empty[at & 1]);
           __syncwarp();
         }
         const int jj = j - behind;
-        if (ok && jj >= 0) {
+        if (jj >= 0) {
           const int at = step + jj;
           ok = wait(sm, &sm.v_full[at & 1], (at >> 1) & 1, p.err);
 #pragma unroll
-          for (int i = 0; i < 2; i++) {
-            if (!ok || (!two && (jj & 1) != i)) continue;
-            ok = wait(sm, &sm.p_full[i], done[i] & 1, p.err);
-            if (!ok) continue;
-            tc::fence_after();
-            if (lead) {
-              const uint32_t v = v_low + (at & 1) * (kTileBytes >> 4);
-              const uint32_t pp = p_low + i * (kPBytes >> 4);
-              const bool add = two ? jj > 0 : jj > 1;
+          for (int i = 0; i < 2; i++)
+            if (ok && (two || (jj & 1) == i)) ok = wait(sm, &sm.p_full[i], done[i] & 1, p.err);
+          if (!ok) break;
+          tc::fence_after();
+          if (two)
+            values(
+                std::integral_constant<uint32_t, tc::instr_f16(128, 2 * kStreamRows, true, true)>{},
+                tmem + kColO, p_low, at, jj > 0);
+          else
+            values(std::integral_constant<uint32_t, tc::instr_f16(128, kStreamRows, true, true)>{},
+                   tmem + kColO + kStreamRows * (jj & 1), p_low + (jj & 1) * (kPBytes >> 4), at,
+                   jj > 1);
 #pragma unroll
-              for (int c = 0; c < 8; c++)
-                tc::mma_ss<kPv>(tmem + kColO + kStreamRows * i, v + c * (2048 >> 4),
-                                pp + c * (2048 >> 4), add || c > 0);
-              tc::commit(&sm.pv_done[i]);
+          for (int i = 0; i < 2; i++)
+            if (two || (jj & 1) == i) {
+              if (lead) tc::commit(&sm.pv_done[i]);
+              done[i]++;
             }
-            __syncwarp();
-            done[i]++;
-          }
-          if (ok && lead) tc::commit(&sm.v_empty[at & 1]);
+          if (lead) tc::commit(&sm.v_empty[at & 1]);
           __syncwarp();
         }
       }
@@ -1070,16 +1125,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const bool mine = lane >> 3 == j;
         const int blocks = __popc(__ballot_sync(0xffffffffu, mine && cur.valid > 0));
-        if (mine) {
-          if (is_k) {
-            const float log = log2f(cur.sv);
+        if (is_k) {
+          const float log = log2f(cur.sv);
+          const bool far = mine && cur.valid > 0 && !(fabsf(log) <= kPlainScale);
+          const int flags = (blocks < kTilePages ? kHidden : 0) |
+                            (__any_sync(0xffffffffu, far) ? kFarScale : 0);
+          if (mine)
             sm.page[step % kPageRing][lane & 7] =
-                cur.valid == 0 ? make_float4(-INFINITY, 0.0f, 0.0f, -INFINITY)
-                               : make_float4(fabsf(log) <= kPlainScale ? log : INFINITY,
-                                             cur.sv == 0.0f ? 1.0f : 1.0f / cur.sv, cur.sk, log);
-          } else {
-            sm.v_valid[stage][lane & 7] = cur.valid;
-          }
+                cur.valid == 0 ? make_float4(0.0f, 0.0f, 0.0f, -INFINITY)
+                               : make_float4(0.0f, cur.sv == 0.0f ? 1.0f : 1.0f / cur.sv, cur.sk,
+                                             log);
+          if (lane == 0) sm.flags[step % kPageRing] = flags;
+        } else if (mine) {
+          sm.v_valid[stage][lane & 7] = cur.valid;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&full[stage], blocks * kBlockBytesI8);
