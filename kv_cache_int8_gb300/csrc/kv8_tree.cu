@@ -17,17 +17,19 @@
 // up to 128 rows here), so the products are turned round: the tokens are the 128 rows of the
 // tensor core's tile and the queries its columns,
 //   S^T [128 tokens][64 queries] = K Q^T        O^T [128 channels][64 queries] += V^T P^T
-// and everything but the turning of codes into fp16 costs what there are queries. A thread has one
-// token, so its scales are two numbers for a whole step; the rows' maxima are only looked at
-// (one vote of 128 threads a step), and found when a score passes the lag. K's codes go from
-// shared memory through registers into tensor memory (the left operand), V's into a swizzled fp16
-// tile in shared memory, read transposed.
+// and everything but the turning of codes into fp16 costs what there are queries. A lane has the
+// scores of four tokens (of two blocks: its scales are a few numbers) and sixteen rows, whose sums
+// and maxima stay in registers; the maxima are only looked at (one vote of 128 threads a step), and
+// found when a score passes the lag. The codes of K and V
+// become left operands in tensor memory, V's turned on the way (ldmatrix on bytes), so shared
+// memory, whose bandwidth the products' right operands need, sees each code twice.
 //   warps 0-3, 4-7: the softmax of two streams. More than 64 rows: each has its rows of every step;
 //     up to 64: both have all rows and take the steps in turn, with a maximum, a sum and an O of
 //     its own, joined where the rows end.
 //   warps 8-11 K's codes, 12-15 V's, warp 16 the products, 17 and 18 the copies (TMA, a block
 //     each) of K and V, several steps ahead.
-// Tensor memory: S 2 streams x 2 steps x 64 columns, O 2 x 64, K 2 steps x 64.
+// Tensor memory: S 2 streams x 2 steps x 64 columns, O 2 x 64, K 64, V 64 (while the products with
+// one of them run, the other's next codes come in).
 //
 // Work. All steps (row block, token tile) of all sequences and heads form one line, cut into equal
 // slices, one CTA each; the parts of a row block that is cut go through the workspace to a second
@@ -49,31 +51,30 @@ constexpr int kRows = 128;        // rows of a block
 constexpr int kStreamRows = 64;   // of a stream: columns of its S and O
 constexpr int kTokens = 128;      // tokens of a step
 constexpr int kTilePages = kTokens / kPage;
-constexpr int kTileBytes = 128 * kHeadDim * 2;
+constexpr int kTileBytes = kRows * kHeadDim * 2;      // the queries
 constexpr int kHalfBytes = kTileBytes / 2;            // 64 channels of 128 rows
 constexpr int kRawBytes = kTokens * kHeadDim;         // codes of a step, of K or V
 constexpr int kPBytes = kTokens * kStreamRows * 2;
-constexpr int kKStages = 3, kVStages = 2;             // steps of raw codes
+constexpr int kStages = 4;                            // steps of raw codes, of K and of V
 constexpr int kPageRing = 16;                         // steps whose scales are kept (see Smem)
 constexpr int kWords = kKv8TreeNodes / 32;
-constexpr int kSeqs = 192;                            // sequences of a launch
+constexpr int kSeqs = 512;                            // sequences of a launch
 constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 16, kKLoad = 17, kVLoad = 18;
 constexpr int kThreads = 640;
 // registers a thread: softmax warpgroups, converting ones, the last; 96 on average
-constexpr int kSoftmaxRegs = 144, kConvertRegs = 72, kOtherRegs = 48;
+constexpr int kSoftmaxRegs = 152, kConvertRegs = 64, kOtherRegs = 48;
 static_assert(2 * kSoftmaxRegs + 2 * kConvertRegs + kOtherRegs == 5 * 96, "the launch's registers");
 constexpr float kHeadroom = 7.0f, kLag = 8.0f;  // P up to 2^15
-constexpr float kSumLag = 60.0f;     // of the second form's sum, in fp32
 constexpr float kPlainScale = 40.0f; // largest |log2 s_v| of the plain form
 constexpr float kTiny = 1e-37f;      // smallest factor of a score: a masked -inf stays one
 constexpr float kLow = -1e30f;       // a maximum before any score
 constexpr int kBlockCost = 4;        // what a row block costs beside its tiles, in tiles
-constexpr int kMinPlaces = 6;        // shortest slice
+constexpr int kMinPlaces = 2;        // shortest slice
 // O takes the products of at most this many steps: their own sums round to zero, 2^-23 a product
 constexpr int kMaxSteps = 256;
 // of a step: a block without tokens; an s_v that the plain form does not take
 constexpr int kHidden = 1, kFarScale = 2;
-constexpr uint32_t kColS = 0, kColO = 256, kColK = 384;
+constexpr uint32_t kColS = 0, kColO = 256, kColK = 384, kColV = 448;
 
 struct Record {  // a row block that begins in a CTA's slice and goes on behind it
   int rows, parts;
@@ -102,15 +103,14 @@ struct Params {
 
 struct Smem {
   alignas(1024) unsigned char q[kTileBytes];
-  unsigned char v[2][kTileBytes];
   unsigned char p[2][kPBytes];  // of a stream; between row blocks its scratch
-  unsigned char k_raw[kKStages][kRawBytes];
-  unsigned char v_raw[kVStages][kRawBytes];
+  unsigned char k_raw[kStages][kRawBytes];
+  unsigned char v_raw[kStages][kRawBytes];
   // Of a step's blocks: y = 1 / s_v (any number above 0 for zeros, 0 where there are no tokens);
   // z = s_k; w = log2 s_v (-inf for both). The
-  // copies of a step begin when the codes three steps back are converted, so when the scores
-  // five back are complete; their buffer was read by its stream's softmax two of its own steps
-  // before, at most nine back, and the other stream is at most one step behind.
+  // copies of a step begin when the codes four steps back are read, so when the scores six back
+  // are complete; their buffer was read by its stream's softmax two of its own steps before, at
+  // most ten back, and the other stream's eleven back.
   float4 page[kPageRing][kTilePages];
   uint32_t branch[kRows][kWords];  // of each row: its node and the node's ancestors
   float c[2][kStreamRows];         // kHeadroom - m
@@ -119,12 +119,11 @@ struct Smem {
   float by[2][kStreamRows];
   float f[kRows];                  // row factors (NaN where the query is not finite)
   float red[2][4][kStreamRows];    // of a stream's warps: maxima, then sums
-  float extra[2][4][kStreamRows];  // sums of a warp's tokens, of the steps with hidden tokens
   int flags[kPageRing];            // of a step: kHidden, kFarScale
-  alignas(8) int v_valid[kVStages][kTilePages];
-  alignas(8) uint64_t q_full, k_raw_full[kKStages], k_raw_empty[kKStages], v_raw_full[kVStages],
-      v_raw_empty[kVStages], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2],
-      s_empty[2][2], p_full[2], pv_done[2], all_done;
+  alignas(8) int v_valid[kStages][kTilePages];
+  alignas(8) uint64_t q_full, k_raw_full[kStages], k_raw_empty[kStages], v_raw_full[kStages],
+      v_raw_empty[kStages], k_full, k_empty, v_full, v_empty, s_full[2][2], s_empty[2][2], p_full[2],
+      pv_done[2], all_done;
   long long per;
   int start_b, start_h, start_q, start_off;
   uint32_t tmem;
@@ -183,6 +182,61 @@ __device__ __forceinline__ bool any_of(int id, bool x) {
       : "r"(id), "r"((uint32_t)x)
       : "memory");
   return y != 0;
+}
+
+// 16 lanes x 16 columns of tensor memory: lane l gets columns 8 i + 2 (l % 4) + {0, 1} of rows l / 4
+// (r[4 i], r[4 i + 1]) and l / 4 + 8 (r[4 i + 2], r[4 i + 3]), i < 2; wait_loaded() before use.
+__device__ __forceinline__ void load_16x16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(addr));
+}
+// tc::wait_ld() that what is made of the loaded values stays behind
+__device__ __forceinline__ void wait_loaded(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ float2 as_floats(const uint32_t* s) {
+  return make_float2(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+
+// Four 8 x 8 matrices of 16-bit values: lane l points at row l % 8 of matrix l / 8 and holds, of each,
+// row l / 4's values 2 (l % 4), + 1.
+__device__ __forceinline__ void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                               uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// Two 16 x 16 byte matrices, turned: lanes 0 .. 15 and 16 .. 31 point at their rows (tokens); lane
+// l gets, of each, the bytes of rows 4 (l % 4) .. + 3 in columns (channels) l / 4 and l / 4 + 8.
+__device__ __forceinline__ void load_turned(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// 16 lanes x 64 columns of tensor memory: lane l has columns 8 i + 2 (l % 4) + {0, 1} of rows l / 4
+// (r[4 i], r[4 i + 1]) and l / 4 + 8 (r[4 i + 2], r[4 i + 3]).
+__device__ __forceinline__ void store_16x64(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10,"
+      " %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28,"
+      " %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
 }
 
 // Waits with a limit, a whole warp alike; once a wait has run out every wait of the CTA gives up.
@@ -289,19 +343,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_descriptor(&k_map);
     tma_prefetch_descriptor(&v_map);
     mbar_init(&sm.q_full, 256);
-    for (int i = 0; i < kKStages; i++) {
+    for (int i = 0; i < kStages; i++) {
       mbar_init(&sm.k_raw_full[i], 1);
       mbar_init(&sm.k_raw_empty[i], 4);
-    }
-    for (int i = 0; i < kVStages; i++) {
       mbar_init(&sm.v_raw_full[i], 1);
       mbar_init(&sm.v_raw_empty[i], 4);
     }
+    mbar_init(&sm.k_full, 128);
+    mbar_init(&sm.k_empty, 1);
+    mbar_init(&sm.v_full, 128);
+    mbar_init(&sm.v_empty, 1);
     for (int i = 0; i < 2; i++) {
-      mbar_init(&sm.k_full[i], 128);
-      mbar_init(&sm.k_empty[i], 1);
-      mbar_init(&sm.v_full[i], 4);
-      mbar_init(&sm.v_empty[i], 1);
       mbar_init(&sm.s_full[i][0], 1);
       mbar_init(&sm.s_full[i][1], 1);
       mbar_init(&sm.s_empty[i][0], 128);
@@ -506,16 +558,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.mx[st][t] = kLow;
         sm.c[st][t] = kHeadroom - kLow;
       }
-      for (int i = tid; i < 2 * 4 * kStreamRows; i += 256) (&sm.extra[0][0][0])[i] = 0.0f;
       named_sync(1, 256);
 
-      float l[kStreamRows];
+      // A lane's share of a step, as the 16-lane loads give it: of each half h of its warp's 32
+      // tokens (a block of the cache) tokens tok + 8 i, and rows 8 b + col, + 1 of every b.
+      const int tok = 32 * (warp & 3) + (lane >> 2), col = 2 * (lane & 3);
+      float2 l[8], c[8];  // the rows' sums over its tokens, and kHeadroom - m
 #pragma unroll
-      for (int k = 0; k < kStreamRows; k++) l[k] = 0.0f;
+      for (int b = 0; b < 8; b++) l[b] = make_float2(0.0f, 0.0f);
       const int first = two ? 0 : st, stride = two ? 1 : 2;
       const uint32_t o_col = at + kColO + kStreamRows * st;
-      float* const extra = sm.extra[st][warp & 3];
-      // The maxima may be far off: before the first step, and behind a step that rows saw nothing of.
+      // The maxima may be far off: before the first step, and behind one that rows saw nothing of.
       bool unknown = true;
       for (int j = first; j < pc.tiles; j += stride, used++) {
         const int buf = (two ? j : j >> 1) & 1;
@@ -523,28 +576,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_phase ^= 1u << buf;
         tc::fence_after();
         const int ring = (step0 + j) % kPageRing;
-        const float4 pg = sm.page[ring][t >> 4];
+        const float4* pages = &sm.page[ring][2 * (warp & 3)];
         const int flags = sm.flags[ring];
         const uint32_t s_col = at + kColS + kStreamRows * st + 2 * kStreamRows * buf;
-        const int token = (pc.tile + j) * kTokens + t, node = token - start;
-        const bool seen = token < n_all && pg.y > 0.0f;
         // some of the tokens are hidden from some row
         const bool masked = (flags & kHidden) != 0 || (pc.tile + j + 1) * kTokens > start;
-        // scores of rows [16 c, 16 c + 16)
-        auto scores = [&](int c, uint32_t (&s)[16]) {
-          tc::load16(s_col + c * 16, s);
-          tc::wait_ld();
-          if (masked) {
-            const uint32_t* bits =
-                &sm.branch[base_row + 16 * c][max(node, 0) >> 5 & (kWords - 1)];
+        auto load32 = [&](int h, int b, uint32_t (&s)[16]) {  // rows [8 b, 8 b + 32)
 #pragma unroll
-            for (int k = 0; k < 16; k++) {
-              const bool on = seen && (node < 0 || (bits[k * kWords] >> (node & 31) & 1));
-              if (!on) s[k] = 0xFF800000u;
-            }
+          for (int k = 0; k < 2; k++)
+            if (b / 2 + k < chunks)
+              load_16x16(s_col + ((uint32_t)(16 * h) << 16) + 8 * b + 16 * k, s + 8 * k);
+        };
+        // scores that a row does not see become -inf
+        auto hide = [&](int h, int b0, const float4& pg, uint32_t (&s)[16]) {
+#pragma unroll
+          for (int i = 0; i < 2; i++) {
+            const int token = (pc.tile + j) * kTokens + tok + 16 * h + 8 * i, node = token - start;
+            const bool seen = token < n_all && pg.y > 0.0f;
+            const uint32_t* bits =
+                &sm.branch[base_row + col + 8 * b0][max(node, 0) >> 5 & (kWords - 1)];
+#pragma unroll
+            for (int b = 0; b < 4; b++)
+#pragma unroll
+              for (int k = 0; k < 2; k++) {
+                const bool on =
+                    seen && (node < 0 || (bits[(8 * b + k) * kWords] >> (node & 31) & 1));
+                if (!on) s[4 * b + 2 * i + k] = 0xFF800000u;
+              }
           }
         };
-        auto factor = [&](int r) { return fmaxf(sm.f[base_row + r] * pg.z, kTiny); };
+        auto factors = [&](const float4& pg, int b) {  // of rows 8 b + col, + 1, in the second form
+          const float2 v = *reinterpret_cast<const float2*>(&sm.f[base_row + 8 * b + col]);
+          return make_float2(fmaxf(v.x * pg.z, kTiny), fmaxf(v.y * pg.z, kTiny));
+        };
         // The rows' maxima up to this step, over the stream's tokens, and what is kept under them.
         auto adjust = [&]() {
           const bool any_o = j > first;  // O holds something
@@ -554,18 +618,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll 1
           for (int side = general ? 1 : 0; side >= 0; side--) {  // 1: of x, 0: of y
-#pragma unroll 1
-            for (int c = 0; c < chunks; c++) {
-              uint32_t s[16];
-              scores(c, s);
-              float mine = 0.0f;
+            float2 top[8];
 #pragma unroll
-              for (int k = 0; k < 16; k++) {
-                const float top = warp_max(
-                    fmaf(__uint_as_float(s[k]), factor(16 * c + k), side ? 0.0f : pg.w));
-                if (lane == k) mine = top;
+            for (int b = 0; b < 8; b++) top[b] = make_float2(-INFINITY, -INFINITY);
+#pragma unroll 1
+            for (int h = 0; h < 2; h++) {
+              const float4 pg = pages[h];
+              const float add = side ? 0.0f : pg.w;
+              const float2 w2 = make_float2(add, add);
+#pragma unroll
+              for (int b0 = 0; b0 < 8; b0 += 4) {
+                if (b0 >= 2 * chunks) continue;
+                uint32_t s[16];
+                load32(h, b0, s);
+                wait_loaded(s);
+                if (masked) hide(h, b0, pg, s);
+#pragma unroll
+                for (int b = b0; b < b0 + 4; b++) {
+                  const float2 g2 = factors(pg, b);
+                  const float2 v0 = fma2(as_floats(s + 4 * (b - b0)), g2, w2);
+                  const float2 v1 = fma2(as_floats(s + 4 * (b - b0) + 2), g2, w2);
+                  top[b] = make_float2(max3(top[b].x, v0.x, v1.x), max3(top[b].y, v0.y, v1.y));
+                }
               }
-              if (lane < 16) sm.red[st][warp & 3][16 * c + lane] = mine;
+            }
+#pragma unroll
+            for (int b = 0; b < 8; b++) {
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) {
+                top[b].x = fmaxf(top[b].x, __shfl_xor_sync(0xffffffffu, top[b].x, d));
+                top[b].y = fmaxf(top[b].y, __shfl_xor_sync(0xffffffffu, top[b].y, d));
+              }
+              if (lane < 4)
+                *reinterpret_cast<float2*>(&sm.red[st][warp & 3][8 * b + col]) = top[b];
             }
             named_sync(2 + st, 128);
             if (t < 16 * chunks) {
@@ -578,154 +663,136 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!side) sm.c[st][t] = kHeadroom - now;
             }
             named_sync(2 + st, 128);
-            if (side || !general) {  // the sums
 #pragma unroll
-              for (int k = 0; k < kStreamRows; k += 4) {
-                if (k >= 16 * chunks) continue;
-                const float4 by = *reinterpret_cast<const float4*>(&sm.by[st][k]);
-                l[k] *= by.x;
-                l[k + 1] *= by.y;
-                l[k + 2] *= by.z;
-                l[k + 3] *= by.w;
+            for (int b = 0; b < 8; b++) {
+              if (b >= 2 * chunks) continue;
+              if (side || !general) {  // the sums
+                const float2 by = *reinterpret_cast<const float2*>(&sm.by[st][8 * b + col]);
+                l[b].x *= by.x;
+                l[b].y *= by.y;
               }
-              for (int r = lane; r < 16 * chunks; r += 32) extra[r] *= sm.by[st][r];
+              if (!side) c[b] = *reinterpret_cast<const float2*>(&sm.c[st][8 * b + col]);
             }
             if (!side && any_o) {  // the results
 #pragma unroll 1
-              for (int c = 0; c < chunks; c++) {
+              for (int k0 = 0; k0 < chunks; k0++) {
                 uint32_t o[16];
-                tc::load16(o_col + c * 16, o);
+                tc::load16(o_col + k0 * 16, o);
                 tc::wait_ld();
 #pragma unroll
                 for (int k = 0; k < 16; k++)
-                  o[k] = __float_as_uint(__uint_as_float(o[k]) * sm.by[st][16 * c + k]);
-                tc::store16(o_col + c * 16, o);
+                  o[k] = __float_as_uint(__uint_as_float(o[k]) * sm.by[st][16 * k0 + k]);
+                tc::store16(o_col + k0 * 16, o);
               }
               tc::wait_st();
             }
             if (side) named_sync(2 + st, 128);  // `by` is read
           }
         };
-        unsigned char* const row = sm.p[st] + t * 128;
-        auto put = [&](int c, const uint32_t (&w)[8]) {
-#pragma unroll
-          for (int k = 0; k < 2; k++)
-            *reinterpret_cast<uint4*>(row + (((2 * c + k) ^ (t & 7)) << 4)) =
-                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        // P of a half's rows [8 b, 8 b + 16): eight tokens and eight rows a matrix
+        auto put = [&](int h, int b, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+          const int r = lane & 7, token = 32 * (warp & 3) + 16 * h + (lane & 8) + r;
+          store_matrices(smem_addr(sm.p[st]) + token * 128 + (((b + (lane >> 4)) ^ r) << 4), w0, w1,
+                         w2, w3);
         };
         if (!general && (flags & kFarScale)) {
           general = true;
           if (t < kStreamRows) sm.mx[st][t] = fmaxf(sm.m[st][t] - kHeadroom, kLow);
           unknown = true;
         }
-        if (!general && !masked) {
-          // ---- P and the sums in one pass, under the maxima as they are. Where that goes over the
-          // lag (rare), the pass is taken back, the sums by the same terms again (what is lost, 2^-24
-          // of those terms, is little beside the terms under the new maxima), and made anew.
-          if (unknown) adjust();
-          unknown = false;
+        const bool slow = general || masked;
+        bool again = unknown || slow;
+        unknown = slow;  // (hidden tokens: rows may still have no maximum)
+        for (;;) {
+          if (again) adjust();
+          // the products of the stream's step before have read their P
           if (used > 0) wait(sm, &sm.pv_done[st], (used - 1) & 1, p.err);
-          const float g = fmaxf(f * pg.z, kTiny);
-          const float2 g2 = make_float2(g, g), w2 = make_float2(pg.w, pg.w);
-          float sign = 1.0f;
-          for (;;) {
-            const float2 inv2 = make_float2(sign * pg.y, sign * pg.y);
-            float top = -INFINITY;
+          if (slow) {
+            // ---- hidden tokens, or the second form: every row under its own factor
+#pragma unroll 1
+            for (int h = 0; h < 2; h++) {
+              const float4 pg = pages[h];
+              const float2 w2 = make_float2(pg.w, pg.w), none = make_float2(0.0f, 0.0f);
+              const float2 inv2 = make_float2(pg.y, pg.y);
+              uint32_t s[16];
 #pragma unroll
-            for (int c = 0; c < 4; c++) {
-              if (c >= chunks) continue;
-              uint32_t s[16], w[8];
-              float y[16], of = -INFINITY;
-              tc::load16(s_col + c * 16, s);
-              tc::wait_ld();
-#pragma unroll
-              for (int k = 0; k < 16; k += 4) {
-                const float4 add = *reinterpret_cast<const float4*>(&sm.c[st][16 * c + k]);
-                const float2 a = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
-                                      g2, add2(make_float2(add.x, add.y), w2));
-                const float2 b =
-                    fma2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), g2,
-                         add2(make_float2(add.z, add.w), w2));
-                of = max3(of, a.x, a.y);
-                of = max3(of, b.x, b.y);
-                y[k] = ex2(a.x);
-                y[k + 1] = ex2(a.y);
-                y[k + 2] = ex2(b.x);
-                y[k + 3] = ex2(b.y);
-                w[k / 2] = half_pair(y[k], y[k + 1]);
-                w[k / 2 + 1] = half_pair(y[k + 2], y[k + 3]);
-              }
-              top = fmaxf(top, of);
-              if (of < 100.0f) {  // (the same both ways: an infinity could not be taken back)
-#pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                  float* const sum = l + 16 * c + k;
-                  const float2 v =
-                      fma2(make_float2(y[k], y[k + 1]), inv2, make_float2(sum[0], sum[1]));
-                  sum[0] = v.x;
-                  sum[1] = v.y;
+              for (int b = 0; b < 8; b += 2) {
+                if (b >= 2 * chunks) continue;
+                if (b % 4 == 0) {
+                  load32(h, b, s);
+                  wait_loaded(s);
+                  if (masked) hide(h, b, pg, s);
                 }
-              }
-              put(c, w);
-            }
-            if (sign < 0.0f) {
-              adjust();
-              sign = 1.0f;
-            } else if (any_of(2 + st, top > kHeadroom + kLag)) {
-              sign = -1.0f;
-            } else {
-              break;
-            }
-          }
-        } else {
-          // ---- hidden tokens, or the second form: looked at first, 16 rows at a time, each under
-          // its own factor; a step's sums over a warp's tokens go to shared memory
-          bool over = unknown;
-#pragma unroll 1
-          for (int c = 0; c < chunks; c++) {
-            uint32_t s[16];
-            scores(c, s);
+                uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 16; k++) {
-              const int r = 16 * c + k;
-              const float x = __uint_as_float(s[k]) * factor(r);
-              over = over || x + (sm.c[st][r] + pg.w) > kHeadroom + kLag ||
-                     (general && x - sm.mx[st][r] > kSumLag);
-            }
-          }
-          if (any_of(2 + st, over)) adjust();
-          unknown = true;  // (rows that saw nothing have no maximum yet)
-          if (used > 0) wait(sm, &sm.pv_done[st], (used - 1) & 1, p.err);
-#pragma unroll 1
-          for (int c = 0; c < chunks; c++) {
-            uint32_t s[16], w[8];
-            scores(c, s);
-            float z[16];
-#pragma unroll
-            for (int k = 0; k < 16; k++) {
-              const int r = 16 * c + k;
-              const float x = __uint_as_float(s[k]) * factor(r);
-              const float y = ex2(x + (sm.c[st][r] + pg.w));
-              z[k] = general ? ex2(x - sm.mx[st][r]) : y * pg.y;
-              s[k] = __float_as_uint(y);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; k++)
-              w[k] = half_pair(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
-            put(c, w);
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1) {
-              const bool upper = lane & d;
-#pragma unroll
-              for (int k = 0; k < d; k++) {
-                const float send = upper ? z[k] : z[k + d], stay = upper ? z[k + d] : z[k];
-                z[k] = stay + __shfl_xor_sync(0xffffffffu, send, d);
+                for (int k = 0; k < 2; k++) {
+                  const float2 g2 = factors(pg, b + k), add = add2(c[b + k], w2);
+                  const uint32_t* v = &s[4 * (b % 4 + k)];
+                  float2 x0 = fma2(as_floats(v), g2, none), x1 = fma2(as_floats(v + 2), g2, none);
+                  float2 y0 = add2(x0, add), y1 = add2(x1, add);
+                  y0 = make_float2(ex2(y0.x), ex2(y0.y));
+                  y1 = make_float2(ex2(y1.x), ex2(y1.y));
+                  w[2 * k] = half_pair(y0.x, y0.y);
+                  w[2 * k + 1] = half_pair(y1.x, y1.y);
+                  if (general) {
+                    const float2 mx =
+                        *reinterpret_cast<const float2*>(&sm.mx[st][8 * (b + k) + col]);
+                    x0 = make_float2(ex2(x0.x - mx.x), ex2(x0.y - mx.y));
+                    x1 = make_float2(ex2(x1.x - mx.x), ex2(x1.y - mx.y));
+                    l[b + k] = add2(l[b + k], add2(x0, x1));
+                  } else {
+                    l[b + k] = fma2(y1, inv2, fma2(y0, inv2, l[b + k]));
+                  }
+                }
+                put(h, b, w[0], w[1], w[2], w[3]);
               }
             }
-            z[0] += __shfl_xor_sync(0xffffffffu, z[0], 16);
-            if (lane < 16) extra[16 * c + lane] += z[0];
-            __syncwarp();
+            break;
           }
+          // ---- P and the sums under the maxima as they are; taken back where a score has gone over
+          // the lag (rare)
+          float2 was[8];
+#pragma unroll
+          for (int b = 0; b < 8; b++) was[b] = l[b];
+          float top = -INFINITY;
+          uint32_t s[2][16];  // 32 rows of a half; the next ones are on their way meanwhile
+          load32(0, 0, s[0]);
+#pragma unroll
+          for (int u = 0; u < 4; u++) {
+            const int h = u & 1, b0 = 4 * (u >> 1);
+            if (b0 >= 2 * chunks) continue;
+            wait_loaded(s[h]);
+            if (u == 0) load32(1, 0, s[1]);
+            if (u == 1 && chunks > 2) load32(0, 4, s[0]);
+            if (u == 2) load32(1, 4, s[1]);
+            const float4 pg = pages[h];
+            const float g = fmaxf(f * pg.z, kTiny);
+            const float2 g2 = make_float2(g, g), w2 = make_float2(pg.w, pg.w);
+            const float2 inv2 = make_float2(pg.y, pg.y);
+#pragma unroll
+            for (int b = b0; b < b0 + 4; b += 2) {
+              if (b >= 2 * chunks) continue;
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 2; k++) {
+                const uint32_t* v = &s[h][4 * (b + k - b0)];
+                const float2 add = add2(c[b + k], w2);
+                float2 y0 = fma2(as_floats(v), g2, add), y1 = fma2(as_floats(v + 2), g2, add);
+                top = max3(top, y0.x, y0.y);
+                top = max3(top, y1.x, y1.y);
+                y0 = make_float2(ex2(y0.x), ex2(y0.y));
+                y1 = make_float2(ex2(y1.x), ex2(y1.y));
+                w[2 * k] = half_pair(y0.x, y0.y);
+                w[2 * k + 1] = half_pair(y1.x, y1.y);
+                l[b + k] = fma2(y1, inv2, fma2(y0, inv2, l[b + k]));
+              }
+              put(h, b, w[0], w[1], w[2], w[3]);
+            }
+          }
+          again = any_of(2 + st, top > kHeadroom + kLag);
+          if (!again) break;
+#pragma unroll
+          for (int b = 0; b < 8; b++) l[b] = was[b];
         }
         tc::fence_before();
         mbar_arrive(&sm.s_empty[st][buf]);
@@ -737,22 +804,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (any) wait(sm, &sm.pv_done[st], (used - 1) & 1, p.err);
       tc::fence_after();
 
-      // ---- the sums over the stream's tokens: halves of the rows change lanes
+      // ---- the sums over the stream's tokens
 #pragma unroll
-      for (int d = 16, n = 32; d > 0; d >>= 1, n >>= 1) {
-        const bool upper = lane & d;
+      for (int b = 0; b < 8; b++) {
 #pragma unroll
-        for (int k = 0; k < n; k++) {
-          const float send = upper ? l[k] : l[k + n], stay = upper ? l[k + n] : l[k];
-          l[k] = stay + __shfl_xor_sync(0xffffffffu, send, d);
+        for (int d = 4; d < 32; d <<= 1) {
+          l[b].x += __shfl_xor_sync(0xffffffffu, l[b].x, d);
+          l[b].y += __shfl_xor_sync(0xffffffffu, l[b].y, d);
         }
-      }
-      {  // this lane's two rows: bit 4 of the lane chose 32, bit 3 16, ..
-        const int r = ((lane & 16) << 1) | ((lane & 8) << 1) | ((lane & 4) << 1) |
-                      ((lane & 2) << 1) | ((lane & 1) << 1);
-        const float2 more = *reinterpret_cast<const float2*>(extra + r);
-        *reinterpret_cast<float2*>(&sm.red[st][warp & 3][r]) =
-            make_float2(l[0] + more.x, l[1] + more.y);
+        if (lane < 4) *reinterpret_cast<float2*>(&sm.red[st][warp & 3][8 * b + col]) = l[b];
       }
       if (t < kStreamRows) {
         // The second form's frames brought together, within 2^50 of the sum's own: O (the result
@@ -874,21 +934,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ============================================ K's codes: one token a thread, into TMEM
     const int t = tid & 127;
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21) + kColK;
-    int step = 0, stage = 0;
-    uint32_t parity = 0;
+    int step = 0;
     bool ok = true;
     while (ok && walk.next(pc)) {
       for (int j = 0; ok && j < pc.tiles; j++, step++) {
-        ok = wait(sm, &sm.k_raw_full[stage], parity, p.err);
+        const int stage = step % kStages;
+        ok = wait(sm, &sm.k_raw_full[stage], step / kStages & 1, p.err);
         if (!ok) break;
         const uint32_t raw = smem_addr(sm.k_raw[stage]) + t * 128;
+        uint4 v[8];
+#pragma unroll
+        for (int c = 0; c < 8; c++) v[c] = lds128(raw + ((c ^ (t & 7)) << 4));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.k_raw_empty[stage]);
 #pragma unroll
         for (int h = 0; h < 2; h++) {
           uint32_t w[32];
 #pragma unroll
           for (int c = 0; c < 4; c++) {
-            const uint4 v = lds128(raw + (((4 * h + c) ^ (t & 7)) << 4));
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t u[4] = {v[4 * h + c].x, v[4 * h + c].y, v[4 * h + c].z, v[4 * h + c].w};
 #pragma unroll
             for (int k = 0; k < 4; k++) {
               const uint32_t x = Codes<F>::prepare(u[k]);
@@ -897,69 +961,71 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (h == 0) {
-            ok = wait(sm, &sm.k_empty[step & 1], ((step >> 1) & 1) ^ 1, p.err);
+            ok = wait(sm, &sm.k_empty, (step & 1) ^ 1, p.err);
             tc::fence_after();
           }
-          tc::store32(at + kStreamRows * (step & 1) + 32 * h, w);
+          tc::store32(at + 32 * h, w);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.k_raw_empty[stage]);
         tc::wait_st();
         tc::fence_before();
-        mbar_arrive(&sm.k_full[step & 1]);
-        stage = stage == kKStages - 1 ? 0 : stage + 1;
-        parity ^= stage == 0;
+        mbar_arrive(&sm.k_full);
       }
     }
   } else if (warp < kMmaWarp) {
     tc::fewer_registers<kConvertRegs>();
-    // ============================================ V's codes: into a swizzled tile
-    const int w0 = (warp - kVWarp) * 32, sub = lane >> 3, c = lane & 7;
+    // ============================================ V's codes: turned, 32 channels a warp, into TMEM
+    const int w = warp - kVWarp;
+    const uint32_t at = tmem + ((uint32_t)w << 21) + kColV;
     int step = 0;
     bool ok = true;
     while (ok && walk.next(pc)) {
       for (int j = 0; ok && j < pc.tiles; j++, step++) {
-        const int stage = step & 1, parity = (step >> 1) & 1;
-        ok = wait(sm, &sm.v_raw_full[stage], parity, p.err);
+        const int stage = step % kStages;
+        ok = wait(sm, &sm.v_raw_full[stage], step / kStages & 1, p.err);
         if (!ok) break;
-        const int2 valid = *reinterpret_cast<const int2*>(&sm.v_valid[stage][w0 / kPage]);
-        uint4 v[8];
+        const uint32_t raw = smem_addr(sm.v_raw[stage]);
+        uint32_t u[2][16];  // [16 channels][2 x 16 tokens: 4 words]
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          const int t = w0 + 4 * i + sub;
-          v[i] = lds128(smem_addr(sm.v_raw[stage]) + t * 128 + ((c ^ (t & 7)) << 4));
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int t = 32 * i + lane;
+            load_turned(raw + t * 128 + (((2 * w + h) ^ (t & 7)) << 4), &u[h][4 * i]);
+          }
+        const int valid = sm.v_valid[stage][lane & 7];
+        if (__any_sync(0xffffffffu, valid < kPage)) {
           // bytes no token wrote may be NaN, and a weight of 0 does not hide one
-          if ((t & 15) >= (i < 4 ? valid.x : valid.y)) v[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int b = 0; b < kTilePages; b++) {
+            const int left = __shfl_sync(0xffffffffu, valid, b) - 4 * (lane & 3);
+            const uint32_t mask = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << 8 * left) - 1;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              u[h][2 * b] &= mask;
+              u[h][2 * b + 1] &= mask;
+            }
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.v_raw_empty[stage]);
-        ok = wait(sm, &sm.v_empty[stage], parity ^ 1, p.err);
-        if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          const int t = w0 + 4 * i + sub;
-          const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-          uint32_t w[8];
+        for (int h = 0; h < 2; h++) {
+          uint32_t r[32];
 #pragma unroll
-          for (int k = 0; k < 4; k++) {
-            const uint32_t x = Codes<F>::prepare(u[k]);
-            w[2 * k] = Codes<F>::template pair<0>(x);
-            w[2 * k + 1] = Codes<F>::template pair<1>(x);
+          for (int i = 0; i < 16; i++) {
+            const uint32_t x = Codes<F>::prepare(u[h][i]);
+            r[2 * i] = Codes<F>::template pair<0>(x);
+            r[2 * i + 1] = Codes<F>::template pair<1>(x);
           }
-          unsigned char* dst = sm.v[stage] + (c >> 2) * kHalfBytes + t * 128;
-          // the lanes of the other half of the channels store their second chunk first: the two
-          // halves' chunks then lie in different banks
-          const int swap = c >> 2;
-#pragma unroll
-          for (int k = 0; k < 2; k++) {
-            const int which = k ^ swap;
-            *reinterpret_cast<uint4*>(dst + ((((2 * c + which) & 7) ^ (t & 7)) << 4)) =
-                which ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(w[0], w[1], w[2], w[3]);
+          if (h == 0) {
+            ok = wait(sm, &sm.v_empty, (step & 1) ^ 1, p.err);
+            tc::fence_after();
           }
+          store_16x64(at + ((uint32_t)(16 * h) << 16), r);
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.v_full[stage]);
+        tc::wait_st();
+        tc::fence_before();
+        mbar_arrive(&sm.v_full);
       }
     }
   } else {
@@ -968,7 +1034,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     // ============================================ the products
     const uint32_t q_low = tc::desc_low(smem_addr(sm.q), 16);
-    const uint32_t v_low = tc::desc_low(smem_addr(sm.v[0]), kHalfBytes);
     const uint32_t p_low = tc::desc_low(smem_addr(sm.p[0]), kPBytes);
     const bool lead = tc::elect();
     int step = 0;
@@ -983,29 +1048,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int behind = two ? 1 : 2;
       ok = wait(sm, &sm.q_full, q_phase, p.err);
       q_phase ^= 1;
-      // S of stream i (0: of both) in buffer `buf` from the K tile of step `at`
-      auto scores = [&](auto instr, uint32_t d, int at) {
-        const uint32_t a = tmem + kColK + kStreamRows * (at & 1);
+      auto scores = [&](auto instr, uint32_t d) {  // from the queries of stream 0, or of both
         if (lead) {
 #pragma unroll
           for (int c = 0; c < 8; c++)
             tc::mma_ts<decltype(instr)::value>(
-                d, a + c * 8, q_low + (((c >> 2) * kHalfBytes + (c & 3) * 32) >> 4), c > 0);
+                d, tmem + kColK + c * 8, q_low + (((c >> 2) * kHalfBytes + (c & 3) * 32) >> 4),
+                c > 0);
         }
       };
-      auto values = [&](auto instr, uint32_t d, uint32_t pp, int at, bool add) {
-        const uint32_t v = v_low + (at & 1) * (kTileBytes >> 4);
+      auto values = [&](auto instr, uint32_t d, uint32_t pp, bool add) {
         if (lead) {
 #pragma unroll
           for (int c = 0; c < 8; c++)
-            tc::mma_ss<decltype(instr)::value>(d, v + c * (2048 >> 4), pp + c * (2048 >> 4),
+            tc::mma_ts<decltype(instr)::value>(d, tmem + kColV + c * 8, pp + c * (2048 >> 4),
                                                add || c > 0);
         }
       };
       for (int j = 0; ok && j < pc.tiles + behind; j++) {
         if (j < pc.tiles) {
           const int at = step + j;
-          ok = wait(sm, &sm.k_full[at & 1], (at >> 1) & 1, p.err);
+          ok = wait(sm, &sm.k_full, at & 1, p.err);
           const int buf = (two ? j : j >> 1) & 1;
 #pragma unroll
           for (int i = 0; i < 2; i++)
@@ -1017,21 +1080,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::fence_after();
           const uint32_t d = tmem + kColS + 2 * kStreamRows * buf;
           if (two)
-            scores(std::integral_constant<uint32_t, tc::instr_f16(128, 2 * kStreamRows, false)>{}, d,
-                   at);
+            scores(std::integral_constant<uint32_t, tc::instr_f16(128, 2 * kStreamRows, false)>{},
+                   d);
           else
             scores(std::integral_constant<uint32_t, tc::instr_f16(128, kStreamRows, false)>{},
-                   d + kStreamRows * (j & 1), at);
+                   d + kStreamRows * (j & 1));
 #pragma unroll
           for (int i = 0; i < 2; i++)
             if ((two || (j & 1) == i) && lead) tc::commit(&sm.s_full[i][buf]);
-          if (lead) tc::commit(&sm.k_empty[at & 1]);
+          if (lead) tc::commit(&sm.k_empty);
           __syncwarp();
         }
         const int jj = j - behind;
         if (jj >= 0) {
           const int at = step + jj;
-          ok = wait(sm, &sm.v_full[at & 1], (at >> 1) & 1, p.err);
+          ok = wait(sm, &sm.v_full, at & 1, p.err);
 #pragma unroll
           for (int i = 0; i < 2; i++)
             if (ok && (two || (jj & 1) == i)) ok = wait(sm, &sm.p_full[i], done[i] & 1, p.err);
@@ -1039,11 +1102,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::fence_after();
           if (two)
             values(
-                std::integral_constant<uint32_t, tc::instr_f16(128, 2 * kStreamRows, true, true)>{},
-                tmem + kColO, p_low, at, jj > 0);
+                std::integral_constant<uint32_t, tc::instr_f16(128, 2 * kStreamRows, true)>{},
+                tmem + kColO, p_low, jj > 0);
           else
-            values(std::integral_constant<uint32_t, tc::instr_f16(128, kStreamRows, true, true)>{},
-                   tmem + kColO + kStreamRows * (jj & 1), p_low + (jj & 1) * (kPBytes >> 4), at,
+            values(std::integral_constant<uint32_t, tc::instr_f16(128, kStreamRows, true)>{},
+                   tmem + kColO + kStreamRows * (jj & 1), p_low + (jj & 1) * (kPBytes >> 4),
                    jj > 1);
 #pragma unroll
           for (int i = 0; i < 2; i++)
@@ -1051,7 +1114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (lead) tc::commit(&sm.pv_done[i]);
               done[i]++;
             }
-          if (lead) tc::commit(&sm.v_empty[at & 1]);
+          if (lead) tc::commit(&sm.v_empty);
           __syncwarp();
         }
       }
@@ -1059,8 +1122,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // the last arrivals on the barriers come before the CTA ends
     if (ok && step > 0) {
-      wait(sm, &sm.k_empty[(step - 1) & 1], ((step - 1) >> 1) & 1, p.err);
-      wait(sm, &sm.v_empty[(step - 1) & 1], ((step - 1) >> 1) & 1, p.err);
+      wait(sm, &sm.k_empty, (step - 1) & 1, p.err);
+      wait(sm, &sm.v_empty, (step - 1) & 1, p.err);
     }
     // nor may products go on in shared and tensor memory that are given up
     if (!ok) {
@@ -1070,7 +1133,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kKLoad || warp == kVLoad) {
     // ============================================ the copies: 4 tiles' blocks a batch, one a lane
     const bool is_k = warp == kKLoad;
-    const int stages = is_k ? kKStages : kVStages;
     uint64_t* const full = is_k ? sm.k_raw_full : sm.v_raw_full;
     uint64_t* const empty = is_k ? sm.k_raw_empty : sm.v_raw_empty;
     unsigned char* const raw = is_k ? sm.k_raw[0] : sm.v_raw[0];
@@ -1116,12 +1178,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       return a;
     };
     Ahead cur = fetch(), next = fetch();
-    int step = 0, stage = 0;
-    uint32_t parity = 0;  // of `full` in this round through the stages
+    int step = 0;
     bool ok = true;
     while (ok && cur.count > 0) {
       for (int j = 0; j < cur.count; j++, step++) {
-        ok = wait(sm, &empty[stage], parity ^ 1, p.err);
+        const int stage = step % kStages;
+        ok = wait(sm, &empty[stage], (step / kStages & 1) ^ 1, p.err);
         if (!ok) break;
         const bool mine = lane >> 3 == j;
         const int blocks = __popc(__ballot_sync(0xffffffffu, mine && cur.valid > 0));
@@ -1147,20 +1209,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (cur.again) tma_load_2d(dst, map, 0, cur.y, &full[stage]);
           else tma_load_2d_hint(dst, map, 0, cur.y, &full[stage], policy);
         }
-        stage = stage == stages - 1 ? 0 : stage + 1;
-        parity ^= stage == 0;
       }
       cur = next;
       next = fetch();
     }
     // copies under way write this CTA's shared memory: one more wait for each
-    if (!ok) {
-      for (int i = 0; i < min(step, stages); i++) {
-        stage = stage == 0 ? stages - 1 : stage - 1;
-        parity ^= stage == stages - 1;
-        mbar_wait(&full[stage], parity);
-      }
-    }
+    if (!ok)
+      for (int i = max(step - kStages, 0); i < step; i++)
+        mbar_wait(&full[i % kStages], i / kStages & 1);
   }
   tc::fence_before();
   __syncthreads();
