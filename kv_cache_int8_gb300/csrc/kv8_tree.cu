@@ -57,9 +57,8 @@ constexpr int kRawBytes = kTokens * kHeadDim;         // codes of a step, of K o
 constexpr int kPBytes = kTokens * kStreamRows * 2;
 constexpr int kStages = 4;                            // steps of raw codes, of K and of V
 constexpr int kPageRing = 16;                         // steps whose scales are kept (see Smem)
-constexpr int kWords = kKv8TreeNodes / 32;
-constexpr int kSeqs = 512;                            // sequences of a launch
-constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 16, kKLoad = 17, kVLoad = 18;
+constexpr int kPieces = 4;                            // pieces told ahead
+constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 16, kKLoad = 17, kVLoad = 18, kPlanWarp = 19;
 constexpr int kThreads = 640;
 // registers a thread: softmax warpgroups, converting ones, the last; 96 on average
 constexpr int kSoftmaxRegs = 152, kConvertRegs = 64, kOtherRegs = 48;
@@ -101,36 +100,52 @@ struct Params {
   float scale_log2;
 };
 
+// A stretch of one row block's tiles: what a CTA does at a time.
+struct alignas(16) Piece {
+  int tiles;         // 0: no more
+  int tile;          // the first
+  int rows;          // nodes x group
+  int b, h;          // sequence, kv head
+  int n_all, start;  // its tokens, those in front of the tree
+  int node;          // the first node
+  int row0;          // q's row of node 0
+  int flags;         // kWhole ..
+  int slot;          // of the parts
+  int parts;         // kRecord: how many
+};
+// the whole row block; a piece of the same stretch in front, behind; the first part, to be
+// recorded; other row blocks read the same tokens
+constexpr int kWhole = 1, kAfter = 2, kBefore = 4, kRecord = 8, kShared = 16;
+
 struct Smem {
   alignas(1024) unsigned char q[kTileBytes];
   unsigned char p[2][kPBytes];  // of a stream; between row blocks its scratch
   unsigned char k_raw[kStages][kRawBytes];
   unsigned char v_raw[kStages][kRawBytes];
   // Of a step's blocks: y = 1 / s_v (any number above 0 for zeros, 0 where there are no tokens);
-  // z = s_k; w = log2 s_v (-inf for both). The
-  // copies of a step begin when the codes four steps back are read, so when the scores six back
-  // are complete; their buffer was read by its stream's softmax two of its own steps before, at
-  // most ten back, and the other stream's eleven back.
+  // z = s_k; w = log2 s_v (-inf for both). The copies of a step begin when the codes four steps
+  // back are read, so when the scores six back are complete; their buffer was read by its
+  // stream's softmax two of its own steps before, at most ten back, and the other stream's eleven
+  // back.
   float4 page[kPageRing][kTilePages];
-  uint32_t branch[kRows][kWords];  // of each row: its node and the node's ancestors
+  int flags[kPageRing];            // of a step: kHidden, kFarScale
+  uint32_t seen[kKv8TreeNodes][kRows / 32];  // of each node: the rows that see it
   float c[2][kStreamRows];         // kHeadroom - m
   float m[2][kStreamRows];         // the rows' maxima
   float mx[2][kStreamRows];        // those under which the second form's sums are kept
   float by[2][kStreamRows];
   float f[kRows];                  // row factors (NaN where the query is not finite)
   float red[2][4][kStreamRows];    // of a stream's warps: maxima, then sums
-  int flags[kPageRing];            // of a step: kHidden, kFarScale
   alignas(8) int v_valid[kStages][kTilePages];
+  Piece piece[kPieces];
   alignas(8) uint64_t q_full, k_raw_full[kStages], k_raw_empty[kStages], v_raw_full[kStages],
       v_raw_empty[kStages], k_full, k_empty, v_full, v_empty, s_full[2][2], s_empty[2][2], p_full[2],
-      pv_done[2], all_done;
-  long long per;
-  int start_b, start_h, start_q, start_off;
+      pv_done[2], piece_full[kPieces], piece_empty[kPieces], all_done;
   uint32_t tmem;
-  int shift_max[8], shift_min[8];
+  int exponent_max, exponent_min;
   int dead;
 };
-// behind it: pre (long long [batch + 1]), then len, n, row0 (int [batch] each)
+// behind it: len, n, row0 (int [batch] each)
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -172,14 +187,14 @@ __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// a barrier of the stream's 128 threads that tells whether any of them says so
-__device__ __forceinline__ bool any_of(int id, bool x) {
+// a barrier that tells whether any of its threads says so
+__device__ __forceinline__ bool any_of(int id, int threads, bool x) {
   uint32_t y;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.or.pred q, %1, 128, p;\n\t"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(y)
-      : "r"(id), "r"((uint32_t)x)
+      : "r"(id), "r"(threads), "r"((uint32_t)x)
       : "memory");
   return y != 0;
 }
@@ -224,6 +239,14 @@ __device__ __forceinline__ void load_turned(uint32_t addr, uint32_t* r) {
                : "memory");
 }
 
+// 32 lanes x 8 columns, one lane's a lane; tc::wait_ld() before use.
+__device__ __forceinline__ void load8(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(addr));
+}
+
 // 16 lanes x 64 columns of tensor memory: lane l has columns 8 i + 2 (l % 4) + {0, 1} of rows l / 4
 // (r[4 i], r[4 i + 1]) and l / 4 + 8 (r[4 i + 2], r[4 i + 3]).
 __device__ __forceinline__ void store_16x64(uint32_t addr, const uint32_t (&r)[32]) {
@@ -239,91 +262,33 @@ __device__ __forceinline__ void store_16x64(uint32_t addr, const uint32_t (&r)[3
       : "memory");
 }
 
-// Waits with a limit, a whole warp alike; once a wait has run out every wait of the CTA gives up.
-__device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity, int* err) {
+// Waits with a limit (4 to 8 billion cycles); once a wait has run out every wait of the CTA gives
+// up (false). What goes on then works on whatever is there, in bounds: a piece is always gone
+// through to its end, as its barriers must find all threads.
+__device__ __forceinline__ uint32_t clock_hi() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%clock_hi;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity) {
   bool ok = mbar_try_wait(bar, parity);
   if (!ok) {
-    const long long t0 = clock64();
+    const uint32_t t0 = clock_hi();
     while (!(ok = mbar_try_wait(bar, parity))) {
       if (*reinterpret_cast<volatile int*>(&sm.dead)) break;
-      if (clock64() - t0 > kWaitLimitCycles) {
-        *reinterpret_cast<volatile int*>(&sm.dead) = 1;
-        set_error(err, kDevErrTimeout);
-        break;
-      }
+      if (clock_hi() - t0 > 1) *reinterpret_cast<volatile int*>(&sm.dead) = 1;
     }
   }
-  return __all_sync(0xffffffffu, ok);
+  __syncwarp();
+  return ok;
 }
 
-// Row blocks of a sequence of n nodes, as equal as they come, and the nodes of each.
-__device__ __forceinline__ int row_blocks(int n, int most) { return (n + most - 1) / most; }
+// Row blocks of a sequence of n nodes, as equal as they come: the nodes of each.
+__device__ __forceinline__ int nodes_a_block(int n, int most) {
+  const int blocks = (n + most - 1) / most;
+  return (n + blocks - 1) / blocks;
+}
 __device__ __forceinline__ int token_tiles(int len) { return (len + kTokens - 1) / kTokens; }
-
-// A stretch of one row block's tiles: what a CTA does at a time.
-struct Piece {
-  int b, h;          // sequence, kv head
-  int node, nodes;   // first node, number of nodes
-  int rows;          // nodes x group
-  int tile, tiles;   // first tile, number of tiles
-  int all_tiles;     // of the whole row block
-  long long begin;   // the row block's first place on the line
-};
-
-// The pieces of the slice [x, end) of the line, in order. A row block's places are kBlockCost for
-// what it costs beside its tiles, then one a tile.
-struct Walk {
-  const int* len;
-  const int* n;
-  int batch, hkv, group, block_nodes;
-  long long x, end;
-  int b, h, q, off;  // off: place in the row block
-
-  __device__ __forceinline__ bool next(Piece& p) {
-    for (;;) {
-      if (x >= end) return false;
-      const int blocks = row_blocks(n[b], block_nodes), most = (n[b] + blocks - 1) / blocks;
-      p.b = b;
-      p.h = h;
-      p.node = q * most;
-      p.nodes = min(most, n[b] - p.node);
-      p.rows = p.nodes * group;
-      p.begin = x - off;
-      p.all_tiles = token_tiles(len[b]);
-      int stop = (int)min((long long)(p.all_tiles + kBlockCost), off + (end - x));
-      p.tile = max(off - kBlockCost, 0);
-      p.tiles = max(stop - kBlockCost, 0) - p.tile;
-      const int limit = p.rows > kStreamRows ? kMaxSteps : 2 * kMaxSteps;
-      if (p.tiles > limit) {  // the rest of the stretch is the next piece
-        p.tiles = limit;
-        stop = p.tile + limit + kBlockCost;
-        x += stop - off;
-        off = stop;
-        return true;
-      }
-      x += stop - off;
-      off = 0;
-      // (equal blocks may be fewer than row_blocks says: the last ones would be empty)
-      if ((q + 1) * most < n[b]) {
-        q++;
-      } else {
-        q = 0;
-        if (++h == hkv) {
-          h = 0;
-          do b++;
-          while (b < batch && n[b] == 0);
-        }
-      }
-      if (p.tiles > 0) return true;
-    }
-  }
-};
-// row blocks that are not empty
-__device__ __forceinline__ int full_blocks(int n, int most_nodes) {
-  if (n == 0) return 0;
-  const int blocks = row_blocks(n, most_nodes), most = (n + blocks - 1) / blocks;
-  return (n + most - 1) / most;
-}
 
 template <int F>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -333,8 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem& sm = *reinterpret_cast<Smem*>(
       smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
   const int batch = p.rows.batch;
-  long long* pre = reinterpret_cast<long long*>(&sm + 1);
-  int* len = reinterpret_cast<int*>(pre + batch + 1);
+  int* len = reinterpret_cast<int*>(&sm + 1);
   int* num = len + batch;
   int* row0 = num + batch;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -361,6 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.p_full[i], 128);
       mbar_init(&sm.pv_done[i], 1);
     }
+    for (int i = 0; i < kPieces; i++) {
+      mbar_init(&sm.piece_full[i], 1);
+      mbar_init(&sm.piece_empty[i], kPlanWarp);
+    }
     mbar_init(&sm.all_done, 1);
     sm.dead = 0;
     fence_barrier_init();
@@ -369,182 +337,116 @@ __global__ void __launch_bounds__(kThreads, 1)
   // of two kernels holds it on an SM never waits for the other.
   grid_dep_wait();
   if (warp == kMmaWarp) tc::alloc(&sm.tmem, 512);
-  if (tid == 0) p.records[blockIdx.x].rows = 0;
-
-  // ---- the line of all steps; warp 0 finds where this CTA's slice begins
-  if (warp == 0) {
-    long long sum = 0;
-    for (int b0 = 0; b0 < batch; b0 += 32) {
-      const int b = b0 + lane;
-      long long incl = 0;
-      if (b < batch) {
-        NewSpan sp = new_span(p.rows, b);
-        if (sp.n > kKv8TreeNodes) {
-          sp.bad = true;
-          sp.n = 0;
-        }
-        if (sp.bad) set_error(p.err, kDevErrCheck);
-        len[b] = sp.start + sp.n;
-        num[b] = sp.n;
-        row0[b] = sp.row0;
-        incl = (long long)full_blocks(sp.n, p.block_nodes) * p.hkv *
-               (token_tiles(len[b]) + kBlockCost);
-      }
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += v;
-      }
-      if (b < batch) pre[b + 1] = sum + incl;
-      sum += __shfl_sync(0xffffffffu, incl, 31);
+  for (int b = tid; b < batch; b += kThreads) {
+    NewSpan sp = new_span(p.rows, b);
+    if (sp.n > kKv8TreeNodes) {
+      sp.bad = true;
+      sp.n = 0;
     }
-    if (lane == 0) pre[0] = 0;
-    __syncwarp();
-    const long long per = max((sum + gridDim.x - 1) / gridDim.x, (long long)kMinPlaces);
-    const long long begin = min(blockIdx.x * per, sum);
-    if (lane == 0) {
-      sm.per = per;
-      if (begin < sum) {
-        int lo = 0, hi = batch;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (pre[mid] <= begin) lo = mid;
-          else hi = mid;
-        }
-        const int one = token_tiles(len[lo]) + kBlockCost;  // places of a row block
-        const long long at = begin - pre[lo];
-        const int head = one * full_blocks(num[lo], p.block_nodes);
-        sm.start_b = lo;
-        sm.start_h = (int)(at / head);
-        const int rest = (int)(at % head);
-        sm.start_q = rest / one;
-        sm.start_off = rest % one;
-      }
-    }
+    if (sp.bad) set_error(p.err, kDevErrCheck);
+    len[b] = sp.start + sp.n;
+    num[b] = sp.n;
+    row0[b] = sp.row0;
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = sm.tmem;
-  const long long per = sm.per, all = pre[batch];
-  const long long begin = min(blockIdx.x * per, all), end = min(begin + per, all);
-  Walk walk = {len, num, batch, p.hkv, p.group, p.block_nodes, begin, end,
-               sm.start_b, sm.start_h, sm.start_q, sm.start_off};
+  // The pieces, as the plan's warp tells them; every other warp takes each and gives it back.
+  int pieces = 0;
+  auto take = [&](Piece& pc) {
+    const int slot = pieces % kPieces;
+    wait(sm, &sm.piece_full[slot], pieces / kPieces & 1);
+    pc = sm.piece[slot];
+    if (sm.dead) pc.tiles = 0;
+    return __shfl_sync(0xffffffffu, pc.tiles, 0) > 0;
+  };
+  auto give_back = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.piece_empty[pieces % kPieces]);
+    pieces++;
+  };
   Piece pc;
 
   if (warp < kKWarp) {
     tc::more_registers<kSoftmaxRegs>();
-    // ============================================ softmax: one token a thread, 64 rows
+    // ============================================ softmax
     const int st = warp >> 2, t = tid & 127;
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
-    uint32_t used = 0;    // steps of this stream so far
-    uint32_t s_phase = 0; // bit i: of buffer i of its S
-    int step0 = 0;      // steps of the pieces so far
-    // After a wait that ran out everything goes on, on whatever is there: the barriers must find
-    // all threads, every access stays in bounds, and no later wait takes time.
-    // rows of sequences that do not fit: 0 and -inf
-    for (int b = blockIdx.x; b < batch; b += gridDim.x) {
-      if (p.rows.cu == nullptr ? num[b] != 0 : p.rows.cu[b + 1] - p.rows.cu[b] == num[b]) continue;
-      const int first = max(row0[b], 0);
-      const int count = min(p.rows.cu ? p.rows.cu[b + 1] : b + 1, p.rows.total) - first;
-      for (long long i = tid; i < (long long)count * p.hq * (kHeadDim / 8); i += 256)
-        reinterpret_cast<uint4*>(p.out + (size_t)first * p.hq * kHeadDim)[i] =
-            make_uint4(0u, 0u, 0u, 0u);
-      if (p.lse != nullptr)
-        for (long long i = tid; i < (long long)count * p.hq; i += 256)
-          p.lse[(size_t)first * p.hq + i] = -INFINITY;
-    }
-    while (walk.next(pc)) {
+    // A lane's share of a step, as the 16-lane loads give it: of each half h of its warp's 32 tokens
+    // (a block of the cache) tokens tok + 8 i, and rows 8 b + col, + 1 of every b.
+    const int tok = 32 * (warp & 3) + (lane >> 2), col = 2 * (lane & 3);
+    // where it points stmatrix at, of P's rows 0 .. 15: token 32 w + (lane & 8) + lane % 8
+    const uint32_t p_row = smem_addr(sm.p[st]) + (32 * (warp & 3) + (lane & 15)) * 128;
+    const uint32_t p_chunk = ((lane >> 4) ^ (lane & 7)) << 4;
+    uint32_t used = 0;     // steps of this stream so far
+    uint32_t s_phase = 0;  // bit i: of buffer i of its S
+    int step0 = 0;         // steps of the pieces so far
+    for (;;) {
+      const bool more = take(pc);
+      // the row block before is read out of shared and tensor memory; after a wait that ran out all
+      // leave together
+      if (any_of(1, 256, !more)) break;
       const bool two = pc.rows > kStreamRows;
       const int base_row = two ? kStreamRows * st : 0;
       const int rows = min(pc.rows - base_row, kStreamRows);  // of this stream
       const int chunks = (rows + 15) / 16;
-      const int n_all = len[pc.b], start = n_all - num[pc.b];
-      const int q_row = row0[pc.b] + pc.node;
-      named_sync(1, 256);  // the row block before is read out of shared and tensor memory
+      const int q_row = pc.row0 + pc.node;
+      if (tid == 0) {
+        sm.exponent_max = 0;
+        sm.exponent_min = 255;
+      }
+      const bool branches = (pc.tile + pc.tiles) * kTokens > pc.start;
+      if (branches) *reinterpret_cast<uint4*>(sm.seen[tid]) = make_uint4(0u, 0u, 0u, 0u);
+      if (t < kStreamRows) {
+        sm.m[st][t] = kLow;
+        sm.mx[st][t] = kLow;
+        sm.c[st][t] = kHeadroom - kLow;
+      }
+      named_sync(1, 256);
       // ---- the queries in fp16, four threads a row. All rows under one power of two that puts
       // the largest value in [2^13, 2^14), as long as the smallest row's largest is within 2^-15
       // of it (its values down to 2^-22 of their largest are then exact in fp16, and the rest is
       // off by less than 2^-23 of it); else each under its own, and the second form of the step.
-      bool general = false;
-      float f = 0.0f;
-      {
-        const int part = tid & 3;
-        uint4 raw[2][4];
-        int e[2];
-        int e_max = 0, e_min = 255;
+      auto query = [&](int r) {
+        return p.q + (long long)(q_row + r / p.group) * p.q_stride +
+               (pc.h * p.group + r % p.group) * kHeadDim + (tid & 3) * 32;
+      };
+      auto exponent = [&](const uint4 (&v)[4]) {  // of the row's largest value; 0: zeros, 255: none
+        uint32_t mx = 0;
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-          const int r = (tid >> 2) + 64 * i;
-          const bool real = r < pc.rows;
-          const __nv_bfloat16* src = p.q + (long long)(q_row + r / p.group) * p.q_stride +
-                                     (pc.h * p.group + r % p.group) * kHeadDim + part * 32;
-          uint32_t mx = 0;
+        for (int k = 0; k < 4; k++) {
+          mx = __vmaxu2(mx, __vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu));
+          mx = __vmaxu2(mx, __vmaxu2(v[k].z & 0x7FFF7FFFu, v[k].w & 0x7FFF7FFFu));
+        }
+        uint32_t m16 = max(mx & 0xFFFFu, mx >> 16);
+        m16 = max(m16, __shfl_xor_sync(0xffffffffu, m16, 1));
+        m16 = max(m16, __shfl_xor_sync(0xffffffffu, m16, 2));
+        return m16 == 0 ? -1 : (int)(m16 >> 7);
+      };
+      const int passes = two ? 2 : 1;
+#pragma unroll 1
+      for (int i = 0; i < passes; i++) {
+        const int r = (tid >> 2) + 64 * i;
+        uint4 v[4];
 #pragma unroll
-          for (int k = 0; k < 4; k++) {
-            raw[i][k] = real ? *reinterpret_cast<const uint4*>(src + 8 * k)
+        for (int k = 0; k < 4; k++)
+          v[k] = r < pc.rows ? reinterpret_cast<const uint4*>(query(r))[k]
                              : make_uint4(0u, 0u, 0u, 0u);
-            mx = __vmaxu2(mx, __vmaxu2(raw[i][k].x & 0x7FFF7FFFu, raw[i][k].y & 0x7FFF7FFFu));
-            mx = __vmaxu2(mx, __vmaxu2(raw[i][k].z & 0x7FFF7FFFu, raw[i][k].w & 0x7FFF7FFFu));
-          }
-          uint32_t m16 = max(mx & 0xFFFFu, mx >> 16);
-          m16 = max(m16, __shfl_xor_sync(0xffffffffu, m16, 1));
-          m16 = max(m16, __shfl_xor_sync(0xffffffffu, m16, 2));
-          e[i] = m16 >> 7;
-          if (m16 != 0 && e[i] < 255) {
-            e_max = max(e_max, e[i]);
-            e_min = min(e_min, e[i]);
-          } else {
-            e[i] = m16 == 0 ? -1 : 255;
-          }
-        }
-        e_max = __reduce_max_sync(0xffffffffu, e_max);
-        e_min = __reduce_min_sync(0xffffffffu, e_min);
+        const int e = exponent(v);
+        const bool counts = e >= 0 && e < 255;
+        const int e_max = __reduce_max_sync(0xffffffffu, counts ? e : 0);
+        const int e_min = __reduce_min_sync(0xffffffffu, counts ? e : 255);
         if (lane == 0) {
-          sm.shift_max[warp] = e_max;
-          sm.shift_min[warp] = e_min;
+          atomicMax(&sm.exponent_max, e_max);
+          atomicMin(&sm.exponent_min, e_min);
         }
-        named_sync(1, 256);
-#pragma unroll
-        for (int w = 0; w < 8; w++) {
-          e_max = max(e_max, sm.shift_max[w]);
-          e_min = min(e_min, sm.shift_min[w]);
-        }
-        general = e_max - e_min > 15 && e_min < 255;
-        const int common = min(13 + 127 - e_max, 126);
-        f = p.scale_log2 * __uint_as_float((uint32_t)(127 - common) << 23);
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-          const int r = (tid >> 2) + 64 * i;
-          if (i == 1 && !two) continue;
-          const int shift = !general || e[i] < 0 || e[i] == 255 ? common : min(13 + 127 - e[i], 126);
-          const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
-          unsigned char* dst = sm.q + (part >> 1) * kHalfBytes + (r >> 3) * 1024 + (r & 7) * 128;
-#pragma unroll
-          for (int k = 0; k < 4; k++) {
-            const uint4 v = raw[i][k];
-            const int chunk = (part & 1) * 4 + k;
-            *reinterpret_cast<uint4*>(dst + ((chunk ^ (r & 7)) << 4)) =
-                make_uint4(half_pair(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
-                           half_pair(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
-                           half_pair(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
-                           half_pair(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
-          }
-          if (part == 0)
-            sm.f[r] = e[i] == 255
-                          ? NAN
-                          : p.scale_log2 * __uint_as_float((uint32_t)(127 - shift) << 23);
-        }
-        fence_proxy_async();
-        mbar_arrive(&sm.q_full);
       }
-      // ---- which nodes a row sees
-      if (tid < pc.rows && (pc.tile + pc.tiles) * kTokens > start) {
-#pragma unroll
-        for (int k = 0; k < kWords; k++) sm.branch[tid][k] = 0;
-        const int32_t* parents = p.parents ? p.parents + row0[pc.b] : nullptr;
+      // which rows see a node: its own, and those of the nodes below it
+      if (branches && tid < pc.rows) {
+        const int32_t* parents = p.parents ? p.parents + pc.row0 : nullptr;
         for (int i = pc.node + tid / p.group; i >= 0;) {
-          sm.branch[tid][i >> 5] |= 1u << (i & 31);
+          atomicOr(&sm.seen[i][tid >> 5], 1u << (tid & 31));
           const int up = parents ? parents[i] : i - 1;
           if (up < -1 || up >= i) {
             set_error(p.err, kDevErrCheck);
@@ -553,26 +455,48 @@ __global__ void __launch_bounds__(kThreads, 1)
           i = up;
         }
       }
-      if (t < kStreamRows) {
-        sm.m[st][t] = kLow;
-        sm.mx[st][t] = kLow;
-        sm.c[st][t] = kHeadroom - kLow;
+      named_sync(1, 256);
+      const int e_max = sm.exponent_max, e_min = sm.exponent_min;
+      bool general = e_max - e_min > 15;
+      const int common = min(13 + 127 - e_max, 126);
+      const float f = p.scale_log2 * __uint_as_float((uint32_t)(127 - common) << 23);
+#pragma unroll 1
+      for (int i = 0; i < passes; i++) {
+        const int r = (tid >> 2) + 64 * i, part = tid & 3;
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+          v[k] = r < pc.rows ? reinterpret_cast<const uint4*>(query(r))[k]
+                             : make_uint4(0u, 0u, 0u, 0u);
+        const int e = exponent(v);
+        const int shift = general && e >= 0 && e < 255 ? min(13 + 127 - e, 126) : common;
+        const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+        unsigned char* dst = sm.q + (part >> 1) * kHalfBytes + r * 128;
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+          *reinterpret_cast<uint4*>(dst + ((((part & 1) * 4 + k) ^ (r & 7)) << 4)) =
+              make_uint4(half_pair(bf16_lo(v[k].x) * up, bf16_hi(v[k].x) * up),
+                         half_pair(bf16_lo(v[k].y) * up, bf16_hi(v[k].y) * up),
+                         half_pair(bf16_lo(v[k].z) * up, bf16_hi(v[k].z) * up),
+                         half_pair(bf16_lo(v[k].w) * up, bf16_hi(v[k].w) * up));
+        if (part == 0)
+          sm.f[r] =
+              e == 255 ? NAN : p.scale_log2 * __uint_as_float((uint32_t)(127 - shift) << 23);
       }
+      fence_proxy_async();
+      mbar_arrive(&sm.q_full);
       named_sync(1, 256);
 
-      // A lane's share of a step, as the 16-lane loads give it: of each half h of its warp's 32
-      // tokens (a block of the cache) tokens tok + 8 i, and rows 8 b + col, + 1 of every b.
-      const int tok = 32 * (warp & 3) + (lane >> 2), col = 2 * (lane & 3);
-      float2 l[8], c[8];  // the rows' sums over its tokens, and kHeadroom - m
+      float2 l[8], c[8];  // the rows' sums over the lane's tokens, and kHeadroom - m
 #pragma unroll
-      for (int b = 0; b < 8; b++) l[b] = make_float2(0.0f, 0.0f);
+      for (int b = 0; b < 8; b++) l[b] = c[b] = make_float2(0.0f, 0.0f);
       const int first = two ? 0 : st, stride = two ? 1 : 2;
       const uint32_t o_col = at + kColO + kStreamRows * st;
       // The maxima may be far off: before the first step, and behind one that rows saw nothing of.
       bool unknown = true;
       for (int j = first; j < pc.tiles; j += stride, used++) {
         const int buf = (two ? j : j >> 1) & 1;
-        wait(sm, &sm.s_full[st][buf], s_phase >> buf & 1, p.err);
+        wait(sm, &sm.s_full[st][buf], s_phase >> buf & 1);
         s_phase ^= 1u << buf;
         tc::fence_after();
         const int ring = (step0 + j) % kPageRing;
@@ -580,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int flags = sm.flags[ring];
         const uint32_t s_col = at + kColS + kStreamRows * st + 2 * kStreamRows * buf;
         // some of the tokens are hidden from some row
-        const bool masked = (flags & kHidden) != 0 || (pc.tile + j + 1) * kTokens > start;
+        const bool masked = (flags & kHidden) != 0 || (pc.tile + j + 1) * kTokens > pc.start;
         auto load32 = [&](int h, int b, uint32_t (&s)[16]) {  // rows [8 b, 8 b + 32)
 #pragma unroll
           for (int k = 0; k < 2; k++)
@@ -591,18 +515,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto hide = [&](int h, int b0, const float4& pg, uint32_t (&s)[16]) {
 #pragma unroll
           for (int i = 0; i < 2; i++) {
-            const int token = (pc.tile + j) * kTokens + tok + 16 * h + 8 * i, node = token - start;
-            const bool seen = token < n_all && pg.y > 0.0f;
-            const uint32_t* bits =
-                &sm.branch[base_row + col + 8 * b0][max(node, 0) >> 5 & (kWords - 1)];
+            const int token = (pc.tile + j) * kTokens + tok + 16 * h + 8 * i;
+            const int node = token - pc.start;
+            uint32_t bits = node < 0 ? ~0u
+                                     : sm.seen[node & (kKv8TreeNodes - 1)][(base_row + 8 * b0) >> 5];
+            if (token >= pc.n_all || !(pg.y > 0.0f)) bits = 0;
+            bits >>= col;
 #pragma unroll
             for (int b = 0; b < 4; b++)
 #pragma unroll
-              for (int k = 0; k < 2; k++) {
-                const bool on =
-                    seen && (node < 0 || (bits[(8 * b + k) * kWords] >> (node & 31) & 1));
-                if (!on) s[4 * b + 2 * i + k] = 0xFF800000u;
-              }
+              for (int k = 0; k < 2; k++)
+                if (!(bits & (1u << (8 * b + k)))) s[4 * b + 2 * i + k] = 0xFF800000u;
           }
         };
         auto factors = [&](const float4& pg, int b) {  // of rows 8 b + col, + 1, in the second form
@@ -613,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto adjust = [&]() {
           const bool any_o = j > first;  // O holds something
           if (any_o) {
-            wait(sm, &sm.pv_done[st], (used - 1) & 1, p.err);
+            wait(sm, &sm.pv_done[st], (used - 1) & 1);
             tc::fence_after();
           }
 #pragma unroll 1
@@ -644,6 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int b = 0; b < 8; b++) {
+              if (b >= 2 * chunks) continue;
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) {
                 top[b].x = fmaxf(top[b].x, __shfl_xor_sync(0xffffffffu, top[b].x, d));
@@ -675,14 +599,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!side && any_o) {  // the results
 #pragma unroll 1
-              for (int k0 = 0; k0 < chunks; k0++) {
+              for (int k0 = 0; k0 < 16 * chunks; k0 += 16) {
                 uint32_t o[16];
-                tc::load16(o_col + k0 * 16, o);
+                tc::load16(o_col + k0, o);
                 tc::wait_ld();
 #pragma unroll
                 for (int k = 0; k < 16; k++)
-                  o[k] = __float_as_uint(__uint_as_float(o[k]) * sm.by[st][16 * k0 + k]);
-                tc::store16(o_col + k0 * 16, o);
+                  o[k] = __float_as_uint(__uint_as_float(o[k]) * sm.by[st][k0 + k]);
+                tc::store16(o_col + k0, o);
               }
               tc::wait_st();
             }
@@ -690,10 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         // P of a half's rows [8 b, 8 b + 16): eight tokens and eight rows a matrix
-        auto put = [&](int h, int b, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
-          const int r = lane & 7, token = 32 * (warp & 3) + 16 * h + (lane & 8) + r;
-          store_matrices(smem_addr(sm.p[st]) + token * 128 + (((b + (lane >> 4)) ^ r) << 4), w0, w1,
-                         w2, w3);
+        auto put = [&](int h, int b, const uint32_t (&w)[4]) {
+          store_matrices(p_row + h * (16 * 128) + (p_chunk ^ (b << 4)), w[0], w[1], w[2], w[3]);
         };
         if (!general && (flags & kFarScale)) {
           general = true;
@@ -706,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (;;) {
           if (again) adjust();
           // the products of the stream's step before have read their P
-          if (used > 0) wait(sm, &sm.pv_done[st], (used - 1) & 1, p.err);
+          if (used > 0) wait(sm, &sm.pv_done[st], (used - 1) & 1);
           if (slow) {
             // ---- hidden tokens, or the second form: every row under its own factor
 #pragma unroll 1
@@ -744,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l[b + k] = fma2(y1, inv2, fma2(y0, inv2, l[b + k]));
                   }
                 }
-                put(h, b, w[0], w[1], w[2], w[3]);
+                put(h, b, w);
               }
             }
             break;
@@ -786,10 +708,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w[2 * k + 1] = half_pair(y1.x, y1.y);
                 l[b + k] = fma2(y1, inv2, fma2(y0, inv2, l[b + k]));
               }
-              put(h, b, w[0], w[1], w[2], w[3]);
+              put(h, b, w);
             }
           }
-          again = any_of(2 + st, top > kHeadroom + kLag);
+          again = any_of(2 + st, 128, top > kHeadroom + kLag);
           if (!again) break;
 #pragma unroll
           for (int b = 0; b < 8; b++) l[b] = was[b];
@@ -801,12 +723,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       step0 += pc.tiles;
       const bool any = pc.tiles > first;  // this stream had steps
-      if (any) wait(sm, &sm.pv_done[st], (used - 1) & 1, p.err);
-      tc::fence_after();
+      if (any) wait(sm, &sm.pv_done[st], (used - 1) & 1);
 
       // ---- the sums over the stream's tokens
 #pragma unroll
       for (int b = 0; b < 8; b++) {
+        if (b >= 2 * chunks) continue;
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
           l[b].x += __shfl_xor_sync(0xffffffffu, l[b].x, d);
@@ -839,20 +761,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_after();
 
       // ---- the rows' weights: thread t < 64 of each stream for the rows that it writes
-      struct Weights {  // O0 * a0 * b0 + O1 * a1 * b1 + part before * w, all times inv
+      struct alignas(16) Weights {  // (O0 a0 b0 + O1 a1 b1 + part before w) inv
         float a0, b0, a1, b1, w, inv;
         long long out;  // the output row
       };
       Weights* const weights = reinterpret_cast<Weights*>(sm.p[st]);
-      const long long tiles_begin = pc.begin + kBlockCost, tiles_end = tiles_begin + pc.all_tiles;
-      // of the same stretch: a piece in front of this one, a piece behind it
-      const bool after = pc.tile > 0 && tiles_begin + pc.tile > begin;
-      const bool before = tiles_begin + pc.tile + pc.tiles < min(tiles_end, end);
-      const bool whole = !before && begin <= tiles_begin && tiles_end <= end;
-      const size_t slot = 2 * (size_t)blockIdx.x + (begin < pc.begin ? 1 : 0);
-      float2* const pml = reinterpret_cast<float2*>(p.part_ml) + slot * kRows;
-      float* const po = p.part_o + slot * kRows * kHeadDim + t;
+      const bool whole = pc.flags & kWhole, after = pc.flags & kAfter;
       const bool both = !two && pc.tiles > 1;
+      float2* const pml = reinterpret_cast<float2*>(p.part_ml) + (size_t)pc.slot * kRows;
+      float* const po = p.part_o + (size_t)pc.slot * kRows * kHeadDim + t;
       float m = kLow, sum = 0.0f;
       if (t < rows) {
         const int s0 = two ? st : 0;
@@ -894,57 +811,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (after) named_sync(1, 256);  // both streams have read what is written now
       if (!whole && t < rows && (two || st == 0)) pml[base_row + t] = make_float2(m, sum);
       named_sync(2 + st, 128);
-      // ---- one channel a thread
+      // ---- one channel a thread; of one block of rows the streams write 16 in turn
       const uint32_t o0 = at + kColO + (two ? kStreamRows * st : 0);
 #pragma unroll 1
-      for (int c = two ? 0 : st; c < chunks; c += two ? 1 : 2) {
-        uint32_t x[16], y[16];
-        tc::load16(o0 + c * 16, x);
-        if (both) tc::load16(at + kColO + kStreamRows + c * 16, y);
+      for (int r0 = two ? 0 : 16 * st; r0 < rows; r0 += two || (r0 & 8) == 0 ? 8 : 24) {
+        uint32_t x[8], y[8];
+        load8(o0 + r0, x);
+        if (both) load8(at + kColO + kStreamRows + r0, y);
         tc::wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; k++) {
-          const int r = 16 * c + k;
+        for (int k = 0; k < 8; k++) {
+          const int r = r0 + k;
           if (r >= rows) continue;
           const Weights w = weights[r];
           float v = __uint_as_float(x[k]) * w.a0 * w.b0;
           if (both) v += __uint_as_float(y[k]) * w.a1 * w.b1;
-          if (after) v += __ldcg(po + (size_t)(base_row + r) * kHeadDim) * w.w;
+          if (after) v += __ldcg(po + (base_row + r) * kHeadDim) * w.w;
           if (whole) p.out[w.out * kHeadDim + t] = __float2bfloat16(v * w.inv);
-          else po[(size_t)(base_row + r) * kHeadDim] = v;
+          else po[(base_row + r) * kHeadDim] = v;
         }
       }
-      // the block's parts are joined by the kernel behind this one, from the CTA of the first
-      if (!whole && !before && tid == 0 && tiles_begin >= begin) {
-        const int c0 = (int)(tiles_begin / per);
+      // the block's parts are joined by the kernel behind this one
+      if ((pc.flags & kRecord) && tid == 0) {
         Record rec;
         rec.rows = pc.rows;
-        rec.parts = (int)((tiles_end - 1) / per) - c0 + 1;
-        rec.slot0 = (int)slot;
-        rec.cta = c0;
+        rec.parts = pc.parts;
+        rec.slot0 = pc.slot;
+        rec.cta = blockIdx.x;
         rec.row0 = q_row;
         rec.head0 = pc.h * p.group;
         rec.pad[0] = rec.pad[1] = 0;
         p.records[blockIdx.x] = rec;
       }
       tc::fence_before();
+      give_back();
     }
   } else if (warp < kVWarp) {
     tc::fewer_registers<kConvertRegs>();
     // ============================================ K's codes: one token a thread, into TMEM
     const int t = tid & 127;
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21) + kColK;
+    const uint32_t raw0 = smem_addr(sm.k_raw[0]) + t * 128, turn = (t & 7) << 4;
     int step = 0;
-    bool ok = true;
-    while (ok && walk.next(pc)) {
-      for (int j = 0; ok && j < pc.tiles; j++, step++) {
+    while (take(pc)) {
+#pragma unroll 1
+      for (int j = 0; j < pc.tiles; j++, step++) {
         const int stage = step % kStages;
-        ok = wait(sm, &sm.k_raw_full[stage], step / kStages & 1, p.err);
-        if (!ok) break;
-        const uint32_t raw = smem_addr(sm.k_raw[stage]) + t * 128;
+        wait(sm, &sm.k_raw_full[stage], step / kStages & 1);
         uint4 v[8];
 #pragma unroll
-        for (int c = 0; c < 8; c++) v[c] = lds128(raw + ((c ^ (t & 7)) << 4));
+        for (int c = 0; c < 8; c++) v[c] = lds128(raw0 + stage * kRawBytes + ((c << 4) ^ turn));
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.k_raw_empty[stage]);
 #pragma unroll
@@ -961,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (h == 0) {
-            ok = wait(sm, &sm.k_empty, (step & 1) ^ 1, p.err);
+            wait(sm, &sm.k_empty, (step & 1) ^ 1);
             tc::fence_after();
           }
           tc::store32(at + 32 * h, w);
@@ -970,28 +886,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before();
         mbar_arrive(&sm.k_full);
       }
+      give_back();
     }
   } else if (warp < kMmaWarp) {
     tc::fewer_registers<kConvertRegs>();
     // ============================================ V's codes: turned, 32 channels a warp, into TMEM
     const int w = warp - kVWarp;
     const uint32_t at = tmem + ((uint32_t)w << 21) + kColV;
+    // lane l points at token l of 32: the 16 channels of half 0, and those of half 1 beside them
+    const uint32_t raw0 = smem_addr(sm.v_raw[0]) + lane * 128, turn = (lane & 7) << 4;
     int step = 0;
-    bool ok = true;
-    while (ok && walk.next(pc)) {
-      for (int j = 0; ok && j < pc.tiles; j++, step++) {
+    while (take(pc)) {
+#pragma unroll 1
+      for (int j = 0; j < pc.tiles; j++, step++) {
         const int stage = step % kStages;
-        ok = wait(sm, &sm.v_raw_full[stage], step / kStages & 1, p.err);
-        if (!ok) break;
-        const uint32_t raw = smem_addr(sm.v_raw[stage]);
+        wait(sm, &sm.v_raw_full[stage], step / kStages & 1);
         uint32_t u[2][16];  // [16 channels][2 x 16 tokens: 4 words]
 #pragma unroll
         for (int h = 0; h < 2; h++)
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const int t = 32 * i + lane;
-            load_turned(raw + t * 128 + (((2 * w + h) ^ (t & 7)) << 4), &u[h][4 * i]);
-          }
+          for (int i = 0; i < 4; i++)
+            load_turned(raw0 + stage * kRawBytes + i * (32 * 128) + (((2 * w + h) << 4) ^ turn),
+                        &u[h][4 * i]);
         const int valid = sm.v_valid[stage][lane & 7];
         if (__any_sync(0xffffffffu, valid < kPage)) {
           // bytes no token wrote may be NaN, and a weight of 0 does not hide one
@@ -1018,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             r[2 * i + 1] = Codes<F>::template pair<1>(x);
           }
           if (h == 0) {
-            ok = wait(sm, &sm.v_empty, (step & 1) ^ 1, p.err);
+            wait(sm, &sm.v_empty, (step & 1) ^ 1);
             tc::fence_after();
           }
           store_16x64(at + ((uint32_t)(16 * h) << 16), r);
@@ -1027,6 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before();
         mbar_arrive(&sm.v_full);
       }
+      give_back();
     }
   } else {
     tc::fewer_registers<kOtherRegs>();
@@ -1037,46 +954,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t p_low = tc::desc_low(smem_addr(sm.p[0]), kPBytes);
     const bool lead = tc::elect();
     int step = 0;
-    uint32_t q_phase = 0, done[2] = {0, 0};
+    uint32_t done[2] = {0, 0};
     uint32_t s_phase = 0xF;  // bit 2 i + b: of the next wait for buffer b of stream i's S
-    bool ok = true;
-    while (ok && walk.next(pc)) {
+    // 128 products of 16 values of k each: K's tile or V's, in TMEM, with the queries or P
+    auto scores = [&](auto instr, uint32_t d) {  // from the queries of stream 0, or of both
+      if (lead) {
+#pragma unroll
+        for (int c = 0; c < 8; c++)
+          tc::mma_ts<decltype(instr)::value>(
+              d, tmem + kColK + c * 8, q_low + (((c >> 2) * kHalfBytes + (c & 3) * 32) >> 4), c > 0);
+      }
+    };
+    auto values = [&](auto instr, uint32_t d, uint32_t pp, bool add) {
+      if (lead) {
+#pragma unroll
+        for (int c = 0; c < 8; c++)
+          tc::mma_ts<decltype(instr)::value>(d, tmem + kColV + c * 8, pp + c * (2048 >> 4),
+                                             add || c > 0);
+      }
+    };
+    while (take(pc)) {
       const bool two = pc.rows > kStreamRows;
       // The products with V come one step (two streams on it) or two steps (in turn) behind the
       // scores, so that a stream's next scores are there when its softmax is done. Two streams'
       // products are one: 128 columns, K and V read once.
       const int behind = two ? 1 : 2;
-      ok = wait(sm, &sm.q_full, q_phase, p.err);
-      q_phase ^= 1;
-      auto scores = [&](auto instr, uint32_t d) {  // from the queries of stream 0, or of both
-        if (lead) {
-#pragma unroll
-          for (int c = 0; c < 8; c++)
-            tc::mma_ts<decltype(instr)::value>(
-                d, tmem + kColK + c * 8, q_low + (((c >> 2) * kHalfBytes + (c & 3) * 32) >> 4),
-                c > 0);
-        }
-      };
-      auto values = [&](auto instr, uint32_t d, uint32_t pp, bool add) {
-        if (lead) {
-#pragma unroll
-          for (int c = 0; c < 8; c++)
-            tc::mma_ts<decltype(instr)::value>(d, tmem + kColV + c * 8, pp + c * (2048 >> 4),
-                                               add || c > 0);
-        }
-      };
-      for (int j = 0; ok && j < pc.tiles + behind; j++) {
+      wait(sm, &sm.q_full, pieces & 1);
+#pragma unroll 1
+      for (int j = 0; j < pc.tiles + behind; j++) {
         if (j < pc.tiles) {
-          const int at = step + j;
-          ok = wait(sm, &sm.k_full, at & 1, p.err);
           const int buf = (two ? j : j >> 1) & 1;
+          wait(sm, &sm.k_full, (step + j) & 1);
 #pragma unroll
           for (int i = 0; i < 2; i++)
-            if (ok && (two || (j & 1) == i)) {
-              ok = wait(sm, &sm.s_empty[i][buf], s_phase >> (2 * i + buf) & 1, p.err);
+            if (two || (j & 1) == i) {
+              wait(sm, &sm.s_empty[i][buf], s_phase >> (2 * i + buf) & 1);
               s_phase ^= 1u << (2 * i + buf);
             }
-          if (!ok) break;
           tc::fence_after();
           const uint32_t d = tmem + kColS + 2 * kStreamRows * buf;
           if (two)
@@ -1085,51 +999,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             scores(std::integral_constant<uint32_t, tc::instr_f16(128, kStreamRows, false)>{},
                    d + kStreamRows * (j & 1));
-#pragma unroll
-          for (int i = 0; i < 2; i++)
-            if ((two || (j & 1) == i) && lead) tc::commit(&sm.s_full[i][buf]);
-          if (lead) tc::commit(&sm.k_empty);
+          if (lead) {
+            tc::commit(&sm.k_empty);
+            if (two || !(j & 1)) tc::commit(&sm.s_full[0][buf]);
+            if (two || (j & 1)) tc::commit(&sm.s_full[1][buf]);
+          }
           __syncwarp();
         }
         const int jj = j - behind;
         if (jj >= 0) {
-          const int at = step + jj;
-          ok = wait(sm, &sm.v_full, at & 1, p.err);
-#pragma unroll
-          for (int i = 0; i < 2; i++)
-            if (ok && (two || (jj & 1) == i)) ok = wait(sm, &sm.p_full[i], done[i] & 1, p.err);
-          if (!ok) break;
-          tc::fence_after();
-          if (two)
-            values(
-                std::integral_constant<uint32_t, tc::instr_f16(128, 2 * kStreamRows, true)>{},
-                tmem + kColO, p_low, jj > 0);
-          else
-            values(std::integral_constant<uint32_t, tc::instr_f16(128, kStreamRows, true)>{},
-                   tmem + kColO + kStreamRows * (jj & 1), p_low + (jj & 1) * (kPBytes >> 4),
-                   jj > 1);
+          wait(sm, &sm.v_full, (step + jj) & 1);
 #pragma unroll
           for (int i = 0; i < 2; i++)
             if (two || (jj & 1) == i) {
-              if (lead) tc::commit(&sm.pv_done[i]);
+              wait(sm, &sm.p_full[i], done[i] & 1);
               done[i]++;
             }
-          if (lead) tc::commit(&sm.v_empty);
+          tc::fence_after();
+          if (two)
+            values(std::integral_constant<uint32_t, tc::instr_f16(128, 2 * kStreamRows, true)>{},
+                   tmem + kColO, p_low, jj > 0);
+          else
+            values(std::integral_constant<uint32_t, tc::instr_f16(128, kStreamRows, true)>{},
+                   tmem + kColO + kStreamRows * (jj & 1), p_low + (jj & 1) * (kPBytes >> 4), jj > 1);
+          if (lead) {
+            tc::commit(&sm.v_empty);
+            if (two || !(jj & 1)) tc::commit(&sm.pv_done[0]);
+            if (two || (jj & 1)) tc::commit(&sm.pv_done[1]);
+          }
           __syncwarp();
         }
       }
       step += pc.tiles;
+      give_back();
     }
-    // the last arrivals on the barriers come before the CTA ends
-    if (ok && step > 0) {
-      wait(sm, &sm.k_empty, (step - 1) & 1, p.err);
-      wait(sm, &sm.v_empty, (step - 1) & 1, p.err);
-    }
-    // nor may products go on in shared and tensor memory that are given up
-    if (!ok) {
-      if (lead) tc::commit(&sm.all_done);
-      mbar_wait(&sm.all_done, 0);
-    }
+    // the last arrivals on the barriers come before the CTA ends, and no product goes on in shared
+    // and tensor memory that are given up
+    if (lead) tc::commit(&sm.all_done);
+    mbar_wait(&sm.all_done, 0);
   } else if (warp == kKLoad || warp == kVLoad) {
     // ============================================ the copies: 4 tiles' blocks a batch, one a lane
     const bool is_k = warp == kKLoad;
@@ -1139,22 +1046,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const CUtensorMap* const map = is_k ? &k_map : &v_map;
     const uint64_t policy = l2_evict_first_policy();
     struct Ahead {
-      int count;      // tiles of the batch (0: the end)
-      int y;          // this lane's block: its first row in the code array
-      int valid;      // its tokens
-      bool again;     // other row blocks read it too
+      int count;  // tiles of the batch (0: the end)
+      int y;      // this lane's block: its first row in the code array
+      int valid;  // its tokens
+      bool again; // other row blocks read it too
       float sk, sv;
     };
-    bool more = walk.next(pc);
+    bool more = take(pc);
     int done = 0;  // tiles of the piece that were fetched
     auto fetch = [&]() {
       Ahead a = {0, 0, 0, false, 0.0f, -1.0f};
       if (!more) return a;
       a.count = min(pc.tiles - done, 4);
       const int i = (pc.tile + done) * kTilePages + lane;
-      a.again = num[pc.b] > pc.nodes;
+      a.again = pc.flags & kShared;
       if (lane < a.count * kTilePages) {
-        a.valid = min(max(len[pc.b] - i * kPage, 0), kPage);
+        a.valid = min(max(pc.n_all - i * kPage, 0), kPage);
         if (a.valid > 0) {
           const int page = p.page_table[(size_t)pc.b * p.rows.max_pages + i];
           if (page >= 0 && page < p.num_pages) {
@@ -1173,17 +1080,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       done += a.count;
       if (done == pc.tiles) {
         done = 0;
-        more = walk.next(pc);
+        give_back();
+        more = take(pc);
       }
       return a;
     };
-    Ahead cur = fetch(), next = fetch();
+    Ahead cur = fetch(), next = {0, 0, 0, false, 0.0f, -1.0f};
     int step = 0;
     bool ok = true;
     while (ok && cur.count > 0) {
+#pragma unroll 1
       for (int j = 0; j < cur.count; j++, step++) {
         const int stage = step % kStages;
-        ok = wait(sm, &empty[stage], (step / kStages & 1) ^ 1, p.err);
+        ok = __all_sync(0xffffffffu, wait(sm, &empty[stage], (step / kStages & 1) ^ 1));
         if (!ok) break;
         const bool mine = lane >> 3 == j;
         const int blocks = __popc(__ballot_sync(0xffffffffu, mine && cur.valid > 0));
@@ -1209,18 +1118,153 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (cur.again) tma_load_2d(dst, map, 0, cur.y, &full[stage]);
           else tma_load_2d_hint(dst, map, 0, cur.y, &full[stage], policy);
         }
+        if (j == 0) next = fetch();  // while the first copies are on their way
       }
       cur = next;
-      next = fetch();
+      next.count = 0;
     }
     // copies under way write this CTA's shared memory: one more wait for each
     if (!ok)
       for (int i = max(step - kStages, 0); i < step; i++)
         mbar_wait(&full[i % kStages], i / kStages & 1);
+  } else if (warp == kPlanWarp) {
+    // ============================================ the plan: this CTA's slice of the line of steps
+    // A row block's places on the line are kBlockCost for what it costs beside its tiles, then one a
+    // tile; the pieces are told in order.
+    auto places = [&](int b) {  // of one row block
+      return token_tiles(len[b]) + kBlockCost;
+    };
+    auto blocks_of = [&](int n, int& most) {  // row blocks, their nodes
+      most = n > 0 ? nodes_a_block(n, p.block_nodes) : 1;
+      return (n + most - 1) / most;
+    };
+    auto sequence = [&](int b) {  // places of a whole sequence
+      int most;
+      return (long long)blocks_of(num[b], most) * p.hkv * places(b);
+    };
+    long long all = 0;
+    for (int b = lane; b < batch; b += 32) all += sequence(b);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+    const long long per = max((all + gridDim.x - 1) / gridDim.x, (long long)kMinPlaces);
+    const long long begin = min(blockIdx.x * per, all), end = min(begin + per, all);
+    // the sequence that holds place `begin`
+    int b = 0;
+    long long before = 0;  // places in front of sequence b
+    if (begin < end) {
+      for (int b0 = 0;; b0 += 32) {
+        long long incl = b0 + lane < batch ? sequence(b0 + lane) : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + incl > begin);
+        if (past != 0 || b0 + 32 >= batch) {
+          const int i = past ? __ffs(past) - 1 : 31;
+          b = min(b0 + i, batch - 1);
+          before += i > 0 ? __shfl_sync(0xffffffffu, incl, max(i - 1, 0)) : 0;
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    int most, blocks = blocks_of(num[b], most), one = places(b);
+    int h = 0, q = 0, off = 0;
+    if (begin < end) {
+      const long long at = begin - before;
+      h = (int)(at / ((long long)blocks * one));
+      const int rest = (int)(at - (long long)h * blocks * one);
+      q = rest / one;
+      off = rest % one;
+    }
+    long long x = begin;
+    int told = 0;
+    auto tell = [&](const Piece& piece) {
+      const int slot = told % kPieces;
+      if (!__all_sync(0xffffffffu,
+                      wait(sm, &sm.piece_empty[slot], (told / kPieces & 1) ^ 1)))
+        return false;
+      if (lane == 0) {
+        sm.piece[slot] = piece;
+        mbar_arrive(&sm.piece_full[slot]);
+      }
+      __syncwarp();
+      told++;
+      return true;
+    };
+    bool ok = true;
+    if (lane == 0) p.records[blockIdx.x].rows = 0;
+    while (ok && x < end) {
+      const long long block_begin = x - off, tiles_begin = block_begin + kBlockCost;
+      const int all_tiles = one - kBlockCost;
+      const long long tiles_end = tiles_begin + all_tiles;
+      int stop = (int)min((long long)one, off + (end - x));
+      Piece piece = {};
+      piece.tile = max(off - kBlockCost, 0);
+      piece.tiles = max(stop - kBlockCost, 0) - piece.tile;
+      const int nodes = min(most, num[b] - q * most);
+      piece.rows = nodes * p.group;
+      const int limit = piece.rows > kStreamRows ? kMaxSteps : 2 * kMaxSteps;
+      const bool cut = piece.tiles > limit;  // the rest of the stretch is the next piece
+      if (cut) {
+        piece.tiles = limit;
+        stop = piece.tile + limit + kBlockCost;
+      }
+      if (piece.tiles > 0) {
+        piece.b = b;
+        piece.h = h;
+        piece.n_all = len[b];
+        piece.start = len[b] - num[b];
+        piece.node = q * most;
+        piece.row0 = row0[b];
+        const bool after = piece.tile > 0 && tiles_begin + piece.tile > begin;
+        const bool whole = !cut && begin <= tiles_begin && tiles_end <= end;
+        const int c0 = (int)(tiles_begin / per);
+        piece.flags = (whole ? kWhole : 0) | (after ? kAfter : 0) | (cut ? kBefore : 0) |
+                      (!whole && !cut && tiles_begin >= begin ? kRecord : 0) |
+                      (num[b] > nodes ? kShared : 0);
+        piece.slot = 2 * blockIdx.x + (begin < block_begin ? 1 : 0);
+        piece.parts = (int)((tiles_end - 1) / per) - c0 + 1;
+        ok = tell(piece);
+      }
+      x += stop - off;
+      off = stop;
+      if (!cut) {
+        off = 0;
+        if (++q == blocks) {
+          q = 0;
+          if (++h == p.hkv) {
+            h = 0;
+            do b++;
+            while (b < batch && num[b] == 0);
+            if (b < batch) {
+              blocks = blocks_of(num[b], most);
+              one = places(b);
+            }
+          }
+        }
+      }
+    }
+    if (ok) tell(Piece{});
+    // rows of sequences that do not fit: 0 and -inf
+    for (int s = blockIdx.x; s < batch; s += gridDim.x) {
+      const int rows = p.rows.cu ? p.rows.cu[s + 1] - p.rows.cu[s] : 1;
+      if (rows == num[s]) continue;
+      const int first = max(row0[s], 0);
+      const int count = min(p.rows.cu ? p.rows.cu[s + 1] : s + 1, p.rows.total) - first;
+      for (long long i = lane; i < (long long)count * p.hq * (kHeadDim / 8); i += 32)
+        reinterpret_cast<uint4*>(p.out + (size_t)first * p.hq * kHeadDim)[i] =
+            make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse != nullptr)
+        for (long long i = lane; i < (long long)count * p.hq; i += 32)
+          p.lse[(size_t)first * p.hq + i] = -INFINITY;
+    }
   }
   tc::fence_before();
   __syncthreads();
   grid_dep_launch();
+  if (tid == 0 && sm.dead) set_error(p.err, kDevErrTimeout);
   if (warp == kMmaWarp) {
     tc::fence_after();
     tc::dealloc(tmem, 512);
@@ -1304,10 +1348,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_tree_join_kernel(const Jo
   }
 }
 
-size_t smem_bytes(int batch) {
-  return 1024 + sizeof(Smem) + 8 * (size_t)(batch + 1) + 12 * (size_t)batch;
-}
-static_assert(1024 + sizeof(Smem) + 8 * (kSeqs + 1) + 12 * kSeqs <= 227 * 1024, "shared memory");
+size_t smem_bytes(int batch) { return 1024 + sizeof(Smem) + 12 * (size_t)batch; }
+static_assert(1024 + sizeof(Smem) + 12 * 1024 <= 227 * 1024, "shared memory for the largest batch");
 
 }  // namespace
 
@@ -1322,39 +1364,35 @@ cudaError_t launch_kv8_tree(const Shape& s, const Kv8& c, const CUtensorMap& k_m
                             float* lse, float* part_ml, float* part_o, void* records, int* err,
                             int num_sms, cudaStream_t st) {
   auto kernel = c.format == kE4m3 ? kv8_tree_kernel<kE4m3> : kv8_tree_kernel<kInt8>;
-  const size_t smem = smem_bytes(std::min(s.batch, kSeqs));
+  const size_t smem = smem_bytes(s.batch);
   cudaError_t e = set_kernel_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
   const int grid = std::min(num_sms, kKv8MaxCtas);
-  for (int b0 = 0; e == cudaSuccess && b0 < s.batch; b0 += kSeqs) {
-    const int batch = std::min(s.batch - b0, kSeqs);
-    const int skip = cu ? 0 : b0;  // without offsets a sequence's row goes by its number
-    Params p;
-    p.rows = NewRows{cu ? cu + b0 : nullptr, seq_lens + b0, batch, total - skip, s.max_pages};
-    p.q = static_cast<const __nv_bfloat16*>(q) + skip * q_stride;
-    p.q_stride = q_stride;
-    p.k_scale = c.k_scale;
-    p.v_scale = c.v_scale;
-    p.parents = parents ? parents + skip : nullptr;
-    p.page_table = page_table + (size_t)b0 * s.max_pages;
-    p.out = static_cast<__nv_bfloat16*>(out) + (size_t)skip * s.hq * kHeadDim;
-    p.lse = lse ? lse + (size_t)skip * s.hq : nullptr;
-    p.part_ml = part_ml;
-    p.part_o = part_o;
-    p.records = static_cast<Record*>(records);
-    p.err = err;
-    p.hq = s.hq;
-    p.hkv = s.hkv;
-    p.group = s.group;
-    p.num_pages = s.num_pages;
-    p.block_nodes = kRows / s.group;
-    p.scale_log2 = s.sm_scale * 1.44269504088896341f;
-    e = launch_kernel(kernel, dim3(grid), dim3(kThreads), smem, st, true, k_map, v_map, p);
-    if (e != cudaSuccess) break;
-    const JoinParams jp = {part_ml, part_o, p.records, p.out, p.lse, s.hq, s.group};
-    e = launch_kernel(kv8_tree_join_kernel, dim3(grid, kRows / kJoinRows), dim3(kJoinWarps * 32), 0,
-                      st, true, jp);
-  }
-  return e;
+  Params p;
+  p.rows = NewRows{cu, seq_lens, s.batch, total, s.max_pages};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.parents = parents;
+  p.page_table = page_table;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.part_ml = part_ml;
+  p.part_o = part_o;
+  p.records = static_cast<Record*>(records);
+  p.err = err;
+  p.hq = s.hq;
+  p.hkv = s.hkv;
+  p.group = s.group;
+  p.num_pages = s.num_pages;
+  p.block_nodes = kRows / s.group;
+  p.scale_log2 = s.sm_scale * 1.44269504088896341f;
+  e = launch_kernel(kernel, dim3(grid), dim3(kThreads), smem, st, true, k_map, v_map, p);
+  if (e != cudaSuccess) return e;
+  const JoinParams jp = {part_ml, part_o, p.records, p.out, p.lse, s.hq, s.group};
+  return launch_kernel(kv8_tree_join_kernel, dim3(grid, kRows / kJoinRows), dim3(kJoinWarps * 32), 0,
+                       st, true, jp);
 }
 
 }  // namespace hsa
