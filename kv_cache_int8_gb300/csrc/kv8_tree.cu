@@ -162,23 +162,40 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
-// a * m + c and a + b on two values at once
-__device__ __forceinline__ float2 fma2(float2 a, float2 m, float2 c) {
-  float2 y;
-  asm("{.reg .b64 a, m, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 m, {%4, %5};\n\t"
-      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 a, a, m, c;\n\tmov.b64 {%0, %1}, a;}"
-      : "=f"(y.x), "=f"(y.y)
-      : "f"(a.x), "f"(a.y), "f"(m.x), "f"(m.y), "f"(c.x), "f"(c.y));
+// Two fp32 values in a pair of registers.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 pack(float lo, float hi) {
+  F2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ F2 pack(const uint32_t* v) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(v[0]), "r"(v[1]));
+  return r;
+}
+__device__ __forceinline__ F2 pack(float2 v) { return pack(v.x, v.y); }
+__device__ __forceinline__ float2 unpack(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 m, F2 c) {
+  F2 y;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(m), "l"(c));
   return y;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 y;
-  asm("{.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;}"
-      : "=f"(y.x), "=f"(y.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 y;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
   return y;
 }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 y;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+  return y;
+}
+__device__ __forceinline__ float2 ex2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -199,26 +216,16 @@ __device__ __forceinline__ bool any_of(int id, int threads, bool x) {
   return y != 0;
 }
 
-// 16 lanes x 16 columns of tensor memory: lane l gets columns 8 i + 2 (l % 4) + {0, 1} of rows l / 4
-// (r[4 i], r[4 i + 1]) and l / 4 + 8 (r[4 i + 2], r[4 i + 3]), i < 2; wait_loaded() before use.
-__device__ __forceinline__ void load_16x16(uint32_t addr, uint32_t* r) {
+// 16 lanes x 32 columns of tensor memory: lane l gets columns 8 i + 2 (l % 4) + {0, 1} of rows l / 4
+// (r[4 i], r[4 i + 1]) and l / 4 + 8 (r[4 i + 2], r[4 i + 3]), i < 4; tc::wait_ld() before use.
+__device__ __forceinline__ void load_16x32(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11,"
+      " %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
-}
-// tc::wait_ld() that what is made of the loaded values stays behind
-__device__ __forceinline__ void wait_loaded(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-__device__ __forceinline__ float2 as_floats(const uint32_t* s) {
-  return make_float2(__uint_as_float(s[0]), __uint_as_float(s[1]));
 }
 
 // Four 8 x 8 matrices of 16-bit values: lane l points at row l % 8 of matrix l / 8 and holds, of each,
@@ -487,9 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&sm.q_full);
       named_sync(1, 256);
 
-      float2 l[8], c[8];  // the rows' sums over the lane's tokens, and kHeadroom - m
+      F2 l[8], c[8];  // the rows' sums over the lane's tokens, and kHeadroom - m
 #pragma unroll
-      for (int b = 0; b < 8; b++) l[b] = c[b] = make_float2(0.0f, 0.0f);
+      for (int b = 0; b < 8; b++) l[b] = c[b] = 0;
       const int first = two ? 0 : st, stride = two ? 1 : 2;
       const uint32_t o_col = at + kColO + kStreamRows * st;
       // The maxima may be far off: before the first step, and behind one that rows saw nothing of.
@@ -506,10 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // some of the tokens are hidden from some row
         const bool masked = (flags & kHidden) != 0 || (pc.tile + j + 1) * kTokens > pc.start;
         auto load32 = [&](int h, int b, uint32_t (&s)[16]) {  // rows [8 b, 8 b + 32)
-#pragma unroll
-          for (int k = 0; k < 2; k++)
-            if (b / 2 + k < chunks)
-              load_16x16(s_col + ((uint32_t)(16 * h) << 16) + 8 * b + 16 * k, s + 8 * k);
+          load_16x32(s_col + ((uint32_t)(16 * h) << 16) + 8 * b, s);
         };
         // scores that a row does not see become -inf
         auto hide = [&](int h, int b0, const float4& pg, uint32_t (&s)[16]) {
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto factors = [&](const float4& pg, int b) {  // of rows 8 b + col, + 1, in the second form
           const float2 v = *reinterpret_cast<const float2*>(&sm.f[base_row + 8 * b + col]);
-          return make_float2(fmaxf(v.x * pg.z, kTiny), fmaxf(v.y * pg.z, kTiny));
+          return pack(fmaxf(v.x * pg.z, kTiny), fmaxf(v.y * pg.z, kTiny));
         };
         // The rows' maxima up to this step, over the stream's tokens, and what is kept under them.
         auto adjust = [&]() {
@@ -548,19 +552,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < 2; h++) {
               const float4 pg = pages[h];
               const float add = side ? 0.0f : pg.w;
-              const float2 w2 = make_float2(add, add);
+              const F2 w2 = pack(add, add);
 #pragma unroll
               for (int b0 = 0; b0 < 8; b0 += 4) {
                 if (b0 >= 2 * chunks) continue;
                 uint32_t s[16];
                 load32(h, b0, s);
-                wait_loaded(s);
+                tc::wait_ld();
                 if (masked) hide(h, b0, pg, s);
 #pragma unroll
                 for (int b = b0; b < b0 + 4; b++) {
-                  const float2 g2 = factors(pg, b);
-                  const float2 v0 = fma2(as_floats(s + 4 * (b - b0)), g2, w2);
-                  const float2 v1 = fma2(as_floats(s + 4 * (b - b0) + 2), g2, w2);
+                  const F2 g2 = factors(pg, b);
+                  const float2 v0 = unpack(fma2(pack(s + 4 * (b - b0)), g2, w2));
+                  const float2 v1 = unpack(fma2(pack(s + 4 * (b - b0) + 2), g2, w2));
                   top[b] = make_float2(max3(top[b].x, v0.x, v1.x), max3(top[b].y, v0.y, v1.y));
                 }
               }
@@ -590,12 +594,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int b = 0; b < 8; b++) {
               if (b >= 2 * chunks) continue;
-              if (side || !general) {  // the sums
-                const float2 by = *reinterpret_cast<const float2*>(&sm.by[st][8 * b + col]);
-                l[b].x *= by.x;
-                l[b].y *= by.y;
-              }
-              if (!side) c[b] = *reinterpret_cast<const float2*>(&sm.c[st][8 * b + col]);
+              if (side || !general)  // the sums
+                l[b] = mul2(l[b], *reinterpret_cast<const F2*>(&sm.by[st][8 * b + col]));
+              if (!side) c[b] = *reinterpret_cast<const F2*>(&sm.c[st][8 * b + col]);
             }
             if (!side && any_o) {  // the results
 #pragma unroll 1
@@ -634,36 +635,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int h = 0; h < 2; h++) {
               const float4 pg = pages[h];
-              const float2 w2 = make_float2(pg.w, pg.w), none = make_float2(0.0f, 0.0f);
-              const float2 inv2 = make_float2(pg.y, pg.y);
+              const F2 w2 = pack(pg.w, pg.w), inv2 = pack(pg.y, pg.y);
               uint32_t s[16];
 #pragma unroll
               for (int b = 0; b < 8; b += 2) {
                 if (b >= 2 * chunks) continue;
                 if (b % 4 == 0) {
                   load32(h, b, s);
-                  wait_loaded(s);
+                  tc::wait_ld();
                   if (masked) hide(h, b, pg, s);
                 }
                 uint32_t w[4];
 #pragma unroll
                 for (int k = 0; k < 2; k++) {
-                  const float2 g2 = factors(pg, b + k), add = add2(c[b + k], w2);
+                  const F2 g2 = factors(pg, b + k), add = add2(c[b + k], w2);
                   const uint32_t* v = &s[4 * (b % 4 + k)];
-                  float2 x0 = fma2(as_floats(v), g2, none), x1 = fma2(as_floats(v + 2), g2, none);
-                  float2 y0 = add2(x0, add), y1 = add2(x1, add);
-                  y0 = make_float2(ex2(y0.x), ex2(y0.y));
-                  y1 = make_float2(ex2(y1.x), ex2(y1.y));
+                  const F2 x0 = mul2(pack(v), g2), x1 = mul2(pack(v + 2), g2);
+                  const float2 y0 = ex2(unpack(add2(x0, add))), y1 = ex2(unpack(add2(x1, add)));
                   w[2 * k] = half_pair(y0.x, y0.y);
                   w[2 * k + 1] = half_pair(y1.x, y1.y);
                   if (general) {
                     const float2 mx =
                         *reinterpret_cast<const float2*>(&sm.mx[st][8 * (b + k) + col]);
-                    x0 = make_float2(ex2(x0.x - mx.x), ex2(x0.y - mx.y));
-                    x1 = make_float2(ex2(x1.x - mx.x), ex2(x1.y - mx.y));
-                    l[b + k] = add2(l[b + k], add2(x0, x1));
+                    const F2 to = pack(-mx.x, -mx.y);
+                    l[b + k] = add2(l[b + k], add2(pack(ex2(unpack(add2(x0, to)))),
+                                                   pack(ex2(unpack(add2(x1, to))))));
                   } else {
-                    l[b + k] = fma2(y1, inv2, fma2(y0, inv2, l[b + k]));
+                    l[b + k] = fma2(pack(y1), inv2, fma2(pack(y0), inv2, l[b + k]));
                   }
                 }
                 put(h, b, w);
@@ -673,9 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // ---- P and the sums under the maxima as they are; taken back where a score has gone over
           // the lag (rare)
-          float2 was[8];
-#pragma unroll
-          for (int b = 0; b < 8; b++) was[b] = l[b];
+          F2 d[8];  // the step's sums
           float top = -INFINITY;
           uint32_t s[2][16];  // 32 rows of a half; the next ones are on their way meanwhile
           load32(0, 0, s[0]);
@@ -683,14 +679,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < 4; u++) {
             const int h = u & 1, b0 = 4 * (u >> 1);
             if (b0 >= 2 * chunks) continue;
-            wait_loaded(s[h]);
+            tc::wait_ld();
             if (u == 0) load32(1, 0, s[1]);
             if (u == 1 && chunks > 2) load32(0, 4, s[0]);
             if (u == 2) load32(1, 4, s[1]);
             const float4 pg = pages[h];
             const float g = fmaxf(f * pg.z, kTiny);
-            const float2 g2 = make_float2(g, g), w2 = make_float2(pg.w, pg.w);
-            const float2 inv2 = make_float2(pg.y, pg.y);
+            const F2 g2 = pack(g, g), w2 = pack(pg.w, pg.w), inv2 = pack(pg.y, pg.y);
 #pragma unroll
             for (int b = b0; b < b0 + 4; b += 2) {
               if (b >= 2 * chunks) continue;
@@ -698,23 +693,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 2; k++) {
                 const uint32_t* v = &s[h][4 * (b + k - b0)];
-                const float2 add = add2(c[b + k], w2);
-                float2 y0 = fma2(as_floats(v), g2, add), y1 = fma2(as_floats(v + 2), g2, add);
+                const F2 add = add2(c[b + k], w2);
+                float2 y0 = unpack(fma2(pack(v), g2, add)), y1 = unpack(fma2(pack(v + 2), g2, add));
                 top = max3(top, y0.x, y0.y);
                 top = max3(top, y1.x, y1.y);
-                y0 = make_float2(ex2(y0.x), ex2(y0.y));
-                y1 = make_float2(ex2(y1.x), ex2(y1.y));
+                y0 = ex2(y0);
+                y1 = ex2(y1);
                 w[2 * k] = half_pair(y0.x, y0.y);
                 w[2 * k + 1] = half_pair(y1.x, y1.y);
-                l[b + k] = fma2(y1, inv2, fma2(y0, inv2, l[b + k]));
+                const F2 e = h == 0 ? mul2(pack(y0), inv2) : fma2(pack(y0), inv2, d[b + k]);
+                d[b + k] = fma2(pack(y1), inv2, e);
               }
               put(h, b, w);
             }
           }
           again = any_of(2 + st, 128, top > kHeadroom + kLag);
-          if (!again) break;
+          if (!again) {
 #pragma unroll
-          for (int b = 0; b < 8; b++) l[b] = was[b];
+            for (int b = 0; b < 8; b++)
+              if (b < 2 * chunks) l[b] = add2(l[b], d[b]);
+            break;
+          }
         }
         tc::fence_before();
         mbar_arrive(&sm.s_empty[st][buf]);
@@ -729,12 +728,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int b = 0; b < 8; b++) {
         if (b >= 2 * chunks) continue;
+        float2 v = unpack(l[b]);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
-          l[b].x += __shfl_xor_sync(0xffffffffu, l[b].x, d);
-          l[b].y += __shfl_xor_sync(0xffffffffu, l[b].y, d);
+          v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
+          v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
         }
-        if (lane < 4) *reinterpret_cast<float2*>(&sm.red[st][warp & 3][8 * b + col]) = l[b];
+        if (lane < 4) *reinterpret_cast<float2*>(&sm.red[st][warp & 3][8 * b + col]) = v;
       }
       if (t < kStreamRows) {
         // The second form's frames brought together, within 2^50 of the sum's own: O (the result
@@ -858,17 +858,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < pc.tiles; j++, step++) {
         const int stage = step % kStages;
         wait(sm, &sm.k_raw_full[stage], step / kStages & 1);
-        uint4 v[8];
-#pragma unroll
-        for (int c = 0; c < 8; c++) v[c] = lds128(raw0 + stage * kRawBytes + ((c << 4) ^ turn));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.k_raw_empty[stage]);
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
+#pragma unroll 1
+        for (int h = 0; h < 2; h++) {  // 64 channels
           uint32_t w[32];
 #pragma unroll
           for (int c = 0; c < 4; c++) {
-            const uint32_t u[4] = {v[4 * h + c].x, v[4 * h + c].y, v[4 * h + c].z, v[4 * h + c].w};
+            const uint4 v = lds128(raw0 + stage * kRawBytes + (((4 * h + c) << 4) ^ turn));
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; k++) {
               const uint32_t x = Codes<F>::prepare(u[k]);
@@ -882,6 +878,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc::store32(at + 32 * h, w);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.k_raw_empty[stage]);
         tc::wait_st();
         tc::fence_before();
         mbar_arrive(&sm.k_full);
@@ -901,35 +899,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < pc.tiles; j++, step++) {
         const int stage = step % kStages;
         wait(sm, &sm.v_raw_full[stage], step / kStages & 1);
-        uint32_t u[2][16];  // [16 channels][2 x 16 tokens: 4 words]
-#pragma unroll
-        for (int h = 0; h < 2; h++)
+        const int valid = sm.v_valid[stage][lane & 7];
+        const bool partial = __any_sync(0xffffffffu, valid < kPage);
+#pragma unroll 1
+        for (int h = 0; h < 2; h++) {  // 16 channels
+          uint32_t u[16], r[32];  // of each 16 tokens 2 words
 #pragma unroll
           for (int i = 0; i < 4; i++)
             load_turned(raw0 + stage * kRawBytes + i * (32 * 128) + (((2 * w + h) << 4) ^ turn),
-                        &u[h][4 * i]);
-        const int valid = sm.v_valid[stage][lane & 7];
-        if (__any_sync(0xffffffffu, valid < kPage)) {
-          // bytes no token wrote may be NaN, and a weight of 0 does not hide one
+                        &u[4 * i]);
+          if (partial) {
+            // bytes no token wrote may be NaN, and a weight of 0 does not hide one
 #pragma unroll
-          for (int b = 0; b < kTilePages; b++) {
-            const int left = __shfl_sync(0xffffffffu, valid, b) - 4 * (lane & 3);
-            const uint32_t mask = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << 8 * left) - 1;
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-              u[h][2 * b] &= mask;
-              u[h][2 * b + 1] &= mask;
+            for (int b = 0; b < kTilePages; b++) {
+              const int left = __shfl_sync(0xffffffffu, valid, b) - 4 * (lane & 3);
+              const uint32_t mask = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << 8 * left) - 1;
+              u[2 * b] &= mask;
+              u[2 * b + 1] &= mask;
             }
           }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.v_raw_empty[stage]);
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-          uint32_t r[32];
 #pragma unroll
           for (int i = 0; i < 16; i++) {
-            const uint32_t x = Codes<F>::prepare(u[h][i]);
+            const uint32_t x = Codes<F>::prepare(u[i]);
             r[2 * i] = Codes<F>::template pair<0>(x);
             r[2 * i + 1] = Codes<F>::template pair<1>(x);
           }
@@ -939,6 +930,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           store_16x64(at + ((uint32_t)(16 * h) << 16), r);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.v_raw_empty[stage]);
         tc::wait_st();
         tc::fence_before();
         mbar_arrive(&sm.v_full);
