@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool two = pc.rows > kStreamRows;
       const int base_row = two ? kStreamRows * st : 0;
       const int rows = min(pc.rows - base_row, kStreamRows);  // of this stream
-      const int chunks = (rows + 15) / 16;
+      const bool wide = rows > 32;
       const int q_row = pc.row0 + pc.node;
       if (tid == 0) {
         sm.exponent_max = 0;
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const F2 w2 = pack(add, add);
 #pragma unroll
               for (int b0 = 0; b0 < 8; b0 += 4) {
-                if (b0 >= 2 * chunks) continue;
+                if (b0 > 0 && !wide) continue;
                 uint32_t s[16];
                 load32(h, b0, s);
                 tc::wait_ld();
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int b = 0; b < 8; b++) {
-              if (b >= 2 * chunks) continue;
+              if (b >= 4 && !wide) continue;
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) {
                 top[b].x = fmaxf(top[b].x, __shfl_xor_sync(0xffffffffu, top[b].x, d));
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<float2*>(&sm.red[st][warp & 3][8 * b + col]) = top[b];
             }
             named_sync(2 + st, 128);
-            if (t < 16 * chunks) {
+            if (t < (wide ? 64 : 32)) {
               float* const kept = side ? sm.mx[st] : sm.m[st];
               const float was = kept[t];
               const float now = fmaxf(max3(was, sm.red[st][0][t], sm.red[st][1][t]),
@@ -593,14 +593,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_sync(2 + st, 128);
 #pragma unroll
             for (int b = 0; b < 8; b++) {
-              if (b >= 2 * chunks) continue;
+              if (b >= 4 && !wide) continue;
               if (side || !general)  // the sums
                 l[b] = mul2(l[b], *reinterpret_cast<const F2*>(&sm.by[st][8 * b + col]));
               if (!side) c[b] = *reinterpret_cast<const F2*>(&sm.c[st][8 * b + col]);
             }
             if (!side && any_o) {  // the results
 #pragma unroll 1
-              for (int k0 = 0; k0 < 16 * chunks; k0 += 16) {
+              for (int k0 = 0; k0 < rows; k0 += 16) {
                 uint32_t o[16];
                 tc::load16(o_col + k0, o);
                 tc::wait_ld();
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t s[16];
 #pragma unroll
               for (int b = 0; b < 8; b += 2) {
-                if (b >= 2 * chunks) continue;
+                if (b >= 4 && !wide) continue;
                 if (b % 4 == 0) {
                   load32(h, b, s);
                   tc::wait_ld();
@@ -678,17 +678,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int u = 0; u < 4; u++) {
             const int h = u & 1, b0 = 4 * (u >> 1);
-            if (b0 >= 2 * chunks) continue;
+            if (b0 > 0 && !wide) continue;
             tc::wait_ld();
             if (u == 0) load32(1, 0, s[1]);
-            if (u == 1 && chunks > 2) load32(0, 4, s[0]);
+            if (u == 1 && wide) load32(0, 4, s[0]);
             if (u == 2) load32(1, 4, s[1]);
             const float4 pg = pages[h];
             const float g = fmaxf(f * pg.z, kTiny);
             const F2 g2 = pack(g, g), w2 = pack(pg.w, pg.w), inv2 = pack(pg.y, pg.y);
 #pragma unroll
             for (int b = b0; b < b0 + 4; b += 2) {
-              if (b >= 2 * chunks) continue;
               uint32_t w[4];
 #pragma unroll
               for (int k = 0; k < 2; k++) {
@@ -711,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!again) {
 #pragma unroll
             for (int b = 0; b < 8; b++)
-              if (b < 2 * chunks) l[b] = add2(l[b], d[b]);
+              if (b < 4 || wide) l[b] = add2(l[b], d[b]);
             break;
           }
         }
@@ -727,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the sums over the stream's tokens
 #pragma unroll
       for (int b = 0; b < 8; b++) {
-        if (b >= 2 * chunks) continue;
+        if (b >= 4 && !wide) continue;
         float2 v = unpack(l[b]);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
