@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
+  grid_dep_launch();  // the joining kernel, whose CTAs take the places of those that end
   const uint32_t tmem = sm.tmem;
   // The pieces, as the plan's warp tells them; every other warp takes each and gives it back.
   int pieces = 0;
@@ -1088,6 +1089,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const bool mine = lane >> 3 == j;
         const int blocks = __popc(__ballot_sync(0xffffffffu, mine && cur.valid > 0));
+        if (mine && cur.valid > 0) {  // (before the scales are there; the bytes are told below)
+          unsigned char* dst = raw + stage * kRawBytes + (lane & 7) * kBlockBytesI8;
+          if (cur.again) tma_load_2d(dst, map, 0, cur.y, &full[stage]);
+          else tma_load_2d_hint(dst, map, 0, cur.y, &full[stage], policy);
+        }
         if (is_k) {
           const float log = log2f(cur.sv);
           const bool far = mine && cur.valid > 0 && !(fabsf(log) <= kPlainScale);
@@ -1104,12 +1110,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&full[stage], blocks * kBlockBytesI8);
-        __syncwarp();
-        if (mine && cur.valid > 0) {
-          unsigned char* dst = raw + stage * kRawBytes + (lane & 7) * kBlockBytesI8;
-          if (cur.again) tma_load_2d(dst, map, 0, cur.y, &full[stage]);
-          else tma_load_2d_hint(dst, map, 0, cur.y, &full[stage], policy);
-        }
         if (j == 0) next = fetch();  // while the first copies are on their way
       }
       cur = next;
@@ -1123,6 +1123,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ============================================ the plan: this CTA's slice of the line of steps
     // A row block's places on the line are kBlockCost for what it costs beside its tiles, then one a
     // tile; the pieces are told in order.
+    auto over = [](long long a, long long by) {  // a / by (a division of 64 bits takes a microsecond)
+      return ((a | by) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)by) : a / by;
+    };
     auto places = [&](int b) {  // of one row block
       return token_tiles(len[b]) + kBlockCost;
     };
@@ -1138,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = lane; b < batch; b += 32) all += sequence(b);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
-    const long long per = max((all + gridDim.x - 1) / gridDim.x, (long long)kMinPlaces);
+    const long long per = max(over(all + gridDim.x - 1, gridDim.x), (long long)kMinPlaces);
     const long long begin = min(blockIdx.x * per, all), end = min(begin + per, all);
     // the sequence that holds place `begin`
     int b = 0;
@@ -1164,9 +1167,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int most, blocks = blocks_of(num[b], most), one = places(b);
     int h = 0, q = 0, off = 0;
     if (begin < end) {
-      const long long at = begin - before;
-      h = (int)(at / ((long long)blocks * one));
-      const int rest = (int)(at - (long long)h * blocks * one);
+      const long long at = begin - before, head = (long long)blocks * one;
+      h = (int)over(at, head);
+      const int rest = (int)(at - h * head);
       q = rest / one;
       off = rest % one;
     }
@@ -1212,12 +1215,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         piece.row0 = row0[b];
         const bool after = piece.tile > 0 && tiles_begin + piece.tile > begin;
         const bool whole = !cut && begin <= tiles_begin && tiles_end <= end;
-        const int c0 = (int)(tiles_begin / per);
+        const int c0 = (int)over(tiles_begin, per);
         piece.flags = (whole ? kWhole : 0) | (after ? kAfter : 0) | (cut ? kBefore : 0) |
                       (!whole && !cut && tiles_begin >= begin ? kRecord : 0) |
                       (num[b] > nodes ? kShared : 0);
         piece.slot = 2 * blockIdx.x + (begin < block_begin ? 1 : 0);
-        piece.parts = (int)((tiles_end - 1) / per) - c0 + 1;
+        piece.parts = (int)over(tiles_end - 1, per) - c0 + 1;
         ok = tell(piece);
       }
       x += stop - off;
@@ -1255,7 +1258,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before();
   __syncthreads();
-  grid_dep_launch();
   if (tid == 0 && sm.dead) set_error(p.err, kDevErrTimeout);
   if (warp == kMmaWarp) {
     tc::fence_after();
@@ -1265,9 +1267,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------- row blocks that were cut, joined
 //
-// Grid: (CTAs of the attention, kRows / kJoinRows); a warp takes a row at a time, four channels a
-// lane. The weights of up to 256 parts come first, then their values, eight under way at once.
-constexpr int kJoinRows = 8, kJoinWarps = 4;
+// Rows of all records in one line, a warp each, or where they are few a CTA each, whose warps take
+// the parts in turn. A lane has four channels; values are asked for before their weights are known.
+constexpr int kJoinWarps = 8, kJoinAhead = 8;
 
 struct JoinParams {
   const float* part_ml;
@@ -1279,58 +1281,100 @@ struct JoinParams {
 };
 
 __global__ void __launch_bounds__(kJoinWarps * 32) kv8_tree_join_kernel(const JoinParams p) {
-  __shared__ float weight[kJoinWarps][kKv8MaxCtas];
+  __shared__ int upto[kKv8MaxCtas];  // rows of records 0 .. i
+  __shared__ int sums[kJoinWarps];
+  __shared__ float4 part_acc[kJoinWarps][32];
+  __shared__ float2 part_sum[kJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
   grid_dep_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Record rec = p.records[blockIdx.x];
-  for (int r = blockIdx.y * kJoinRows + warp; r < min(rec.rows, (int)(blockIdx.y + 1) * kJoinRows);
-       r += kJoinWarps) {
-    // part 0 in its own slot, part i in the first slot of the i-th CTA behind
-    auto slot_of = [&](int i) { return (size_t)(i == 0 ? rec.slot0 : 2 * (rec.cta + i)); };
-    float2 ml[kKv8MaxCtas / 32];
-    float top = kLow;
+  {
+    static_assert(kJoinWarps * 32 >= kKv8MaxCtas, "a thread a record");
+    int incl = threadIdx.x < gridDim.x ? p.records[threadIdx.x].rows : 0;
 #pragma unroll
-    for (int k = 0; k < kKv8MaxCtas / 32; k++) {
-      const int i = 32 * k + lane;
-      ml[k] = make_float2(kLow, 0.0f);
-      if (i < rec.parts)
-        ml[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(i) * kRows + r);
-      top = fmaxf(top, ml[k].x);
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
     }
-    top = warp_max(top);
-    float sum = 0.0f;
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < kKv8MaxCtas / 32; k++) {
-      const float w = ex2(ml[k].x - top);
-      weight[warp][32 * k + lane] = w;
-      sum += w * ml[k].y;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    __syncwarp();
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; w++) incl += sums[w];
+    upto[threadIdx.x] = incl;
+    __syncthreads();
+  }
+  const int rows = upto[gridDim.x - 1];
+  const bool shared = rows <= 2 * (int)gridDim.x;  // a row is the CTA's
+  const int first = shared ? warp : 0, stride = shared ? kJoinWarps : 1;
+  for (int u = shared ? blockIdx.x : blockIdx.x * kJoinWarps + warp; u < rows;
+       u += gridDim.x * (shared ? 1 : kJoinWarps)) {
+    int i = 0;  // the record that holds row u: the first with upto > u
+    for (int step = kKv8MaxCtas / 2; step > 0; step >>= 1)
+      if (i + step <= (int)gridDim.x && upto[i + step - 1] <= u) i += step;
+    const Record rec = p.records[i];
+    const int r = u - (i > 0 ? upto[i - 1] : 0);
+    // part 0 in its own slot, part k in the first slot of the k-th CTA behind
+    auto slot_of = [&](int k) { return (size_t)(k == 0 ? rec.slot0 : 2 * (rec.cta + k)); };
     const float4* src = reinterpret_cast<const float4*>(p.part_o) + r * (kHeadDim / 4) + lane;
-    for (int i0 = 0; i0 < rec.parts; i0 += 8) {
-      float4 v[8];
+    float top = kLow, sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k0 = first; k0 < rec.parts; k0 += 32 * stride) {
+      const int mine = k0 + lane * stride;
+      float2 ml = make_float2(kLow, 0.0f);
+      if (mine < rec.parts)
+        ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(mine) * kRows + r);
+      float weight = 0.0f;
+      for (int j0 = 0; j0 < 32 && k0 + j0 * stride < rec.parts; j0 += kJoinAhead) {
+        float4 v[kJoinAhead];
 #pragma unroll
-      for (int k = 0; k < 8; k++) {
-        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (i0 + k < rec.parts) v[k] = __ldcg(src + slot_of(i0 + k) * (kRows * kHeadDim / 4));
-      }
+        for (int j = 0; j < kJoinAhead; j++) {
+          const int k = k0 + (j0 + j) * stride;
+          v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (k < rec.parts) v[j] = __ldcg(src + slot_of(k) * (kRows * kHeadDim / 4));
+        }
+        if (j0 == 0) {
+          const float now = fmaxf(top, warp_max(ml.x)), keep = ex2(top - now);
+          weight = mine < rec.parts ? ex2(ml.x - now) : 0.0f;
+          float of = weight * ml.y;
 #pragma unroll
-      for (int k = 0; k < 8; k++) {
-        const float w = i0 + k < rec.parts ? weight[warp][i0 + k] : 0.0f;
-        acc.x += w * v[k].x;
-        acc.y += w * v[k].y;
-        acc.z += w * v[k].z;
-        acc.w += w * v[k].w;
+          for (int d = 16; d > 0; d >>= 1) of += __shfl_xor_sync(0xffffffffu, of, d);
+          sum = sum * keep + of;
+          acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+          top = now;
+        }
+#pragma unroll
+        for (int j = 0; j < kJoinAhead; j++) {
+          const float w = __shfl_sync(0xffffffffu, weight, j0 + j);
+          acc.x += w * v[j].x;
+          acc.y += w * v[j].y;
+          acc.z += w * v[j].z;
+          acc.w += w * v[j].w;
+        }
       }
+    }
+    if (shared) {
+      part_acc[warp][lane] = acc;
+      if (lane == 0) part_sum[warp] = make_float2(top, sum);
+      __syncthreads();
+      if (warp == 0) {
+        const int ways = min(kJoinWarps, rec.parts);
+        for (int w = 0; w < ways; w++) top = fmaxf(top, part_sum[w].x);
+        sum = 0.0f;
+        acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int w = 0; w < ways; w++) {
+          const float by = ex2(part_sum[w].x - top);
+          const float4 v = part_acc[w][lane];
+          sum += by * part_sum[w].y;
+          acc.x += by * v.x;
+          acc.y += by * v.y;
+          acc.z += by * v.z;
+          acc.w += by * v.w;
+        }
+      }
+      __syncthreads();
+      if (warp != 0) continue;
     }
     const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-    const size_t out =
-        (size_t)(rec.row0 + r / p.group) * p.hq + rec.head0 + r % p.group;
+    const size_t out = (size_t)(rec.row0 + r / p.group) * p.hq + rec.head0 + r % p.group;
     __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
     __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
     reinterpret_cast<uint2*>(p.out + out * kHeadDim)[lane] =
@@ -1383,8 +1427,7 @@ cudaError_t launch_kv8_tree(const Shape& s, const Kv8& c, const CUtensorMap& k_m
   e = launch_kernel(kernel, dim3(grid), dim3(kThreads), smem, st, true, k_map, v_map, p);
   if (e != cudaSuccess) return e;
   const JoinParams jp = {part_ml, part_o, p.records, p.out, p.lse, s.hq, s.group};
-  return launch_kernel(kv8_tree_join_kernel, dim3(grid, kRows / kJoinRows), dim3(kJoinWarps * 32), 0,
-                       st, true, jp);
+  return launch_kernel(kv8_tree_join_kernel, dim3(grid), dim3(kJoinWarps * 32), 0, st, true, jp);
 }
 
 }  // namespace hsa
