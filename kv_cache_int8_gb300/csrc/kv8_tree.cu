@@ -616,8 +616,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         // P of a half's rows [8 b, 8 b + 16): eight tokens and eight rows a matrix
-        auto put = [&](int h, int b, const uint32_t (&w)[4]) {
+        auto put = [&](int h, int b, const uint32_t* w) {
           store_matrices(p_row + h * (16 * 128) + (p_chunk ^ (b << 4)), w[0], w[1], w[2], w[3]);
+        };
+        auto free_p = [&]() {  // the products of the stream's step before have read their P
+          if (used > 0) wait(sm, &sm.pv_done[st], (used - 1) & 1);
         };
         if (!general && (flags & kFarScale)) {
           general = true;
@@ -629,9 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         unknown = slow;  // (hidden tokens: rows may still have no maximum)
         for (;;) {
           if (again) adjust();
-          // the products of the stream's step before have read their P
-          if (used > 0) wait(sm, &sm.pv_done[st], (used - 1) & 1);
           if (slow) {
+            free_p();
             // ---- hidden tokens, or the second form: every row under its own factor
 #pragma unroll 1
             for (int h = 0; h < 2; h++) {
@@ -672,7 +674,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // ---- P and the sums under the maxima as they are; taken back where a score has gone over
           // the lag (rare)
-          F2 d[8];  // the step's sums
+          F2 d[8];           // the step's sums
+          uint32_t w[4][8];  // and its P, which goes to shared memory when that is free
           float top = -INFINITY;
           uint32_t s[2][16];  // 32 rows of a half; the next ones are on their way meanwhile
           load32(0, 0, s[0]);
@@ -688,27 +691,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float g = fmaxf(f * pg.z, kTiny);
             const F2 g2 = pack(g, g), w2 = pack(pg.w, pg.w), inv2 = pack(pg.y, pg.y);
 #pragma unroll
-            for (int b = b0; b < b0 + 4; b += 2) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 2; k++) {
-                const uint32_t* v = &s[h][4 * (b + k - b0)];
-                const F2 add = add2(c[b + k], w2);
-                float2 y0 = unpack(fma2(pack(v), g2, add)), y1 = unpack(fma2(pack(v + 2), g2, add));
-                top = max3(top, y0.x, y0.y);
-                top = max3(top, y1.x, y1.y);
-                y0 = ex2(y0);
-                y1 = ex2(y1);
-                w[2 * k] = half_pair(y0.x, y0.y);
-                w[2 * k + 1] = half_pair(y1.x, y1.y);
-                const F2 e = h == 0 ? mul2(pack(y0), inv2) : fma2(pack(y0), inv2, d[b + k]);
-                d[b + k] = fma2(pack(y1), inv2, e);
-              }
-              put(h, b, w);
+            for (int b = b0; b < b0 + 4; b++) {
+              const uint32_t* v = &s[h][4 * (b - b0)];
+              const F2 add = add2(c[b], w2);
+              float2 y0 = unpack(fma2(pack(v), g2, add)), y1 = unpack(fma2(pack(v + 2), g2, add));
+              top = max3(top, y0.x, y0.y);
+              top = max3(top, y1.x, y1.y);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              w[u][2 * (b - b0)] = half_pair(y0.x, y0.y);
+              w[u][2 * (b - b0) + 1] = half_pair(y1.x, y1.y);
+              const F2 e = h == 0 ? mul2(pack(y0), inv2) : fma2(pack(y0), inv2, d[b]);
+              d[b] = fma2(pack(y1), inv2, e);
             }
           }
           again = any_of(2 + st, 128, top > kHeadroom + kLag);
           if (!again) {
+            free_p();
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+              if (u > 1 && !wide) continue;
+              put(u & 1, 4 * (u >> 1), w[u]);
+              put(u & 1, 4 * (u >> 1) + 2, w[u] + 4);
+            }
 #pragma unroll
             for (int b = 0; b < 8; b++)
               if (b < 4 || wide) l[b] = add2(l[b], d[b]);
