@@ -142,10 +142,10 @@ struct Smem {
       v_raw_empty[kStages], k_full, k_empty, v_full, v_empty, s_full[2][2], s_empty[2][2], p_full[2],
       pv_done[2], piece_full[kPieces], piece_empty[kPieces], all_done;
   uint32_t tmem;
-  int exponent_max, exponent_min;
+  int2 exponents[kKWarp];
   int dead;
 };
-// behind it: len, n, row0 (int [batch] each)
+// behind it: len, n, row0, block_nodes, blocks (int [batch] each)
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -292,7 +292,7 @@ __device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity) {
 
 // Row blocks of a sequence of n nodes, as equal as they come: the nodes of each.
 __device__ __forceinline__ int nodes_a_block(int n, int most) {
-  const int blocks = (n + most - 1) / most;
+  const int blocks = max((n + most - 1) / most, 1);
   return (n + blocks - 1) / blocks;
 }
 __device__ __forceinline__ int token_tiles(int len) { return (len + kTokens - 1) / kTokens; }
@@ -308,6 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* len = reinterpret_cast<int*>(&sm + 1);
   int* num = len + batch;
   int* row0 = num + batch;
+  int* block_nodes = row0 + batch;
+  int* blocks = block_nodes + batch;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -354,6 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     len[b] = sp.start + sp.n;
     num[b] = sp.n;
     row0[b] = sp.row0;
+    // row blocks, as equal as they come, and a row block's places on the line (see the plan)
+    const int most = max(nodes_a_block(sp.n, p.block_nodes), 1);
+    block_nodes[b] = most;
+    blocks[b] = (sp.n + most - 1) / most;
   }
   tc::fence_before();
   __syncthreads();
@@ -400,10 +406,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = min(pc.rows - base_row, kStreamRows);  // of this stream
       const bool wide = rows > 32;
       const int q_row = pc.row0 + pc.node;
-      if (tid == 0) {
-        sm.exponent_max = 0;
-        sm.exponent_min = 255;
-      }
       const bool branches = (pc.tile + pc.tiles) * kTokens > pc.start;
       if (branches) *reinterpret_cast<uint4*>(sm.seen[tid]) = make_uint4(0u, 0u, 0u, 0u);
       if (t < kStreamRows) {
@@ -411,7 +413,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.mx[st][t] = kLow;
         sm.c[st][t] = kHeadroom - kLow;
       }
-      named_sync(1, 256);
       // ---- the queries in fp16, four threads a row. All rows under one power of two that puts
       // the largest value in [2^13, 2^14), as long as the smallest row's largest is within 2^-15
       // of it (its values down to 2^-22 of their largest are then exact in fp16, and the rest is
@@ -432,24 +433,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         m16 = max(m16, __shfl_xor_sync(0xffffffffu, m16, 2));
         return m16 == 0 ? -1 : (int)(m16 >> 7);
       };
-      const int passes = two ? 2 : 1;
-#pragma unroll 1
-      for (int i = 0; i < passes; i++) {
+      uint4 raw[2][4];
+      int e[2];
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
         const int r = (tid >> 2) + 64 * i;
-        uint4 v[4];
 #pragma unroll
         for (int k = 0; k < 4; k++)
-          v[k] = r < pc.rows ? reinterpret_cast<const uint4*>(query(r))[k]
-                             : make_uint4(0u, 0u, 0u, 0u);
-        const int e = exponent(v);
-        const bool counts = e >= 0 && e < 255;
-        const int e_max = __reduce_max_sync(0xffffffffu, counts ? e : 0);
-        const int e_min = __reduce_min_sync(0xffffffffu, counts ? e : 255);
-        if (lane == 0) {
-          atomicMax(&sm.exponent_max, e_max);
-          atomicMin(&sm.exponent_min, e_min);
-        }
+          raw[i][k] = r < pc.rows ? reinterpret_cast<const uint4*>(query(r))[k]
+                                  : make_uint4(0u, 0u, 0u, 0u);
       }
+      {
+        int most = 0, least = 255;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          e[i] = exponent(raw[i]);
+          if (e[i] >= 0 && e[i] < 255) {
+            most = max(most, e[i]);
+            least = min(least, e[i]);
+          }
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        least = __reduce_min_sync(0xffffffffu, least);
+        if (lane == 0) sm.exponents[warp] = make_int2(most, least);
+      }
+      named_sync(1, 256);
       // which rows see a node: its own, and those of the nodes below it
       if (branches && tid < pc.rows) {
         const int32_t* parents = p.parents ? p.parents + pc.row0 : nullptr;
@@ -463,33 +471,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           i = up;
         }
       }
-      named_sync(1, 256);
-      const int e_max = sm.exponent_max, e_min = sm.exponent_min;
+      int e_max = 0, e_min = 255;
+#pragma unroll
+      for (int k = 0; k < kKWarp; k++) {
+        e_max = max(e_max, sm.exponents[k].x);
+        e_min = min(e_min, sm.exponents[k].y);
+      }
       bool general = e_max - e_min > 15;
       const int common = min(13 + 127 - e_max, 126);
       const float f = p.scale_log2 * __uint_as_float((uint32_t)(127 - common) << 23);
-#pragma unroll 1
-      for (int i = 0; i < passes; i++) {
-        const int r = (tid >> 2) + 64 * i, part = tid & 3;
-        uint4 v[4];
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-          v[k] = r < pc.rows ? reinterpret_cast<const uint4*>(query(r))[k]
-                             : make_uint4(0u, 0u, 0u, 0u);
-        const int e = exponent(v);
-        const int shift = general && e >= 0 && e < 255 ? min(13 + 127 - e, 126) : common;
+      for (int i = 0; i < 2; i++) {
+        if (i == 1 && !two) continue;
+        const int r = (tid >> 2) + 64 * i, part = tid & 3;
+        const int shift = general && e[i] >= 0 && e[i] < 255 ? min(13 + 127 - e[i], 126) : common;
         const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
         unsigned char* dst = sm.q + (part >> 1) * kHalfBytes + r * 128;
 #pragma unroll
-        for (int k = 0; k < 4; k++)
+        for (int k = 0; k < 4; k++) {
+          const uint4 v = raw[i][k];
           *reinterpret_cast<uint4*>(dst + ((((part & 1) * 4 + k) ^ (r & 7)) << 4)) =
-              make_uint4(half_pair(bf16_lo(v[k].x) * up, bf16_hi(v[k].x) * up),
-                         half_pair(bf16_lo(v[k].y) * up, bf16_hi(v[k].y) * up),
-                         half_pair(bf16_lo(v[k].z) * up, bf16_hi(v[k].z) * up),
-                         half_pair(bf16_lo(v[k].w) * up, bf16_hi(v[k].w) * up));
+              make_uint4(half_pair(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
+                         half_pair(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                         half_pair(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
+                         half_pair(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+        }
         if (part == 0)
           sm.f[r] =
-              e == 255 ? NAN : p.scale_log2 * __uint_as_float((uint32_t)(127 - shift) << 23);
+              e[i] == 255 ? NAN : p.scale_log2 * __uint_as_float((uint32_t)(127 - shift) << 23);
       }
       fence_proxy_async();
       mbar_arrive(&sm.q_full);
@@ -766,52 +775,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_after();
 
       // ---- the rows' weights: thread t < 64 of each stream for the rows that it writes
-      struct alignas(16) Weights {  // (O0 a0 b0 + O1 a1 b1 + part before w) inv
-        float a0, b0, a1, b1, w, inv;
-        long long out;  // the output row
+      struct Weights {
+        float4 of[kStreamRows];  // (O0 x y + O1 z w + part before `front`) inv
+        float front[kStreamRows], inv[kStreamRows];
+        long long out[kStreamRows];  // the output row
       };
-      Weights* const weights = reinterpret_cast<Weights*>(sm.p[st]);
+      Weights& weights = *reinterpret_cast<Weights*>(sm.p[st]);
       const bool whole = pc.flags & kWhole, after = pc.flags & kAfter;
       const bool both = !two && pc.tiles > 1;
       float2* const pml = reinterpret_cast<float2*>(p.part_ml) + (size_t)pc.slot * kRows;
-      float* const po = p.part_o + (size_t)pc.slot * kRows * kHeadDim + t;
+      float* const po = p.part_o + ((size_t)pc.slot * kRows + base_row) * kHeadDim + t;
       float m = kLow, sum = 0.0f;
       if (t < rows) {
-        const int s0 = two ? st : 0;
+        const int s0 = two ? st : 0, r = base_row + t;
         auto total = [&](int s) {
           return ((sm.red[s][0][t] + sm.red[s][1][t]) + (sm.red[s][2][t] + sm.red[s][3][t])) *
                  sm.mx[s][t];
         };
         m = sm.m[s0][t];
         sum = total(s0);
-        Weights w = {sm.by[s0][t], sm.by[s0][t], 0.0f, 0.0f, 0.0f, 1.0f, 0};
+        float4 w = make_float4(sm.by[s0][t], sm.by[s0][t], 0.0f, 0.0f);
         if (both) {
           const float m0 = m, m1 = sm.m[1][t];
           m = fmaxf(m0, m1);
-          w.b0 *= ex2(m0 - m);
-          w.a1 = sm.by[1][t];
-          w.b1 = w.a1 * ex2(m1 - m);
+          w.y *= ex2(m0 - m);
+          w.z = sm.by[1][t];
+          w.w = w.z * ex2(m1 - m);
           sum = sum * ex2(m0 - m) + total(1) * ex2(m1 - m);
         }
-        const int r = base_row + t;
         if (sm.f[r] != sm.f[r]) sum = NAN;
         if (after) {
           const float2 was = __ldcg(pml + r);
-          const float top = fmaxf(m, was.x);
-          w.w = ex2(was.x - top);
-          const float keep = ex2(m - top);
-          w.b0 *= keep;
-          w.b1 *= keep;
-          sum = sum * keep + was.y * w.w;
+          const float top = fmaxf(m, was.x), keep = ex2(m - top), front = ex2(was.x - top);
+          weights.front[t] = front;
+          w.y *= keep;
+          w.w *= keep;
+          sum = sum * keep + was.y * front;
           m = top;
         }
-        w.out = (long long)(q_row + r / p.group) * p.hq + pc.h * p.group + r % p.group;
+        weights.of[t] = w;
         if (whole) {
-          w.inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+          const long long out =
+              (long long)(q_row + r / p.group) * p.hq + pc.h * p.group + r % p.group;
+          weights.out[t] = out * kHeadDim;
+          weights.inv[t] = sum != 0.0f ? 1.0f / sum : 0.0f;
           if (p.lse != nullptr && (two || st == 0))
-            p.lse[w.out] = (m - kHeadroom + log2f(sum)) * 0.693147180559945309f;
+            p.lse[out] = (m - kHeadroom + log2f(sum)) * 0.693147180559945309f;
         }
-        weights[t] = w;
       }
       if (after) named_sync(1, 256);  // both streams have read what is written now
       if (!whole && t < rows && (two || st == 0)) pml[base_row + t] = make_float2(m, sum);
@@ -821,19 +831,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int r0 = two ? 0 : 16 * st; r0 < rows; r0 += two || (r0 & 8) == 0 ? 8 : 24) {
         uint32_t x[8], y[8];
+        float v[8];
         load8(o0 + r0, x);
         if (both) load8(at + kColO + kStreamRows + r0, y);
         tc::wait_ld();
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-          const int r = r0 + k;
-          if (r >= rows) continue;
-          const Weights w = weights[r];
-          float v = __uint_as_float(x[k]) * w.a0 * w.b0;
-          if (both) v += __uint_as_float(y[k]) * w.a1 * w.b1;
-          if (after) v += __ldcg(po + (base_row + r) * kHeadDim) * w.w;
-          if (whole) p.out[w.out * kHeadDim + t] = __float2bfloat16(v * w.inv);
-          else po[(base_row + r) * kHeadDim] = v;
+          const float4 w = weights.of[r0 + k];
+          v[k] = __uint_as_float(x[k]) * w.x * w.y;
+          if (both) v[k] += __uint_as_float(y[k]) * w.z * w.w;
+        }
+        if (after) {
+          float was[8];
+#pragma unroll
+          for (int k = 0; k < 8; k++)
+            was[k] = r0 + k < rows ? __ldcg(po + (r0 + k) * kHeadDim) : 0.0f;
+#pragma unroll
+          for (int k = 0; k < 8; k++) v[k] += was[k] * weights.front[r0 + k];
+        }
+        if (whole) {
+#pragma unroll
+          for (int k = 0; k < 8; k++)
+            if (r0 + k < rows)
+              p.out[weights.out[r0 + k] + t] = __float2bfloat16(v[k] * weights.inv[r0 + k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; k++)
+            if (r0 + k < rows) po[(r0 + k) * kHeadDim] = v[k];
         }
       }
       // the block's parts are joined by the kernel behind this one
@@ -1131,53 +1155,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto over = [](long long a, long long by) {  // a / by (a division of 64 bits takes a microsecond)
       return ((a | by) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)by) : a / by;
     };
-    auto places = [&](int b) {  // of one row block
-      return token_tiles(len[b]) + kBlockCost;
+    auto places = [&](int b) { return token_tiles(len[b]) + kBlockCost; };  // of one row block
+    auto sequence = [&](int b) {  // of all its row blocks under all heads
+      return b < batch ? (long long)blocks[b] * p.hkv * places(b) : 0;
     };
-    auto blocks_of = [&](int n, int& most) {  // row blocks, their nodes
-      most = n > 0 ? nodes_a_block(n, p.block_nodes) : 1;
-      return (n + most - 1) / most;
+    // inclusive sums over 32 sequences
+    auto scan = [&](int b0) {
+      long long incl = sequence(b0 + lane);
+#pragma unroll 1
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      return incl;
     };
-    auto sequence = [&](int b) {  // places of a whole sequence
-      int most;
-      return (long long)blocks_of(num[b], most) * p.hkv * places(b);
-    };
-    long long all = 0;
-    for (int b = lane; b < batch; b += 32) all += sequence(b);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+    long long incl = scan(0), all = __shfl_sync(0xffffffffu, incl, 31);
+    for (int b0 = 32; b0 < batch; b0 += 32) all += __shfl_sync(0xffffffffu, scan(b0), 31);
     const long long per = max(over(all + gridDim.x - 1, gridDim.x), (long long)kMinPlaces);
     const long long begin = min(blockIdx.x * per, all), end = min(begin + per, all);
-    // the sequence that holds place `begin`
-    int b = 0;
-    long long before = 0;  // places in front of sequence b
-    if (begin < end) {
-      for (int b0 = 0;; b0 += 32) {
-        long long incl = b0 + lane < batch ? sequence(b0 + lane) : 0;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, incl, d);
-          if (lane >= d) incl += v;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, before + incl > begin);
-        if (past != 0 || b0 + 32 >= batch) {
-          const int i = past ? __ffs(past) - 1 : 31;
-          b = min(b0 + i, batch - 1);
-          before += i > 0 ? __shfl_sync(0xffffffffu, incl, max(i - 1, 0)) : 0;
-          break;
-        }
+    int b = 0, h = 0, q = 0, off = 0;
+    if (begin < end) {  // the sequence that holds place `begin`, and where in it that is
+      long long before = 0;  // places in front of the 32 sequences looked at
+      while (!__any_sync(0xffffffffu, before + incl > begin)) {
         before += __shfl_sync(0xffffffffu, incl, 31);
+        b += 32;
+        incl = scan(b);
       }
-    }
-    int most, blocks = blocks_of(num[b], most), one = places(b);
-    int h = 0, q = 0, off = 0;
-    if (begin < end) {
-      const long long at = begin - before, head = (long long)blocks * one;
+      const int i = __ffs(__ballot_sync(0xffffffffu, before + incl > begin)) - 1;
+      b += i;
+      before += __shfl_sync(0xffffffffu, incl, i) - sequence(b);
+      const int one = places(b);
+      const long long at = begin - before, head = (long long)blocks[b] * one;
       h = (int)over(at, head);
-      const int rest = (int)(at - h * head);
+      const unsigned rest = (unsigned)(at - h * head);
       q = rest / one;
       off = rest % one;
     }
+    int one = places(b);
     long long x = begin;
     int told = 0;
     auto tell = [&](const Piece& piece) {
@@ -1203,7 +1217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Piece piece = {};
       piece.tile = max(off - kBlockCost, 0);
       piece.tiles = max(stop - kBlockCost, 0) - piece.tile;
-      const int nodes = min(most, num[b] - q * most);
+      const int most = block_nodes[b], nodes = min(most, num[b] - q * most);
       piece.rows = nodes * p.group;
       const int limit = piece.rows > kStreamRows ? kMaxSteps : 2 * kMaxSteps;
       const bool cut = piece.tiles > limit;  // the rest of the stretch is the next piece
@@ -1232,16 +1246,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       off = stop;
       if (!cut) {
         off = 0;
-        if (++q == blocks) {
+        if (++q == blocks[b]) {
           q = 0;
           if (++h == p.hkv) {
             h = 0;
             do b++;
             while (b < batch && num[b] == 0);
-            if (b < batch) {
-              blocks = blocks_of(num[b], most);
-              one = places(b);
-            }
+            if (b < batch) one = places(b);
           }
         }
       }
@@ -1389,8 +1400,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_tree_join_kernel(const Jo
   }
 }
 
-size_t smem_bytes(int batch) { return 1024 + sizeof(Smem) + 12 * (size_t)batch; }
-static_assert(1024 + sizeof(Smem) + 12 * 1024 <= 227 * 1024, "shared memory for the largest batch");
+size_t smem_bytes(int batch) { return 1024 + sizeof(Smem) + 20 * (size_t)batch; }
+static_assert(1024 + sizeof(Smem) + 20 * 1024 <= 227 * 1024, "shared memory for the largest batch");
 
 }  // namespace
 
