@@ -67,8 +67,10 @@ constexpr float kHeadroom = 7.0f, kLag = 8.0f;  // P up to 2^15
 constexpr float kPlainScale = 40.0f; // largest |log2 s_v| of the plain form
 constexpr float kTiny = 1e-37f;      // smallest factor of a score: a masked -inf stays one
 constexpr float kLow = -1e30f;       // a maximum before any score
-constexpr int kBlockCost = 4;        // what a row block costs beside its tiles, in tiles
-constexpr int kMinPlaces = 2;        // shortest slice
+// Places on the line of steps (see the plan): a tile's, with one stream on it and with two, a row
+// block's beside its tiles, and the shortest slice.
+constexpr int kTilePlaces = 2, kTwoPlaces = 3, kBlockPlaces = 22, kMinPlaces = 4;
+static_assert(kMinPlaces >= kTwoPlaces, "no slice without the first place of a tile");
 // O takes the products of at most this many steps: their own sums round to zero, 2^-23 a product
 constexpr int kMaxSteps = 256;
 // of a step: a block without tokens; an s_v that the plain form does not take
@@ -1150,12 +1152,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&full[i % kStages], i / kStages & 1);
   } else if (warp == kPlanWarp) {
     // ============================================ the plan: this CTA's slice of the line of steps
-    // A row block's places on the line are kBlockCost for what it costs beside its tiles, then one a
-    // tile; the pieces are told in order.
+    // All steps of all row blocks, under all heads, of all sequences, in equal slices. A row block has
+    // kBlockPlaces for what it costs beside its tiles, then each tile's; a tile is the CTA's that has
+    // its first place. The pieces are told in order.
     auto over = [](long long a, long long by) {  // a / by (a division of 64 bits takes a microsecond)
       return ((a | by) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)by) : a / by;
     };
-    auto places = [&](int b) { return token_tiles(len[b]) + kBlockCost; };  // of one row block
+    auto each = [&](int b) {  // places of a tile
+      return block_nodes[b] * p.group > kStreamRows ? kTwoPlaces : kTilePlaces;
+    };
+    auto places = [&](int b) {  // of one row block
+      return token_tiles(len[b]) * each(b) + kBlockPlaces;
+    };
     auto sequence = [&](int b) {  // of all its row blocks under all heads
       return b < batch ? (long long)blocks[b] * p.hkv * places(b) : 0;
     };
@@ -1210,20 +1218,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     if (lane == 0) p.records[blockIdx.x].rows = 0;
     while (ok && x < end) {
-      const long long block_begin = x - off, tiles_begin = block_begin + kBlockCost;
-      const int all_tiles = one - kBlockCost;
-      const long long tiles_end = tiles_begin + all_tiles;
+      const long long block_begin = x - off, tiles_begin = block_begin + kBlockPlaces;
+      const int tile_places = each(b), all_tiles = token_tiles(len[b]);
+      auto tile_at = [&](int place) {  // the first tile from this place of the row block on
+        return (max(place - kBlockPlaces, 0) + tile_places - 1) / tile_places;
+      };
+      const long long last_begin = tiles_begin + (long long)(all_tiles - 1) * tile_places;
       int stop = (int)min((long long)one, off + (end - x));
       Piece piece = {};
-      piece.tile = max(off - kBlockCost, 0);
-      piece.tiles = max(stop - kBlockCost, 0) - piece.tile;
+      piece.tile = tile_at(off);
+      piece.tiles = min(tile_at(stop), all_tiles) - piece.tile;
       const int most = block_nodes[b], nodes = min(most, num[b] - q * most);
       piece.rows = nodes * p.group;
       const int limit = piece.rows > kStreamRows ? kMaxSteps : 2 * kMaxSteps;
       const bool cut = piece.tiles > limit;  // the rest of the stretch is the next piece
       if (cut) {
         piece.tiles = limit;
-        stop = piece.tile + limit + kBlockCost;
+        stop = (piece.tile + limit) * tile_places + kBlockPlaces;
       }
       if (piece.tiles > 0) {
         piece.b = b;
@@ -1232,14 +1243,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         piece.start = len[b] - num[b];
         piece.node = q * most;
         piece.row0 = row0[b];
-        const bool after = piece.tile > 0 && tiles_begin + piece.tile > begin;
-        const bool whole = !cut && begin <= tiles_begin && tiles_end <= end;
+        const bool after =
+            piece.tile > 0 && tiles_begin + (piece.tile - 1) * tile_places >= begin;
+        const bool whole = !cut && begin <= tiles_begin && last_begin < end;
         const int c0 = (int)over(tiles_begin, per);
         piece.flags = (whole ? kWhole : 0) | (after ? kAfter : 0) | (cut ? kBefore : 0) |
                       (!whole && !cut && tiles_begin >= begin ? kRecord : 0) |
                       (num[b] > nodes ? kShared : 0);
         piece.slot = 2 * blockIdx.x + (begin < block_begin ? 1 : 0);
-        piece.parts = (int)over(tiles_end - 1, per) - c0 + 1;
+        piece.parts = (int)over(last_begin, per) - c0 + 1;
         ok = tell(piece);
       }
       x += stop - off;
