@@ -29,39 +29,41 @@ __device__ __forceinline__ float max_abs3(float m, float a, float b) {
   return y;
 }
 
-// The codes of one block from its new values: lane l has, of tokens 2 i + l / 16 (i = 0 .. 7),
+// The codes of one block from its new values: lane l has, of tokens t0 + 2 i + l / 16 (i < N),
 // channels a .. a + 3 (x[i][0..3]) and b .. b + 3; slots [first, last) are new, x is zero in the
-// others. `codes` points at the block. kRow: b = a + 4.
-template <int F, bool kRow>
-__device__ __forceinline__ void put_block(float (&x)[8][8], int first, int last, uint8_t* codes,
-                                          float* scale, int a, int b, int lane) {
+// others. `codes` points at the block. kRow: b = a + 4. most(v): the largest of the v of the warps
+// that share the block; it orders their reads of the block before their writes.
+template <int F, bool kRow, int N, typename Most>
+__device__ __forceinline__ void put_block(float (&x)[N][8], int t0, int first, int last,
+                                          uint8_t* codes, float* scale, int a, int b, int lane,
+                                          Most most) {
   const float s_old = *scale;
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; i++)
+  for (int i = 0; i < N; i++)
 #pragma unroll
     for (int k = 0; k < 8; k += 2) m = max_abs3(m, x[i][k], x[i][k + 1]);
   // as bits, infinities and NaN above every number
-  uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7FFFFFFFu);
+  uint32_t top = most(__reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7FFFFFFFu));
   const bool odd_values = top >= 0x7F800000u;
   if (odd_values) {  // the maximum of the finite ones
     m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; i++)
+    for (int i = 0; i < N; i++)
 #pragma unroll
       for (int k = 0; k < 8; k++) {
         const float v = fabsf(x[i][k]);
         if (v <= 3.402823466e38f) m = fmaxf(m, v);
       }
-    top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    top = most(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
   }
   float s = __fdiv_rn(__uint_as_float(top), levels<F>());
   if (s < 1.17549435e-38f) s = 0.0f;
   if (first > 0) s = fmaxf(s_old, s);
   const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
-  const int sub = lane >> 4;
-  uint8_t* const at_a = codes + sub * kHeadDim + a;
-  uint8_t* const at_b = codes + sub * kHeadDim + b;
+  const int token = t0 + (lane >> 4);  // of i = 0
+  uint8_t* const at_a = codes + token * kHeadDim + a;
+  uint8_t* const at_b = codes + token * kHeadDim + b;
   auto store = [&](int i, uint32_t lo, uint32_t hi) {
     if constexpr (kRow) {
       *reinterpret_cast<uint2*>(at_a + 2 * i * kHeadDim) = make_uint2(lo, hi);
@@ -73,8 +75,8 @@ __device__ __forceinline__ void put_block(float (&x)[8][8], int first, int last,
   if (first > 0 && s > s_old) {  // the older tokens' codes under the larger scale
     const float ratio = __fmul_rn(s_old, inv);
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      if (2 * i + sub >= first) continue;
+    for (int i = 0; i < N; i++) {
+      if (token + 2 * i >= first) continue;
       float f[8];
       values4<F>(*reinterpret_cast<const uint32_t*>(at_a + 2 * i * kHeadDim), f);
       values4<F>(*reinterpret_cast<const uint32_t*>(at_b + 2 * i * kHeadDim), f + 4);
@@ -82,8 +84,8 @@ __device__ __forceinline__ void put_block(float (&x)[8][8], int first, int last,
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const int slot = 2 * i + sub;
+  for (int i = 0; i < N; i++) {
+    const int slot = token + 2 * i;
     if (slot < first || slot >= last) continue;
     float by = inv;
     if (odd_values) {
@@ -94,7 +96,7 @@ __device__ __forceinline__ void put_block(float (&x)[8][8], int first, int last,
     store(i, codes4<F>(x[i][0], x[i][1], x[i][2], x[i][3], by),
           codes4<F>(x[i][4], x[i][5], x[i][6], x[i][7], by));
   }
-  if (lane == 0) *scale = s;
+  if (lane == 0 && t0 == 0) *scale = s;
 }
 
 struct WriteSide {
@@ -104,18 +106,21 @@ struct WriteSide {
   float* scale;
 };
 
-// Units: blocks x heads x (K, V), then (row, 16 query heads); one warp behind them reports
-// sequences that do not fit.
+// Units: blocks x heads x (K, V) x halves, then (row, 16 query heads); one warp behind them reports
+// sequences that do not fit. Two warps share a block, eight tokens each, and meet over its maximum:
+// with a warp a block, 64 fp32 values a lane, 16 warps fit an SM and 123K tokens' keys and values
+// took 200 us beside the queries' 300; with 32 values a lane @.
 template <int F, bool kNeighbours>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+__global__ void __launch_bounds__(kWarps * 32, 4)
     kv8_write_rotated_kernel(const NewRows rows, const Rotary rot, const WriteSide ks,
                              const WriteSide vs, const RowSide qs,
                              const int32_t* __restrict__ page_table, int hkv, int num_pages,
                              int block_units, int units, int* err) {
+  __shared__ uint32_t tops[2][kWarps];
   grid_dep_wait();
   grid_dep_launch();
-  const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int unit = blockIdx.x * kWarps + warp;
   if (unit == units) report_bad(rows, lane, err);
   if (unit >= units) return;
   if (unit >= block_units) {  // queries
@@ -134,8 +139,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     turn_row<kNeighbours>(qs, rot, row, part * kRowHeads, position, lane);
     return;
   }
-  const bool is_v = unit & 1;
-  const int h = (unit >> 1) % hkv, item = (unit >> 1) / hkv;
+  const int t0 = 8 * (unit & 1);
+  const bool is_v = unit >> 1 & 1;
+  const int h = (unit >> 2) % hkv, item = (unit >> 2) / hkv;
   const int b =
       rows.cu ? warp_search(rows.batch, item, lane, [&](int i) { return item_base(rows, i); })
               : item;
@@ -156,35 +162,41 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     if (rot.positions) position = rot.positions[row + lane];
     bad = bad || position < 0 || position >= rot.rows;
   }
-  if (__any_sync(0xffffffffu, bad)) {
+  if (__any_sync(0xffffffffu, bad)) {  // (both warps of a block alike)
     if (lane == 0) set_error(err, kDevErrCheck);
     return;
   }
+  int turn_of = 0;
+  auto most = [&](uint32_t v) {  // of the block's two warps
+    if (lane == 0) tops[turn_of][warp] = v;
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+    return max(v, tops[turn_of++][warp ^ 1]);
+  };
   const size_t block = (size_t)page * hkv + h;
-  const int sub = lane >> 4, l16 = lane & 15;
-  float x[8][8];
+  const int token = t0 + (lane >> 4), l16 = lane & 15;
+  float x[4][8];
   if (is_v) {
-    const __nv_bfloat16* src = vs.x + (row + sub) * vs.stride + h * kHeadDim + 8 * l16;
-    uint4 raw[8];
+    const __nv_bfloat16* src = vs.x + (row + token) * vs.stride + h * kHeadDim + 8 * l16;
+    uint4 raw[4];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const int slot = 2 * i + sub;
+    for (int i = 0; i < 4; i++) {
+      const int slot = token + 2 * i;
       raw[i] = make_uint4(0u, 0u, 0u, 0u);
       if (slot >= first && slot < last) raw[i] = ldg128_nc(src + 2 * i * vs.stride);
     }
 #pragma unroll
-    for (int i = 0; i < 8; i++)
+    for (int i = 0; i < 4; i++)
       unpack(make_uint2(raw[i].x, raw[i].y), make_uint2(raw[i].z, raw[i].w), x[i]);
-    put_block<F, true>(x, first, last, vs.codes + block * kBlockBytesI8, vs.scale + block,
-                       8 * l16, 8 * l16 + 4, lane);
+    put_block<F, true>(x, t0, first, last, vs.codes + block * kBlockBytesI8, vs.scale + block,
+                       8 * l16, 8 * l16 + 4, lane, most);
     return;
   }
   const Place pl = place<kNeighbours>(l16, rot.dim);
-  const __nv_bfloat16* src = ks.x + (row + sub) * ks.stride + h * kHeadDim;
-  uint2 u[8], v[8];
+  const __nv_bfloat16* src = ks.x + (row + token) * ks.stride + h * kHeadDim;
+  uint2 u[4], v[4];
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const int slot = 2 * i + sub;
+  for (int i = 0; i < 4; i++) {
+    const int slot = token + 2 * i;
     u[i] = v[i] = make_uint2(0u, 0u);
     if (slot >= first && slot < last) {
       u[i] = load4(src + 2 * i * ks.stride + pl.a);
@@ -192,14 +204,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const int slot = 2 * i + sub;
+  for (int i = 0; i < 4; i++) {
+    const int slot = token + 2 * i;
     const int at = __shfl_sync(0xffffffffu, position, slot);
     unpack(u[i], v[i], x[i]);
     if (pl.turns && slot >= first && slot < last) turn<kNeighbours>(x[i], angles(rot, at, l16));
   }
-  put_block<F, kNeighbours>(x, first, last, ks.codes + block * kBlockBytesI8, ks.scale + block,
-                            pl.a, pl.b, lane);
+  put_block<F, kNeighbours>(x, t0, first, last, ks.codes + block * kBlockBytesI8, ks.scale + block,
+                            pl.a, pl.b, lane, most);
 }
 
 // ------------------------------------------------------------- the accepted branch into place
@@ -297,8 +309,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_keep_kernel(const KeepArgs p)
     }
     // (the maximum over the lanes orders all their reads before the first write)
     const size_t to = (size_t)to_page * p.hkv + h;
-    put_block<F, true>(x, first, last, codes + to * kBlockBytesI8, scale + to, 8 * l16,
-                       8 * l16 + 4, lane);
+    put_block<F, true>(x, 0, first, last, codes + to * kBlockBytesI8, scale + to, 8 * l16,
+                       8 * l16 + 4, lane, [](uint32_t v) { return v; });
     __syncwarp();
   }
 }
@@ -320,7 +332,7 @@ cudaError_t launch_kv8_write_rotated(const Shape& s, const Kv8& c, const RotaryT
                         static_cast<uint8_t*>(c.v), c.v_scale};
   const RowSide qs = {static_cast<const __nv_bfloat16*>(q), q_stride,
                       static_cast<__nv_bfloat16*>(q_out), q_out_stride, q ? s.hq : 0};
-  const int block_units = new_block_items(s.batch, total, cu != nullptr) * s.hkv * 2;
+  const int block_units = new_block_items(s.batch, total, cu != nullptr) * s.hkv * 4;
   const int units = block_units + total * row_units(qs.heads);
   auto kernel = kv8_write_rotated_kernel<kInt8, false>;
   if (c.format == kE4m3)

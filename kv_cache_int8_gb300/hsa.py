@@ -113,6 +113,20 @@ class Dims:
     key_fp8: int = 0  # 1: FP8 E4M3 key codes (8-bit layout), fp32 scores
     cache_policy: int = 0  # block cache victims: 0 least recently used, 1 least cumulative mass
 
+    def __setattr__(self, name, value):
+        self.__dict__.pop("_ref", None)
+        object.__setattr__(self, name, value)
+
+    def __getstate__(self):  # (copies and pickles make their own)
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+
+    def ref(self):
+        """A reference to the C struct, kept until a field is set."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = self.__dict__["_ref"] = ctypes.byref(self.c())
+        return r
+
     def c(self) -> hsa_dims:
         """The C struct, built once per set of field values (every call of a step passes it)."""
         key = (self.batch, self.hq, self.hkv, self.head_dim, self.page_size,
@@ -195,12 +209,13 @@ def _p(t) -> Optional[int]:
 
 
 _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream=None) -> int:
     if stream is None:
         if _RAW_STREAM is not None:  # the current stream's handle without a Stream object
-            return _RAW_STREAM(torch.cuda.current_device())
+            return _RAW_STREAM(_DEVICE())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -534,7 +549,7 @@ def hsa_kv8_write(d: Dims, cache: KV8, k_new, v_new, cu_tokens, page_table, seq_
     rows, k_stride, v_stride = _row_pair(name, k_new, v_new, d.hkv)
     cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
     rc = load().hsa_kv8_write(
-        ctypes.byref(d.c()), _cache(name, d, cache), k_new.data_ptr(), k_stride, v_new.data_ptr(),
+        d.ref(), _cache(name, d, cache), k_new.data_ptr(), k_stride, v_new.data_ptr(),
         v_stride, cu, rows, table, lens, _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check(name, rc)
@@ -547,7 +562,7 @@ def hsa_kv8_read(d: Dims, cache: KV8, k_out, v_out, cu_tokens, page_table, seq_l
     rows, k_stride, v_stride = _row_pair(name, k_out, v_out, d.hkv)
     cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
     rc = load().hsa_kv8_read(
-        ctypes.byref(d.c()), _cache(name, d, cache), k_out.data_ptr(), k_stride, v_out.data_ptr(),
+        d.ref(), _cache(name, d, cache), k_out.data_ptr(), k_stride, v_out.data_ptr(),
         v_stride, cu, rows, table, lens, _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check(name, rc)
@@ -560,7 +575,7 @@ def hsa_kv8_decode(d: Dims, cache: KV8, q, page_table, seq_lens, out, lse, ws,
     name = "hsa_kv8_decode"
     q, out, lse = _heads(name, d, q, out, lse)
     _, table, lens = _lists(name, d, None, page_table, seq_lens)
-    rc = load().hsa_kv8_decode(ctypes.byref(d.c()), _cache(name, d, cache), q, table, lens, out,
+    rc = load().hsa_kv8_decode(d.ref(), _cache(name, d, cache), q, table, lens, out,
                                lse, _p(ws), ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check(name, rc)
@@ -572,7 +587,7 @@ def hsa_kv8_attend(d: Dims, cache: KV8, q, page_table, seq_lens, block_idx, n_bl
     name = "hsa_kv8_attend"
     q, out, lse = _heads(name, d, q, out, lse)
     _, table, lens = _lists(name, d, None, page_table, seq_lens)
-    rc = load().hsa_kv8_attend(ctypes.byref(d.c()), _cache(name, d, cache), q, table, lens,
+    rc = load().hsa_kv8_attend(d.ref(), _cache(name, d, cache), q, table, lens,
                                _list(name, block_idx), _list(name, n_blocks), out, lse, _p(ws),
                                ws.numel(), _stream(stream))
     if rc != HSA_OK:
@@ -590,7 +605,7 @@ def hsa_kv8_prefill(d: Dims, cache: KV8, q, cu_tokens, page_table, seq_lens, out
     lse = _dense(name, "lse", lse, torch.float32, rows * d.hq)
     cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
     rc = load().hsa_kv8_prefill(
-        ctypes.byref(d.c()), _cache(name, d, cache), q.data_ptr(), q_stride, cu, rows, table, lens,
+        d.ref(), _cache(name, d, cache), q.data_ptr(), q_stride, cu, rows, table, lens,
         out.data_ptr(), lse, _p(ws), ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check(name, rc)
@@ -631,12 +646,22 @@ def _row_list(name: str, what: str, t, rows: int) -> Optional[int]:
     return t.data_ptr()
 
 
-def _same_rows(name: str, x, y, heads: int):
-    """(rows, row stride of x, of y) of an input and its output of as many rows."""
-    if x is None or y is None or x.shape != y.shape:
-        raise HsaError(name, HSA_ERR_INVALID_ARG, "an output has its input's shape")
-    rows, xs = _rows(name, x, heads)
-    return rows, xs, _rows(name, y, heads)[1]
+def _turned_rows(name: str, x, y, heads: int):
+    """(rows, row stride of x, of y) of bf16 rows [tokens][heads][128] and their output."""
+    try:
+        shape, xs, ys = x.shape, x.stride(), y.stride()
+        tokens, h, channels = shape
+        good = (x.dtype is torch.bfloat16 and y.dtype is torch.bfloat16 and y.shape == shape and
+                h == heads and channels == 128 and xs[2] == 1 and ys[2] == 1 and
+                (h == 1 or (xs[1] == 128 and ys[1] == 128)))
+    except (AttributeError, ValueError):  # None, other dimensions
+        good = False
+    if not good:
+        raise HsaError(name, HSA_ERR_INVALID_ARG,
+                       f"rows and their output must be bf16 [tokens][{heads}][128], rows contiguous")
+    if tokens < 2:  # a single row's stride means nothing
+        return tokens, h * 128, h * 128
+    return tokens, xs[0], ys[0]
 
 
 def hsa_rotate(d: Dims, rotary: Rotary, q, q_out, k, k_out, positions=None, cu_tokens=None,
@@ -645,18 +670,22 @@ def hsa_rotate(d: Dims, rotary: Rotary, q, q_out, k, k_out, positions=None, cu_t
     rows contiguous (any row stride), an output may be its input. positions: int32 [total_tokens],
     or None: the tokens' places by seq_lens and cu_tokens."""
     name = "hsa_rotate"
-    rows, qs, qos = _same_rows(name, q, q_out, d.hq)
-    if (k is None) != (k_out is None):
-        raise HsaError(name, HSA_ERR_INVALID_ARG, "k and k_out go together")
+    rows, qs, qos = _turned_rows(name, q, q_out, d.hq)
+    k_at = k_out_at = None
     ks = kos = 0
-    if k is not None:
-        n, ks, kos = _same_rows(name, k, k_out, d.hkv)
+    if k is not None or k_out is not None:
+        n, ks, kos = _turned_rows(name, k, k_out, d.hkv)
         if n != rows:
             raise HsaError(name, HSA_ERR_INVALID_ARG, "q and k must have as many rows")
+        k_at, k_out_at = k.data_ptr(), k_out.data_ptr()
+    if positions is not None:
+        positions = _row_list(name, "positions", positions, rows)
+    if cu_tokens is not None:
+        cu_tokens = _offsets(name, d, cu_tokens)
     rc = load().hsa_rotate(
-        ctypes.byref(d.c()), rotary._ref, q.data_ptr(), qs, q_out.data_ptr(), qos, _p(k), ks,
-        _p(k_out), kos, _row_list(name, "positions", positions, rows), _offsets(name, d, cu_tokens),
-        rows, _list(name, seq_lens), _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
+        d.ref(), rotary._ref, q.data_ptr(), qs, q_out.data_ptr(), qos, k_at, ks,
+        k_out_at, kos, positions, cu_tokens, rows, _list(name, seq_lens), _p(ws),
+        0 if ws is None else ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check(name, rc)
 
@@ -667,19 +696,20 @@ def hsa_kv8_write_rotated(d: Dims, cache: KV8, rotary: Rotary, q, q_out, k_new, 
     None; rows contiguous (any row stride). positions: as hsa_rotate."""
     name = "hsa_kv8_write_rotated"
     rows, k_stride, v_stride = _row_pair(name, k_new, v_new, d.hkv)
-    if (q is None) != (q_out is None):
-        raise HsaError(name, HSA_ERR_INVALID_ARG, "q and q_out go together")
+    q_at = q_out_at = None
     qs = qos = 0
-    if q is not None:
-        n, qs, qos = _same_rows(name, q, q_out, d.hq)
+    if q is not None or q_out is not None:
+        n, qs, qos = _turned_rows(name, q, q_out, d.hq)
         if n != rows:
             raise HsaError(name, HSA_ERR_INVALID_ARG, "q and k must have as many rows")
+        q_at, q_out_at = q.data_ptr(), q_out.data_ptr()
+    if positions is not None:
+        positions = _row_list(name, "positions", positions, rows)
     cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
     rc = load().hsa_kv8_write_rotated(
-        ctypes.byref(d.c()), _cache(name, d, cache), rotary._ref, _p(q), qs, _p(q_out), qos,
-        k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
-        _row_list(name, "positions", positions, rows), cu, rows, table, lens, _p(ws),
-        0 if ws is None else ws.numel(), _stream(stream))
+        d.ref(), _cache(name, d, cache), rotary._ref, q_at, qs, q_out_at, qos,
+        k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride, positions, cu, rows, table, lens,
+        _p(ws), 0 if ws is None else ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check(name, rc)
 
@@ -694,7 +724,7 @@ def hsa_kv8_tree(d: Dims, cache: KV8, q, parents, cu_tokens, page_table, seq_len
     lse = _dense(name, "lse", lse, torch.float32, rows * d.hq)
     cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
     rc = load().hsa_kv8_tree(
-        ctypes.byref(d.c()), _cache(name, d, cache), q.data_ptr(), q_stride,
+        d.ref(), _cache(name, d, cache), q.data_ptr(), q_stride,
         _row_list(name, "parents", parents, rows), cu, rows, table, lens, out.data_ptr(), lse,
         _p(ws), ws.numel(), _stream(stream))
     if rc != HSA_OK:
@@ -712,7 +742,7 @@ def hsa_kv8_keep(d: Dims, cache: KV8, keep_idx, n_keep, cu_tokens, page_table, s
                        "keep_idx must be contiguous torch.int32 [batch][most kept]")
     cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
     rc = load().hsa_kv8_keep(
-        ctypes.byref(d.c()), _cache(name, d, cache), keep_idx.data_ptr(), keep_idx.shape[1],
+        d.ref(), _cache(name, d, cache), keep_idx.data_ptr(), keep_idx.shape[1],
         _row_list(name, "n_keep", n_keep, d.batch), cu, table, lens,
         _row_list(name, "new_lens", new_lens, d.batch), _p(ws), 0 if ws is None else ws.numel(),
         _stream(stream))
