@@ -1274,10 +1274,8 @@ int32_t hsa_kv8_write_rotated(const hsa_dims* d, const hsa_kv8* cache, const hsa
   if (rc == HSA_OK && q && q == q_out && q_stride != q_out_stride) rc = HSA_ERR_INVALID_ARG;
   if (rc == HSA_OK) rc = error_word(workspace, workspace_bytes, &err);
   if (rc != HSA_OK) return rc;
-  // work items: half blocks x heads x K and V, and a row and 16 query heads
-  if (((long long)total_tokens / hsa::kPage + 2 * s.batch) * s.hkv * 4 > INT32_MAX / 4 ||
-      (long long)total_tokens * ((s.hq + 15) / 16) > INT32_MAX / 4)
-    return HSA_ERR_UNSUPPORTED;
+  // work items: check_rows counts the blocks'; a row and 16 query heads the others
+  if ((long long)total_tokens * ((s.hq + 15) / 16) > INT32_MAX / 4) return HSA_ERR_UNSUPPORTED;
   return cuda_status(hsa::launch_kv8_write_rotated(
       s, c, t, q, q_stride, q_out, q_out_stride, k_new, k_stride, v_new, v_stride, positions,
       cu_tokens, total_tokens, page_table, seq_lens, err, as_stream(stream)));

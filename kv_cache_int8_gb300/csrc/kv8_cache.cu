@@ -46,7 +46,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_write_kernel(
   const bool is_v = unit & 1;
   const int h = (unit >> 1) % hkv, item = (unit >> 1) / hkv;
   const WriteSide& w = is_v ? vs : ks;
-  const int b = rows.cu ? item_sequence(rows, item) : item;
+  const int b = rows.cu ? item_sequence(rows, item, lane) : item;
+  if (b < 0) return;
   const NewSpan sp = new_span(rows, b);
   const int j = rows.cu ? item - item_base(rows, b) : 0;
   const int end = sp.start + sp.n;  // N_b
@@ -161,7 +162,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_read_kernel(
   const bool is_v = unit & 1;
   const int h = (unit >> 1) % hkv, item = (unit >> 1) / hkv;
   const ReadSide& r = is_v ? vs : ks;
-  const int b = rows.cu ? item_sequence(rows, item) : item;
+  const int b = rows.cu ? item_sequence(rows, item, lane) : item;
+  if (b < 0) return;
   const NewSpan sp = new_span(rows, b);
   const int j = rows.cu ? item - item_base(rows, b) : 0;
   const int end = sp.start + sp.n;

@@ -10,6 +10,8 @@
 // registers between the maximum and the codes, here in fp32: a rotated key is quantised as it is
 // computed, not rounded to bf16 in between (that would add 2^-9 of a value to half a code step,
 // 2^-8 of the block's largest). The queries of the same tokens turn in the same launch.
+#include <type_traits>
+
 #include "internal.h"
 #include "kv8.cuh"
 #include "rotary.cuh"
@@ -31,13 +33,13 @@ __device__ __forceinline__ float max_abs3(float m, float a, float b) {
 
 // The codes of one block from its new values: lane l has, of tokens t0 + 2 i + l / 16 (i < N),
 // channels a .. a + 3 (x[i][0..3]) and b .. b + 3; slots [first, last) are new, x is zero in the
-// others. `codes` points at the block. kRow: b = a + 4. most(v): the largest of the v of the warps
+// others. `codes` points at the block, s_old is its scale (read before: it is one load less on the
+// way). kRow: b = a + 4. most(v): the largest of the v of the warps
 // that share the block; it orders their reads of the block before their writes.
 template <int F, bool kRow, int N, typename Most>
 __device__ __forceinline__ void put_block(float (&x)[N][8], int t0, int first, int last,
-                                          uint8_t* codes, float* scale, int a, int b, int lane,
-                                          Most most) {
-  const float s_old = *scale;
+                                          uint8_t* codes, float s_old, float* scale, int a, int b,
+                                          int lane, Most most) {
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; i++)
@@ -106,17 +108,22 @@ struct WriteSide {
   float* scale;
 };
 
-// Units: blocks x heads x (K, V) x halves, then (row, 16 query heads); one warp behind them reports
-// sequences that do not fit. Two warps share a block, eight tokens each, and meet over its maximum:
-// with a warp a block, 64 fp32 values a lane, 16 warps fit an SM and 123K tokens' keys and values
-// took 200 us beside the queries' 300; with 32 values a lane @.
-template <int F, bool kNeighbours>
-__global__ void __launch_bounds__(kWarps * 32, 4)
+// Units: blocks x heads x halves, then (row, 16 query heads); one warp behind them reports sequences
+// that do not fit. Two warps share a block of K and of V, eight tokens each, and meet over its
+// maxima. A unit's way to its data (sequence, length, page, rows) is four loads one after the other,
+// so what is then under way at once decides: 123K new tokens' keys and values, queries aside, took
+// 200 us with a warp a block of K or V and 16 tokens (16 warps an SM), 188 with two warps, 175 with
+// both K and V of a block in a warp. kSplit: units of K and of V apart, for a token a sequence of few
+// sequences, where the one behind the other only takes longer (one sequence of 8 kv heads 2.9 us a
+// call, not 3.4; 256 sequences 8.1, not 6.3, as the warps no longer fit the GPU at once).
+constexpr int kSplitUnits = 2048;  // 13 warps an SM, of 24
+template <int F, bool kNeighbours, bool kSplit>
+__global__ void __launch_bounds__(kWarps * 32, 3)
     kv8_write_rotated_kernel(const NewRows rows, const Rotary rot, const WriteSide ks,
                              const WriteSide vs, const RowSide qs,
                              const int32_t* __restrict__ page_table, int hkv, int num_pages,
                              int block_units, int units, int* err) {
-  __shared__ uint32_t tops[2][kWarps];
+  __shared__ uint32_t tops[4][kWarps];
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -140,11 +147,9 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     return;
   }
   const int t0 = 8 * (unit & 1);
-  const bool is_v = unit >> 1 & 1;
-  const int h = (unit >> 2) % hkv, item = (unit >> 2) / hkv;
-  const int b =
-      rows.cu ? warp_search(rows.batch, item, lane, [&](int i) { return item_base(rows, i); })
-              : item;
+  const int pair = kSplit ? unit >> 2 : unit >> 1, h = pair % hkv, item = pair / hkv;
+  const bool do_k = !kSplit || !(unit & 2), do_v = !kSplit || (unit & 2);
+  const int b = rows.cu ? item_sequence(rows, item, lane) : item;
   if (b < 0) return;
   const NewSpan sp = new_span(rows, b);
   const int j = rows.cu ? item - item_base(rows, b) : 0;
@@ -173,45 +178,47 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     return max(v, tops[turn_of++][warp ^ 1]);
   };
   const size_t block = (size_t)page * hkv + h;
+  const float k_old = first > 0 ? __ldcg(ks.scale + block) : 0.0f;
+  const float v_old = first > 0 ? __ldcg(vs.scale + block) : 0.0f;
   const int token = t0 + (lane >> 4), l16 = lane & 15;
-  float x[4][8];
-  if (is_v) {
-    const __nv_bfloat16* src = vs.x + (row + token) * vs.stride + h * kHeadDim + 8 * l16;
-    uint4 raw[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int slot = token + 2 * i;
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (slot >= first && slot < last) raw[i] = ldg128_nc(src + 2 * i * vs.stride);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-      unpack(make_uint2(raw[i].x, raw[i].y), make_uint2(raw[i].z, raw[i].w), x[i]);
-    put_block<F, true>(x, t0, first, last, vs.codes + block * kBlockBytesI8, vs.scale + block,
-                       8 * l16, 8 * l16 + 4, lane, most);
-    return;
-  }
   const Place pl = place<kNeighbours>(l16, rot.dim);
-  const __nv_bfloat16* src = ks.x + (row + token) * ks.stride + h * kHeadDim;
+  const __nv_bfloat16* k_src = ks.x + (row + token) * ks.stride + h * kHeadDim;
+  const __nv_bfloat16* v_src = vs.x + (row + token) * vs.stride + h * kHeadDim + 8 * l16;
   uint2 u[4], v[4];
+  uint4 raw[4];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     const int slot = token + 2 * i;
     u[i] = v[i] = make_uint2(0u, 0u);
-    if (slot >= first && slot < last) {
-      u[i] = load4(src + 2 * i * ks.stride + pl.a);
-      v[i] = load4(src + 2 * i * ks.stride + pl.b);
+    if (do_k && slot >= first && slot < last) {
+      u[i] = load4(k_src + 2 * i * ks.stride + pl.a);
+      v[i] = load4(k_src + 2 * i * ks.stride + pl.b);
     }
   }
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     const int slot = token + 2 * i;
-    const int at = __shfl_sync(0xffffffffu, position, slot);
-    unpack(u[i], v[i], x[i]);
-    if (pl.turns && slot >= first && slot < last) turn<kNeighbours>(x[i], angles(rot, at, l16));
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (do_v && slot >= first && slot < last) raw[i] = ldg128_nc(v_src + 2 * i * vs.stride);
   }
-  put_block<F, kNeighbours>(x, t0, first, last, ks.codes + block * kBlockBytesI8, ks.scale + block,
-                            pl.a, pl.b, lane, most);
+  float x[4][8];
+  if (do_k) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int slot = token + 2 * i;
+      const int at = __shfl_sync(0xffffffffu, position, slot);
+      unpack(u[i], v[i], x[i]);
+      if (pl.turns && slot >= first && slot < last) turn<kNeighbours>(x[i], angles(rot, at, l16));
+    }
+    put_block<F, kNeighbours>(x, t0, first, last, ks.codes + block * kBlockBytesI8, k_old,
+                              ks.scale + block, pl.a, pl.b, lane, most);
+  }
+  if (!do_v) return;
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+    unpack(make_uint2(raw[i].x, raw[i].y), make_uint2(raw[i].z, raw[i].w), x[i]);
+  put_block<F, true>(x, t0, first, last, vs.codes + block * kBlockBytesI8, v_old,
+                     vs.scale + block, 8 * l16, 8 * l16 + 4, lane, most);
 }
 
 // ------------------------------------------------------------- the accepted branch into place
@@ -237,7 +244,7 @@ struct KeepArgs {
 };
 
 template <int F>
-__global__ void __launch_bounds__(kWarps * 32) kv8_keep_kernel(const KeepArgs p) {
+__global__ void __launch_bounds__(kWarps * 32, 3) kv8_keep_kernel(const KeepArgs p) {
   grid_dep_wait();
   grid_dep_launch();
   const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -286,7 +293,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_keep_kernel(const KeepArgs p)
       from = (long long)block * kBlockBytesI8 + src % kPage * kHeadDim;
       s = __ldcg(scale + block);
     }
-    const int to_page = table[base / kPage];
+    const size_t to = (size_t)table[base / kPage] * p.hkv + h;
+    const float s_old = first > 0 ? __ldcg(scale + to) : 0.0f;
     uint2 raw[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) {
@@ -308,8 +316,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_keep_kernel(const KeepArgs p)
         x[i][k] = slot >= first && slot < last ? __fmul_rn(x[i][k], by) : 0.0f;
     }
     // (the maximum over the lanes orders all their reads before the first write)
-    const size_t to = (size_t)to_page * p.hkv + h;
-    put_block<F, true>(x, 0, first, last, codes + to * kBlockBytesI8, scale + to, 8 * l16,
+    put_block<F, true>(x, 0, first, last, codes + to * kBlockBytesI8, s_old, scale + to, 8 * l16,
                        8 * l16 + 4, lane, [](uint32_t v) { return v; });
     __syncwarp();
   }
@@ -332,14 +339,20 @@ cudaError_t launch_kv8_write_rotated(const Shape& s, const Kv8& c, const RotaryT
                         static_cast<uint8_t*>(c.v), c.v_scale};
   const RowSide qs = {static_cast<const __nv_bfloat16*>(q), q_stride,
                       static_cast<__nv_bfloat16*>(q_out), q_out_stride, q ? s.hq : 0};
-  const int block_units = new_block_items(s.batch, total, cu != nullptr) * s.hkv * 4;
+  const bool split = cu == nullptr && s.batch * s.hkv * 4 <= kSplitUnits;
+  const int block_units =
+      new_block_items(s.batch, total, cu != nullptr) * s.hkv * (split ? 4 : 2);
   const int units = block_units + total * row_units(qs.heads);
-  auto kernel = kv8_write_rotated_kernel<kInt8, false>;
-  if (c.format == kE4m3)
-    kernel = t.neighbours ? kv8_write_rotated_kernel<kE4m3, true>
-                          : kv8_write_rotated_kernel<kE4m3, false>;
-  else if (t.neighbours)
-    kernel = kv8_write_rotated_kernel<kInt8, true>;
+  auto pick = [&](auto format) {
+    constexpr int kF = decltype(format)::value;
+    if (split)
+      return t.neighbours ? kv8_write_rotated_kernel<kF, true, true>
+                          : kv8_write_rotated_kernel<kF, false, true>;
+    return t.neighbours ? kv8_write_rotated_kernel<kF, true, false>
+                        : kv8_write_rotated_kernel<kF, false, false>;
+  };
+  auto kernel = c.format == kE4m3 ? pick(std::integral_constant<int, kE4m3>{})
+                                  : pick(std::integral_constant<int, kInt8>{});
   return launch_kernel(kernel, dim3(units / kWarps + 1), dim3(kWarps * 32), 0, st, true, rows, rot,
                        ks, vs, qs, page_table, s.hkv, s.num_pages, block_units, units, err);
 }

@@ -21,6 +21,7 @@ using namespace rotary_detail;
 using kv8_detail::NewRows;
 using kv8_detail::NewSpan;
 using kv8_detail::new_span;
+using kv8_detail::warp_search;
 
 constexpr int kWarps = 8;
 

@@ -138,22 +138,5 @@ __device__ __forceinline__ void turn_row(const RowSide& r, const Rotary& rot, lo
   }
 }
 
-// The last b in [0, batch) with first(b) <= key, for ascending first: a warp together, 32 ways a
-// step (1024 sequences: two loads one after the other, not ten). -1 where there is none.
-template <typename First>
-__device__ __forceinline__ int warp_search(int batch, int key, int lane, First first) {
-  int lo = 0, n = batch;
-  for (;;) {
-    const int step = (n + 31) / 32;
-    const int at = lane * step;
-    const bool below = at < n && first(lo + at) <= key;
-    const int count = __popc(__ballot_sync(0xffffffffu, below));
-    if (count == 0) return -1;
-    lo += (count - 1) * step;
-    n = min(step, n - (count - 1) * step);
-    if (step == 1) return lo;
-  }
-}
-
 }  // namespace rotary_detail
 }  // namespace hsa
