@@ -586,7 +586,7 @@ int32_t hsa_kv8_tree(const hsa_dims* d, const hsa_kv8* cache, const void* q, int
  * hsa_kv8_write's rules (a block's scale from the kept values, or with older tokens in it at least
  * the old one), K and V of every kv head. Entries from n_keep[b] on are ignored. Tokens that are
  * not kept are gone; slots behind the last kept one are as good as never written. new_lens
- * (int32 [batch], nullable, not seq_lens itself) receives N_b - n_b + n_keep[b]. A sequence whose
+ * (int32 [batch], nullable, neither seq_lens nor n_keep itself) receives N_b - n_b + n_keep[b]. A sequence whose
  * numbers, indices or pages do not fit is left as it was, its new length N_b, and reported as
  * HSA_ERR_DEVICE_CHECK. Two sequences must not share a page that receives tokens. workspace
  * (nullable) supplies the error word only.

@@ -1323,7 +1323,8 @@ int32_t hsa_kv8_keep(const hsa_dims* d, const hsa_kv8* cache, const int32_t* kee
   if (!aligned(keep_idx, 4) || !aligned(n_keep, 4) || !aligned(cu_tokens, 4) ||
       !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(new_lens, 4))
     return HSA_ERR_INVALID_ARG;
-  if (new_lens == seq_lens) return HSA_ERR_INVALID_ARG;  // other warps still read the lengths
+  // other warps still read the lengths and the numbers
+  if (new_lens == seq_lens || new_lens == n_keep) return HSA_ERR_INVALID_ARG;
   rc = error_word(workspace, workspace_bytes, &err);
   if (rc != HSA_OK) return rc;
   return cuda_status(hsa::launch_kv8_keep(s, c, keep_idx, keep_stride, n_keep, cu_tokens,

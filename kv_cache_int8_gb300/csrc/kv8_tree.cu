@@ -66,15 +66,20 @@ static_assert(2 * kSoftmaxRegs + 2 * kConvertRegs + kOtherRegs == 5 * 96, "the l
 constexpr float kHeadroom = 7.0f, kLag = 8.0f;  // P up to 2^15
 constexpr float kPlainScale = 40.0f; // largest |log2 s_v| of the plain form
 constexpr float kTiny = 1e-37f;      // smallest factor of a score: a masked -inf stays one
-constexpr float kLow = -1e30f;       // a maximum before any score
+constexpr float kLow = -3.4e38f;     // a maximum before any score
 // Places on the line of steps (see the plan): a tile's, with one stream on it and with two, a row
 // block's beside its tiles, and the shortest slice.
 constexpr int kTilePlaces = 2, kTwoPlaces = 3, kBlockPlaces = 22, kMinPlaces = 4;
 static_assert(kMinPlaces >= kTwoPlaces, "no slice without the first place of a tile");
 // O takes the products of at most this many steps: their own sums round to zero, 2^-23 a product
 constexpr int kMaxSteps = 256;
-// of a step: a block without tokens; an s_v that the plain form does not take
-constexpr int kHidden = 1, kFarScale = 2;
+// Of a step: an s_v that the plain form does not take; the exponent of its largest s_k (from bit 1
+// on); a block without tokens.
+constexpr int kFarScale = 1, kHidden = 1 << 16;
+// A score is within 2^30 of its factors f s_k (128 channels of 2^14 by 2^9). Where f s_k is 2^-6 or
+// more that is 2^24, and fp32's rounding of scores could come near the lag: the step is taken in
+// the form that rounds them first.
+constexpr int kFarFactors = 247;  // the sum of the two biased exponents
 constexpr uint32_t kColS = 0, kColO = 256, kColK = 384, kColV = 448;
 
 struct Record {  // a row block that begins in a CTA's slice and goes on behind it
@@ -115,9 +120,9 @@ struct alignas(16) Piece {
   int slot;          // of the parts
   int parts;         // kRecord: how many
 };
-// the whole row block; a piece of the same stretch in front, behind; the first part, to be
-// recorded; other row blocks read the same tokens
-constexpr int kWhole = 1, kAfter = 2, kBefore = 4, kRecord = 8, kShared = 16;
+// the whole row block; a piece of the same stretch in front; the first part, to be recorded; other
+// row blocks read the same tokens
+constexpr int kWhole = 1, kAfter = 2, kRecord = 4, kShared = 8;
 
 struct Smem {
   alignas(1024) unsigned char q[kTileBytes];
@@ -130,7 +135,7 @@ struct Smem {
   // stream's softmax two of its own steps before, at most ten back, and the other stream's eleven
   // back.
   float4 page[kPageRing][kTilePages];
-  int flags[kPageRing];            // of a step: kHidden, kFarScale
+  int flags[kPageRing];            // of a step: see kFarScale
   uint32_t seen[kKv8TreeNodes][kRows / 32];  // of each node: the rows that see it
   float c[2][kStreamRows];         // kHeadroom - m
   float m[2][kStreamRows];         // the rows' maxima
@@ -145,6 +150,7 @@ struct Smem {
       pv_done[2], piece_full[kPieces], piece_empty[kPieces], all_done;
   uint32_t tmem;
   int2 exponents[kKWarp];
+  int far;  // flags from here on: hidden tokens, or scores that may be far from 0
   int dead;
 };
 // behind it: len, n, row0, block_nodes, blocks (int [batch] each)
@@ -482,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool general = e_max - e_min > 15;
       const int common = min(13 + 127 - e_max, 126);
       const float f = p.scale_log2 * __uint_as_float((uint32_t)(127 - common) << 23);
+      if (tid == 0) sm.far = 2 * (kFarFactors - (int)(__float_as_uint(fabsf(f)) >> 23));
 #pragma unroll
       for (int i = 0; i < 2; i++) {
         if (i == 1 && !two) continue;
@@ -522,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float4* pages = &sm.page[ring][2 * (warp & 3)];
         const int flags = sm.flags[ring];
         const uint32_t s_col = at + kColS + kStreamRows * st + 2 * kStreamRows * buf;
-        // some of the tokens are hidden from some row
-        const bool masked = (flags & kHidden) != 0 || (pc.tile + j + 1) * kTokens > pc.start;
+        // some of the tokens are hidden from some row, or scores may be far from 0
+        const bool masked = flags >= sm.far || (pc.tile + j + 1) * kTokens > pc.start;
         auto load32 = [&](int h, int b, uint32_t (&s)[16]) {  // rows [8 b, 8 b + 32)
           load_16x32(s_col + ((uint32_t)(16 * h) << 16) + 8 * b, s);
         };
@@ -600,7 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       fmaxf(sm.red[st][2][t], sm.red[st][3][t]));
               kept[t] = now;
               sm.by[st][t] = ex2(was - now);
-              if (!side) sm.c[st][t] = kHeadroom - now;
+              // (scores of a wait that ran out may be any: they must not pass the lag for ever)
+              if (!side) sm.c[st][t] = sm.dead ? -INFINITY : kHeadroom - now;
             }
             named_sync(2 + st, 128);
 #pragma unroll
@@ -645,7 +653,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (again) adjust();
           if (slow) {
             free_p();
-            // ---- hidden tokens, or the second form: every row under its own factor
+            // ---- hidden tokens, far scores, or the second form: every row under its own factor. A
+            // score is rounded as it is for the maxima before c is added: none is above its maximum,
+            // and P is 2^8 at most however c is rounded.
 #pragma unroll 1
             for (int h = 0; h < 2; h++) {
               const float4 pg = pages[h];
@@ -662,10 +672,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t w[4];
 #pragma unroll
                 for (int k = 0; k < 2; k++) {
-                  const F2 g2 = factors(pg, b + k), add = add2(c[b + k], w2);
+                  const F2 g2 = factors(pg, b + k);
                   const uint32_t* v = &s[4 * (b % 4 + k)];
                   const F2 x0 = mul2(pack(v), g2), x1 = mul2(pack(v + 2), g2);
-                  const float2 y0 = ex2(unpack(add2(x0, add))), y1 = ex2(unpack(add2(x1, add)));
+                  const float2 y0 = ex2(unpack(add2(fma2(pack(v), g2, w2), c[b + k])));
+                  const float2 y1 = ex2(unpack(add2(fma2(pack(v + 2), g2, w2), c[b + k])));
                   w[2 * k] = half_pair(y0.x, y0.y);
                   w[2 * k + 1] = half_pair(y1.x, y1.y);
                   if (general) {
@@ -1128,7 +1139,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (is_k) {
           const float log = log2f(cur.sv);
           const bool far = mine && cur.valid > 0 && !(fabsf(log) <= kPlainScale);
-          const int flags = (blocks < kTilePages ? kHidden : 0) |
+          const int largest = __reduce_max_sync(
+              0xffffffffu, mine ? __float_as_uint(fabsf(cur.sk)) >> 23 : 0u);
+          const int flags = (blocks < kTilePages ? kHidden : 0) | 2 * largest |
                             (__any_sync(0xffffffffu, far) ? kFarScale : 0);
           if (mine)
             sm.page[step % kPageRing][lane & 7] =
@@ -1247,7 +1260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             piece.tile > 0 && tiles_begin + (piece.tile - 1) * tile_places >= begin;
         const bool whole = !cut && begin <= tiles_begin && last_begin < end;
         const int c0 = (int)over(tiles_begin, per);
-        piece.flags = (whole ? kWhole : 0) | (after ? kAfter : 0) | (cut ? kBefore : 0) |
+        piece.flags = (whole ? kWhole : 0) | (after ? kAfter : 0) |
                       (!whole && !cut && tiles_begin >= begin ? kRecord : 0) |
                       (num[b] > nodes ? kShared : 0);
         piece.slot = 2 * blockIdx.x + (begin < block_begin ? 1 : 0);

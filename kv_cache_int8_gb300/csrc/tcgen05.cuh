@@ -51,18 +51,16 @@ __device__ __forceinline__ bool elect() {
 // Shared-memory operands are described by 64 bits, of which the upper half is the same for all
 // here: 16-bit values under the 128-byte swizzle in rows of 128 bytes, groups of 8 rows 1024
 // bytes apart. The lower half holds the address / 16 (add distances / 16 to it) and `lbo`: the
-// bytes between 64-value parts of the N (M) extent, for operands whose N (M) runs along the rows.
+// bytes between 64-value parts of the N extent, for operands whose N runs along the rows.
 constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) {
   return (addr >> 4) | ((lbo >> 4) << 16);
 }
 
-// fp16 operands, fp32 result, M x N; b_along_n, a_along_m: the rows of B (A) run along N (M), each
-// row one k.
-__host__ __device__ constexpr uint32_t instr_f16(int m, int n, bool b_along_n,
-                                                 bool a_along_m = false) {
-  return (1u << 4) | ((a_along_m ? 1u : 0u) << 15) | ((b_along_n ? 1u : 0u) << 16) |
-         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+// fp16 operands, fp32 result, M x N; b_along_n: B's rows run along N (each row one k).
+__host__ __device__ constexpr uint32_t instr_f16(int m, int n, bool b_along_n) {
+  return (1u << 4) | ((b_along_n ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(m >> 4) << 24);
 }
 
 // d (TMEM) = a b (+ d): a and b in shared memory, 16 values of k. One lane issues them; what it

@@ -95,7 +95,7 @@ class Call:
         self.a = dict(d=dims(lib), kk=OK, format=0, rot=True, angles=OK, rows=1000, dim=128, nb=0,
                       q=OK, qs=32 * 128, qo=2 * OK, qos=32 * 128, k=OK, ks=8 * 128, ko=2 * OK,
                       kos=8 * 128, v=OK, vs=8 * 128, pos=OK, parents=OK, cu=OK, total=100, table=OK,
-                      lens=OK, out=OK, lse=OK, idx=OK, stride=9, cnt=OK, new=2 * OK, ws=OK,
+                      lens=OK, out=OK, lse=OK, idx=OK, stride=9, cnt=3 * OK, new=2 * OK, ws=OK,
                       ws_bytes=1 << 40)
         self.a.update(kw)
 
@@ -159,6 +159,7 @@ ROTARY, CACHE, ROWS = ALL[:2], ALL[1:], ALL[:3]
     (("keep",), dict(idx=None), INVALID), (("keep",), dict(idx=OK + 2), INVALID),
     (("keep",), dict(stride=-1), INVALID), (("keep",), dict(cnt=None), INVALID),
     (("keep",), dict(cnt=OK + 2), INVALID), (("keep",), dict(new=OK), INVALID),
+    (("keep",), dict(new=3 * OK), INVALID),
     (("keep",), dict(new=OK + 2), INVALID),
 ])
 def test_refusals_of_arguments(lib, fns, bad, code):  # noqa: F811

@@ -587,6 +587,36 @@ def test_one_token_takes_everything_at_every_place():
         check_tree(s, q, parents, [m], out, lse)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("power", (14, 20, 24, 30, 60, 100, 120))
+@pytest.mark.parametrize("m", (2, 16))
+def test_scores_of_any_size(fmt, power, m):
+    """Queries up to 2^120: one token of a row has the largest score by far (its key is twice the
+    others' largest along the query), so the row is that token's value but for fp16's and bf16's
+    rounding, and lse its score within fp32's own roundings of it."""
+    n = 700
+    s = Batch([n], 8, 1, fmt, seed=44, fill=False)
+    k, v = s.rows(n), s.rows(n)
+    k[:, :, 0] = 1.0
+    k[333, 0, 0] = 4.0
+    O.write(s.cache, bf16(k), v, s.table[0], 0)
+    q = np.zeros((m, 8, D), np.float32)
+    q[..., 0] = 2.0 ** power
+    q[m - 1, 3, 0] = -2.0 ** power  # (all scores alike but for one that is far below)
+    parents = [R.tree(s.rng, m)]
+    out, lse = run_tree(s, q, parents, [m])
+    kk, vv = (O.values(s.cache, w, s.table[0], n, 0) for w in "kv")
+    score = kk[333, 0] * 2.0 ** power * D ** -0.5
+    rows = np.ones((m, 8), bool)
+    rows[m - 1, 3] = False
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    # the weight of the one token is a power of two but for the sum's rounding: bf16's half step
+    err = np.abs(out[rows] - vv[333])
+    assert (err <= 2.0 ** -8 * np.abs(vv[333]) + 2.0 ** -20 * np.abs(vv[333]).max()).all()
+    # factor, scale, product and logarithm: six roundings of the score, 2^-24 each
+    assert (np.abs(lse[rows] - score) <= 6 * 2.0 ** -24 * score + 1e-5).all()
+
+
 @pytest.mark.parametrize("hq,hkv,batch,m", [(8, 8, 300, 2), (4, 1, 1024, 1), (8, 1, 600, 5)])
 def test_trees_of_large_batches(hq, hkv, batch, m):
     """Ragged batches of hundreds; a sample of the sequences against the oracle."""
