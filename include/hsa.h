@@ -565,14 +565,14 @@ int32_t hsa_kv8_write_rotated(const hsa_dims* d, const hsa_kv8* cache, const hsa
 /*
  * Attention of drafted tokens: the n_b last tokens of each sequence (their own K and V written
  * before, at most 256 of them) are the nodes of a tree or of several; parents (int32
- * [total_tokens], rows as q's) names each node's parent among its sequence's nodes, an earlier
- * one, or -1 for a child of the context. Node i attends the context, tokens [0, N_b - n_b), its
+ * [total_tokens], rows as q's) names each node's parent among its sequence's nodes, an earlier one,
+ * or -1 for a child of the context. Node i attends the context, tokens [0, N_b - n_b), its
  * ancestors and itself. parents NULL: node i - 1 is node i's parent (a draft without branches:
- * hsa_kv8_prefill's causal attention). q, out, lse and strides as hsa_kv8_prefill's; the weights
- * enter the product with V as fp16 numbers, within 2^-11 of themselves. A parent that is no
- * earlier node is reported as HSA_ERR_DEVICE_CHECK and counts as -1; rows of a sequence that is
- * left out (also one of more than 256 nodes) get 0 and lse -inf; rows of no sequence stay as they
- * were. Needs the HSA_OP_KV8_TREE workspace.
+ * hsa_kv8_prefill's causal attention). q, out, lse and strides as hsa_kv8_prefill's, out not over
+ * q; the weights enter the product with V as fp16 numbers, within 2^-11 of themselves. A parent
+ * that is no earlier node is reported as HSA_ERR_DEVICE_CHECK and counts as -1; rows of a sequence
+ * that is left out (also one of more than 256 nodes) get 0 and lse -inf; rows of no sequence stay
+ * as they were. Needs the HSA_OP_KV8_TREE workspace.
  */
 int32_t hsa_kv8_tree(const hsa_dims* d, const hsa_kv8* cache, const void* q, int64_t q_stride,
                      const int32_t* parents, const int32_t* cu_tokens, int32_t total_tokens,
@@ -586,7 +586,7 @@ int32_t hsa_kv8_tree(const hsa_dims* d, const hsa_kv8* cache, const void* q, int
  * hsa_kv8_write's rules (a block's scale from the kept values, or with older tokens in it at least
  * the old one), K and V of every kv head. Entries from n_keep[b] on are ignored. Tokens that are
  * not kept are gone; slots behind the last kept one are as good as never written. new_lens
- * (int32 [batch], nullable, neither seq_lens nor n_keep itself) receives N_b - n_b + n_keep[b]. A sequence whose
+ * (int32 [batch], nullable, an array of its own) receives N_b - n_b + n_keep[b]. A sequence whose
  * numbers, indices or pages do not fit is left as it was, its new length N_b, and reported as
  * HSA_ERR_DEVICE_CHECK. Two sequences must not share a page that receives tokens. workspace
  * (nullable) supplies the error word only.

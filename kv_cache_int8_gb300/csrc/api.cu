@@ -1293,7 +1293,8 @@ int32_t hsa_kv8_tree(const hsa_dims* d, const hsa_kv8* cache, const void* q, int
   if (rc != HSA_OK || total_tokens == 0) return rc;  // no rows, no arrays of them
   rc = check_row_array(q, q_stride, s.hq);
   if (rc != HSA_OK) return rc;
-  if (!out || !aligned(out, 16) || !aligned(lse, 4)) return HSA_ERR_INVALID_ARG;
+  // (rows are read by several CTAs, so they cannot be replaced by their results)
+  if (!out || !aligned(out, 16) || out == q || !aligned(lse, 4)) return HSA_ERR_INVALID_ARG;
   const TreeLayout l = kv8_tree_layout();
   rc = check_ws(s, workspace, workspace_bytes, l.end);
   if (rc != HSA_OK) return rc;
@@ -1323,8 +1324,10 @@ int32_t hsa_kv8_keep(const hsa_dims* d, const hsa_kv8* cache, const int32_t* kee
   if (!aligned(keep_idx, 4) || !aligned(n_keep, 4) || !aligned(cu_tokens, 4) ||
       !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(new_lens, 4))
     return HSA_ERR_INVALID_ARG;
-  // other warps still read the lengths and the numbers
-  if (new_lens == seq_lens || new_lens == n_keep) return HSA_ERR_INVALID_ARG;
+  // other warps still read the lists
+  if (new_lens && (new_lens == seq_lens || new_lens == n_keep || new_lens == keep_idx ||
+                   new_lens == cu_tokens))
+    return HSA_ERR_INVALID_ARG;
   rc = error_word(workspace, workspace_bytes, &err);
   if (rc != HSA_OK) return rc;
   return cuda_status(hsa::launch_kv8_keep(s, c, keep_idx, keep_stride, n_keep, cu_tokens,

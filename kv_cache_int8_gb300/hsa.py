@@ -617,10 +617,14 @@ def hsa_rotary_table(rows: int, dim: int = 128, base: float = 10000.0, scaling: 
                      stream=None) -> torch.Tensor:
     """A rotary table for positions 0 .. rows - 1, float32 [rows][dim] (include/hsa.h: scaling 0
     none, 1 linear, 2 by parts)."""
-    table = torch.empty((rows, dim), dtype=torch.float32, device=device)
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise HsaError("hsa_rotary_table", HSA_ERR_INVALID_ARG, "a table is made on a GPU")
     a = hsa_rotary_angles(base, factor, low, high, original, magnitude, scaling)
-    _check("hsa_rotary_table", load().hsa_rotary_table(ctypes.byref(a), table.data_ptr(), rows, dim,
-                                                       _stream(stream)))
+    with torch.cuda.device(device):
+        table = torch.empty((rows, dim), dtype=torch.float32, device=device)
+        _check("hsa_rotary_table", load().hsa_rotary_table(
+            ctypes.byref(a), table.data_ptr(), rows, dim, _stream(stream)))
     return table
 
 

@@ -1,11 +1,15 @@
 """Rotary positions and drafted tokens without a GPU: the oracle by hand, the binding's structs
 against the header, and the refusals that come before any CUDA call."""
+import copy
 import ctypes
+import dataclasses
+import pickle
 
 import numpy as np
 import pytest
 import torch
 
+from kv_cache_int8_gb300 import hsa
 from oracle import draft as R
 from oracle import kv8 as O
 from test_abi import _header_struct_fields
@@ -95,7 +99,7 @@ class Call:
         self.a = dict(d=dims(lib), kk=OK, format=0, rot=True, angles=OK, rows=1000, dim=128, nb=0,
                       q=OK, qs=32 * 128, qo=2 * OK, qos=32 * 128, k=OK, ks=8 * 128, ko=2 * OK,
                       kos=8 * 128, v=OK, vs=8 * 128, pos=OK, parents=OK, cu=OK, total=100, table=OK,
-                      lens=OK, out=OK, lse=OK, idx=OK, stride=9, cnt=3 * OK, new=2 * OK, ws=OK,
+                      lens=OK, out=4 * OK, lse=OK, idx=OK, stride=9, cnt=3 * OK, new=2 * OK, ws=OK,
                       ws_bytes=1 << 40)
         self.a.update(kw)
 
@@ -159,7 +163,8 @@ ROTARY, CACHE, ROWS = ALL[:2], ALL[1:], ALL[:3]
     (("keep",), dict(idx=None), INVALID), (("keep",), dict(idx=OK + 2), INVALID),
     (("keep",), dict(stride=-1), INVALID), (("keep",), dict(cnt=None), INVALID),
     (("keep",), dict(cnt=OK + 2), INVALID), (("keep",), dict(new=OK), INVALID),
-    (("keep",), dict(new=3 * OK), INVALID),
+    (("keep",), dict(new=3 * OK), INVALID), (("keep",), dict(new=5 * OK, idx=5 * OK), INVALID),
+    (("keep",), dict(new=5 * OK, cu=5 * OK), INVALID), (("tree",), dict(out=OK), INVALID),
     (("keep",), dict(new=OK + 2), INVALID),
 ])
 def test_refusals_of_arguments(lib, fns, bad, code):  # noqa: F811
@@ -283,3 +288,20 @@ def test_the_binding_refuses_what_it_would_misread(binding):  # noqa: F811
         with pytest.raises(hsa.HsaError):
             hsa.Rotary(bad)
     assert not fake.calls
+
+
+def test_a_descriptor_keeps_its_struct_until_a_field_is_set():
+    d = hsa.Dims(batch=2, hq=8, hkv=2, max_pages_per_seq=4, num_pages=9)
+    held = d.ref()
+    assert d.ref() is held and held._obj.batch == 2
+    twins = [copy.copy(d), copy.deepcopy(d), pickle.loads(pickle.dumps(d)),
+             dataclasses.replace(d, batch=3)]
+    d.batch = 5
+    assert d.ref()._obj.batch == 5 and held._obj.batch == 2
+    assert [t.ref()._obj.batch for t in twins] == [2, 2, 2, 3]
+    assert twins[0] == twins[1] != d
+
+
+def test_a_table_is_made_on_a_gpu():
+    with pytest.raises(hsa.HsaError):
+        hsa.hsa_rotary_table(16, 128, device="cpu")

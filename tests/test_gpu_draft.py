@@ -879,6 +879,107 @@ def test_a_loop_of_drafted_tokens(fmt):
     assert hsa.hsa_read_device_error(ws) == 0 and hsa.hsa_read_device_error(err) == 0
 
 
+class Step:
+    """A verification step's arrays: write with positions, attend the trees, keep a branch."""
+
+    def __init__(self, seed, lens, new, hq=8, hkv=2, fmt="int8"):
+        s = Batch([n + m for n, m in zip(lens, new)], hq, hkv, fmt, seed=seed)
+        T, self.d, self.cache, self.table = sum(new), s.dims(), s.gpu_cache(), s.gpu_table()
+        self.rot = hsa.Rotary(torch.from_numpy(angle_table(2048, D)).cuda())
+        self.x = [to_bf16(bf16(s.rng.standard_normal((T, h, D)))) for h in (hq, hkv, hkv)]
+        trees = [R.tree(s.rng, m) for m in new]
+        self.up = i32([p for t in trees for p in t])
+        self.at = i32(np.concatenate([n + R.depths(t) for n, t in zip(lens, trees) if t]))
+        paths = [np.flatnonzero(R.branches(t)[-1]) if t else [] for t in trees]
+        idx = np.full((len(lens), max(map(len, paths))), -1, dtype=np.int32)
+        for b, path in enumerate(paths):
+            idx[b, :len(path)] = path
+        self.idx, self.kept, self.cu = i32(idx), i32([len(path) for path in paths]), cu_of(new)
+        self.lens = s.gpu_lens()
+        self.ws = hsa.workspace(self.d, hsa.HSA_OP_KV8_PREFILL)
+        self.q, self.out = (torch.zeros(T, hq, D, dtype=torch.bfloat16, device="cuda")
+                            for _ in range(2))
+        self.lse = torch.zeros(T, hq, device="cuda")
+        self.after = torch.zeros(len(lens), dtype=torch.int32, device="cuda")
+
+    def run(self):
+        hsa.hsa_kv8_write_rotated(self.d, self.cache, self.rot, self.x[0], self.q, self.x[1],
+                                  self.x[2], self.at, self.cu, self.table, self.lens, self.ws)
+        hsa.hsa_kv8_tree(self.d, self.cache, self.q, self.up, self.cu, self.table, self.lens,
+                         self.out, self.lse, self.ws)
+        hsa.hsa_kv8_keep(self.d, self.cache, self.idx, self.kept, self.cu, self.table, self.lens,
+                         self.after, self.ws)
+
+    def state(self):
+        c = self.cache
+        return [t.clone().view(torch.uint8) for t in
+                (self.q, self.out, self.lse, self.after, c.k, c.v, c.k_scale, c.v_scale)]
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_two_verification_steps_at_once():
+    """Two batches on two streams, each with its workspace: the bits of one after the other."""
+    make = [lambda: Step(90, [700, 33, 1500], [25, 7, 60]),
+            lambda: Step(91, [260] * 40, [9] * 40, hq=16, hkv=8, fmt="e4m3")]
+    want = []
+    for m in make:
+        s = m()
+        for _ in range(6):
+            s.run()
+        torch.cuda.synchronize()
+        want.append(s.state())
+    steps, streams = [m() for m in make], [torch.cuda.Stream() for _ in make]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for s, stream in zip(steps, streams):
+            with torch.cuda.stream(stream):
+                s.run()
+    torch.cuda.synchronize()
+    for s, w in zip(steps, want):
+        assert hsa.hsa_read_device_error(s.ws) == 0
+        assert same(s.state(), w)
+
+
+def test_a_captured_verification_step():
+    """A step captured once and replayed over new tokens, trees, lengths and kept branches; between
+    the replays another graph's prompt attention uses the same workspace."""
+    lens, new = [300, 64, 1000, 17], [20, 0, 64, 5]
+    s = Step(92, lens, new)
+    graph, other = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    prompt = torch.zeros_like(s.out)
+    with torch.cuda.graph(graph):
+        s.run()
+    with torch.cuda.graph(other):
+        hsa.hsa_kv8_prefill(s.d, s.cache, s.x[0], s.cu, s.table, s.lens, prompt, None, s.ws)
+    for seed, now, m in ((93, [310, 60, 1000, 5], [3, 4, 70, 12]), (94, lens, new),
+                         (95, [1, 50, 31, 20], [89, 0, 0, 0])):
+        e = Step(seed, now, m)  # run as it is, in memory of its own
+        for mine, its in zip(s.x + [s.up, s.at, s.cu, s.lens, s.kept],
+                             e.x + [e.up, e.at, e.cu, e.lens, e.kept]):
+            mine.copy_(its)
+        # (branches as long as the captured step's rows of indices)
+        s.idx.fill_(-1)
+        short = min(s.idx.shape[1], e.idx.shape[1])
+        s.idx[:, :short] = e.idx[:, :short]
+        e.kept.clamp_(max=short)
+        s.kept.copy_(e.kept)
+        e.d, e.table, held = s.d, s.table, s.state()[4:]
+        e.cache = hsa.KV8(s.cache.k.clone(), s.cache.v.clone(), s.cache.k_scale.clone(),
+                          s.cache.v_scale.clone())
+        e.run()
+        want = torch.zeros_like(prompt)
+        hsa.hsa_kv8_prefill(e.d, e.cache, e.x[0], e.cu, e.table, e.lens, want, None, e.ws)
+        graph.replay()
+        other.replay()
+        torch.cuda.synchronize()
+        assert hsa.hsa_read_device_error(s.ws) == 0 and hsa.hsa_read_device_error(e.ws) == 0
+        assert same(s.state(), e.state()) and torch.equal(prompt, want)
+        assert not same(s.state()[4:], held)
+
+
 def test_rotated_rows_go_into_the_bf16_cache():
     """hsa_rotate in front of the bf16 path: the append stores the turned key."""
     lens, hq, hkv = [100, 33], 8, 2
