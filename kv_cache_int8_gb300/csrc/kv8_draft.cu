@@ -108,21 +108,27 @@ struct WriteSide {
   float* scale;
 };
 
-// Units: blocks x heads x halves, then (row, 16 query heads); one warp behind them reports sequences
-// that do not fit. Two warps share a block of K and of V, eight tokens each, and meet over its
-// maxima. A unit's way to its data (sequence, length, page, rows) is four loads one after the other,
-// so what is then under way at once decides: 123K new tokens' keys and values, queries aside, took
-// 200 us with a warp a block of K or V and 16 tokens (16 warps an SM), 188 with two warps, 175 with
-// both K and V of a block in a warp. kSplit: units of K and of V apart, for a token a sequence of few
-// sequences, where the one behind the other only takes longer (one sequence of 8 kv heads 2.9 us a
-// call, not 3.4; 256 sequences 8.1, not 6.3, as the warps no longer fit the GPU at once).
+// Units: blocks x kv heads (or runs of `heads` of them) x halves, then (row, 16 query heads); one warp
+// behind them reports sequences that do not fit. Two warps share a block of K and of V, eight tokens
+// each, and meet over its maxima. Bound by memory: 109K new tokens of 32 + 8 heads (2.47 GB) take
+// 390 us, 6.3 TB/s; one token 2.9 us, latency.
+//
+// A unit's way to its data (sequence, length, page, rows) is four loads one after the other. Where
+// there are many blocks a warp goes it once for several kv heads (kMany); the positions' angles then
+// come out of L1 (in registers they cost 32 and 2% of the time). One head a unit against four and
+// eight: 4096 tokens of 8 heads with their read-back 22.6, 26.8, 40.7 us, 8192 46.8, 39.5, 47.7, 24000
+// 132.5, 117.7, 114.6, 109K 541, 495, 491; so as many heads as leave 1024 runs (2048 warps, 13 an
+// SM). kSplit: units of K and of V apart, for a token a sequence of few sequences, where the one
+// behind the other only takes longer (one sequence of 8 kv heads 2.9 us a call, not 3.4; 256
+// sequences 8.1, not 6.3, as the warps no longer fit the GPU at once).
+constexpr int kBlocksAHead = 1024;
 constexpr int kSplitUnits = 2048;  // 13 warps an SM, of 24
-template <int F, bool kNeighbours, bool kSplit>
+template <int F, bool kNeighbours, bool kSplit, bool kMany>
 __global__ void __launch_bounds__(kWarps * 32, 3)
     kv8_write_rotated_kernel(const NewRows rows, const Rotary rot, const WriteSide ks,
                              const WriteSide vs, const RowSide qs,
-                             const int32_t* __restrict__ page_table, int hkv, int num_pages,
-                             int block_units, int units, int* err) {
+                             const int32_t* __restrict__ page_table, int hkv, int heads,
+                             int num_pages, int block_units, int units, int* err) {
   __shared__ uint32_t tops[4][kWarps];
   grid_dep_wait();
   grid_dep_launch();
@@ -147,7 +153,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     return;
   }
   const int t0 = 8 * (unit & 1);
-  const int pair = kSplit ? unit >> 2 : unit >> 1, h = pair % hkv, item = pair / hkv;
+  const int pair = kSplit ? unit >> 2 : unit >> 1, groups = kMany ? (hkv + heads - 1) / heads : hkv;
+  const int h0 = kMany ? pair % groups * heads : pair % groups, item = pair / groups;
   const bool do_k = !kSplit || !(unit & 2), do_v = !kSplit || (unit & 2);
   const int b = rows.cu ? item_sequence(rows, item, lane) : item;
   if (b < 0) return;
@@ -173,52 +180,57 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   }
   int turn_of = 0;
   auto most = [&](uint32_t v) {  // of the block's two warps
-    if (lane == 0) tops[turn_of][warp] = v;
+    const int at = turn_of++ & 3;
+    if (lane == 0) tops[at][warp] = v;
     asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
-    return max(v, tops[turn_of++][warp ^ 1]);
+    return max(v, tops[at][warp ^ 1]);
   };
-  const size_t block = (size_t)page * hkv + h;
-  const float k_old = first > 0 ? __ldcg(ks.scale + block) : 0.0f;
-  const float v_old = first > 0 ? __ldcg(vs.scale + block) : 0.0f;
   const int token = t0 + (lane >> 4), l16 = lane & 15;
   const Place pl = place<kNeighbours>(l16, rot.dim);
-  const __nv_bfloat16* k_src = ks.x + (row + token) * ks.stride + h * kHeadDim;
-  const __nv_bfloat16* v_src = vs.x + (row + token) * vs.stride + h * kHeadDim + 8 * l16;
-  uint2 u[4], v[4];
-  uint4 raw[4];
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int slot = token + 2 * i;
-    u[i] = v[i] = make_uint2(0u, 0u);
-    if (do_k && slot >= first && slot < last) {
-      u[i] = load4(k_src + 2 * i * ks.stride + pl.a);
-      v[i] = load4(k_src + 2 * i * ks.stride + pl.b);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int slot = token + 2 * i;
-    raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (do_v && slot >= first && slot < last) raw[i] = ldg128_nc(v_src + 2 * i * vs.stride);
-  }
-  float x[4][8];
-  if (do_k) {
+  const int h1 = kMany ? min(h0 + heads, hkv) : h0 + 1;
+#pragma unroll 1
+  for (int h = h0; h < h1; h++) {
+    const size_t block = (size_t)page * hkv + h;
+    const float k_old = first > 0 ? __ldcg(ks.scale + block) : 0.0f;
+    const float v_old = first > 0 ? __ldcg(vs.scale + block) : 0.0f;
+    const __nv_bfloat16* k_src = ks.x + (row + token) * ks.stride + h * kHeadDim;
+    const __nv_bfloat16* v_src = vs.x + (row + token) * vs.stride + h * kHeadDim + 8 * l16;
+    uint2 u[4], v[4];
+    uint4 raw[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       const int slot = token + 2 * i;
-      const int at = __shfl_sync(0xffffffffu, position, slot);
-      unpack(u[i], v[i], x[i]);
-      if (pl.turns && slot >= first && slot < last) turn<kNeighbours>(x[i], angles(rot, at, l16));
+      u[i] = v[i] = make_uint2(0u, 0u);
+      if (do_k && slot >= first && slot < last) {
+        u[i] = load4(k_src + 2 * i * ks.stride + pl.a);
+        v[i] = load4(k_src + 2 * i * ks.stride + pl.b);
+      }
     }
-    put_block<F, kNeighbours>(x, t0, first, last, ks.codes + block * kBlockBytesI8, k_old,
-                              ks.scale + block, pl.a, pl.b, lane, most);
-  }
-  if (!do_v) return;
 #pragma unroll
-  for (int i = 0; i < 4; i++)
-    unpack(make_uint2(raw[i].x, raw[i].y), make_uint2(raw[i].z, raw[i].w), x[i]);
-  put_block<F, true>(x, t0, first, last, vs.codes + block * kBlockBytesI8, v_old,
-                     vs.scale + block, 8 * l16, 8 * l16 + 4, lane, most);
+    for (int i = 0; i < 4; i++) {
+      const int slot = token + 2 * i;
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (do_v && slot >= first && slot < last) raw[i] = ldg128_nc(v_src + 2 * i * vs.stride);
+    }
+    float x[4][8];
+    if (do_k) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int slot = token + 2 * i;
+        const int at = __shfl_sync(0xffffffffu, position, slot);
+        unpack(u[i], v[i], x[i]);
+        if (pl.turns && slot >= first && slot < last) turn<kNeighbours>(x[i], angles(rot, at, l16));
+      }
+      put_block<F, kNeighbours>(x, t0, first, last, ks.codes + block * kBlockBytesI8, k_old,
+                                ks.scale + block, pl.a, pl.b, lane, most);
+    }
+    if (!do_v) continue;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      unpack(make_uint2(raw[i].x, raw[i].y), make_uint2(raw[i].z, raw[i].w), x[i]);
+    put_block<F, true>(x, t0, first, last, vs.codes + block * kBlockBytesI8, v_old,
+                       vs.scale + block, 8 * l16, 8 * l16 + 4, lane, most);
+  }
 }
 
 // ------------------------------------------------------------- the accepted branch into place
@@ -340,21 +352,26 @@ cudaError_t launch_kv8_write_rotated(const Shape& s, const Kv8& c, const RotaryT
   const RowSide qs = {static_cast<const __nv_bfloat16*>(q), q_stride,
                       static_cast<__nv_bfloat16*>(q_out), q_out_stride, q ? s.hq : 0};
   const bool split = cu == nullptr && s.batch * s.hkv * 4 <= kSplitUnits;
-  const int block_units =
-      new_block_items(s.batch, total, cu != nullptr) * s.hkv * (split ? 4 : 2);
+  const int items = new_block_items(s.batch, total, cu != nullptr);
+  const long long full = (long long)total / kPage * s.hkv;  // about as many blocks
+  const int heads = (int)std::min(std::max(full / kBlocksAHead, 1ll), (long long)s.hkv);
+  const int block_units = items * ((s.hkv + heads - 1) / heads) * (split ? 4 : 2);
   const int units = block_units + total * row_units(qs.heads);
   auto pick = [&](auto format) {
     constexpr int kF = decltype(format)::value;
     if (split)
-      return t.neighbours ? kv8_write_rotated_kernel<kF, true, true>
-                          : kv8_write_rotated_kernel<kF, false, true>;
-    return t.neighbours ? kv8_write_rotated_kernel<kF, true, false>
-                        : kv8_write_rotated_kernel<kF, false, false>;
+      return t.neighbours ? kv8_write_rotated_kernel<kF, true, true, false>
+                          : kv8_write_rotated_kernel<kF, false, true, false>;
+    if (heads > 1)
+      return t.neighbours ? kv8_write_rotated_kernel<kF, true, false, true>
+                          : kv8_write_rotated_kernel<kF, false, false, true>;
+    return t.neighbours ? kv8_write_rotated_kernel<kF, true, false, false>
+                        : kv8_write_rotated_kernel<kF, false, false, false>;
   };
   auto kernel = c.format == kE4m3 ? pick(std::integral_constant<int, kE4m3>{})
                                   : pick(std::integral_constant<int, kInt8>{});
   return launch_kernel(kernel, dim3(units / kWarps + 1), dim3(kWarps * 32), 0, st, true, rows, rot,
-                       ks, vs, qs, page_table, s.hkv, s.num_pages, block_units, units, err);
+                       ks, vs, qs, page_table, s.hkv, heads, s.num_pages, block_units, units, err);
 }
 
 cudaError_t launch_kv8_keep(const Shape& s, const Kv8& c, const int32_t* keep_idx, int keep_stride,

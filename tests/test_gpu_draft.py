@@ -220,6 +220,15 @@ def test_rotated_write(fmt, hq, hkv, dim, neighbours, before, new):
     assert hsa.hsa_read_device_error(err) == 0
 
 
+@pytest.mark.parametrize("fmt,hq,hkv,dim,neighbours,before,new", [
+    ("int8", 5, 5, 128, False, [7, 0], [4000, 2600]), ("e4m3", 8, 8, 64, True, [100, 3, 0], [5000, 1, 1600]),
+    ("int8", 8, 8, 24, False, [5], [9000]), ("e4m3", 3, 3, 128, True, [33, 0, 2], [9, 0, 11000]),
+])
+def test_rotated_write_of_long_prompts(fmt, hq, hkv, dim, neighbours, before, new):
+    """Enough blocks that a warp takes several heads, runs that do not divide the heads among them."""
+    test_rotated_write(fmt, hq, hkv, dim, neighbours, before, new)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_rotated_write_token_by_token_from_a_graph(fmt):
     """A decode loop whose one graph replays: the scale of a block grows, its codes follow."""
