@@ -55,7 +55,7 @@ constexpr int kTileBytes = kRows * kHeadDim * 2;      // the queries
 constexpr int kHalfBytes = kTileBytes / 2;            // 64 channels of 128 rows
 constexpr int kRawBytes = kTokens * kHeadDim;         // codes of a step, of K or V
 constexpr int kPBytes = kTokens * kStreamRows * 2;
-constexpr int kStages = 4;                            // steps of raw codes, of K and of V
+constexpr int kStages = 3;                            // steps of raw codes, of K and of V
 constexpr int kPageRing = 16;                         // steps whose scales are kept (see Smem)
 constexpr int kPieces = 4;                            // pieces told ahead
 constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 16, kKLoad = 17, kVLoad = 18, kPlanWarp = 19;
@@ -68,8 +68,12 @@ constexpr float kPlainScale = 40.0f; // largest |log2 s_v| of the plain form
 constexpr float kTiny = 1e-37f;      // smallest factor of a score: a masked -inf stays one
 constexpr float kLow = -3.4e38f;     // a maximum before any score
 // Places on the line of steps (see the plan): a tile's, with one stream on it and with two, a row
-// block's beside its tiles, and the shortest slice.
-constexpr int kTilePlaces = 2, kTwoPlaces = 3, kBlockPlaces = 22, kMinPlaces = 4;
+// block's beside its tiles, and the shortest slice. In the order of their times: 600K tokens of 8
+// heads take 262 us with 64 rows, 342 with 128. Tiles of 2 and 3 places 8 x 32-128K tokens of 48 to
+// 136 rows 420 us, of 3 and 4 391, of 4 and 5 394, of 5 and 7 396, alike 434; 4 chats of 20 to 132
+// rows 38.2, 40.2, 38.8, 39.9. A block's 44 (11 tiles; 16, 28 and 72 places before: 44, 41, 41 us of
+// the chats, 38).
+constexpr int kTilePlaces = 4, kTwoPlaces = 5, kBlockPlaces = 44, kMinPlaces = 8;
 static_assert(kMinPlaces >= kTwoPlaces, "no slice without the first place of a tile");
 // O takes the products of at most this many steps: their own sums round to zero, 2^-23 a product
 constexpr int kMaxSteps = 256;
@@ -126,13 +130,13 @@ constexpr int kWhole = 1, kAfter = 2, kRecord = 4, kShared = 8;
 
 struct Smem {
   alignas(1024) unsigned char q[kTileBytes];
-  unsigned char p[2][kPBytes];  // of a stream; between row blocks its scratch
+  unsigned char p[2][2][kPBytes];  // two steps' of a stream each; between row blocks its scratch
   unsigned char k_raw[kStages][kRawBytes];
   unsigned char v_raw[kStages][kRawBytes];
   // Of a step's blocks: y = 1 / s_v (any number above 0 for zeros, 0 where there are no tokens);
-  // z = s_k; w = log2 s_v (-inf for both). The copies of a step begin when the codes four steps
-  // back are read, so when the scores six back are complete; their buffer was read by its
-  // stream's softmax two of its own steps before, at most ten back, and the other stream's eleven
+  // z = s_k; w = log2 s_v (-inf for both). The copies of a step begin when the codes three steps
+  // back are read, so when the scores five back are complete; their buffer was read by its
+  // stream's softmax two of its own steps before, at most nine back, and the other stream's ten
   // back.
   float4 page[kPageRing][kTilePages];
   int flags[kPageRing];            // of a step: see kFarScale
@@ -146,8 +150,8 @@ struct Smem {
   alignas(8) int v_valid[kStages][kTilePages];
   Piece piece[kPieces];
   alignas(8) uint64_t q_full, k_raw_full[kStages], k_raw_empty[kStages], v_raw_full[kStages],
-      v_raw_empty[kStages], k_full, k_empty, v_full, v_empty, s_full[2][2], s_empty[2][2], p_full[2],
-      pv_done[2], piece_full[kPieces], piece_empty[kPieces], all_done;
+      v_raw_empty[kStages], k_full, k_empty, v_full, v_empty, s_full[2][2], s_empty[2][2], p_full[2][2],
+      pv_done[2][2], piece_full[kPieces], piece_empty[kPieces], all_done;
   uint32_t tmem;
   int2 exponents[kKWarp];
   int far;  // flags from here on: hidden tokens, or scores that may be far from 0
@@ -339,8 +343,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.s_full[i][1], 1);
       mbar_init(&sm.s_empty[i][0], 128);
       mbar_init(&sm.s_empty[i][1], 128);
-      mbar_init(&sm.p_full[i], 128);
-      mbar_init(&sm.pv_done[i], 1);
+      mbar_init(&sm.p_full[i][0], 128);
+      mbar_init(&sm.p_full[i][1], 128);
+      mbar_init(&sm.pv_done[i][0], 1);
+      mbar_init(&sm.pv_done[i][1], 1);
     }
     for (int i = 0; i < kPieces; i++) {
       mbar_init(&sm.piece_full[i], 1);
@@ -399,9 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (a block of the cache) tokens tok + 8 i, and rows 8 b + col, + 1 of every b.
     const int tok = 32 * (warp & 3) + (lane >> 2), col = 2 * (lane & 3);
     // where it points stmatrix at, of P's rows 0 .. 15: token 32 w + (lane & 8) + lane % 8
-    const uint32_t p_row = smem_addr(sm.p[st]) + (32 * (warp & 3) + (lane & 15)) * 128;
+    const uint32_t p_row = smem_addr(sm.p[0][st]) + (32 * (warp & 3) + (lane & 15)) * 128;
     const uint32_t p_chunk = ((lane >> 4) ^ (lane & 7)) << 4;
-    uint32_t used = 0;     // steps of this stream so far
+    uint32_t p_phase = 0;  // bit i: of buffer i of its P, uses so far
     uint32_t s_phase = 0;  // bit i: of buffer i of its S
     int step0 = 0;         // steps of the pieces so far
     for (;;) {
@@ -520,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t o_col = at + kColO + kStreamRows * st;
       // The maxima may be far off: before the first step, and behind one that rows saw nothing of.
       bool unknown = true;
-      for (int j = first; j < pc.tiles; j += stride, used++) {
+      for (int j = first; j < pc.tiles; j += stride) {
         const int buf = (two ? j : j >> 1) & 1;
         wait(sm, &sm.s_full[st][buf], s_phase >> buf & 1);
         s_phase ^= 1u << buf;
@@ -559,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto adjust = [&]() {
           const bool any_o = j > first;  // O holds something
           if (any_o) {
-            wait(sm, &sm.pv_done[st], (used - 1) & 1);
+            wait(sm, &sm.pv_done[st][buf ^ 1], (p_phase >> (buf ^ 1) & 1) ^ 1);
             tc::fence_after();
           }
 #pragma unroll 1
@@ -634,12 +640,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (side) named_sync(2 + st, 128);  // `by` is read
           }
         };
-        // P of a half's rows [8 b, 8 b + 16): eight tokens and eight rows a matrix
+        // P of a half's rows [8 b, 8 b + 16): eight tokens and eight rows a matrix. The products two
+        // of the stream's steps before have read theirs.
+        const uint32_t p_buf = p_row + buf * (2 * kPBytes);
         auto put = [&](int h, int b, const uint32_t* w) {
-          store_matrices(p_row + h * (16 * 128) + (p_chunk ^ (b << 4)), w[0], w[1], w[2], w[3]);
-        };
-        auto free_p = [&]() {  // the products of the stream's step before have read their P
-          if (used > 0) wait(sm, &sm.pv_done[st], (used - 1) & 1);
+          store_matrices(p_buf + h * (16 * 128) + (p_chunk ^ (b << 4)), w[0], w[1], w[2], w[3]);
         };
         if (!general && (flags & kFarScale)) {
           general = true;
@@ -647,12 +652,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           unknown = true;
         }
         const bool slow = general || masked;
+        if (j >= first + 2 * stride) wait(sm, &sm.pv_done[st][buf], (p_phase >> buf & 1) ^ 1);
         bool again = unknown || slow;
         unknown = slow;  // (hidden tokens: rows may still have no maximum)
         for (;;) {
           if (again) adjust();
           if (slow) {
-            free_p();
             // ---- hidden tokens, far scores, or the second form: every row under its own factor. A
             // score is rounded as it is for the maxima before c is added: none is above its maximum,
             // and P is 2^8 at most however c is rounded.
@@ -696,8 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // ---- P and the sums under the maxima as they are; taken back where a score has gone over
           // the lag (rare)
-          F2 d[8];           // the step's sums
-          uint32_t w[4][8];  // and its P, which goes to shared memory when that is free
+          F2 d[8];  // the step's sums
           float top = -INFINITY;
           uint32_t s[2][16];  // 32 rows of a half; the next ones are on their way meanwhile
           load32(0, 0, s[0]);
@@ -712,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float4 pg = pages[h];
             const float g = fmaxf(f * pg.z, kTiny);
             const F2 g2 = pack(g, g), w2 = pack(pg.w, pg.w), inv2 = pack(pg.y, pg.y);
+            uint32_t w[4];
 #pragma unroll
             for (int b = b0; b < b0 + 4; b++) {
               const uint32_t* v = &s[h][4 * (b - b0)];
@@ -721,21 +726,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               top = max3(top, y1.x, y1.y);
               y0 = ex2(y0);
               y1 = ex2(y1);
-              w[u][2 * (b - b0)] = half_pair(y0.x, y0.y);
-              w[u][2 * (b - b0) + 1] = half_pair(y1.x, y1.y);
+              w[2 * (b & 1)] = half_pair(y0.x, y0.y);
+              w[2 * (b & 1) + 1] = half_pair(y1.x, y1.y);
+              if (b & 1) put(h, b - 1, w);
               const F2 e = h == 0 ? mul2(pack(y0), inv2) : fma2(pack(y0), inv2, d[b]);
               d[b] = fma2(pack(y1), inv2, e);
             }
           }
           again = any_of(2 + st, 128, top > kHeadroom + kLag);
           if (!again) {
-            free_p();
-#pragma unroll
-            for (int u = 0; u < 4; u++) {
-              if (u > 1 && !wide) continue;
-              put(u & 1, 4 * (u >> 1), w[u]);
-              put(u & 1, 4 * (u >> 1) + 2, w[u] + 4);
-            }
 #pragma unroll
             for (int b = 0; b < 8; b++)
               if (b < 4 || wide) l[b] = add2(l[b], d[b]);
@@ -745,11 +744,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before();
         mbar_arrive(&sm.s_empty[st][buf]);
         fence_proxy_async();
-        mbar_arrive(&sm.p_full[st]);
+        mbar_arrive(&sm.p_full[st][buf]);
+        p_phase ^= 1u << buf;
       }
       step0 += pc.tiles;
       const bool any = pc.tiles > first;  // this stream had steps
-      if (any) wait(sm, &sm.pv_done[st], (used - 1) & 1);
+      if (any) {
+        const int buf = (two ? pc.tiles - 1 : (pc.tiles - 1 - first) >> 1) & 1;  // the last step's
+        wait(sm, &sm.pv_done[st][buf], (p_phase >> buf & 1) ^ 1);
+      }
 
       // ---- the sums over the stream's tokens
 #pragma unroll
@@ -793,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float front[kStreamRows], inv[kStreamRows];
         long long out[kStreamRows];  // the output row
       };
-      Weights& weights = *reinterpret_cast<Weights*>(sm.p[st]);
+      Weights& weights = *reinterpret_cast<Weights*>(sm.p[0][st]);
       const bool whole = pc.flags & kWhole, after = pc.flags & kAfter;
       const bool both = !two && pc.tiles > 1;
       float2* const pml = reinterpret_cast<float2*>(p.part_ml) + (size_t)pc.slot * kRows;
@@ -986,10 +989,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     // ============================================ the products
     const uint32_t q_low = tc::desc_low(smem_addr(sm.q), 16);
-    const uint32_t p_low = tc::desc_low(smem_addr(sm.p[0]), kPBytes);
+    const uint32_t p_low = tc::desc_low(smem_addr(sm.p[0][0]), kPBytes);
     const bool lead = tc::elect();
     int step = 0;
-    uint32_t done[2] = {0, 0};
+    uint32_t p_phase = 0;    // of the next wait for its P
     uint32_t s_phase = 0xF;  // bit 2 i + b: of the next wait for buffer b of stream i's S
     // 128 products of 16 values of k each: K's tile or V's, in TMEM, with the queries or P
     auto scores = [&](auto instr, uint32_t d) {  // from the queries of stream 0, or of both
@@ -1043,24 +1046,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int jj = j - behind;
         if (jj >= 0) {
+          const int st = two ? 0 : jj & 1, buf = (two ? jj : jj >> 1) & 1;
           wait(sm, &sm.v_full, (step + jj) & 1);
 #pragma unroll
           for (int i = 0; i < 2; i++)
-            if (two || (jj & 1) == i) {
-              wait(sm, &sm.p_full[i], done[i] & 1);
-              done[i]++;
+            if (two || st == i) {
+              wait(sm, &sm.p_full[i][buf], p_phase >> (2 * i + buf) & 1);
+              p_phase ^= 1u << (2 * i + buf);
             }
           tc::fence_after();
+          const uint32_t pp = p_low + (2 * buf + st) * (kPBytes >> 4);
           if (two)
             values(std::integral_constant<uint32_t, tc::instr_f16(128, 2 * kStreamRows, true)>{},
-                   tmem + kColO, p_low, jj > 0);
+                   tmem + kColO, pp, jj > 0);
           else
             values(std::integral_constant<uint32_t, tc::instr_f16(128, kStreamRows, true)>{},
-                   tmem + kColO + kStreamRows * (jj & 1), p_low + (jj & 1) * (kPBytes >> 4), jj > 1);
+                   tmem + kColO + kStreamRows * st, pp, jj > 1);
           if (lead) {
             tc::commit(&sm.v_empty);
-            if (two || !(jj & 1)) tc::commit(&sm.pv_done[0]);
-            if (two || (jj & 1)) tc::commit(&sm.pv_done[1]);
+            tc::commit(&sm.pv_done[st][buf]);
+            if (two) tc::commit(&sm.pv_done[1][buf]);
           }
           __syncwarp();
         }
