@@ -61,7 +61,7 @@ constexpr int kPieces = 4;                            // pieces told ahead
 constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 16, kKLoad = 17, kVLoad = 18, kPlanWarp = 19;
 constexpr int kThreads = 640;
 // registers a thread: softmax warpgroups, converting ones, the last; 96 on average
-constexpr int kSoftmaxRegs = 152, kConvertRegs = 64, kOtherRegs = 48;
+constexpr int kSoftmaxRegs = 144, kConvertRegs = 72, kOtherRegs = 48;
 static_assert(2 * kSoftmaxRegs + 2 * kConvertRegs + kOtherRegs == 5 * 96, "the launch's registers");
 constexpr float kHeadroom = 7.0f, kLag = 8.0f;  // P up to 2^15
 constexpr float kPlainScale = 40.0f; // largest |log2 s_v| of the plain form
