@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 // tokens, first to last: node idx_j moves from place start + idx_j to start + j, never upwards,
 // so what a block receives lies in itself or behind it, where this warp has not written yet.
 // Latency counts (a branch is a few tokens): lengths, indices, pages and codes are four loads one
-// after the other.
+// after the other. One branch of 8 kv heads 3.3 us, 256 branches of 1 to 12 tokens 7.8 us.
 struct KeepArgs {
   NewRows rows;
   const int32_t* idx;  // [batch][stride]

@@ -29,11 +29,21 @@
 //   warps 8-11 K's codes, 12-15 V's, warp 16 the products, 17 and 18 the copies (TMA, a block
 //     each) of K and V, several steps ahead.
 // Tensor memory: S 2 streams x 2 steps x 64 columns, O 2 x 64, K 64, V 64 (while the products with
-// one of them run, the other's next codes come in).
+// one of them run, the other's next codes come in). Shared memory: the queries 32 KB, three steps of
+// codes 96, two of P for each stream 64.
+//
+// Bounds. Memory, for few rows: the codes of a step are 32 KB, 0.73 us of one SM's share of 6.8 TB/s.
+// 600K tokens of 8 heads (1.23 GB, 181 us at 6.8 TB/s) take 233 us where only the copies run, 262
+// with 64 rows and 340 with 128, where the chain scores -> exponentials -> P of a stream is the
+// longest: 1.3 us a step; tensor pipe 30 %, issue slots 53 %, exponentials 15 % busy. A call's fixed
+// part is 14 us:
+// lengths, plan, queries and the first copies 7.5, the first maxima 2, the results 2, the joining
+// kernel 2 to 3. 8 nodes of 4 heads over 8K tokens 14.4 us, 25 nodes of 32 heads over 128K 88,
+// 8 x 6-17 nodes of 64 heads over 32-128K tokens 390 (1.41 GB, 3.6 TB/s), 4 chats of 5-33 nodes 39.
 //
 // Work. All steps (row block, token tile) of all sequences and heads form one line, cut into equal
 // slices, one CTA each; the parts of a row block that is cut go through the workspace to a second
-// kernel that joins them, a warp a row, so that joining takes all SMs and no CTA waits.
+// kernel that joins them, so that joining takes all SMs and no CTA waits.
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -69,10 +79,10 @@ constexpr float kTiny = 1e-37f;      // smallest factor of a score: a masked -in
 constexpr float kLow = -3.4e38f;     // a maximum before any score
 // Places on the line of steps (see the plan): a tile's, with one stream on it and with two, a row
 // block's beside its tiles, and the shortest slice. In the order of their times: 600K tokens of 8
-// heads take 262 us with 64 rows, 342 with 128. Tiles of 2 and 3 places 8 x 32-128K tokens of 48 to
-// 136 rows 420 us, of 3 and 4 391, of 4 and 5 394, of 5 and 7 396, alike 434; 4 chats of 20 to 132
-// rows 38.2, 40.2, 38.8, 39.9. A block's 44 (11 tiles; 16, 28 and 72 places before: 44, 41, 41 us of
-// the chats, 38).
+// heads take 262 us with 64 rows, 340 with 128. With 2 and 3 places a tile 8 x 32-128K tokens of 48
+// to 136 rows take 420 us, with 3 and 4 391, 4 and 5 394, 5 and 7 396; 4 chats of 20 to 132 rows 38.2,
+// 40.2, 38.8, 39.9. A block's are 11 tiles': 4, 7, 11 and 18 gave those chats 44, 41, 38 and 41 us (in
+// an earlier form of the step).
 constexpr int kTilePlaces = 4, kTwoPlaces = 5, kBlockPlaces = 44, kMinPlaces = 8;
 static_assert(kMinPlaces >= kTwoPlaces, "no slice without the first place of a tile");
 // O takes the products of at most this many steps: their own sums round to zero, 2^-23 a product
@@ -1313,8 +1323,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------- row blocks that were cut, joined
 //
-// Rows of all records in one line, a warp each, or where they are few a CTA each, whose warps take
-// the parts in turn. A lane has four channels; values are asked for before their weights are known.
+// Rows of all records in one line, a warp each, or where they are few (two for each CTA at most) a
+// CTA each, whose warps take the parts in turn (calls of 32 rows over 8K tokens 14.0 us, by warps
+// 17.5; of 2400 rows over 4 contexts 38.2 by warps, by CTAs 58.5). A lane has four channels; values
+// are asked for before their weights are known. Bound by latency.
 constexpr int kJoinWarps = 8, kJoinAhead = 8;
 
 struct JoinParams {
