@@ -1174,10 +1174,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       cur = next;
       next.count = 0;
     }
-    // copies under way write this CTA's shared memory: one more wait for each
-    if (!ok)
-      for (int i = max(step - kStages, 0); i < step; i++)
-        mbar_wait(&full[i % kStages], i / kStages & 1);
+    // Copies under way write this CTA's shared memory: one more wait for each. Not only where a wait
+    // of this warp ran out: where another warp's did, the pieces end early, and nobody may have
+    // waited for the last copies. (Else they have long arrived, as their codes were read.)
+    for (int i = max(step - kStages, 0); i < step; i++)
+      mbar_wait(&full[i % kStages], i / kStages & 1);
   } else if (warp == kPlanWarp) {
     // ============================================ the plan: this CTA's slice of the line of steps
     // All steps of all row blocks, under all heads, of all sequences, in equal slices. A row block has
