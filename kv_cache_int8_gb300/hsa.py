@@ -89,8 +89,14 @@ class hsa_rotary(ctypes.Structure):
 _DIMS_CACHE: dict = {}  # field values -> their C struct (read-only to the library)
 
 
+class _Held:
+    """Beside a descriptor's fields (and not among them: ``__dict__`` has the fields alone): a
+    reference to its C struct with the version of the fields that it was made of."""
+    __slots__ = ("_held", "_version")
+
+
 @dataclasses.dataclass
-class Dims:
+class Dims(_Held):
     batch: int
     hq: int
     hkv: int
@@ -114,17 +120,32 @@ class Dims:
     cache_policy: int = 0  # block cache victims: 0 least recently used, 1 least cumulative mass
 
     def __setattr__(self, name, value):
-        self.__dict__.pop("_ref", None)
         object.__setattr__(self, name, value)
+        _Held._version.__set__(self, object())
 
-    def __getstate__(self):  # (copies and pickles make their own)
-        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+    def __delattr__(self, name):
+        object.__delattr__(self, name)
+        _Held._version.__set__(self, object())
+
+    def __getstate__(self):  # the fields alone: copies and pickles hold nothing yet
+        return self.__dict__.copy()
 
     def ref(self):
-        """A reference to the C struct, kept until a field is set."""
-        r = self.__dict__.get("_ref")
-        if r is None:
-            r = self.__dict__["_ref"] = ctypes.byref(self.c())
+        """A reference to the C struct, held until a field is set. The struct is made under the
+        version that was there before its fields were read, so that one of another thread's
+        older values is not held; a field has its value before its version."""
+        try:
+            version, r = self._held
+            if version is self._version:
+                return r
+        except AttributeError:  # nothing held
+            pass
+        version = getattr(self, "_version", None)
+        if version is None:  # a copy, which no field was set of
+            version = object()
+            _Held._version.__set__(self, version)
+        r = ctypes.byref(self.c())
+        _Held._held.__set__(self, (version, r))
         return r
 
     def c(self) -> hsa_dims:

@@ -305,3 +305,60 @@ def test_a_descriptor_keeps_its_struct_until_a_field_is_set():
 def test_a_table_is_made_on_a_gpu():
     with pytest.raises(hsa.HsaError):
         hsa.hsa_rotary_table(16, 128, device="cpu")
+
+
+def test_a_descriptor_has_its_fields_alone():
+    """What derives one descriptor from another's fields finds nothing else among them."""
+    d = hsa.Dims(batch=2, hq=8, hkv=2, max_pages_per_seq=4, num_pages=9)
+    names = [f.name for f in dataclasses.fields(d)]
+    d.ref()
+    assert list(vars(d)) == names
+    other = hsa.Dims(**{**d.__dict__, "batch": 3})
+    assert other.ref()._obj.batch == 3 and d.ref()._obj.batch == 2
+    pickle.dumps(vars(d))
+    d.chunk = 128
+    assert d.ref()._obj.chunk == 128
+    del d.chunk  # (the class's value again)
+    assert d.ref()._obj.chunk == 64
+
+
+def test_a_descriptor_set_while_its_struct_is_made():
+    """A struct of fields that another thread sets meanwhile is not held: neither one whose fields
+    were read before the set and that is there after it, nor one made between a field's value and
+    the end of the call that sets it."""
+    class Slow(hsa.Dims):
+        def c(self):
+            made = super().c()
+            if hook:
+                hook.pop()()
+            return made
+
+    d, hook = Slow(batch=2, hq=8, hkv=2, max_pages_per_seq=4, num_pages=9), []
+    hook.append(lambda: setattr(d, "batch", 5))
+    assert d.ref()._obj.batch == 2
+    assert d.ref()._obj.batch == 5
+    twin = copy.copy(d)
+    hook.append(lambda: setattr(twin, "batch", 6))
+    twin.ref()
+    assert twin.ref()._obj.batch == 6 and d.ref()._obj.batch == 5
+
+    class Early(hsa.Dims):  # asked for its struct as soon as a field may have changed
+        def __setattr__(self, name, value):
+            super().__setattr__(name, value)
+            if watched:
+                watched.append(self.ref()._obj.batch)
+
+    watched = []
+    e = Early(batch=2, hq=8, hkv=2, max_pages_per_seq=4, num_pages=9)
+    e.ref()
+    watched.append(0)
+    e.batch = 7
+    assert watched == [0, 7]
+
+    class Between(int):  # a value that asks for the struct while it replaces the one before
+        def __del__(self):
+            d.ref()
+
+    d.num_pages = Between(9)
+    d.num_pages = 11
+    assert d.ref()._obj.num_pages == 11
