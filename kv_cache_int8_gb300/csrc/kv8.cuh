@@ -64,6 +64,18 @@ __device__ __forceinline__ int warp_search(int batch, int key, int lane, First f
   }
 }
 
+// Up to kFewSequences a bisection by every lane for itself: no load for one sequence, two for four,
+// and a smaller kernel (kv8_cache.cu has a form of its own for it).
+constexpr int kFewSequences = 4;
+__device__ __forceinline__ int item_sequence_of_few(const NewRows& r, int item) {
+  int lo = 0, hi = r.batch;  // the last b in [lo, hi) with item_base(b) <= item
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (item_base(r, mid) <= item) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
 __device__ __forceinline__ int item_sequence(const NewRows& r, int item, int lane) {
   return warp_search(r.batch, item, lane, [&](int b) { return item_base(r, b); });
 }

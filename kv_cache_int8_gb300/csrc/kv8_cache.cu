@@ -12,8 +12,10 @@
 //
 // Measured (GB300, copy 6.8 TB/s, 8 kv heads): 108K new tokens of 8 prompts written in 108 us
 // (664 MB, 6.1 TB/s), 117K tokens read back in 109 us (720 MB, 6.6 TB/s); one token of one
-// sequence written in 2.3 us, of 256 sequences in 3.7, 1024 tokens read in 2.9; one token of each of 256 ragged
-// sequences read in 5.4.
+// sequence written in 2.3 us, of 256 sequences in 3.7, 1024 tokens read in 2.9. With offsets, one
+// token of each of 256 sequences written in 6.05 us and read in 4.4 (found by bisection 7.2 and 5.6);
+// 25 tokens of one sequence 2.7 and 2.2 (by the warp's search, which loads an offset first, 3.0 and
+// 2.5), 8000 tokens 8.1 and 6.8 (8.8 and 7.2); 25 of each of four 3.1 and 2.6 either way.
 #include "append.cuh"
 #include "kv8.cuh"
 
@@ -34,7 +36,7 @@ struct WriteSide {
 
 // Lane l holds channels [8 (l % 16), 8 (l % 16) + 8) of tokens 2 i + l / 16, i = 0 .. 7: a warp
 // reads two rows of 256 contiguous bytes an instruction and writes two rows of 128.
-template <int F>
+template <int F, bool kFew>
 __global__ void __launch_bounds__(kWarps * 32) kv8_write_kernel(
     NewRows rows, WriteSide ks, WriteSide vs, const int32_t* __restrict__ page_table, int hkv,
     int num_pages, int units, int* err) {
@@ -47,8 +49,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_write_kernel(
   const bool is_v = unit & 1;
   const int h = (unit >> 1) % hkv, item = (unit >> 1) / hkv;
   const WriteSide& w = is_v ? vs : ks;
-  const int b = rows.cu ? item_sequence(rows, item, lane) : item;
-  if (b < 0) return;
+  const int b = !rows.cu ? item
+                : kFew   ? item_sequence_of_few(rows, item)
+                         : item_sequence(rows, item, lane);
+  if (!kFew && b < 0) return;
   const NewSpan sp = new_span(rows, b);
   const int j = rows.cu ? item - item_base(rows, b) : 0;
   const int end = sp.start + sp.n;  // N_b
@@ -150,7 +154,7 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 }
 
 // Lanes as in the write: 8 bytes of codes in, 16 bytes of bf16 out.
-template <int F>
+template <int F, bool kFew>
 __global__ void __launch_bounds__(kWarps * 32) kv8_read_kernel(
     NewRows rows, ReadSide ks, ReadSide vs, const int32_t* __restrict__ page_table, int hkv,
     int num_pages, int units, int* err) {
@@ -163,8 +167,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_read_kernel(
   const bool is_v = unit & 1;
   const int h = (unit >> 1) % hkv, item = (unit >> 1) / hkv;
   const ReadSide& r = is_v ? vs : ks;
-  const int b = rows.cu ? item_sequence(rows, item, lane) : item;
-  if (b < 0) return;
+  const int b = !rows.cu ? item
+                : kFew   ? item_sequence_of_few(rows, item)
+                         : item_sequence(rows, item, lane);
+  if (!kFew && b < 0) return;
   const NewSpan sp = new_span(rows, b);
   const int j = rows.cu ? item - item_base(rows, b) : 0;
   const int end = sp.start + sp.n;
@@ -213,7 +219,10 @@ cudaError_t launch_kv8_write(const Shape& s, const Kv8& c, const void* k_new, lo
   const WriteSide vs = {static_cast<const __nv_bfloat16*>(v_new), v_stride,
                         static_cast<uint8_t*>(c.v), c.v_scale};
   const int units = new_block_items(s.batch, total, cu != nullptr) * s.hkv * 2;
-  auto kernel = c.format == kE4m3 ? kv8_write_kernel<kE4m3> : kv8_write_kernel<kInt8>;
+  const bool few = s.batch <= kFewSequences;
+  auto kernel = c.format == kE4m3
+                    ? (few ? kv8_write_kernel<kE4m3, true> : kv8_write_kernel<kE4m3, false>)
+                    : (few ? kv8_write_kernel<kInt8, true> : kv8_write_kernel<kInt8, false>);
   return launch_kernel(kernel, dim3(units / kWarps + 1), dim3(kWarps * 32), 0, st,
                        true, rows, ks, vs, page_table, s.hkv, s.num_pages, units, err);
 }
@@ -228,7 +237,10 @@ cudaError_t launch_kv8_read(const Shape& s, const Kv8& c, void* k_out, long long
   const ReadSide vs = {static_cast<__nv_bfloat16*>(v_out), v_stride,
                        static_cast<const uint8_t*>(c.v), c.v_scale};
   const int units = new_block_items(s.batch, total, cu != nullptr) * s.hkv * 2;
-  auto kernel = c.format == kE4m3 ? kv8_read_kernel<kE4m3> : kv8_read_kernel<kInt8>;
+  const bool few = s.batch <= kFewSequences;
+  auto kernel = c.format == kE4m3
+                    ? (few ? kv8_read_kernel<kE4m3, true> : kv8_read_kernel<kE4m3, false>)
+                    : (few ? kv8_read_kernel<kInt8, true> : kv8_read_kernel<kInt8, false>);
   return launch_kernel(kernel, dim3(units / kWarps + 1), dim3(kWarps * 32), 0, st,
                        true, rows, ks, vs, page_table, s.hkv, s.num_pages, units, err);
 }

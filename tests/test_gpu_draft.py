@@ -1010,3 +1010,46 @@ def test_rotated_rows_go_into_the_bf16_cache():
         page, slot = int(table[b, (n - 1) // PAGE]), (n - 1) % PAGE
         assert torch.equal(caches[0][page, :, slot], k[b])
         assert torch.equal(caches[1][page, :, slot], v[b])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("front,n,before", [(1, 1, 0), (3, 25, 5), (16, 16, 16), (40, 100, 7), (37, 0, 20)])
+def test_one_sequence_behind_rows_of_none(fmt, front, n, before):
+    """A single sequence's offsets may begin behind rows of no sequence, and rows may lie behind it:
+    the calls that find a row's or a block's sequence leave both as they are."""
+    hq, hkv, dim, behind = 8, 2, 128, 9
+    s = Batch([before + n], hq, hkv, fmt, seed=front, fill=False)
+    held = s.rows(before), s.rows(before)
+    if before:
+        O.write(s.cache, *held, s.table[0], 0)
+    total = front + n + behind
+    q = bf16(s.rng.standard_normal((total, hq, D)))
+    k, v = (bf16(s.rng.standard_normal((total, hkv, D))) for _ in "kv")
+    t = angle_table(before + n + 1, dim)
+    rot = hsa.Rotary(torch.from_numpy(t).cuda(), False)
+    d, caches, err = s.dims(), [s.gpu_cache(), s.gpu_cache()], err_word()
+    cu, table, lens = i32([front, front + n]), s.gpu_table(), s.gpu_lens()
+    mine = slice(front, front + n)
+    at = t[np.arange(before, before + n)]
+    plain = {name: c.copy() if isinstance(c, np.ndarray) else c for name, c in s.cache.items()}
+    if n:
+        O.write(plain, k[mine], v[mine], s.table[0], before)
+        O.write(s.cache, R.turn(k[mine], at, False), v[mine], s.table[0], before)
+    gq, gk, gv = to_bf16(q), to_bf16(k), to_bf16(v)
+    hsa.hsa_kv8_write(d, caches[0], gk, gv, cu, table, lens, err)
+    assert_same_cache(caches[0], plain)
+    out = torch.full_like(gq, 9.0)
+    hsa.hsa_kv8_write_rotated(d, caches[1], rot, gq, out, gk, gv, None, cu, table, lens, err)
+    assert_same_cache(caches[1], s.cache)
+    turned = torch.full_like(gq, 9.0), torch.full_like(gk, 9.0)
+    hsa.hsa_rotate(d, rot, gq, turned[0], gk, turned[1], None, cu, lens, err)
+    for got, x in ((out, q), (turned[0], q), (turned[1], k)):
+        np.testing.assert_array_equal(bits(got[mine]), to_bf16_bits(R.turn(x[mine], at, False)))
+        assert (got[:front] == 9.0).all() and (got[front + n:] == 9.0).all()
+    back = torch.full_like(gk, 9.0), torch.full_like(gv, 9.0)
+    hsa.hsa_kv8_read(d, caches[0], *back, cu, table, lens, err)
+    for got, which in zip(back, "kv"):
+        want = np.stack([O.values(plain, which, s.table[0], before + n, h) for h in range(hkv)], 1)
+        np.testing.assert_array_equal(bits(got[mine]), to_bf16_bits(want[before:]))
+        assert (got[:front] == 9.0).all() and (got[front + n:] == 9.0).all()
+    assert hsa.hsa_read_device_error(err) == 0
