@@ -637,13 +637,18 @@ def hsa_rotary_table(rows: int, dim: int = 128, base: float = 10000.0, scaling: 
                      original: float = 8192.0, magnitude: float = 1.0, device="cuda",
                      stream=None) -> torch.Tensor:
     """A rotary table for positions 0 .. rows - 1, float32 [rows][dim] (include/hsa.h: scaling 0
-    none, 1 linear, 2 by parts)."""
+    none, 1 linear, 2 by parts). It is made and allocated on `stream` (None: the current one);
+    other streams wait for that one before they read it."""
     device = torch.device(device)
     if device.type != "cuda":
         raise HsaError("hsa_rotary_table", HSA_ERR_INVALID_ARG, "a table is made on a GPU")
     a = hsa_rotary_angles(base, factor, low, high, original, magnitude, scaling)
     with torch.cuda.device(device):
-        table = torch.empty((rows, dim), dtype=torch.float32, device=device)
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):  # a handle
+            at = _stream(stream)
+            stream = torch.cuda.ExternalStream(at) if at else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):  # else memory that the current stream still uses
+            table = torch.empty((rows, dim), dtype=torch.float32, device=device)
         _check("hsa_rotary_table", load().hsa_rotary_table(
             ctypes.byref(a), table.data_ptr(), rows, dim, _stream(stream)))
     return table

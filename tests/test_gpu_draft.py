@@ -1053,3 +1053,25 @@ def test_one_sequence_behind_rows_of_none(fmt, front, n, before):
         np.testing.assert_array_equal(bits(got[mine]), to_bf16_bits(want[before:]))
         assert (got[:front] == 9.0).all() and (got[front + n:] == 9.0).all()
     assert hsa.hsa_read_device_error(err) == 0
+
+
+@pytest.mark.parametrize("given", ("stream", "handle"))
+def test_a_table_made_on_another_stream(given):
+    """Memory that the current stream gave back while its work on it was still to come does not
+    become the other stream's table."""
+    rows, dim = 5000, 128
+    want = hsa.hsa_rotary_table(rows, dim)
+    other = torch.cuda.Stream()
+    torch.cuda._sleep(1)
+    held = torch.empty(rows, dim, device="cuda").fill_(1.0)  # (every kernel is loaded)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # a tenth of a second
+    held.fill_(7.0)
+    del held
+    table = hsa.hsa_rotary_table(rows, dim, stream=other if given == "stream" else other.cuda_stream)
+    other.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(table, want)
+    zero = hsa.hsa_rotary_table(rows, dim, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(zero, want)
