@@ -443,6 +443,14 @@ def hsa_decode_step_kernels(d: Dims) -> int:
     return int(load().hsa_decode_step_kernels(ctypes.byref(d.c())))
 
 
+def _device_of(name: str, first, *others) -> int:
+    """The one device that the tensors lie on (-1: the host)."""
+    at = first.get_device()
+    if any(t.get_device() != at for t in others):
+        raise HsaError(name, HSA_ERR_INVALID_ARG, "tensors on several devices")
+    return at
+
+
 class KV8:
     """The 8-bit K/V cache of include/hsa.h: code tensors k and v [num_pages][hkv][16][128],
     both torch.int8 or both torch.float8_e4m3fn (the format follows), and float32 scales
@@ -458,6 +466,7 @@ class KV8:
                 raise HsaError("KV8", HSA_ERR_INVALID_ARG, "shapes, types or layout rejected")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.hkv = k.shape[:2]
+        self.device = _device_of("KV8", k, v, k_scale, v_scale)
         self._c = hsa_kv8(_p(k), _p(v), _p(k_scale), _p(v_scale), formats[k.dtype])
         self._ref = ctypes.byref(self._c)
 
@@ -663,17 +672,73 @@ class Rotary:
         if table.dtype is not torch.float32 or table.dim() != 2 or not table.is_contiguous():
             raise HsaError("Rotary", HSA_ERR_INVALID_ARG, "a table is contiguous float32 [rows][dim]")
         self.table = table
+        self.device = table.get_device()
         self._c = hsa_rotary(_p(table), table.shape[0], table.shape[1], 1 if neighbours else 0)
         self._ref = ctypes.byref(self._c)
 
 
-def _row_list(name: str, what: str, t, rows: int) -> Optional[int]:
+def _elsewhere(name: str):
+    return HsaError(name, HSA_ERR_INVALID_ARG,
+                    "tensors lie on the current device, lists there or in pinned memory")
+
+
+def _current(name: str, at: int) -> None:
+    """For a cache or a table on a device that is not the current one, whose stream a call takes.
+    (The library runs on no host tensors; what stands in for it in tests takes any.)"""
+    if at >= 0 or isinstance(load(), ctypes.CDLL):
+        raise _elsewhere(name)
+
+
+def _row_list(name: str, what: str, t, rows: int, at: int) -> Optional[int]:
     """The address of one int32 a row (None stays None, an address itself)."""
     if t is None or type(t) is int:
         return t
     if t.dtype is not torch.int32 or t.numel() < rows or not t.is_contiguous():
         raise HsaError(name, HSA_ERR_INVALID_ARG, f"{what} must be contiguous torch.int32, one a row")
+    if t.get_device() != at and not t.is_pinned():
+        raise _elsewhere(name)
     return t.data_ptr()
+
+
+def _offsets_at(name: str, d: Dims, cu, at: int) -> Optional[int]:
+    if cu is not None and type(cu) is not int and cu.get_device() != at and not cu.is_pinned():
+        raise _elsewhere(name)
+    return _offsets(name, d, cu)
+
+
+def _sized_lists(name: str, d: Dims, cu, page_table, seq_lens, at: int):
+    """_lists, of the descriptor's sizes and where the GPU reads them."""
+    rows, columns, i32 = d.batch, d.max_pages_per_seq, torch.int32
+    try:  # the lists as they should be, without a call for each
+        if (page_table.dtype is i32 and page_table.shape == (rows, columns) and
+                page_table.is_contiguous() and page_table.get_device() == at and
+                seq_lens.dtype is i32 and seq_lens.numel() >= rows and seq_lens.is_contiguous() and
+                seq_lens.get_device() == at and
+                (cu is None or (cu.dtype is i32 and cu.numel() > rows and cu.is_contiguous() and
+                                cu.get_device() == at))):
+            return (cu if cu is None else cu.data_ptr(), page_table.data_ptr(),
+                    seq_lens.data_ptr())
+    except AttributeError:  # addresses, no page table
+        pass
+    good = True
+    if page_table is not None and type(page_table) is not int:
+        shape = page_table.shape
+        good = (page_table.dtype is i32 and page_table.numel() >= rows * columns and
+                page_table.is_contiguous() and
+                (len(shape) < 2 or shape[-1] == columns or rows == 1))
+        if page_table.get_device() != at and not page_table.is_pinned():
+            raise _elsewhere(name)
+        page_table = page_table.data_ptr()
+    if seq_lens is not None and type(seq_lens) is not int:
+        good = (good and seq_lens.dtype is i32 and seq_lens.numel() >= rows and
+                seq_lens.is_contiguous())
+        if seq_lens.get_device() != at and not seq_lens.is_pinned():
+            raise _elsewhere(name)
+        seq_lens = seq_lens.data_ptr()
+    if not good:
+        raise HsaError(name, HSA_ERR_INVALID_ARG, f"page tables are contiguous torch.int32 "
+                       f"[{rows}][{columns}], lengths contiguous torch.int32 [{rows}]")
+    return _offsets_at(name, d, cu, at), page_table, seq_lens
 
 
 def _turned_rows(name: str, x, y, heads: int):
@@ -698,23 +763,33 @@ def hsa_rotate(d: Dims, rotary: Rotary, q, q_out, k, k_out, positions=None, cu_t
                seq_lens=None, ws=None, stream=None) -> None:
     """q / q_out: bf16 [total_tokens][hq][128], k / k_out: [total_tokens][hkv][128] or both None;
     rows contiguous (any row stride), an output may be its input. positions: int32 [total_tokens],
-    or None: the tokens' places by seq_lens and cu_tokens."""
-    name = "hsa_rotate"
+    or None: the tokens' places by seq_lens and cu_tokens. All on the table's device, the current
+    one (the lists may lie in pinned memory)."""
+    name, at = "hsa_rotate", rotary.device
+    if at < 0 or at != _DEVICE():
+        _current(name, at)
     rows, qs, qos = _turned_rows(name, q, q_out, d.hq)
+    if q.get_device() != at or q_out.get_device() != at or (
+            ws is not None and ws.get_device() != at):
+        raise _elsewhere(name)
     k_at = k_out_at = None
     ks = kos = 0
     if k is not None or k_out is not None:
         n, ks, kos = _turned_rows(name, k, k_out, d.hkv)
         if n != rows:
             raise HsaError(name, HSA_ERR_INVALID_ARG, "q and k must have as many rows")
+        if k.get_device() != at or k_out.get_device() != at:
+            raise _elsewhere(name)
         k_at, k_out_at = k.data_ptr(), k_out.data_ptr()
     if positions is not None:
-        positions = _row_list(name, "positions", positions, rows)
-    if cu_tokens is not None:
-        cu_tokens = _offsets(name, d, cu_tokens)
+        positions = _row_list(name, "positions", positions, rows, at)
+        cu_tokens, seq_lens = _offsets(name, d, cu_tokens), _list(name, seq_lens)  # (not read)
+    else:
+        seq_lens = _row_list(name, "seq_lens", seq_lens, d.batch, at)
+        cu_tokens = _offsets_at(name, d, cu_tokens, at)
     rc = load().hsa_rotate(
         d.ref(), rotary._ref, q.data_ptr(), qs, q_out.data_ptr(), qos, k_at, ks,
-        k_out_at, kos, positions, cu_tokens, rows, _list(name, seq_lens), _p(ws),
+        k_out_at, kos, positions, cu_tokens, rows, seq_lens, _p(ws),
         0 if ws is None else ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check(name, rc)
@@ -723,19 +798,28 @@ def hsa_rotate(d: Dims, rotary: Rotary, q, q_out, k, k_out, positions=None, cu_t
 def hsa_kv8_write_rotated(d: Dims, cache: KV8, rotary: Rotary, q, q_out, k_new, v_new, positions,
                           cu_tokens, page_table, seq_lens, ws=None, stream=None) -> None:
     """k_new / v_new: bf16 [total_tokens][hkv][128]; q / q_out: [total_tokens][hq][128] or both
-    None; rows contiguous (any row stride). positions: as hsa_rotate."""
-    name = "hsa_kv8_write_rotated"
+    None; rows contiguous (any row stride). positions: as hsa_rotate. All on the cache's device,
+    the current one (positions, offsets, page table and lengths may lie in pinned memory); page
+    table contiguous [batch][max_pages_per_seq], lengths [batch]."""
+    name, at = "hsa_kv8_write_rotated", cache.device
+    if at < 0 or at != _DEVICE():
+        _current(name, at)
     rows, k_stride, v_stride = _row_pair(name, k_new, v_new, d.hkv)
+    if rotary.device != at or k_new.get_device() != at or v_new.get_device() != at or (
+            ws is not None and ws.get_device() != at):
+        raise _elsewhere(name)
     q_at = q_out_at = None
     qs = qos = 0
     if q is not None or q_out is not None:
         n, qs, qos = _turned_rows(name, q, q_out, d.hq)
         if n != rows:
             raise HsaError(name, HSA_ERR_INVALID_ARG, "q and k must have as many rows")
+        if q.get_device() != at or q_out.get_device() != at:
+            raise _elsewhere(name)
         q_at, q_out_at = q.data_ptr(), q_out.data_ptr()
     if positions is not None:
-        positions = _row_list(name, "positions", positions, rows)
-    cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
+        positions = _row_list(name, "positions", positions, rows, at)
+    cu, table, lens = _sized_lists(name, d, cu_tokens, page_table, seq_lens, at)
     rc = load().hsa_kv8_write_rotated(
         d.ref(), _cache(name, d, cache), rotary._ref, q_at, qs, q_out_at, qos,
         k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride, positions, cu, rows, table, lens,
@@ -746,16 +830,22 @@ def hsa_kv8_write_rotated(d: Dims, cache: KV8, rotary: Rotary, q, q_out, k_new, 
 
 def hsa_kv8_tree(d: Dims, cache: KV8, q, parents, cu_tokens, page_table, seq_lens, out, lse, ws,
                  stream=None) -> None:
-    """q, out, lse: as hsa_kv8_prefill; parents: int32 [total_tokens] or None (no branches)."""
-    name = "hsa_kv8_tree"
+    """q, out, lse: as hsa_kv8_prefill; parents: int32 [total_tokens] or None (no branches).
+    Tensors as for hsa_kv8_write_rotated."""
+    name, at = "hsa_kv8_tree", cache.device
+    if at < 0 or at != _DEVICE():
+        _current(name, at)
     rows, q_stride = _rows(name, q, d.hq)
     if not out.is_contiguous() or out.shape != q.shape or out.dtype is not torch.bfloat16:
         raise HsaError(name, HSA_ERR_INVALID_ARG, "out must be contiguous, as q")
+    if q.get_device() != at or out.get_device() != at or ws.get_device() != at or (
+            lse is not None and type(lse) is not int and lse.get_device() != at):
+        raise _elsewhere(name)
     lse = _dense(name, "lse", lse, torch.float32, rows * d.hq)
-    cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
+    cu, table, lens = _sized_lists(name, d, cu_tokens, page_table, seq_lens, at)
     rc = load().hsa_kv8_tree(
         d.ref(), _cache(name, d, cache), q.data_ptr(), q_stride,
-        _row_list(name, "parents", parents, rows), cu, rows, table, lens, out.data_ptr(), lse,
+        _row_list(name, "parents", parents, rows, at), cu, rows, table, lens, out.data_ptr(), lse,
         _p(ws), ws.numel(), _stream(stream))
     if rc != HSA_OK:
         _check(name, rc)
@@ -764,17 +854,22 @@ def hsa_kv8_tree(d: Dims, cache: KV8, q, parents, cu_tokens, page_table, seq_len
 def hsa_kv8_keep(d: Dims, cache: KV8, keep_idx, n_keep, cu_tokens, page_table, seq_lens,
                  new_lens=None, ws=None, stream=None) -> None:
     """keep_idx: int32 [batch][most kept], rows contiguous; n_keep and new_lens: int32 [batch],
-    new_lens another tensor than seq_lens, or None."""
-    name = "hsa_kv8_keep"
+    new_lens another tensor than seq_lens, or None. Tensors as for hsa_kv8_write_rotated."""
+    name, at = "hsa_kv8_keep", cache.device
+    if at < 0 or at != _DEVICE():
+        _current(name, at)
     if (keep_idx.dtype is not torch.int32 or keep_idx.dim() != 2 or keep_idx.shape[0] != d.batch or
             not keep_idx.is_contiguous()):
         raise HsaError(name, HSA_ERR_INVALID_ARG,
                        "keep_idx must be contiguous torch.int32 [batch][most kept]")
-    cu, table, lens = _lists(name, d, cu_tokens, page_table, seq_lens)
+    if (keep_idx.get_device() != at and not keep_idx.is_pinned()) or (
+            ws is not None and ws.get_device() != at):
+        raise _elsewhere(name)
+    cu, table, lens = _sized_lists(name, d, cu_tokens, page_table, seq_lens, at)
     rc = load().hsa_kv8_keep(
         d.ref(), _cache(name, d, cache), keep_idx.data_ptr(), keep_idx.shape[1],
-        _row_list(name, "n_keep", n_keep, d.batch), cu, table, lens,
-        _row_list(name, "new_lens", new_lens, d.batch), _p(ws), 0 if ws is None else ws.numel(),
+        _row_list(name, "n_keep", n_keep, d.batch, at), cu, table, lens,
+        _row_list(name, "new_lens", new_lens, d.batch, at), _p(ws), 0 if ws is None else ws.numel(),
         _stream(stream))
     if rc != HSA_OK:
         _check(name, rc)

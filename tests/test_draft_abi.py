@@ -362,3 +362,119 @@ def test_a_descriptor_set_while_its_struct_is_made():
     d.num_pages = Between(9)
     d.num_pages = 11
     assert d.ref()._obj.num_pages == 11
+
+
+class On:
+    """A tensor as if it lay on another device (-1: the host), pinned or not."""
+
+    def __init__(self, t, device, pinned=False):
+        self.t, self.device_index, self.pinned = t, device, pinned
+
+    def get_device(self):
+        return self.device_index
+
+    def is_pinned(self):
+        return self.pinned
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def on_devices(hsa, monkeypatch, current=0):
+    monkeypatch.setattr(hsa, "_DEVICE", lambda: current)
+    d = dims(hsa, batch=3, hq=4, hkv=2, num_pages=8, max_pages_per_seq=4)
+    bf, i32 = torch.bfloat16, torch.int32
+    cache = cpu_cache(hsa, 8, 2)
+    cache.device = 0
+    rotary = hsa.Rotary(_aligned((64, 32), torch.float32))
+    rotary.device = 0
+    rows = dict(q=torch.zeros(5, 4, 128, dtype=bf), q_out=torch.zeros(5, 4, 128, dtype=bf),
+                k=torch.zeros(5, 2, 128, dtype=bf), k_out=torch.zeros(5, 2, 128, dtype=bf),
+                v=torch.zeros(5, 2, 128, dtype=bf), out=torch.zeros(5, 4, 128, dtype=bf),
+                lse=torch.zeros(5, 4), ws=torch.zeros(64, dtype=torch.uint8))
+    lists = dict(pos=torch.zeros(5, dtype=i32), parents=torch.zeros(5, dtype=i32),
+                 cu=torch.zeros(4, dtype=i32), table=torch.zeros(3, 4, dtype=i32),
+                 lens=torch.zeros(3, dtype=i32), idx=torch.zeros(3, 4, dtype=i32),
+                 cnt=torch.zeros(3, dtype=i32), new=torch.zeros(3, dtype=i32))
+    return d, cache, rotary, rows, lists
+
+
+# what each call reads and writes
+TAKES = {
+    "hsa_rotate": "q q_out k k_out pos",
+    "hsa_kv8_write_rotated": "q q_out k v pos cu table lens",
+    "hsa_kv8_tree": "q out lse ws parents cu table lens",
+    "hsa_kv8_keep": "idx cnt cu table lens new",
+}
+
+
+def test_tensors_of_another_device_are_refused(binding, monkeypatch):  # noqa: F811
+    """The library sees addresses alone: it would follow one of host memory, or of another GPU's."""
+    hsa, fake = binding  # noqa: F811
+    d, cache, rotary, rows, lists = on_devices(hsa, monkeypatch)
+    every = {**rows, **lists}
+
+    def made(**kw):
+        a = {n: On(t, 0) for n, t in every.items()}
+        a.update(kw)
+        return calls(hsa, d, cache, rotary=rotary, **a)
+
+    for name, takes in TAKES.items():
+        made()[name]()
+        assert fake.calls.pop() == name
+        for n in takes.split():
+            for device in (-1, 1):
+                with pytest.raises(hsa.HsaError):
+                    made(**{n: On(every[n], device)})[name]()
+            pinned = made(**{n: On(every[n], -1, True)})[name]
+            if n in lists:
+                pinned()
+                assert fake.calls.pop() == name
+            else:
+                with pytest.raises(hsa.HsaError):
+                    pinned()
+    for n in ("cu", "lens"):  # read by a rotation without positions only
+        with pytest.raises(hsa.HsaError):
+            made(pos=None, **{n: On(every[n], -1)})["hsa_rotate"]()
+    monkeypatch.setattr(hsa, "_DEVICE", lambda: 1)
+    for name in TAKES:
+        with pytest.raises(hsa.HsaError):
+            made()[name]()
+    assert not fake.calls
+    with pytest.raises(hsa.HsaError):
+        hsa.KV8(cache.k, cache.v, cache.k_scale, On(cache.v_scale, 0))
+
+
+@needs_lib
+def test_host_tensors_are_refused_by_the_library_itself(lib):  # noqa: F811
+    """Also where all of them lie there. (None of these calls reaches a GPU.)"""
+    d = dims(lib, batch=3, hq=4, hkv=2, num_pages=8, max_pages_per_seq=4)
+    for name, call in calls(lib, d, cpu_cache(lib, 8, 2)).items():
+        with pytest.raises(lib.HsaError) as e:
+            call()
+        assert e.value.code == INVALID, name
+
+
+def test_lists_of_other_sizes_are_refused(binding):  # noqa: F811
+    hsa, fake = binding  # noqa: F811
+    d = dims(hsa, batch=3, hq=4, hkv=2, num_pages=8, max_pages_per_seq=4)
+    cache, i32 = cpu_cache(hsa, 8, 2), torch.int32
+    names = ("hsa_kv8_write_rotated", "hsa_kv8_tree", "hsa_kv8_keep")
+    for good in (dict(table=torch.zeros(64, 4, dtype=i32)), dict(table=torch.zeros(12, dtype=i32)),
+                 dict(lens=torch.zeros(64, dtype=i32)), dict(lens=torch.zeros(3, 1, dtype=i32))):
+        for name in names:
+            calls(hsa, d, cache, **good)[name]()
+            assert fake.calls.pop() == name
+    for bad in (dict(table=torch.zeros(2, 4, dtype=i32)), dict(table=torch.zeros(3, 8, dtype=i32)[:, :4]),
+                dict(table=torch.zeros(3, 8, dtype=i32)), dict(table=torch.zeros(4, 3, dtype=i32)),
+                dict(table=torch.zeros(11, dtype=i32)), dict(lens=torch.zeros(2, dtype=i32)),
+                dict(lens=torch.zeros(6, dtype=i32)[::2])):
+        for name in names:
+            with pytest.raises(hsa.HsaError):
+                calls(hsa, d, cache, **bad)[name]()
+    for lens in (torch.zeros(2, dtype=i32), torch.zeros(6, dtype=i32)[::2]):
+        with pytest.raises(hsa.HsaError):
+            calls(hsa, d, cache, pos=None, lens=lens)["hsa_rotate"]()
+    one = dims(hsa, batch=1, hq=4, hkv=2, num_pages=8, max_pages_per_seq=4)
+    calls(hsa, one, cache, idx=torch.zeros(1, 4, dtype=i32), table=torch.zeros(1, 8, dtype=i32))[names[2]]()
+    assert fake.calls == [names[2]]
