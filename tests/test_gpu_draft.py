@@ -1075,3 +1075,62 @@ def test_a_table_made_on_another_stream(given):
     zero = hsa.hsa_rotary_table(rows, dim, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(zero, want)
+
+
+def sawtooth_context(d, n, fp8, far, period):
+    """A cache of n tokens whose scores (under a query of 31 in channel 0) rise by 8.2 over every
+    `period` tokens, values of mean 2; `far`: one block in a period with values 2^-60 of that."""
+    g = torch.Generator(device="cuda").manual_seed(17)
+    cache = hsa.KV8.zeros(d, fp8)
+    table = torch.randperm(d.num_pages, generator=g, device="cuda").to(torch.int32)[None].contiguous()
+    t = torch.arange(n, device="cuda")
+    k = torch.randn(n, d.hkv, D, generator=g, device="cuda")
+    k[:, :, 0] = (t % period / period * 3.0)[:, None]
+    k = k.to(torch.bfloat16)
+    v = (torch.randn(n, d.hkv, D, generator=g, device="cuda") + 2.0).to(torch.bfloat16)
+    if far:
+        v[t // PAGE % (period // PAGE) == 7] *= 2.0 ** -60
+    hsa.hsa_kv8_write(d, cache, k, v, i32([0, n]), table, i32([n]))
+    return cache, table, g
+
+
+@pytest.mark.parametrize("fp8", (False, True))
+@pytest.mark.parametrize("far", (False, True))
+@pytest.mark.parametrize("hq,hkv,n,m", [(64, 8, 700001, 16), (64, 64, 200003, 20), (64, 16, 640007, 11)])
+def test_stretches_longer_than_the_products_add_up(fp8, far, hq, hkv, n, m):
+    """A CTA has more tiles of a row block in one stretch than its products add up by themselves
+    (256 with two streams of rows, 512 with one), so it takes them in pieces that follow one
+    another. The scores' sawtooth is a little longer than a stretch: its top, which a stretch's
+    maximum follows by the lag, is in the first piece of some stretches and in the second of
+    others. far: the second form of the step in the pieces that have such a block.
+
+    Tolerances as for long contexts, products at their limit (2048 of them round to zero, 2^-23
+    each: 2^-12); the weights' fp16 rounding is a random sum over 1e4 weights or more (a sixth of
+    a sawtooth is within e of its top; logits of variance 1): 2^-11 / 1e2, 5e-6. lse: logits of
+    magnitudes up to 40 in 8 products that round to zero, 4e-5, and sums of 2e-5."""
+    group = hq // hkv
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count
+    tiles, limit = -(-n // 128), 256 if group * m > 64 else 512
+    assert tiles * hkv > 1.02 * limit * min(ctas, 256)  # (row blocks beside their tiles: 1 %)
+    pages = -(-n // PAGE)
+    d = hsa.Dims(batch=1, hq=hq, hkv=hkv, max_pages_per_seq=pages, num_pages=pages)
+    cache, table, g = sawtooth_context(d, n, fp8, far, (limit + 45) * 128)
+    q = torch.randn(m, hq, D, generator=g, device="cuda")
+    q[..., 0] = 31.0
+    q = q.to(torch.bfloat16)
+    parents = R.tree(np.random.default_rng(18), m)
+    seen = torch.from_numpy(R.seen(n, parents)).cuda()
+    out = torch.empty(m, hq, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(m, hq, device="cuda")
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_TREE)
+    hsa.hsa_kv8_tree(d, cache, q, i32(parents), i32([0, m]), table, i32([n]), out, lse, ws)
+    assert hsa.hsa_read_device_error(ws) == 0
+    want, wl = plain_tree(cache, table[0].long(), n, q, seen, group)
+    delta = 2.0 ** -12 + 2.0 ** -14
+    assert (want > 1.0).all()
+    low, high = (want * (1 - delta)).to(torch.bfloat16), (want * (1 + delta)).to(torch.bfloat16)
+    assert ((out >= low) & (out <= high)).all()
+    assert float((lse.double() - wl).abs().max()) <= 1e-4
+    again = torch.empty_like(out)
+    hsa.hsa_kv8_tree(d, cache, q, i32(parents), i32([0, m]), table, i32([n]), again, lse, ws)
+    assert torch.equal(again, out)
