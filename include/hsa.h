@@ -569,7 +569,9 @@ int32_t hsa_kv8_write_rotated(const hsa_dims* d, const hsa_kv8* cache, const hsa
  * or -1 for a child of the context. Node i attends the context, tokens [0, N_b - n_b), its
  * ancestors and itself. parents NULL: node i - 1 is node i's parent (a draft without branches:
  * hsa_kv8_prefill's causal attention). q, out, lse and strides as hsa_kv8_prefill's, out not over
- * q; the weights enter the product with V as fp16 numbers, within 2^-11 of themselves. A parent
+ * q. The weights, times V's scale, enter the product with V's codes as fp16 numbers: within 2^-11 of
+ * themselves or 2^-32 of the row's largest one, whichever is more (tokens that are that far below
+ * another one may be lost, N_b 2^-32 of the largest value together); lse sums them in fp32. A parent
  * that is no earlier node is reported as HSA_ERR_DEVICE_CHECK and counts as -1; rows of a sequence
  * that is left out (also one of more than 256 nodes) get 0 and lse -inf; rows of no sequence stay
  * as they were. Needs the HSA_OP_KV8_TREE workspace.

@@ -11,7 +11,10 @@
 // The sum takes 2^(y - M) / s_v, one factor a token, as long as every s_v is within 2^-40 ..
 // 2^40; from the first step on that has another (or a block of zeros), a second form of the step
 // sums 2^x under a maximum of its own. P = 2^(y - M + 7) is rounded to fp16 (11 bits, against 8 of
-// the bf16 result); M lags the running maximum by at most 8.
+// the bf16 result: one product with V and 16 KB of shared memory a buffer, where two numbers would
+// take two and 32), below 2^-14 to steps of 2^-24: a weight is off by 2^-11 of itself or by 2^-32
+// of the row's largest, and the sum, which takes the fp32 numbers, keeps what P loses. n tokens lose
+// n 2^-32 of the largest value at most: 2^-12 at 1M. M lags the running maximum by at most 8.
 //
 // Layout. A tree is few rows against many tokens (a kv head's group of query heads x the nodes:
 // up to 128 rows here), so the products are turned round: the tokens are the 128 rows of the
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     len[b] = sp.start + sp.n;
     num[b] = sp.n;
     row0[b] = sp.row0;
-    // row blocks, as equal as they come, and a row block's places on the line (see the plan)
+    // row blocks, as equal as they come
     const int most = max(nodes_a_block(sp.n, p.block_nodes), 1);
     block_nodes[b] = most;
     blocks[b] = (sp.n + most - 1) / most;
@@ -439,8 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- the queries in fp16, four threads a row. All rows under one power of two that puts
       // the largest value in [2^13, 2^14), as long as the smallest row's largest is within 2^-15
-      // of it (its values down to 2^-22 of their largest are then exact in fp16, and the rest is
-      // off by less than 2^-23 of it); else each under its own, and the second form of the step.
+      // of it: its largest is then 2^-2 or more, its values down to 2^-15 of that are exact in fp16,
+      // and smaller ones, in steps of 2^-24, are off by 2^-25 or less, 2^-23 of it. Else each row
+      // under its own, and the second form of the step.
       auto query = [&](int r) {
         return p.q + (long long)(q_row + r / p.group) * p.q_stride +
                (pc.h * p.group + r % p.group) * kHeadDim + (tid & 3) * 32;

@@ -1134,3 +1134,53 @@ def test_stretches_longer_than_the_products_add_up(fp8, far, hq, hkv, n, m):
     again = torch.empty_like(out)
     hsa.hsa_kv8_tree(d, cache, q, i32(parents), i32([0, m]), table, i32([n]), again, lse, ws)
     assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("fp8", (False, True))
+@pytest.mark.parametrize("low,high", [(20.0, 33.0), (33.0, 33.8)])
+def test_weights_far_below_the_largest(fp8, low, high):
+    """One token takes nearly everything, and its value is 0: the result is what the others, 2^-low
+    to 2^-high of it, leave. (19 sequences of 8 heads over one context: a row block for each CTA
+    of 152, so no part has a maximum of its own.)
+
+    P is off by 2^-11 of itself or 2^-32 of the row's largest weight times scale: n times that, times
+    the codes, is n 2^-32 of the largest value. Of the tail's sum: the products' rounding to zero
+    2^-12, scores of 33 (log2) in three roundings of 2^-24 and ex2's 2^-22, 2^-17 together. Of the
+    sum of weights: a lane adds one number a step of 128 tokens, each rounded by 2^-24. The result
+    to bf16, 2^-8."""
+    n, batch, hq, hkv = 65536, 19, 32, 8
+    pages = n // PAGE
+    d = hsa.Dims(batch=batch, hq=hq, hkv=hkv, max_pages_per_seq=pages, num_pages=pages)
+    g = torch.Generator(device="cuda").manual_seed(23)
+    cache = hsa.KV8.zeros(d, fp8)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    k = torch.randn(n, hkv, D, generator=g, device="cuda")
+    drop = low + (high - low) * torch.rand(n, generator=g, device="cuda")
+    drop[1234] = 0.0
+    k[:, :, 0] = (4.0 - 4.0 / 33.0 * drop)[:, None]
+    v = torch.randn(n, hkv, D, generator=g, device="cuda") + 2.0
+    v[1234] = 0.0
+    k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+    one = hsa.Dims(batch=1, hq=hq, hkv=hkv, max_pages_per_seq=pages, num_pages=pages)
+    hsa.hsa_kv8_write(one, cache, k, v, i32([0, n]), table[None].contiguous(), i32([n]))
+    q = torch.zeros(batch, hq, D, device="cuda", dtype=torch.bfloat16)
+    q[..., 0] = 33.0 / 4.0 * np.log(2.0) * D ** 0.5
+    out = torch.empty_like(q)
+    lse = torch.empty(batch, hq, device="cuda")
+    ws = hsa.workspace(d, hsa.HSA_OP_KV8_TREE)
+    hsa.hsa_kv8_tree(d, cache, q, None, i32(range(batch + 1)), table.expand(batch, -1).contiguous(),
+                     i32([n] * batch), out, lse, ws)
+    assert hsa.hsa_read_device_error(ws) == 0
+    seen = torch.ones(1, n, dtype=torch.bool, device="cuda")
+    want, wl = plain_tree(cache, table.long(), n, q[:1], seen, hq // hkv)
+    largest = float(cache.v_scale.max()) * (448.0 if fp8 else 127.0)
+    page, slot = int(table[1234 // PAGE]), 1234 % PAGE
+    key = (cache.k.view(torch.int8)[page, :, slot].view(cache.k.dtype).float().double() *
+           cache.k_scale[page, :, None].double()).repeat_interleave(hq // hkv, 0)
+    others = 1.0 - torch.exp((q[0].double() * key).sum(-1) * D ** -0.5 - wl)  # [1][hq]
+    sums = n / 128 * 2.0 ** -24
+    tol = (2.0 ** -8 * want.abs() + n * 2.0 ** -32 * largest +
+           (2.0 ** -11 + 2.0 ** -12 + 2.0 ** -17 + sums) * largest * others[..., None])
+    assert 0.0 < float(others.min()) and float(others.max()) < 0.02
+    assert ((out.double() - want).abs() <= tol).all()
+    assert float((lse.double() - wl).abs().max()) <= 23 * 4 * 2.0 ** -24 + 2.0 ** -20 + sums
