@@ -587,7 +587,15 @@ int32_t hsa_kv8_tree(const hsa_dims* d, const hsa_kv8* cache, const void* q, int
  * the first N_b - n_b: their values f32(code * scale) are written to positions N_b - n_b + j by
  * hsa_kv8_write's rules (a block's scale from the kept values, or with older tokens in it at least
  * the old one), K and V of every kv head. Entries from n_keep[b] on are ignored. Tokens that are
- * not kept are gone; slots behind the last kept one are as good as never written. new_lens
+ * not kept are gone; slots behind the last kept one are as good as never written. Not so the
+ * scale of the block with the context's last tokens: where a node was larger than they, its write
+ * has raised it and rounded their codes again, by at most half a code step of the new scale each
+ * time it grew, and that stays when the node is not kept (eight tokens, then eight times six nodes
+ * of which none is kept, all normal: 1.7 times the error of the first rounding). A program that
+ * does not want it copies that block (of each sequence with N_b - n_b not a multiple of 16: codes
+ * and scale of K and V, every kv head) before the tree is written, copies it back in place of this
+ * call, and writes the accepted tokens' rows again with hsa_kv8_write_rotated: the cache is then
+ * what it would be had the others never been drafted. new_lens
  * (int32 [batch], nullable, an array of its own) receives N_b - n_b + n_keep[b]. A sequence whose
  * numbers, indices or pages do not fit is left as it was, its new length N_b, and reported as
  * HSA_ERR_DEVICE_CHECK. Two sequences must not share a page that receives tokens. workspace

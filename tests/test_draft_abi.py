@@ -66,6 +66,39 @@ def test_keep_by_hand():
     assert all(np.array_equal(before[n], c[n]) for n in before)
 
 
+@pytest.mark.parametrize("fmt", ("int8", "e4m3"))
+def test_the_mark_of_nodes_that_are_not_kept(fmt):
+    """They leave a block's scale raised and its older tokens rounded again, by half a step of the
+    new scale (int8: s / 2; E4M3: 2^-4 of a value, 2^-10 s among its smallest) beside fp32's own
+    roundings; nodes that are not larger leave every bit as it was."""
+    rng = np.random.default_rng(5)
+    c = O.empty(fmt, 2, 3)
+    pages = np.array([1, 0])
+
+    def first():
+        return np.stack([O.values(c, "k", pages, 11, h) for h in range(3)], 1)
+
+    x = rng.standard_normal((11, 3, 128)).astype(np.float32)
+    O.write(c, x, x, pages, 0)
+    grown = 0
+    for size in (1.0, 0.5, 1.1, 0.9, 3.0, 1.0, 100.0, 2.0 ** 30):
+        codes, scale, was = c["k"].copy(), c["ks"].copy(), first()
+        y = (size * rng.uniform(-4, 4, (9, 3, 128))).astype(np.float32)
+        O.write(c, y, y, pages, 11)
+        assert R.keep(c, pages, 20, 9, []) == 11
+        largest = np.abs(y[:5]).max((0, 2)) / O.LEVELS[fmt]  # of the nodes in the block
+        np.testing.assert_array_equal(c["ks"][1], np.maximum(scale[1], largest))
+        s = c["ks"][1][None, :, None].astype(np.float64)
+        half = s / 2 if fmt == "int8" else np.maximum(2.0 ** -4 * np.abs(was), 2.0 ** -10 * s)
+        assert (np.abs(first() - was) <= half + 2.0 ** -22 * np.abs(was)).all()
+        for h in range(3):
+            if c["ks"][1, h] == scale[1, h]:
+                np.testing.assert_array_equal(c["k"][1, h, :11], codes[1, h, :11])
+            else:
+                grown += 1
+    assert grown >= 9  # (3.0, 100.0 and 2^30 under every head)
+
+
 # ------------------------------------------------------------------------------ the library
 
 def test_binding_structs_match_the_header():

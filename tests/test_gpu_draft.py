@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from kv8_harness import D, PAGE, Batch, assert_rows, assert_same_cache, bf16, to_bf16
+from kv8_harness import (D, PAGE, Batch, assert_rows, assert_same_cache, bf16, codes_of,
+                         to_bf16)
 from kv_cache_int8_gb300 import hsa
 from oracle import draft as R
 from oracle import kv8 as O
@@ -1184,3 +1185,54 @@ def test_weights_far_below_the_largest(fp8, low, high):
     assert 0.0 < float(others.min()) and float(others.max()) < 0.02
     assert ((out.double() - want).abs() <= tol).all()
     assert float((lse.double() - wl).abs().max()) <= 23 * 4 * 2.0 ** -24 + 2.0 ** -20 + sums
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_accepted_rows_written_again_leave_no_mark(fmt):
+    """The block of the context's last tokens copied before a tree is written and copied back behind
+    its verification, then the accepted rows written again: the cache of the accepted tokens alone,
+    bit for bit, whatever was drafted in between (nodes ten times as large)."""
+    hq, hkv, dim, rng = 4, 2, 128, np.random.default_rng(90)
+    lens = [50, 16, 7]
+    s = Batch([n + 100 for n in lens], hq, hkv, fmt, seed=91, fill=False)
+    t = angle_table(300, dim)
+    rot = hsa.Rotary(torch.from_numpy(t).cuda())
+    d, cache, table, err = s.dims(), s.gpu_cache(), s.gpu_table(), err_word()
+    arrays = (cache.k.view(torch.int8), cache.v.view(torch.int8), cache.k_scale, cache.v_scale)
+
+    def write(lens, new, rows, positions):
+        q = torch.empty(sum(new), hq, D, dtype=torch.bfloat16, device="cuda")
+        hsa.hsa_kv8_write_rotated(d, cache, rot, q, q, *(to_bf16(x) for x in rows), i32(positions),
+                                  cu_of(new), table, i32(lens), err)
+
+    def normal(n, size=1.0):
+        return [bf16(size * rng.standard_normal((n, hkv, D))) for _ in "kv"]
+
+    rows = normal(sum(lens))
+    write(lens, lens, rows, places(lens, lens))
+    oracle_write(s, lens, lens, *rows, t, places(lens, lens), False)
+    for new in ([9, 25, 1], [33, 3, 12], [2, 7, 16]):
+        pages = torch.stack([table[b, n // PAGE] for b, n in enumerate(lens) if n % PAGE]).long()
+        held = [a[pages].clone() for a in arrays]
+        trees = [R.tree(rng, m) for m in new]
+        rows = normal(sum(new), 10.0)
+        at = np.concatenate([n + R.depths(p) for n, p in zip(lens, trees)])
+        write([n + m for n, m in zip(lens, new)], new, rows, at)
+        for a, h in zip(arrays, held):
+            a[pages] = h
+        paths = [np.flatnonzero(R.branches(u)[rng.integers(len(u))]) for u in trees]
+        first = np.concatenate([[0], np.cumsum(new)])
+        taken = np.concatenate([first[b] + p for b, p in enumerate(paths)])
+        kept = [len(p) for p in paths]
+        lens = [n + m for n, m in zip(lens, kept)]
+        accepted = [x[taken] for x in rows]
+        write(lens, kept, accepted, at[taken])
+        oracle_write(s, lens, kept, *accepted, t, at[taken], False)
+        got = codes_of(cache)
+        for b, n in enumerate(lens):
+            page = s.table[b, np.arange(n) // PAGE]
+            for name in ("k", "v"):
+                np.testing.assert_array_equal(got[name][page, :, np.arange(n) % PAGE],
+                                              s.cache[name][page, :, np.arange(n) % PAGE])
+                np.testing.assert_array_equal(got[name + "s"][page], s.cache[name + "s"][page])
+    assert hsa.hsa_read_device_error(err) == 0
