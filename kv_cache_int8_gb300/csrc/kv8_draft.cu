@@ -110,17 +110,21 @@ struct WriteSide {
 
 // Units: blocks x kv heads (or runs of `heads` of them) x halves, then (row, 16 query heads); one warp
 // behind them reports sequences that do not fit. Two warps share a block of K and of V, eight tokens
-// each, and meet over its maxima. Bound by memory: 109K new tokens of 32 + 8 heads (2.47 GB) take
+// each, and meet over its maxima. Bound by memory: 108K new tokens of 32 + 8 heads (2.47 GB) take
 // 390 us, 6.3 TB/s; one token 2.9 us, latency.
 //
 // A unit's way to its data (sequence, length, page, rows) is four loads one after the other. Where
 // there are many blocks a warp goes it once for several kv heads (kMany); the positions' angles then
 // come out of L1 (in registers they cost 32 and 2% of the time). One head a unit against four and
 // eight: 4096 tokens of 8 heads with their read-back 22.6, 26.8, 40.7 us, 8192 46.8, 39.5, 47.7, 24000
-// 132.5, 117.7, 114.6, 109K 541, 495, 491; so as many heads as leave 1024 runs (2048 warps, 13 an
+// 132.5, 117.7, 114.6, 108K 541, 495, 491; so as many heads as leave 1024 runs (2048 warps, 13 an
 // SM). kSplit: units of K and of V apart, for a token a sequence of few sequences, where the one
 // behind the other only takes longer (one sequence of 8 kv heads 2.9 us a call, not 3.4; 256
-// sequences 8.1, not 6.3, as the warps no longer fit the GPU at once).
+// sequences 8.1, not 6.3, as the warps no longer fit the GPU at once). Both hold for 1, 2 and 4 kv
+// heads too: 8 x 4096 tokens 25.5, 37.2, 62 us (one head a unit 25.5, 38, 67.5; hkv heads wherever 64
+// runs are left: 4096 tokens of 2 and 4 heads 8.6 and 15.4 us, not 5.6 and 8.4); one sequence 3.2 to
+// 3.3 us apart and 3.5 to 3.9 together, 1024, 1024 and 512 sequences 4.3, 6.4 and 6.6 together, 5.6,
+// 8.0 and 8.0 apart.
 constexpr int kBlocksAHead = 1024;
 constexpr int kSplitUnits = 2048;  // 13 warps an SM, of 24
 template <int F, bool kNeighbours, bool kSplit, bool kMany>
@@ -239,7 +243,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 // tokens, first to last: node idx_j moves from place start + idx_j to start + j, never upwards,
 // so what a block receives lies in itself or behind it, where this warp has not written yet.
 // Latency counts (a branch is a few tokens): lengths, indices, pages and codes are four loads one
-// after the other. One branch of 8 kv heads 3.3 us, 256 branches of 1 to 12 tokens 7.8 us.
+// after the other. One branch of 8 kv heads 3.3 us, 256 branches of 0 to 8 tokens 7.8 us. Three CTAs
+// an SM leave 80 registers a thread, and some 190 bytes are spilled; with two there are none (one
+// branch 2.9 us, 256 the same), with four 3.5 and 9.2 us.
 struct KeepArgs {
   NewRows rows;
   const int32_t* idx;  // [batch][stride]

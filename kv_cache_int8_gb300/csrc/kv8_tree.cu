@@ -42,7 +42,10 @@
 // part is 14 us:
 // lengths, plan, queries and the first copies 7.5, the first maxima 2, the results 2, the joining
 // kernel 2 to 3. 8 nodes of 4 heads over 8K tokens 14.4 us, 25 nodes of 32 heads over 128K 88,
-// 8 x 6-17 nodes of 64 heads over 32-128K tokens 390 (1.41 GB, 3.6 TB/s), 4 chats of 5-33 nodes 39.
+// 8 x 6-15 nodes of 64 heads over 32-128K tokens 390 (1.41 GB, 3.6 TB/s), 4 chats of 7-24 nodes 39.
+// The other forms of a step are for rare data and far from that: with one block of V in 64 of another
+// scale (or of zeros) 330 us behind 128K where all alike take 83, with queries of 2^10 194 (far
+// scores). The kernel spills 80 bytes a thread (stack of 40).
 //
 // Work. All steps (row block, token tile) of all sequences and heads form one line, cut into equal
 // slices, one CTA each; the parts of a row block that is cut go through the workspace to a second
@@ -83,9 +86,12 @@ constexpr float kLow = -3.4e38f;     // a maximum before any score
 // Places on the line of steps (see the plan): a tile's, with one stream on it and with two, a row
 // block's beside its tiles, and the shortest slice. In the order of their times: 600K tokens of 8
 // heads take 262 us with 64 rows, 340 with 128. With 2 and 3 places a tile 8 x 32-128K tokens of 48
-// to 136 rows take 420 us, with 3 and 4 391, 4 and 5 394, 5 and 7 396; 4 chats of 20 to 132 rows 38.2,
-// 40.2, 38.8, 39.9. A block's are 11 tiles': 4, 7, 11 and 18 gave those chats 44, 41, 38 and 41 us (in
-// an earlier form of the step).
+// to 120 rows take 420 us, with 3 and 4 391, 4 and 5 394, 5 and 7 396; 4 chats of 28 to 96 rows 38.2,
+// 40.2, 38.8, 39.9. A block's are 11 tiles': with 3, 6, 11 and 18 those chats take 42.6, 41.0, 38.8
+// and 41.4 us, 25 nodes behind 128K 89, 87, 82 and 82, 16 x 2K tokens 43.8, 43.6, 40.8 and 40.6, 64 x
+// 4K 160, 159, 157 and 159, 600K tokens of 128 rows 332, 324, 326 and 327. Slices of 5 places at least
+// take as long as of 8 everywhere, of 16 and 32 longer where they are short (8K tokens of one head
+// 15.9 and 18.9 us, not 14.4).
 constexpr int kTilePlaces = 4, kTwoPlaces = 5, kBlockPlaces = 44, kMinPlaces = 8;
 static_assert(kMinPlaces >= kTwoPlaces, "no slice without the first place of a tile");
 // O takes the products of at most this many steps: their own sums round to zero, 2^-23 a product
